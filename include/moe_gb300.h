@@ -55,6 +55,8 @@ enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 };
 enum { MOE_EPI_NONE = 0, MOE_EPI_SWIGLU_FWD = 1, MOE_EPI_SWIGLU_BWD = 2 };
 /* 8-bit float formats (OCP): E4M3FN (max 448, no infinities), E5M2 (max 57344) */
 enum { MOE_FP8_E4M3 = 0, MOE_FP8_E5M2 = 1 };
+/* 4-bit block-scaled formats (E2M1 elements): MXFP4 and NVFP4 */
+enum { MOE_FP4_MX = 0, MOE_FP4_NV = 1 };
 /* row orders of block-scale atoms (moe_mx_quantize) */
 enum { MOE_MX_ROWS_PLAIN = 0, MOE_MX_ROWS_GROUPED = 1, MOE_MX_ROWS_SWIGLU = 2,
        MOE_MX_ROWS_TILES = 3 };
@@ -541,6 +543,136 @@ moe_status_t moe_tgmm_mx(const uint8_t *At, int64_t ldat, const uint8_t *sfa, in
                          const int32_t *group_offsets, int E, int64_t rows_cap, int M, int N,
                          void *W, int w_dtype, int64_t ldw, int64_t stride_w, int accumulate,
                          int32_t *dev_status, moe_stream_t stream);
+
+/* ------------------------------------------------- microscaled 4-bit floats --
+ * Experts served from 4-bit codes.  Elements are E2M1 (0, .5, 1, 1.5, 2, 3, 4,
+ * 6 and a sign), two a byte along a row, the even column in the low nibble,
+ * rounded to nearest even and saturated; a scale covers a block of one row:
+ *   MOE_FP4_MX  32 elements, scale 2^s as the E8M0 code s + 127,
+ *               s = floor(log2 max|x|) - 2 (OCP Microscaling (MX) v1.0);
+ *               element value = code * 2^s
+ *   MOE_FP4_NV  16 elements, scale E4M3(max|x| / (6 g)) with one fp32 scale
+ *               g > 0 for the tensor (a weight: one an expert);
+ *               element value = code * scale * g
+ * A block that holds a NaN or an infinity takes the NaN scale and zero codes
+ * (it reads as NaN).  The `scale` arguments are g: fp32 on the device, one for
+ * activations and one an expert for weights, NULL for 1; MXFP4 products take
+ * them too (as plain factors), its quantisers ignore them.
+ * Scales are kept in 512-byte atoms of 128 rows x 4 blocks: row r0 + 32 r1 (r0 <
+ * 32, r1 < 4), block j at byte 16 r0 + 4 r1 + j; a row of atoms holds ceil(cols /
+ * (4 block)) of them, the last one's spare blocks zero.  Rows map to atoms as
+ * in moe_mx_quantize: MOE_MX_ROWS_GROUPED for activations, MOE_MX_ROWS_TILES
+ * and MOE_MX_ROWS_SWIGLU for weights of E experts (SWIGLU: 2F rows an expert,
+ * [gate | up], row n < F of expert e in tile t = n / 96 at padded row
+ * 256 (e ceil(F / 96) + t) + n % 96, row F + n 96 further).
+ * Columns (the contraction): multiples of 32.
+ */
+
+/* Bytes of scale atoms for a [rows, cols] matrix; 0 for bad arguments. */
+size_t moe_fp4_scale_bytes(int64_t rows, int cols, int fmt, int row_map, int E);
+
+/*
+ * moe_fp4_quantize -- codes q uint8 [rows, ldq >= cols / 2 bytes] and scale
+ * atoms sf of rows of x bf16 [src_rows, ldx >= cols].
+ *   row_index  int32 [rows] device or NULL: row p is row_index[p] / index_div of
+ *              x (a negative index: zeros; moe_permute's sorted_to_flat with
+ *              index_div = k gathers and quantises the tokens of every expert in
+ *              one pass); a row that x does not have sets MOE_ERR_DEVICE in
+ *              dev_status and reads as zeros.  NULL: row p (src_rows >= rows)
+ *   GROUPED    group_offsets int32 [E + 1] device; rows at or past
+ *              group_offsets[E], and the scales of padding rows, are not written
+ *   TILES, SWIGLU  K-major weights, rows = E equal groups; scale fp32 [E]
+ *   ldx % 8 == 0, ldq % 16 == 0; x, q, sf 16-byte aligned; E <= 256 (GROUPED)
+ */
+moe_status_t moe_fp4_quantize(const uint16_t *x, int64_t ldx, int64_t src_rows,
+                              const int32_t *row_index, int index_div, int64_t rows, int cols,
+                              int fmt, int row_map, const int32_t *group_offsets, int E,
+                              const float *scale, uint8_t *q, int64_t ldq, uint8_t *sf,
+                              size_t sf_bytes, int32_t *dev_status, moe_stream_t stream);
+
+/*
+ * moe_fp4_dequantize -- the values of moe_fp4_quantize's codes, rounded once to
+ * bf16: x bf16 [rows, ldx >= cols]; the other arguments as there.
+ */
+moe_status_t moe_fp4_dequantize(const uint8_t *q, int64_t ldq, const uint8_t *sf, size_t sf_bytes,
+                                int64_t rows, int cols, int fmt, int row_map,
+                                const int32_t *group_offsets, int E, const float *scale,
+                                uint16_t *x, int64_t ldx, moe_stream_t stream);
+
+/*
+ * moe_fp4_quantize_weights -- w bf16 [E, K, N] contiguous (contraction K down
+ * the rows, the layer's wi and wo) -> K-major codes q uint8 [E, N, K / 2] and
+ * atoms of the [E N, K] matrix in TILES or SWIGLU order.  K % 32 == 0.
+ */
+moe_status_t moe_fp4_quantize_weights(const uint16_t *w, int E, int K, int N, int fmt, int row_map,
+                                      const float *scale, uint8_t *q, uint8_t *sf,
+                                      size_t sf_bytes, moe_stream_t stream);
+
+/*
+ * moe_fp4_arrange_scales -- scales in row order, uint8 [rows, cols / block]
+ * contiguous (as 4-bit checkpoints store them), into atoms (TILES or SWIGLU).
+ */
+moe_status_t moe_fp4_arrange_scales(const uint8_t *scales, int64_t rows, int cols, int fmt,
+                                    int row_map, int E, uint8_t *sf, size_t sf_bytes,
+                                    moe_stream_t stream);
+
+/*
+ * moe_gmm_fp4 -- moe_gmm on 4-bit codes (fp32 accumulation in the tensor cores):
+ *     S[r, :] = a_scale b_scale[e] sum over blocks (code scale) . (code scale)
+ *   A    codes [rows_cap, lda >= K / 2 bytes], atoms sfa GROUPED
+ *   B    codes of expert e at B + e * stride_b, [N, ldb >= K / 2 bytes]; atoms sfb
+ *        TILES (MOE_EPI_NONE) or SWIGLU (MOE_EPI_SWIGLU_FWD, N = 2F, F % 32 == 0)
+ *   MOE_EPI_NONE        C = S as c_dtype (ldc rows of whole 16 bytes)
+ *   MOE_EPI_SWIGLU_FWD  Act = silu(S[:, :F]) * S[:, F:], quantised from the fp32
+ *        values with q2_scale: codes Q2 [rows_cap, ldq2 >= F / 2 bytes] and atoms
+ *        sf2 (GROUPED, F columns); C bf16 or NULL: H = S as well
+ * Only rows r < group_offsets[E] are written.  K % 32 == 0, N % 8 == 0; lda,
+ * ldb, stride_b, ldq2 multiples of 16 bytes, operands 16-byte aligned; E <= 256,
+ * rows_cap + 128 E < 2^23.
+ */
+moe_status_t moe_gmm_fp4(const uint8_t *A, int64_t lda, const uint8_t *sfa, const float *a_scale,
+                         const uint8_t *B, int64_t ldb, int64_t stride_b, const uint8_t *sfb,
+                         const float *b_scale, int fmt, const int32_t *group_offsets, int E,
+                         int64_t rows_cap, int K, int N, int epilogue, void *C, int c_dtype,
+                         int64_t ldc, uint8_t *Q2, int64_t ldq2, uint8_t *sf2, size_t sf2_bytes,
+                         const float *q2_scale, int32_t *dev_status, moe_stream_t stream);
+
+/* -------------------------------------------- activation checkpoints in 8 bits --
+ * What the forward saves for the backward, in 8.5 bits an element: signed 8-bit
+ * codes and one bf16 scale per 32 consecutive columns of a row (a row's last
+ * block may be shorter),
+ *     s = (max |x| of the block) / 127 rounded up to bf16, code = rne(x / s),
+ * value code * s (error <= s / 2).  A block under 2^-100 reads as zeros, one
+ * with a NaN or an infinity as NaN.  group_offsets int32 [E + 1] device or NULL:
+ * only rows < group_offsets[E] are read and written (NULL: all).  Columns and
+ * leading dimensions multiples of 8; bf16 matrices 16-byte, codes 8-byte aligned.
+ *
+ * moe_act8_quantize    x bf16 [rows, ldx] -> q int8 [rows, ldq >= cols], scales
+ *                      bf16 [rows, lds >= ceil(cols / 32)]
+ * moe_act8_dequantize  the values, rounded once to bf16
+ * moe_act8_swiglu_fwd  h bf16 [rows, ldh >= 2F] = [gate | up] -> act bf16 =
+ *                      silu(gate) * up (from the bf16 values) and the codes of h:
+ *                      q int8 [rows, ldq >= 2F], scales [rows, lds >= 2 ceil(F /
+ *                      32)] (the up half's blocks start at ceil(F / 32))
+ * moe_act8_swiglu_bwd  from the codes' values g, u and dact bf16 [rows, F]: dh
+ *                      bf16 [rows, 2F] = [dact u s (1 + g (1 - s)) | dact g s], s
+ *                      = sigmoid(g), and act (or NULL) bf16 [rows, F] = g s u
+ *                      (the operand of the weight gradient, not kept)
+ */
+moe_status_t moe_act8_quantize(const uint16_t *x, int64_t ldx, int64_t rows, int cols,
+                               const int32_t *group_offsets, int E, int8_t *q, int64_t ldq,
+                               uint16_t *scales, int64_t lds, moe_stream_t stream);
+moe_status_t moe_act8_dequantize(const int8_t *q, int64_t ldq, const uint16_t *scales, int64_t lds,
+                                 int64_t rows, int cols, const int32_t *group_offsets, int E,
+                                 uint16_t *x, int64_t ldx, moe_stream_t stream);
+moe_status_t moe_act8_swiglu_fwd(const uint16_t *h, int64_t ldh, int64_t rows, int F,
+                                 const int32_t *group_offsets, int E, uint16_t *act, int64_t lda,
+                                 int8_t *q, int64_t ldq, uint16_t *scales, int64_t lds,
+                                 moe_stream_t stream);
+moe_status_t moe_act8_swiglu_bwd(const int8_t *q, int64_t ldq, const uint16_t *scales, int64_t lds,
+                                 const uint16_t *dact, int64_t ld_dact, int64_t rows, int F,
+                                 const int32_t *group_offsets, int E, uint16_t *dh, int64_t ld_dh,
+                                 uint16_t *act, int64_t lda, moe_stream_t stream);
 
 /*
  * moe_tgmm -- weight-gradient grouped GEMM, ragged along the contraction:

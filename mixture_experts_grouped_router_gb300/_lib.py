@@ -98,6 +98,19 @@ _SIGS = {
                         _I, _I, _P, _I64, _P, _I, _I64, _P, _I64, _P, _P]),
     "moe_tgmm_mx": (_I, [_P, _I64, _P, _I, _P, _I64, _P, _I, _P, _I, _I64, _I, _I, _P, _I, _I64,
                          _I64, _I, _P, _P]),
+    "moe_fp4_scale_bytes": (_SZ, [_I64, _I, _I, _I, _I]),
+    "moe_fp4_quantize": (_I, [_P, _I64, _I64, _P, _I, _I64, _I, _I, _I, _P, _I, _P, _P, _I64, _P,
+                              _SZ, _P, _P]),
+    "moe_fp4_dequantize": (_I, [_P, _I64, _P, _SZ, _I64, _I, _I, _I, _P, _I, _P, _P, _I64, _P]),
+    "moe_fp4_quantize_weights": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P]),
+    "moe_fp4_arrange_scales": (_I, [_P, _I64, _I, _I, _I, _I, _P, _SZ, _P]),
+    "moe_gmm_fp4": (_I, [_P, _I64, _P, _P, _P, _I64, _I64, _P, _P, _I, _P, _I, _I64, _I, _I, _I,
+                         _P, _I, _I64, _P, _I64, _P, _SZ, _P, _P, _P]),
+    "moe_act8_quantize": (_I, [_P, _I64, _I64, _I, _P, _I, _P, _I64, _P, _I64, _P]),
+    "moe_act8_dequantize": (_I, [_P, _I64, _P, _I64, _I64, _I, _P, _I, _P, _I64, _P]),
+    "moe_act8_swiglu_fwd": (_I, [_P, _I64, _I64, _I, _P, _I, _P, _I64, _P, _I64, _P, _I64, _P]),
+    "moe_act8_swiglu_bwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _I64, _I, _P, _I, _P, _I64, _P,
+                                 _I64, _P]),
     "moe_ep_recv_rows_cap": (_I64, [_I, _I, _I, _I, _I]),
     "moe_ep_a2a_params": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P]),
     "moe_ep_local_layout": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P]),
@@ -435,6 +448,109 @@ def moe_tgmm_mx(At, sfa, a_fmt, Bt, sfb, b_fmt, group_offsets, rows_cap, W, accu
                            b_fmt, _ptr(group_offsets), E, rows_cap, M, N, _ptr(W), w_dtype,
                            W.stride(1), W.stride(0), int(accumulate), _ptr(dev_status),
                            _stream(stream)))
+
+
+# ------------------------------------------------------- microscaled 4-bit floats
+FP4_MX = 0
+FP4_NV = 1
+
+
+def moe_fp4_scale_bytes(rows: int, cols: int, fmt: int, row_map: int, E: int = 1) -> int:
+    return int(LIB.moe_fp4_scale_bytes(rows, cols, fmt, row_map, E))
+
+
+def _groups(group_offsets, groups):
+    return groups if group_offsets is None else group_offsets.shape[0] - 1
+
+
+def moe_fp4_quantize(x, fmt, q, sf, row_map=MX_ROWS_GROUPED, group_offsets=None, groups=1,
+                     row_index=None, index_div=1, scale=None, dev_status=None, stream=None):
+    """Rows of x bf16 [src_rows, cols] (gathered through row_index / index_div) -> q uint8
+    [rows, cols / 2], sf uint8 scale atoms; GROUPED takes group_offsets, TILES / SWIGLU the
+    number of equal row groups."""
+    rows, cols = q.shape[0], x.shape[1]
+    _check(LIB.moe_fp4_quantize(_ptr(x), _ld(x), x.shape[0], _ptr(row_index), index_div, rows,
+                                cols, fmt, row_map, _ptr(group_offsets),
+                                _groups(group_offsets, groups), _ptr(scale), _ptr(q), _ld(q),
+                                _ptr(sf), sf.numel(), _ptr(dev_status), _stream(stream)))
+
+
+def moe_fp4_dequantize(q, sf, fmt, x, row_map=MX_ROWS_GROUPED, group_offsets=None, groups=1,
+                       scale=None, stream=None):
+    """Codes q [rows, cols / 2] with scale atoms sf -> x bf16 [rows, cols]."""
+    rows, cols = x.shape
+    _check(LIB.moe_fp4_dequantize(_ptr(q), _ld(q), _ptr(sf), sf.numel(), rows, cols, fmt, row_map,
+                                  _ptr(group_offsets), _groups(group_offsets, groups),
+                                  _ptr(scale), _ptr(x), _ld(x), _stream(stream)))
+
+
+def moe_fp4_quantize_weights(w, fmt, row_map, q, sf, scale=None, stream=None):
+    """w bf16 [E, K, N] contiguous -> q uint8 [E, N, K / 2], sf uint8 scale atoms."""
+    E, K, N = w.shape
+    assert w.is_contiguous() and q.is_contiguous(), "contiguous tensors only"
+    _check(LIB.moe_fp4_quantize_weights(_ptr(w), E, K, N, fmt, row_map, _ptr(scale), _ptr(q),
+                                        _ptr(sf), sf.numel(), _stream(stream)))
+
+
+def moe_fp4_arrange_scales(scales, cols, fmt, row_map, E, sf, stream=None):
+    """scales uint8 [rows, cols / block] in row order -> sf uint8 scale atoms."""
+    assert scales.is_contiguous(), "contiguous tensors only"
+    rows = scales.numel() // (cols // (16 if fmt == FP4_NV else 32))
+    _check(LIB.moe_fp4_arrange_scales(_ptr(scales), rows, cols, fmt, row_map, E, _ptr(sf),
+                                      sf.numel(), _stream(stream)))
+
+
+def moe_gmm_fp4(A, sfa, B, sfb, fmt, group_offsets, K=None, epilogue=EPI_NONE, C=None, Q2=None,
+                sf2=None, a_scale=None, b_scale=None, q2_scale=None, dev_status=None, stream=None):
+    """A uint8 codes [rows_cap, K / 2], B uint8 codes [E, N, K / 2]; C bf16 or fp32 (optional
+    bf16 H with the SwiGLU epilogue), Q2 uint8 codes of Act [rows_cap, F / 2]."""
+    E, N, kb = B.shape
+    K = 2 * kb if K is None else K
+    c_dtype = DTYPE_F32 if C is not None and C.dtype == torch.float32 else DTYPE_BF16
+    _check(LIB.moe_gmm_fp4(_ptr(A), _ld(A), _ptr(sfa), _ptr(a_scale), _ptr(B), B.stride(1),
+                           B.stride(0), _ptr(sfb), _ptr(b_scale), fmt, _ptr(group_offsets), E,
+                           A.shape[0], K, N, epilogue, _ptr(C), c_dtype,
+                           _ld(C) if C is not None else 0, _ptr(Q2),
+                           _ld(Q2) if Q2 is not None else 0, _ptr(sf2),
+                           sf2.numel() if sf2 is not None else 0, _ptr(q2_scale),
+                           _ptr(dev_status), _stream(stream)))
+
+
+# -------------------------------------------------- activation checkpoints in 8 bits
+def _offsets(group_offsets):
+    return _ptr(group_offsets), 0 if group_offsets is None else group_offsets.shape[0] - 1
+
+
+def moe_act8_quantize(x, q, scales, group_offsets=None, stream=None):
+    """x bf16 [rows, cols] -> q int8 [rows, cols], scales bf16 [rows, ceil(cols / 32)]."""
+    rows, cols = x.shape
+    _check(LIB.moe_act8_quantize(_ptr(x), _ld(x), rows, cols, *_offsets(group_offsets), _ptr(q),
+                                 _ld(q), _ptr(scales), _ld(scales), _stream(stream)))
+
+
+def moe_act8_dequantize(q, scales, x, group_offsets=None, stream=None):
+    """The values of the codes, in x bf16 [rows, cols]."""
+    rows, cols = x.shape
+    _check(LIB.moe_act8_dequantize(_ptr(q), _ld(q), _ptr(scales), _ld(scales), rows, cols,
+                                   *_offsets(group_offsets), _ptr(x), _ld(x), _stream(stream)))
+
+
+def moe_act8_swiglu_fwd(h, act, q, scales, group_offsets=None, stream=None):
+    """h bf16 [rows, 2F] -> act bf16 [rows, F], q int8 [rows, 2F], scales bf16
+    [rows, 2 ceil(F / 32)]."""
+    rows, F = act.shape
+    _check(LIB.moe_act8_swiglu_fwd(_ptr(h), _ld(h), rows, F, *_offsets(group_offsets), _ptr(act),
+                                   _ld(act), _ptr(q), _ld(q), _ptr(scales), _ld(scales),
+                                   _stream(stream)))
+
+
+def moe_act8_swiglu_bwd(q, scales, dact, dh, act=None, group_offsets=None, stream=None):
+    """Codes of h and dact bf16 [rows, F] -> dh bf16 [rows, 2F], act bf16 [rows, F]."""
+    rows, F = dact.shape
+    _check(LIB.moe_act8_swiglu_bwd(_ptr(q), _ld(q), _ptr(scales), _ld(scales), _ptr(dact),
+                                   _ld(dact), rows, F, *_offsets(group_offsets), _ptr(dh),
+                                   _ld(dh), _ptr(act), _ld(act) if act is not None else 0,
+                                   _stream(stream)))
 
 
 # ------------------------------------------------------------ expert parallelism

@@ -1,0 +1,375 @@
+// Microscaled 4-bit floating point: quantisation of activations (gathered
+// through the permutation in the same pass) and weights, the scale layout the
+// tensor cores read, and the way back.
+//
+// Two formats, both with E2M1 elements (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign),
+// packed two a byte, the even column in the low nibble:
+//   MXFP4  blocks of 32 along a row, scale 2^s as E8M0 (OCP Microscaling v1.0):
+//          s = floor(log2 max|x|) - 2
+//   NVFP4  blocks of 16, scale E4M3(max|x| / (6 g)), and one fp32 scale g of
+//          the tensor (or of each expert's weight); an element's value is
+//          code * scale * g
+// Elements round to nearest even and saturate.  A block that holds a NaN or an
+// infinity takes a NaN scale and zero codes, and reads as NaN.
+//
+// Scales sit in 512-byte atoms of 128 rows x 4 blocks, which tcgen05.cp brings
+// to tensor memory as they are: row r0 + 32 r1, block j at byte 16 r0 + 4 r1 +
+// j; the atoms of a row of atoms follow one another, ceil(cols / (4 block)) of
+// them, the last one's spare blocks zero.  Row maps: GROUPED (activations, each
+// group padded to whole atoms), TILES and SWIGLU (weights, 192 rows of an
+// expert to two atoms).
+#include <algorithm>
+
+#include "internal.h"
+#include "lowbit.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kUnroll = 4;  // chunks of 256 columns a warp holds at a time
+constexpr int kMaxE = 256;
+
+// Padded row of row r of rows = E G under the maps that need no offsets.
+MOE_DEVINL int64_t weight_row(int64_t r, int64_t G, int row_map) {
+  const int64_t e = r / G, n = r - e * G;
+  if (row_map == MOE_MX_ROWS_SWIGLU) {
+    const int64_t F = G / 2;
+    const int64_t m = n < F ? n : n - F;
+    return (e * ((F + 95) / 96) + m / 96) * 256 + (n < F ? 0 : 96) + m % 96;
+  }
+  return (e * ((G + 191) / 192) + n / 192) * 256 + n % 192;
+}
+
+// The groups' first rows and their padded starts (sizes rounded up to 128), by
+// the first warp of a block.  The offsets are clamped to [0, rows] and to their
+// running maximum, so that a bad table names no row or atom that is not there.
+struct Groups {
+  int off[kMaxE + 1];
+  int pad[kMaxE];
+};
+
+MOE_DEVINL void scan_groups(Groups &gr, const int32_t *offsets, int E, int64_t rows) {
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    auto offset = [&](int e) {
+      return (int)min(max((int64_t)__ldg(offsets + e), (int64_t)0), rows);
+    };
+    int top = offset(0), carry = 0;  // running maximum, padded rows so far
+    for (int c0 = 0; c0 < E; c0 += 32) {
+      const int e = c0 + lane;
+      int hi = e < E ? offset(e + 1) : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, hi, o);
+        if (lane >= o) hi = max(hi, y);
+      }
+      hi = max(hi, top);
+      int lo = __shfl_up_sync(0xffffffffu, hi, 1);
+      if (lane == 0) lo = top;
+      const int p = (hi - lo + 127) / 128 * 128;
+      int incl = p;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (e < E) {
+        gr.off[e] = lo;
+        gr.pad[e] = carry + incl - p;
+        if (e == E - 1) gr.off[E] = hi;
+      }
+      carry += __shfl_sync(0xffffffffu, incl, 31);
+      top = __shfl_sync(0xffffffffu, hi, 31);
+    }
+  }
+}
+
+// Padded row of row r < off[E]: in the last group that starts at or before it
+// (-1 before the first group).
+MOE_DEVINL int64_t grouped_row(const Groups &gr, int E, int64_t r) {
+  int lo = 0, hi = E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (gr.off[mid] <= r) lo = mid;
+    else hi = mid - 1;
+  }
+  return gr.off[lo] <= r ? gr.pad[lo] + (r - gr.off[lo]) : -1;
+}
+
+// The scale codes of a warp's chunk (the lane's block code in c) as the words
+// of its atoms: a word is 4 blocks, 8 lanes of two per block (NVFP4) or 16
+// lanes of four (MXFP4); every lane of a word returns it.
+template <int FMT>
+MOE_DEVINL uint32_t scale_word(uint32_t c, int lane) {
+  constexpr int kSh = FMT == MOE_FP4_NV ? 1 : 2;  // log2 of lanes a block
+  uint32_t v = c << (8 * ((lane >> kSh) & 3));
+  v |= __shfl_xor_sync(0xffffffffu, v, 1 << kSh);
+  v |= __shfl_xor_sync(0xffffffffu, v, 2 << kSh);
+  return v;
+}
+
+// One warp: one row, up to 4 chunks of 256 columns (a lane 8 of them, 16 bytes
+// in, 4 bytes of codes out), so that a row's loads are all in flight together
+// and every access is coalesced.
+template <int FMT, bool GROUPED>
+__global__ void __launch_bounds__(kThreads)
+fp4_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t src_rows,
+                    const int32_t *__restrict__ row_index, int index_div, int64_t rows, int cols,
+                    int row_map, const int32_t *__restrict__ offsets, int E,
+                    const float *__restrict__ gscale, uint8_t *__restrict__ q, int64_t ldq,
+                    uint8_t *__restrict__ sf, int32_t *dev_status) {
+  __shared__ Groups gr;
+  const int lane = threadIdx.x & 31;
+  const int segs = (cols + 256 * kUnroll - 1) / (256 * kUnroll);
+  const int ac = (cols + fp4_atom_cols(FMT) - 1) / fp4_atom_cols(FMT);
+  const int64_t G = rows / max(E, 1);
+  int64_t R = rows;
+  if (GROUPED) {
+    scan_groups(gr, offsets, E, rows);
+    __syncthreads();
+    R = gr.off[E];
+  }
+  const int64_t warp = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
+  const int64_t warps = (int64_t)gridDim.x * kWarps;
+  for (int64_t it = warp; it < R * segs; it += warps) {
+    const int64_t r = it / segs;
+    const int c0 = (int)(it - r * segs) * (256 * kUnroll) + lane * 8;
+    int64_t src = r;
+    if (row_index != nullptr) {
+      const int i = __ldg(row_index + r);
+      src = i < 0 ? -1 : i / index_div;
+      if (src >= src_rows) {
+        if (lane == 0) moe_set_status(dev_status, MOE_ERR_DEVICE);
+        src = -1;
+      }
+    }
+    uint4 w[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (src >= 0 && c0 + 256 * i < cols) w[i] = ld_nc_v4(x + src * ldx + c0 + 256 * i);
+    }
+    const float g = FMT != MOE_FP4_NV || gscale == nullptr ? 1.0f
+                    : __ldg(gscale + (GROUPED ? 0 : r / G));
+    const int64_t pr = GROUPED ? grouped_row(gr, E, r) : weight_row(r, G, row_map);
+    if (pr < 0) continue;
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int c = c0 + 256 * i;
+      if (c - lane * 8 >= cols) break;  // the whole chunk
+      uint32_t a = amax_bits8(w[i]);
+      a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+      if (FMT != MOE_FP4_NV) a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+      float t, inv, v[8];
+      uint32_t code = fp4_block_scale<FMT>(__uint_as_float(a << 16), g, t, inv);
+      if (c >= cols) code = 0;
+      bf16x8_to_f32(w[i], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = fp4_quotient<FMT>(v[j], t, inv);
+      uint32_t codes = cvt_e2m1x8(v);
+      if (inv == 0.0f) codes = 0;  // (a NaN times 0 is no zero code)
+      if (c < cols) *reinterpret_cast<uint32_t *>(q + r * ldq + (c >> 1)) = codes;
+      const uint32_t word = scale_word<FMT>(code, lane);
+      constexpr int kLanes = FMT == MOE_FP4_NV ? 8 : 16;  // lanes of a word
+      if (lane % kLanes == 0 && c < cols)
+        *reinterpret_cast<uint32_t *>(sf + fp4_scale_byte(pr, c / fp4_block(FMT), ac)) = word;
+    }
+  }
+}
+
+// The way back: values (code * scale * g, rounded once to bf16).
+template <int FMT, bool GROUPED>
+__global__ void __launch_bounds__(kThreads)
+fp4_dequantize_kernel(const uint8_t *__restrict__ q, int64_t ldq, const uint8_t *__restrict__ sf,
+                      int64_t rows, int cols, int row_map, const int32_t *__restrict__ offsets,
+                      int E, const float *__restrict__ gscale, uint16_t *__restrict__ x,
+                      int64_t ldx) {
+  __shared__ Groups gr;
+  const int lane = threadIdx.x & 31;
+  const int segs = (cols + 256 * kUnroll - 1) / (256 * kUnroll);
+  const int ac = (cols + fp4_atom_cols(FMT) - 1) / fp4_atom_cols(FMT);
+  const int64_t G = rows / max(E, 1);
+  int64_t R = rows;
+  if (GROUPED) {
+    scan_groups(gr, offsets, E, rows);
+    __syncthreads();
+    R = gr.off[E];
+  }
+  const int64_t warp = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
+  const int64_t warps = (int64_t)gridDim.x * kWarps;
+  for (int64_t it = warp; it < R * segs; it += warps) {
+    const int64_t r = it / segs;
+    const int c0 = (int)(it - r * segs) * (256 * kUnroll) + lane * 8;
+    const int64_t pr = GROUPED ? grouped_row(gr, E, r) : weight_row(r, G, row_map);
+    if (pr < 0) continue;
+    uint32_t w[kUnroll], s[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int c = c0 + 256 * i;
+      w[i] = s[i] = 0;
+      if (c < cols) {
+        w[i] = __ldg(reinterpret_cast<const uint32_t *>(q + r * ldq + (c >> 1)));
+        s[i] = __ldg(sf + fp4_scale_byte(pr, c / fp4_block(FMT), ac));
+      }
+    }
+    const float g = FMT != MOE_FP4_NV || gscale == nullptr ? 1.0f
+                    : __ldg(gscale + (GROUPED ? 0 : r / G));
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int c = c0 + 256 * i;
+      if (c < cols) {
+        float v[8];
+        e2m1x8_to_f32(w[i], v);
+        const float t = fp4_scale_value(s[i], FMT);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = v[j] * t * g;
+        st_v4(x + r * ldx + c, f32_to_bf16x8(v));
+      }
+    }
+  }
+}
+
+// Weights w [E, K, N] (contraction down the rows) to K-major codes [E, N, K]:
+// a block transposes 64 x 64 elements through shared memory; a thread then
+// quantises 32 consecutive k of one column.  Run once when weights are laid out.
+constexpr int kWT = 64;
+
+template <int FMT>
+__global__ void __launch_bounds__(128)
+fp4_quantize_weights_kernel(const uint16_t *__restrict__ w, int K, int N, int row_map,
+                            const float *__restrict__ gscale, uint8_t *__restrict__ q,
+                            uint8_t *__restrict__ sf) {
+  __shared__ uint16_t tile[kWT][kWT + 2];
+  const int e = blockIdx.z, k0 = blockIdx.y * kWT, n0 = blockIdx.x * kWT;
+  const uint16_t *src = w + (int64_t)e * K * N;
+  for (int i = threadIdx.x; i < kWT * kWT; i += 128) {
+    const int kk = i / kWT, nn = i % kWT;
+    tile[kk][nn] = k0 + kk < K && n0 + nn < N ? src[(int64_t)(k0 + kk) * N + n0 + nn] : 0;
+  }
+  __syncthreads();
+  const int nn = threadIdx.x & 63, kb = (threadIdx.x >> 6) * 32;
+  const int n = n0 + nn, k = k0 + kb;
+  if (n >= N) return;
+  constexpr int kB = fp4_block(FMT);
+  const int ac = (K + fp4_atom_cols(FMT) - 1) / fp4_atom_cols(FMT);
+  const int64_t pr = weight_row((int64_t)e * N + n, N, row_map);
+  const float g = FMT != MOE_FP4_NV || gscale == nullptr ? 1.0f : __ldg(gscale + e);
+  uint32_t codes[4];
+#pragma unroll
+  for (int b = 0; b < 32 / kB; ++b) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int j = 0; j < kB; ++j) a = max(a, (uint32_t)tile[kb + b * kB + j][nn] & 0x7FFFu);
+    float t, inv, v[kB];
+    const uint32_t code = fp4_block_scale<FMT>(__uint_as_float(a << 16), g, t, inv);
+#pragma unroll
+    for (int j = 0; j < kB; ++j)
+      v[j] = fp4_quotient<FMT>(__uint_as_float((uint32_t)tile[kb + b * kB + j][nn] << 16), t, inv);
+#pragma unroll
+    for (int j = 0; j < kB / 8; ++j)
+      codes[b * (kB / 8) + j] = inv == 0.0f ? 0u : cvt_e2m1x8(v + 8 * j);
+    const int blk = k / kB + b;
+    if (blk < 4 * ac) sf[fp4_scale_byte(pr, blk, ac)] = k < K ? (uint8_t)code : (uint8_t)0;
+  }
+  if (k < K)
+    *reinterpret_cast<uint4 *>(q + ((int64_t)e * N + n) * (K / 2) + k / 2) =
+        make_uint4(codes[0], codes[1], codes[2], codes[3]);
+  // the spare blocks of the last atom past this tile's columns (MXFP4 atoms
+  // hold two tiles): zero
+  if (kb == 0 && k0 + kWT >= K)
+    for (int blk = (k0 + kWT) / kB; blk < 4 * ac; ++blk) sf[fp4_scale_byte(pr, blk, ac)] = 0;
+}
+
+// Row-order scales [rows, nb] of a 4-bit checkpoint into atoms (a thread one
+// word of 4 blocks).
+__global__ void __launch_bounds__(kThreads)
+fp4_arrange_scales_kernel(const uint8_t *__restrict__ s, int64_t rows, int nb, int64_t G,
+                          int row_map, uint8_t *__restrict__ sf) {
+  const int ac = (nb + 3) / 4;
+  const int64_t stride = (int64_t)gridDim.x * kThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < rows * ac; i += stride) {
+    const int64_t r = i / ac;
+    const int b = (int)(i - r * ac) * 4;
+    uint32_t w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (b + j < nb) w |= (uint32_t)__ldg(s + r * nb + b + j) << (8 * j);
+    *reinterpret_cast<uint32_t *>(sf + fp4_scale_byte(weight_row(r, G, row_map), b, ac)) = w;
+  }
+}
+
+// All resident at once (a persistent walk over rows and segments).
+int grid_for(int64_t rows, int cols) {
+  const int64_t warps = rows * ((cols + 256 * kUnroll - 1) / (256 * kUnroll));
+  return (int)std::max<int64_t>(
+      1, std::min<int64_t>((warps + kWarps - 1) / kWarps, (int64_t)num_sms() * 8));
+}
+
+}  // namespace
+
+int64_t fp4_atom_rows(int64_t rows, int row_map, int E) {
+  const int64_t G = rows / E;
+  if (row_map == MOE_MX_ROWS_GROUPED) return f8_padded_rows(rows, E) / 128;
+  if (row_map == MOE_MX_ROWS_SWIGLU) return 2 * (int64_t)E * ((G / 2 + 95) / 96);
+  return 2 * (int64_t)E * ((G + 191) / 192);
+}
+
+cudaError_t launch_fp4_quantize(const uint16_t *x, int64_t ldx, int64_t src_rows,
+                                const int32_t *row_index, int index_div, int64_t rows, int cols,
+                                int fmt, int row_map, const int32_t *offsets, int E,
+                                const float *gscale, uint8_t *q, int64_t ldq, uint8_t *sf,
+                                int32_t *dev_status, cudaStream_t st) {
+  const int grid = grid_for(rows, cols);
+  const bool grouped = row_map == MOE_MX_ROWS_GROUPED;
+  auto run = [&](auto kernel) {
+    kernel<<<grid, kThreads, 0, st>>>(x, ldx, src_rows, row_index, index_div, rows, cols, row_map,
+                                      offsets, E, gscale, q, ldq, sf, dev_status);
+    return cudaGetLastError();
+  };
+  if (fmt == MOE_FP4_NV)
+    return grouped ? run(fp4_quantize_kernel<MOE_FP4_NV, true>)
+                   : run(fp4_quantize_kernel<MOE_FP4_NV, false>);
+  return grouped ? run(fp4_quantize_kernel<MOE_FP4_MX, true>)
+                 : run(fp4_quantize_kernel<MOE_FP4_MX, false>);
+}
+
+cudaError_t launch_fp4_dequantize(const uint8_t *q, int64_t ldq, const uint8_t *sf, int64_t rows,
+                                  int cols, int fmt, int row_map, const int32_t *offsets, int E,
+                                  const float *gscale, uint16_t *x, int64_t ldx,
+                                  cudaStream_t st) {
+  const int grid = grid_for(rows, cols);
+  const bool grouped = row_map == MOE_MX_ROWS_GROUPED;
+  auto run = [&](auto kernel) {
+    kernel<<<grid, kThreads, 0, st>>>(q, ldq, sf, rows, cols, row_map, offsets, E, gscale, x, ldx);
+    return cudaGetLastError();
+  };
+  if (fmt == MOE_FP4_NV)
+    return grouped ? run(fp4_dequantize_kernel<MOE_FP4_NV, true>)
+                   : run(fp4_dequantize_kernel<MOE_FP4_NV, false>);
+  return grouped ? run(fp4_dequantize_kernel<MOE_FP4_MX, true>)
+                 : run(fp4_dequantize_kernel<MOE_FP4_MX, false>);
+}
+
+cudaError_t launch_fp4_quantize_weights(const uint16_t *w, int E, int K, int N, int fmt,
+                                        int row_map, const float *gscale, uint8_t *q, uint8_t *sf,
+                                        cudaStream_t st) {
+  const dim3 grid((N + kWT - 1) / kWT, (K + kWT - 1) / kWT, E);
+  if (fmt == MOE_FP4_NV)
+    fp4_quantize_weights_kernel<MOE_FP4_NV><<<grid, 128, 0, st>>>(w, K, N, row_map, gscale, q, sf);
+  else
+    fp4_quantize_weights_kernel<MOE_FP4_MX><<<grid, 128, 0, st>>>(w, K, N, row_map, gscale, q, sf);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fp4_arrange_scales(const uint8_t *s, int64_t rows, int nb, int E, int row_map,
+                                      uint8_t *sf, cudaStream_t st) {
+  const int64_t words = rows * ((nb + 3) / 4);
+  const int grid = (int)std::max<int64_t>(
+      1, std::min<int64_t>((words + kThreads - 1) / kThreads, (int64_t)num_sms() * 8));
+  fp4_arrange_scales_kernel<<<grid, kThreads, 0, st>>>(s, rows, nb, rows / E, row_map, sf);
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -165,4 +165,49 @@ struct TgmmMxArgs {
 };
 moe_status_t launch_tgmm_mx(const TgmmMxArgs &a, cudaStream_t s);
 
+// fp4.cu (4-bit block-scaled formats: quantisers, scale layout)
+int64_t fp4_atom_rows(int64_t rows, int row_map, int E);
+cudaError_t launch_fp4_quantize(const uint16_t *x, int64_t ldx, int64_t src_rows,
+                                const int32_t *row_index, int index_div, int64_t rows, int cols,
+                                int fmt, int row_map, const int32_t *offsets, int E,
+                                const float *gscale, uint8_t *q, int64_t ldq, uint8_t *sf,
+                                int32_t *dev_status, cudaStream_t s);
+cudaError_t launch_fp4_dequantize(const uint8_t *q, int64_t ldq, const uint8_t *sf, int64_t rows,
+                                  int cols, int fmt, int row_map, const int32_t *offsets, int E,
+                                  const float *gscale, uint16_t *x, int64_t ldx, cudaStream_t s);
+cudaError_t launch_fp4_quantize_weights(const uint16_t *w, int E, int K, int N, int fmt,
+                                        int row_map, const float *gscale, uint8_t *q, uint8_t *sf,
+                                        cudaStream_t s);
+cudaError_t launch_fp4_arrange_scales(const uint8_t *scales, int64_t rows, int nb, int E,
+                                      int row_map, uint8_t *sf, cudaStream_t s);
+
+// gmm_fp4_sm103.cu
+struct GmmFp4Args {
+  const uint8_t *A; int64_t lda; const uint8_t *sfa; const float *ga;
+  const uint8_t *B; int64_t ldb; int64_t stride_b; const uint8_t *sfb; const float *gb;
+  int fmt;
+  const int32_t *offsets; int E; int64_t rows_cap; int K; int N;
+  int epilogue;
+  void *C; int c_dtype; int64_t ldc;
+  uint8_t *Q2; int64_t ldq2; uint8_t *sf2; const float *g2;  // SwiGLU: codes of Act
+  int32_t *dev_status;
+};
+moe_status_t launch_gmm_fp4(const GmmFp4Args &a, cudaStream_t s);
+
+// act8.cu (8-bit activation checkpoints)
+cudaError_t launch_act8_quantize(const uint16_t *x, int64_t ldx, int64_t rows, int cols,
+                                 const int32_t *offsets, int E, int8_t *q, int64_t ldq,
+                                 uint16_t *s, int64_t lds, cudaStream_t st);
+cudaError_t launch_act8_dequantize(const int8_t *q, int64_t ldq, const uint16_t *s, int64_t lds,
+                                   int64_t rows, int cols, const int32_t *offsets, int E,
+                                   uint16_t *x, int64_t ldx, cudaStream_t st);
+cudaError_t launch_act8_swiglu_fwd(const uint16_t *h, int64_t ldh, int64_t rows, int F,
+                                   const int32_t *offsets, int E, uint16_t *act, int64_t lda,
+                                   int8_t *q, int64_t ldq, uint16_t *s, int64_t lds,
+                                   cudaStream_t st);
+cudaError_t launch_act8_swiglu_bwd(const int8_t *q, int64_t ldq, const uint16_t *s, int64_t lds,
+                                   const uint16_t *dact, int64_t ldda, int64_t rows, int F,
+                                   const int32_t *offsets, int E, uint16_t *dh, int64_t lddh,
+                                   uint16_t *act, int64_t lda, cudaStream_t st);
+
 }  // namespace moe

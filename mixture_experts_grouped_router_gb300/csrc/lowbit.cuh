@@ -1,0 +1,130 @@
+// Device helpers of the low-bit formats: E2M1 codes with block scales (MXFP4,
+// NVFP4) and 8-bit integer codes with one bf16 scale per 32 elements.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace moe {
+
+// Elements per scale of a 4-bit format, and columns per 512-byte scale atom
+// (128 rows x 4 blocks).
+__host__ __device__ constexpr int fp4_block(int fmt) { return fmt == MOE_FP4_NV ? 16 : 32; }
+__host__ __device__ constexpr int fp4_atom_cols(int fmt) { return 4 * fp4_block(fmt); }
+
+// Byte of (padded row pr, block b) in scale atoms of `ac` atom columns.
+MOE_DEVINL int64_t fp4_scale_byte(int64_t pr, int b, int ac) {
+  const int rw = (int)(pr & 127);
+  return ((pr >> 7) * ac + (b >> 2)) * 512 + (rw & 31) * 16 + (rw >> 5) * 4 + (b & 3);
+}
+
+// 8 values -> 8 E2M1 codes (round to nearest even, saturated at 6), value 2i in
+// the low nibble of byte i.
+MOE_DEVINL uint32_t cvt_e2m1x8(const float *v) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+// 8 E2M1 codes -> 8 values (exact).
+MOE_DEVINL void e2m1x8_to_f32(uint32_t c, float *v) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(c));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+    v[2 * i] = t.x;
+    v[2 * i + 1] = t.y;
+  }
+}
+
+// E4M3 code of v >= 0 (round to nearest even, saturated at 448) and its value.
+MOE_DEVINL uint32_t e4m3_code(float v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
+  return r & 0xFFu;
+}
+
+MOE_DEVINL float e4m3_value(uint32_t code) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)code));
+  return __half2float(__ushort_as_half((uint16_t)(h & 0xFFFFu)));
+}
+
+// 2^(code - 127), code 255: NaN.
+MOE_DEVINL float e8m0_value(uint32_t code) {
+  if (code == 255u) return __uint_as_float(0x7FC00000u);
+  return __uint_as_float(code > 0 ? code << 23 : 1u << 22);
+}
+
+MOE_DEVINL float fp4_scale_value(uint32_t code, int fmt) {
+  return fmt == MOE_FP4_NV ? e4m3_value(code) : e8m0_value(code);
+}
+
+// Scale code of a block with largest magnitude a, and the reciprocal pair that
+// divides its elements: t is the block's scale (times g for NVFP4), inv = 1/t,
+// or 0 where every code of the block is 0 (no magnitude, or a NaN / infinity,
+// which takes the NaN scale).
+//   MXFP4: t = 2^s, s = floor(log2 a) - 2 clamped to [-127, 127] (OCP MX v1.0)
+//   NVFP4: E4M3(a / (6 g)), g the tensor's fp32 scale
+template <int FMT>
+MOE_DEVINL uint32_t fp4_block_scale(float a, float g, float &t, float &inv) {
+  t = 1.0f;
+  inv = 0.0f;
+  const bool finite = a <= 3.402823466e38f;
+  if (FMT == MOE_FP4_NV) {
+    if (!finite) return 0x7Fu;
+    const uint32_t code = e4m3_code(__fdiv_rn(a, 6.0f * g));
+    const float s = e4m3_value(code) * g;
+    if (s >= 1.17549435e-38f) {
+      t = s;
+      inv = __frcp_rn(s);
+    }
+    return code;
+  }
+  if (!finite) return 0xFFu;
+  if (!(a > 0.0f)) return 0u;
+  const uint32_t b = __float_as_uint(a);
+  const int e = (b >> 23) != 0 ? (int)(b >> 23) - 127 : (31 - __clz(b)) - 149;
+  const int s = max(-127, e - 2);
+  inv = __uint_as_float((uint32_t)(127 - s) << 23);
+  t = 0.0f;  // unused: products with a power of two are exact
+  return (uint32_t)(s + 127);
+}
+
+// x / t by a reciprocal and one residual step: where x / t is representable
+// (a tie of the code grid, for bf16 x and scales of few bits) the result is
+// exact, so that ties round as the quotient's definition says.
+MOE_DEVINL float div_exact(float x, float t, float inv) {
+  const float q = x * inv;
+  return fmaf(fmaf(-q, t, x), inv, q);
+}
+
+template <int FMT>
+MOE_DEVINL float fp4_quotient(float x, float t, float inv) {
+  return FMT == MOE_FP4_NV ? div_exact(x, t, inv) : x * inv;
+}
+
+// Largest magnitude of 8 bf16 values, as bf16 bits: compared as integers, so
+// that a NaN or an infinity wins.
+MOE_DEVINL uint32_t amax_bits8(const uint4 &w) {
+  const uint32_t m = 0x7FFF7FFFu;
+  const uint32_t a = __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
+  return max(a & 0xFFFFu, a >> 16);
+}
+
+}  // namespace moe

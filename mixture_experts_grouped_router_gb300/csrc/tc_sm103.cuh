@@ -324,6 +324,42 @@ MOE_DEVINL void umma_mxf8_2sm(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, u
       : "memory");
 }
 
+// Instruction descriptor of kind::mxf4nvf4 with block scaling, fp32
+// accumulation, both operands K-major E2M1 (format 1): bits 4-5 and 29-30 the
+// first byte of B's / A's 32-bit scale words that this MMA uses (scale_vec::4X
+// takes the whole word, id 0; scale_vec::2X two bytes, id 0 or 2), 23 scale
+// format (0 = UE4M3, 1 = UE8M0), 17-22 N >> 3, 27-28 M >> 7, 31 K (0 = 64).
+__host__ __device__ constexpr uint32_t idesc_fp4(int M, int N, bool nv, int sf_id) {
+  return (static_cast<uint32_t>(sf_id) << 4) | (1u << 7) | (1u << 10) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(!nv) << 23) |
+         (static_cast<uint32_t>(M >> 7) << 27) | (static_cast<uint32_t>(sf_id) << 29);
+}
+
+// 4-bit block-scaled MMA over both CTAs of the pair (K = 64 codes): one E4M3
+// scale per 16 codes (NV) or one E8M0 scale per 32.
+template <bool NV>
+MOE_DEVINL void umma_fp4_2sm(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                             uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  if (NV)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem),
+        "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem),
+        "r"(accumulate)
+        : "memory");
+}
+
 // Tensor-memory columns for the CTA pair (warp-collective, both CTAs), the
 // permit release after it, and the matching deallocation.
 MOE_DEVINL void tmem_alloc_2sm(uint32_t *dst_smem, uint32_t ncols) {
