@@ -149,15 +149,22 @@ def _check(status: int):
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    return ctypes.c_void_p(t.data_ptr())
+    # a plain int: the argument types turn it into a pointer
+    return None if t is None else t.data_ptr()
+
+
+try:  # the current stream's handle without a Stream object around it (3 us a call)
+    _raw_stream, _raw_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+except AttributeError:  # a torch built without CUDA
+    _raw_stream = _raw_device = None
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(_raw_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _ld(t):

@@ -21,8 +21,13 @@
 //   warps 2-5  epilogue, one per quarter of the tensor-memory lanes
 // Tensor memory: two accumulators of 192 columns, and scale slots in the 128
 // columns that they leave: 48 columns a K block (NVFP4, 2 slots) or 24 (MXFP4,
-// 5).  A slot is rewritten after the MMAs that read it are done: the issuer
-// waits for the release of the stage that it last served.
+// 5).  A slot is rewritten after the MMAs that read it are done: their commit
+// arrives on the full barrier of the K block that takes the slot next, beside the
+// stage's copies, so that the issuer has one barrier to wait for.  That wait and
+// the issue set the pace (a K block's MMAs take about 300 cycles): the next
+// barrier is tested before a block's MMAs are issued, and the issuing warp stays
+// uniform, elect_one() choosing the lane.  8 experts, 32768 rows, 4096 x 28672:
+// lane == 0 in place of elect_one() 2.41 ms, a second wait for the slot 1.36 ms.
 // Every wait is bounded; on time-out the CTA winds down and reports
 // MOE_ERR_TIMEOUT through dev_status.
 #include <cudaTypedefs.h>
@@ -60,6 +65,7 @@ struct Lay {
   static constexpr int stage_bytes = (tx_bytes + 1023) / 1024 * 1024;
   static constexpr int sf_cols = atoms * 12;               // tensor-memory columns a slot
   static constexpr int sf_slots = (kTmemCols - 2 * BN) / sf_cols;
+  static_assert(sf_slots <= kStages, "a commit names a K block's next user by its stage");
   static constexpr int stg_offset = kStages * stage_bytes;
   static constexpr int book_offset = stg_offset + kEpiWarps * kStgBytes;
 };
@@ -134,6 +140,12 @@ MOE_DEVINL TileInfo decode_tile(const Book &bk, const Fp4Params &p, int t, int c
   return ti;
 }
 
+// Rows of A that a CTA loads for a tile of `valid` rows, in boxes of 32 (the
+// others keep what the stage held: their products are not stored).
+MOE_DEVINL int rows_loaded(int valid) {
+  return valid > BM - 32 ? BM : valid > 0 ? (valid + 31) / 32 * 32 : 0;
+}
+
 // ---------------------------------------------------------------- epilogue
 // One thread's 32-value row segment staged as the TMA store reads it (64-byte
 // swizzle for bf16, 128-byte for fp32).
@@ -191,6 +203,7 @@ MOE_DEVINL void epilogue(const Book &bk, const Fp4Params &p, const TileInfo &ti,
   const int64_t row = (int64_t)wrow0 + lane;
   const bool valid = row < ti.row_end;
   const bool bulk = wrow0 + 32 <= ti.row_end;
+  if (wrow0 >= ti.row_end) return;  // no row of this warp is the expert's
   if (EPI == MOE_EPI_SWIGLU_FWD) {
     const int F = p.F;
     const int n0 = ti.n_idx * (BN / 2);
@@ -308,14 +321,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gmm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                const __grid_constant__ CUtensorMap tmC0, const __grid_constant__ CUtensorMap tmC1,
-               const Fp4Params p) {
+               const __grid_constant__ CUtensorMap tmA32, const Fp4Params p) {
   using L = Lay<FMT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   Book &bk = *reinterpret_cast<Book *>(smem + L::book_offset);
   volatile int *abort_flag = &bk.abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = tc::uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int crank = (int)tc::cluster_ctarank();
   const int cid = (int)tc::cluster_id_x();
   const int ncl = (int)tc::nclusters_x();
@@ -324,7 +337,7 @@ gmm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      tc::mbar_init(&bk.full[s], 1);
+      tc::mbar_init(&bk.full[s], 2);  // the stage's copies, and a free scale slot
       tc::mbar_init(&bk.empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -379,11 +392,11 @@ gmm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   __syncthreads();
   tc::cluster_sync();
   tc::tc_fence_after();
-  const uint32_t tmem = bk.tmem_base;
-  const int total = bk.total_tiles;
+  const uint32_t tmem = (uint32_t)tc::uniform((int)bk.tmem_base);
+  const int total = tc::uniform(bk.total_tiles);
 
   if (warp == 0) {
-    if (lane == 0 && !p.stall_loads) {
+    if (!p.stall_loads) {
       uint32_t issued = 0;
       int s = 0;
       uint32_t ph = 0;
@@ -395,19 +408,32 @@ gmm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                              : ti.n_idx * BN + crank * (BN / 2);
         const int arow = (int)bk.poff[ti.e] + ti.m_idx;
         const int brow = 2 * (ti.e * p.n_tiles + ti.n_idx);
+        const int left = ti.row_end - ti.row0;  // rows from this CTA's first on
+        const int rows = rows_loaded(left);
+        // the leader's barrier counts the pair's copies
+        const int tx = 2 * (L::tx_bytes - A_BYTES) + (rows + rows_loaded(left - BM)) * kRowBytes;
         for (int kb = 0; kb < p.kblocks; ++kb) {
-          if (!tc::mbar_wait(&bk.empty[s], ph ^ 1, abort_flag, p.wait_limit_ns)) {
+          if (!tc::mbar_wait_warp(&bk.empty[s], ph ^ 1, abort_flag, p.wait_limit_ns)) {
             ok = false;
             break;
           }
-          uint8_t *sa = smem + s * L::stage_bytes;
-          const uint32_t fb = tc::mapa_shared(tc::smem_u32(&bk.full[s]), 0);
-          if (leader) tc::mbar_expect_tx(&bk.full[s], 2 * L::tx_bytes);
-          tc::tma_load_3d_2sm(sa, &tmA, fb, kb * kRowBytes, ti.row0, 0);
-          tc::tma_load_3d_2sm(sa + A_BYTES, &tmB, fb, kb * kRowBytes, nrow, ti.e);
-          tc::tma_load_3d_2sm(sa + A_BYTES + B_BYTES, &tmSA, fb, 0, kb * L::atoms, arow);
-          tc::tma_load_3d_2sm(sa + A_BYTES + B_BYTES + L::sfa_bytes, &tmSB, fb, 0, kb * L::atoms,
-                              brow);
+          if (tc::elect_one()) {
+            uint8_t *sa = smem + s * L::stage_bytes;
+            const uint32_t fb = tc::mapa_shared(tc::smem_u32(&bk.full[s]), 0);
+            if (leader) tc::mbar_expect_tx(&bk.full[s], tx);
+            if (rows == BM) {
+              tc::tma_load_3d_2sm(sa, &tmA, fb, kb * kRowBytes, ti.row0, 0);
+            } else {
+              for (int r = 0; r < rows; r += 32)
+                tc::tma_load_3d_2sm(sa + r * kRowBytes, &tmA32, fb, kb * kRowBytes, ti.row0 + r,
+                                    0);
+            }
+            tc::tma_load_3d_2sm(sa + A_BYTES, &tmB, fb, kb * kRowBytes, nrow, ti.e);
+            tc::tma_load_3d_2sm(sa + A_BYTES + B_BYTES, &tmSA, fb, 0, kb * L::atoms, arow);
+            tc::tma_load_3d_2sm(sa + A_BYTES + B_BYTES + L::sfa_bytes, &tmSB, fb, 0,
+                                kb * L::atoms, brow);
+          }
+          __syncwarp();
           ++issued;
           if (++s == kStages) {
             s = 0;
@@ -423,13 +449,15 @@ gmm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     }
   } else if (warp == 1 && leader) {
     uint32_t acc_it = 0;
-    uint32_t blk = 0;   // K blocks issued
-    int s = 0;
+    int s = 0;          // ring slot of the next K block
     uint32_t ph = 0;
-    uint32_t slot = 0;  // scale slot of the next K block
-    int os = 0;         // stage and pass of the K block that last used that slot
-    uint32_t oph = 0;
+    int slot = 0;       // its scale slot
+    bool ready = false; // its barrier has been seen complete
     bool ok = true;
+    // the first K blocks find their scale slots free
+    if (tc::elect_one())
+      for (int i = 0; i < L::sf_slots; ++i) tc::mbar_arrive(&bk.full[i]);
+    __syncwarp();
     for (int t = cid; t < total && ok; t += ncl) {
       const uint32_t a = acc_it & 1;
       const uint32_t aph = (acc_it >> 1) & 1;
@@ -437,22 +465,16 @@ gmm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       tc::tc_fence_after();
       const uint32_t d_tmem = tmem + a * BN;
       for (int kb = 0; kb < p.kblocks; ++kb) {
-        if (!tc::mbar_wait_warp(&bk.full[s], ph, abort_flag, p.wait_limit_ns)) {
+        if (!__all_sync(0xffffffffu, ready) &&
+            !tc::mbar_wait_warp(&bk.full[s], ph, abort_flag, p.wait_limit_ns)) {
           ok = false;
           break;
         }
-        if (blk >= (uint32_t)L::sf_slots) {
-          if (!tc::mbar_wait_warp(&bk.empty[os], oph, abort_flag, p.wait_limit_ns)) {
-            ok = false;
-            break;
-          }
-          if (++os == kStages) {
-            os = 0;
-            oph ^= 1;
-          }
-        }
+        const int s1 = s + 1 == kStages ? 0 : s + 1;
+        const uint32_t ph1 = s1 == 0 ? ph ^ 1 : ph;
+        ready = tc::mbar_test(&bk.full[s1], ph1);
         tc::tc_fence_after();
-        if (lane == 0) {
+        if (tc::elect_one()) {
           const uint32_t sa = tc::smem_u32(smem + s * L::stage_bytes);
           const uint64_t ad = tc::sdesc(sa, 16, 1024);
           const uint64_t bd = tc::sdesc(sa + A_BYTES, 16, 1024);
@@ -475,21 +497,21 @@ gmm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                                                sft + 12 * j, sft + 12 * j + 4, (kb | kk) != 0);
           }
           tc::umma_commit_2sm_mc(&bk.empty[s], kPair);
+          // this block's scale slot is free for the block sf_slots further
+          const int sn = s + L::sf_slots;
+          tc::umma_commit_2sm_mc(&bk.full[sn < kStages ? sn : sn - kStages], 0x1);
         }
         __syncwarp();
-        ++blk;
-        if (++slot == (uint32_t)L::sf_slots) slot = 0;
-        if (++s == kStages) {
-          s = 0;
-          ph ^= 1;
-        }
+        if (++slot == L::sf_slots) slot = 0;
+        s = s1;
+        ph = ph1;
       }
       if (!ok) break;
-      if (lane == 0) tc::umma_commit_2sm_mc(&bk.tfull[a], kPair);
+      if (tc::elect_one()) tc::umma_commit_2sm_mc(&bk.tfull[a], kPair);
       __syncwarp();
       ++acc_it;
     }
-    if (lane == 0) tc::umma_commit_2sm_mc(&bk.drain, 0x1);
+    if (tc::elect_one()) tc::umma_commit_2sm_mc(&bk.drain, 0x1);
     __syncwarp();
     tc::mbar_wait_drain(&bk.drain, 0, p.wait_limit_ns);
   } else if (warp >= 2) {
@@ -611,7 +633,8 @@ moe_status_t launch(const CUtensorMap *m, const Fp4Params &p, int64_t tiles_uppe
     return MOE_ERR_CUDA;
   }
   const int grid = 2 * (int)std::max<int64_t>(1, std::min<int64_t>(max_clusters, tiles_upper));
-  gmm_fp4_kernel<FMT, EPI><<<grid, kThreads, kSmem, s>>>(m[0], m[1], m[2], m[3], m[4], m[5], p);
+  gmm_fp4_kernel<FMT, EPI><<<grid, kThreads, kSmem, s>>>(m[0], m[1], m[2], m[3], m[4], m[5], m[6],
+                                                     p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     set_error("moe_gmm_fp4 launch: %s", cudaGetErrorString(e));
@@ -649,13 +672,14 @@ moe_status_t launch_gmm_fp4(const GmmFp4Args &a, cudaStream_t s) {
   p.dev_status = a.dev_status;
   p.wait_limit_ns = wait_limit_ns();
   p.stall_loads = test_stall_loads();
-  CUtensorMap m[6];
+  CUtensorMap m[7];
   const int64_t ac = (a.K + acols - 1) / acols;
   const int64_t stride_b = a.E > 1 ? a.stride_b : (int64_t)a.N * a.ldb;
   bool ok = make_code_map(&m[0], a.A, a.K / 2, a.rows_cap, a.lda, 1, a.rows_cap * a.lda, BM) &&
             make_code_map(&m[1], a.B, a.K / 2, a.N, a.ldb, a.E, stride_b, BN / 2) &&
             make_scale_map(&m[2], a.sfa, ac, p.atom_rows2, atoms, 1) &&
             make_scale_map(&m[3], a.sfb, ac, 2 * (int64_t)a.E * p.n_tiles, atoms, 2);
+  ok = ok && make_code_map(&m[6], a.A, a.K / 2, a.rows_cap, a.lda, 1, a.rows_cap * a.lda, 32);
   if (swiglu && a.C != nullptr) {
     const uint16_t *H = static_cast<const uint16_t *>(a.C);
     ok = ok && make_out_map(&m[4], H, false, p.F, a.rows_cap, a.ldc) &&

@@ -46,6 +46,23 @@ MOE_DEVINL bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Whether that phase has completed, without waiting.
+MOE_DEVINL bool mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+MOE_DEVINL void mbar_arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // Wait for the phase with the given parity to complete.  Gives up when the
 // CTA's abort flag is raised or after `limit_ns`; then raises the flag and
 // returns false so that every role of the CTA winds down.
@@ -242,6 +259,23 @@ MOE_DEVINL void st_cluster_zero16(uint32_t cluster_addr) {
   asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(cluster_addr), "r"(0u)
                : "memory");
 }
+
+// True in one lane of a converged warp.  Tensor-core and TMA instructions take
+// their operands from uniform registers: behind `if (elect_one())` in a warp whose
+// control flow and operands are uniform, the compiler keeps them there, where
+// behind `if (lane == 0)` it moves every operand of every instruction first.
+MOE_DEVINL bool elect_one() {
+  uint32_t pred;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(pred));
+  return pred != 0;
+}
+
+// A value that every lane holds alike, as one the compiler knows to be uniform.
+MOE_DEVINL int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // ------------------------------------------------- tcgen05 descriptors
 // Shared-memory matrix descriptor, 128-byte swizzle, descriptor version 1.
