@@ -637,6 +637,41 @@ moe_status_t moe_gmm_fp4(const uint8_t *A, int64_t lda, const uint8_t *sfa, cons
                          int64_t ldc, uint8_t *Q2, int64_t ldq2, uint8_t *sf2, size_t sf2_bytes,
                          const float *q2_scale, int32_t *dev_status, moe_stream_t stream);
 
+/*
+ * moe_fp4_experts -- the expert FFN on 4-bit codes in one call: moe_fp4_quantize
+ * of the permuted rows of x, moe_gmm_fp4 with the SwiGLU epilogue, moe_gmm_fp4:
+ *     y[p] = FFN_e(x[sorted_to_flat[p] / k])   for the rows p of group e
+ *   w   the weights: wi codes [E, 2f, d / 2] with atoms SWIGLU, wo codes
+ *       [E, d, f / 2] with atoms TILES (contiguous), their fp32 scales [E] or
+ *       NULL, the scales of x and of Act (fp32 [1] or NULL)
+ *   b   buffers for rows_cap permuted rows: codes and atoms (GROUPED) of x and of
+ *       Act, y bf16 [rows_cap, d]; h bf16 [rows_cap, 2f] or NULL
+ *   x bf16 [T, ldx >= d]; sorted_to_flat int32 [rows_cap], group_offsets int32
+ *   [E + 1] as moe_permute leaves them.  d, f multiples of 32.
+ */
+typedef struct moe_fp4_weights {
+  int32_t E, d, f, fmt;
+  const uint8_t *wi_q, *wi_sf;
+  const float *wi_scale;
+  const uint8_t *wo_q, *wo_sf;
+  const float *wo_scale;
+  const float *x_scale, *act_scale;
+} moe_fp4_weights;
+
+typedef struct moe_fp4_buffers {
+  int64_t rows_cap;
+  uint8_t *x_q, *x_sf;
+  size_t x_sf_bytes;
+  uint8_t *act_q, *act_sf;
+  size_t act_sf_bytes;
+  uint16_t *h, *y;
+  int32_t *dev_status;
+} moe_fp4_buffers;
+
+moe_status_t moe_fp4_experts(const moe_fp4_weights *w, const moe_fp4_buffers *b,
+                             const uint16_t *x, int64_t ldx, int T, const int32_t *sorted_to_flat,
+                             int k, const int32_t *group_offsets, moe_stream_t stream);
+
 /* -------------------------------------------- activation checkpoints in 8 bits --
  * What the forward saves for the backward, in 8.5 bits an element: signed 8-bit
  * codes and one bf16 scale per 32 consecutive columns of a row (a row's last

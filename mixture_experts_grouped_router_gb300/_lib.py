@@ -106,6 +106,7 @@ _SIGS = {
     "moe_fp4_arrange_scales": (_I, [_P, _I64, _I, _I, _I, _I, _P, _SZ, _P]),
     "moe_gmm_fp4": (_I, [_P, _I64, _P, _P, _P, _I64, _I64, _P, _P, _I, _P, _I, _I64, _I, _I, _I,
                          _P, _I, _I64, _P, _I64, _P, _SZ, _P, _P, _P]),
+    "moe_fp4_experts": (_I, [_P, _P, _P, _I64, _I, _P, _I, _P, _P]),
     "moe_act8_quantize": (_I, [_P, _I64, _I64, _I, _P, _I, _P, _I64, _P, _I64, _P]),
     "moe_act8_dequantize": (_I, [_P, _I64, _P, _I64, _I64, _I, _P, _I, _P, _I64, _P]),
     "moe_act8_swiglu_fwd": (_I, [_P, _I64, _I64, _I, _P, _I, _P, _I64, _P, _I64, _P, _I64, _P]),
@@ -521,6 +522,26 @@ def moe_gmm_fp4(A, sfa, B, sfb, fmt, group_offsets, K=None, epilogue=EPI_NONE, C
                            _ld(Q2) if Q2 is not None else 0, _ptr(sf2),
                            sf2.numel() if sf2 is not None else 0, _ptr(q2_scale),
                            _ptr(dev_status), _stream(stream)))
+
+
+class Fp4WeightsArg(ctypes.Structure):
+    """moe_fp4_weights."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("E", "d", "f", "fmt")] + [
+        (n, _P) for n in ("wi_q", "wi_sf", "wi_scale", "wo_q", "wo_sf", "wo_scale", "x_scale",
+                          "act_scale")]
+
+
+class Fp4BuffersArg(ctypes.Structure):
+    """moe_fp4_buffers."""
+    _fields_ = [("rows_cap", _I64), ("x_q", _P), ("x_sf", _P), ("x_sf_bytes", _SZ), ("act_q", _P),
+                ("act_sf", _P), ("act_sf_bytes", _SZ), ("h", _P), ("y", _P), ("dev_status", _P)]
+
+
+def moe_fp4_experts(w, b, x, sorted_to_flat, k, group_offsets, stream=None):
+    """w, b: Fp4WeightsArg, Fp4BuffersArg; x bf16 [T, d] -> y of b."""
+    _check(LIB.moe_fp4_experts(ctypes.byref(w), ctypes.byref(b), x.data_ptr(), _ld(x), x.shape[0],
+                               sorted_to_flat.data_ptr(), k, group_offsets.data_ptr(),
+                               _stream(stream)))
 
 
 # -------------------------------------------------- activation checkpoints in 8 bits

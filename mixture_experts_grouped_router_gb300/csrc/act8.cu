@@ -77,20 +77,6 @@ MOE_DEVINL void act8_values8(const uint2 &q, uint32_t sbits, float *v) {
   }
 }
 
-MOE_DEVINL uint2 ld_nc_v2(const void *p) {
-  uint2 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
-               : "=r"(r.x), "=r"(r.y)
-               : "l"(p));
-  return r;
-}
-
-MOE_DEVINL uint32_t ld_nc_u16(const void *p) {
-  uint16_t r;
-  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(r) : "l"(p));
-  return r;
-}
-
 // The warps' walk over (row, chunk of 256 columns): chunk c of warp w is c0 + w,
 // then steps of all warps; a step is taken by additions alone.
 struct Walk {
@@ -116,7 +102,7 @@ struct Walk {
 
 MOE_DEVINL int64_t live_rows(const int32_t *offsets, int E, int64_t rows) {
   if (offsets == nullptr) return rows;
-  return min(max((int64_t)__ldg(offsets + E), (int64_t)0), rows);
+  return min(max((int64_t)ld_i32(offsets + E), (int64_t)0), rows);
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -124,6 +110,7 @@ act8_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t rows, 
                      const int32_t *__restrict__ offsets, int E, int8_t *__restrict__ q,
                      int64_t ldq, uint16_t *__restrict__ s, int64_t lds) {
   const int lane = threadIdx.x & 31;
+  grid_dependency_begin();
   const int64_t R = live_rows(offsets, E, rows);
   Walk w((cols + 255) / 256);
   while (w.row < R) {
@@ -135,7 +122,7 @@ act8_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t rows, 
       at[i] = w.row;
       col[i] = w.ch * 256 + lane * 8;
       v[i] = make_uint4(0, 0, 0, 0);
-      if (w.row < R && col[i] < cols) v[i] = ld_nc_v4(x + w.row * ldx + col[i]);
+      if (w.row < R && col[i] < cols) v[i] = ld_stream_v4(x + w.row * ldx + col[i]);
       w.step();
     }
 #pragma unroll
@@ -155,6 +142,7 @@ act8_dequantize_kernel(const int8_t *__restrict__ q, int64_t ldq, const uint16_t
                        int64_t lds, int64_t rows, int cols, const int32_t *__restrict__ offsets,
                        int E, uint16_t *__restrict__ x, int64_t ldx) {
   const int lane = threadIdx.x & 31;
+  grid_dependency_begin();
   const int64_t R = live_rows(offsets, E, rows);
   Walk w((cols + 255) / 256);
   while (w.row < R) {
@@ -167,8 +155,8 @@ act8_dequantize_kernel(const int8_t *__restrict__ q, int64_t ldq, const uint16_t
       at[i] = w.row;
       col[i] = w.ch * 256 + lane * 8;
       if (w.row < R && col[i] < cols) {
-        c[i] = ld_nc_v2(q + w.row * ldq + col[i]);
-        sb[i] = ld_nc_u16(s + w.row * lds + (col[i] >> 5));
+        c[i] = ld_stream_v2(q + w.row * ldq + col[i]);
+        sb[i] = ld_u16(s + w.row * lds + (col[i] >> 5));
       }
       w.step();
     }
@@ -193,6 +181,7 @@ act8_swiglu_fwd_kernel(const uint16_t *__restrict__ h, int64_t ldh, int64_t rows
   constexpr int kU = kUnroll / 2;  // two loads a chunk
   const int lane = threadIdx.x & 31;
   const int nb = (F + 31) / 32;
+  grid_dependency_begin();
   const int64_t R = live_rows(offsets, E, rows);
   Walk w((F + 255) / 256);
   while (w.row < R) {
@@ -205,8 +194,8 @@ act8_swiglu_fwd_kernel(const uint16_t *__restrict__ h, int64_t ldh, int64_t rows
       col[i] = w.ch * 256 + lane * 8;
       g[i] = u[i] = make_uint4(0, 0, 0, 0);
       if (w.row < R && col[i] < F) {
-        g[i] = ld_nc_v4(h + w.row * ldh + col[i]);
-        u[i] = ld_nc_v4(h + w.row * ldh + F + col[i]);
+        g[i] = ld_stream_v4(h + w.row * ldh + col[i]);
+        u[i] = ld_stream_v4(h + w.row * ldh + F + col[i]);
       }
       w.step();
     }
@@ -244,6 +233,7 @@ act8_swiglu_bwd_kernel(const int8_t *__restrict__ q, int64_t ldq, const uint16_t
   constexpr int kU = kUnroll / 2;
   const int lane = threadIdx.x & 31;
   const int nb = (F + 31) / 32;
+  grid_dependency_begin();
   const int64_t R = live_rows(offsets, E, rows);
   Walk w((F + 255) / 256);
   while (w.row < R) {
@@ -259,11 +249,11 @@ act8_swiglu_bwd_kernel(const int8_t *__restrict__ q, int64_t ldq, const uint16_t
       if (w.row < R && col[i] < F) {
         const int8_t *qr = q + w.row * ldq + col[i];
         const uint16_t *sr = s + w.row * lds + (col[i] >> 5);
-        cg[i] = ld_nc_v2(qr);
-        cu[i] = ld_nc_v2(qr + F);
-        da[i] = ld_nc_v4(dact + w.row * ldda + col[i]);
-        sg[i] = ld_nc_u16(sr);
-        su[i] = ld_nc_u16(sr + nb);
+        cg[i] = ld_stream_v2(qr);
+        cu[i] = ld_stream_v2(qr + F);
+        da[i] = ld_stream_v4(dact + w.row * ldda + col[i]);
+        sg[i] = ld_u16(sr);
+        su[i] = ld_u16(sr + nb);
       }
       w.step();
     }
@@ -305,35 +295,31 @@ int grid_for(int64_t rows, int cols) {
 cudaError_t launch_act8_quantize(const uint16_t *x, int64_t ldx, int64_t rows, int cols,
                                  const int32_t *offsets, int E, int8_t *q, int64_t ldq,
                                  uint16_t *s, int64_t lds, cudaStream_t st) {
-  act8_quantize_kernel<<<grid_for(rows, cols), kThreads, 0, st>>>(x, ldx, rows, cols, offsets, E,
-                                                                  q, ldq, s, lds);
-  return cudaGetLastError();
+  return launch_dependent(act8_quantize_kernel, grid_for(rows, cols), kThreads, 0, st,
+                          x, ldx, rows, cols, offsets, E, q, ldq, s, lds);
 }
 
 cudaError_t launch_act8_dequantize(const int8_t *q, int64_t ldq, const uint16_t *s, int64_t lds,
                                    int64_t rows, int cols, const int32_t *offsets, int E,
                                    uint16_t *x, int64_t ldx, cudaStream_t st) {
-  act8_dequantize_kernel<<<grid_for(rows, cols), kThreads, 0, st>>>(q, ldq, s, lds, rows, cols,
-                                                                    offsets, E, x, ldx);
-  return cudaGetLastError();
+  return launch_dependent(act8_dequantize_kernel, grid_for(rows, cols), kThreads, 0, st,
+                          q, ldq, s, lds, rows, cols, offsets, E, x, ldx);
 }
 
 cudaError_t launch_act8_swiglu_fwd(const uint16_t *h, int64_t ldh, int64_t rows, int F,
                                    const int32_t *offsets, int E, uint16_t *act, int64_t lda,
                                    int8_t *q, int64_t ldq, uint16_t *s, int64_t lds,
                                    cudaStream_t st) {
-  act8_swiglu_fwd_kernel<<<grid_for(rows, F), kThreads, 0, st>>>(h, ldh, rows, F, offsets, E, act,
-                                                                 lda, q, ldq, s, lds);
-  return cudaGetLastError();
+  return launch_dependent(act8_swiglu_fwd_kernel, grid_for(rows, F), kThreads, 0, st,
+                          h, ldh, rows, F, offsets, E, act, lda, q, ldq, s, lds);
 }
 
 cudaError_t launch_act8_swiglu_bwd(const int8_t *q, int64_t ldq, const uint16_t *s, int64_t lds,
                                    const uint16_t *dact, int64_t ldda, int64_t rows, int F,
                                    const int32_t *offsets, int E, uint16_t *dh, int64_t lddh,
                                    uint16_t *act, int64_t lda, cudaStream_t st) {
-  act8_swiglu_bwd_kernel<<<grid_for(rows, F), kThreads, 0, st>>>(
-      q, ldq, s, lds, dact, ldda, rows, F, offsets, E, dh, lddh, act, lda);
-  return cudaGetLastError();
+  return launch_dependent(act8_swiglu_bwd_kernel, grid_for(rows, F), kThreads, 0, st,
+                          q, ldq, s, lds, dact, ldda, rows, F, offsets, E, dh, lddh, act, lda);
 }
 
 }  // namespace moe

@@ -39,7 +39,7 @@ static moe_status_t check_rows(const char *who, int64_t rows, int cols, int fmt,
   REQUIRE(good_fmt(fmt), MOE_ERR_INVALID_ARG, "%s: bad fmt %d", who, fmt);
   REQUIRE(good_map(row_map), MOE_ERR_INVALID_ARG, "%s: bad row_map %d", who, row_map);
   REQUIRE(cols % 32 == 0, MOE_ERR_UNSUPPORTED, "%s: cols=%d is no multiple of 32", who, cols);
-  REQUIRE(rows < (1ll << 31), MOE_ERR_UNSUPPORTED, "%s: more than 2^31 rows", who);
+  REQUIRE(rows < (1ll << 31) - (1 << 20), MOE_ERR_UNSUPPORTED, "%s: too many rows (2^31)", who);
   if (row_map == MOE_MX_ROWS_GROUPED) {
     REQUIRE(E <= 256, MOE_ERR_UNSUPPORTED, "%s: E=%d > 256", who, E);
     REQUIRE(offsets != nullptr || rows == 0, MOE_ERR_INVALID_ARG,
@@ -206,6 +206,59 @@ moe_status_t moe_gmm_fp4(const uint8_t *A, int64_t lda, const uint8_t *sfa, cons
                     rows_cap, K, N, epilogue, C, c_dtype, ldc, Q2, ldq2, sf2, q2_scale,
                     dev_status};
   return moe::launch_gmm_fp4(a, (cudaStream_t)stream);
+}
+
+moe_status_t moe_fp4_experts(const moe_fp4_weights *w, const moe_fp4_buffers *b,
+                             const uint16_t *x, int64_t ldx, int T, const int32_t *sorted_to_flat,
+                             int k, const int32_t *group_offsets, moe_stream_t stream) {
+  set_error("");
+  REQUIRE(w != nullptr && b != nullptr, MOE_ERR_INVALID_ARG, "moe_fp4_experts: null pointer");
+  REQUIRE(w->E > 0 && w->d > 0 && w->f > 0 && T >= 0 && k > 0 && b->rows_cap >= 0,
+          MOE_ERR_INVALID_ARG, "moe_fp4_experts: E=%d d=%d f=%d T=%d k=%d rows_cap=%lld", w->E,
+          w->d, w->f, T, k, (long long)b->rows_cap);
+  // everything is checked before the first launch: the three calls repeat only
+  // what these do not cover
+  REQUIRE(good_fmt(w->fmt), MOE_ERR_INVALID_ARG, "moe_fp4_experts: bad fmt %d", w->fmt);
+  REQUIRE(w->d % 32 == 0 && w->f % 32 == 0 && w->E <= 256, MOE_ERR_UNSUPPORTED,
+          "moe_fp4_experts: d=%d and f=%d must be multiples of 32, E=%d at most 256", w->d, w->f,
+          w->E);
+  REQUIRE(b->rows_cap + 128ll * w->E < (1ll << 23), MOE_ERR_UNSUPPORTED,
+          "moe_fp4_experts: rows_cap=%lld E=%d: more than 2^23 padded rows",
+          (long long)b->rows_cap, w->E);
+  if (b->rows_cap == 0) return MOE_OK;
+  REQUIRE(w->wi_q && w->wi_sf && w->wo_q && w->wo_sf && b->x_q && b->x_sf && b->act_q &&
+              b->act_sf && b->y && (x || T == 0) && sorted_to_flat && group_offsets,
+          MOE_ERR_INVALID_ARG, "moe_fp4_experts: null pointer");
+  REQUIRE(aligned(w->wi_q, 16) && aligned(w->wi_sf, 16) && aligned(w->wo_q, 16) &&
+              aligned(w->wo_sf, 16) && aligned(b->x_q, 16) && aligned(b->x_sf, 16) &&
+              aligned(b->act_q, 16) && aligned(b->act_sf, 16) && aligned(b->y, 16) &&
+              aligned(b->h, 16) && aligned(x, 16) && ldx % 8 == 0,
+          MOE_ERR_UNSUPPORTED, "moe_fp4_experts: operands must be 16-byte aligned");
+  REQUIRE(ldx >= w->d, MOE_ERR_INVALID_ARG, "moe_fp4_experts: ldx=%lld < d", (long long)ldx);
+  REQUIRE(b->x_sf_bytes >=
+                  moe_fp4_scale_bytes(b->rows_cap, w->d, w->fmt, MOE_MX_ROWS_GROUPED, w->E) &&
+              b->act_sf_bytes >=
+                  moe_fp4_scale_bytes(b->rows_cap, w->f, w->fmt, MOE_MX_ROWS_GROUPED, w->E),
+          MOE_ERR_INVALID_ARG, "moe_fp4_experts: scale buffers too small");
+  cudaStream_t s = (cudaStream_t)stream;
+  moe_status_t st = cuda_status(
+      moe::launch_fp4_quantize(x, ldx, T, sorted_to_flat, k, b->rows_cap, w->d, w->fmt,
+                               MOE_MX_ROWS_GROUPED, group_offsets, w->E, w->x_scale, b->x_q,
+                               w->d / 2, b->x_sf, b->dev_status, s),
+      "moe_fp4_experts: quantise");
+  if (st != MOE_OK) return st;
+  const int64_t d2 = w->d / 2, f2 = w->f / 2;
+  moe::GmmFp4Args up{b->x_q, d2, b->x_sf, w->x_scale, w->wi_q, d2, 2ll * w->f * d2, w->wi_sf,
+                     w->wi_scale, w->fmt, group_offsets, w->E, b->rows_cap, w->d, 2 * w->f,
+                     MOE_EPI_SWIGLU_FWD, b->h, MOE_DTYPE_BF16, 2ll * w->f, b->act_q, f2, b->act_sf,
+                     w->act_scale, b->dev_status};
+  st = moe::launch_gmm_fp4(up, s);
+  if (st != MOE_OK) return st;
+  moe::GmmFp4Args down{b->act_q, f2, b->act_sf, w->act_scale, w->wo_q, f2, (int64_t)w->d * f2,
+                       w->wo_sf, w->wo_scale, w->fmt, group_offsets, w->E, b->rows_cap, w->f, w->d,
+                       MOE_EPI_NONE, b->y, MOE_DTYPE_BF16, w->d, nullptr, 0, nullptr, nullptr,
+                       b->dev_status};
+  return moe::launch_gmm_fp4(down, s);
 }
 
 // ------------------------------------------------- 8-bit activation checkpoints

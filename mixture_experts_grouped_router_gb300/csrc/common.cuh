@@ -19,6 +19,64 @@ MOE_DEVINL void moe_set_status(int32_t *status, int code) {
 // have completed and their writes are visible (a no-op for a plain launch).
 MOE_DEVINL void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Start of a kernel launched as a dependent: waits as above, then lets the grid
+// after this one be placed (so that no more than two overlap, and no load of the
+// one before last can follow the launch whose start clears the L1 caches).
+MOE_DEVINL void grid_dependency_begin() {
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Plain global loads that stay behind grid_dependency_begin(): a __ldg, or a load
+// through a const __restrict__ pointer, may be moved above it as an invariant.
+MOE_DEVINL int ld_i32(const int32_t *p) {
+  int v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+MOE_DEVINL uint32_t ld_u32(const void *p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+MOE_DEVINL uint32_t ld_u16(const void *p) {
+  uint16_t v;
+  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
+  return v;
+}
+
+MOE_DEVINL uint32_t ld_u8(const void *p) {
+  uint32_t v;
+  asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+MOE_DEVINL float ld_f32(const float *p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// Streamed 16 and 8 bytes, not kept in L1.
+MOE_DEVINL uint4 ld_stream_v4(const void *p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
+MOE_DEVINL uint2 ld_stream_v2(const void *p) {
+  uint2 r;
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
+               : "=r"(r.x), "=r"(r.y)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
 MOE_DEVINL float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);

@@ -54,7 +54,7 @@ MOE_DEVINL void scan_groups(Groups &gr, const int32_t *offsets, int E, int64_t r
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
     auto offset = [&](int e) {
-      return (int)min(max((int64_t)__ldg(offsets + e), (int64_t)0), rows);
+      return (int)min(max((int64_t)ld_i32(offsets + e), (int64_t)0), rows);
     };
     int top = offset(0), carry = 0;  // running maximum, padded rows so far
     for (int c0 = 0; c0 < E; c0 += 32) {
@@ -86,17 +86,33 @@ MOE_DEVINL void scan_groups(Groups &gr, const int32_t *offsets, int E, int64_t r
   }
 }
 
-// Padded row of row r < off[E]: in the last group that starts at or before it
-// (-1 before the first group).
-MOE_DEVINL int64_t grouped_row(const Groups &gr, int E, int64_t r) {
-  int lo = 0, hi = E - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (gr.off[mid] <= r) lo = mid;
-    else hi = mid - 1;
-  }
-  return gr.off[lo] <= r ? gr.pad[lo] + (r - gr.off[lo]) : -1;
+// Padded row of row r < off[E], in the group that holds it (-1 before the first
+// group); e: the group of an earlier row, advanced.
+MOE_DEVINL int grouped_row(const Groups &gr, int &e, int r) {
+  while (gr.off[e + 1] <= r) ++e;
+  return gr.off[e] <= r ? gr.pad[e] + (r - gr.off[e]) : -1;
 }
+
+// A warp's walk over (row, segment of 4 chunks): additions only.
+struct Walk {
+  int row, seg, d_row, d_seg, segs;
+  MOE_DEVINL Walk(int segments) : segs(segments) {
+    const int warp = (int)((blockIdx.x * kThreads + threadIdx.x) >> 5);
+    const int warps = (int)gridDim.x * kWarps;
+    row = warp / segs;
+    seg = warp - row * segs;
+    d_row = warps / segs;
+    d_seg = warps - d_row * segs;
+  }
+  MOE_DEVINL void step() {
+    row += d_row;
+    seg += d_seg;
+    if (seg >= segs) {
+      seg -= segs;
+      ++row;
+    }
+  }
+};
 
 // The scale codes of a warp's chunk (the lane's block code in c) as the words
 // of its atoms: a word is 4 blocks, 8 lanes of two per block (NVFP4) or 16
@@ -112,70 +128,88 @@ MOE_DEVINL uint32_t scale_word(uint32_t c, int lane) {
 
 // One warp: one row, up to 4 chunks of 256 columns (a lane 8 of them, 16 bytes
 // in, 4 bytes of codes out), so that a row's loads are all in flight together
-// and every access is coalesced.
+// and every access is coalesced; the next row's loads are issued before this
+// one is quantised, the first row's before the groups are scanned.
 template <int FMT, bool GROUPED>
 __global__ void __launch_bounds__(kThreads)
 fp4_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t src_rows,
-                    const int32_t *__restrict__ row_index, int index_div, int64_t rows, int cols,
+                    const int32_t *__restrict__ row_index, int index_div, int rows, int cols,
                     int row_map, const int32_t *__restrict__ offsets, int E,
                     const float *__restrict__ gscale, uint8_t *__restrict__ q, int64_t ldq,
                     uint8_t *__restrict__ sf, int32_t *dev_status) {
   __shared__ Groups gr;
   const int lane = threadIdx.x & 31;
-  const int segs = (cols + 256 * kUnroll - 1) / (256 * kUnroll);
   const int ac = (cols + fp4_atom_cols(FMT) - 1) / fp4_atom_cols(FMT);
-  const int64_t G = rows / max(E, 1);
-  int64_t R = rows;
+  const int G = rows / max(E, 1);
+  grid_dependency_begin();
+  Walk w((cols + 256 * kUnroll - 1) / (256 * kUnroll));
+  // this warp's piece of row w.row as it stands; a row that x does not have
+  // (src_rows of them) reads as zeros
+  auto load = [&](uint4 *v, int64_t &src) {
+    src = -1;
+    if (w.row < rows) {
+      src = w.row;
+      if (row_index != nullptr) {
+        const int i = ld_i32(row_index + w.row);
+        src = i < 0 ? -1 : i / index_div;
+      }
+    }
+    const int c0 = w.seg * (256 * kUnroll) + lane * 8;
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (src >= 0 && src < src_rows && c0 + 256 * i < cols)
+        v[i] = ld_stream_v4(x + src * ldx + c0 + 256 * i);
+    }
+  };
+  uint4 cur[kUnroll];
+  int64_t src;
+  load(cur, src);
+  int R = rows;
   if (GROUPED) {
     scan_groups(gr, offsets, E, rows);
     __syncthreads();
     R = gr.off[E];
   }
-  const int64_t warp = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
-  const int64_t warps = (int64_t)gridDim.x * kWarps;
-  for (int64_t it = warp; it < R * segs; it += warps) {
-    const int64_t r = it / segs;
-    const int c0 = (int)(it - r * segs) * (256 * kUnroll) + lane * 8;
-    int64_t src = r;
-    if (row_index != nullptr) {
-      const int i = __ldg(row_index + r);
-      src = i < 0 ? -1 : i / index_div;
-      if (src >= src_rows) {
-        if (lane == 0) moe_set_status(dev_status, MOE_ERR_DEVICE);
-        src = -1;
+  const float g1 = FMT == MOE_FP4_NV && GROUPED && gscale != nullptr ? ld_f32(gscale) : 1.0f;
+  int e = 0;
+  while (w.row < R) {
+    const int r = w.row, c0 = w.seg * (256 * kUnroll) + lane * 8;
+    if (src >= src_rows && lane == 0) moe_set_status(dev_status, MOE_ERR_DEVICE);
+    uint4 next[kUnroll];
+    w.step();
+    load(next, src);
+    const float g = FMT == MOE_FP4_NV && !GROUPED && gscale != nullptr ? ld_f32(gscale + r / G) : g1;
+    const int64_t pr = GROUPED ? grouped_row(gr, e, r) : weight_row(r, G, row_map);
+    if (pr >= 0) {
+      uint8_t *qr = q + r * ldq + (c0 >> 1);
+      // atoms of 4 blocks follow one another 512 bytes apart
+      uint8_t *sr = sf + fp4_scale_byte(pr, c0 / fp4_block(FMT), ac);
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        const int c = c0 + 256 * i;
+        if (c - lane * 8 >= cols) break;  // the whole chunk
+        uint32_t a = amax_bits8(cur[i]);
+        a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+        if (FMT != MOE_FP4_NV) a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+        float t, inv, v[8];
+        const uint32_t code = fp4_block_scale<FMT>(__uint_as_float(a << 16), g, t, inv);
+        bf16x8_to_f32(cur[i], v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = fp4_quotient<FMT>(v[j], t, inv);
+        uint32_t codes = cvt_e2m1x8(v);
+        if (inv == 0.0f) codes = 0;  // (a NaN times 0 is no zero code)
+        const uint32_t word = scale_word<FMT>(c < cols ? code : 0u, lane);
+        constexpr int kLanes = FMT == MOE_FP4_NV ? 8 : 16;  // lanes of a word
+        if (c < cols) {
+          *reinterpret_cast<uint32_t *>(qr + 128 * i) = codes;
+          if (lane % kLanes == 0)
+            *reinterpret_cast<uint32_t *>(sr + i * (256 / fp4_atom_cols(FMT)) * 512) = word;
+        }
       }
     }
-    uint4 w[kUnroll];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      w[i] = make_uint4(0, 0, 0, 0);
-      if (src >= 0 && c0 + 256 * i < cols) w[i] = ld_nc_v4(x + src * ldx + c0 + 256 * i);
-    }
-    const float g = FMT != MOE_FP4_NV || gscale == nullptr ? 1.0f
-                    : __ldg(gscale + (GROUPED ? 0 : r / G));
-    const int64_t pr = GROUPED ? grouped_row(gr, E, r) : weight_row(r, G, row_map);
-    if (pr < 0) continue;
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int c = c0 + 256 * i;
-      if (c - lane * 8 >= cols) break;  // the whole chunk
-      uint32_t a = amax_bits8(w[i]);
-      a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-      if (FMT != MOE_FP4_NV) a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-      float t, inv, v[8];
-      uint32_t code = fp4_block_scale<FMT>(__uint_as_float(a << 16), g, t, inv);
-      if (c >= cols) code = 0;
-      bf16x8_to_f32(w[i], v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = fp4_quotient<FMT>(v[j], t, inv);
-      uint32_t codes = cvt_e2m1x8(v);
-      if (inv == 0.0f) codes = 0;  // (a NaN times 0 is no zero code)
-      if (c < cols) *reinterpret_cast<uint32_t *>(q + r * ldq + (c >> 1)) = codes;
-      const uint32_t word = scale_word<FMT>(code, lane);
-      constexpr int kLanes = FMT == MOE_FP4_NV ? 8 : 16;  // lanes of a word
-      if (lane % kLanes == 0 && c < cols)
-        *reinterpret_cast<uint32_t *>(sf + fp4_scale_byte(pr, c / fp4_block(FMT), ac)) = word;
-    }
+    for (int i = 0; i < kUnroll; ++i) cur[i] = next[i];
   }
 }
 
@@ -183,49 +217,47 @@ fp4_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t src_row
 template <int FMT, bool GROUPED>
 __global__ void __launch_bounds__(kThreads)
 fp4_dequantize_kernel(const uint8_t *__restrict__ q, int64_t ldq, const uint8_t *__restrict__ sf,
-                      int64_t rows, int cols, int row_map, const int32_t *__restrict__ offsets,
-                      int E, const float *__restrict__ gscale, uint16_t *__restrict__ x,
-                      int64_t ldx) {
+                      int rows, int cols, int row_map, const int32_t *__restrict__ offsets, int E,
+                      const float *__restrict__ gscale, uint16_t *__restrict__ x, int64_t ldx) {
   __shared__ Groups gr;
   const int lane = threadIdx.x & 31;
-  const int segs = (cols + 256 * kUnroll - 1) / (256 * kUnroll);
   const int ac = (cols + fp4_atom_cols(FMT) - 1) / fp4_atom_cols(FMT);
-  const int64_t G = rows / max(E, 1);
-  int64_t R = rows;
+  const int G = rows / max(E, 1);
+  grid_dependency_begin();
+  int R = rows;
   if (GROUPED) {
     scan_groups(gr, offsets, E, rows);
     __syncthreads();
     R = gr.off[E];
   }
-  const int64_t warp = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
-  const int64_t warps = (int64_t)gridDim.x * kWarps;
-  for (int64_t it = warp; it < R * segs; it += warps) {
-    const int64_t r = it / segs;
-    const int c0 = (int)(it - r * segs) * (256 * kUnroll) + lane * 8;
-    const int64_t pr = GROUPED ? grouped_row(gr, E, r) : weight_row(r, G, row_map);
+  const float g1 = FMT == MOE_FP4_NV && GROUPED && gscale != nullptr ? ld_f32(gscale) : 1.0f;
+  int e = 0;
+  for (Walk w((cols + 256 * kUnroll - 1) / (256 * kUnroll)); w.row < R; w.step()) {
+    const int r = w.row, c0 = w.seg * (256 * kUnroll) + lane * 8;
+    const int64_t pr = GROUPED ? grouped_row(gr, e, r) : weight_row(r, G, row_map);
     if (pr < 0) continue;
-    uint32_t w[kUnroll], s[kUnroll];
+    const uint8_t *qr = q + r * ldq + (c0 >> 1);
+    const uint8_t *sr = sf + fp4_scale_byte(pr, c0 / fp4_block(FMT), ac);
+    uint32_t codes[kUnroll], sc[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const int c = c0 + 256 * i;
-      w[i] = s[i] = 0;
-      if (c < cols) {
-        w[i] = __ldg(reinterpret_cast<const uint32_t *>(q + r * ldq + (c >> 1)));
-        s[i] = __ldg(sf + fp4_scale_byte(pr, c / fp4_block(FMT), ac));
+      codes[i] = sc[i] = 0;
+      if (c0 + 256 * i < cols) {
+        codes[i] = ld_u32(qr + 128 * i);
+        sc[i] = ld_u8(sr + i * (256 / fp4_atom_cols(FMT)) * 512);
       }
     }
-    const float g = FMT != MOE_FP4_NV || gscale == nullptr ? 1.0f
-                    : __ldg(gscale + (GROUPED ? 0 : r / G));
+    const float g = FMT == MOE_FP4_NV && !GROUPED && gscale != nullptr ? ld_f32(gscale + r / G) : g1;
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
-      const int c = c0 + 256 * i;
-      if (c < cols) {
+      if (c0 + 256 * i < cols) {
         float v[8];
-        e2m1x8_to_f32(w[i], v);
-        const float t = fp4_scale_value(s[i], FMT);
+        e2m1x8_to_f32(codes[i], v);
+        // code times scale is exact (6 significant bits): one rounding by g, one to bf16
+        const float t = fp4_scale_value(sc[i], FMT);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = v[j] * t * g;
-        st_v4(x + r * ldx + c, f32_to_bf16x8(v));
+        for (int j = 0; j < 8; ++j) v[j] = FMT == MOE_FP4_NV ? v[j] * t * g : v[j] * t;
+        st_v4(x + r * ldx + c0 + 256 * i, f32_to_bf16x8(v));
       }
     }
   }
@@ -324,9 +356,8 @@ cudaError_t launch_fp4_quantize(const uint16_t *x, int64_t ldx, int64_t src_rows
   const int grid = grid_for(rows, cols);
   const bool grouped = row_map == MOE_MX_ROWS_GROUPED;
   auto run = [&](auto kernel) {
-    kernel<<<grid, kThreads, 0, st>>>(x, ldx, src_rows, row_index, index_div, rows, cols, row_map,
-                                      offsets, E, gscale, q, ldq, sf, dev_status);
-    return cudaGetLastError();
+    return launch_dependent(kernel, grid, kThreads, 0, st, x, ldx, src_rows, row_index, index_div,
+                            (int)rows, cols, row_map, offsets, E, gscale, q, ldq, sf, dev_status);
   };
   if (fmt == MOE_FP4_NV)
     return grouped ? run(fp4_quantize_kernel<MOE_FP4_NV, true>)
@@ -342,8 +373,8 @@ cudaError_t launch_fp4_dequantize(const uint8_t *q, int64_t ldq, const uint8_t *
   const int grid = grid_for(rows, cols);
   const bool grouped = row_map == MOE_MX_ROWS_GROUPED;
   auto run = [&](auto kernel) {
-    kernel<<<grid, kThreads, 0, st>>>(q, ldq, sf, rows, cols, row_map, offsets, E, gscale, x, ldx);
-    return cudaGetLastError();
+    return launch_dependent(kernel, grid, kThreads, 0, st, q, ldq, sf, (int)rows, cols, row_map,
+                            offsets, E, gscale, x, ldx);
   };
   if (fmt == MOE_FP4_NV)
     return grouped ? run(fp4_dequantize_kernel<MOE_FP4_NV, true>)

@@ -112,7 +112,7 @@ struct TileInfo {
 };
 
 MOE_DEVINL int group_offset(const Fp4Params &p, int e) {
-  return min(max(__ldg(p.offsets + e), 0), p.rows_cap);
+  return min(max(ld_i32(p.offsets + e), 0), p.rows_cap);
 }
 
 // Tile t: the two CTAs of a pair take row tiles 2 pm and 2 pm + 1 of an expert
@@ -197,8 +197,8 @@ template <int FMT, int EPI>
 MOE_DEVINL void epilogue(const Book &bk, const Fp4Params &p, const TileInfo &ti, uint32_t taddr,
                          int q, int lane, uint8_t *stg, const CUtensorMap *m0,
                          const CUtensorMap *m1) {
-  const float sc = (p.ga != nullptr ? __ldg(p.ga) : 1.0f) *
-                   (p.gb != nullptr ? __ldg(p.gb + ti.e) : 1.0f);
+  const float sc = (p.ga != nullptr ? ld_f32(p.ga) : 1.0f) *
+                   (p.gb != nullptr ? ld_f32(p.gb + ti.e) : 1.0f);
   const int wrow0 = ti.row0 + q * 32;
   const int64_t row = (int64_t)wrow0 + lane;
   const bool valid = row < ti.row_end;
@@ -207,7 +207,7 @@ MOE_DEVINL void epilogue(const Book &bk, const Fp4Params &p, const TileInfo &ti,
   if (EPI == MOE_EPI_SWIGLU_FWD) {
     const int F = p.F;
     const int n0 = ti.n_idx * (BN / 2);
-    const float g2 = FMT == MOE_FP4_NV && p.g2 != nullptr ? __ldg(p.g2) : 1.0f;
+    const float g2 = FMT == MOE_FP4_NV && p.g2 != nullptr ? ld_f32(p.g2) : 1.0f;
     // the row's place in Act's scale atoms
     const int arow = (int)bk.poff[ti.e] + ti.m_idx;
     uint8_t *srow = p.sf2 + (int64_t)arow * p.ac2 * 512 + lane * 16 + q * 4;
@@ -348,7 +348,19 @@ gmm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     bk.abort_flag = 0;
     tc::fence_mbar_init();
   }
-  __syncthreads();
+  if (warp == 2 && lane == 0) {
+    tc::tma_prefetch(&tmA);
+    tc::tma_prefetch(&tmB);
+    tc::tma_prefetch(&tmSA);
+    tc::tma_prefetch(&tmSB);
+    tc::tma_prefetch(&tmC0);
+    tc::tma_prefetch(&tmA32);
+  }
+  if (warp == 1) {
+    tc::tmem_alloc_2sm(&bk.tmem_base, kTmemCols);
+    tc::tmem_relinquish_2sm();
+  }
+  grid_dependency_begin();  // the work above overlaps the end of the kernel before
   if (warp == 0) {
     // per-expert tile counts and padded sizes, and their exclusive scans
     int carry = 0, pcarry = 0;
@@ -383,10 +395,6 @@ gmm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       bk.cum[p.E] = carry;
       bk.total_tiles = carry;
     }
-  }
-  if (warp == 1) {
-    tc::tmem_alloc_2sm(&bk.tmem_base, kTmemCols);
-    tc::tmem_relinquish_2sm();
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -633,9 +641,8 @@ moe_status_t launch(const CUtensorMap *m, const Fp4Params &p, int64_t tiles_uppe
     return MOE_ERR_CUDA;
   }
   const int grid = 2 * (int)std::max<int64_t>(1, std::min<int64_t>(max_clusters, tiles_upper));
-  gmm_fp4_kernel<FMT, EPI><<<grid, kThreads, kSmem, s>>>(m[0], m[1], m[2], m[3], m[4], m[5], m[6],
-                                                     p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_dependent(gmm_fp4_kernel<FMT, EPI>, grid, kThreads, kSmem, s, m[0],
+                                         m[1], m[2], m[3], m[4], m[5], m[6], p);
   if (e != cudaSuccess) {
     set_error("moe_gmm_fp4 launch: %s", cudaGetErrorString(e));
     return MOE_ERR_CUDA;

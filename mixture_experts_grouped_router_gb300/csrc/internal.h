@@ -165,6 +165,25 @@ struct TgmmMxArgs {
 };
 moe_status_t launch_tgmm_mx(const TgmmMxArgs &a, cudaStream_t s);
 
+// Launch as a programmatic dependent: the kernel's blocks may be placed while the
+// one before it in the stream drains; it calls grid_dependency_wait() before it
+// touches global memory.  Hides most of a launch's latency where kernels are short.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                             cudaStream_t s, Args... args) {
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
 // fp4.cu (4-bit block-scaled formats: quantisers, scale layout)
 int64_t fp4_atom_rows(int64_t rows, int row_map, int E);
 cudaError_t launch_fp4_quantize(const uint16_t *x, int64_t ldx, int64_t src_rows,

@@ -74,6 +74,11 @@ class Fp4Experts:
         if wi_q.shape != (self.E, 2 * self.f, self.d // 2):
             raise ValueError("wi codes of shape %s do not match wo's %s"
                              % (tuple(wi_q.shape), tuple(wo_q.shape)))
+        if not (wi_q.is_contiguous() and wo_q.is_contiguous()):
+            raise ValueError("the weights' codes are contiguous")
+        self.arg = L.Fp4WeightsArg(
+            self.E, self.d, self.f, fmt, *(None if t is None else t.data_ptr() for t in (
+                wi_q, wi_sf, wi_scale, wo_q, wo_sf, wo_scale, x_scale, act_scale)))
 
     @classmethod
     def from_codes(cls, fmt, wi_q, wi_s, wi_scale, wo_q, wo_s, wo_scale, x_scale=None,
@@ -129,19 +134,24 @@ class Fp4Buffers:
                              device=dev) if save_h else None
         self.y = torch.empty(rows_cap, w.d, dtype=torch.bfloat16, device=dev)
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.arg = L.Fp4BuffersArg(
+            rows_cap, self.x.q.data_ptr(), self.x.sf.data_ptr(), self.x.sf.numel(),
+            self.act.q.data_ptr(), self.act.sf.data_ptr(), self.act.sf.numel(),
+            None if self.h is None else self.h.data_ptr(), self.y.data_ptr(),
+            self.dev_status.data_ptr())
 
 
 def fp4_experts(w: Fp4Experts, b: Fp4Buffers, x, sorted_to_flat, k, group_offsets, stream=None):
     """Expert outputs y bf16 [rows_cap, d] of the permuted rows of x bf16 [T, d]
     (sorted_to_flat int32 [rows_cap], group_offsets int32 [E + 1] as moe_permute leaves them;
     rows past group_offsets[E] are not written).  With b.h also H = [gate | up] in bf16."""
-    fp4_quantize(x, b.x, group_offsets, sorted_to_flat, k, w.x_scale, b.dev_status, stream)
-    L.moe_gmm_fp4(b.x.q, b.x.sf, w.wi_q, w.wi_sf, w.fmt, group_offsets,
-                  epilogue=L.EPI_SWIGLU_FWD, C=b.h, Q2=b.act.q, sf2=b.act.sf,
-                  a_scale=w.x_scale, b_scale=w.wi_scale, q2_scale=w.act_scale,
-                  dev_status=b.dev_status, stream=stream)
-    L.moe_gmm_fp4(b.act.q, b.act.sf, w.wo_q, w.wo_sf, w.fmt, group_offsets, C=b.y,
-                  a_scale=w.act_scale, b_scale=w.wo_scale, dev_status=b.dev_status, stream=stream)
+    if sorted_to_flat.shape[0] < b.rows_cap or group_offsets.shape[0] != w.E + 1:
+        raise ValueError("sorted_to_flat of %d rows (rows_cap %d), group_offsets of %d (E %d)"
+                         % (sorted_to_flat.shape[0], b.rows_cap, group_offsets.shape[0], w.E))
+    if x.shape[1] != w.d or b.y.shape[1] != w.d or b.act.cols != w.f:
+        raise ValueError("x of %d columns, buffers for (%d, %d), experts (%d, %d)"
+                         % (x.shape[1], b.y.shape[1], b.act.cols, w.d, w.f))
+    L.moe_fp4_experts(w.arg, b.arg, x, sorted_to_flat, k, group_offsets, stream)
     return b.y
 
 
