@@ -169,11 +169,13 @@ def _stream(stream):
 
 
 def _ld(t):
-    assert t.dim() >= 2, "matrices only"
-    if t.numel() == 0:
-        return t.shape[-1]
-    assert t.stride(-1) == 1, "row-major tensors only"
-    return t.stride(-2)
+    st = t.stride()
+    assert len(st) >= 2, "matrices only"
+    if st[-1] != 1:
+        assert t.numel() == 0, "row-major tensors only"
+    elif t.numel() != 0:
+        return st[-2]
+    return t.shape[-1]
 
 
 def moe_set_wait_limit_ns(limit_ns: int):
@@ -545,40 +547,47 @@ def moe_fp4_experts(w, b, x, sorted_to_flat, k, group_offsets, stream=None):
 
 
 # -------------------------------------------------- activation checkpoints in 8 bits
+# (short kernels: the argument marshalling is kept to what they need)
 def _offsets(group_offsets):
-    return _ptr(group_offsets), 0 if group_offsets is None else group_offsets.shape[0] - 1
+    if group_offsets is None:
+        return None, 0
+    return group_offsets.data_ptr(), group_offsets.shape[0] - 1
 
 
 def moe_act8_quantize(x, q, scales, group_offsets=None, stream=None):
     """x bf16 [rows, cols] -> q int8 [rows, cols], scales bf16 [rows, ceil(cols / 32)]."""
     rows, cols = x.shape
-    _check(LIB.moe_act8_quantize(_ptr(x), _ld(x), rows, cols, *_offsets(group_offsets), _ptr(q),
-                                 _ld(q), _ptr(scales), _ld(scales), _stream(stream)))
+    off, E = _offsets(group_offsets)
+    _check(LIB.moe_act8_quantize(x.data_ptr(), _ld(x), rows, cols, off, E, q.data_ptr(), _ld(q),
+                                 scales.data_ptr(), _ld(scales), _stream(stream)))
 
 
 def moe_act8_dequantize(q, scales, x, group_offsets=None, stream=None):
     """The values of the codes, in x bf16 [rows, cols]."""
     rows, cols = x.shape
-    _check(LIB.moe_act8_dequantize(_ptr(q), _ld(q), _ptr(scales), _ld(scales), rows, cols,
-                                   *_offsets(group_offsets), _ptr(x), _ld(x), _stream(stream)))
+    off, E = _offsets(group_offsets)
+    _check(LIB.moe_act8_dequantize(q.data_ptr(), _ld(q), scales.data_ptr(), _ld(scales), rows,
+                                   cols, off, E, x.data_ptr(), _ld(x), _stream(stream)))
 
 
 def moe_act8_swiglu_fwd(h, act, q, scales, group_offsets=None, stream=None):
     """h bf16 [rows, 2F] -> act bf16 [rows, F], q int8 [rows, 2F], scales bf16
     [rows, 2 ceil(F / 32)]."""
     rows, F = act.shape
-    _check(LIB.moe_act8_swiglu_fwd(_ptr(h), _ld(h), rows, F, *_offsets(group_offsets), _ptr(act),
-                                   _ld(act), _ptr(q), _ld(q), _ptr(scales), _ld(scales),
+    off, E = _offsets(group_offsets)
+    _check(LIB.moe_act8_swiglu_fwd(h.data_ptr(), _ld(h), rows, F, off, E, act.data_ptr(), _ld(act),
+                                   q.data_ptr(), _ld(q), scales.data_ptr(), _ld(scales),
                                    _stream(stream)))
 
 
 def moe_act8_swiglu_bwd(q, scales, dact, dh, act=None, group_offsets=None, stream=None):
     """Codes of h and dact bf16 [rows, F] -> dh bf16 [rows, 2F], act bf16 [rows, F]."""
     rows, F = dact.shape
-    _check(LIB.moe_act8_swiglu_bwd(_ptr(q), _ld(q), _ptr(scales), _ld(scales), _ptr(dact),
-                                   _ld(dact), rows, F, *_offsets(group_offsets), _ptr(dh),
-                                   _ld(dh), _ptr(act), _ld(act) if act is not None else 0,
-                                   _stream(stream)))
+    off, E = _offsets(group_offsets)
+    _check(LIB.moe_act8_swiglu_bwd(q.data_ptr(), _ld(q), scales.data_ptr(), _ld(scales),
+                                   dact.data_ptr(), _ld(dact), rows, F, off, E, dh.data_ptr(),
+                                   _ld(dh), None if act is None else act.data_ptr(),
+                                   0 if act is None else _ld(act), _stream(stream)))
 
 
 # ------------------------------------------------------------ expert parallelism

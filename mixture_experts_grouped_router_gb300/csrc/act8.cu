@@ -40,17 +40,19 @@ MOE_DEVINL uint32_t act8_scale(uint32_t amax, float &s, float &inv) {
   const float t = div_exact(a, 127.0f, kInv127);
   const uint32_t bits = (__float_as_uint(t) + 0xFFFFu) >> 16;
   s = __uint_as_float(bits << 16);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));  // div_exact corrects its last bit
+  inv = rcp_approx(s);
   return bits;
 }
 
 // 4 values -> 4 signed bytes, each rounded to the nearest even integer: adding
 // 1.5 * 2^23 leaves the integer in the low bits of the sum.
-MOE_DEVINL uint32_t act8_codes4(const float *v, float s, float inv) {
-  uint32_t b[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(div_exact(v[i], s, inv) + 12582912.0f);
-  return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+MOE_DEVINL uint32_t act8_codes4(const float *v, uint64_t minus_s, uint64_t inv) {
+  const uint64_t magic = pack2(12582912.0f, 12582912.0f);
+  float b[4];
+  unpack2(add2(div_exact2(pack2(v[0], v[1]), minus_s, inv), magic), b[0], b[1]);
+  unpack2(add2(div_exact2(pack2(v[2], v[3]), minus_s, inv), magic), b[2], b[3]);
+  return __byte_perm(__byte_perm(__float_as_uint(b[0]), __float_as_uint(b[1]), 0x0040),
+                     __byte_perm(__float_as_uint(b[2]), __float_as_uint(b[3]), 0x0040), 0x5410);
 }
 
 // Codes of the lane's 8 values and the block's scale bits (4 lanes a block).
@@ -61,11 +63,9 @@ MOE_DEVINL uint2 act8_quantize8(const uint4 &w, uint32_t &sbits) {
   float s, inv, v[8];
   sbits = act8_scale(a, s, inv);
   bf16x8_to_f32(w, v);
-  if (sbits == 0x7FC0u) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  }
-  return make_uint2(act8_codes4(v, s, inv), act8_codes4(v + 4, s, inv));
+  const uint64_t inv2 = pack2(inv, inv), ms2 = pack2(-s, -s);
+  const uint2 q = make_uint2(act8_codes4(v, ms2, inv2), act8_codes4(v + 4, ms2, inv2));
+  return sbits == 0x7FC0u ? make_uint2(0u, 0u) : q;  // (a NaN's code is no number)
 }
 
 MOE_DEVINL void act8_values8(const uint2 &q, uint32_t sbits, float *v) {

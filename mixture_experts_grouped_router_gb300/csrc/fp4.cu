@@ -172,6 +172,7 @@ fp4_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t src_row
     R = gr.off[E];
   }
   const float g1 = FMT == MOE_FP4_NV && GROUPED && gscale != nullptr ? ld_f32(gscale) : 1.0f;
+  const float inv6_1 = __frcp_rn(6.0f * g1);
   int e = 0;
   while (w.row < R) {
     const int r = w.row, c0 = w.seg * (256 * kUnroll) + lane * 8;
@@ -180,6 +181,7 @@ fp4_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t src_row
     w.step();
     load(next, src);
     const float g = FMT == MOE_FP4_NV && !GROUPED && gscale != nullptr ? ld_f32(gscale + r / G) : g1;
+    const float inv6 = GROUPED ? inv6_1 : __frcp_rn(6.0f * g);
     const int64_t pr = GROUPED ? grouped_row(gr, e, r) : weight_row(r, G, row_map);
     if (pr >= 0) {
       uint8_t *qr = q + r * ldq + (c0 >> 1);
@@ -193,12 +195,10 @@ fp4_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t src_row
         a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
         if (FMT != MOE_FP4_NV) a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
         float t, inv, v[8];
-        const uint32_t code = fp4_block_scale<FMT>(__uint_as_float(a << 16), g, t, inv);
+        const uint32_t code =
+            fp4_block_scale<FMT>(__uint_as_float(a << 16), g, 6.0f * g, inv6, t, inv);
         bf16x8_to_f32(cur[i], v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = fp4_quotient<FMT>(v[j], t, inv);
-        uint32_t codes = cvt_e2m1x8(v);
-        if (inv == 0.0f) codes = 0;  // (a NaN times 0 is no zero code)
+        const uint32_t codes = fp4_codes8<FMT>(v, t, inv);
         const uint32_t word = scale_word<FMT>(c < cols ? code : 0u, lane);
         constexpr int kLanes = FMT == MOE_FP4_NV ? 8 : 16;  // lanes of a word
         if (c < cols) {
@@ -295,13 +295,14 @@ fp4_quantize_weights_kernel(const uint16_t *__restrict__ w, int K, int N, int ro
 #pragma unroll
     for (int j = 0; j < kB; ++j) a = max(a, (uint32_t)tile[kb + b * kB + j][nn] & 0x7FFFu);
     float t, inv, v[kB];
-    const uint32_t code = fp4_block_scale<FMT>(__uint_as_float(a << 16), g, t, inv);
+    const uint32_t code = fp4_block_scale<FMT>(__uint_as_float(a << 16), g, 6.0f * g,
+                                               __frcp_rn(6.0f * g), t, inv);
 #pragma unroll
     for (int j = 0; j < kB; ++j)
-      v[j] = fp4_quotient<FMT>(__uint_as_float((uint32_t)tile[kb + b * kB + j][nn] << 16), t, inv);
+      v[j] = __uint_as_float((uint32_t)tile[kb + b * kB + j][nn] << 16);
 #pragma unroll
     for (int j = 0; j < kB / 8; ++j)
-      codes[b * (kB / 8) + j] = inv == 0.0f ? 0u : cvt_e2m1x8(v + 8 * j);
+      codes[b * (kB / 8) + j] = fp4_codes8<FMT>(v + 8 * j, t, inv);
     const int blk = k / kB + b;
     if (blk < 4 * ac) sf[fp4_scale_byte(pr, blk, ac)] = k < K ? (uint8_t)code : (uint8_t)0;
   }

@@ -168,7 +168,7 @@ MOE_DEVINL void stage_f32(uint8_t *buf, int r, const float *v) {
 // two bytes, MXFP4: one).  The values are continuous, so that no quotient sits
 // on a tie and a product with the reciprocal decides as the quotient would.
 template <int FMT>
-MOE_DEVINL uint4 quantize_chunk(float *v, float g, uint32_t &scale) {
+MOE_DEVINL uint4 quantize_chunk(float *v, float g, float inv6, uint32_t &scale) {
   constexpr int kB = fp4_block(FMT);
   uint32_t codes[4];
   scale = 0;
@@ -183,7 +183,9 @@ MOE_DEVINL uint4 quantize_chunk(float *v, float g, uint32_t &scale) {
       a = fmaxf(a, m);
     }
     float t, inv;
-    scale |= fp4_block_scale<FMT>(finite ? a : __uint_as_float(0x7F800000u), g, t, inv) << (8 * b);
+    scale |= fp4_block_scale<FMT>(finite ? a : __uint_as_float(0x7F800000u), g, 6.0f * g, inv6, t,
+                                  inv)
+             << (8 * b);
 #pragma unroll
     for (int j = 0; j < kB; ++j) v[b * kB + j] *= inv;
 #pragma unroll
@@ -208,6 +210,7 @@ MOE_DEVINL void epilogue(const Book &bk, const Fp4Params &p, const TileInfo &ti,
     const int F = p.F;
     const int n0 = ti.n_idx * (BN / 2);
     const float g2 = FMT == MOE_FP4_NV && p.g2 != nullptr ? ld_f32(p.g2) : 1.0f;
+    const float inv6 = __frcp_rn(6.0f * g2);
     // the row's place in Act's scale atoms
     const int arow = (int)bk.poff[ti.e] + ti.m_idx;
     uint8_t *srow = p.sf2 + (int64_t)arow * p.ac2 * 512 + lane * 16 + q * 4;
@@ -254,7 +257,7 @@ MOE_DEVINL void epilogue(const Book &bk, const Fp4Params &p, const TileInfo &ti,
 #pragma unroll
       for (int j = 0; j < 32; ++j) g[j] = g[j] * sigmoid_f(g[j]) * u[j];
       uint32_t scale;
-      const uint4 codes = quantize_chunk<FMT>(g, g2, scale);
+      const uint4 codes = quantize_chunk<FMT>(g, g2, inv6, scale);
       if (put) {
         st_v4(p.Q2 + row * p.ldq2 + (nc >> 1), codes);
         const int b = nc / fp4_block(FMT);

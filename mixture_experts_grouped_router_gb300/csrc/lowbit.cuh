@@ -7,6 +7,55 @@
 
 namespace moe {
 
+// Pairs of fp32 values in one 64-bit register: one instruction for two of them.
+MOE_DEVINL uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+MOE_DEVINL void unpack2(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+
+MOE_DEVINL uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+MOE_DEVINL uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+MOE_DEVINL uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// 1 / t to within a bit (t a normal float); div_exact corrects what it costs.
+MOE_DEVINL float rcp_approx(float t) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+  return r;
+}
+
+// x / t by a reciprocal and one residual step: where x / t is representable
+// (a tie of the code grid, for bf16 x and scales of few bits) the result is
+// exact, so that ties round as the quotient's definition says.
+MOE_DEVINL float div_exact(float x, float t, float inv) {
+  const float q = x * inv;
+  return fmaf(fmaf(-q, t, x), inv, q);
+}
+
+MOE_DEVINL uint64_t div_exact2(uint64_t x, uint64_t minus_t, uint64_t inv) {
+  const uint64_t q = mul2(x, inv);
+  return fma2(fma2(q, minus_t, x), inv, q);
+}
+
 // Elements per scale of a 4-bit format, and columns per 512-byte scale atom
 // (128 rows x 4 blocks).
 __host__ __device__ constexpr int fp4_block(int fmt) { return fmt == MOE_FP4_NV ? 16 : 32; }
@@ -80,19 +129,20 @@ MOE_DEVINL float fp4_scale_value(uint32_t code, int fmt) {
 // or 0 where every code of the block is 0 (no magnitude, or a NaN / infinity,
 // which takes the NaN scale).
 //   MXFP4: t = 2^s, s = floor(log2 a) - 2 clamped to [-127, 127] (OCP MX v1.0)
-//   NVFP4: E4M3(a / (6 g)), g the tensor's fp32 scale
+//   NVFP4: E4M3(a / (6 g)), g the tensor's fp32 scale; g6 = 6 g, inv6 = 1 / g6
 template <int FMT>
-MOE_DEVINL uint32_t fp4_block_scale(float a, float g, float &t, float &inv) {
+MOE_DEVINL uint32_t fp4_block_scale(float a, float g, float g6, float inv6, float &t,
+                                    float &inv) {
   t = 1.0f;
   inv = 0.0f;
   const bool finite = a <= 3.402823466e38f;
   if (FMT == MOE_FP4_NV) {
     if (!finite) return 0x7Fu;
-    const uint32_t code = e4m3_code(__fdiv_rn(a, 6.0f * g));
+    const uint32_t code = e4m3_code(div_exact(a, g6, inv6));
     const float s = e4m3_value(code) * g;
     if (s >= 1.17549435e-38f) {
       t = s;
-      inv = __frcp_rn(s);
+      inv = rcp_approx(s);
     }
     return code;
   }
@@ -106,25 +156,28 @@ MOE_DEVINL uint32_t fp4_block_scale(float a, float g, float &t, float &inv) {
   return (uint32_t)(s + 127);
 }
 
-// x / t by a reciprocal and one residual step: where x / t is representable
-// (a tie of the code grid, for bf16 x and scales of few bits) the result is
-// exact, so that ties round as the quotient's definition says.
-MOE_DEVINL float div_exact(float x, float t, float inv) {
-  const float q = x * inv;
-  return fmaf(fmaf(-q, t, x), inv, q);
-}
-
+// 8 values -> 8 codes, by the block's t and inv.
 template <int FMT>
-MOE_DEVINL float fp4_quotient(float x, float t, float inv) {
-  return FMT == MOE_FP4_NV ? div_exact(x, t, inv) : x * inv;
+MOE_DEVINL uint32_t fp4_codes8(const float *v, float t, float inv) {
+  const uint64_t inv2 = pack2(inv, inv), mt2 = pack2(-t, -t);
+  float r[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint64_t x = pack2(v[2 * j], v[2 * j + 1]);
+    unpack2(FMT == MOE_FP4_NV ? div_exact2(x, mt2, inv2) : mul2(x, inv2), r[2 * j], r[2 * j + 1]);
+  }
+  // (a NaN or an infinity times 0 is no zero code)
+  return inv == 0.0f ? 0u : cvt_e2m1x8(r);
 }
 
-// Largest magnitude of 8 bf16 values, as bf16 bits: compared as integers, so
-// that a NaN or an infinity wins.
+// Largest magnitude of 8 bf16 values, as bf16 bits; a NaN wins over everything
+// and an infinity over every number.
 MOE_DEVINL uint32_t amax_bits8(const uint4 &w) {
-  const uint32_t m = 0x7FFF7FFFu;
-  const uint32_t a = __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
-  return max(a & 0xFFFFu, a >> 16);
+  const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&w);
+  const __nv_bfloat162 a = __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])),
+                                       __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
+  const uint32_t b = *reinterpret_cast<const uint32_t *>(&a);
+  return max(b & 0xFFFFu, b >> 16);
 }
 
 }  // namespace moe

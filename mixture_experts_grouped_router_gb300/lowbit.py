@@ -156,23 +156,9 @@ def fp4_experts(w: Fp4Experts, b: Fp4Buffers, x, sorted_to_flat, k, group_offset
 
 
 # --------------------------------------------------- 8-bit activation checkpoints
-def act8_quantize(x, q, scales, group_offsets=None, stream=None):
-    """x bf16 [rows, cols] -> q int8 [rows, cols], scales bf16 [rows, ceil(cols / 32)]."""
-    L.moe_act8_quantize(x, q, scales, group_offsets, stream)
-
-
-def act8_dequantize(q, scales, out, group_offsets=None, stream=None):
-    """The values of the codes into out bf16 [rows, cols]."""
-    L.moe_act8_dequantize(q, scales, out, group_offsets, stream)
-
-
-def act8_swiglu_fwd(h, act, q, scales, group_offsets=None, stream=None):
-    """h bf16 [rows, 2F] -> act bf16 [rows, F] and h's codes q int8 [rows, 2F], scales bf16
-    [rows, 2 ceil(F / 32)]."""
-    L.moe_act8_swiglu_fwd(h, act, q, scales, group_offsets, stream)
-
-
-def act8_swiglu_bwd(q, scales, dact, dh, act=None, group_offsets=None, stream=None):
-    """From h's codes and dact bf16 [rows, F]: dh bf16 [rows, 2F] and, unless None, act bf16
-    [rows, F] recomputed."""
-    L.moe_act8_swiglu_bwd(q, scales, dact, dh, act, group_offsets, stream)
+# x bf16 [rows, cols] <-> q int8 [rows, cols], scales bf16 [rows, ceil(cols / 32)]; h bf16
+# [rows, 2F] -> act and its codes; codes and dact -> dh and act (see the functions' own words)
+act8_quantize = L.moe_act8_quantize
+act8_dequantize = L.moe_act8_dequantize
+act8_swiglu_fwd = L.moe_act8_swiglu_fwd
+act8_swiglu_bwd = L.moe_act8_swiglu_bwd
