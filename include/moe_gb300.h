@@ -57,6 +57,8 @@ enum { MOE_EPI_NONE = 0, MOE_EPI_SWIGLU_FWD = 1, MOE_EPI_SWIGLU_BWD = 2 };
 enum { MOE_FP8_E4M3 = 0, MOE_FP8_E5M2 = 1 };
 /* 4-bit block-scaled formats (E2M1 elements): MXFP4 and NVFP4 */
 enum { MOE_FP4_MX = 0, MOE_FP4_NV = 1 };
+/* row orders of their scale atoms */
+enum { MOE_FP4_ROWS_GROUPED = 1, MOE_FP4_ROWS_SWIGLU = 2, MOE_FP4_ROWS_EXPERTS = 3 };
 /* row orders of block-scale atoms (moe_mx_quantize) */
 enum { MOE_MX_ROWS_PLAIN = 0, MOE_MX_ROWS_GROUPED = 1, MOE_MX_ROWS_SWIGLU = 2,
        MOE_MX_ROWS_TILES = 3 };
@@ -560,11 +562,12 @@ moe_status_t moe_tgmm_mx(const uint8_t *At, int64_t ldat, const uint8_t *sfa, in
  * them too (as plain factors), its quantisers ignore them.
  * Scales are kept in 512-byte atoms of 128 rows x 4 blocks: row r0 + 32 r1 (r0 <
  * 32, r1 < 4), block j at byte 16 r0 + 4 r1 + j; a row of atoms holds ceil(cols /
- * (4 block)) of them, the last one's spare blocks zero.  Rows map to atoms as
- * in moe_mx_quantize: MOE_MX_ROWS_GROUPED for activations, MOE_MX_ROWS_TILES
- * and MOE_MX_ROWS_SWIGLU for weights of E experts (SWIGLU: 2F rows an expert,
- * [gate | up], row n < F of expert e in tile t = n / 96 at padded row
- * 256 (e ceil(F / 96) + t) + n % 96, row F + n 96 further).
+ * (4 block)) of them, the last one's spare blocks zero.  Rows map to atom rows by
+ *   MOE_FP4_ROWS_GROUPED  activations: each group starts a new atom
+ *   MOE_FP4_ROWS_EXPERTS  weights: E equal groups, each starting a new atom
+ *   MOE_FP4_ROWS_SWIGLU   the same for a fused up-projection, 2F rows an expert
+ *        as [gate | up]: gate row n at row 64 (n / 32) + n % 32 of the expert's
+ *        atoms, up row n 32 further (32 gate rows and 32 up rows in turn)
  * Columns (the contraction): multiples of 32.
  */
 
@@ -581,7 +584,7 @@ size_t moe_fp4_scale_bytes(int64_t rows, int cols, int fmt, int row_map, int E);
  *              dev_status and reads as zeros.  NULL: row p (src_rows >= rows)
  *   GROUPED    group_offsets int32 [E + 1] device; rows at or past
  *              group_offsets[E], and the scales of padding rows, are not written
- *   TILES, SWIGLU  K-major weights, rows = E equal groups; scale fp32 [E]
+ *   EXPERTS, SWIGLU  K-major weights, rows = E equal groups; scale fp32 [E]
  *   ldx % 8 == 0, ldq % 16 == 0; x, q, sf 16-byte aligned; E <= 256 (GROUPED)
  */
 moe_status_t moe_fp4_quantize(const uint16_t *x, int64_t ldx, int64_t src_rows,
@@ -602,7 +605,7 @@ moe_status_t moe_fp4_dequantize(const uint8_t *q, int64_t ldq, const uint8_t *sf
 /*
  * moe_fp4_quantize_weights -- w bf16 [E, K, N] contiguous (contraction K down
  * the rows, the layer's wi and wo) -> K-major codes q uint8 [E, N, K / 2] and
- * atoms of the [E N, K] matrix in TILES or SWIGLU order.  K % 32 == 0.
+ * atoms of the [E N, K] matrix in EXPERTS or SWIGLU order.  K % 32 == 0.
  */
 moe_status_t moe_fp4_quantize_weights(const uint16_t *w, int E, int K, int N, int fmt, int row_map,
                                       const float *scale, uint8_t *q, uint8_t *sf,
@@ -610,7 +613,7 @@ moe_status_t moe_fp4_quantize_weights(const uint16_t *w, int E, int K, int N, in
 
 /*
  * moe_fp4_arrange_scales -- scales in row order, uint8 [rows, cols / block]
- * contiguous (as 4-bit checkpoints store them), into atoms (TILES or SWIGLU).
+ * contiguous (as 4-bit checkpoints store them), into atoms (EXPERTS or SWIGLU).
  */
 moe_status_t moe_fp4_arrange_scales(const uint8_t *scales, int64_t rows, int cols, int fmt,
                                     int row_map, int E, uint8_t *sf, size_t sf_bytes,
@@ -621,7 +624,7 @@ moe_status_t moe_fp4_arrange_scales(const uint8_t *scales, int64_t rows, int col
  *     S[r, :] = a_scale b_scale[e] sum over blocks (code scale) . (code scale)
  *   A    codes [rows_cap, lda >= K / 2 bytes], atoms sfa GROUPED
  *   B    codes of expert e at B + e * stride_b, [N, ldb >= K / 2 bytes]; atoms sfb
- *        TILES (MOE_EPI_NONE) or SWIGLU (MOE_EPI_SWIGLU_FWD, N = 2F, F % 32 == 0)
+ *        EXPERTS (MOE_EPI_NONE) or SWIGLU (MOE_EPI_SWIGLU_FWD, N = 2F, F % 32 == 0)
  *   MOE_EPI_NONE        C = S as c_dtype (ldc rows of whole 16 bytes)
  *   MOE_EPI_SWIGLU_FWD  Act = silu(S[:, :F]) * S[:, F:], quantised from the fp32
  *        values with q2_scale: codes Q2 [rows_cap, ldq2 >= F / 2 bytes] and atoms
@@ -642,7 +645,7 @@ moe_status_t moe_gmm_fp4(const uint8_t *A, int64_t lda, const uint8_t *sfa, cons
  * of the permuted rows of x, moe_gmm_fp4 with the SwiGLU epilogue, moe_gmm_fp4:
  *     y[p] = FFN_e(x[sorted_to_flat[p] / k])   for the rows p of group e
  *   w   the weights: wi codes [E, 2f, d / 2] with atoms SWIGLU, wo codes
- *       [E, d, f / 2] with atoms TILES (contiguous), their fp32 scales [E] or
+ *       [E, d, f / 2] with atoms EXPERTS (contiguous), their fp32 scales [E] or
  *       NULL, the scales of x and of Act (fp32 [1] or NULL)
  *   b   buffers for rows_cap permuted rows: codes and atoms (GROUPED) of x and of
  *       Act, y bf16 [rows_cap, d]; h bf16 [rows_cap, 2f] or NULL

@@ -463,6 +463,9 @@ def moe_tgmm_mx(At, sfa, a_fmt, Bt, sfb, b_fmt, group_offsets, rows_cap, W, accu
 # ------------------------------------------------------- microscaled 4-bit floats
 FP4_MX = 0
 FP4_NV = 1
+FP4_ROWS_GROUPED = 1
+FP4_ROWS_SWIGLU = 2
+FP4_ROWS_EXPERTS = 3
 
 
 def moe_fp4_scale_bytes(rows: int, cols: int, fmt: int, row_map: int, E: int = 1) -> int:
@@ -473,10 +476,10 @@ def _groups(group_offsets, groups):
     return groups if group_offsets is None else group_offsets.shape[0] - 1
 
 
-def moe_fp4_quantize(x, fmt, q, sf, row_map=MX_ROWS_GROUPED, group_offsets=None, groups=1,
+def moe_fp4_quantize(x, fmt, q, sf, row_map=FP4_ROWS_GROUPED, group_offsets=None, groups=1,
                      row_index=None, index_div=1, scale=None, dev_status=None, stream=None):
     """Rows of x bf16 [src_rows, cols] (gathered through row_index / index_div) -> q uint8
-    [rows, cols / 2], sf uint8 scale atoms; GROUPED takes group_offsets, TILES / SWIGLU the
+    [rows, cols / 2], sf uint8 scale atoms; GROUPED takes group_offsets, EXPERTS / SWIGLU the
     number of equal row groups."""
     rows, cols = q.shape[0], x.shape[1]
     _check(LIB.moe_fp4_quantize(_ptr(x), _ld(x), x.shape[0], _ptr(row_index), index_div, rows,
@@ -485,7 +488,7 @@ def moe_fp4_quantize(x, fmt, q, sf, row_map=MX_ROWS_GROUPED, group_offsets=None,
                                 _ptr(sf), sf.numel(), _ptr(dev_status), _stream(stream)))
 
 
-def moe_fp4_dequantize(q, sf, fmt, x, row_map=MX_ROWS_GROUPED, group_offsets=None, groups=1,
+def moe_fp4_dequantize(q, sf, fmt, x, row_map=FP4_ROWS_GROUPED, group_offsets=None, groups=1,
                        scale=None, stream=None):
     """Codes q [rows, cols / 2] with scale atoms sf -> x bf16 [rows, cols]."""
     rows, cols = x.shape

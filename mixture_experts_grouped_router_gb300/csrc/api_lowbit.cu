@@ -28,7 +28,7 @@ static moe_status_t cuda_status(cudaError_t e, const char *what) {
 static bool good_fmt(int fmt) { return fmt == MOE_FP4_MX || fmt == MOE_FP4_NV; }
 
 static bool good_map(int m) {
-  return m == MOE_MX_ROWS_GROUPED || m == MOE_MX_ROWS_TILES || m == MOE_MX_ROWS_SWIGLU;
+  return m == MOE_FP4_ROWS_GROUPED || m == MOE_FP4_ROWS_EXPERTS || m == MOE_FP4_ROWS_SWIGLU;
 }
 
 // Rows of a quantised matrix: groups, and what their map asks of them.
@@ -40,14 +40,14 @@ static moe_status_t check_rows(const char *who, int64_t rows, int cols, int fmt,
   REQUIRE(good_map(row_map), MOE_ERR_INVALID_ARG, "%s: bad row_map %d", who, row_map);
   REQUIRE(cols % 32 == 0, MOE_ERR_UNSUPPORTED, "%s: cols=%d is no multiple of 32", who, cols);
   REQUIRE(rows < (1ll << 31) - (1 << 20), MOE_ERR_UNSUPPORTED, "%s: too many rows (2^31)", who);
-  if (row_map == MOE_MX_ROWS_GROUPED) {
+  if (row_map == MOE_FP4_ROWS_GROUPED) {
     REQUIRE(E <= 256, MOE_ERR_UNSUPPORTED, "%s: E=%d > 256", who, E);
     REQUIRE(offsets != nullptr || rows == 0, MOE_ERR_INVALID_ARG,
             "%s: GROUPED needs group_offsets", who);
   } else {
     REQUIRE(rows % E == 0, MOE_ERR_INVALID_ARG, "%s: rows=%lld are no E=%d equal groups", who,
             (long long)rows, E);
-    REQUIRE(row_map != MOE_MX_ROWS_SWIGLU || rows / E % 64 == 0, MOE_ERR_UNSUPPORTED,
+    REQUIRE(row_map != MOE_FP4_ROWS_SWIGLU || rows / E % 64 == 0, MOE_ERR_UNSUPPORTED,
             "%s: SWIGLU needs 2F rows an expert, F a multiple of 32", who);
   }
   return MOE_OK;
@@ -120,8 +120,8 @@ moe_status_t moe_fp4_quantize_weights(const uint16_t *w, int E, int K, int N, in
                                       const float *scale, uint8_t *q, uint8_t *sf,
                                       size_t sf_bytes, moe_stream_t stream) {
   set_error("");
-  REQUIRE(row_map != MOE_MX_ROWS_GROUPED, MOE_ERR_INVALID_ARG,
-          "moe_fp4_quantize_weights: row_map must be TILES or SWIGLU");
+  REQUIRE(row_map != MOE_FP4_ROWS_GROUPED, MOE_ERR_INVALID_ARG,
+          "moe_fp4_quantize_weights: row_map must be EXPERTS or SWIGLU");
   REQUIRE(N > 0, MOE_ERR_INVALID_ARG, "moe_fp4_quantize_weights: N=%d", N);
   const moe_status_t st = check_rows("moe_fp4_quantize_weights", (int64_t)std::max(E, 0) * N, K,
                                      fmt, row_map, nullptr, E);
@@ -143,8 +143,8 @@ moe_status_t moe_fp4_arrange_scales(const uint8_t *scales, int64_t rows, int col
                                     int row_map, int E, uint8_t *sf, size_t sf_bytes,
                                     moe_stream_t stream) {
   set_error("");
-  REQUIRE(row_map != MOE_MX_ROWS_GROUPED, MOE_ERR_INVALID_ARG,
-          "moe_fp4_arrange_scales: row_map must be TILES or SWIGLU");
+  REQUIRE(row_map != MOE_FP4_ROWS_GROUPED, MOE_ERR_INVALID_ARG,
+          "moe_fp4_arrange_scales: row_map must be EXPERTS or SWIGLU");
   const moe_status_t st =
       check_rows("moe_fp4_arrange_scales", rows, cols, fmt, row_map, nullptr, E);
   if (st != MOE_OK) return st;
@@ -199,9 +199,9 @@ moe_status_t moe_gmm_fp4(const uint8_t *A, int64_t lda, const uint8_t *sfa, cons
   REQUIRE(aligned(A, 16) && aligned(B, 16) && aligned(sfa, 16) && aligned(sfb, 16) &&
               aligned(C, 16) && aligned(Q2, 16) && aligned(sf2, 16),
           MOE_ERR_UNSUPPORTED, "moe_gmm_fp4: operands must be 16-byte aligned");
-  REQUIRE(!swiglu || sf2_bytes >= moe_fp4_scale_bytes(rows_cap, N / 2, fmt, MOE_MX_ROWS_GROUPED, E),
+  REQUIRE(!swiglu || sf2_bytes >= moe_fp4_scale_bytes(rows_cap, N / 2, fmt, MOE_FP4_ROWS_GROUPED, E),
           MOE_ERR_INVALID_ARG, "moe_gmm_fp4: sf2 of %zu bytes < %zu", sf2_bytes,
-          moe_fp4_scale_bytes(rows_cap, N / 2, fmt, MOE_MX_ROWS_GROUPED, E));
+          moe_fp4_scale_bytes(rows_cap, N / 2, fmt, MOE_FP4_ROWS_GROUPED, E));
   moe::GmmFp4Args a{A, lda, sfa, a_scale, B, ldb, stride_b, sfb, b_scale, fmt, group_offsets, E,
                     rows_cap, K, N, epilogue, C, c_dtype, ldc, Q2, ldq2, sf2, q2_scale,
                     dev_status};
@@ -236,14 +236,14 @@ moe_status_t moe_fp4_experts(const moe_fp4_weights *w, const moe_fp4_buffers *b,
           MOE_ERR_UNSUPPORTED, "moe_fp4_experts: operands must be 16-byte aligned");
   REQUIRE(ldx >= w->d, MOE_ERR_INVALID_ARG, "moe_fp4_experts: ldx=%lld < d", (long long)ldx);
   REQUIRE(b->x_sf_bytes >=
-                  moe_fp4_scale_bytes(b->rows_cap, w->d, w->fmt, MOE_MX_ROWS_GROUPED, w->E) &&
+                  moe_fp4_scale_bytes(b->rows_cap, w->d, w->fmt, MOE_FP4_ROWS_GROUPED, w->E) &&
               b->act_sf_bytes >=
-                  moe_fp4_scale_bytes(b->rows_cap, w->f, w->fmt, MOE_MX_ROWS_GROUPED, w->E),
+                  moe_fp4_scale_bytes(b->rows_cap, w->f, w->fmt, MOE_FP4_ROWS_GROUPED, w->E),
           MOE_ERR_INVALID_ARG, "moe_fp4_experts: scale buffers too small");
   cudaStream_t s = (cudaStream_t)stream;
   moe_status_t st = cuda_status(
       moe::launch_fp4_quantize(x, ldx, T, sorted_to_flat, k, b->rows_cap, w->d, w->fmt,
-                               MOE_MX_ROWS_GROUPED, group_offsets, w->E, w->x_scale, b->x_q,
+                               MOE_FP4_ROWS_GROUPED, group_offsets, w->E, w->x_scale, b->x_q,
                                w->d / 2, b->x_sf, b->dev_status, s),
       "moe_fp4_experts: quantise");
   if (st != MOE_OK) return st;

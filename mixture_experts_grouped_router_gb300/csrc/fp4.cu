@@ -15,9 +15,9 @@
 // Scales sit in 512-byte atoms of 128 rows x 4 blocks, which tcgen05.cp brings
 // to tensor memory as they are: row r0 + 32 r1, block j at byte 16 r0 + 4 r1 +
 // j; the atoms of a row of atoms follow one another, ceil(cols / (4 block)) of
-// them, the last one's spare blocks zero.  Row maps: GROUPED (activations, each
-// group padded to whole atoms), TILES and SWIGLU (weights, 192 rows of an
-// expert to two atoms).
+// them, the last one's spare blocks zero.  Row maps: GROUPED (activations) and
+// EXPERTS (weights), each group or expert padded to whole atoms, and SWIGLU, the
+// fused up-projection with 32 gate rows and 32 up rows in turn.
 #include <algorithm>
 
 #include "internal.h"
@@ -34,12 +34,13 @@ constexpr int kMaxE = 256;
 // Padded row of row r of rows = E G under the maps that need no offsets.
 MOE_DEVINL int64_t weight_row(int64_t r, int64_t G, int row_map) {
   const int64_t e = r / G, n = r - e * G;
-  if (row_map == MOE_MX_ROWS_SWIGLU) {
+  int64_t m = n;
+  if (row_map == MOE_FP4_ROWS_SWIGLU) {
     const int64_t F = G / 2;
-    const int64_t m = n < F ? n : n - F;
-    return (e * ((F + 95) / 96) + m / 96) * 256 + (n < F ? 0 : 96) + m % 96;
+    const int64_t f = n < F ? n : n - F;
+    m = f / 32 * 64 + (n < F ? 0 : 32) + f % 32;
   }
-  return (e * ((G + 191) / 192) + n / 192) * 256 + n % 192;
+  return e * ((G + 127) / 128 * 128) + m;
 }
 
 // The groups' first rows and their padded starts (sizes rounded up to 128), by
@@ -343,10 +344,8 @@ int grid_for(int64_t rows, int cols) {
 }  // namespace
 
 int64_t fp4_atom_rows(int64_t rows, int row_map, int E) {
-  const int64_t G = rows / E;
-  if (row_map == MOE_MX_ROWS_GROUPED) return f8_padded_rows(rows, E) / 128;
-  if (row_map == MOE_MX_ROWS_SWIGLU) return 2 * (int64_t)E * ((G / 2 + 95) / 96);
-  return 2 * (int64_t)E * ((G + 191) / 192);
+  if (row_map == MOE_FP4_ROWS_GROUPED) return f8_padded_rows(rows, E) / 128;
+  return (int64_t)E * ((rows / E + 127) / 128);
 }
 
 cudaError_t launch_fp4_quantize(const uint16_t *x, int64_t ldx, int64_t src_rows,
@@ -355,7 +354,7 @@ cudaError_t launch_fp4_quantize(const uint16_t *x, int64_t ldx, int64_t src_rows
                                 const float *gscale, uint8_t *q, int64_t ldq, uint8_t *sf,
                                 int32_t *dev_status, cudaStream_t st) {
   const int grid = grid_for(rows, cols);
-  const bool grouped = row_map == MOE_MX_ROWS_GROUPED;
+  const bool grouped = row_map == MOE_FP4_ROWS_GROUPED;
   auto run = [&](auto kernel) {
     return launch_dependent(kernel, grid, kThreads, 0, st, x, ldx, src_rows, row_index, index_div,
                             (int)rows, cols, row_map, offsets, E, gscale, q, ldq, sf, dev_status);
@@ -372,7 +371,7 @@ cudaError_t launch_fp4_dequantize(const uint8_t *q, int64_t ldq, const uint8_t *
                                   const float *gscale, uint16_t *x, int64_t ldx,
                                   cudaStream_t st) {
   const int grid = grid_for(rows, cols);
-  const bool grouped = row_map == MOE_MX_ROWS_GROUPED;
+  const bool grouped = row_map == MOE_FP4_ROWS_GROUPED;
   auto run = [&](auto kernel) {
     return launch_dependent(kernel, grid, kThreads, 0, st, q, ldq, sf, (int)rows, cols, row_map,
                             offsets, E, gscale, x, ldx);

@@ -3,22 +3,35 @@
 // codes with their scales applied by the tensor cores
 // (tcgen05.mma kind::mxf4nvf4.block_scale), fp32 accumulators in tensor memory.
 //
+// The product runs transposed: the weight's rows are the MMA's M (256, a pair of
+// CTAs), the expert's tokens its N, 16 to 192 in steps of 16.  An expert's last
+// tokens then cost what they are (a row tile of tokens would round them up to
+// 256), a single token costs N = 16, and the weights, which are what few tokens
+// wait for, fill every stage.
+//
 // Epilogues: plain (times the tensors' fp32 scales, to bf16 or fp32), and the
 // SwiGLU forward, which quantises Act = silu(g) u to 4 bits straight from the
-// fp32 accumulators: a thread holds a row's 32 columns, so that a block's
-// maximum needs no other thread, and the down-projection's operand leaves
-// the kernel as 16 bytes of codes and one or two scale bytes instead of 64
-// bytes of bf16 that another pass would read again.
+// fp32 accumulators, so that the down-projection's operand leaves the kernel as
+// codes and scales instead of bf16 that another pass would read again.  Gate and
+// up rows alternate in blocks of 32 along M: one warp holds a block's gates, its
+// neighbour the ups.  A block of 32 weight rows x 32 tokens is turned through
+// shared memory, and leaves as rows of tokens.
 //
-// Persistent; clusters of two CTAs issue 2-SM MMAs (M = 256, N = 192, K = 64
-// codes = 32 bytes).  A stage is a K block of 256 codes (one 128-byte swizzle
-// row a tile row): A 16 KB and half of B 12 KB a CTA, and the K block's scale
-// atoms (512 bytes of 128 rows x 4 blocks): 4 (NVFP4) or 2 (MXFP4) for A and
-// twice as many for B's 192 columns.
+// With many rows an expert and a short contraction the SwiGLU product runs the
+// other way round (kRows: M = 256 tokens, N = 192 weight rows): a thread then holds
+// a token's gates and ups of 32 features and quantises them without the shared
+// memory whose bandwidth the turned blocks share with the MMAs' operands.
+//
+// Persistent; clusters of two CTAs issue 2-SM MMAs (M = 256, K = 64 codes = 32
+// bytes).  A stage is a K block of 256 codes (one 128-byte swizzle row a row): a
+// CTA's 128 weight rows 16 KB, its half of the tokens up to 12 KB (in boxes of 32
+// rows), and the K block's scale atoms (512 bytes of 128 rows x 4 blocks): 4
+// (NVFP4) or 2 (MXFP4) for the weight rows and twice as many for 192 tokens.
 //   warp 0     TMA producer
 //   warp 1     tensor memory, and in the leader CTA the MMA issue: the atoms
 //              to tensor memory (tcgen05.cp), then four MMAs
-//   warps 2-5  epilogue, one per quarter of the tensor-memory lanes
+//   warps 2-9  epilogue, two per quarter of the tensor-memory lanes, which take the
+//              tile's chunks of 32 tokens in turn (kRows: warps 2-5)
 // Tensor memory: two accumulators of 192 columns, and scale slots in the 128
 // columns that they leave: 48 columns a K block (NVFP4, 2 slots) or 24 (MXFP4,
 // 5).  A slot is rewritten after the MMAs that read it are done: their commit
@@ -26,8 +39,7 @@
 // stage's copies, so that the issuer has one barrier to wait for.  That wait and
 // the issue set the pace (a K block's MMAs take about 300 cycles): the next
 // barrier is tested before a block's MMAs are issued, and the issuing warp stays
-// uniform, elect_one() choosing the lane.  8 experts, 32768 rows, 4096 x 28672:
-// lane == 0 in place of elect_one() 2.41 ms, a second wait for the slot 1.36 ms.
+// uniform, elect_one() choosing the lane.
 // Every wait is bounded; on time-out the CTA winds down and reports
 // MOE_ERR_TIMEOUT through dev_status.
 #include <cudaTypedefs.h>
@@ -42,55 +54,63 @@
 namespace moe {
 namespace {
 
-constexpr int BM = 128;        // rows of a CTA's A tile
-constexpr int BN = 192;        // columns of the pair's tile
-constexpr int kRowBytes = 128; // one K block of a tile row: 256 codes
+constexpr int BW = 256;        // weight rows of a tile (the pair's M)
+constexpr int BT = 192;        // most tokens of a tile (N)
+constexpr int kRowBytes = 128; // one K block of a row: 256 codes
 constexpr int kKSteps = 4;     // MMAs a K block
-constexpr int kStages = 6;
-constexpr int A_BYTES = BM * kRowBytes;
-constexpr int B_BYTES = BN / 2 * kRowBytes;
-constexpr int kEpiWarps = 4;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
-constexpr int kStgBytes = 4096;  // staging of an epilogue warp
+constexpr int W_BYTES = BW / 2 * kRowBytes;
+constexpr int T_BYTES = BT / 2 * kRowBytes;
+constexpr int kStgBytes = 4096;  // staging of an epilogue warp: one 32 x 32 fp32 block
 constexpr int kMaxE = 256;
-constexpr int kGroupPairs = 16;  // raster group: row-tile pairs that share B columns in L2
 constexpr int kTmemCols = 512;
 
-template <int FMT>
+// EPI: MOE_EPI_NONE, MOE_EPI_SWIGLU_FWD, or kRows (SwiGLU with tokens as M, whose
+// epilogue needs no staging).
+constexpr int kRows = 3;
+
+template <int FMT, int EPI>
 struct Lay {
+  static constexpr int epi_warps = EPI == kRows ? 4 : 8;
+  static constexpr int threads = 64 + 32 * epi_warps;
+  static constexpr int stages = FMT == MOE_FP4_NV && EPI != kRows ? 5 : 6;
   static constexpr int atoms = 256 / fp4_atom_cols(FMT);  // atom columns a K block
-  static constexpr int sfa_bytes = atoms * 512;
-  static constexpr int sfb_bytes = 2 * sfa_bytes;
-  static constexpr int tx_bytes = A_BYTES + B_BYTES + sfa_bytes + sfb_bytes;
-  static constexpr int stage_bytes = (tx_bytes + 1023) / 1024 * 1024;
+  static constexpr int sfw_bytes = atoms * 512;
+  static constexpr int sft_bytes = 2 * sfw_bytes;
+  static constexpr int stage_bytes = (W_BYTES + T_BYTES + sfw_bytes + sft_bytes + 1023) / 1024 * 1024;
   static constexpr int sf_cols = atoms * 12;               // tensor-memory columns a slot
-  static constexpr int sf_slots = (kTmemCols - 2 * BN) / sf_cols;
-  static_assert(sf_slots <= kStages, "a commit names a K block's next user by its stage");
-  static constexpr int stg_offset = kStages * stage_bytes;
-  static constexpr int book_offset = stg_offset + kEpiWarps * kStgBytes;
+  static constexpr int sf_slots = (kTmemCols - 2 * BT) / sf_cols;
+  static_assert(sf_slots <= stages, "a commit names a K block's next user by its stage");
+  static constexpr int stg_offset = stages * stage_bytes;
+  static constexpr int book_offset =
+      stg_offset + (EPI == kRows ? 0 : epi_warps * kStgBytes);
 };
 
+constexpr int kMaxStages = 6;
+
 struct Book {
-  uint64_t full[kStages];
-  uint64_t empty[kStages];
+  uint64_t full[kMaxStages];
+  uint64_t empty[kMaxStages];
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
   int total_tiles;
+  int off[kMaxE + 1];        // group offsets, clamped to [0, rows_cap]
   int cum[kMaxE + 1];        // per-expert tile prefix
   uint16_t poff[kMaxE + 1];  // padded group starts in units of 128 rows
 };
 
-template <int FMT>
+template <int FMT, int EPI>
 constexpr int smem_bytes() {
-  return 1024 + Lay<FMT>::book_offset + (int)((sizeof(Book) + 127) / 128 * 128);
+  return 1024 + Lay<FMT, EPI>::book_offset + (int)((sizeof(Book) + 127) / 128 * 128);
 }
-static_assert(smem_bytes<MOE_FP4_NV>() <= 232448, "shared memory of one CTA");
+static_assert(smem_bytes<MOE_FP4_NV, MOE_EPI_NONE>() <= 232448, "shared memory of one CTA");
+static_assert(smem_bytes<MOE_FP4_MX, MOE_EPI_NONE>() <= 232448, "shared memory of one CTA");
+static_assert(smem_bytes<MOE_FP4_NV, kRows>() <= 232448, "shared memory of one CTA");
 
 struct Fp4Params {
-  int E, rows_cap, N, F, n_tiles, kblocks;
+  int E, rows_cap, N, F, w_tiles, w_atoms, kblocks;
   const int32_t *offsets;
   void *C;
   int64_t ldc;
@@ -107,17 +127,28 @@ struct Fp4Params {
   int stall_loads;
 };
 
+struct Maps {
+  CUtensorMap w;     // weight codes
+  CUtensorMap t[3];  // token codes, boxes of 32, 64 and 96 rows
+  CUtensorMap sw;    // weight scale atoms
+  CUtensorMap st[2]; // token scale atoms, boxes of one and two atom rows
+  CUtensorMap c;     // plain output
+};
+
 struct TileInfo {
-  int e, m_idx, n_idx, row0, row_end;
+  int e, w_idx;      // expert, weight tile
+  int t0;            // first token within the group (a multiple of 192)
+  int row0, tokens;  // its row, and the tile's tokens (1 to 192)
+  int n;             // tokens rounded up to the MMA's step of 16
 };
 
 MOE_DEVINL int group_offset(const Fp4Params &p, int e) {
   return min(max(ld_i32(p.offsets + e), 0), p.rows_cap);
 }
 
-// Tile t: the two CTAs of a pair take row tiles 2 pm and 2 pm + 1 of an expert
-// and one column tile (the second may lie past the expert's rows).
-MOE_DEVINL TileInfo decode_tile(const Book &bk, const Fp4Params &p, int t, int crank) {
+// Tile t: an expert's token tiles follow one another under one weight tile, so
+// that the pairs that run at a time share its rows in L2.
+MOE_DEVINL TileInfo decode_tile(const Book &bk, const Fp4Params &p, int t) {
   int lo = 0, hi = p.E - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -125,48 +156,244 @@ MOE_DEVINL TileInfo decode_tile(const Book &bk, const Fp4Params &p, int t, int c
     else hi = mid - 1;
   }
   TileInfo ti;
-  ti.e = lo;
-  const int local = t - bk.cum[lo];
-  ti.row0 = group_offset(p, lo);
-  ti.row_end = max(group_offset(p, lo + 1), ti.row0);
-  const int mp = ((ti.row_end - ti.row0 + BM - 1) / BM + 1) / 2;
-  const int group = kGroupPairs * p.n_tiles;
+  ti.e = tc::uniform(lo);
+  const int off = tc::uniform(bk.off[ti.e]);
+  const int size = tc::uniform(max(bk.off[ti.e + 1], off)) - off;
+  const int local = t - tc::uniform(bk.cum[ti.e]);
+  const int tt = (size + BT - 1) / BT;
+  ti.w_idx = local / tt;
+  ti.t0 = (local - ti.w_idx * tt) * BT;
+  ti.row0 = off + ti.t0;
+  ti.tokens = min(size - ti.t0, BT);
+  ti.n = (ti.tokens + 15) / 16 * 16;
+  return ti;
+}
+
+// The tile's first token sits in row 0 of an atom, or in row 64 (two scale
+// columns on); whether its tokens reach into a second one.
+MOE_DEVINL int scale_shift(const TileInfo &ti) { return ti.t0 & 127 ? 2 : 0; }
+MOE_DEVINL bool second_atom(const TileInfo &ti) { return scale_shift(ti) * 32 + ti.n > 128; }
+
+// ---------------------------------------------------------------- epilogue
+// Thread `r`'s 32 values become column r of a 32 x 32 block (block row j = value
+// j), as the TMA store reads it: bf16 rows of 64 bytes under the 64-byte swizzle.
+// Lanes r and r ^ 1 trade a value a row pair and write 32-bit words, free of
+// bank conflicts.
+MOE_DEVINL void stage_bf16_t(uint8_t *buf, int r, const float *v) {
+  const bool odd = r & 1;
+  const int off = ((r >> 1) & 3) * 4;  // byte of the word within its 16-byte chunk
+  const int chunk = r >> 3;
+#pragma unroll
+  for (int m = 0; m < 16; ++m) {
+    const float recv = __shfl_xor_sync(0xffffffffu, odd ? v[2 * m] : v[2 * m + 1], 1);
+    const int n = 2 * m + (odd ? 1 : 0);
+    const __nv_bfloat162 w = odd ? __floats2bfloat162_rn(recv, v[2 * m + 1])
+                                 : __floats2bfloat162_rn(v[2 * m], recv);
+    *reinterpret_cast<__nv_bfloat162 *>(buf + n * 64 + ((chunk ^ ((n >> 1) & 3)) << 4) + off) = w;
+  }
+}
+
+// The same in fp32: rows of 128 bytes under the 128-byte swizzle.
+MOE_DEVINL void stage_f32_t(uint8_t *buf, int r, const float *v) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    *reinterpret_cast<float *>(buf + j * 128 + (((r >> 2) ^ (j & 7)) << 4) + (r & 3) * 4) = v[j];
+}
+
+// 16 fp32 values from 16 h on of row r of such a block.
+MOE_DEVINL void unstage_f32_16(const uint8_t *buf, int r, int h, float *v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 w = *reinterpret_cast<const float4 *>(buf + r * 128 + (((4 * h + i) ^ (r & 7)) << 4));
+    v[4 * i] = w.x;
+    v[4 * i + 1] = w.y;
+    v[4 * i + 2] = w.z;
+    v[4 * i + 3] = w.w;
+  }
+}
+
+// Two neighbouring epilogue warps (a block's gates and its ups) meet.
+MOE_DEVINL void pair_sync(int pair) {
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");
+}
+
+// The same, with one verdict for both.
+MOE_DEVINL bool pair_agree(bool ok, int pair) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "r"(1 + pair)
+      : "memory");
+  return r != 0;
+}
+
+// SwiGLU: warp q holds the gates (q even) or ups (q odd) of 32 features for the
+// tile's tokens.  A chunk of 32 tokens goes through the two warps' staging; a
+// thread then has one token's gates and ups of 16 features, which are a block of
+// NVFP4 or half a block of MXFP4, whose other half is its neighbour's.  The
+// values are continuous, so that no quotient sits on a tie and a product with the
+// reciprocal decides as the quotient would.
+template <int FMT>
+MOE_DEVINL void epilogue_swiglu(const Book &bk, const Fp4Params &p, const TileInfo &ti, float sc,
+                                float g2, float inv6, uint32_t taddr, int crank, int q, int sub,
+                                int lane, uint8_t *stg_pair) {
+  const int F = p.F;
+  // the pair of warps' 32 features
+  const int f0 = ti.w_idx * (BW / 2) + crank * (BW / 4) + (q >> 1) * 32;
+  if (f0 >= F) return;
+  const int pair = 2 * sub + (q >> 1);
+  const int tok = (q & 1) * 16 + (lane >> 1), h = lane & 1;
+  const int fh = f0 + 16 * h;  // this thread's features
+  if (sub * 32 >= ti.tokens) return;
+  uint32_t r[32];
+  tc::tmem_ld32_issue(taddr + sub * 32, r);
+#pragma unroll 1
+  for (int c = sub; c * 32 < ti.tokens; c += 2) {
+    {
+      float v[32];
+      tc::tmem_wait_ld(r);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * sc;
+      if (c > sub) pair_sync(pair);  // both warps are done with the last chunk
+      stage_f32_t(stg_pair + (q & 1) * kStgBytes, lane, v);
+    }
+    // the next chunk's values on their way while this one is worked on
+    if ((c + 2) * 32 < ti.tokens) tc::tmem_ld32_issue(taddr + (c + 2) * 32, r);
+    pair_sync(pair);
+    float g[16], u[16];
+    unstage_f32_16(stg_pair, tok, h, g);
+    unstage_f32_16(stg_pair + kStgBytes, tok, h, u);
+    const int t = c * 32 + tok;  // token of the tile
+    const int64_t row = (int64_t)ti.row0 + t;
+    const bool valid = t < ti.tokens;
+    if (p.C != nullptr && valid) {  // H in bf16 as well
+      uint16_t *H = static_cast<uint16_t *>(p.C) + row * p.ldc + fh;
+      st_v4(H, f32_to_bf16x8(g));
+      st_v4(H + 8, f32_to_bf16x8(g + 8));
+      st_v4(H + F, f32_to_bf16x8(u));
+      st_v4(H + F + 8, f32_to_bf16x8(u + 8));
+    }
+    float a = 0.0f;
+    bool finite = true;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      g[j] = g[j] * sigmoid_f(g[j]) * u[j];
+      const float m = fabsf(g[j]);
+      finite &= m <= 3.402823466e38f;
+      a = fmaxf(a, m);
+    }
+    if (!finite) a = __uint_as_float(0x7F800000u);
+    if (FMT != MOE_FP4_NV) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    float td, inv;
+    const uint32_t scale = fp4_block_scale<FMT>(a, g2, 6.0f * g2, inv6, td, inv);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) g[j] *= inv;
+    const uint32_t lo = inv == 0.0f ? 0u : cvt_e2m1x8(g);
+    const uint32_t hi = inv == 0.0f ? 0u : cvt_e2m1x8(g + 8);
+    // the row's place in Act's scale atoms
+    const int pr = ti.t0 + t;
+    const int arow = (int)bk.poff[ti.e] + (pr >> 7);
+    if (valid && arow < p.atom_rows2) {
+      *reinterpret_cast<uint2 *>(p.Q2 + row * p.ldq2 + (fh >> 1)) = make_uint2(lo, hi);
+      uint8_t *srow = p.sf2 + (int64_t)arow * p.ac2 * 512 + (pr & 31) * 16 + ((pr >> 5) & 3) * 4;
+      const int b = fh / fp4_block(FMT);
+      if (FMT == MOE_FP4_NV || h == 0) srow[(b >> 2) * 512 + (b & 3)] = (uint8_t)scale;
+      if (f0 + 32 >= F && h == 0)  // the last atom's spare blocks
+        for (int x = F / fp4_block(FMT); x < 4 * p.ac2; ++x)
+          srow[(x >> 2) * 512 + (x & 3)] = 0;
+    }
+  }
+}
+
+// Plain: warp q holds 32 output columns of the tile's tokens.
+MOE_DEVINL void epilogue_plain(const Fp4Params &p, const TileInfo &ti, float sc, uint32_t taddr,
+                               int crank, int q, int sub, int lane, uint8_t *stg,
+                               const CUtensorMap *m0) {
+  const int nc = ti.w_idx * BW + crank * (BW / 2) + q * 32;
+  if (nc >= p.N) return;
+#pragma unroll 1
+  for (int c = sub; c * 32 < ti.tokens; c += 2) {
+    float v[32];
+    tc::tmem_ld32(taddr + c * 32, v);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] *= sc;
+    const int left = ti.tokens - c * 32;  // rows of this block that are the tile's
+    const int r0 = ti.row0 + c * 32;
+    // bf16 blocks take the staging's halves in turn (from the first one on, once
+    // the last tile's stores have read them), fp32 ones all of it
+    uint8_t *buf = p.c_f32 ? stg : stg + (c >> 1 & 1) * 2048;
+    if (lane == 0) {
+      if (p.c_f32 || c == sub) tc::bulk_wait_read0();
+      else tc::bulk_wait_read<1>();
+    }
+    __syncwarp();
+    if (p.c_f32) stage_f32_t(buf, lane, v);
+    else stage_bf16_t(buf, lane, v);
+    if (left >= 32) {
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tc::tma_store_2d(m0, buf, nc, r0);
+        tc::bulk_commit();
+      }
+    } else {  // rows past the group are the next expert's
+      __syncwarp();
+      const int sh = p.c_f32 ? 3 : 2;  // log2 of a row's 16-byte chunks
+      for (int i = lane; i < (32 << sh); i += 32) {
+        const int r = i >> sh, k = i & ((1 << sh) - 1);
+        const int n = nc + (k << (p.c_f32 ? 2 : 3));
+        if (r < left && n < p.N) {
+          const int at = p.c_f32 ? r * 128 + ((k ^ (r & 7)) << 4) : r * 64 + ((k ^ ((r >> 1) & 3)) << 4);
+          uint8_t *o = static_cast<uint8_t *>(p.C) + ((r0 + r) * p.ldc + n) * (p.c_f32 ? 4 : 2);
+          st_v4(o, *reinterpret_cast<const uint4 *>(buf + at));
+        }
+      }
+      __syncwarp();
+    }
+  }
+}
+
+// ------------------------------------------- SwiGLU with many rows an expert
+// The same pipeline with the roles exchanged: a CTA's 128 tokens are its share of
+// M, the pair's 192 weight rows N, 96 to a CTA, alternating gates and ups in blocks
+// of 32.  A tile of 192 rows starts in row 0 or 64 of its scale atoms.
+constexpr int BR = 192;  // weight rows of a tile: 96 features
+
+struct RowTile {
+  int e, m_idx, n_idx, row0, row_end;
+};
+
+constexpr int kGroupPairs = 16;  // raster group: token-tile pairs that share weight rows in L2
+
+MOE_DEVINL RowTile decode_row_tile(const Book &bk, const Fp4Params &p, int t, int crank) {
+  int lo = 0, hi = p.E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (bk.cum[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  RowTile ti;
+  ti.e = tc::uniform(lo);
+  const int local = t - tc::uniform(bk.cum[ti.e]);
+  ti.row0 = tc::uniform(bk.off[ti.e]);
+  ti.row_end = max(tc::uniform(bk.off[ti.e + 1]), ti.row0);
+  const int mp = (ti.row_end - ti.row0 + 255) / 256;
+  const int group = kGroupPairs * p.w_tiles;
   const int g = local / group;
   const int within = local - g * group;
   const int gm = min(kGroupPairs, mp - g * kGroupPairs);
   ti.n_idx = within / gm;
   ti.m_idx = 2 * (g * kGroupPairs + (within - ti.n_idx * gm)) + crank;
-  ti.row0 += ti.m_idx * BM;
+  ti.row0 += ti.m_idx * 128;
   return ti;
 }
 
-// Rows of A that a CTA loads for a tile of `valid` rows, in boxes of 32 (the
-// others keep what the stage held: their products are not stored).
-MOE_DEVINL int rows_loaded(int valid) {
-  return valid > BM - 32 ? BM : valid > 0 ? (valid + 31) / 32 * 32 : 0;
-}
-
-// ---------------------------------------------------------------- epilogue
-// One thread's 32-value row segment staged as the TMA store reads it (64-byte
-// swizzle for bf16, 128-byte for fp32).
-MOE_DEVINL void stage_bf16(uint8_t *buf, int r, const float *v) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    *reinterpret_cast<uint4 *>(buf + r * 64 + ((c ^ ((r >> 1) & 3)) << 4)) =
-        f32_to_bf16x8(v + 8 * c);
-}
-
-MOE_DEVINL void stage_f32(uint8_t *buf, int r, const float *v) {
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<uint4 *>(buf + r * 128 + ((c ^ (r & 7)) << 4)) =
-        make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
-                   __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
-}
-
 // 32 values of a row -> 16 bytes of codes and the chunk's scale codes (NVFP4:
-// two bytes, MXFP4: one).  The values are continuous, so that no quotient sits
-// on a tie and a product with the reciprocal decides as the quotient would.
+// two bytes, MXFP4: one).
 template <int FMT>
 MOE_DEVINL uint4 quantize_chunk(float *v, float g, float inv6, uint32_t &scale) {
   constexpr int kB = fp4_block(FMT);
@@ -195,137 +422,66 @@ MOE_DEVINL uint4 quantize_chunk(float *v, float g, float inv6, uint32_t &scale) 
   return make_uint4(codes[0], codes[1], codes[2], codes[3]);
 }
 
-template <int FMT, int EPI>
-MOE_DEVINL void epilogue(const Book &bk, const Fp4Params &p, const TileInfo &ti, uint32_t taddr,
-                         int q, int lane, uint8_t *stg, const CUtensorMap *m0,
-                         const CUtensorMap *m1) {
-  const float sc = (p.ga != nullptr ? ld_f32(p.ga) : 1.0f) *
-                   (p.gb != nullptr ? ld_f32(p.gb + ti.e) : 1.0f);
-  const int wrow0 = ti.row0 + q * 32;
-  const int64_t row = (int64_t)wrow0 + lane;
+template <int FMT>
+MOE_DEVINL void epilogue_rows(const Book &bk, const Fp4Params &p, const RowTile &ti, float sc,
+                              float g2, float inv6, uint32_t taddr, int q, int sub, int subs,
+                              int lane) {
+  const int64_t row = (int64_t)ti.row0 + q * 32 + lane;
   const bool valid = row < ti.row_end;
-  const bool bulk = wrow0 + 32 <= ti.row_end;
-  if (wrow0 >= ti.row_end) return;  // no row of this warp is the expert's
-  if (EPI == MOE_EPI_SWIGLU_FWD) {
-    const int F = p.F;
-    const int n0 = ti.n_idx * (BN / 2);
-    const float g2 = FMT == MOE_FP4_NV && p.g2 != nullptr ? ld_f32(p.g2) : 1.0f;
-    const float inv6 = __frcp_rn(6.0f * g2);
-    // the row's place in Act's scale atoms
-    const int arow = (int)bk.poff[ti.e] + ti.m_idx;
-    uint8_t *srow = p.sf2 + (int64_t)arow * p.ac2 * 512 + lane * 16 + q * 4;
-    const bool put = valid && arow < p.atom_rows2;
+  if (ti.row0 + q * 32 >= ti.row_end) return;  // no row of this warp is the expert's
+  const int F = p.F;
+  const int f0 = ti.n_idx * (BR / 2);
+  // the row's place in Act's scale atoms
+  const int arow = (int)bk.poff[ti.e] + ti.m_idx;
+  uint8_t *srow = p.sf2 + (int64_t)arow * p.ac2 * 512 + lane * 16 + q * 4;
+  const bool put = valid && arow < p.atom_rows2;
 #pragma unroll 1
-    for (int c = 0; c < BN / 64; ++c) {
-      const int nc = n0 + c * 32;
-      if (nc >= F) break;
-      float g[32], u[32];
-      {
-        uint32_t rg[32], ru[32];
-        tc::tmem_ld32_issue(taddr + c * 32, rg);
-        tc::tmem_ld32_issue(taddr + BN / 2 + c * 32, ru);
-        tc::tmem_wait_ld(rg);
-        tc::reg_after(ru);
+  for (int c = sub; c < BR / 64; c += subs) {
+    const int nc = f0 + c * 32;
+    if (nc >= F) break;
+    float g[32], u[32];
+    {
+      uint32_t rg[32], ru[32];
+      tc::tmem_ld32_issue(taddr + c * 64, rg);
+      tc::tmem_ld32_issue(taddr + c * 64 + 32, ru);
+      tc::tmem_wait_ld(rg);
+      tc::reg_after(ru);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          g[j] = __uint_as_float(rg[j]) * sc;
-          u[j] = __uint_as_float(ru[j]) * sc;
-        }
-      }
-      if (p.C != nullptr) {  // H in bf16 as well
-        if (bulk) {
-          if (lane == 0) tc::bulk_wait_read0();
-          __syncwarp();
-          stage_bf16(stg, lane, g);
-          stage_bf16(stg + 2048, lane, u);
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tc::tma_store_2d(m0, stg, nc, wrow0);
-            tc::tma_store_2d(m1, stg + 2048, nc, wrow0);
-            tc::bulk_commit();
-          }
-        } else if (valid) {
-          uint16_t *H = static_cast<uint16_t *>(p.C) + row * p.ldc + nc;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            st_v4(H + 8 * j, f32_to_bf16x8(g + 8 * j));
-            st_v4(H + F + 8 * j, f32_to_bf16x8(u + 8 * j));
-          }
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 32; ++j) g[j] = g[j] * sigmoid_f(g[j]) * u[j];
-      uint32_t scale;
-      const uint4 codes = quantize_chunk<FMT>(g, g2, inv6, scale);
-      if (put) {
-        st_v4(p.Q2 + row * p.ldq2 + (nc >> 1), codes);
-        const int b = nc / fp4_block(FMT);
-        uint8_t *s = srow + (b >> 2) * 512 + (b & 3);
-        if (FMT == MOE_FP4_NV) *reinterpret_cast<uint16_t *>(s) = (uint16_t)scale;
-        else *s = (uint8_t)scale;
-        if (nc + 32 >= F)  // the last atom's spare blocks
-          for (int x = F / fp4_block(FMT); x < 4 * p.ac2; ++x)
-            srow[(x >> 2) * 512 + (x & 3)] = 0;
+      for (int j = 0; j < 32; ++j) {
+        g[j] = __uint_as_float(rg[j]) * sc;
+        u[j] = __uint_as_float(ru[j]) * sc;
       }
     }
-    return;
-  }
-  const int N = p.N;
-  const int n0 = ti.n_idx * BN;
-  int slot = 0;
-#pragma unroll 1
-  for (int c = 0; c < BN / 32; ++c) {
-    const int nc = n0 + c * 32;
-    if (nc >= N) break;
-    float v[32];
-    tc::tmem_ld32(taddr + c * 32, v);
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] *= sc;
-    if (bulk) {
-      // bf16 blocks take the staging's halves in turn, fp32 ones all of it
-      uint8_t *buf = p.c_f32 ? stg : stg + slot * 2048;
-      if (lane == 0) {
-        if (p.c_f32) tc::bulk_wait_read0();
-        else tc::bulk_wait_read<1>();
-      }
-      __syncwarp();
-      if (p.c_f32) stage_f32(buf, lane, v);
-      else stage_bf16(buf, lane, v);
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tc::tma_store_2d(m0, buf, nc, wrow0);
-        tc::bulk_commit();
-      }
-      slot ^= 1;
-    } else if (valid) {
+    if (p.C != nullptr && valid) {  // H in bf16 as well
+      uint16_t *H = static_cast<uint16_t *>(p.C) + row * p.ldc + nc;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int n = nc + j * 8;
-        if (n >= N) break;
-        if (p.c_f32) {
-          float *o = static_cast<float *>(p.C) + row * p.ldc + n;
-          st_v4(o, make_uint4(__float_as_uint(v[8 * j]), __float_as_uint(v[8 * j + 1]),
-                              __float_as_uint(v[8 * j + 2]), __float_as_uint(v[8 * j + 3])));
-          st_v4(o + 4, make_uint4(__float_as_uint(v[8 * j + 4]), __float_as_uint(v[8 * j + 5]),
-                                  __float_as_uint(v[8 * j + 6]), __float_as_uint(v[8 * j + 7])));
-        } else {
-          st_v4(static_cast<uint16_t *>(p.C) + row * p.ldc + n, f32_to_bf16x8(v + 8 * j));
-        }
+        st_v4(H + 8 * j, f32_to_bf16x8(g + 8 * j));
+        st_v4(H + F + 8 * j, f32_to_bf16x8(u + 8 * j));
       }
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) g[j] = g[j] * sigmoid_f(g[j]) * u[j];
+    uint32_t scale;
+    const uint4 codes = quantize_chunk<FMT>(g, g2, inv6, scale);
+    if (put) {
+      st_v4(p.Q2 + row * p.ldq2 + (nc >> 1), codes);
+      const int b = nc / fp4_block(FMT);
+      uint8_t *s = srow + (b >> 2) * 512 + (b & 3);
+      if (FMT == MOE_FP4_NV) *reinterpret_cast<uint16_t *>(s) = (uint16_t)scale;
+      else *s = (uint8_t)scale;
+      if (nc + 32 >= F)  // the last atom's spare blocks
+        for (int x = F / fp4_block(FMT); x < 4 * p.ac2; ++x)
+          srow[(x >> 2) * 512 + (x & 3)] = 0;
     }
   }
 }
 
 // ------------------------------------------------------------------ kernel
 template <int FMT, int EPI>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-gmm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-               const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
-               const __grid_constant__ CUtensorMap tmC0, const __grid_constant__ CUtensorMap tmC1,
-               const __grid_constant__ CUtensorMap tmA32, const Fp4Params p) {
-  using L = Lay<FMT>;
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<FMT, EPI>::threads, 1)
+gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
+  using L = Lay<FMT, EPI>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -336,6 +492,7 @@ gmm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const int cid = (int)tc::cluster_id_x();
   const int ncl = (int)tc::nclusters_x();
   constexpr uint16_t kPair = 0x3;
+  constexpr int kStages = L::stages;
   const bool leader = crank == 0;
 
   if (threadIdx.x == 0) {
@@ -345,19 +502,18 @@ gmm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     }
     for (int a = 0; a < 2; ++a) {
       tc::mbar_init(&bk.tfull[a], 1);
-      tc::mbar_init(&bk.tempty[a], 2 * kEpiWarps);
+      tc::mbar_init(&bk.tempty[a], 2 * L::epi_warps);
     }
     tc::mbar_init(&bk.drain, 1);
     bk.abort_flag = 0;
     tc::fence_mbar_init();
   }
   if (warp == 2 && lane == 0) {
-    tc::tma_prefetch(&tmA);
-    tc::tma_prefetch(&tmB);
-    tc::tma_prefetch(&tmSA);
-    tc::tma_prefetch(&tmSB);
-    tc::tma_prefetch(&tmC0);
-    tc::tma_prefetch(&tmA32);
+    tc::tma_prefetch(&m.w);
+    tc::tma_prefetch(&m.t[0]);
+    tc::tma_prefetch(&m.sw);
+    tc::tma_prefetch(&m.st[0]);
+    tc::tma_prefetch(&m.c);
   }
   if (warp == 1) {
     tc::tmem_alloc_2sm(&bk.tmem_base, kTmemCols);
@@ -373,8 +529,10 @@ gmm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       if (e < p.E) {
         const int lo = group_offset(p, e), hi = group_offset(p, e + 1);
         const int size = max(hi - lo, 0);
-        padded = (size + BM - 1) / BM;
-        tiles = (padded + 1) / 2 * p.n_tiles;
+        bk.off[e] = lo;
+        if (e == p.E - 1) bk.off[p.E] = hi;
+        padded = (size + 127) / 128;
+        tiles = (EPI == kRows ? (size + 255) / 256 : (size + BT - 1) / BT) * p.w_tiles;
         if (hi < lo) moe_set_status(p.dev_status, MOE_ERR_DEVICE);
       }
       int incl = tiles, pincl = padded;
@@ -412,37 +570,72 @@ gmm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int t = cid; t < total && ok; t += ncl) {
-        const TileInfo ti = decode_tile(bk, p, t, crank);
-        const int nrow = EPI == MOE_EPI_SWIGLU_FWD
-                             ? (crank == 0 ? 0 : p.F) + ti.n_idx * (BN / 2)
-                             : ti.n_idx * BN + crank * (BN / 2);
-        const int arow = (int)bk.poff[ti.e] + ti.m_idx;
-        const int brow = 2 * (ti.e * p.n_tiles + ti.n_idx);
-        const int left = ti.row_end - ti.row0;  // rows from this CTA's first on
-        const int rows = rows_loaded(left);
-        // the leader's barrier counts the pair's copies
-        const int tx = 2 * (L::tx_bytes - A_BYTES) + (rows + rows_loaded(left - BM)) * kRowBytes;
+      for (int t = cid; t < total && ok && EPI == kRows; t += ncl) {
+        const RowTile ti = decode_row_tile(bk, p, t, crank);
+        const int tok_sf = (int)bk.poff[ti.e] + ti.m_idx;
+        const int wgt_sf = ti.e * p.w_atoms + ti.n_idx * BR / 128;
+        // a CTA past the expert's rows loads none: its products are not stored
+        const bool own = ti.row0 < ti.row_end;
+        const bool both = ti.row0 + (1 - 2 * crank) * 128 < ti.row_end;  // the other CTA's
+        const int tx = (own + both) * (W_BYTES + L::sfw_bytes) + 2 * (T_BYTES + L::sft_bytes);
         for (int kb = 0; kb < p.kblocks; ++kb) {
           if (!tc::mbar_wait_warp(&bk.empty[s], ph ^ 1, abort_flag, p.wait_limit_ns)) {
             ok = false;
             break;
           }
           if (tc::elect_one()) {
-            uint8_t *sa = smem + s * L::stage_bytes;
+            uint8_t *st = smem + s * L::stage_bytes;
             const uint32_t fb = tc::mapa_shared(tc::smem_u32(&bk.full[s]), 0);
             if (leader) tc::mbar_expect_tx(&bk.full[s], tx);
-            if (rows == BM) {
-              tc::tma_load_3d_2sm(sa, &tmA, fb, kb * kRowBytes, ti.row0, 0);
-            } else {
-              for (int r = 0; r < rows; r += 32)
-                tc::tma_load_3d_2sm(sa + r * kRowBytes, &tmA32, fb, kb * kRowBytes, ti.row0 + r,
-                                    0);
+            const int k = kb * kRowBytes;
+            if (own) {
+              tc::tma_load_2d_2sm(st, &m.t[0], fb, k, ti.row0);
+              tc::tma_load_3d_2sm(st + W_BYTES + T_BYTES, &m.st[0], fb, 0, kb * L::atoms, tok_sf);
             }
-            tc::tma_load_3d_2sm(sa + A_BYTES, &tmB, fb, kb * kRowBytes, nrow, ti.e);
-            tc::tma_load_3d_2sm(sa + A_BYTES + B_BYTES, &tmSA, fb, 0, kb * L::atoms, arow);
-            tc::tma_load_3d_2sm(sa + A_BYTES + B_BYTES + L::sfa_bytes, &tmSB, fb, 0,
-                                kb * L::atoms, brow);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {  // three of the tile's six blocks of 32 rows
+              const int b = 3 * crank + i;
+              tc::tma_load_5d_2sm(st + W_BYTES + i * 4096, &m.w, fb, k, 0, b & 1,
+                                  3 * ti.n_idx + (b >> 1), ti.e);
+            }
+            tc::tma_load_3d_2sm(st + W_BYTES + T_BYTES + L::sfw_bytes, &m.sw, fb, 0,
+                                kb * L::atoms, wgt_sf);
+          }
+          __syncwarp();
+          ++issued;
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      for (int t = cid; t < total && ok && EPI != kRows; t += ncl) {
+        const TileInfo ti = decode_tile(bk, p, t);
+        // this CTA's half of the tokens, rounded up to 32 rows; their scale atoms
+        const int trow = ti.row0 + crank * (ti.n / 2);
+        const int tbox = (ti.n / 2 + 31) / 32;
+        const int sbox = second_atom(ti) ? 2 : 1;
+        const int trow_sf = (int)bk.poff[ti.e] + (ti.t0 >> 7);
+        const int wrow_sf = ti.e * p.w_atoms + 2 * ti.w_idx + crank;
+        const int tx = 2 * (W_BYTES + tbox * 4096 + (1 + sbox) * L::sfw_bytes);  // the pair's
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          if (!tc::mbar_wait_warp(&bk.empty[s], ph ^ 1, abort_flag, p.wait_limit_ns)) {
+            ok = false;
+            break;
+          }
+          if (tc::elect_one()) {
+            uint8_t *sw = smem + s * L::stage_bytes;
+            const uint32_t fb = tc::mapa_shared(tc::smem_u32(&bk.full[s]), 0);
+            if (leader) tc::mbar_expect_tx(&bk.full[s], tx);
+            const int k = kb * kRowBytes;
+            if (EPI == MOE_EPI_SWIGLU_FWD)  // 32 gate rows, 32 up rows, twice
+              tc::tma_load_5d_2sm(sw, &m.w, fb, k, 0, 0, 4 * ti.w_idx + 2 * crank, ti.e);
+            else
+              tc::tma_load_3d_2sm(sw, &m.w, fb, k, ti.w_idx * BW + crank * (BW / 2), ti.e);
+            tc::tma_load_2d_2sm(sw + W_BYTES, &m.t[tbox - 1], fb, k, trow);
+            tc::tma_load_3d_2sm(sw + W_BYTES + T_BYTES, &m.sw, fb, 0, kb * L::atoms, wrow_sf);
+            tc::tma_load_3d_2sm(sw + W_BYTES + T_BYTES + L::sfw_bytes, &m.st[sbox - 1], fb, 0,
+                                kb * L::atoms, trow_sf);
           }
           __syncwarp();
           ++issued;
@@ -472,9 +665,22 @@ gmm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     for (int t = cid; t < total && ok; t += ncl) {
       const uint32_t a = acc_it & 1;
       const uint32_t aph = (acc_it >> 1) & 1;
+      // N, where it starts in its scale atoms, and whether it reaches into a second
+      int n = BR, shift = 0;
+      bool second = true;
+      if (EPI == kRows) {
+        shift = decode_row_tile(bk, p, t, crank).n_idx & 1 ? 2 : 0;
+      } else {
+        const TileInfo ti = decode_tile(bk, p, t);
+        n = ti.n;
+        shift = scale_shift(ti);
+        second = second_atom(ti);
+      }
+      const uint32_t id0 = tc::idesc_fp4(BW, n, FMT == MOE_FP4_NV, 0);
+      const uint32_t id2 = tc::idesc_fp4(BW, n, FMT == MOE_FP4_NV, 2);
       if (!tc::mbar_wait_warp(&bk.tempty[a], aph ^ 1, abort_flag, p.wait_limit_ns)) break;
       tc::tc_fence_after();
-      const uint32_t d_tmem = tmem + a * BN;
+      const uint32_t d_tmem = tmem + a * BT;
       for (int kb = 0; kb < p.kblocks; ++kb) {
         if (!__all_sync(0xffffffffu, ready) &&
             !tc::mbar_wait_warp(&bk.full[s], ph, abort_flag, p.wait_limit_ns)) {
@@ -486,26 +692,28 @@ gmm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         ready = tc::mbar_test(&bk.full[s1], ph1);
         tc::tc_fence_after();
         if (tc::elect_one()) {
-          const uint32_t sa = tc::smem_u32(smem + s * L::stage_bytes);
-          const uint64_t ad = tc::sdesc(sa, 16, 1024);
-          const uint64_t bd = tc::sdesc(sa + A_BYTES, 16, 1024);
-          const uint32_t sfa = sa + A_BYTES + B_BYTES;
-          const uint32_t sfb = sfa + L::sfa_bytes;
-          const uint32_t sft = tmem + 2 * BN + slot * L::sf_cols;
+          const uint32_t sw = tc::smem_u32(smem + s * L::stage_bytes);
+          const uint64_t wd = tc::sdesc(sw, 16, 1024);
+          const uint64_t td = tc::sdesc(sw + W_BYTES, 16, 1024);
+          const uint32_t sfw = sw + W_BYTES + T_BYTES;
+          const uint32_t sft = sfw + L::sfw_bytes;
+          const uint32_t at = tmem + 2 * BT + slot * L::sf_cols;
 #pragma unroll
           for (int j = 0; j < L::atoms; ++j) {
-            tc::tmem_cp_32x128b_x4_2sm(sft + 12 * j, tc::sdesc_plain(sfa + 512 * j, 0, 128));
-            tc::tmem_cp_32x128b_x4_2sm(sft + 12 * j + 4, tc::sdesc_plain(sfb + 512 * j, 0, 128));
-            tc::tmem_cp_32x128b_x4_2sm(sft + 12 * j + 8,
-                                       tc::sdesc_plain(sfb + 512 * (L::atoms + j), 0, 128));
+            tc::tmem_cp_32x128b_x4_2sm(at + 12 * j, tc::sdesc_plain(sfw + 512 * j, 0, 128));
+            tc::tmem_cp_32x128b_x4_2sm(at + 12 * j + 4, tc::sdesc_plain(sft + 512 * j, 0, 128));
+            if (second)
+              tc::tmem_cp_32x128b_x4_2sm(at + 12 * j + 8,
+                                         tc::sdesc_plain(sft + 512 * (L::atoms + j), 0, 128));
           }
 #pragma unroll
           for (int kk = 0; kk < kKSteps; ++kk) {
-            const int j = kk * L::atoms / kKSteps;            // atom of this step
-            const int id = L::atoms == kKSteps ? 0 : (kk & 1) * 2;  // byte of its scale words
-            tc::umma_fp4_2sm<FMT == MOE_FP4_NV>(d_tmem, ad + 2 * kk, bd + 2 * kk,
-                                               tc::idesc_fp4(2 * BM, BN, FMT == MOE_FP4_NV, id),
-                                               sft + 12 * j, sft + 12 * j + 4, (kb | kk) != 0);
+            const int j = kk * L::atoms / kKSteps;  // atom of this step
+            // MXFP4: two steps share an atom, two bytes of its scale words each
+            tc::umma_fp4_2sm<FMT == MOE_FP4_NV>(d_tmem, wd + 2 * kk, td + 2 * kk,
+                                               L::atoms == kKSteps || !(kk & 1) ? id0 : id2,
+                                               at + 12 * j, at + 12 * j + 4 + shift,
+                                               (kb | kk) != 0);
           }
           tc::umma_commit_2sm_mc(&bk.empty[s], kPair);
           // this block's scale slot is free for the block sf_slots further
@@ -526,17 +734,35 @@ gmm_fp4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     __syncwarp();
     tc::mbar_wait_drain(&bk.drain, 0, p.wait_limit_ns);
   } else if (warp >= 2) {
-    const int q = warp & 3;
-    uint8_t *stg = smem + L::stg_offset + (warp - 2) * kStgBytes;
+    const int q = warp & 3;           // the tensor-memory lanes that it may read
+    const int sub = (warp - 2) >> 2;  // its chunks of 32 tokens: every other one
+    uint8_t *stg = smem + L::stg_offset;
+    const float ga = p.ga != nullptr ? ld_f32(p.ga) : 1.0f;
+    const float g2 = FMT == MOE_FP4_NV && p.g2 != nullptr ? ld_f32(p.g2) : 1.0f;
+    const float inv6 = __frcp_rn(6.0f * g2);
     uint32_t acc_it = 0;
     for (int t = cid; t < total; t += ncl) {
-      const TileInfo ti = decode_tile(bk, p, t, crank);
+      TileInfo ti;
+      RowTile rt;
+      if (EPI == kRows) rt = decode_row_tile(bk, p, t, crank);
+      else ti = decode_tile(bk, p, t);
+      const float sc = p.gb != nullptr ? ga * ld_f32(p.gb + (EPI == kRows ? rt.e : ti.e)) : ga;
       const uint32_t a = acc_it & 1;
       const uint32_t aph = (acc_it >> 1) & 1;
-      if (!tc::mbar_wait_warp(&bk.tfull[a], aph, abort_flag, p.wait_limit_ns)) break;
+      // the two warps of a pair give up together (one barrier between them below)
+      bool go = tc::mbar_wait_warp(&bk.tfull[a], aph, abort_flag, p.wait_limit_ns);
+      if (EPI == MOE_EPI_SWIGLU_FWD) go = pair_agree(go, 2 * sub + (q >> 1));
+      if (!go) break;
       tc::tc_fence_after();
-      epilogue<FMT, EPI>(bk, p, ti, tmem + a * BN + (static_cast<uint32_t>(q * 32) << 16), q, lane,
-                         stg, &tmC0, &tmC1);
+      const uint32_t taddr = tmem + a * BT + (static_cast<uint32_t>(q * 32) << 16);
+      if (EPI == kRows)
+        epilogue_rows<FMT>(bk, p, rt, sc, g2, inv6, taddr, q, sub, L::epi_warps / 4, lane);
+      else if (EPI == MOE_EPI_SWIGLU_FWD)
+        epilogue_swiglu<FMT>(bk, p, ti, sc, g2, inv6, taddr, crank, q, sub, lane,
+                             stg + (2 * sub + (q >> 1)) * 2 * kStgBytes);
+      else
+        epilogue_plain(p, ti, sc, taddr, crank, q, sub, lane, stg + (4 * sub + q) * kStgBytes,
+                       &m.c);
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&bk.tempty[a]), 0));
@@ -574,8 +800,8 @@ bool make_map(CUtensorMap *m, const void *base, CUtensorMapDataType type, int ra
               CUtensorMapSwizzle swizzle) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
-  cuuint64_t d[3], st[2];
-  cuuint32_t b[3], es[3] = {1, 1, 1};
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], es[5] = {1, 1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) {
     d[i] = dims[i];
     b[i] = box[i];
@@ -587,12 +813,12 @@ bool make_map(CUtensorMap *m, const void *base, CUtensorMapDataType type, int ra
 }
 
 // Rows of packed codes: boxes of 128 bytes (256 codes) x `box_rows` rows.
-bool make_code_map(CUtensorMap *m, const uint8_t *base, int64_t bytes, int64_t rows, int64_t ld,
-                   int64_t groups, int64_t group_stride, int box_rows) {
+bool make_code_map(CUtensorMap *m, const uint8_t *base, int rank, int64_t bytes, int64_t rows,
+                   int64_t ld, int64_t groups, int64_t group_stride, int box_rows) {
   const uint64_t dims[3] = {(uint64_t)bytes, (uint64_t)rows, (uint64_t)groups};
   const uint64_t st[2] = {(uint64_t)ld, (uint64_t)group_stride};
   const uint32_t box[3] = {kRowBytes, (uint32_t)box_rows, 1};
-  return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, dims, st, box,
+  return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, dims, st, box,
                   CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
@@ -617,9 +843,10 @@ bool make_out_map(CUtensorMap *m, const void *base, bool f32, int64_t cols, int6
 }
 
 template <int FMT, int EPI>
-moe_status_t launch(const CUtensorMap *m, const Fp4Params &p, int64_t tiles_upper,
+moe_status_t launch(const Maps &m, const Fp4Params &p, int64_t tiles_upper,
                     cudaStream_t s) {
-  constexpr int kSmem = smem_bytes<FMT>();
+  constexpr int kSmem = smem_bytes<FMT, EPI>();
+  constexpr int kThreads = Lay<FMT, EPI>::threads;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   static int max_clusters = 0;
@@ -644,8 +871,7 @@ moe_status_t launch(const CUtensorMap *m, const Fp4Params &p, int64_t tiles_uppe
     return MOE_ERR_CUDA;
   }
   const int grid = 2 * (int)std::max<int64_t>(1, std::min<int64_t>(max_clusters, tiles_upper));
-  const cudaError_t e = launch_dependent(gmm_fp4_kernel<FMT, EPI>, grid, kThreads, kSmem, s, m[0],
-                                         m[1], m[2], m[3], m[4], m[5], m[6], p);
+  const cudaError_t e = launch_dependent(gmm_fp4_kernel<FMT, EPI>, grid, kThreads, kSmem, s, m, p);
   if (e != cudaSuccess) {
     set_error("moe_gmm_fp4 launch: %s", cudaGetErrorString(e));
     return MOE_ERR_CUDA;
@@ -654,6 +880,13 @@ moe_status_t launch(const CUtensorMap *m, const Fp4Params &p, int64_t tiles_uppe
 }
 
 }  // namespace
+
+// SwiGLU with tokens as M (kRows): from so many rows an expert on, where K is short
+// enough for the turned epilogue to be what a tile waits for.  MXFP4, us with
+// tokens / weights as M:  8 experts of 4096 x 28672, rows an expert 512: 208 / 200,
+// 1024: 329 / 364, 2048: 603 / 650, 4096: 1106 / 1270;  32 of 7168 x 4096, 512: 194 /
+// 181, 1024: 327 / 318, 2048: 587 / 565.  NVFP4 likewise (1024: 388 / 420, 382 / 389).
+constexpr int kRowsFrom = 1024, kRowsMaxK = 5120;
 
 moe_status_t launch_gmm_fp4(const GmmFp4Args &a, cudaStream_t s) {
   const bool swiglu = a.epilogue == MOE_EPI_SWIGLU_FWD;
@@ -665,7 +898,10 @@ moe_status_t launch_gmm_fp4(const GmmFp4Args &a, cudaStream_t s) {
   p.rows_cap = (int)a.rows_cap;
   p.N = a.N;
   p.F = swiglu ? a.N / 2 : a.N;
-  p.n_tiles = swiglu ? (p.F + BN / 2 - 1) / (BN / 2) : (a.N + BN - 1) / BN;
+  const bool rows =
+      swiglu && a.rows_cap >= (int64_t)kRowsFrom * a.E && a.K <= kRowsMaxK;
+  p.w_tiles = rows ? (a.N + BR - 1) / BR : (a.N + BW - 1) / BW;
+  p.w_atoms = (a.N + 127) / 128;
   p.kblocks = (a.K + 255) / 256;
   p.offsets = a.offsets;
   p.C = a.C;
@@ -682,31 +918,42 @@ moe_status_t launch_gmm_fp4(const GmmFp4Args &a, cudaStream_t s) {
   p.dev_status = a.dev_status;
   p.wait_limit_ns = wait_limit_ns();
   p.stall_loads = test_stall_loads();
-  CUtensorMap m[7];
+  Maps m;
   const int64_t ac = (a.K + acols - 1) / acols;
   const int64_t stride_b = a.E > 1 ? a.stride_b : (int64_t)a.N * a.ldb;
-  bool ok = make_code_map(&m[0], a.A, a.K / 2, a.rows_cap, a.lda, 1, a.rows_cap * a.lda, BM) &&
-            make_code_map(&m[1], a.B, a.K / 2, a.N, a.ldb, a.E, stride_b, BN / 2) &&
-            make_scale_map(&m[2], a.sfa, ac, p.atom_rows2, atoms, 1) &&
-            make_scale_map(&m[3], a.sfb, ac, 2 * (int64_t)a.E * p.n_tiles, atoms, 2);
-  ok = ok && make_code_map(&m[6], a.A, a.K / 2, a.rows_cap, a.lda, 1, a.rows_cap * a.lda, 32);
-  if (swiglu && a.C != nullptr) {
-    const uint16_t *H = static_cast<const uint16_t *>(a.C);
-    ok = ok && make_out_map(&m[4], H, false, p.F, a.rows_cap, a.ldc) &&
-         make_out_map(&m[5], H + p.F, false, p.F, a.rows_cap, a.ldc);
-  } else if (!swiglu) {
-    ok = ok && make_out_map(&m[4], a.C, p.c_f32, a.N, a.rows_cap, a.ldc);
-    m[5] = m[4];
+  bool ok = make_scale_map(&m.sw, a.sfb, ac, (int64_t)a.E * p.w_atoms, atoms, 1) &&
+            make_scale_map(&m.st[0], a.sfa, ac, p.atom_rows2, atoms, 1) &&
+            make_scale_map(&m.st[1], a.sfa, ac, p.atom_rows2, atoms, 2);
+  for (int i = 0; i < 3; ++i)
+    ok = ok && make_code_map(&m.t[i], a.A, 2, a.K / 2, a.rows_cap, a.lda, 1, 0, 32 * (i + 1));
+  if (rows) {  // tokens in boxes of 128, weights of 32 rows, their atoms two rows
+    ok = ok && make_code_map(&m.t[0], a.A, 2, a.K / 2, a.rows_cap, a.lda, 1, 0, 128) &&
+         make_scale_map(&m.sw, a.sfb, ac, (int64_t)a.E * p.w_atoms, atoms, 2);
+  }
+  if (swiglu) {
+    // [E][F / 32][gate, up][32] rows: a box takes two blocks of 32 gates and 32 ups
+    const uint64_t dims[5] = {(uint64_t)a.K / 2, 32, 2, (uint64_t)p.F / 32, (uint64_t)a.E};
+    const uint64_t st[4] = {(uint64_t)a.ldb, (uint64_t)p.F * a.ldb, 32 * (uint64_t)a.ldb,
+                            (uint64_t)stride_b};
+    const uint32_t nb = rows ? 1 : 2;
+    const uint32_t box[5] = {kRowBytes, 32, nb, nb, 1};
+    ok = ok && make_map(&m.w, a.B, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, dims, st, box,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
+    m.c = m.w;
   } else {
-    m[4] = m[5] = m[0];
+    ok = ok && make_code_map(&m.w, a.B, 3, a.K / 2, a.N, a.ldb, a.E, stride_b, BW / 2) &&
+         make_out_map(&m.c, a.C, p.c_f32, a.N, a.rows_cap, a.ldc);
   }
   if (!ok) {
     set_error("moe_gmm_fp4: cannot encode a TMA descriptor");
     return MOE_ERR_CUDA;
   }
-  // pairs of row tiles: at most one partly filled pair an expert that has rows
+  // token tiles: at most one partly filled an expert that has rows
   const int64_t live = std::min<int64_t>(a.E, a.rows_cap);
-  const int64_t tiles_upper = ((a.rows_cap + 2 * BM - 1) / (2 * BM) + live) * p.n_tiles;
+  const int64_t tiles_upper = ((a.rows_cap + BT - 1) / BT + live) * p.w_tiles;
+  if (rows)
+    return nv ? launch<MOE_FP4_NV, kRows>(m, p, tiles_upper, s)
+              : launch<MOE_FP4_MX, kRows>(m, p, tiles_upper, s);
   if (swiglu)
     return nv ? launch<MOE_FP4_NV, MOE_EPI_SWIGLU_FWD>(m, p, tiles_upper, s)
               : launch<MOE_FP4_MX, MOE_EPI_SWIGLU_FWD>(m, p, tiles_upper, s);

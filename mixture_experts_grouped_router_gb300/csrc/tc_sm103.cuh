@@ -243,6 +243,15 @@ MOE_DEVINL void tma_load_3d_2sm(void *dst, const CUtensorMap *map, uint32_t bar,
       : "memory");
 }
 
+MOE_DEVINL void tma_load_5d_2sm(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1,
+                                int c2, int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+
 // Generic-proxy writes to shared memory made visible to the async proxy
 // (tensor-core operand reads).
 MOE_DEVINL void fence_proxy_async_smem() {

@@ -36,7 +36,7 @@ class Fp4Rows:
 
     def __init__(self, rows: int, cols: int, E: int, fmt: str, device="cuda"):
         self.rows, self.cols, self.E, self.fmt = rows, cols, E, _fmt(fmt)
-        nb = L.moe_fp4_scale_bytes(rows, cols, self.fmt, L.MX_ROWS_GROUPED, E)
+        nb = L.moe_fp4_scale_bytes(rows, cols, self.fmt, L.FP4_ROWS_GROUPED, E)
         self.q = torch.empty(rows, cols // 2, dtype=torch.uint8, device=device)
         self.sf = torch.empty(nb, dtype=torch.uint8, device=device)
 
@@ -46,7 +46,7 @@ def fp4_quantize(x, rows: Fp4Rows, group_offsets, row_index=None, index_div=1, s
     """Rows of x bf16 into `rows`; with row_index int32 [rows] row p is
     x[row_index[p] / index_div] (the permute's sorted_to_flat with index_div = k),
     zeros where it is negative.  scale: fp32 [1] (nv)."""
-    L.moe_fp4_quantize(x, rows.fmt, rows.q, rows.sf, L.MX_ROWS_GROUPED, group_offsets,
+    L.moe_fp4_quantize(x, rows.fmt, rows.q, rows.sf, L.FP4_ROWS_GROUPED, group_offsets,
                        row_index=row_index, index_div=index_div, scale=scale,
                        dev_status=dev_status, stream=stream)
 
@@ -54,7 +54,7 @@ def fp4_quantize(x, rows: Fp4Rows, group_offsets, row_index=None, index_div=1, s
 def fp4_dequantize(rows: Fp4Rows, group_offsets, out, scale=None, stream=None):
     """The values of `rows` into out bf16 [rows, cols] (rows past group_offsets[-1] are not
     written)."""
-    L.moe_fp4_dequantize(rows.q, rows.sf, rows.fmt, out, L.MX_ROWS_GROUPED, group_offsets,
+    L.moe_fp4_dequantize(rows.q, rows.sf, rows.fmt, out, L.FP4_ROWS_GROUPED, group_offsets,
                          scale=scale, stream=stream)
 
 
@@ -94,8 +94,8 @@ class Fp4Experts:
             L.moe_fp4_arrange_scales(s, 2 * kb, f, row_map, E, sf, stream)
             return sf
 
-        return cls(f, wi_q, atoms(wi_q, wi_s, L.MX_ROWS_SWIGLU), wi_scale,
-                   wo_q, atoms(wo_q, wo_s, L.MX_ROWS_TILES), wo_scale, x_scale, act_scale)
+        return cls(f, wi_q, atoms(wi_q, wi_s, L.FP4_ROWS_SWIGLU), wi_scale,
+                   wo_q, atoms(wo_q, wo_s, L.FP4_ROWS_EXPERTS), wo_scale, x_scale, act_scale)
 
     @classmethod
     def from_weights(cls, fmt, wi, wo, x_scale=None, act_scale=None, stream=None):
@@ -117,7 +117,7 @@ class Fp4Experts:
             L.moe_fp4_quantize_weights(w, f, row_map, q, sf, scale, stream)
             return q, sf, scale
 
-        return cls(f, *quantise(wi, L.MX_ROWS_SWIGLU), *quantise(wo, L.MX_ROWS_TILES), x_scale,
+        return cls(f, *quantise(wi, L.FP4_ROWS_SWIGLU), *quantise(wo, L.FP4_ROWS_EXPERTS), x_scale,
                    act_scale)
 
 

@@ -89,13 +89,12 @@ def unpack(q):
 
 
 def padded_row(r, G, row_map):
-    """Padded row (TILES, SWIGLU) of row r of E groups of G rows."""
+    """Padded row ("experts", "swiglu") of row r of E groups of G rows."""
     e, n = divmod(r, G)
     if row_map == "swiglu":
-        F = G // 2
-        m = n % F
-        return (e * -(-F // 96) + m // 96) * 256 + (0 if n < F else 96) + m % 96
-    return (e * -(-G // 192) + n // 192) * 256 + n % 192
+        up, m = divmod(n, G // 2)
+        n = m // 32 * 64 + 32 * up + m % 32
+    return e * (-(-G // 128) * 128) + n
 
 
 def scale_byte(pr, blk, ac):

@@ -140,11 +140,11 @@ def test_bad_offset_tables_touch_nothing_outside(L, fmt, offs):
 
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
-@pytest.mark.parametrize("row_map", ["tiles", "swiglu"])
+@pytest.mark.parametrize("row_map", ["experts", "swiglu"])
 @pytest.mark.parametrize("E,K,N", [(1, 32, 64), (2, 96, 192), (3, 160, 448)])
 def test_weights_and_arranged_scales(L, fmt, row_map, E, K, N):
     rng = np.random.default_rng(K + N)
-    m = 3 if row_map == "tiles" else 2
+    m = 3 if row_map == "experts" else 2
     w = f64(bf16(rng.standard_normal((E, K, N)) * 0.02))
     g = np.exp2(-6.0 - np.arange(E)).astype(np.float32)
     gt = torch.from_numpy(g).cuda()
@@ -232,7 +232,8 @@ def test_gmm_plain(L, fmt, f32, sizes, K, N):
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
 @pytest.mark.parametrize("save_h", [False, True])
 @pytest.mark.parametrize("sizes,K,F", [([5], 32, 32), ([1, 0, 2], 64, 96), ([130, 1, 300], 512, 416),
-                                       ([40], 4096, 288)])
+                                       ([40], 4096, 288), ([515], 160, 96),
+                                       ([700, 0, 3, 1345], 544, 416)])
 def test_gmm_swiglu_quantises_act(L, fmt, save_h, sizes, K, F):
     c = gemm_case(L, fmt, sizes, K, 2 * F, swiglu=True)
     n, cap, E = c["n"], c["cap"], len(sizes)

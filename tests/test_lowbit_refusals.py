@@ -21,12 +21,12 @@ BIG = 1 << 30
 
 def test_scale_bytes(L):
     f = L.moe_fp4_scale_bytes
-    assert f(100, 256, L.FP4_MX, L.MX_ROWS_GROUPED, 4) == (100 + 4 * 127 + 127) // 128 * 2 * 512
-    assert f(100, 256, L.FP4_NV, L.MX_ROWS_GROUPED, 4) == (100 + 4 * 127 + 127) // 128 * 4 * 512
-    assert f(3 * 200, 96, L.FP4_NV, L.MX_ROWS_TILES, 3) == 3 * 2 * 2 * 2 * 512
-    assert f(2 * 448, 96, L.FP4_MX, L.MX_ROWS_SWIGLU, 2) == 2 * 2 * 3 * 1 * 512
+    assert f(100, 256, L.FP4_MX, L.FP4_ROWS_GROUPED, 4) == (100 + 4 * 127 + 127) // 128 * 2 * 512
+    assert f(100, 256, L.FP4_NV, L.FP4_ROWS_GROUPED, 4) == (100 + 4 * 127 + 127) // 128 * 4 * 512
+    assert f(3 * 200, 96, L.FP4_NV, L.FP4_ROWS_EXPERTS, 3) == 3 * 2 * 2 * 512
+    assert f(2 * 448, 96, L.FP4_MX, L.FP4_ROWS_SWIGLU, 2) == 2 * 4 * 1 * 512
     assert f(-1, 96, 0, 1, 2) == 0 and f(8, 96, 7, 1, 2) == 0 and f(8, 96, 0, 0, 2) == 0
-    assert f(0, 96, 0, L.MX_ROWS_TILES, 2) == 0
+    assert f(0, 96, 0, L.FP4_ROWS_EXPERTS, 2) == 0
 
 
 def quantize(L, x=P(), ldx=64, src=10, idx=None, div=1, rows=10, cols=64, fmt=0, m=1, off=P(), E=2,

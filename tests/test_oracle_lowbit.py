@@ -43,7 +43,7 @@ def test_e4m3_codes_round_trip():
 
 
 def test_padded_rows_are_distinct():
-    for G, E, m in ((200, 3, "tiles"), (192, 2, "swiglu"), (2 * 224, 2, "swiglu")):
+    for G, E, m in ((200, 3, "experts"), (192, 2, "swiglu"), (2 * 224, 2, "swiglu")):
         rows = [R.padded_row(r, G, m) for r in range(E * G)]
         assert len(set(rows)) == E * G
     assert R.scale_byte(128 + 33, 5, 2) == (1 * 2 + 1) * 512 + 16 + 4 + 1
