@@ -585,13 +585,19 @@ size_t moe_fp4_scale_bytes(int64_t rows, int cols, int fmt, int row_map, int E);
  *   GROUPED    group_offsets int32 [E + 1] device; rows at or past
  *              group_offsets[E], and the scales of padding rows, are not written
  *   EXPERTS, SWIGLU  K-major weights, rows = E equal groups; scale fp32 [E]
- *   ldx % 8 == 0, ldq % 16 == 0; x, q, sf 16-byte aligned; E <= 256 (GROUPED)
+ *   workspace  device scratch or NULL: with moe_fp4_quantize_workspace_bytes(
+ *              src_rows, rows) bytes a gather that takes rows of x twice or more
+ *              on average quantises each of them once
+ *   ldx % 8 == 0, ldq % 16 == 0; x, q, sf, workspace 16-byte aligned; E <= 256
+ *   (GROUPED)
  */
+size_t moe_fp4_quantize_workspace_bytes(int64_t src_rows, int64_t rows);
 moe_status_t moe_fp4_quantize(const uint16_t *x, int64_t ldx, int64_t src_rows,
                               const int32_t *row_index, int index_div, int64_t rows, int cols,
                               int fmt, int row_map, const int32_t *group_offsets, int E,
                               const float *scale, uint8_t *q, int64_t ldq, uint8_t *sf,
-                              size_t sf_bytes, int32_t *dev_status, moe_stream_t stream);
+                              size_t sf_bytes, void *workspace, size_t workspace_bytes,
+                              int32_t *dev_status, moe_stream_t stream);
 
 /*
  * moe_fp4_dequantize -- the values of moe_fp4_quantize's codes, rounded once to
@@ -668,6 +674,8 @@ typedef struct moe_fp4_buffers {
   uint8_t *act_q, *act_sf;
   size_t act_sf_bytes;
   uint16_t *h, *y;
+  void *workspace;        /* of moe_fp4_quantize, or NULL */
+  size_t workspace_bytes;
   int32_t *dev_status;
 } moe_fp4_buffers;
 

@@ -99,8 +99,9 @@ _SIGS = {
     "moe_tgmm_mx": (_I, [_P, _I64, _P, _I, _P, _I64, _P, _I, _P, _I, _I64, _I, _I, _P, _I, _I64,
                          _I64, _I, _P, _P]),
     "moe_fp4_scale_bytes": (_SZ, [_I64, _I, _I, _I, _I]),
+    "moe_fp4_quantize_workspace_bytes": (_SZ, [_I64, _I64]),
     "moe_fp4_quantize": (_I, [_P, _I64, _I64, _P, _I, _I64, _I, _I, _I, _P, _I, _P, _P, _I64, _P,
-                              _SZ, _P, _P]),
+                              _SZ, _P, _SZ, _P, _P]),
     "moe_fp4_dequantize": (_I, [_P, _I64, _P, _SZ, _I64, _I, _I, _I, _P, _I, _P, _P, _I64, _P]),
     "moe_fp4_quantize_weights": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P]),
     "moe_fp4_arrange_scales": (_I, [_P, _I64, _I, _I, _I, _I, _P, _SZ, _P]),
@@ -477,7 +478,8 @@ def _groups(group_offsets, groups):
 
 
 def moe_fp4_quantize(x, fmt, q, sf, row_map=FP4_ROWS_GROUPED, group_offsets=None, groups=1,
-                     row_index=None, index_div=1, scale=None, dev_status=None, stream=None):
+                     row_index=None, index_div=1, scale=None, workspace=None, dev_status=None,
+                     stream=None):
     """Rows of x bf16 [src_rows, cols] (gathered through row_index / index_div) -> q uint8
     [rows, cols / 2], sf uint8 scale atoms; GROUPED takes group_offsets, EXPERTS / SWIGLU the
     number of equal row groups."""
@@ -485,7 +487,13 @@ def moe_fp4_quantize(x, fmt, q, sf, row_map=FP4_ROWS_GROUPED, group_offsets=None
     _check(LIB.moe_fp4_quantize(_ptr(x), _ld(x), x.shape[0], _ptr(row_index), index_div, rows,
                                 cols, fmt, row_map, _ptr(group_offsets),
                                 _groups(group_offsets, groups), _ptr(scale), _ptr(q), _ld(q),
-                                _ptr(sf), sf.numel(), _ptr(dev_status), _stream(stream)))
+                                _ptr(sf), sf.numel(), _ptr(workspace),
+                                0 if workspace is None else workspace.numel(),
+                                _ptr(dev_status), _stream(stream)))
+
+
+def moe_fp4_quantize_workspace_bytes(src_rows: int, rows: int) -> int:
+    return int(LIB.moe_fp4_quantize_workspace_bytes(src_rows, rows))
 
 
 def moe_fp4_dequantize(q, sf, fmt, x, row_map=FP4_ROWS_GROUPED, group_offsets=None, groups=1,
@@ -539,7 +547,8 @@ class Fp4WeightsArg(ctypes.Structure):
 class Fp4BuffersArg(ctypes.Structure):
     """moe_fp4_buffers."""
     _fields_ = [("rows_cap", _I64), ("x_q", _P), ("x_sf", _P), ("x_sf_bytes", _SZ), ("act_q", _P),
-                ("act_sf", _P), ("act_sf_bytes", _SZ), ("h", _P), ("y", _P), ("dev_status", _P)]
+                ("act_sf", _P), ("act_sf_bytes", _SZ), ("h", _P), ("y", _P), ("workspace", _P),
+                ("workspace_bytes", _SZ), ("dev_status", _P)]
 
 
 def moe_fp4_experts(w, b, x, sorted_to_flat, k, group_offsets, stream=None):

@@ -61,11 +61,17 @@ size_t moe_fp4_scale_bytes(int64_t rows, int cols, int fmt, int row_map, int E) 
   return (size_t)moe::fp4_atom_rows(rows, row_map, E) * (size_t)((cols + ac - 1) / ac) * 512u;
 }
 
+size_t moe_fp4_quantize_workspace_bytes(int64_t src_rows, int64_t rows) {
+  if (src_rows < 0 || rows < 0) return 0;
+  return moe::fp4_quantize_workspace_bytes(src_rows, rows);
+}
+
 moe_status_t moe_fp4_quantize(const uint16_t *x, int64_t ldx, int64_t src_rows,
                               const int32_t *row_index, int index_div, int64_t rows, int cols,
                               int fmt, int row_map, const int32_t *group_offsets, int E,
                               const float *scale, uint8_t *q, int64_t ldq, uint8_t *sf,
-                              size_t sf_bytes, int32_t *dev_status, moe_stream_t stream) {
+                              size_t sf_bytes, void *workspace, size_t workspace_bytes,
+                              int32_t *dev_status, moe_stream_t stream) {
   set_error("");
   const moe_status_t st =
       check_rows("moe_fp4_quantize", rows, cols, fmt, row_map, group_offsets, E);
@@ -79,15 +85,15 @@ moe_status_t moe_fp4_quantize(const uint16_t *x, int64_t ldx, int64_t src_rows,
           (long long)src_rows, index_div);
   if (rows == 0) return MOE_OK;
   REQUIRE((x || src_rows == 0) && q && sf, MOE_ERR_INVALID_ARG, "moe_fp4_quantize: null pointer");
-  REQUIRE(aligned(x, 16) && aligned(q, 16) && aligned(sf, 16), MOE_ERR_UNSUPPORTED,
-          "moe_fp4_quantize: x, q and sf must be 16-byte aligned");
+  REQUIRE(aligned(x, 16) && aligned(q, 16) && aligned(sf, 16) && aligned(workspace, 16),
+          MOE_ERR_UNSUPPORTED, "moe_fp4_quantize: x, q, sf and workspace must be 16-byte aligned");
   REQUIRE(sf_bytes >= moe_fp4_scale_bytes(rows, cols, fmt, row_map, E), MOE_ERR_INVALID_ARG,
           "moe_fp4_quantize: sf of %zu bytes < %zu", sf_bytes,
           moe_fp4_scale_bytes(rows, cols, fmt, row_map, E));
   return cuda_status(
       moe::launch_fp4_quantize(x, ldx, src_rows, row_index, index_div, rows, cols, fmt, row_map,
-                               group_offsets, E, scale, q, ldq, sf, dev_status,
-                               (cudaStream_t)stream),
+                               group_offsets, E, scale, q, ldq, sf, workspace, workspace_bytes,
+                               dev_status, (cudaStream_t)stream),
       "moe_fp4_quantize launch");
 }
 
@@ -232,7 +238,7 @@ moe_status_t moe_fp4_experts(const moe_fp4_weights *w, const moe_fp4_buffers *b,
   REQUIRE(aligned(w->wi_q, 16) && aligned(w->wi_sf, 16) && aligned(w->wo_q, 16) &&
               aligned(w->wo_sf, 16) && aligned(b->x_q, 16) && aligned(b->x_sf, 16) &&
               aligned(b->act_q, 16) && aligned(b->act_sf, 16) && aligned(b->y, 16) &&
-              aligned(b->h, 16) && aligned(x, 16) && ldx % 8 == 0,
+              aligned(b->h, 16) && aligned(b->workspace, 16) && aligned(x, 16) && ldx % 8 == 0,
           MOE_ERR_UNSUPPORTED, "moe_fp4_experts: operands must be 16-byte aligned");
   REQUIRE(ldx >= w->d, MOE_ERR_INVALID_ARG, "moe_fp4_experts: ldx=%lld < d", (long long)ldx);
   REQUIRE(b->x_sf_bytes >=
@@ -244,7 +250,8 @@ moe_status_t moe_fp4_experts(const moe_fp4_weights *w, const moe_fp4_buffers *b,
   moe_status_t st = cuda_status(
       moe::launch_fp4_quantize(x, ldx, T, sorted_to_flat, k, b->rows_cap, w->d, w->fmt,
                                MOE_FP4_ROWS_GROUPED, group_offsets, w->E, w->x_scale, b->x_q,
-                               w->d / 2, b->x_sf, b->dev_status, s),
+                               w->d / 2, b->x_sf, b->workspace, b->workspace_bytes, b->dev_status,
+                               s),
       "moe_fp4_experts: quantise");
   if (st != MOE_OK) return st;
   const int64_t d2 = w->d / 2, f2 = w->f / 2;

@@ -34,6 +34,12 @@ MOE_DEVINL int ld_i32(const int32_t *p) {
   return v;
 }
 
+MOE_DEVINL int2 ld_i32x2(const int2 *p) {
+  int2 v;
+  asm volatile("ld.global.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+  return v;
+}
+
 MOE_DEVINL uint32_t ld_u32(const void *p) {
   uint32_t v;
   asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");

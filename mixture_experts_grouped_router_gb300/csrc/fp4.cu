@@ -127,10 +127,60 @@ MOE_DEVINL uint32_t scale_word(uint32_t c, int lane) {
   return v;
 }
 
-// One warp: one row, up to 4 chunks of 256 columns (a lane 8 of them, 16 bytes
-// in, 4 bytes of codes out), so that a row's loads are all in flight together
-// and every access is coalesced; the next row's loads are issued before this
-// one is quantised, the first row's before the groups are scanned.
+// A warp's 4 chunks of 256 columns of a row (a lane 8 values of each, 16 bytes in,
+// 4 bytes of codes out): the codes, and the words of the scale atoms (4 blocks
+// each; the lanes that share a word all hold it).
+template <int FMT>
+MOE_DEVINL void quantize_piece(const uint4 *w, int c0, int cols, int lane, float g, float inv6,
+                               uint32_t *codes, uint32_t *words) {
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    const int c = c0 + 256 * i;
+    codes[i] = words[i] = 0;
+    if (c - lane * 8 >= cols) break;  // the whole chunk
+    uint32_t a = amax_bits8(w[i]);
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    if (FMT != MOE_FP4_NV) a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+    float t, inv, v[8];
+    const uint32_t code =
+        fp4_block_scale<FMT>(__uint_as_float(a << 16), g, 6.0f * g, inv6, t, inv);
+    bf16x8_to_f32(w[i], v);
+    codes[i] = fp4_codes8<FMT>(v, t, inv);
+    words[i] = scale_word<FMT>(c < cols ? code : 0u, lane);
+  }
+}
+
+// Stores a piece as row r, padded row pr.
+template <int FMT>
+MOE_DEVINL void store_piece(const uint32_t *codes, const uint32_t *words, int c0, int cols,
+                            int lane, int64_t r, int64_t pr, int ac, uint8_t *q, int64_t ldq,
+                            uint8_t *sf) {
+  constexpr int kLanes = FMT == MOE_FP4_NV ? 8 : 16;  // lanes of a word
+  uint8_t *qr = q + r * ldq + (c0 >> 1);
+  // atoms of 4 blocks follow one another 512 bytes apart
+  uint8_t *sr = sf + fp4_scale_byte(pr, c0 / fp4_block(FMT), ac);
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    if (c0 + 256 * i < cols) {
+      *reinterpret_cast<uint32_t *>(qr + 128 * i) = codes[i];
+      if (lane % kLanes == 0)
+        *reinterpret_cast<uint32_t *>(sr + i * (256 / fp4_atom_cols(FMT)) * 512) = words[i];
+    }
+  }
+}
+
+// A warp's piece of source row src (zeros where there is none).
+MOE_DEVINL void load_piece(const uint16_t *x, int64_t ldx, int64_t src, int c0, int cols,
+                           uint4 *w) {
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (src >= 0 && c0 + 256 * i < cols) w[i] = ld_stream_v4(x + src * ldx + c0 + 256 * i);
+  }
+}
+
+// One warp, one piece of a row; the next row's loads are issued before this one
+// is quantised, the first row's before the groups are scanned.
 template <int FMT, bool GROUPED>
 __global__ void __launch_bounds__(kThreads)
 fp4_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t src_rows,
@@ -144,10 +194,9 @@ fp4_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t src_row
   const int G = rows / max(E, 1);
   grid_dependency_begin();
   Walk w((cols + 256 * kUnroll - 1) / (256 * kUnroll));
-  // this warp's piece of row w.row as it stands; a row that x does not have
-  // (src_rows of them) reads as zeros
-  auto load = [&](uint4 *v, int64_t &src) {
-    src = -1;
+  // the source row of row w.row (-1: zeros; one that x does not have likewise)
+  auto source = [&](bool &bad) {
+    int64_t src = -1;
     if (w.row < rows) {
       src = w.row;
       if (row_index != nullptr) {
@@ -155,17 +204,12 @@ fp4_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t src_row
         src = i < 0 ? -1 : i / index_div;
       }
     }
-    const int c0 = w.seg * (256 * kUnroll) + lane * 8;
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (src >= 0 && src < src_rows && c0 + 256 * i < cols)
-        v[i] = ld_stream_v4(x + src * ldx + c0 + 256 * i);
-    }
+    bad = src >= src_rows;
+    return bad ? (int64_t)-1 : src;
   };
   uint4 cur[kUnroll];
-  int64_t src;
-  load(cur, src);
+  bool bad;
+  load_piece(x, ldx, source(bad), w.seg * (256 * kUnroll) + lane * 8, cols, cur);
   int R = rows;
   if (GROUPED) {
     scan_groups(gr, offsets, E, rows);
@@ -177,40 +221,97 @@ fp4_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t src_row
   int e = 0;
   while (w.row < R) {
     const int r = w.row, c0 = w.seg * (256 * kUnroll) + lane * 8;
-    if (src >= src_rows && lane == 0) moe_set_status(dev_status, MOE_ERR_DEVICE);
+    if (bad && lane == 0) moe_set_status(dev_status, MOE_ERR_DEVICE);
     uint4 next[kUnroll];
     w.step();
-    load(next, src);
+    load_piece(x, ldx, source(bad), w.seg * (256 * kUnroll) + lane * 8, cols, next);
     const float g = FMT == MOE_FP4_NV && !GROUPED && gscale != nullptr ? ld_f32(gscale + r / G) : g1;
     const float inv6 = GROUPED ? inv6_1 : __frcp_rn(6.0f * g);
     const int64_t pr = GROUPED ? grouped_row(gr, e, r) : weight_row(r, G, row_map);
     if (pr >= 0) {
-      uint8_t *qr = q + r * ldq + (c0 >> 1);
-      // atoms of 4 blocks follow one another 512 bytes apart
-      uint8_t *sr = sf + fp4_scale_byte(pr, c0 / fp4_block(FMT), ac);
-#pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
-        const int c = c0 + 256 * i;
-        if (c - lane * 8 >= cols) break;  // the whole chunk
-        uint32_t a = amax_bits8(cur[i]);
-        a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-        if (FMT != MOE_FP4_NV) a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-        float t, inv, v[8];
-        const uint32_t code =
-            fp4_block_scale<FMT>(__uint_as_float(a << 16), g, 6.0f * g, inv6, t, inv);
-        bf16x8_to_f32(cur[i], v);
-        const uint32_t codes = fp4_codes8<FMT>(v, t, inv);
-        const uint32_t word = scale_word<FMT>(c < cols ? code : 0u, lane);
-        constexpr int kLanes = FMT == MOE_FP4_NV ? 8 : 16;  // lanes of a word
-        if (c < cols) {
-          *reinterpret_cast<uint32_t *>(qr + 128 * i) = codes;
-          if (lane % kLanes == 0)
-            *reinterpret_cast<uint32_t *>(sr + i * (256 / fp4_atom_cols(FMT)) * 512) = word;
-        }
-      }
+      uint32_t codes[kUnroll], words[kUnroll];
+      quantize_piece<FMT>(cur, c0, cols, lane, g, inv6, codes, words);
+      store_piece<FMT>(codes, words, c0, cols, lane, r, pr, ac, q, ldq, sf);
     }
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) cur[i] = next[i];
+  }
+}
+
+// Top-k routing gathers every token k times.  With many rows each token is
+// quantised once and stored k times instead: fp4_link_kernel threads the rows of
+// a source row into a list (next[p] = the row before p and p's padded row), and
+// fp4_quantize_linked_kernel walks the source rows.  Rows of zeros are spread over
+// kZeroLists lists of their own.  The lists' order varies from run to run; what is
+// stored does not.
+constexpr int kZeroLists = 512;
+
+__global__ void __launch_bounds__(kThreads)
+fp4_link_kernel(const int32_t *__restrict__ row_index, int index_div, int64_t src_rows, int rows,
+                const int32_t *__restrict__ offsets, int E, int32_t *__restrict__ head,
+                int2 *__restrict__ next, int32_t *dev_status) {
+  __shared__ Groups gr;
+  grid_dependency_begin();
+  scan_groups(gr, offsets, E, rows);
+  __syncthreads();
+  const int R = gr.off[E];
+  int e = 0;
+  for (int p = blockIdx.x * kThreads + threadIdx.x; p < R; p += gridDim.x * kThreads) {
+    const int pr = grouped_row(gr, e, p);
+    if (pr < 0) continue;
+    const int i = ld_i32(row_index + p);
+    int64_t src = i < 0 ? -1 : i / index_div;
+    if (src >= src_rows) {
+      moe_set_status(dev_status, MOE_ERR_DEVICE);
+      src = -1;
+    }
+    if (src < 0) src = src_rows + p % kZeroLists;
+    next[p] = make_int2(atomicExch(head + src, p), pr);
+  }
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads)
+fp4_quantize_linked_kernel(const uint16_t *__restrict__ x, int64_t ldx, int src_rows, int cols,
+                           const float *__restrict__ gscale, const int32_t *__restrict__ head,
+                           const int2 *__restrict__ next, uint8_t *__restrict__ q, int64_t ldq,
+                           uint8_t *__restrict__ sf) {
+  const int lane = threadIdx.x & 31;
+  const int ac = (cols + fp4_atom_cols(FMT) - 1) / fp4_atom_cols(FMT);
+  grid_dependency_begin();
+  const int lists = src_rows + kZeroLists;
+  Walk w((cols + 256 * kUnroll - 1) / (256 * kUnroll));
+  auto load = [&](uint4 *v, int &p) {
+    p = -1;
+    if (w.row < lists) p = ld_i32(head + w.row);
+    load_piece(x, ldx, p >= 0 && w.row < src_rows ? w.row : -1,
+               w.seg * (256 * kUnroll) + lane * 8, cols, v);
+  };
+  const float g = FMT == MOE_FP4_NV && gscale != nullptr ? ld_f32(gscale) : 1.0f;
+  const float inv6 = __frcp_rn(6.0f * g);
+  uint4 cur[kUnroll];
+  int p;
+  load(cur, p);
+  while (w.row < lists) {
+    const int c0 = w.seg * (256 * kUnroll) + lane * 8;
+    int at = p;
+    int2 nx = make_int2(-1, 0);
+    if (at >= 0) nx = ld_i32x2(next + at);
+    uint4 ahead[kUnroll];
+    w.step();
+    load(ahead, p);
+    if (at >= 0) {
+      uint32_t codes[kUnroll], words[kUnroll];
+      quantize_piece<FMT>(cur, c0, cols, lane, g, inv6, codes, words);
+      while (at >= 0) {
+        const int r = at, pr = nx.y;
+        at = nx.x;
+        if (at >= 0) nx = ld_i32x2(next + at);
+        store_piece<FMT>(codes, words, c0, cols, lane, r, pr, ac, q, ldq, sf);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) cur[i] = ahead[i];
   }
 }
 
@@ -348,13 +449,41 @@ int64_t fp4_atom_rows(int64_t rows, int row_map, int E) {
   return (int64_t)E * ((rows / E + 127) / 128);
 }
 
+// Linked quantisation pays from so many gathered values on, for its two more
+// launches (about 7 us): 32768 rows of 4096 from 16384 tokens 78 us directly, 47
+// linked; 6216 rows of 7168 from 777 tokens 27 and 16 us; under 2^24 values the
+// direct kernel takes some 10 us.
+constexpr int64_t kLinkFrom = 1 << 24;
+
+size_t fp4_quantize_workspace_bytes(int64_t src_rows, int64_t rows) {
+  return (size_t)rows * sizeof(int2) + (size_t)(src_rows + kZeroLists) * sizeof(int32_t);
+}
+
 cudaError_t launch_fp4_quantize(const uint16_t *x, int64_t ldx, int64_t src_rows,
                                 const int32_t *row_index, int index_div, int64_t rows, int cols,
                                 int fmt, int row_map, const int32_t *offsets, int E,
                                 const float *gscale, uint8_t *q, int64_t ldq, uint8_t *sf,
-                                int32_t *dev_status, cudaStream_t st) {
-  const int grid = grid_for(rows, cols);
+                                void *ws, size_t ws_bytes, int32_t *dev_status, cudaStream_t st) {
   const bool grouped = row_map == MOE_FP4_ROWS_GROUPED;
+  if (grouped && row_index != nullptr && rows >= 2 * src_rows && rows * cols >= kLinkFrom &&
+      ws != nullptr && ws_bytes >= fp4_quantize_workspace_bytes(src_rows, rows)) {
+    int2 *next = static_cast<int2 *>(ws);
+    int32_t *head = reinterpret_cast<int32_t *>(next + rows);
+    cudaError_t e = cudaMemsetAsync(head, 0xFF, (size_t)(src_rows + kZeroLists) * 4, st);
+    if (e != cudaSuccess) return e;
+    const int lg = (int)std::min<int64_t>((rows + kThreads - 1) / kThreads, (int64_t)num_sms() * 4);
+    e = launch_dependent(fp4_link_kernel, lg, kThreads, 0, st, row_index, index_div, src_rows,
+                         (int)rows, offsets, E, head, next, dev_status);
+    if (e != cudaSuccess) return e;
+    const int grid = grid_for(src_rows + kZeroLists, cols);
+    auto run = [&](auto kernel) {
+      return launch_dependent(kernel, grid, kThreads, 0, st, x, ldx, (int)src_rows, cols, gscale,
+                              (const int32_t *)head, (const int2 *)next, q, ldq, sf);
+    };
+    return fmt == MOE_FP4_NV ? run(fp4_quantize_linked_kernel<MOE_FP4_NV>)
+                             : run(fp4_quantize_linked_kernel<MOE_FP4_MX>);
+  }
+  const int grid = grid_for(rows, cols);
   auto run = [&](auto kernel) {
     return launch_dependent(kernel, grid, kThreads, 0, st, x, ldx, src_rows, row_index, index_div,
                             (int)rows, cols, row_map, offsets, E, gscale, q, ldq, sf, dev_status);

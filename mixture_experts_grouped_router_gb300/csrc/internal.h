@@ -190,7 +190,8 @@ cudaError_t launch_fp4_quantize(const uint16_t *x, int64_t ldx, int64_t src_rows
                                 const int32_t *row_index, int index_div, int64_t rows, int cols,
                                 int fmt, int row_map, const int32_t *offsets, int E,
                                 const float *gscale, uint8_t *q, int64_t ldq, uint8_t *sf,
-                                int32_t *dev_status, cudaStream_t s);
+                                void *ws, size_t ws_bytes, int32_t *dev_status, cudaStream_t s);
+size_t fp4_quantize_workspace_bytes(int64_t src_rows, int64_t rows);
 cudaError_t launch_fp4_dequantize(const uint8_t *q, int64_t ldq, const uint8_t *sf, int64_t rows,
                                   int cols, int fmt, int row_map, const int32_t *offsets, int E,
                                   const float *gscale, uint16_t *x, int64_t ldx, cudaStream_t s);

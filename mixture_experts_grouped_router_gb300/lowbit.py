@@ -39,6 +39,9 @@ class Fp4Rows:
         nb = L.moe_fp4_scale_bytes(rows, cols, self.fmt, L.FP4_ROWS_GROUPED, E)
         self.q = torch.empty(rows, cols // 2, dtype=torch.uint8, device=device)
         self.sf = torch.empty(nb, dtype=torch.uint8, device=device)
+        # scratch of a gather from up to rows / 2 source rows (others do without)
+        self.workspace = torch.empty(L.moe_fp4_quantize_workspace_bytes(rows // 2, rows),
+                                     dtype=torch.uint8, device=device)
 
 
 def fp4_quantize(x, rows: Fp4Rows, group_offsets, row_index=None, index_div=1, scale=None,
@@ -48,7 +51,7 @@ def fp4_quantize(x, rows: Fp4Rows, group_offsets, row_index=None, index_div=1, s
     zeros where it is negative.  scale: fp32 [1] (nv)."""
     L.moe_fp4_quantize(x, rows.fmt, rows.q, rows.sf, L.FP4_ROWS_GROUPED, group_offsets,
                        row_index=row_index, index_div=index_div, scale=scale,
-                       dev_status=dev_status, stream=stream)
+                       workspace=rows.workspace, dev_status=dev_status, stream=stream)
 
 
 def fp4_dequantize(rows: Fp4Rows, group_offsets, out, scale=None, stream=None):
@@ -138,7 +141,7 @@ class Fp4Buffers:
             rows_cap, self.x.q.data_ptr(), self.x.sf.data_ptr(), self.x.sf.numel(),
             self.act.q.data_ptr(), self.act.sf.data_ptr(), self.act.sf.numel(),
             None if self.h is None else self.h.data_ptr(), self.y.data_ptr(),
-            self.dev_status.data_ptr())
+            self.x.workspace.data_ptr(), self.x.workspace.numel(), self.dev_status.data_ptr())
 
 
 def fp4_experts(w: Fp4Experts, b: Fp4Buffers, x, sorted_to_flat, k, group_offsets, stream=None):

@@ -106,6 +106,36 @@ def test_quantize_grouped_is_bit_exact(L, fmt, sizes, cols):
 
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("sizes,src,cols", [([0, 4000, 1, 900], 1500, 4096),
+                                            ([20000, 130], 5000, 928)])
+def test_gather_of_repeated_rows_quantises_them_once(L, fmt, sizes, src, cols):
+    """The same codes and scales with the workspace of a repeating gather as without:
+    repeats, rows of zeros (a long run of them), unused and missing source rows."""
+    rng = np.random.default_rng(src)
+    off = offsets_of(sizes)
+    cap, E = int(off[-1]) + 7, len(sizes)
+    x = bf16(rng.standard_normal((src, cols)))
+    idx = rng.integers(0, 4 * (src - 9), cap)
+    idx[rng.random(cap) < 0.1] = -1
+    idx[100:400] = -1
+    idx[3] = 4 * src  # not there
+    g = torch.tensor([0.015625], device="cuda")
+    res = []
+    for ws in (None, torch.empty(L.moe_fp4_quantize_workspace_bytes(src, cap), dtype=torch.uint8,
+                                 device="cuda")):
+        q = torch.full((cap, cols // 2), 0xAB, dtype=torch.uint8, device="cuda")
+        sf = torch.full((L.moe_fp4_scale_bytes(cap, cols, FMT[fmt], 1, E),), 0xCD,
+                        dtype=torch.uint8, device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        for _ in range(2):
+            L.moe_fp4_quantize(x, FMT[fmt], q, sf, group_offsets=i32(off), row_index=i32(idx),
+                               index_div=4, scale=g, workspace=ws, dev_status=st)
+        assert int(st.item()) == L.MOE_ERR_DEVICE
+        res.append((q, sf))
+    assert (res[0][0] == res[1][0]).all() and (res[0][1] == res[1][1]).all()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
 def test_nan_blocks_and_bad_rows(L, fmt):
     x = np.ones((4, 64))
     x[0, 3], x[1, 40], x[2, 0], x[3] = np.nan, np.inf, -np.inf, 0.0

@@ -30,9 +30,9 @@ def test_scale_bytes(L):
 
 
 def quantize(L, x=P(), ldx=64, src=10, idx=None, div=1, rows=10, cols=64, fmt=0, m=1, off=P(), E=2,
-             q=P(), ldq=32, sf=P(), nb=BIG):
+             q=P(), ldq=32, sf=P(), nb=BIG, ws=None, wsb=0):
     return L.LIB.moe_fp4_quantize(x, ldx, src, idx, div, rows, cols, fmt, m, off, E, None, q, ldq,
-                                  sf, nb, None, None)
+                                  sf, nb, ws, wsb, None, None)
 
 
 def test_fp4_quantize(L):
@@ -50,6 +50,7 @@ def test_fp4_quantize(L):
     assert quantize(L, src=9) == bad
     assert quantize(L, idx=P(), div=0) == bad and "index_div" in L.last_error()
     assert quantize(L, q=None) == bad and quantize(L, x=P(4100)) == uns
+    assert quantize(L, ws=P(4100), wsb=BIG) == uns
     assert quantize(L, nb=512) == bad and "sf of 512" in L.last_error()
     assert quantize(L, rows=0, x=None, q=None, sf=None, off=None) == L.MOE_OK
 
