@@ -210,7 +210,7 @@ moe_status_t moe_gmm_fp4(const uint8_t *A, int64_t lda, const uint8_t *sfa, cons
           moe_fp4_scale_bytes(rows_cap, N / 2, fmt, MOE_FP4_ROWS_GROUPED, E));
   moe::GmmFp4Args a{A, lda, sfa, a_scale, B, ldb, stride_b, sfb, b_scale, fmt, group_offsets, E,
                     rows_cap, K, N, epilogue, C, c_dtype, ldc, Q2, ldq2, sf2, q2_scale,
-                    dev_status};
+                    dev_status, 0};
   return moe::launch_gmm_fp4(a, (cudaStream_t)stream);
 }
 
@@ -258,13 +258,13 @@ moe_status_t moe_fp4_experts(const moe_fp4_weights *w, const moe_fp4_buffers *b,
   moe::GmmFp4Args up{b->x_q, d2, b->x_sf, w->x_scale, w->wi_q, d2, 2ll * w->f * d2, w->wi_sf,
                      w->wi_scale, w->fmt, group_offsets, w->E, b->rows_cap, w->d, 2 * w->f,
                      MOE_EPI_SWIGLU_FWD, b->h, MOE_DTYPE_BF16, 2ll * w->f, b->act_q, f2, b->act_sf,
-                     w->act_scale, b->dev_status};
+                     w->act_scale, b->dev_status, 1};
   st = moe::launch_gmm_fp4(up, s);
   if (st != MOE_OK) return st;
   moe::GmmFp4Args down{b->act_q, f2, b->act_sf, w->act_scale, w->wo_q, f2, (int64_t)w->d * f2,
                        w->wo_sf, w->wo_scale, w->fmt, group_offsets, w->E, b->rows_cap, w->f, w->d,
                        MOE_EPI_NONE, b->y, MOE_DTYPE_BF16, w->d, nullptr, 0, nullptr, nullptr,
-                       b->dev_status};
+                       b->dev_status, 1};
   return moe::launch_gmm_fp4(down, s);
 }
 

@@ -125,6 +125,7 @@ struct Fp4Params {
   int32_t *dev_status;
   uint64_t wait_limit_ns;
   int stall_loads;
+  int early;          // offsets and weights may be read before the kernel before is done
 };
 
 struct Maps {
@@ -519,7 +520,10 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
     tc::tmem_alloc_2sm(&bk.tmem_base, kTmemCols);
     tc::tmem_relinquish_2sm();
   }
-  grid_dependency_begin();  // the work above overlaps the end of the kernel before
+  // The work above overlaps the end of the kernel before; with `early` so do the
+  // tile counts and the first weights' copies (each role then waits for itself).
+  const bool early = EPI != kRows && p.early;
+  if (!early) grid_dependency_begin();
   if (warp == 0) {
     // per-expert tile counts and padded sizes, and their exclusive scans
     int carry = 0, pcarry = 0;
@@ -564,6 +568,7 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
   const uint32_t tmem = (uint32_t)tc::uniform((int)bk.tmem_base);
   const int total = tc::uniform(bk.total_tiles);
 
+  if (early && warp != 0) grid_dependency_begin();
   if (warp == 0) {
     if (!p.stall_loads) {
       uint32_t issued = 0;
@@ -609,6 +614,7 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
           }
         }
       }
+      int done = 0;  // K blocks of the first tile that are issued
       for (int t = cid; t < total && ok && EPI != kRows; t += ncl) {
         const TileInfo ti = decode_tile(bk, p, t);
         // this CTA's half of the tokens, rounded up to 32 rows; their scale atoms
@@ -618,24 +624,46 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
         const int trow_sf = (int)bk.poff[ti.e] + (ti.t0 >> 7);
         const int wrow_sf = ti.e * p.w_atoms + 2 * ti.w_idx + crank;
         const int tx = 2 * (W_BYTES + tbox * 4096 + (1 + sbox) * L::sfw_bytes);  // the pair's
-        for (int kb = 0; kb < p.kblocks; ++kb) {
+        auto load_weights = [&](int st, int kb) {
+          uint8_t *sw = smem + st * L::stage_bytes;
+          const uint32_t fb = tc::mapa_shared(tc::smem_u32(&bk.full[st]), 0);
+          if (leader) tc::mbar_expect_tx(&bk.full[st], tx);
+          const int k = kb * kRowBytes;
+          if (EPI == MOE_EPI_SWIGLU_FWD)  // 32 gate rows, 32 up rows, twice
+            tc::tma_load_5d_2sm(sw, &m.w, fb, k, 0, 0, 4 * ti.w_idx + 2 * crank, ti.e);
+          else
+            tc::tma_load_3d_2sm(sw, &m.w, fb, k, ti.w_idx * BW + crank * (BW / 2), ti.e);
+          tc::tma_load_3d_2sm(sw + W_BYTES + T_BYTES, &m.sw, fb, 0, kb * L::atoms, wrow_sf);
+        };
+        auto load_tokens = [&](int st, int kb) {
+          uint8_t *sw = smem + st * L::stage_bytes;
+          const uint32_t fb = tc::mapa_shared(tc::smem_u32(&bk.full[st]), 0);
+          tc::tma_load_2d_2sm(sw + W_BYTES, &m.t[tbox - 1], fb, kb * kRowBytes, trow);
+          tc::tma_load_3d_2sm(sw + W_BYTES + T_BYTES + L::sfw_bytes, &m.st[sbox - 1], fb, 0,
+                              kb * L::atoms, trow_sf);
+        };
+        if (early && t == cid) {
+          // the stages are free: their weights first, the tokens once they are there
+          done = min(p.kblocks, kStages);
+          if (tc::elect_one())
+            for (int kb = 0; kb < done; ++kb) load_weights(kb, kb);
+          __syncwarp();
+          grid_dependency_begin();
+          if (tc::elect_one())
+            for (int kb = 0; kb < done; ++kb) load_tokens(kb, kb);
+          __syncwarp();
+          issued = done;
+          s = done == kStages ? 0 : done;
+          ph = done == kStages ? 1 : 0;
+        }
+        for (int kb = t == cid ? done : 0; kb < p.kblocks; ++kb) {
           if (!tc::mbar_wait_warp(&bk.empty[s], ph ^ 1, abort_flag, p.wait_limit_ns)) {
             ok = false;
             break;
           }
           if (tc::elect_one()) {
-            uint8_t *sw = smem + s * L::stage_bytes;
-            const uint32_t fb = tc::mapa_shared(tc::smem_u32(&bk.full[s]), 0);
-            if (leader) tc::mbar_expect_tx(&bk.full[s], tx);
-            const int k = kb * kRowBytes;
-            if (EPI == MOE_EPI_SWIGLU_FWD)  // 32 gate rows, 32 up rows, twice
-              tc::tma_load_5d_2sm(sw, &m.w, fb, k, 0, 0, 4 * ti.w_idx + 2 * crank, ti.e);
-            else
-              tc::tma_load_3d_2sm(sw, &m.w, fb, k, ti.w_idx * BW + crank * (BW / 2), ti.e);
-            tc::tma_load_2d_2sm(sw + W_BYTES, &m.t[tbox - 1], fb, k, trow);
-            tc::tma_load_3d_2sm(sw + W_BYTES + T_BYTES, &m.sw, fb, 0, kb * L::atoms, wrow_sf);
-            tc::tma_load_3d_2sm(sw + W_BYTES + T_BYTES + L::sfw_bytes, &m.st[sbox - 1], fb, 0,
-                                kb * L::atoms, trow_sf);
+            load_weights(s, kb);
+            load_tokens(s, kb);
           }
           __syncwarp();
           ++issued;
@@ -918,6 +946,7 @@ moe_status_t launch_gmm_fp4(const GmmFp4Args &a, cudaStream_t s) {
   p.dev_status = a.dev_status;
   p.wait_limit_ns = wait_limit_ns();
   p.stall_loads = test_stall_loads();
+  p.early = a.early;
   Maps m;
   const int64_t ac = (a.K + acols - 1) / acols;
   const int64_t stride_b = a.E > 1 ? a.stride_b : (int64_t)a.N * a.ldb;

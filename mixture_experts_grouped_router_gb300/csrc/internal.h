@@ -211,6 +211,9 @@ struct GmmFp4Args {
   void *C; int c_dtype; int64_t ldc;
   uint8_t *Q2; int64_t ldq2; uint8_t *sf2; const float *g2;  // SwiGLU: codes of Act
   int32_t *dev_status;
+  // the kernel before in the stream is one of this library's that waited for its
+  // own predecessors and writes neither the offsets nor the weights
+  int early;
 };
 moe_status_t launch_gmm_fp4(const GmmFp4Args &a, cudaStream_t s);
 
