@@ -80,15 +80,14 @@ MOE_DEVINL void act8_values8(const uint2 &q, uint32_t sbits, float *v) {
 // The warps' walk over (row, chunk of 256 columns): chunk c of warp w is c0 + w,
 // then steps of all warps; a step is taken by additions alone.
 struct Walk {
-  int64_t row, d_row;
-  int ch, d_ch, n_ch;
+  int row, d_row, ch, d_ch, n_ch;
   MOE_DEVINL Walk(int chunks) : n_ch(chunks) {
-    const int64_t warp = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
-    const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+    const int warp = (int)((blockIdx.x * kThreads + threadIdx.x) >> 5);
+    const int warps = (int)gridDim.x * (kThreads / 32);
     row = warp / chunks;
-    ch = (int)(warp - row * chunks);
+    ch = warp - row * chunks;
     d_row = warps / chunks;
-    d_ch = (int)(warps - d_row * chunks);
+    d_ch = warps - d_row * chunks;
   }
   MOE_DEVINL void step() {
     row += d_row;
@@ -100,29 +99,29 @@ struct Walk {
   }
 };
 
-MOE_DEVINL int64_t live_rows(const int32_t *offsets, int E, int64_t rows) {
+MOE_DEVINL int live_rows(const int32_t *offsets, int E, int rows) {
   if (offsets == nullptr) return rows;
-  return min(max((int64_t)ld_i32(offsets + E), (int64_t)0), rows);
+  return min(max(ld_i32(offsets + E), 0), rows);
 }
 
 __global__ void __launch_bounds__(kThreads)
-act8_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t rows, int cols,
+act8_quantize_kernel(const uint16_t *__restrict__ x, int ldx, int rows, int cols,
                      const int32_t *__restrict__ offsets, int E, int8_t *__restrict__ q,
-                     int64_t ldq, uint16_t *__restrict__ s, int64_t lds) {
+                     int ldq, uint16_t *__restrict__ s, int lds) {
   const int lane = threadIdx.x & 31;
   grid_dependency_begin();
-  const int64_t R = live_rows(offsets, E, rows);
+  const int R = live_rows(offsets, E, rows);
   Walk w((cols + 255) / 256);
   while (w.row < R) {
     uint4 v[kUnroll];
-    int64_t at[kUnroll];
+    int at[kUnroll];
     int col[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       at[i] = w.row;
       col[i] = w.ch * 256 + lane * 8;
       v[i] = make_uint4(0, 0, 0, 0);
-      if (w.row < R && col[i] < cols) v[i] = ld_stream_v4(x + w.row * ldx + col[i]);
+      if (w.row < R && col[i] < cols) v[i] = ld_stream_v4(x + (int64_t)w.row * ldx + col[i]);
       w.step();
     }
 #pragma unroll
@@ -130,33 +129,33 @@ act8_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t rows, 
       uint32_t sb;
       const uint2 c = act8_quantize8(v[i], sb);
       if (at[i] < R && col[i] < cols) {
-        *reinterpret_cast<uint2 *>(q + at[i] * ldq + col[i]) = c;
-        if ((lane & 3) == 0) s[at[i] * lds + (col[i] >> 5)] = (uint16_t)sb;
+        *reinterpret_cast<uint2 *>(q + (int64_t)at[i] * ldq + col[i]) = c;
+        if ((lane & 3) == 0) s[(int64_t)at[i] * lds + (col[i] >> 5)] = (uint16_t)sb;
       }
     }
   }
 }
 
 __global__ void __launch_bounds__(kThreads)
-act8_dequantize_kernel(const int8_t *__restrict__ q, int64_t ldq, const uint16_t *__restrict__ s,
-                       int64_t lds, int64_t rows, int cols, const int32_t *__restrict__ offsets,
-                       int E, uint16_t *__restrict__ x, int64_t ldx) {
+act8_dequantize_kernel(const int8_t *__restrict__ q, int ldq, const uint16_t *__restrict__ s,
+                       int lds, int rows, int cols, const int32_t *__restrict__ offsets,
+                       int E, uint16_t *__restrict__ x, int ldx) {
   const int lane = threadIdx.x & 31;
   grid_dependency_begin();
-  const int64_t R = live_rows(offsets, E, rows);
+  const int R = live_rows(offsets, E, rows);
   Walk w((cols + 255) / 256);
   while (w.row < R) {
     uint2 c[kUnroll];
     uint32_t sb[kUnroll];
-    int64_t at[kUnroll];
+    int at[kUnroll];
     int col[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       at[i] = w.row;
       col[i] = w.ch * 256 + lane * 8;
       if (w.row < R && col[i] < cols) {
-        c[i] = ld_stream_v2(q + w.row * ldq + col[i]);
-        sb[i] = ld_u16(s + w.row * lds + (col[i] >> 5));
+        c[i] = ld_stream_v2(q + (int64_t)w.row * ldq + col[i]);
+        sb[i] = ld_u16(s + (int64_t)w.row * lds + (col[i] >> 5));
       }
       w.step();
     }
@@ -165,7 +164,7 @@ act8_dequantize_kernel(const int8_t *__restrict__ q, int64_t ldq, const uint16_t
       if (at[i] < R && col[i] < cols) {
         float v[8];
         act8_values8(c[i], sb[i], v);
-        st_v4(x + at[i] * ldx + col[i], f32_to_bf16x8(v));
+        st_v4(x + (int64_t)at[i] * ldx + col[i], f32_to_bf16x8(v));
       }
     }
   }
@@ -174,19 +173,19 @@ act8_dequantize_kernel(const int8_t *__restrict__ q, int64_t ldq, const uint16_t
 // h [rows, 2F] -> act [rows, F], codes [rows, 2F], scales [rows, 2 nb] (nb =
 // ceil(F / 32); the up half's blocks start at nb, so that no block straddles).
 __global__ void __launch_bounds__(kThreads)
-act8_swiglu_fwd_kernel(const uint16_t *__restrict__ h, int64_t ldh, int64_t rows, int F,
+act8_swiglu_fwd_kernel(const uint16_t *__restrict__ h, int ldh, int rows, int F,
                        const int32_t *__restrict__ offsets, int E, uint16_t *__restrict__ act,
-                       int64_t lda, int8_t *__restrict__ q, int64_t ldq,
-                       uint16_t *__restrict__ s, int64_t lds) {
+                       int lda, int8_t *__restrict__ q, int ldq,
+                       uint16_t *__restrict__ s, int lds) {
   constexpr int kU = kUnroll / 2;  // two loads a chunk
   const int lane = threadIdx.x & 31;
   const int nb = (F + 31) / 32;
   grid_dependency_begin();
-  const int64_t R = live_rows(offsets, E, rows);
+  const int R = live_rows(offsets, E, rows);
   Walk w((F + 255) / 256);
   while (w.row < R) {
     uint4 g[kU], u[kU];
-    int64_t at[kU];
+    int at[kU];
     int col[kU];
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
@@ -194,8 +193,8 @@ act8_swiglu_fwd_kernel(const uint16_t *__restrict__ h, int64_t ldh, int64_t rows
       col[i] = w.ch * 256 + lane * 8;
       g[i] = u[i] = make_uint4(0, 0, 0, 0);
       if (w.row < R && col[i] < F) {
-        g[i] = ld_stream_v4(h + w.row * ldh + col[i]);
-        u[i] = ld_stream_v4(h + w.row * ldh + F + col[i]);
+        g[i] = ld_stream_v4(h + (int64_t)w.row * ldh + col[i]);
+        u[i] = ld_stream_v4(h + (int64_t)w.row * ldh + F + col[i]);
       }
       w.step();
     }
@@ -210,12 +209,12 @@ act8_swiglu_fwd_kernel(const uint16_t *__restrict__ h, int64_t ldh, int64_t rows
 #pragma unroll
       for (int j = 0; j < 8; ++j) fg[j] = fg[j] * sigmoid_f(fg[j]) * fu[j];
       if (at[i] < R && col[i] < F) {
-        st_v4(act + at[i] * lda + col[i], f32_to_bf16x8(fg));
-        int8_t *qr = q + at[i] * ldq + col[i];
+        st_v4(act + (int64_t)at[i] * lda + col[i], f32_to_bf16x8(fg));
+        int8_t *qr = q + (int64_t)at[i] * ldq + col[i];
         *reinterpret_cast<uint2 *>(qr) = cg;
         *reinterpret_cast<uint2 *>(qr + F) = cu;
         if ((lane & 3) == 0) {
-          uint16_t *sr = s + at[i] * lds + (col[i] >> 5);
+          uint16_t *sr = s + (int64_t)at[i] * lds + (col[i] >> 5);
           sr[0] = (uint16_t)sg;
           sr[nb] = (uint16_t)su;
         }
@@ -225,33 +224,33 @@ act8_swiglu_fwd_kernel(const uint16_t *__restrict__ h, int64_t ldh, int64_t rows
 }
 
 __global__ void __launch_bounds__(kThreads)
-act8_swiglu_bwd_kernel(const int8_t *__restrict__ q, int64_t ldq, const uint16_t *__restrict__ s,
-                       int64_t lds, const uint16_t *__restrict__ dact, int64_t ldda,
-                       int64_t rows, int F, const int32_t *__restrict__ offsets, int E,
-                       uint16_t *__restrict__ dh, int64_t lddh, uint16_t *__restrict__ act,
-                       int64_t lda) {
+act8_swiglu_bwd_kernel(const int8_t *__restrict__ q, int ldq, const uint16_t *__restrict__ s,
+                       int lds, const uint16_t *__restrict__ dact, int ldda,
+                       int rows, int F, const int32_t *__restrict__ offsets, int E,
+                       uint16_t *__restrict__ dh, int lddh, uint16_t *__restrict__ act,
+                       int lda) {
   constexpr int kU = kUnroll / 2;
   const int lane = threadIdx.x & 31;
   const int nb = (F + 31) / 32;
   grid_dependency_begin();
-  const int64_t R = live_rows(offsets, E, rows);
+  const int R = live_rows(offsets, E, rows);
   Walk w((F + 255) / 256);
   while (w.row < R) {
     uint2 cg[kU], cu[kU];
     uint4 da[kU];
     uint32_t sg[kU], su[kU];
-    int64_t at[kU];
+    int at[kU];
     int col[kU];
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
       at[i] = w.row;
       col[i] = w.ch * 256 + lane * 8;
       if (w.row < R && col[i] < F) {
-        const int8_t *qr = q + w.row * ldq + col[i];
-        const uint16_t *sr = s + w.row * lds + (col[i] >> 5);
+        const int8_t *qr = q + (int64_t)w.row * ldq + col[i];
+        const uint16_t *sr = s + (int64_t)w.row * lds + (col[i] >> 5);
         cg[i] = ld_stream_v2(qr);
         cu[i] = ld_stream_v2(qr + F);
-        da[i] = ld_stream_v4(dact + w.row * ldda + col[i]);
+        da[i] = ld_stream_v4(dact + (int64_t)w.row * ldda + col[i]);
         sg[i] = ld_u16(sr);
         su[i] = ld_u16(sr + nb);
       }
@@ -274,20 +273,24 @@ act8_swiglu_bwd_kernel(const int8_t *__restrict__ q, int64_t ldq, const uint16_t
           u[j] = d[j] * silu;
           g[j] = dg;
         }
-        uint16_t *o = dh + at[i] * lddh + col[i];
+        uint16_t *o = dh + (int64_t)at[i] * lddh + col[i];
         st_v4(o, f32_to_bf16x8(g));
         st_v4(o + F, f32_to_bf16x8(u));
-        if (act != nullptr) st_v4(act + at[i] * lda + col[i], f32_to_bf16x8(a));
+        if (act != nullptr) st_v4(act + (int64_t)at[i] * lda + col[i], f32_to_bf16x8(a));
       }
     }
   }
 }
 
-// Blocks for rows x chunks warps' worth of work: all resident at once.
-int grid_for(int64_t rows, int cols) {
+// Launches a kernel's walk over rows x chunks of 256 columns: as many blocks as
+// there is work for, no more than the GPU holds at a time.
+template <auto Kernel, typename... Args>
+cudaError_t run(int64_t rows, int cols, cudaStream_t st, Args... args) {
   const int64_t warps = rows * ((cols + 255) / 256);
   const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(blocks, (int64_t)num_sms() * 8));
+  const int64_t most = (int64_t)num_sms() * blocks_per_sm<Kernel>(kThreads);
+  return launch_dependent(Kernel, (unsigned)std::max<int64_t>(1, std::min(blocks, most)), kThreads,
+                          0, st, args...);
 }
 
 }  // namespace
@@ -295,31 +298,31 @@ int grid_for(int64_t rows, int cols) {
 cudaError_t launch_act8_quantize(const uint16_t *x, int64_t ldx, int64_t rows, int cols,
                                  const int32_t *offsets, int E, int8_t *q, int64_t ldq,
                                  uint16_t *s, int64_t lds, cudaStream_t st) {
-  return launch_dependent(act8_quantize_kernel, grid_for(rows, cols), kThreads, 0, st,
-                          x, ldx, rows, cols, offsets, E, q, ldq, s, lds);
+  return run<act8_quantize_kernel>(rows, cols, st, x, (int)ldx, (int)rows, cols, offsets, E, q,
+      (int)ldq, s, (int)lds);
 }
 
 cudaError_t launch_act8_dequantize(const int8_t *q, int64_t ldq, const uint16_t *s, int64_t lds,
                                    int64_t rows, int cols, const int32_t *offsets, int E,
                                    uint16_t *x, int64_t ldx, cudaStream_t st) {
-  return launch_dependent(act8_dequantize_kernel, grid_for(rows, cols), kThreads, 0, st,
-                          q, ldq, s, lds, rows, cols, offsets, E, x, ldx);
+  return run<act8_dequantize_kernel>(rows, cols, st, q, (int)ldq, s, (int)lds, (int)rows, cols,
+      offsets, E, x, (int)ldx);
 }
 
 cudaError_t launch_act8_swiglu_fwd(const uint16_t *h, int64_t ldh, int64_t rows, int F,
                                    const int32_t *offsets, int E, uint16_t *act, int64_t lda,
                                    int8_t *q, int64_t ldq, uint16_t *s, int64_t lds,
                                    cudaStream_t st) {
-  return launch_dependent(act8_swiglu_fwd_kernel, grid_for(rows, F), kThreads, 0, st,
-                          h, ldh, rows, F, offsets, E, act, lda, q, ldq, s, lds);
+  return run<act8_swiglu_fwd_kernel>(rows, F, st, h, (int)ldh, (int)rows, F, offsets, E, act,
+      (int)lda, q, (int)ldq, s, (int)lds);
 }
 
 cudaError_t launch_act8_swiglu_bwd(const int8_t *q, int64_t ldq, const uint16_t *s, int64_t lds,
                                    const uint16_t *dact, int64_t ldda, int64_t rows, int F,
                                    const int32_t *offsets, int E, uint16_t *dh, int64_t lddh,
                                    uint16_t *act, int64_t lda, cudaStream_t st) {
-  return launch_dependent(act8_swiglu_bwd_kernel, grid_for(rows, F), kThreads, 0, st,
-                          q, ldq, s, lds, dact, ldda, rows, F, offsets, E, dh, lddh, act, lda);
+  return run<act8_swiglu_bwd_kernel>(rows, F, st, q, (int)ldq, s, (int)lds, dact, (int)ldda,
+      (int)rows, F, offsets, E, dh, (int)lddh, act, (int)lda);
 }
 
 }  // namespace moe

@@ -25,6 +25,12 @@ static moe_status_t cuda_status(cudaError_t e, const char *what) {
   return MOE_ERR_CUDA;
 }
 
+// Rows and leading dimensions that the kernels index in 32 bits (offsets are 64).
+static bool fits(int64_t rows, int64_t a, int64_t b = 0, int64_t c = 0, int64_t d = 0) {
+  const int64_t most = (1ll << 31) - (1 << 20);
+  return rows < most && a < most && b < most && c < most && d < most;
+}
+
 static bool good_fmt(int fmt) { return fmt == MOE_FP4_MX || fmt == MOE_FP4_NV; }
 
 static bool good_map(int m) {
@@ -39,7 +45,7 @@ static moe_status_t check_rows(const char *who, int64_t rows, int cols, int fmt,
   REQUIRE(good_fmt(fmt), MOE_ERR_INVALID_ARG, "%s: bad fmt %d", who, fmt);
   REQUIRE(good_map(row_map), MOE_ERR_INVALID_ARG, "%s: bad row_map %d", who, row_map);
   REQUIRE(cols % 32 == 0, MOE_ERR_UNSUPPORTED, "%s: cols=%d is no multiple of 32", who, cols);
-  REQUIRE(rows < (1ll << 31) - (1 << 20), MOE_ERR_UNSUPPORTED, "%s: too many rows (2^31)", who);
+  REQUIRE(fits(rows + 128ll * E, 0), MOE_ERR_UNSUPPORTED, "%s: too many rows (2^31)", who);
   if (row_map == MOE_FP4_ROWS_GROUPED) {
     REQUIRE(E <= 256, MOE_ERR_UNSUPPORTED, "%s: E=%d > 256", who, E);
     REQUIRE(offsets != nullptr || rows == 0, MOE_ERR_INVALID_ARG,
@@ -80,6 +86,8 @@ moe_status_t moe_fp4_quantize(const uint16_t *x, int64_t ldx, int64_t src_rows,
           "moe_fp4_quantize: leading dimension too small");
   REQUIRE(ldx % 8 == 0 && ldq % 16 == 0, MOE_ERR_UNSUPPORTED,
           "moe_fp4_quantize: ldx must be a multiple of 8, ldq of 16");
+  REQUIRE(fits(src_rows, ldx, ldq), MOE_ERR_UNSUPPORTED,
+          "moe_fp4_quantize: src_rows, ldx or ldq of 2^31 and more");
   REQUIRE(src_rows >= 0 && (row_index == nullptr ? src_rows >= rows : index_div > 0),
           MOE_ERR_INVALID_ARG, "moe_fp4_quantize: src_rows=%lld index_div=%d",
           (long long)src_rows, index_div);
@@ -109,6 +117,7 @@ moe_status_t moe_fp4_dequantize(const uint8_t *q, int64_t ldq, const uint8_t *sf
           "moe_fp4_dequantize: leading dimension too small");
   REQUIRE(ldx % 8 == 0 && ldq % 16 == 0, MOE_ERR_UNSUPPORTED,
           "moe_fp4_dequantize: ldx must be a multiple of 8, ldq of 16");
+  REQUIRE(fits(0, ldx, ldq), MOE_ERR_UNSUPPORTED, "moe_fp4_dequantize: ldx or ldq of 2^31 and more");
   if (rows == 0) return MOE_OK;
   REQUIRE(x && q && sf, MOE_ERR_INVALID_ARG, "moe_fp4_dequantize: null pointer");
   REQUIRE(aligned(x, 16) && aligned(q, 16) && aligned(sf, 16), MOE_ERR_UNSUPPORTED,
@@ -132,7 +141,8 @@ moe_status_t moe_fp4_quantize_weights(const uint16_t *w, int E, int K, int N, in
   const moe_status_t st = check_rows("moe_fp4_quantize_weights", (int64_t)std::max(E, 0) * N, K,
                                      fmt, row_map, nullptr, E);
   if (st != MOE_OK) return st;
-  REQUIRE(E <= 65535 && K <= 65535 * 64, MOE_ERR_UNSUPPORTED,
+  REQUIRE(E <= 65535 && K <= 65535 * 64 && fits((int64_t)E * ((N + 127) / 128 * 128), 0),
+          MOE_ERR_UNSUPPORTED,
           "moe_fp4_quantize_weights: E=%d K=%d", E, K);
   REQUIRE(w && q && sf, MOE_ERR_INVALID_ARG, "moe_fp4_quantize_weights: null pointer");
   REQUIRE(aligned(w, 2) && aligned(q, 16) && aligned(sf, 16), MOE_ERR_UNSUPPORTED,
@@ -240,6 +250,7 @@ moe_status_t moe_fp4_experts(const moe_fp4_weights *w, const moe_fp4_buffers *b,
               aligned(b->act_q, 16) && aligned(b->act_sf, 16) && aligned(b->y, 16) &&
               aligned(b->h, 16) && aligned(b->workspace, 16) && aligned(x, 16) && ldx % 8 == 0,
           MOE_ERR_UNSUPPORTED, "moe_fp4_experts: operands must be 16-byte aligned");
+  REQUIRE(fits(T, ldx), MOE_ERR_UNSUPPORTED, "moe_fp4_experts: T or ldx of 2^31 and more");
   REQUIRE(ldx >= w->d, MOE_ERR_INVALID_ARG, "moe_fp4_experts: ldx=%lld < d", (long long)ldx);
   REQUIRE(b->x_sf_bytes >=
                   moe_fp4_scale_bytes(b->rows_cap, w->d, w->fmt, MOE_FP4_ROWS_GROUPED, w->E) &&
@@ -278,6 +289,7 @@ static moe_status_t check_act8(const char *who, int64_t rows, int cols, const in
           "%s: ldq=%lld (>= %lld) or lds=%lld (>= %lld) too small", who, (long long)ldq,
           (long long)need_q, (long long)lds, (long long)need_s);
   REQUIRE(ldq % 8 == 0, MOE_ERR_UNSUPPORTED, "%s: ldq must be a multiple of 8", who);
+  REQUIRE(fits(rows, ldq, lds), MOE_ERR_UNSUPPORTED, "%s: rows, ldq or lds of 2^31 and more", who);
   return MOE_OK;
 }
 
@@ -289,7 +301,8 @@ moe_status_t moe_act8_quantize(const uint16_t *x, int64_t ldx, int64_t rows, int
                                      lds, (cols + 31) / 32);
   if (st != MOE_OK) return st;
   REQUIRE(ldx >= cols, MOE_ERR_INVALID_ARG, "moe_act8_quantize: ldx too small");
-  REQUIRE(ldx % 8 == 0, MOE_ERR_UNSUPPORTED, "moe_act8_quantize: ldx must be a multiple of 8");
+  REQUIRE(ldx % 8 == 0 && fits(0, ldx), MOE_ERR_UNSUPPORTED,
+          "moe_act8_quantize: ldx must be a multiple of 8 under 2^31");
   if (rows == 0) return MOE_OK;
   REQUIRE(x && q && scales, MOE_ERR_INVALID_ARG, "moe_act8_quantize: null pointer");
   REQUIRE(aligned(x, 16) && aligned(q, 8) && aligned(scales, 2), MOE_ERR_UNSUPPORTED,
@@ -307,7 +320,8 @@ moe_status_t moe_act8_dequantize(const int8_t *q, int64_t ldq, const uint16_t *s
                                      cols, lds, (cols + 31) / 32);
   if (st != MOE_OK) return st;
   REQUIRE(ldx >= cols, MOE_ERR_INVALID_ARG, "moe_act8_dequantize: ldx too small");
-  REQUIRE(ldx % 8 == 0, MOE_ERR_UNSUPPORTED, "moe_act8_dequantize: ldx must be a multiple of 8");
+  REQUIRE(ldx % 8 == 0 && fits(0, ldx), MOE_ERR_UNSUPPORTED,
+          "moe_act8_dequantize: ldx must be a multiple of 8 under 2^31");
   if (rows == 0) return MOE_OK;
   REQUIRE(x && q && scales, MOE_ERR_INVALID_ARG, "moe_act8_dequantize: null pointer");
   REQUIRE(aligned(x, 16) && aligned(q, 8) && aligned(scales, 2), MOE_ERR_UNSUPPORTED,
@@ -327,8 +341,8 @@ moe_status_t moe_act8_swiglu_fwd(const uint16_t *h, int64_t ldh, int64_t rows, i
   if (st != MOE_OK) return st;
   REQUIRE(ldh >= 2ll * F && lda >= F, MOE_ERR_INVALID_ARG,
           "moe_act8_swiglu_fwd: leading dimension too small");
-  REQUIRE(ldh % 8 == 0 && lda % 8 == 0, MOE_ERR_UNSUPPORTED,
-          "moe_act8_swiglu_fwd: ldh and lda must be multiples of 8");
+  REQUIRE(ldh % 8 == 0 && lda % 8 == 0 && fits(0, ldh, lda), MOE_ERR_UNSUPPORTED,
+          "moe_act8_swiglu_fwd: ldh and lda must be multiples of 8 under 2^31");
   if (rows == 0) return MOE_OK;
   REQUIRE(h && act && q && scales, MOE_ERR_INVALID_ARG, "moe_act8_swiglu_fwd: null pointer");
   REQUIRE(aligned(h, 16) && aligned(act, 16) && aligned(q, 8) && aligned(scales, 2),
@@ -348,8 +362,10 @@ moe_status_t moe_act8_swiglu_bwd(const int8_t *q, int64_t ldq, const uint16_t *s
   if (st != MOE_OK) return st;
   REQUIRE(ld_dact >= F && ld_dh >= 2ll * F && (act == nullptr || lda >= F), MOE_ERR_INVALID_ARG,
           "moe_act8_swiglu_bwd: leading dimension too small");
-  REQUIRE(ld_dact % 8 == 0 && ld_dh % 8 == 0 && (act == nullptr || lda % 8 == 0),
-          MOE_ERR_UNSUPPORTED, "moe_act8_swiglu_bwd: ld_dact, ld_dh, lda must be multiples of 8");
+  REQUIRE(ld_dact % 8 == 0 && ld_dh % 8 == 0 && (act == nullptr || lda % 8 == 0) &&
+              fits(0, ld_dact, ld_dh, act == nullptr ? 0 : lda),
+          MOE_ERR_UNSUPPORTED,
+          "moe_act8_swiglu_bwd: ld_dact, ld_dh, lda must be multiples of 8 under 2^31");
   if (rows == 0) return MOE_OK;
   REQUIRE(q && scales && dact && dh, MOE_ERR_INVALID_ARG, "moe_act8_swiglu_bwd: null pointer");
   REQUIRE(aligned(dact, 16) && aligned(dh, 16) && aligned(act, 16) && aligned(q, 8) &&

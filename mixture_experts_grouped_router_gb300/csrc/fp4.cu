@@ -32,12 +32,12 @@ constexpr int kUnroll = 4;  // chunks of 256 columns a warp holds at a time
 constexpr int kMaxE = 256;
 
 // Padded row of row r of rows = E G under the maps that need no offsets.
-MOE_DEVINL int64_t weight_row(int64_t r, int64_t G, int row_map) {
-  const int64_t e = r / G, n = r - e * G;
-  int64_t m = n;
+MOE_DEVINL int weight_row(int r, int G, int row_map) {
+  const int e = r / G, n = r - e * G;
+  int m = n;
   if (row_map == MOE_FP4_ROWS_SWIGLU) {
-    const int64_t F = G / 2;
-    const int64_t f = n < F ? n : n - F;
+    const int F = G / 2;
+    const int f = n < F ? n : n - F;
     m = f / 32 * 64 + (n < F ? 0 : 32) + f % 32;
   }
   return e * ((G + 127) / 128 * 128) + m;
@@ -153,10 +153,10 @@ MOE_DEVINL void quantize_piece(const uint4 *w, int c0, int cols, int lane, float
 // Stores a piece as row r, padded row pr.
 template <int FMT>
 MOE_DEVINL void store_piece(const uint32_t *codes, const uint32_t *words, int c0, int cols,
-                            int lane, int64_t r, int64_t pr, int ac, uint8_t *q, int64_t ldq,
+                            int lane, int r, int pr, int ac, uint8_t *q, int ldq,
                             uint8_t *sf) {
   constexpr int kLanes = FMT == MOE_FP4_NV ? 8 : 16;  // lanes of a word
-  uint8_t *qr = q + r * ldq + (c0 >> 1);
+  uint8_t *qr = q + (int64_t)r * ldq + (c0 >> 1);
   // atoms of 4 blocks follow one another 512 bytes apart
   uint8_t *sr = sf + fp4_scale_byte(pr, c0 / fp4_block(FMT), ac);
 #pragma unroll
@@ -170,12 +170,12 @@ MOE_DEVINL void store_piece(const uint32_t *codes, const uint32_t *words, int c0
 }
 
 // A warp's piece of source row src (zeros where there is none).
-MOE_DEVINL void load_piece(const uint16_t *x, int64_t ldx, int64_t src, int c0, int cols,
+MOE_DEVINL void load_piece(const uint16_t *x, int ldx, int src, int c0, int cols,
                            uint4 *w) {
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
     w[i] = make_uint4(0, 0, 0, 0);
-    if (src >= 0 && c0 + 256 * i < cols) w[i] = ld_stream_v4(x + src * ldx + c0 + 256 * i);
+    if (src >= 0 && c0 + 256 * i < cols) w[i] = ld_stream_v4(x + (int64_t)src * ldx + c0 + 256 * i);
   }
 }
 
@@ -183,10 +183,10 @@ MOE_DEVINL void load_piece(const uint16_t *x, int64_t ldx, int64_t src, int c0, 
 // is quantised, the first row's before the groups are scanned.
 template <int FMT, bool GROUPED>
 __global__ void __launch_bounds__(kThreads)
-fp4_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t src_rows,
+fp4_quantize_kernel(const uint16_t *__restrict__ x, int ldx, int src_rows,
                     const int32_t *__restrict__ row_index, int index_div, int rows, int cols,
                     int row_map, const int32_t *__restrict__ offsets, int E,
-                    const float *__restrict__ gscale, uint8_t *__restrict__ q, int64_t ldq,
+                    const float *__restrict__ gscale, uint8_t *__restrict__ q, int ldq,
                     uint8_t *__restrict__ sf, int32_t *dev_status) {
   __shared__ Groups gr;
   const int lane = threadIdx.x & 31;
@@ -196,7 +196,7 @@ fp4_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t src_row
   Walk w((cols + 256 * kUnroll - 1) / (256 * kUnroll));
   // the source row of row w.row (-1: zeros; one that x does not have likewise)
   auto source = [&](bool &bad) {
-    int64_t src = -1;
+    int src = -1;
     if (w.row < rows) {
       src = w.row;
       if (row_index != nullptr) {
@@ -205,7 +205,7 @@ fp4_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t src_row
       }
     }
     bad = src >= src_rows;
-    return bad ? (int64_t)-1 : src;
+    return bad ? -1 : src;
   };
   uint4 cur[kUnroll];
   bool bad;
@@ -227,7 +227,7 @@ fp4_quantize_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t src_row
     load_piece(x, ldx, source(bad), w.seg * (256 * kUnroll) + lane * 8, cols, next);
     const float g = FMT == MOE_FP4_NV && !GROUPED && gscale != nullptr ? ld_f32(gscale + r / G) : g1;
     const float inv6 = GROUPED ? inv6_1 : __frcp_rn(6.0f * g);
-    const int64_t pr = GROUPED ? grouped_row(gr, e, r) : weight_row(r, G, row_map);
+    const int pr = GROUPED ? grouped_row(gr, e, r) : weight_row(r, G, row_map);
     if (pr >= 0) {
       uint32_t codes[kUnroll], words[kUnroll];
       quantize_piece<FMT>(cur, c0, cols, lane, g, inv6, codes, words);
@@ -272,9 +272,9 @@ fp4_link_kernel(const int32_t *__restrict__ row_index, int index_div, int64_t sr
 
 template <int FMT>
 __global__ void __launch_bounds__(kThreads)
-fp4_quantize_linked_kernel(const uint16_t *__restrict__ x, int64_t ldx, int src_rows, int cols,
+fp4_quantize_linked_kernel(const uint16_t *__restrict__ x, int ldx, int src_rows, int cols,
                            const float *__restrict__ gscale, const int32_t *__restrict__ head,
-                           const int2 *__restrict__ next, uint8_t *__restrict__ q, int64_t ldq,
+                           const int2 *__restrict__ next, uint8_t *__restrict__ q, int ldq,
                            uint8_t *__restrict__ sf) {
   const int lane = threadIdx.x & 31;
   const int ac = (cols + fp4_atom_cols(FMT) - 1) / fp4_atom_cols(FMT);
@@ -318,9 +318,9 @@ fp4_quantize_linked_kernel(const uint16_t *__restrict__ x, int64_t ldx, int src_
 // The way back: values (code * scale * g, rounded once to bf16).
 template <int FMT, bool GROUPED>
 __global__ void __launch_bounds__(kThreads)
-fp4_dequantize_kernel(const uint8_t *__restrict__ q, int64_t ldq, const uint8_t *__restrict__ sf,
+fp4_dequantize_kernel(const uint8_t *__restrict__ q, int ldq, const uint8_t *__restrict__ sf,
                       int rows, int cols, int row_map, const int32_t *__restrict__ offsets, int E,
-                      const float *__restrict__ gscale, uint16_t *__restrict__ x, int64_t ldx) {
+                      const float *__restrict__ gscale, uint16_t *__restrict__ x, int ldx) {
   __shared__ Groups gr;
   const int lane = threadIdx.x & 31;
   const int ac = (cols + fp4_atom_cols(FMT) - 1) / fp4_atom_cols(FMT);
@@ -336,9 +336,9 @@ fp4_dequantize_kernel(const uint8_t *__restrict__ q, int64_t ldq, const uint8_t 
   int e = 0;
   for (Walk w((cols + 256 * kUnroll - 1) / (256 * kUnroll)); w.row < R; w.step()) {
     const int r = w.row, c0 = w.seg * (256 * kUnroll) + lane * 8;
-    const int64_t pr = GROUPED ? grouped_row(gr, e, r) : weight_row(r, G, row_map);
+    const int pr = GROUPED ? grouped_row(gr, e, r) : weight_row(r, G, row_map);
     if (pr < 0) continue;
-    const uint8_t *qr = q + r * ldq + (c0 >> 1);
+    const uint8_t *qr = q + (int64_t)r * ldq + (c0 >> 1);
     const uint8_t *sr = sf + fp4_scale_byte(pr, c0 / fp4_block(FMT), ac);
     uint32_t codes[kUnroll], sc[kUnroll];
 #pragma unroll
@@ -359,7 +359,7 @@ fp4_dequantize_kernel(const uint8_t *__restrict__ q, int64_t ldq, const uint8_t 
         const float t = fp4_scale_value(sc[i], FMT);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = FMT == MOE_FP4_NV ? v[j] * t * g : v[j] * t;
-        st_v4(x + r * ldx + c0 + 256 * i, f32_to_bf16x8(v));
+        st_v4(x + (int64_t)r * ldx + c0 + 256 * i, f32_to_bf16x8(v));
       }
     }
   }
@@ -388,7 +388,7 @@ fp4_quantize_weights_kernel(const uint16_t *__restrict__ w, int K, int N, int ro
   if (n >= N) return;
   constexpr int kB = fp4_block(FMT);
   const int ac = (K + fp4_atom_cols(FMT) - 1) / fp4_atom_cols(FMT);
-  const int64_t pr = weight_row((int64_t)e * N + n, N, row_map);
+  const int pr = weight_row(e * N + n, N, row_map);
   const float g = FMT != MOE_FP4_NV || gscale == nullptr ? 1.0f : __ldg(gscale + e);
   uint32_t codes[4];
 #pragma unroll
@@ -420,7 +420,7 @@ fp4_quantize_weights_kernel(const uint16_t *__restrict__ w, int K, int N, int ro
 // Row-order scales [rows, nb] of a 4-bit checkpoint into atoms (a thread one
 // word of 4 blocks).
 __global__ void __launch_bounds__(kThreads)
-fp4_arrange_scales_kernel(const uint8_t *__restrict__ s, int64_t rows, int nb, int64_t G,
+fp4_arrange_scales_kernel(const uint8_t *__restrict__ s, int64_t rows, int nb, int G,
                           int row_map, uint8_t *__restrict__ sf) {
   const int ac = (nb + 3) / 4;
   const int64_t stride = (int64_t)gridDim.x * kThreads;
@@ -431,15 +431,25 @@ fp4_arrange_scales_kernel(const uint8_t *__restrict__ s, int64_t rows, int nb, i
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (b + j < nb) w |= (uint32_t)__ldg(s + r * nb + b + j) << (8 * j);
-    *reinterpret_cast<uint32_t *>(sf + fp4_scale_byte(weight_row(r, G, row_map), b, ac)) = w;
+    *reinterpret_cast<uint32_t *>(sf + fp4_scale_byte(weight_row((int)r, G, row_map), b, ac)) = w;
   }
 }
 
-// All resident at once (a persistent walk over rows and segments).
-int grid_for(int64_t rows, int cols) {
+// A kernel as a value that a lambda can take.
+template <auto Kernel>
+struct K {
+  static constexpr auto value = Kernel;
+};
+
+// Launches a kernel's walk over rows x segments of 4 chunks: as many blocks as
+// there is work for, no more than the GPU holds at a time.
+template <auto Kernel, typename... Args>
+cudaError_t run(int64_t rows, int cols, cudaStream_t st, Args... args) {
   const int64_t warps = rows * ((cols + 256 * kUnroll - 1) / (256 * kUnroll));
-  return (int)std::max<int64_t>(
-      1, std::min<int64_t>((warps + kWarps - 1) / kWarps, (int64_t)num_sms() * 8));
+  const int64_t most = (int64_t)num_sms() * blocks_per_sm<Kernel>(kThreads);
+  const int64_t blocks = std::min((warps + kWarps - 1) / kWarps, most);
+  return launch_dependent(Kernel, (unsigned)std::max<int64_t>(1, blocks), kThreads, 0, st,
+                          args...);
 }
 
 }  // namespace
@@ -475,41 +485,39 @@ cudaError_t launch_fp4_quantize(const uint16_t *x, int64_t ldx, int64_t src_rows
     e = launch_dependent(fp4_link_kernel, lg, kThreads, 0, st, row_index, index_div, src_rows,
                          (int)rows, offsets, E, head, next, dev_status);
     if (e != cudaSuccess) return e;
-    const int grid = grid_for(src_rows + kZeroLists, cols);
-    auto run = [&](auto kernel) {
-      return launch_dependent(kernel, grid, kThreads, 0, st, x, ldx, (int)src_rows, cols, gscale,
-                              (const int32_t *)head, (const int2 *)next, q, ldq, sf);
+    auto link = [&](auto kernel) {
+      return run<kernel.value>(src_rows + kZeroLists, cols, st, x, (int)ldx, (int)src_rows, cols,
+                               gscale, (const int32_t *)head, (const int2 *)next, q, (int)ldq, sf);
     };
-    return fmt == MOE_FP4_NV ? run(fp4_quantize_linked_kernel<MOE_FP4_NV>)
-                             : run(fp4_quantize_linked_kernel<MOE_FP4_MX>);
+    return fmt == MOE_FP4_NV ? link(K<fp4_quantize_linked_kernel<MOE_FP4_NV>>{})
+                             : link(K<fp4_quantize_linked_kernel<MOE_FP4_MX>>{});
   }
-  const int grid = grid_for(rows, cols);
-  auto run = [&](auto kernel) {
-    return launch_dependent(kernel, grid, kThreads, 0, st, x, ldx, src_rows, row_index, index_div,
-                            (int)rows, cols, row_map, offsets, E, gscale, q, ldq, sf, dev_status);
+  auto go = [&](auto kernel) {
+    return run<kernel.value>(rows, cols, st, x, (int)ldx, (int)src_rows, row_index, index_div,
+                             (int)rows, cols, row_map, offsets, E, gscale, q, (int)ldq, sf,
+                             dev_status);
   };
   if (fmt == MOE_FP4_NV)
-    return grouped ? run(fp4_quantize_kernel<MOE_FP4_NV, true>)
-                   : run(fp4_quantize_kernel<MOE_FP4_NV, false>);
-  return grouped ? run(fp4_quantize_kernel<MOE_FP4_MX, true>)
-                 : run(fp4_quantize_kernel<MOE_FP4_MX, false>);
+    return grouped ? go(K<fp4_quantize_kernel<MOE_FP4_NV, true>>{})
+                   : go(K<fp4_quantize_kernel<MOE_FP4_NV, false>>{});
+  return grouped ? go(K<fp4_quantize_kernel<MOE_FP4_MX, true>>{})
+                 : go(K<fp4_quantize_kernel<MOE_FP4_MX, false>>{});
 }
 
 cudaError_t launch_fp4_dequantize(const uint8_t *q, int64_t ldq, const uint8_t *sf, int64_t rows,
                                   int cols, int fmt, int row_map, const int32_t *offsets, int E,
                                   const float *gscale, uint16_t *x, int64_t ldx,
                                   cudaStream_t st) {
-  const int grid = grid_for(rows, cols);
   const bool grouped = row_map == MOE_FP4_ROWS_GROUPED;
-  auto run = [&](auto kernel) {
-    return launch_dependent(kernel, grid, kThreads, 0, st, q, ldq, sf, (int)rows, cols, row_map,
-                            offsets, E, gscale, x, ldx);
+  auto go = [&](auto kernel) {
+    return run<kernel.value>(rows, cols, st, q, (int)ldq, sf, (int)rows, cols, row_map, offsets, E,
+                             gscale, x, (int)ldx);
   };
   if (fmt == MOE_FP4_NV)
-    return grouped ? run(fp4_dequantize_kernel<MOE_FP4_NV, true>)
-                   : run(fp4_dequantize_kernel<MOE_FP4_NV, false>);
-  return grouped ? run(fp4_dequantize_kernel<MOE_FP4_MX, true>)
-                 : run(fp4_dequantize_kernel<MOE_FP4_MX, false>);
+    return grouped ? go(K<fp4_dequantize_kernel<MOE_FP4_NV, true>>{})
+                   : go(K<fp4_dequantize_kernel<MOE_FP4_NV, false>>{});
+  return grouped ? go(K<fp4_dequantize_kernel<MOE_FP4_MX, true>>{})
+                 : go(K<fp4_dequantize_kernel<MOE_FP4_MX, false>>{});
 }
 
 cudaError_t launch_fp4_quantize_weights(const uint16_t *w, int E, int K, int N, int fmt,
@@ -528,7 +536,7 @@ cudaError_t launch_fp4_arrange_scales(const uint8_t *s, int64_t rows, int nb, in
   const int64_t words = rows * ((nb + 3) / 4);
   const int grid = (int)std::max<int64_t>(
       1, std::min<int64_t>((words + kThreads - 1) / kThreads, (int64_t)num_sms() * 8));
-  fp4_arrange_scales_kernel<<<grid, kThreads, 0, st>>>(s, rows, nb, rows / E, row_map, sf);
+  fp4_arrange_scales_kernel<<<grid, kThreads, 0, st>>>(s, rows, nb, (int)(rows / E), row_map, sf);
   return cudaGetLastError();
 }
 

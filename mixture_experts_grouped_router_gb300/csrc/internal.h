@@ -184,6 +184,21 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, s
   return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
 }
 
+// Blocks of `threads` threads of a kernel that one SM holds at a time.
+template <auto Kernel>
+int blocks_per_sm(int threads) {
+  static int n = 0;  // same answer whichever thread asks first
+  if (n == 0) {
+    int v = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, Kernel, threads, 0) != cudaSuccess) {
+      cudaGetLastError();
+      v = 1;
+    }
+    n = v > 0 ? v : 1;
+  }
+  return n;
+}
+
 // fp4.cu (4-bit block-scaled formats: quantisers, scale layout)
 int64_t fp4_atom_rows(int64_t rows, int row_map, int E);
 cudaError_t launch_fp4_quantize(const uint16_t *x, int64_t ldx, int64_t src_rows,
