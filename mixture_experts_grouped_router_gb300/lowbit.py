@@ -6,11 +6,17 @@ steps whose saved activations take 8 bits.
 layer's bf16 weights or loaded from a 4-bit checkpoint; :func:`fp4_experts`
 takes the router's permutation and runs gather + quantise, the up-projection
 with the SwiGLU and the quantisation of Act in its epilogue, and the
-down-projection.  :func:`fp4_layer` is the whole serving layer around it (route,
-permute, experts, combine).
+down-projection.  :class:`Fp4Layer` is the serving layer around it (route,
+permute, experts, combine), for prompts and for single tokens.
 
 8-bit activation checkpoints: :func:`act8_swiglu_fwd` / :func:`act8_swiglu_bwd`
-and :func:`act8_quantize` / :func:`act8_dequantize`.
+and :func:`act8_quantize` / :func:`act8_dequantize`.  :class:`Checkpoint8` keeps
+what the bf16 layer's backward needs of a forward in 8 bits, so that layers share
+one workspace: ``layer.forward(bufs, ...)``, ``ck.save(bufs)``, other layers'
+forwards in the same ``bufs``, then ``ck.backward(bufs, ...)``.  The codes of H
+feed the SwiGLU backward as they are, Act is recomputed there, and the permuted
+tokens and the expert outputs are restored for the weight gradient and the
+routing weights' gradient.
 
 Every function launches on the given or current stream and returns without
 waiting; each arithmetic step runs in libmoe_gb300.so.
@@ -144,18 +150,74 @@ class Fp4Buffers:
             self.x.workspace.data_ptr(), self.x.workspace.numel(), self.dev_status.data_ptr())
 
 
-def fp4_experts(w: Fp4Experts, b: Fp4Buffers, x, sorted_to_flat, k, group_offsets, stream=None):
+def fp4_experts(w: Fp4Experts, b: Fp4Buffers, x, sorted_to_flat, k, group_offsets, stream=None,
+                rows=None):
     """Expert outputs y bf16 [rows_cap, d] of the permuted rows of x bf16 [T, d]
     (sorted_to_flat int32 [rows_cap], group_offsets int32 [E + 1] as moe_permute leaves them;
-    rows past group_offsets[E] are not written).  With b.h also H = [gate | up] in bf16."""
+    rows past group_offsets[E] are not written).  With b.h also H = [gate | up] in bf16.
+    rows: the first so many rows hold every group (fewer than rows_cap where x is short of what
+    the buffers are for); group_offsets past them are clamped."""
     if sorted_to_flat.shape[0] < b.rows_cap or group_offsets.shape[0] != w.E + 1:
         raise ValueError("sorted_to_flat of %d rows (rows_cap %d), group_offsets of %d (E %d)"
                          % (sorted_to_flat.shape[0], b.rows_cap, group_offsets.shape[0], w.E))
     if x.shape[1] != w.d or b.y.shape[1] != w.d or b.act.cols != w.f:
         raise ValueError("x of %d columns, buffers for (%d, %d), experts (%d, %d)"
                          % (x.shape[1], b.y.shape[1], b.act.cols, w.d, w.f))
-    L.moe_fp4_experts(w.arg, b.arg, x, sorted_to_flat, k, group_offsets, stream)
+    if rows is not None and rows != b.rows_cap:
+        if not 0 <= rows <= b.rows_cap:
+            raise ValueError("rows = %d of %d" % (rows, b.rows_cap))
+        arg = L.Fp4BuffersArg.from_buffer_copy(b.arg)
+        arg.rows_cap = rows
+        L.moe_fp4_experts(w.arg, arg, x, sorted_to_flat, k, group_offsets, stream)
+    else:
+        L.moe_fp4_experts(w.arg, b.arg, x, sorted_to_flat, k, group_offsets, stream)
     return b.y
+
+
+class Fp4Layer:
+    """The serving layer for up to T tokens: routing (a LayerShape's router options), the 4-bit
+    experts and the combine.  ``forward(x, logits)`` -> out bf16 [T', d] for x bf16 [T', d],
+    logits fp32 [T', E], T' <= T (a view of the layer's buffer)."""
+
+    def __init__(self, w: Fp4Experts, s):
+        if (s.E, s.d, s.f) != (w.E, w.d, w.f):
+            raise ValueError("shape (E, d, f) = (%d, %d, %d) for experts (%d, %d, %d)"
+                             % (s.E, s.d, s.f, w.E, w.d, w.f))
+        if s.bias:
+            raise ValueError("the 4-bit experts take no biases")
+        dev = w.wo_q.device
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.w, self.s = w, s
+        R = L.moe_rows_cap(s.T, s.E, s.k, s.align, s.capacity)
+        self.bufs = Fp4Buffers(w, R)
+        self.topk_idx = torch.empty(s.T, s.k, **i32)
+        self.topk_w = torch.empty(s.T, s.k, dtype=torch.float32, device=dev)
+        self.sizes, self.kept = torch.empty(s.E, **i32), torch.empty(s.E, **i32)
+        self.offsets = torch.empty(s.E + 1, **i32)
+        self.s2f, self.f2s = torch.empty(R, **i32), torch.empty(s.T * s.k, **i32)
+        # the permute gathers no more than 8 columns: the experts gather codes themselves
+        self.head = torch.empty(R, 8, dtype=torch.bfloat16, device=dev)
+        self.ws = torch.empty(L.moe_permute_workspace_bytes(s.T, s.E), dtype=torch.uint8,
+                              device=dev)
+        self.out = torch.empty(s.T, s.d, dtype=torch.bfloat16, device=dev)
+
+    def forward(self, x, logits, expert_bias=None, stream=None):
+        s, T = self.s, x.shape[0]
+        if T > s.T or logits.shape != (T, s.E):
+            raise ValueError("x of %d tokens (at most %d), logits of shape %s"
+                             % (T, s.T, tuple(logits.shape)))
+        idx, w, f2s, out = self.topk_idx[:T], self.topk_w[:T], self.f2s[:T * s.k], self.out[:T]
+        if T == 0:
+            return out
+        L.moe_route_topk(logits, s.k, s.score_fn, s.renorm, idx, w, stream,
+                         expert_bias=expert_bias, num_groups=s.num_groups, topk_group=s.topk_group)
+        L.moe_permute(x[:, :8], idx, s.E, s.align, s.capacity, self.head, self.sizes, self.kept,
+                      self.offsets, self.s2f, f2s, self.ws, self.bufs.dev_status, stream)
+        # the kernels take their tiles by the rows that T tokens can fill
+        R = L.moe_rows_cap(T, s.E, s.k, s.align, s.capacity)
+        y = fp4_experts(self.w, self.bufs, x, self.s2f, s.k, self.offsets, stream, rows=R)
+        L.moe_combine(y, f2s, w, out, s.k, stream)
+        return out
 
 
 # --------------------------------------------------- 8-bit activation checkpoints
@@ -165,3 +227,79 @@ act8_quantize = L.moe_act8_quantize
 act8_dequantize = L.moe_act8_dequantize
 act8_swiglu_fwd = L.moe_act8_swiglu_fwd
 act8_swiglu_bwd = L.moe_act8_swiglu_bwd
+
+
+class Checkpoint8:
+    """What the bf16 layer's backward needs of one forward, in 8 bits: codes of the permuted
+    tokens, of H and of the expert outputs, and the routing decision.  One for each layer of a
+    model; all of them may share one MoEBuffers."""
+
+    def __init__(self, b):
+        s = b.s
+        if s.fp8 or s.mxfp8 or s.wgrad_colwise:
+            raise ValueError("8-bit checkpoints are of the bf16 layer without column-wise copies")
+        if s.d % 8 or s.f % 8:
+            raise ValueError("d=%d and f=%d must be multiples of 8" % (s.d, s.f))
+        dev = b.workspace.device
+        R, nf = b.rows_cap, -(-s.f // 32)
+
+        def codes(cols, blocks):
+            return (torch.empty(R, cols, dtype=torch.int8, device=dev),
+                    torch.empty(R, blocks, dtype=torch.bfloat16, device=dev))
+
+        self.xs, self.y = codes(s.d, -(-s.d // 32)), codes(s.d, -(-s.d // 32))
+        self.h = codes(2 * s.f, 2 * nf)
+        self.nf = nf
+        names = ("topk_idx", "topk_w", "group_offsets", "s2f", "f2s") + (
+            ("aux_counts",) if s.aux_coeff else ())
+        self.routing = {n: torch.empty_like(getattr(b, n)) for n in names}
+        self.logits = None
+
+    def nbytes(self) -> int:
+        """Bytes that the checkpoint holds."""
+        ts = [*self.xs, *self.h, *self.y, *self.routing.values()]
+        return sum(t.numel() * t.element_size() for t in ts)
+
+    def save(self, b, stream=None):
+        """After layer.forward(b, ...): afterwards b is free for another layer's forward."""
+        f, nf = b.s.f, self.nf
+        self.logits = b.logits
+        off = b.group_offsets
+        with torch.cuda.stream(stream):
+            for n, t in self.routing.items():
+                t.copy_(getattr(b, n))
+        act8_quantize(b.xs, *self.xs, off, stream)
+        act8_quantize(b.y, *self.y, off, stream)
+        q, sc = self.h
+        if f % 32 == 0:  # no block straddles the halves
+            act8_quantize(b.h, q, sc, off, stream)
+        else:
+            act8_quantize(b.h[:, :f], q[:, :f], sc[:, :nf], off, stream)
+            act8_quantize(b.h[:, f:], q[:, f:], sc[:, nf:], off, stream)
+
+    def backward(self, b, dout, wi, wo, stream=None):
+        """layer.backward of the saved forward: (dx, dwi, dwo, d_topk_w) in b's buffers, the
+        router-logit gradient in b.d_logits, bias gradients in b.dbi and b.dbo."""
+        if self.logits is None:
+            raise ValueError("Checkpoint8.backward before save")
+        s, r = b.s, self.routing
+        off, f2s, st = r["group_offsets"], r["f2s"], b.dev_status
+        act8_dequantize(*self.y, b.y, off, stream)
+        L.moe_unpermute_bwd(dout, b.y, f2s, r["s2f"], off, r["topk_w"], b.dy, b.d_topk_w, stream)
+        L.moe_route_topk_bwd(self.logits, r["topk_idx"], r["topk_w"], b.d_topk_w, s.score_fn,
+                             s.renorm, b.d_logits, stream)
+        if s.aux_coeff:
+            L.moe_aux_loss_bwd(self.logits, r["aux_counts"], s.k, s.score_fn, s.aux_coeff,
+                               b.d_logits, stream=stream)
+        dact = b.h[:, :s.f]  # H itself is not needed: its codes are
+        L.moe_gmm(b.dy, wo, 1, off, dact, dev_status=st, stream=stream)
+        act8_swiglu_bwd(*self.h, dact, b.dh, b.act, off, stream)
+        L.moe_tgmm(b.act, b.dy, off, b.dwo, dev_status=st, stream=stream)
+        if s.bias:
+            L.moe_group_colsum(b.dy, off, b.dbo, stream)
+            L.moe_group_colsum(b.dh, off, b.dbi, stream)
+        L.moe_gmm(b.dh, wi, 1, off, b.dxs, dev_status=st, stream=stream)
+        act8_dequantize(*self.xs, b.xs, off, stream)
+        L.moe_tgmm(b.xs, b.dh, off, b.dwi, dev_status=st, stream=stream)
+        L.moe_combine(b.dxs, f2s, None, b.dx, s.k, stream)
+        return b.dx, b.dwi, b.dwo, b.d_topk_w
