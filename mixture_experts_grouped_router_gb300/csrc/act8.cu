@@ -16,7 +16,16 @@
 //
 // Every kernel streams: a warp takes 256 columns of a row at a time (8 elements
 // = 16 bytes a lane, 4 lanes a block, the block's maximum by two shuffles) and
-// keeps kUnroll such chunks in flight.
+// keeps two to four 16-byte loads a lane in flight.  What bounds them: the reading
+// kernels HBM, the quantising ones the issue of some 15 instructions a value as well
+// (32768 rows, measured copy 6676 GB/s):
+//   swiglu_bwd, F = 14336       735 us, 6460 GB/s
+//   swiglu_fwd, F = 14336       652 us, 5850 GB/s (five resident blocks: 634 us by
+//       itself, but forward and backward in turn 1375 -> 1394 us)
+//   dequantize, 4096 columns     65 us, 6270 GB/s
+//   quantize,   4096 columns     69 us, 5960 GB/s (eight resident blocks of two
+//       loads a lane; four of four: 74 us)
+// Eight loads a lane are slower everywhere (registers).
 #include <algorithm>
 
 #include "internal.h"
@@ -104,20 +113,21 @@ MOE_DEVINL int live_rows(const int32_t *offsets, int E, int rows) {
   return min(max(ld_i32(offsets + E), 0), rows);
 }
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 8)
 act8_quantize_kernel(const uint16_t *__restrict__ x, int ldx, int rows, int cols,
                      const int32_t *__restrict__ offsets, int E, int8_t *__restrict__ q,
                      int ldq, uint16_t *__restrict__ s, int lds) {
+  constexpr int kU = 2;
   const int lane = threadIdx.x & 31;
   grid_dependency_begin();
   const int R = live_rows(offsets, E, rows);
   Walk w((cols + 255) / 256);
   while (w.row < R) {
-    uint4 v[kUnroll];
-    int at[kUnroll];
-    int col[kUnroll];
+    uint4 v[kU];
+    int at[kU];
+    int col[kU];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
+    for (int i = 0; i < kU; ++i) {
       at[i] = w.row;
       col[i] = w.ch * 256 + lane * 8;
       v[i] = make_uint4(0, 0, 0, 0);
@@ -125,7 +135,7 @@ act8_quantize_kernel(const uint16_t *__restrict__ x, int ldx, int rows, int cols
       w.step();
     }
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
+    for (int i = 0; i < kU; ++i) {
       uint32_t sb;
       const uint2 c = act8_quantize8(v[i], sb);
       if (at[i] < R && col[i] < cols) {
