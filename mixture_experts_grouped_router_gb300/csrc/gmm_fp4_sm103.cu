@@ -343,14 +343,19 @@ MOE_DEVINL void epilogue_plain(const Fp4Params &p, const TileInfo &ti, float sc,
       }
     } else {  // rows past the group are the next expert's
       __syncwarp();
-      const int sh = p.c_f32 ? 3 : 2;  // log2 of a row's 16-byte chunks
-      for (int i = lane; i < (32 << sh); i += 32) {
-        const int r = i >> sh, k = i & ((1 << sh) - 1);
-        const int n = nc + (k << (p.c_f32 ? 2 : 3));
-        if (r < left && n < p.N) {
-          const int at = p.c_f32 ? r * 128 + ((k ^ (r & 7)) << 4) : r * 64 + ((k ^ ((r >> 1) & 3)) << 4);
-          uint8_t *o = static_cast<uint8_t *>(p.C) + ((r0 + r) * p.ldc + n) * (p.c_f32 ? 4 : 2);
-          st_v4(o, *reinterpret_cast<const uint4 *>(buf + at));
+      // a row's 16-byte chunks: 4 (bf16) or 8 (fp32), one a lane
+      const int sh = p.c_f32 ? 3 : 2, es = p.c_f32 ? 4 : 2;
+      const int k = lane & ((1 << sh) - 1), first = lane >> sh, step = 32 >> sh;
+      const bool in = nc + k * (16 / es) < p.N;
+      uint8_t *o = static_cast<uint8_t *>(p.C) +
+                   ((int64_t)(r0 + first) * p.ldc + nc) * es + k * 16;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = first + i * step;
+        if (r < left && in) {
+          const int at =
+              p.c_f32 ? r * 128 + ((k ^ (r & 7)) << 4) : r * 64 + ((k ^ ((r >> 1) & 3)) << 4);
+          st_v4(o + (int64_t)i * step * p.ldc * es, *reinterpret_cast<const uint4 *>(buf + at));
         }
       }
       __syncwarp();
