@@ -49,7 +49,7 @@
 
 #include "internal.h"
 #include "lowbit.cuh"
-#include "tc_sm103.cuh"
+#include "tc_fp4_sm103.cuh"
 
 namespace moe {
 namespace {

@@ -46,23 +46,6 @@ MOE_DEVINL bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Whether that phase has completed, without waiting.
-MOE_DEVINL bool mbar_test(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-MOE_DEVINL void mbar_arrive(uint64_t *bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 // Wait for the phase with the given parity to complete.  Gives up when the
 // CTA's abort flag is raised or after `limit_ns`; then raises the flag and
 // returns false so that every role of the CTA winds down.
@@ -243,15 +226,6 @@ MOE_DEVINL void tma_load_3d_2sm(void *dst, const CUtensorMap *map, uint32_t bar,
       : "memory");
 }
 
-MOE_DEVINL void tma_load_5d_2sm(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1,
-                                int c2, int c3, int c4) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
-      : "memory");
-}
-
 // Generic-proxy writes to shared memory made visible to the async proxy
 // (tensor-core operand reads).
 MOE_DEVINL void fence_proxy_async_smem() {
@@ -268,23 +242,6 @@ MOE_DEVINL void st_cluster_zero16(uint32_t cluster_addr) {
   asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(cluster_addr), "r"(0u)
                : "memory");
 }
-
-// True in one lane of a converged warp.  Tensor-core and TMA instructions take
-// their operands from uniform registers: behind `if (elect_one())` in a warp whose
-// control flow and operands are uniform, the compiler keeps them there, where
-// behind `if (lane == 0)` it moves every operand of every instruction first.
-MOE_DEVINL bool elect_one() {
-  uint32_t pred;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(pred));
-  return pred != 0;
-}
-
-// A value that every lane holds alike, as one the compiler knows to be uniform.
-MOE_DEVINL int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // ------------------------------------------------- tcgen05 descriptors
 // Shared-memory matrix descriptor, 128-byte swizzle, descriptor version 1.
@@ -365,42 +322,6 @@ MOE_DEVINL void umma_mxf8_2sm(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, u
       ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem),
       "r"(accumulate)
       : "memory");
-}
-
-// Instruction descriptor of kind::mxf4nvf4 with block scaling, fp32
-// accumulation, both operands K-major E2M1 (format 1): bits 4-5 and 29-30 the
-// first byte of B's / A's 32-bit scale words that this MMA uses (scale_vec::4X
-// takes the whole word, id 0; scale_vec::2X two bytes, id 0 or 2), 23 scale
-// format (0 = UE4M3, 1 = UE8M0), 17-22 N >> 3, 27-28 M >> 7, 31 K (0 = 64).
-__host__ __device__ constexpr uint32_t idesc_fp4(int M, int N, bool nv, int sf_id) {
-  return (static_cast<uint32_t>(sf_id) << 4) | (1u << 7) | (1u << 10) |
-         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(!nv) << 23) |
-         (static_cast<uint32_t>(M >> 7) << 27) | (static_cast<uint32_t>(sf_id) << 29);
-}
-
-// 4-bit block-scaled MMA over both CTAs of the pair (K = 64 codes): one E4M3
-// scale per 16 codes (NV) or one E8M0 scale per 32.
-template <bool NV>
-MOE_DEVINL void umma_fp4_2sm(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                             uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
-  if (NV)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X"
-        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem),
-        "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X"
-        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem),
-        "r"(accumulate)
-        : "memory");
 }
 
 // Tensor-memory columns for the CTA pair (warp-collective, both CTAs), the
