@@ -36,9 +36,9 @@ MOE_DEVINL void tma_load_5d_2sm(void *dst, const CUtensorMap *map, uint32_t bar,
 
 // True in one lane of a converged warp.  Tensor-core and TMA instructions take
 // their operands from uniform registers.  Issued behind `if (elect_one())` by a warp
-// whose control flow and operands are uniform they cost some 15 cycles each, behind
-// `if (lane == 0)` about 60 (a GEMM that issues 10 to 16 of them a K block: 2.41
-// against 1.36 ms), as if every operand were moved there first.
+// whose control flow and operands are uniform they cost far less than behind
+// `if (lane == 0)`: the 4-bit GEMM, which issues 10 to 16 of them a K block, ran
+// 32768 rows of 4096 x 28672 in 1.36 ms with the one and in 2.41 ms with the other.
 MOE_DEVINL bool elect_one() {
   uint32_t pred;
   asm volatile(
