@@ -29,7 +29,8 @@
 // (NVFP4) or 2 (MXFP4) for the weight rows and twice as many for 192 tokens.
 //   warp 0     TMA producer
 //   warp 1     tensor memory, and in the leader CTA the MMA issue: the atoms
-//              to tensor memory (tcgen05.cp), then four MMAs
+//              to tensor memory (tcgen05.cp), then four MMAs.  A tile's shape comes
+//              from the producer with the tile's first stage
 //   warps 2-9  epilogue, two per quarter of the tensor-memory lanes, which take the
 //              tile's chunks of 32 tokens in turn (kRows: warps 2-5)
 // Tensor memory: two accumulators of 192 columns, and scale slots in the 128
@@ -37,9 +38,12 @@
 // 5).  A slot is rewritten after the MMAs that read it are done: their commit
 // arrives on the full barrier of the K block that takes the slot next, beside the
 // stage's copies, so that the issuer has one barrier to wait for.  That wait and
-// the issue set the pace (a K block's MMAs take about 300 cycles): the next
-// barrier is tested before a block's MMAs are issued, and the issuing warp stays
-// uniform, elect_one() choosing the lane.
+// the issue set the pace (at 192 tokens a K block's MMAs take 384 cycles, its issue
+// some 280 and its wait 60): the next barrier is tested before a block's MMAs are
+// issued, the issuing warp stays uniform, elect_one() choosing the lane, its
+// descriptors differ by constants, and it looks up no tile (those two: 1095 -> 1046 us
+// MXFP4, 1345 -> 1222 NVFP4, 32768 rows, 4096 x 28672 with SwiGLU; two K blocks
+// an iteration were no faster).
 // Every wait is bounded; on time-out the CTA winds down and reports
 // MOE_ERR_TIMEOUT through dev_status.
 #include <cudaTypedefs.h>
@@ -94,6 +98,7 @@ struct Book {
   uint64_t tempty[2];
   uint64_t drain;
   uint32_t tmem_base;
+  uint32_t shape[kMaxStages];  // mma_shape of the tile that begins in the stage
   int abort_flag;
   int total_tiles;
   int off[kMaxE + 1];        // group offsets, clamped to [0, rows_cap]
@@ -174,6 +179,12 @@ MOE_DEVINL TileInfo decode_tile(const Book &bk, const Fp4Params &p, int t) {
 // columns on); whether its tokens reach into a second one.
 MOE_DEVINL int scale_shift(const TileInfo &ti) { return ti.t0 & 127 ? 2 : 0; }
 MOE_DEVINL bool second_atom(const TileInfo &ti) { return scale_shift(ti) * 32 + ti.n > 128; }
+
+// A tile's MMAs as the producer hands them to the issuing warp: N, the scale
+// column that the tokens start in, whether they reach into a second atom.
+MOE_DEVINL uint32_t mma_shape(int n, int shift, bool second) {
+  return (uint32_t)n | (uint32_t)shift << 8 | (uint32_t)second << 16;
+}
 
 // ---------------------------------------------------------------- epilogue
 // Thread `r`'s 32 values become column r of a 32 x 32 block (block row j = value
@@ -596,7 +607,10 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
           if (tc::elect_one()) {
             uint8_t *st = smem + s * L::stage_bytes;
             const uint32_t fb = tc::mapa_shared(tc::smem_u32(&bk.full[s]), 0);
-            if (leader) tc::mbar_expect_tx(&bk.full[s], tx);
+            if (leader) {
+              if (kb == 0) bk.shape[s] = mma_shape(BR, ti.n_idx & 1 ? 2 : 0, true);
+              tc::mbar_expect_tx(&bk.full[s], tx);
+            }
             const int k = kb * kRowBytes;
             if (own) {
               tc::tma_load_2d_2sm(st, &m.t[0], fb, k, ti.row0);
@@ -632,7 +646,10 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
         auto load_weights = [&](int st, int kb) {
           uint8_t *sw = smem + st * L::stage_bytes;
           const uint32_t fb = tc::mapa_shared(tc::smem_u32(&bk.full[st]), 0);
-          if (leader) tc::mbar_expect_tx(&bk.full[st], tx);
+          if (leader) {
+            if (kb == 0) bk.shape[st] = mma_shape(ti.n, scale_shift(ti), second_atom(ti));
+            tc::mbar_expect_tx(&bk.full[st], tx);
+          }
           const int k = kb * kRowBytes;
           if (EPI == MOE_EPI_SWIGLU_FWD)  // 32 gate rows, 32 up rows, twice
             tc::tma_load_5d_2sm(sw, &m.w, fb, k, 0, 0, 4 * ti.w_idx + 2 * crank, ti.e);
@@ -691,6 +708,11 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
     int slot = 0;       // its scale slot
     bool ready = false; // its barrier has been seen complete
     bool ok = true;
+    // descriptors of codes and scales at address 0, and the ring in their units
+    const uint64_t dcodes = tc::sdesc(0, 16, 1024), dscales = tc::sdesc_plain(0, 0, 128);
+    const uint32_t ring = (uint32_t)tc::uniform((int)(tc::smem_u32(smem) >> 4));
+    constexpr uint32_t kTok = W_BYTES / 16, kSfw = kTok + T_BYTES / 16,
+                       kSft = kSfw + L::sfw_bytes / 16;
     // the first K blocks find their scale slots free
     if (tc::elect_one())
       for (int i = 0; i < L::sf_slots; ++i) tc::mbar_arrive(&bk.full[i]);
@@ -698,19 +720,8 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
     for (int t = cid; t < total && ok; t += ncl) {
       const uint32_t a = acc_it & 1;
       const uint32_t aph = (acc_it >> 1) & 1;
-      // N, where it starts in its scale atoms, and whether it reaches into a second
-      int n = BR, shift = 0;
-      bool second = true;
-      if (EPI == kRows) {
-        shift = decode_row_tile(bk, p, t, crank).n_idx & 1 ? 2 : 0;
-      } else {
-        const TileInfo ti = decode_tile(bk, p, t);
-        n = ti.n;
-        shift = scale_shift(ti);
-        second = second_atom(ti);
-      }
-      const uint32_t id0 = tc::idesc_fp4(BW, n, FMT == MOE_FP4_NV, 0);
-      const uint32_t id2 = tc::idesc_fp4(BW, n, FMT == MOE_FP4_NV, 2);
+      uint32_t id0 = 0, id2 = 0, shift = 0;
+      bool second = false;
       if (!tc::mbar_wait_warp(&bk.tempty[a], aph ^ 1, abort_flag, p.wait_limit_ns)) break;
       tc::tc_fence_after();
       const uint32_t d_tmem = tmem + a * BT;
@@ -724,29 +735,32 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
         const uint32_t ph1 = s1 == 0 ? ph ^ 1 : ph;
         ready = tc::mbar_test(&bk.full[s1], ph1);
         tc::tc_fence_after();
+        if (kb == 0) {
+          const uint32_t shape = (uint32_t)tc::uniform((int)bk.shape[s]);
+          id0 = tc::idesc_fp4(BW, shape & 0xff, FMT == MOE_FP4_NV, 0);
+          id2 = tc::idesc_fp4(BW, shape & 0xff, FMT == MOE_FP4_NV, 2);
+          shift = shape >> 8 & 0xff;
+          second = shape >> 16;
+        }
         if (tc::elect_one()) {
-          const uint32_t sw = tc::smem_u32(smem + s * L::stage_bytes);
-          const uint64_t wd = tc::sdesc(sw, 16, 1024);
-          const uint64_t td = tc::sdesc(sw + W_BYTES, 16, 1024);
-          const uint32_t sfw = sw + W_BYTES + T_BYTES;
-          const uint32_t sft = sfw + L::sfw_bytes;
+          const uint32_t w = ring + s * (L::stage_bytes / 16);
           const uint32_t at = tmem + 2 * BT + slot * L::sf_cols;
 #pragma unroll
           for (int j = 0; j < L::atoms; ++j) {
-            tc::tmem_cp_32x128b_x4_2sm(at + 12 * j, tc::sdesc_plain(sfw + 512 * j, 0, 128));
-            tc::tmem_cp_32x128b_x4_2sm(at + 12 * j + 4, tc::sdesc_plain(sft + 512 * j, 0, 128));
+            tc::tmem_cp_32x128b_x4_2sm(at + 12 * j, tc::desc_at(dscales, w + kSfw + 32 * j));
+            tc::tmem_cp_32x128b_x4_2sm(at + 12 * j + 4, tc::desc_at(dscales, w + kSft + 32 * j));
             if (second)
               tc::tmem_cp_32x128b_x4_2sm(at + 12 * j + 8,
-                                         tc::sdesc_plain(sft + 512 * (L::atoms + j), 0, 128));
+                                         tc::desc_at(dscales, w + kSft + 32 * (L::atoms + j)));
           }
 #pragma unroll
           for (int kk = 0; kk < kKSteps; ++kk) {
             const int j = kk * L::atoms / kKSteps;  // atom of this step
             // MXFP4: two steps share an atom, two bytes of its scale words each
-            tc::umma_fp4_2sm<FMT == MOE_FP4_NV>(d_tmem, wd + 2 * kk, td + 2 * kk,
-                                               L::atoms == kKSteps || !(kk & 1) ? id0 : id2,
-                                               at + 12 * j, at + 12 * j + 4 + shift,
-                                               (kb | kk) != 0);
+            tc::umma_fp4_2sm<FMT == MOE_FP4_NV>(
+                d_tmem, tc::desc_at(dcodes, w + 2 * kk), tc::desc_at(dcodes, w + kTok + 2 * kk),
+                L::atoms == kKSteps || !(kk & 1) ? id0 : id2, at + 12 * j, at + 12 * j + 4 + shift,
+                (kb | kk) != 0);
           }
           tc::umma_commit_2sm_mc(&bk.empty[s], kPair);
           // this block's scale slot is free for the block sf_slots further

@@ -34,6 +34,13 @@ MOE_DEVINL void tma_load_5d_2sm(void *dst, const CUtensorMap *map, uint32_t bar,
       : "memory");
 }
 
+// A shared-memory descriptor whose address is `units` of 16 bytes past that of d.
+// The sum stays in the low word, so that a K block's descriptors differ from one
+// register by constants.
+MOE_DEVINL uint64_t desc_at(uint64_t d, uint32_t units) {
+  return (d & 0xffffffff00000000ull) | ((uint32_t)d + units);
+}
+
 // True in one lane of a converged warp.  Tensor-core and TMA instructions take
 // their operands from uniform registers.  Issued behind `if (elect_one())` by a warp
 // whose control flow and operands are uniform they cost far less than behind
