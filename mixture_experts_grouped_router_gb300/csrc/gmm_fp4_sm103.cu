@@ -4,7 +4,7 @@
 // (tcgen05.mma kind::mxf4nvf4.block_scale), fp32 accumulators in tensor memory.
 //
 // The product runs transposed: the weight's rows are the MMA's M (256, a pair of
-// CTAs), the expert's tokens its N, 16 to 192 in steps of 16.  An expert's last
+// CTAs), the expert's tokens its N, 16 to 256 in steps of 16.  An expert's last
 // tokens then cost what they are (a row tile of tokens would round them up to
 // 256), a single token costs N = 16, and the weights, which are what few tokens
 // wait for, fill every stage.
@@ -24,26 +24,36 @@
 //
 // Persistent; clusters of two CTAs issue 2-SM MMAs (M = 256, K = 64 codes = 32
 // bytes).  A stage is a K block of 256 codes (one 128-byte swizzle row a row): a
-// CTA's 128 weight rows 16 KB, its half of the tokens up to 12 KB (in boxes of 32
+// CTA's 128 weight rows 16 KB, its half of the tokens up to 16 KB (in boxes of 32
 // rows), and the K block's scale atoms (512 bytes of 128 rows x 4 blocks): 4
-// (NVFP4) or 2 (MXFP4) for the weight rows and twice as many for 192 tokens.
+// (NVFP4) or 2 (MXFP4) for the weight rows and twice as many for 256 tokens.
 //   warp 0     TMA producer
 //   warp 1     tensor memory, and in the leader CTA the MMA issue: the atoms
 //              to tensor memory (tcgen05.cp), then four MMAs.  A tile's shape comes
 //              from the producer with the tile's first stage
 //   warps 2-9  epilogue, two per quarter of the tensor-memory lanes, which take the
 //              tile's chunks of 32 tokens in turn (kRows: warps 2-5)
-// Tensor memory: two accumulators of 192 columns, and scale slots in the 128
-// columns that they leave: 48 columns a K block (NVFP4, 2 slots) or 24 (MXFP4,
-// 5).  A slot is rewritten after the MMAs that read it are done: their commit
-// arrives on the full barrier of the K block that takes the slot next, beside the
-// stage's copies, so that the issuer has one barrier to wait for.  That wait and
-// the issue set the pace (at 192 tokens a K block's MMAs take 384 cycles, its issue
-// some 280 and its wait 60): the next barrier is tested before a block's MMAs are
-// issued, the issuing warp stays uniform, elect_one() choosing the lane, its
-// descriptors differ by constants, and it looks up no tile (those two: 1095 -> 1046 us
-// MXFP4, 1345 -> 1222 NVFP4, 32768 rows, 4096 x 28672 with SwiGLU; two K blocks
-// an iteration were no faster).
+// Tensor memory: two accumulators of 256 columns, at 0 and at 160, that share 96.
+// The epilogue reads those first, and the next tile's products wait until it has
+// (for some 700 cycles) if either tile needs them: one tile of 256 tokens instead of two
+// of 192 and 64 saves a pass over the weights (8192 rows of 32 experts, NVFP4:
+// 7168 x 4096 133 -> 110 us) and takes longer MMAs a K block (32768 rows of 8,
+// 14336 x 4096 606 -> 546 us).  kRows: two of 192.
+// The scale slots are in the columns that they leave: 48 columns a K block (NVFP4, 2
+// slots) or 24 (MXFP4, 4).  A slot is rewritten after the MMAs that read it are
+// done: their commit arrives on the full barrier of the K block that takes the slot
+// next, beside the stage's copies, so that the issuer has one barrier to wait for.
+// That wait and the issue set the pace below 192 tokens (there a K block's MMAs take 384
+// cycles, at 256 512; its issue some 280 and its wait 60): the next barrier is
+// tested between two blocks, the issuing warp stays uniform, elect_one() choosing the
+// lane, its descriptors differ by constants, and it looks up no tile (those two:
+// 1095 -> 1046 us MXFP4, 1345 -> 1222 NVFP4, 32768 rows, 4096 x 28672 with SwiGLU;
+// two K blocks an iteration were no faster).  The epilogue hands its columns back by
+// arrivals that order no memory: releasing ones waited for its global stores (8192
+// rows of 32 experts, NVFP4: 7168 x 4096 110 -> 100 us, 2048 x 7168 90 -> 68 us).
+// At 8 experts and 32768 rows: 14336 x 4096 0.51 ms = 7.5 PFLOP/s (MXFP4), 0.53 ms = 7.3
+// (NVFP4); 4096 x 28672 with SwiGLU 1.07 and 1.14 ms (ragged groups), 7.2 and 6.7.
+// Few tokens wait for the weights: 3 or 4 each of 32 experts, 7168 x 4096 80 us, 6.2 TB/s.
 // Every wait is bounded; on time-out the CTA winds down and reports
 // MOE_ERR_TIMEOUT through dev_status.
 #include <cudaTypedefs.h>
@@ -59,11 +69,10 @@ namespace moe {
 namespace {
 
 constexpr int BW = 256;        // weight rows of a tile (the pair's M)
-constexpr int BT = 192;        // most tokens of a tile (N)
+constexpr int BT = 256;        // most tokens of a tile (N)
 constexpr int kRowBytes = 128; // one K block of a row: 256 codes
 constexpr int kKSteps = 4;     // MMAs a K block
 constexpr int W_BYTES = BW / 2 * kRowBytes;
-constexpr int T_BYTES = BT / 2 * kRowBytes;
 constexpr int kStgBytes = 4096;  // staging of an epilogue warp: one 32 x 32 fp32 block
 constexpr int kMaxE = 256;
 constexpr int kTmemCols = 512;
@@ -71,18 +80,23 @@ constexpr int kTmemCols = 512;
 // EPI: MOE_EPI_NONE, MOE_EPI_SWIGLU_FWD, or kRows (SwiGLU with tokens as M, whose
 // epilogue needs no staging).
 constexpr int kRows = 3;
+constexpr int BR = 192;        // its weight rows of a tile (N): 96 features
 
 template <int FMT, int EPI>
 struct Lay {
   static constexpr int epi_warps = EPI == kRows ? 4 : 8;
   static constexpr int threads = 64 + 32 * epi_warps;
-  static constexpr int stages = FMT == MOE_FP4_NV && EPI != kRows ? 5 : 6;
+  static constexpr int stages = EPI == kRows ? 6 : 5;
+  static constexpr int t_bytes = (EPI == kRows ? BR : BT) / 2 * kRowBytes;
   static constexpr int atoms = 256 / fp4_atom_cols(FMT);  // atom columns a K block
   static constexpr int sfw_bytes = atoms * 512;
   static constexpr int sft_bytes = 2 * sfw_bytes;
-  static constexpr int stage_bytes = (W_BYTES + T_BYTES + sfw_bytes + sft_bytes + 1023) / 1024 * 1024;
+  static constexpr int stage_bytes = (W_BYTES + t_bytes + sfw_bytes + sft_bytes + 1023) / 1024 * 1024;
   static constexpr int sf_cols = atoms * 12;               // tensor-memory columns a slot
-  static constexpr int sf_slots = (kTmemCols - 2 * BT) / sf_cols;
+  // the second accumulator's first column, and the scale slots'
+  static constexpr int acc_step = EPI == kRows ? BR : 160;
+  static constexpr int sf_base = acc_step + (EPI == kRows ? BR : BT);
+  static constexpr int sf_slots = (kTmemCols - sf_base) / sf_cols;
   static_assert(sf_slots <= stages, "a commit names a K block's next user by its stage");
   static constexpr int stg_offset = stages * stage_bytes;
   static constexpr int book_offset =
@@ -96,6 +110,7 @@ struct Book {
   uint64_t empty[kMaxStages];
   uint64_t tfull[2];
   uint64_t tempty[2];
+  uint64_t shared_read;  // the columns that both accumulators use have been read
   uint64_t drain;
   uint32_t tmem_base;
   uint32_t shape[kMaxStages];  // mma_shape of the tile that begins in the stage
@@ -135,7 +150,7 @@ struct Fp4Params {
 
 struct Maps {
   CUtensorMap w;     // weight codes
-  CUtensorMap t[3];  // token codes, boxes of 32, 64 and 96 rows
+  CUtensorMap t[4];  // token codes, boxes of 32, 64, 96 and 128 rows
   CUtensorMap sw;    // weight scale atoms
   CUtensorMap st[2]; // token scale atoms, boxes of one and two atom rows
   CUtensorMap c;     // plain output
@@ -143,8 +158,8 @@ struct Maps {
 
 struct TileInfo {
   int e, w_idx;      // expert, weight tile
-  int t0;            // first token within the group (a multiple of 192)
-  int row0, tokens;  // its row, and the tile's tokens (1 to 192)
+  int t0;            // first token within the group (a multiple of 256)
+  int row0, tokens;  // its row, and the tile's tokens (1 to 256)
   int n;             // tokens rounded up to the MMA's step of 16
 };
 
@@ -175,15 +190,10 @@ MOE_DEVINL TileInfo decode_tile(const Book &bk, const Fp4Params &p, int t) {
   return ti;
 }
 
-// The tile's first token sits in row 0 of an atom, or in row 64 (two scale
-// columns on); whether its tokens reach into a second one.
-MOE_DEVINL int scale_shift(const TileInfo &ti) { return ti.t0 & 127 ? 2 : 0; }
-MOE_DEVINL bool second_atom(const TileInfo &ti) { return scale_shift(ti) * 32 + ti.n > 128; }
-
 // A tile's MMAs as the producer hands them to the issuing warp: N, the scale
 // column that the tokens start in, whether they reach into a second atom.
 MOE_DEVINL uint32_t mma_shape(int n, int shift, bool second) {
-  return (uint32_t)n | (uint32_t)shift << 8 | (uint32_t)second << 16;
+  return (uint32_t)n | (uint32_t)shift << 16 | (uint32_t)second << 24;
 }
 
 // ---------------------------------------------------------------- epilogue
@@ -243,6 +253,34 @@ MOE_DEVINL bool pair_agree(bool ok, int pair) {
   return r != 0;
 }
 
+// A warp's chunks of 32 tokens, every other one, those of the columns that the two
+// accumulators share first: the last ones of the lower accumulator (a = 0), the first
+// ones of the upper.  Its first two are loaded together, after which the next tile's
+// products may take the shared columns; then one is always on its way.
+struct Chunks {
+  uint32_t taddr;
+  int n, a;  // chunks of the tile, accumulator
+  uint32_t cur[32], nxt[32];
+
+  MOE_DEVINL int at(int i) const { return a ? i : n - 1 - i; }
+  MOE_DEVINL void begin(int sub, uint32_t shared_read, int lane) {
+    if (sub < n) tc::tmem_ld32_issue(taddr + at(sub) * 32, cur);
+    if (sub + 2 < n) tc::tmem_ld32_issue(taddr + at(sub + 2) * 32, nxt);
+    tc::tmem_wait_ld(cur);
+    tc::reg_after(nxt);
+    tc::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive_cluster_relaxed(shared_read);
+  }
+  // after chunk i's values have been taken
+  MOE_DEVINL void advance(int i) {
+    tc::tmem_wait_ld(nxt);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) cur[j] = nxt[j];
+    if (i + 4 < n) tc::tmem_ld32_issue(taddr + at(i + 4) * 32, nxt);
+  }
+};
+
 // SwiGLU: warp q holds the gates (q even) or ups (q odd) of 32 features for the
 // tile's tokens.  A chunk of 32 tokens goes through the two warps' staging; a
 // thread then has one token's gates and ups of 16 features, which are a block of
@@ -251,7 +289,7 @@ MOE_DEVINL bool pair_agree(bool ok, int pair) {
 // reciprocal decides as the quotient would.
 template <int FMT>
 MOE_DEVINL void epilogue_swiglu(const Book &bk, const Fp4Params &p, const TileInfo &ti, float sc,
-                                float g2, float inv6, uint32_t taddr, int crank, int q, int sub,
+                                float g2, float inv6, Chunks &ch, int crank, int q, int sub,
                                 int lane, uint8_t *stg_pair) {
   const int F = p.F;
   // the pair of warps' 32 features
@@ -260,21 +298,17 @@ MOE_DEVINL void epilogue_swiglu(const Book &bk, const Fp4Params &p, const TileIn
   const int pair = 2 * sub + (q >> 1);
   const int tok = (q & 1) * 16 + (lane >> 1), h = lane & 1;
   const int fh = f0 + 16 * h;  // this thread's features
-  if (sub * 32 >= ti.tokens) return;
-  uint32_t r[32];
-  tc::tmem_ld32_issue(taddr + sub * 32, r);
 #pragma unroll 1
-  for (int c = sub; c * 32 < ti.tokens; c += 2) {
+  for (int i = sub; i < ch.n; i += 2) {
+    const int c = ch.at(i);
     {
       float v[32];
-      tc::tmem_wait_ld(r);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * sc;
-      if (c > sub) pair_sync(pair);  // both warps are done with the last chunk
+      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(ch.cur[j]) * sc;
+      if (i > sub) pair_sync(pair);  // both warps are done with the last chunk
       stage_f32_t(stg_pair + (q & 1) * kStgBytes, lane, v);
     }
-    // the next chunk's values on their way while this one is worked on
-    if ((c + 2) * 32 < ti.tokens) tc::tmem_ld32_issue(taddr + (c + 2) * 32, r);
+    ch.advance(i);
     pair_sync(pair);
     float g[16], u[16];
     unstage_f32_16(stg_pair, tok, h, g);
@@ -322,24 +356,25 @@ MOE_DEVINL void epilogue_swiglu(const Book &bk, const Fp4Params &p, const TileIn
 }
 
 // Plain: warp q holds 32 output columns of the tile's tokens.
-MOE_DEVINL void epilogue_plain(const Fp4Params &p, const TileInfo &ti, float sc, uint32_t taddr,
+MOE_DEVINL void epilogue_plain(const Fp4Params &p, const TileInfo &ti, float sc, Chunks &ch,
                                int crank, int q, int sub, int lane, uint8_t *stg,
                                const CUtensorMap *m0) {
   const int nc = ti.w_idx * BW + crank * (BW / 2) + q * 32;
   if (nc >= p.N) return;
 #pragma unroll 1
-  for (int c = sub; c * 32 < ti.tokens; c += 2) {
+  for (int i = sub; i < ch.n; i += 2) {
+    const int c = ch.at(i);
     float v[32];
-    tc::tmem_ld32(taddr + c * 32, v);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] *= sc;
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(ch.cur[j]) * sc;
+    ch.advance(i);
     const int left = ti.tokens - c * 32;  // rows of this block that are the tile's
     const int r0 = ti.row0 + c * 32;
     // bf16 blocks take the staging's halves in turn (from the first one on, once
     // the last tile's stores have read them), fp32 ones all of it
-    uint8_t *buf = p.c_f32 ? stg : stg + (c >> 1 & 1) * 2048;
+    uint8_t *buf = p.c_f32 ? stg : stg + (i >> 1 & 1) * 2048;
     if (lane == 0) {
-      if (p.c_f32 || c == sub) tc::bulk_wait_read0();
+      if (p.c_f32 || i == sub) tc::bulk_wait_read0();
       else tc::bulk_wait_read<1>();
     }
     __syncwarp();
@@ -361,12 +396,12 @@ MOE_DEVINL void epilogue_plain(const Fp4Params &p, const TileInfo &ti, float sc,
       uint8_t *o = static_cast<uint8_t *>(p.C) +
                    ((int64_t)(r0 + first) * p.ldc + nc) * es + k * 16;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = first + i * step;
+      for (int x = 0; x < 8; ++x) {
+        const int r = first + x * step;
         if (r < left && in) {
           const int at =
               p.c_f32 ? r * 128 + ((k ^ (r & 7)) << 4) : r * 64 + ((k ^ ((r >> 1) & 3)) << 4);
-          st_v4(o + (int64_t)i * step * p.ldc * es, *reinterpret_cast<const uint4 *>(buf + at));
+          st_v4(o + (int64_t)x * step * p.ldc * es, *reinterpret_cast<const uint4 *>(buf + at));
         }
       }
       __syncwarp();
@@ -378,8 +413,6 @@ MOE_DEVINL void epilogue_plain(const Fp4Params &p, const TileInfo &ti, float sc,
 // The same pipeline with the roles exchanged: a CTA's 128 tokens are its share of
 // M, the pair's 192 weight rows N, 96 to a CTA, alternating gates and ups in blocks
 // of 32.  A tile of 192 rows starts in row 0 or 64 of its scale atoms.
-constexpr int BR = 192;  // weight rows of a tile: 96 features
-
 struct RowTile {
   int e, m_idx, n_idx, row0, row_end;
 };
@@ -521,6 +554,7 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
       tc::mbar_init(&bk.tfull[a], 1);
       tc::mbar_init(&bk.tempty[a], 2 * L::epi_warps);
     }
+    tc::mbar_init(&bk.shared_read, 2 * L::epi_warps);
     tc::mbar_init(&bk.drain, 1);
     bk.abort_flag = 0;
     tc::fence_mbar_init();
@@ -598,7 +632,7 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
         // a CTA past the expert's rows loads none: its products are not stored
         const bool own = ti.row0 < ti.row_end;
         const bool both = ti.row0 + (1 - 2 * crank) * 128 < ti.row_end;  // the other CTA's
-        const int tx = (own + both) * (W_BYTES + L::sfw_bytes) + 2 * (T_BYTES + L::sft_bytes);
+        const int tx = (own + both) * (W_BYTES + L::sfw_bytes) + 2 * (L::t_bytes + L::sft_bytes);
         for (int kb = 0; kb < p.kblocks; ++kb) {
           if (!tc::mbar_wait_warp(&bk.empty[s], ph ^ 1, abort_flag, p.wait_limit_ns)) {
             ok = false;
@@ -613,8 +647,8 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
             }
             const int k = kb * kRowBytes;
             if (own) {
-              tc::tma_load_2d_2sm(st, &m.t[0], fb, k, ti.row0);
-              tc::tma_load_3d_2sm(st + W_BYTES + T_BYTES, &m.st[0], fb, 0, kb * L::atoms, tok_sf);
+              tc::tma_load_2d_2sm(st, &m.t[3], fb, k, ti.row0);
+              tc::tma_load_3d_2sm(st + W_BYTES + L::t_bytes, &m.st[0], fb, 0, kb * L::atoms, tok_sf);
             }
 #pragma unroll
             for (int i = 0; i < 3; ++i) {  // three of the tile's six blocks of 32 rows
@@ -622,7 +656,7 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
               tc::tma_load_5d_2sm(st + W_BYTES + i * 4096, &m.w, fb, k, 0, b & 1,
                                   3 * ti.n_idx + (b >> 1), ti.e);
             }
-            tc::tma_load_3d_2sm(st + W_BYTES + T_BYTES + L::sfw_bytes, &m.sw, fb, 0,
+            tc::tma_load_3d_2sm(st + W_BYTES + L::t_bytes + L::sfw_bytes, &m.sw, fb, 0,
                                 kb * L::atoms, wgt_sf);
           }
           __syncwarp();
@@ -636,10 +670,10 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
       int done = 0;  // K blocks of the first tile that are issued
       for (int t = cid; t < total && ok && EPI != kRows; t += ncl) {
         const TileInfo ti = decode_tile(bk, p, t);
-        // this CTA's half of the tokens, rounded up to 32 rows; their scale atoms
+        // this CTA's half of the tokens, rounded up to 32 rows
         const int trow = ti.row0 + crank * (ti.n / 2);
         const int tbox = (ti.n / 2 + 31) / 32;
-        const int sbox = second_atom(ti) ? 2 : 1;
+        const int sbox = ti.n > 128 ? 2 : 1;  // their scale atoms
         const int trow_sf = (int)bk.poff[ti.e] + (ti.t0 >> 7);
         const int wrow_sf = ti.e * p.w_atoms + 2 * ti.w_idx + crank;
         const int tx = 2 * (W_BYTES + tbox * 4096 + (1 + sbox) * L::sfw_bytes);  // the pair's
@@ -647,7 +681,7 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
           uint8_t *sw = smem + st * L::stage_bytes;
           const uint32_t fb = tc::mapa_shared(tc::smem_u32(&bk.full[st]), 0);
           if (leader) {
-            if (kb == 0) bk.shape[st] = mma_shape(ti.n, scale_shift(ti), second_atom(ti));
+            if (kb == 0) bk.shape[st] = mma_shape(ti.n, 0, ti.n > 128);
             tc::mbar_expect_tx(&bk.full[st], tx);
           }
           const int k = kb * kRowBytes;
@@ -655,13 +689,13 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
             tc::tma_load_5d_2sm(sw, &m.w, fb, k, 0, 0, 4 * ti.w_idx + 2 * crank, ti.e);
           else
             tc::tma_load_3d_2sm(sw, &m.w, fb, k, ti.w_idx * BW + crank * (BW / 2), ti.e);
-          tc::tma_load_3d_2sm(sw + W_BYTES + T_BYTES, &m.sw, fb, 0, kb * L::atoms, wrow_sf);
+          tc::tma_load_3d_2sm(sw + W_BYTES + L::t_bytes, &m.sw, fb, 0, kb * L::atoms, wrow_sf);
         };
         auto load_tokens = [&](int st, int kb) {
           uint8_t *sw = smem + st * L::stage_bytes;
           const uint32_t fb = tc::mapa_shared(tc::smem_u32(&bk.full[st]), 0);
           tc::tma_load_2d_2sm(sw + W_BYTES, &m.t[tbox - 1], fb, kb * kRowBytes, trow);
-          tc::tma_load_3d_2sm(sw + W_BYTES + T_BYTES + L::sfw_bytes, &m.st[sbox - 1], fb, 0,
+          tc::tma_load_3d_2sm(sw + W_BYTES + L::t_bytes + L::sfw_bytes, &m.st[sbox - 1], fb, 0,
                               kb * L::atoms, trow_sf);
         };
         if (early && t == cid) {
@@ -703,6 +737,7 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
     }
   } else if (warp == 1 && leader) {
     uint32_t acc_it = 0;
+    int before = 0;     // N of the tile before
     int s = 0;          // ring slot of the next K block
     uint32_t ph = 0;
     int slot = 0;       // its scale slot
@@ -711,7 +746,7 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
     // descriptors of codes and scales at address 0, and the ring in their units
     const uint64_t dcodes = tc::sdesc(0, 16, 1024), dscales = tc::sdesc_plain(0, 0, 128);
     const uint32_t ring = (uint32_t)tc::uniform((int)(tc::smem_u32(smem) >> 4));
-    constexpr uint32_t kTok = W_BYTES / 16, kSfw = kTok + T_BYTES / 16,
+    constexpr uint32_t kTok = W_BYTES / 16, kSfw = kTok + L::t_bytes / 16,
                        kSft = kSfw + L::sfw_bytes / 16;
     // the first K blocks find their scale slots free
     if (tc::elect_one())
@@ -724,7 +759,7 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
       bool second = false;
       if (!tc::mbar_wait_warp(&bk.tempty[a], aph ^ 1, abort_flag, p.wait_limit_ns)) break;
       tc::tc_fence_after();
-      const uint32_t d_tmem = tmem + a * BT;
+      const uint32_t d_tmem = tmem + a * L::acc_step;
       for (int kb = 0; kb < p.kblocks; ++kb) {
         if (!__all_sync(0xffffffffu, ready) &&
             !tc::mbar_wait_warp(&bk.full[s], ph, abort_flag, p.wait_limit_ns)) {
@@ -733,18 +768,26 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
         }
         const int s1 = s + 1 == kStages ? 0 : s + 1;
         const uint32_t ph1 = s1 == 0 ? ph ^ 1 : ph;
-        ready = tc::mbar_test(&bk.full[s1], ph1);
         tc::tc_fence_after();
         if (kb == 0) {
           const uint32_t shape = (uint32_t)tc::uniform((int)bk.shape[s]);
-          id0 = tc::idesc_fp4(BW, shape & 0xff, FMT == MOE_FP4_NV, 0);
-          id2 = tc::idesc_fp4(BW, shape & 0xff, FMT == MOE_FP4_NV, 2);
-          shift = shape >> 8 & 0xff;
-          second = shape >> 16;
+          const int n = shape & 0xffff;
+          id0 = tc::idesc_fp4(BW, n, FMT == MOE_FP4_NV, 0);
+          id2 = tc::idesc_fp4(BW, n, FMT == MOE_FP4_NV, 2);
+          shift = shape >> 16 & 0xff;
+          second = shape >> 24;
+          // where this tile and the one before share columns, those have to be read
+          if (EPI != kRows && acc_it > 0 && (a ? before : n) > L::acc_step) {
+            ok = tc::mbar_wait_warp(&bk.shared_read, (acc_it - 1) & 1, abort_flag,
+                                    p.wait_limit_ns);
+            if (!ok) break;
+            tc::tc_fence_after();
+          }
+          before = n;
         }
         if (tc::elect_one()) {
           const uint32_t w = ring + s * (L::stage_bytes / 16);
-          const uint32_t at = tmem + 2 * BT + slot * L::sf_cols;
+          const uint32_t at = tmem + L::sf_base + slot * L::sf_cols;
 #pragma unroll
           for (int j = 0; j < L::atoms; ++j) {
             tc::tmem_cp_32x128b_x4_2sm(at + 12 * j, tc::desc_at(dscales, w + kSfw + 32 * j));
@@ -768,6 +811,7 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
           tc::umma_commit_2sm_mc(&bk.full[sn < kStages ? sn : sn - kStages], 0x1);
         }
         __syncwarp();
+        ready = tc::mbar_test(&bk.full[s1], ph1);
         if (++slot == L::sf_slots) slot = 0;
         s = s1;
         ph = ph1;
@@ -801,18 +845,25 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
       if (EPI == MOE_EPI_SWIGLU_FWD) go = pair_agree(go, 2 * sub + (q >> 1));
       if (!go) break;
       tc::tc_fence_after();
-      const uint32_t taddr = tmem + a * BT + (static_cast<uint32_t>(q * 32) << 16);
-      if (EPI == kRows)
+      const uint32_t taddr = tmem + a * L::acc_step + (static_cast<uint32_t>(q * 32) << 16);
+      if (EPI == kRows) {
         epilogue_rows<FMT>(bk, p, rt, sc, g2, inv6, taddr, q, sub, L::epi_warps / 4, lane);
-      else if (EPI == MOE_EPI_SWIGLU_FWD)
-        epilogue_swiglu<FMT>(bk, p, ti, sc, g2, inv6, taddr, crank, q, sub, lane,
-                             stg + (2 * sub + (q >> 1)) * 2 * kStgBytes);
-      else
-        epilogue_plain(p, ti, sc, taddr, crank, q, sub, lane, stg + (4 * sub + q) * kStgBytes,
-                       &m.c);
+      } else {
+        Chunks ch;
+        ch.taddr = taddr;
+        ch.n = (ti.tokens + 31) / 32;
+        ch.a = a;
+        ch.begin(sub, tc::mapa_shared(tc::smem_u32(&bk.shared_read), 0), lane);
+        if (EPI == MOE_EPI_SWIGLU_FWD)
+          epilogue_swiglu<FMT>(bk, p, ti, sc, g2, inv6, ch, crank, q, sub, lane,
+                               stg + (2 * sub + (q >> 1)) * 2 * kStgBytes);
+        else
+          epilogue_plain(p, ti, sc, ch, crank, q, sub, lane, stg + (4 * sub + q) * kStgBytes,
+                         &m.c);
+      }
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&bk.tempty[a]), 0));
+      if (lane == 0) tc::mbar_arrive_cluster_relaxed(tc::mapa_shared(tc::smem_u32(&bk.tempty[a]), 0));
       ++acc_it;
     }
     if (lane == 0) tc::bulk_wait0();
@@ -928,12 +979,16 @@ moe_status_t launch(const Maps &m, const Fp4Params &p, int64_t tiles_upper,
 
 }  // namespace
 
-// SwiGLU with tokens as M (kRows): from so many rows an expert on, where K is short
-// enough for the turned epilogue to be what a tile waits for.  MXFP4, us with
-// tokens / weights as M:  8 experts of 4096 x 28672, rows an expert 512: 208 / 200,
-// 1024: 329 / 364, 2048: 603 / 650, 4096: 1106 / 1270;  32 of 7168 x 4096, 512: 194 /
-// 181, 1024: 327 / 318, 2048: 587 / 565.  NVFP4 likewise (1024: 388 / 420, 382 / 389).
-constexpr int kRowsFrom = 1024, kRowsMaxK = 5120;
+// SwiGLU with tokens as M (kRows): where K is so short that the turned epilogue (some
+// 9000 cycles a tile of 256 tokens) is what a tile waits for, from as many rows an
+// expert on as fill its tile of 256 tokens.  us with tokens / weights as M, ragged
+// groups:
+//   16 experts of 1024 x 4096, MXFP4, 128 rows each 19.3 / 17.9, 256: 24.4 / 27.7,
+//     1024: 61.7 / 70.3, 4096: 207 / 244;  NVFP4, 256: 29.6 / 36.0, 4096: 252 / 284
+//   of 2560 x 8192, MXFP4, 192: 42.2 / 41.1, 256: 51.0 / 55.4, 4096: 439 / 501
+//   of 3584 x 8192, MXFP4, 256: 65.2 / 62.0, 1024: 169 / 159, 4096: 561 / 546
+//   8 of 4096 x 28672, MXFP4, 512: 183 / 165, 4096: 1097 / 1071
+constexpr int kRowsFrom = 256, kRowsMaxK = 2816;
 
 moe_status_t launch_gmm_fp4(const GmmFp4Args &a, cudaStream_t s) {
   const bool swiglu = a.epilogue == MOE_EPI_SWIGLU_FWD;
@@ -971,13 +1026,15 @@ moe_status_t launch_gmm_fp4(const GmmFp4Args &a, cudaStream_t s) {
   const int64_t stride_b = a.E > 1 ? a.stride_b : (int64_t)a.N * a.ldb;
   bool ok = make_scale_map(&m.sw, a.sfb, ac, (int64_t)a.E * p.w_atoms, atoms, 1) &&
             make_scale_map(&m.st[0], a.sfa, ac, p.atom_rows2, atoms, 1) &&
-            make_scale_map(&m.st[1], a.sfa, ac, p.atom_rows2, atoms, 2);
-  for (int i = 0; i < 3; ++i)
+            (rows || a.rows_cap <= 128 ||
+             make_scale_map(&m.st[1], a.sfa, ac, p.atom_rows2, atoms, 2));
+  // the boxes that a tile of at most rows_cap tokens can need (an encoding takes the
+  // host about as long as a launch)
+  const int boxes = (int)(std::min<int64_t>((a.rows_cap + 15) / 16 * 16, BT) + 63) / 64;
+  for (int i = rows ? 3 : 0; i < (rows ? 4 : boxes); ++i)
     ok = ok && make_code_map(&m.t[i], a.A, 2, a.K / 2, a.rows_cap, a.lda, 1, 0, 32 * (i + 1));
-  if (rows) {  // tokens in boxes of 128, weights of 32 rows, their atoms two rows
-    ok = ok && make_code_map(&m.t[0], a.A, 2, a.K / 2, a.rows_cap, a.lda, 1, 0, 128) &&
-         make_scale_map(&m.sw, a.sfb, ac, (int64_t)a.E * p.w_atoms, atoms, 2);
-  }
+  if (rows)  // weights in boxes of 32 rows, their atoms two rows
+    ok = ok && make_scale_map(&m.sw, a.sfb, ac, (int64_t)a.E * p.w_atoms, atoms, 2);
   if (swiglu) {
     // [E][F / 32][gate, up][32] rows: a box takes two blocks of 32 gates and 32 ups
     const uint64_t dims[5] = {(uint64_t)a.K / 2, 32, 2, (uint64_t)p.F / 32, (uint64_t)a.E};

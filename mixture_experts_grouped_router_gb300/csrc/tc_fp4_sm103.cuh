@@ -24,6 +24,14 @@ MOE_DEVINL void mbar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// One arrival on a barrier of the cluster that orders no memory: what it hands over
+// are tensor-memory columns, whose reads tcgen05.wait::ld and the fence before it
+// have ended.  A releasing arrival would also wait for the warp's global stores,
+// some 2000 cycles.
+MOE_DEVINL void mbar_arrive_cluster_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // tma_load_3d_2sm for five dimensions.
 MOE_DEVINL void tma_load_5d_2sm(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1,
                                 int c2, int c3, int c4) {
