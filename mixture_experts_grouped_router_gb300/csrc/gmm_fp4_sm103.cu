@@ -668,8 +668,11 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
         }
       }
       int done = 0;  // K blocks of the first tile that are issued
+      TileInfo next;
+      if (EPI != kRows && cid < total) next = decode_tile(bk, p, cid);
       for (int t = cid; t < total && ok && EPI != kRows; t += ncl) {
-        const TileInfo ti = decode_tile(bk, p, t);
+        const TileInfo ti = next;
+        bool looked = t + ncl >= total;  // the next tile is looked up between copies
         // this CTA's half of the tokens, rounded up to 32 rows
         const int trow = ti.row0 + crank * (ti.n / 2);
         const int tbox = (ti.n / 2 + 31) / 32;
@@ -727,7 +730,10 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
             s = 0;
             ph ^= 1;
           }
+          if (!looked) next = decode_tile(bk, p, t + ncl);
+          looked = true;
         }
+        if (!looked) next = decode_tile(bk, p, t + ncl);
       }
       // every issued copy has landed before the CTA may exit (both CTAs' copies
       // complete on the leader's barriers)
