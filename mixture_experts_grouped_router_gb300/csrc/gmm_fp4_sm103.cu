@@ -158,7 +158,7 @@ struct Maps {
 
 struct TileInfo {
   int e, w_idx;      // expert, weight tile
-  int t0;            // first token within the group (a multiple of 256)
+  int t0;            // first token within the group (a multiple of 64)
   int row0, tokens;  // its row, and the tile's tokens (1 to 256)
   int n;             // tokens rounded up to the MMA's step of 16
 };
@@ -168,7 +168,9 @@ MOE_DEVINL int group_offset(const Fp4Params &p, int e) {
 }
 
 // Tile t: an expert's token tiles follow one another under one weight tile, so
-// that the pairs that run at a time share its rows in L2.
+// that the pairs that run at a time share its rows in L2.  They are as few as can be
+// and of like size, in steps of 64 tokens: 192 and up to 192 rather than 256 and up
+// to 128 (the scale atoms of their tokens then start in row 0 or in row 64).
 MOE_DEVINL TileInfo decode_tile(const Book &bk, const Fp4Params &p, int t) {
   int lo = 0, hi = p.E - 1;
   while (lo < hi) {
@@ -182,13 +184,19 @@ MOE_DEVINL TileInfo decode_tile(const Book &bk, const Fp4Params &p, int t) {
   const int size = tc::uniform(max(bk.off[ti.e + 1], off)) - off;
   const int local = t - tc::uniform(bk.cum[ti.e]);
   const int tt = (size + BT - 1) / BT;
+  const int step = ((size + tt - 1) / tt + 63) & ~63;
   ti.w_idx = local / tt;
-  ti.t0 = (local - ti.w_idx * tt) * BT;
+  ti.t0 = (local - ti.w_idx * tt) * step;
   ti.row0 = off + ti.t0;
-  ti.tokens = min(size - ti.t0, BT);
+  ti.tokens = min(size - ti.t0, step);
   ti.n = (ti.tokens + 15) / 16 * 16;
   return ti;
 }
+
+// The tile's first token sits in row 0 of an atom, or in row 64 (two scale
+// columns on); whether its tokens reach into a second one.
+MOE_DEVINL int scale_shift(const TileInfo &ti) { return ti.t0 & 127 ? 2 : 0; }
+MOE_DEVINL bool second_atom(const TileInfo &ti) { return scale_shift(ti) * 32 + ti.n > 128; }
 
 // A tile's MMAs as the producer hands them to the issuing warp: N, the scale
 // column that the tokens start in, whether they reach into a second atom.
@@ -676,7 +684,7 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
         // this CTA's half of the tokens, rounded up to 32 rows
         const int trow = ti.row0 + crank * (ti.n / 2);
         const int tbox = (ti.n / 2 + 31) / 32;
-        const int sbox = ti.n > 128 ? 2 : 1;  // their scale atoms
+        const int sbox = second_atom(ti) ? 2 : 1;  // their scale atoms
         const int trow_sf = (int)bk.poff[ti.e] + (ti.t0 >> 7);
         const int wrow_sf = ti.e * p.w_atoms + 2 * ti.w_idx + crank;
         const int tx = 2 * (W_BYTES + tbox * 4096 + (1 + sbox) * L::sfw_bytes);  // the pair's
@@ -684,7 +692,7 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
           uint8_t *sw = smem + st * L::stage_bytes;
           const uint32_t fb = tc::mapa_shared(tc::smem_u32(&bk.full[st]), 0);
           if (leader) {
-            if (kb == 0) bk.shape[st] = mma_shape(ti.n, 0, ti.n > 128);
+            if (kb == 0) bk.shape[st] = mma_shape(ti.n, scale_shift(ti), second_atom(ti));
             tc::mbar_expect_tx(&bk.full[st], tx);
           }
           const int k = kb * kRowBytes;
