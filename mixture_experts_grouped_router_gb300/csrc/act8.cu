@@ -40,26 +40,27 @@ constexpr float kInv127 = 1.0f / 127.0f;
 
 // The block's scale as bf16 bits, and 1 / s (0 where the codes are 0), from
 // the block's largest magnitude (bf16 bits).
-MOE_DEVINL uint32_t act8_scale(uint32_t amax, float &s, float &inv) {
-  s = 1.0f;
+MOE_DEVINL uint32_t act8_scale(uint32_t amax, float &inv) {
   inv = 0.0f;
   if (amax >= 0x7F80u) return 0x7FC0u;
   const float a = __uint_as_float(amax << 16);
   if (a < 7.888609052e-31f) return 0u;  // 2^-100
   const float t = div_exact(a, 127.0f, kInv127);
   const uint32_t bits = (__float_as_uint(t) + 0xFFFFu) >> 16;
-  s = __uint_as_float(bits << 16);
-  inv = rcp_approx(s);
+  inv = rcp_approx(__uint_as_float(bits << 16));
   return bits;
 }
 
-// 4 values -> 4 signed bytes, each rounded to the nearest even integer: adding
-// 1.5 * 2^23 leaves the integer in the low bits of the sum.
-MOE_DEVINL uint32_t act8_codes4(const float *v, uint64_t minus_s, uint64_t inv) {
-  const uint64_t magic = pack2(12582912.0f, 12582912.0f);
+// 4 values -> 4 signed bytes, each rounded to the nearest even integer: a sum of
+// 1.5 * 2^23 and the quotient leaves the integer in its low bits.  The quotient comes
+// with 768 added, where floats are 2^-14 apart: ties up to 126.5 are met within
+// 126.5 2^-23, and a bf16 x over a bf16 s is a tie or 2^-10 from one.
+MOE_DEVINL uint32_t act8_codes4(const float *v, uint64_t inv) {
+  const uint64_t grid = pack2(768.0f, 768.0f);
+  const uint64_t magic = pack2(12582912.0f - 768.0f, 12582912.0f - 768.0f);
   float b[4];
-  unpack2(add2(div_exact2(pack2(v[0], v[1]), minus_s, inv), magic), b[0], b[1]);
-  unpack2(add2(div_exact2(pack2(v[2], v[3]), minus_s, inv), magic), b[2], b[3]);
+  unpack2(add2(snap2(pack2(v[0], v[1]), inv, grid), magic), b[0], b[1]);
+  unpack2(add2(snap2(pack2(v[2], v[3]), inv, grid), magic), b[2], b[3]);
   return __byte_perm(__byte_perm(__float_as_uint(b[0]), __float_as_uint(b[1]), 0x0040),
                      __byte_perm(__float_as_uint(b[2]), __float_as_uint(b[3]), 0x0040), 0x5410);
 }
@@ -69,11 +70,11 @@ MOE_DEVINL uint2 act8_quantize8(const uint4 &w, uint32_t &sbits) {
   uint32_t a = amax_bits8(w);
   a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
   a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-  float s, inv, v[8];
-  sbits = act8_scale(a, s, inv);
+  float inv, v[8];
+  sbits = act8_scale(a, inv);
   bf16x8_to_f32(w, v);
-  const uint64_t inv2 = pack2(inv, inv), ms2 = pack2(-s, -s);
-  const uint2 q = make_uint2(act8_codes4(v, ms2, inv2), act8_codes4(v + 4, ms2, inv2));
+  const uint64_t inv2 = pack2(inv, inv);
+  const uint2 q = make_uint2(act8_codes4(v, inv2), act8_codes4(v + 4, inv2));
   return sbits == 0x7FC0u ? make_uint2(0u, 0u) : q;  // (a NaN's code is no number)
 }
 

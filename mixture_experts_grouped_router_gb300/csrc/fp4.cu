@@ -141,11 +141,11 @@ MOE_DEVINL void quantize_piece(const uint4 *w, int c0, int cols, int lane, float
     uint32_t a = amax_bits8(w[i]);
     a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
     if (FMT != MOE_FP4_NV) a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-    float t, inv, v[8];
+    float inv, v[8];
     const uint32_t code =
-        fp4_block_scale<FMT>(__uint_as_float(a << 16), g, 6.0f * g, inv6, t, inv);
+        fp4_block_scale<FMT>(__uint_as_float(a << 16), g, 6.0f * g, inv6, inv);
     bf16x8_to_f32(w[i], v);
-    codes[i] = fp4_codes8<FMT>(v, t, inv);
+    codes[i] = fp4_codes8<FMT>(v, inv);
     words[i] = scale_word<FMT>(c < cols ? code : 0u, lane);
   }
 }
@@ -396,15 +396,15 @@ fp4_quantize_weights_kernel(const uint16_t *__restrict__ w, int K, int N, int ro
     uint32_t a = 0;
 #pragma unroll
     for (int j = 0; j < kB; ++j) a = max(a, (uint32_t)tile[kb + b * kB + j][nn] & 0x7FFFu);
-    float t, inv, v[kB];
+    float inv, v[kB];
     const uint32_t code = fp4_block_scale<FMT>(__uint_as_float(a << 16), g, 6.0f * g,
-                                               __frcp_rn(6.0f * g), t, inv);
+                                               __frcp_rn(6.0f * g), inv);
 #pragma unroll
     for (int j = 0; j < kB; ++j)
       v[j] = __uint_as_float((uint32_t)tile[kb + b * kB + j][nn] << 16);
 #pragma unroll
     for (int j = 0; j < kB / 8; ++j)
-      codes[b * (kB / 8) + j] = fp4_codes8<FMT>(v + 8 * j, t, inv);
+      codes[b * (kB / 8) + j] = fp4_codes8<FMT>(v + 8 * j, inv);
     const int blk = k / kB + b;
     if (blk < 4 * ac) sf[fp4_scale_byte(pr, blk, ac)] = k < K ? (uint8_t)code : (uint8_t)0;
   }

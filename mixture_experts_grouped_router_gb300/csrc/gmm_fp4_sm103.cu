@@ -342,8 +342,8 @@ MOE_DEVINL void epilogue_swiglu(const Book &bk, const Fp4Params &p, const TileIn
     }
     if (!finite) a = __uint_as_float(0x7F800000u);
     if (FMT != MOE_FP4_NV) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    float td, inv;
-    const uint32_t scale = fp4_block_scale<FMT>(a, g2, 6.0f * g2, inv6, td, inv);
+    float inv;
+    const uint32_t scale = fp4_block_scale<FMT>(a, g2, 6.0f * g2, inv6, inv);
 #pragma unroll
     for (int j = 0; j < 16; ++j) g[j] *= inv;
     const uint32_t lo = inv == 0.0f ? 0u : cvt_e2m1x8(g);
@@ -467,8 +467,8 @@ MOE_DEVINL uint4 quantize_chunk(float *v, float g, float inv6, uint32_t &scale) 
       finite &= m <= 3.402823466e38f;
       a = fmaxf(a, m);
     }
-    float t, inv;
-    scale |= fp4_block_scale<FMT>(finite ? a : __uint_as_float(0x7F800000u), g, 6.0f * g, inv6, t,
+    float inv;
+    scale |= fp4_block_scale<FMT>(finite ? a : __uint_as_float(0x7F800000u), g, 6.0f * g, inv6,
                                   inv)
              << (8 * b);
 #pragma unroll

@@ -36,7 +36,7 @@ MOE_DEVINL uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-// 1 / t to within a bit (t a normal float); div_exact corrects what it costs.
+// 1 / t to within a bit, 2^-23 of it (t a normal float).
 MOE_DEVINL float rcp_approx(float t) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
@@ -51,10 +51,12 @@ MOE_DEVINL float div_exact(float x, float t, float inv) {
   return fmaf(fmaf(-q, t, x), inv, q);
 }
 
-MOE_DEVINL uint64_t div_exact2(uint64_t x, uint64_t minus_t, uint64_t inv) {
-  const uint64_t q = mul2(x, inv);
-  return fma2(fma2(q, minus_t, x), inv, q);
-}
+// Quotients on the way to codes: x * inv (inv within 2^-23 of 1 / t) rounded to a
+// multiple of the spacing of floats near `grid`, which is added for that; the
+// result is that much too large.  A tie of the code grid lies on a multiple and the
+// product within half a spacing of it, so that ties are met exactly; a quotient
+// beside a tie is further from it, as x and t have few bits.
+MOE_DEVINL uint64_t snap2(uint64_t x, uint64_t inv, uint64_t grid) { return fma2(x, inv, grid); }
 
 // Elements per scale of a 4-bit format, and columns per 512-byte scale atom
 // (128 rows x 4 blocks).
@@ -124,26 +126,20 @@ MOE_DEVINL float fp4_scale_value(uint32_t code, int fmt) {
   return fmt == MOE_FP4_NV ? e4m3_value(code) : e8m0_value(code);
 }
 
-// Scale code of a block with largest magnitude a, and the reciprocal pair that
-// divides its elements: t is the block's scale (times g for NVFP4), inv = 1/t,
-// or 0 where every code of the block is 0 (no magnitude, or a NaN / infinity,
-// which takes the NaN scale).
+// Scale code of a block with largest magnitude a, and the reciprocal inv of its
+// scale (times g for NVFP4), or 0 where every code of the block is 0 (no magnitude,
+// or a NaN / infinity, which takes the NaN scale).
 //   MXFP4: t = 2^s, s = floor(log2 a) - 2 clamped to [-127, 127] (OCP MX v1.0)
 //   NVFP4: E4M3(a / (6 g)), g the tensor's fp32 scale; g6 = 6 g, inv6 = 1 / g6
 template <int FMT>
-MOE_DEVINL uint32_t fp4_block_scale(float a, float g, float g6, float inv6, float &t,
-                                    float &inv) {
-  t = 1.0f;
+MOE_DEVINL uint32_t fp4_block_scale(float a, float g, float g6, float inv6, float &inv) {
   inv = 0.0f;
   const bool finite = a <= 3.402823466e38f;
   if (FMT == MOE_FP4_NV) {
     if (!finite) return 0x7Fu;
     const uint32_t code = e4m3_code(div_exact(a, g6, inv6));
     const float s = e4m3_value(code) * g;
-    if (s >= 1.17549435e-38f) {
-      t = s;
-      inv = rcp_approx(s);
-    }
+    if (s >= 1.17549435e-38f) inv = rcp_approx(s);
     return code;
   }
   if (!finite) return 0xFFu;
@@ -152,19 +148,23 @@ MOE_DEVINL uint32_t fp4_block_scale(float a, float g, float g6, float inv6, floa
   const int e = (b >> 23) != 0 ? (int)(b >> 23) - 127 : (31 - __clz(b)) - 149;
   const int s = max(-127, e - 2);
   inv = __uint_as_float((uint32_t)(127 - s) << 23);
-  t = 0.0f;  // unused: products with a power of two are exact
   return (uint32_t)(s + 127);
 }
 
-// 8 values -> 8 codes, by the block's t and inv.
+// 8 values -> 8 codes, by the block's inv.  MXFP4: products with a power of two are
+// exact.  NVFP4: the ties are .25 to 5, met within 5 2^-23; near 24 floats are
+// 2^-19 apart; a bf16 x over a scale of 12 bits (an E4M3 times a g of 8 bits) is a
+// tie or 2^-14 from one.
 template <int FMT>
-MOE_DEVINL uint32_t fp4_codes8(const float *v, float t, float inv) {
-  const uint64_t inv2 = pack2(inv, inv), mt2 = pack2(-t, -t);
+MOE_DEVINL uint32_t fp4_codes8(const float *v, float inv) {
+  const uint64_t inv2 = pack2(inv, inv);
+  const uint64_t grid = pack2(24.0f, 24.0f), back = pack2(-24.0f, -24.0f);
   float r[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint64_t x = pack2(v[2 * j], v[2 * j + 1]);
-    unpack2(FMT == MOE_FP4_NV ? div_exact2(x, mt2, inv2) : mul2(x, inv2), r[2 * j], r[2 * j + 1]);
+    unpack2(FMT == MOE_FP4_NV ? add2(snap2(x, inv2, grid), back) : mul2(x, inv2), r[2 * j],
+            r[2 * j + 1]);
   }
   // (a NaN or an infinity times 0 is no zero code)
   return inv == 0.0f ? 0u : cvt_e2m1x8(r);
