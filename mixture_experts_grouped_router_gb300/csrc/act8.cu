@@ -16,15 +16,16 @@
 //
 // Every kernel streams: a warp takes 256 columns of a row at a time (8 elements
 // = 16 bytes a lane, 4 lanes a block, the block's maximum by two shuffles) and
-// keeps two to four 16-byte loads a lane in flight.  What bounds them: the reading
-// kernels HBM, the quantising ones the issue of some 15 instructions a value as well
-// (32768 rows, measured copy 6676 GB/s):
-//   swiglu_bwd, F = 14336       735 us, 6460 GB/s
-//   swiglu_fwd, F = 14336       652 us, 5850 GB/s (five resident blocks: 634 us by
-//       itself, but forward and backward in turn 1375 -> 1394 us)
-//   dequantize, 4096 columns     65 us, 6270 GB/s
-//   quantize,   4096 columns     69 us, 5960 GB/s (eight resident blocks of two
-//       loads a lane; four of four: 74 us)
+// keeps two to four 16-byte loads a lane in flight.  What bounds them: HBM, the
+// quantising ones the issue of some 14 instructions a value as well (32768 rows,
+// measured copy 6676 GB/s):
+//   swiglu_bwd, F = 14336       778 us, 6110 GB/s
+//   swiglu_fwd, F = 14336       604 us, 6320 GB/s (652 with a residual step after each
+//       quotient; five resident blocks were 3% faster by themselves, but forward and
+//       backward in turn 1.4% slower)
+//   dequantize, 4096 columns     69 us, 6000 GB/s
+//   quantize,   4096 columns     67 us, 6130 GB/s (eight resident blocks of two
+//       loads a lane; four of four: 7% slower)
 // Eight loads a lane are slower everywhere (registers).
 #include <algorithm>
 
