@@ -253,19 +253,23 @@ class Checkpoint8:
         names = ("topk_idx", "topk_w", "group_offsets", "s2f", "f2s") + (
             ("aux_counts",) if s.aux_coeff else ())
         self.routing = {n: torch.empty_like(getattr(b, n)) for n in names}
-        self.logits = None
+        self.logits = torch.empty(s.T, s.E, dtype=torch.float32, device=dev)
+        self.saved = False
 
     def nbytes(self) -> int:
-        """Bytes that the checkpoint holds."""
+        """Bytes of the codes and the routing decision (the logits, 4 T E, beside them)."""
         ts = [*self.xs, *self.h, *self.y, *self.routing.values()]
         return sum(t.numel() * t.element_size() for t in ts)
 
     def save(self, b, stream=None):
         """After layer.forward(b, ...): afterwards b is free for another layer's forward."""
+        if b.logits is None:
+            raise ValueError("Checkpoint8.save before a forward")
         f, nf = b.s.f, self.nf
-        self.logits = b.logits
         off = b.group_offsets
+        self.saved = True
         with torch.cuda.stream(stream):
+            self.logits.copy_(b.logits)  # the caller's tensor may hold the next layer's soon
             for n, t in self.routing.items():
                 t.copy_(getattr(b, n))
         act8_quantize(b.xs, *self.xs, off, stream)
@@ -280,7 +284,7 @@ class Checkpoint8:
     def backward(self, b, dout, wi, wo, stream=None):
         """layer.backward of the saved forward: (dx, dwi, dwo, d_topk_w) in b's buffers, the
         router-logit gradient in b.d_logits, bias gradients in b.dbi and b.dbo."""
-        if self.logits is None:
+        if not self.saved:
             raise ValueError("Checkpoint8.backward before save")
         s, r = b.s, self.routing
         off, f2s, st = r["group_offsets"], r["f2s"], b.dev_status

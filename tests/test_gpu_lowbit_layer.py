@@ -66,6 +66,28 @@ def test_backward_from_checkpoint(name, biased):
     assert ck.nbytes() <= 0.54 * 2 * R_ * (2 * d + 2 * f) + 16 * R_ + 8 * cfg.T * cfg.k + 8192
 
 
+def test_checkpoint_outlives_the_callers_logits():
+    """Every layer's logits in one buffer of the caller: the saved layer's router-logit
+    gradient is that of its own."""
+    from mixture_experts_grouped_router_gb300 import layer, lowbit
+    cfg = CASES["odd_sizes"]
+    inp = moe_synth.make_inputs(cfg, seed=5)
+    x, wi, wo, dout = (dev_bf16(inp[n]) for n in ("x", "wi", "wo", "dout"))
+    logits = torch.from_numpy(inp["logits"]).cuda()
+    b = layer.MoEBuffers(layer_shape(cfg, False))
+    ck = lowbit.Checkpoint8(b)
+    with pytest.raises(ValueError, match="before a forward"):
+        ck.save(b)
+    layer.forward(b, x, logits, wi, wo)
+    ck.save(b)
+    ck.backward(b, dout, wi, wo)
+    want = b.d_logits.clone()
+    logits.copy_(torch.randn_like(logits))
+    layer.forward(b, x, logits, wi, wo)
+    ck.backward(b, dout, wi, wo)
+    assert torch.equal(b.d_logits, want)
+
+
 def test_checkpoint_refusals():
     from mixture_experts_grouped_router_gb300 import layer, lowbit
     b = layer.MoEBuffers(layer.LayerShape(64, 128, 128, 4, 2, mxfp8=True))
@@ -117,6 +139,45 @@ def test_serving_layer(fmt, T, align, capacity):
     got = f64(out)
     assert got.shape == want.shape
     assert np.linalg.norm(got - want) <= 1e-2 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("T", [1, 700])
+def test_serving_and_checkpoint_kernels_in_a_graph(T):
+    """Captured once and replayed on other inputs in the same buffers: bit for bit what the
+    calls give (routing, quantisation with the linked gather at T = 700, both products)."""
+    from mixture_experts_grouped_router_gb300 import layer, lowbit
+    d, f, E, k = 6400, 128, 6, 4
+    g = torch.Generator(device="cuda").manual_seed(T)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+    t = lambda v: torch.tensor([v], dtype=torch.float32, device="cuda")  # noqa: E731
+    w = lowbit.Fp4Experts.from_weights("nv", (rnd(E, d, 2 * f) / 80).bfloat16(),
+                                       (rnd(E, f, d) / 11).bfloat16(), t(0.0078125), t(0.0078125))
+    m = lowbit.Fp4Layer(w, layer.LayerShape(T, d, f, E, k))
+    x, logits = rnd(T, d).bfloat16(), rnd(T, E)
+    q = torch.empty(T, d, dtype=torch.int8, device="cuda")
+    s = torch.empty(T, d // 32, dtype=torch.bfloat16, device="cuda")
+
+    def work():
+        lowbit.act8_quantize(x, q, s)
+        return m.forward(x, logits)
+
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        work()
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            out = work()
+    for _ in range(3):
+        x.copy_(rnd(T, d))
+        logits.copy_(rnd(T, E))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone(), q.clone(), s.clone()
+        out.zero_()
+        work()
+        assert all(torch.equal(a, b) for a, b in zip(got, (out, q, s)))
+    assert int(m.bufs.dev_status.item()) == 0
 
 
 def test_example_trains_and_serves():
