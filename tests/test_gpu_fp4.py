@@ -294,6 +294,57 @@ def test_gmm_swiglu_quantises_act(L, fmt, save_h, sizes, K, F):
         assert (h[n:] == 9.0).all()
 
 
+# three to four tiles a pair of CTAs (on 76 of them), token tiles of every kind: one
+# token, exactly 128, 192 and 256, one more, two and three like ones
+ROUNDS = [([300, 0, 256, 193, 515], 288, 8448), ([256, 256, 257, 128], 32, 8448),
+          ([1, 192, 640, 31, 385], 544, 6400), ([130, 300], 2848, 6600)]
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("sizes,K,N", ROUNDS)
+def test_gmm_plain_over_many_tiles(L, fmt, sizes, K, N):
+    """Accumulators and their shared columns handed on from tile to tile."""
+    c = gemm_case(L, fmt, sizes, K, N, seed=N)
+    C = torch.full((c["cap"], N), 9.0, dtype=torch.bfloat16, device="cuda")
+    for _ in range(3):
+        C.fill_(9.0)
+        L.moe_gmm_fp4(c["A"], c["sfa"], c["B"], c["sfb"], FMT[fmt], c["off"], C=C,
+                      a_scale=c["a_scale"], b_scale=c["b_scale"])
+        got = f64(C)
+        tol = R.bf16_half_step(c["S"]) + 2.0 ** -16 * c["mag"]
+        assert (np.abs(got[:c["n"]] - c["S"]) <= tol).all()
+        assert (got[c["n"]:] == 9.0).all()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("sizes,K,F", [([300, 0, 256, 193, 515], 2848, 2080),
+                                       ([1, 192, 270, 31, 385], 96, 3296),
+                                       ([300, 0, 700, 193, 515], 96, 3296)])
+def test_gmm_swiglu_over_many_tiles(L, fmt, sizes, K, F):
+    """Both forms (weights as M: long K or few rows; tokens as M), H in bf16: every
+    value within a rounding and the fp32 sums' error."""
+    c = gemm_case(L, fmt, sizes, K, 2 * F, seed=F, swiglu=True)
+    n, cap, E = c["n"], c["cap"], len(sizes)
+    q2 = torch.full((cap, F // 2), 0xAB, dtype=torch.uint8, device="cuda")
+    sf2 = torch.empty(L.moe_fp4_scale_bytes(cap, F, FMT[fmt], 1, E), dtype=torch.uint8, device="cuda")
+    H = torch.full((cap, 2 * F), 9.0, dtype=torch.bfloat16, device="cuda")
+    g2 = 0.03125
+    L.moe_gmm_fp4(c["A"], c["sfa"], c["B"], c["sfb"], FMT[fmt], c["off"],
+                  epilogue=L.EPI_SWIGLU_FWD, C=H, Q2=q2, sf2=sf2, a_scale=c["a_scale"],
+                  b_scale=c["b_scale"],
+                  q2_scale=torch.tensor([g2], device="cuda") if fmt == "nv" else None)
+    h = f64(H)
+    assert (np.abs(h[:n] - c["S"]) <= R.bf16_half_step(c["S"]) + 2.0 ** -16 * c["mag"]).all()
+    assert (h[n:] == 9.0).all()
+    val = R.fp4_quantize(R.swiglu(c["S"]), fmt, g2)[2]
+    ac = -(-F // (64 if fmt == "nv" else 128))
+    s = grouped_scales(sf2.cpu().numpy(), padded_rows(sizes), -(-F // (16 if fmt == "nv" else 32)), ac)
+    got = R.fp4_values(R.unpack(q2.cpu().numpy()[:n]), s, fmt, g2)
+    assert np.mean(got != val) <= 1e-3
+    assert np.linalg.norm(got - val) <= 1e-2 * np.linalg.norm(val)
+    assert (q2.cpu().numpy()[n:] == 0xAB).all()
+
+
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
 def test_a_nan_block_reaches_its_row_alone(L, fmt):
     c = gemm_case(L, fmt, [6], 256, 64)
