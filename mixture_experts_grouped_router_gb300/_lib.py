@@ -1,6 +1,6 @@
-"""ctypes binding of libmoe_gb300.so: one Python function per C entry point,
-same names, argument marshalling only (tensor -> pointer, shape -> sizes,
-current torch stream -> cudaStream_t).  Every step of the layer runs in the
+"""Binding of libmoe_gb300.so by ctypes (the short low-bit operators by _native.so):
+one Python function per C entry point, same names, argument marshalling only
+(tensor -> pointer, shape -> sizes, current torch stream -> cudaStream_t).  Every step of the layer runs in the
 library's CUDA kernels; there is no fallback: if the library is missing the
 import fails.
 """
@@ -45,6 +45,11 @@ def _load() -> ctypes.CDLL:
 
 
 LIB = _load()
+try:
+    from . import _native  # noqa: E402  (links to the library just loaded)
+except ImportError as e:
+    raise ImportError("_native.so is not built or does not load (%s); run "
+                      "`python -m mixture_experts_grouped_router_gb300.build`" % e) from e
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -473,23 +478,14 @@ def moe_fp4_scale_bytes(rows: int, cols: int, fmt: int, row_map: int, E: int = 1
     return int(LIB.moe_fp4_scale_bytes(rows, cols, fmt, row_map, E))
 
 
-def _groups(group_offsets, groups):
-    return groups if group_offsets is None else group_offsets.shape[0] - 1
-
-
 def moe_fp4_quantize(x, fmt, q, sf, row_map=FP4_ROWS_GROUPED, group_offsets=None, groups=1,
                      row_index=None, index_div=1, scale=None, workspace=None, dev_status=None,
                      stream=None):
     """Rows of x bf16 [src_rows, cols] (gathered through row_index / index_div) -> q uint8
     [rows, cols / 2], sf uint8 scale atoms; GROUPED takes group_offsets, EXPERTS / SWIGLU the
     number of equal row groups."""
-    rows, cols = q.shape[0], x.shape[1]
-    _check(LIB.moe_fp4_quantize(_ptr(x), _ld(x), x.shape[0], _ptr(row_index), index_div, rows,
-                                cols, fmt, row_map, _ptr(group_offsets),
-                                _groups(group_offsets, groups), _ptr(scale), _ptr(q), _ld(q),
-                                _ptr(sf), sf.numel(), _ptr(workspace),
-                                0 if workspace is None else workspace.numel(),
-                                _ptr(dev_status), _stream(stream)))
+    _check(_native.fp4_quantize(x, fmt, q, sf, row_map, group_offsets, groups, row_index, index_div,
+                                scale, workspace, dev_status, _stream(stream)))
 
 
 def moe_fp4_quantize_workspace_bytes(src_rows: int, rows: int) -> int:
@@ -499,10 +495,8 @@ def moe_fp4_quantize_workspace_bytes(src_rows: int, rows: int) -> int:
 def moe_fp4_dequantize(q, sf, fmt, x, row_map=FP4_ROWS_GROUPED, group_offsets=None, groups=1,
                        scale=None, stream=None):
     """Codes q [rows, cols / 2] with scale atoms sf -> x bf16 [rows, cols]."""
-    rows, cols = x.shape
-    _check(LIB.moe_fp4_dequantize(_ptr(q), _ld(q), _ptr(sf), sf.numel(), rows, cols, fmt, row_map,
-                                  _ptr(group_offsets), _groups(group_offsets, groups),
-                                  _ptr(scale), _ptr(x), _ld(x), _stream(stream)))
+    _check(_native.fp4_dequantize(q, sf, fmt, x, row_map, group_offsets, groups, scale,
+                                  _stream(stream)))
 
 
 def moe_fp4_quantize_weights(w, fmt, row_map, q, sf, scale=None, stream=None):
@@ -559,47 +553,25 @@ def moe_fp4_experts(w, b, x, sorted_to_flat, k, group_offsets, stream=None):
 
 
 # -------------------------------------------------- activation checkpoints in 8 bits
-# (short kernels: the argument marshalling is kept to what they need)
-def _offsets(group_offsets):
-    if group_offsets is None:
-        return None, 0
-    return group_offsets.data_ptr(), group_offsets.shape[0] - 1
-
-
 def moe_act8_quantize(x, q, scales, group_offsets=None, stream=None):
     """x bf16 [rows, cols] -> q int8 [rows, cols], scales bf16 [rows, ceil(cols / 32)]."""
-    rows, cols = x.shape
-    off, E = _offsets(group_offsets)
-    _check(LIB.moe_act8_quantize(x.data_ptr(), _ld(x), rows, cols, off, E, q.data_ptr(), _ld(q),
-                                 scales.data_ptr(), _ld(scales), _stream(stream)))
+    _check(_native.act8_quantize(x, q, scales, group_offsets, _stream(stream)))
 
 
 def moe_act8_dequantize(q, scales, x, group_offsets=None, stream=None):
     """The values of the codes, in x bf16 [rows, cols]."""
-    rows, cols = x.shape
-    off, E = _offsets(group_offsets)
-    _check(LIB.moe_act8_dequantize(q.data_ptr(), _ld(q), scales.data_ptr(), _ld(scales), rows,
-                                   cols, off, E, x.data_ptr(), _ld(x), _stream(stream)))
+    _check(_native.act8_dequantize(q, scales, x, group_offsets, _stream(stream)))
 
 
 def moe_act8_swiglu_fwd(h, act, q, scales, group_offsets=None, stream=None):
     """h bf16 [rows, 2F] -> act bf16 [rows, F], q int8 [rows, 2F], scales bf16
     [rows, 2 ceil(F / 32)]."""
-    rows, F = act.shape
-    off, E = _offsets(group_offsets)
-    _check(LIB.moe_act8_swiglu_fwd(h.data_ptr(), _ld(h), rows, F, off, E, act.data_ptr(), _ld(act),
-                                   q.data_ptr(), _ld(q), scales.data_ptr(), _ld(scales),
-                                   _stream(stream)))
+    _check(_native.act8_swiglu_fwd(h, act, q, scales, group_offsets, _stream(stream)))
 
 
 def moe_act8_swiglu_bwd(q, scales, dact, dh, act=None, group_offsets=None, stream=None):
     """Codes of h and dact bf16 [rows, F] -> dh bf16 [rows, 2F], act bf16 [rows, F]."""
-    rows, F = dact.shape
-    off, E = _offsets(group_offsets)
-    _check(LIB.moe_act8_swiglu_bwd(q.data_ptr(), _ld(q), scales.data_ptr(), _ld(scales),
-                                   dact.data_ptr(), _ld(dact), rows, F, off, E, dh.data_ptr(),
-                                   _ld(dh), None if act is None else act.data_ptr(),
-                                   0 if act is None else _ld(act), _stream(stream)))
+    _check(_native.act8_swiglu_bwd(q, scales, dact, dh, act, group_offsets, _stream(stream)))
 
 
 # ------------------------------------------------------------ expert parallelism

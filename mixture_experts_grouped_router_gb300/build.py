@@ -1,7 +1,9 @@
-"""Build libmoe_gb300.so in-tree with nvcc for sm_103a (GB300).
+"""Build libmoe_gb300.so in-tree with nvcc for sm_103a (GB300), and _native.so,
+the Python calls of the short low-bit operators.
 
 Each CUDA translation unit under csrc/ is compiled in parallel, then linked
-into one shared library next to this file.  Run ``python -m
+into one shared library next to this file; _native.so (csrc/native.cpp, the host's
+C++ compiler and Python's headers) links to it by its place.  Run ``python -m
 mixture_experts_grouped_router_gb300.build`` or call :func:`build`.
 """
 from __future__ import annotations
@@ -11,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +22,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_NAME = "libmoe_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
+NATIVE_SRC = os.path.join(CSRC, "native.cpp")
+NATIVE_PATH = os.path.join(HERE, "_native.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I" + INCLUDE, "-I" + CSRC]
@@ -55,10 +60,25 @@ def _compile(src: str, verbose: bool, extra) -> str:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not (os.path.exists(LIB_PATH) and os.path.exists(NATIVE_PATH)):
         return False
     t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return all(os.path.getmtime(p) <= t for p in _deps()) and \
+        os.path.getmtime(NATIVE_SRC) <= os.path.getmtime(NATIVE_PATH)
+
+
+def _run(cmd, what: str):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed:\n%s\n%s" % (what, " ".join(cmd), r.stdout + r.stderr))
+
+
+def _build_native() -> None:
+    tmp = NATIVE_PATH + ".tmp"
+    _run([shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + INCLUDE,
+          "-I" + sysconfig.get_paths()["include"], NATIVE_SRC, "-L" + HERE, "-l:" + LIB_NAME,
+          "-Wl,-rpath,$ORIGIN", "-o", tmp], "compiling " + NATIVE_SRC)
+    os.replace(tmp, NATIVE_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -70,11 +90,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose, extra_flags), srcs))
     tmp = LIB_PATH + ".tmp"
-    cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), r.stdout + r.stderr))
+    _run([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs, "link")
     os.replace(tmp, LIB_PATH)
+    _build_native()
     return LIB_PATH
 
 
