@@ -119,6 +119,7 @@ struct Book {
   int off[kMaxE + 1];        // group offsets, clamped to [0, rows_cap]
   int cum[kMaxE + 1];        // per-expert tile prefix
   uint16_t poff[kMaxE + 1];  // padded group starts in units of 128 rows
+  float gb[kMaxE];           // the weights' fp32 scales
 };
 
 template <int FMT, int EPI>
@@ -167,28 +168,38 @@ MOE_DEVINL int group_offset(const Fp4Params &p, int e) {
   return min(max(ld_i32(p.offsets + e), 0), p.rows_cap);
 }
 
+// The expert of tile t: the last one whose tiles begin at or before it (a warp's
+// lanes look at one expert each; the result is uniform).
+MOE_DEVINL int tile_expert(const Book &bk, const Fp4Params &p, int t) {
+  int n = 0;
+  for (int e0 = 0; e0 < p.E; e0 += 32) {
+    const int e = e0 + (int)(threadIdx.x & 31);
+    n += __popc(__ballot_sync(0xffffffffu, e < p.E && bk.cum[e] <= t));
+  }
+  return n - 1;
+}
+
 // Tile t: an expert's token tiles follow one another under one weight tile, so
 // that the pairs that run at a time share its rows in L2.  They are as few as can be
 // and of like size, in steps of 64 tokens: 192 and up to 192 rather than 256 and up
 // to 128 (the scale atoms of their tokens then start in row 0 or in row 64).
 MOE_DEVINL TileInfo decode_tile(const Book &bk, const Fp4Params &p, int t) {
-  int lo = 0, hi = p.E - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (bk.cum[mid] <= t) lo = mid;
-    else hi = mid - 1;
-  }
   TileInfo ti;
-  ti.e = tc::uniform(lo);
+  ti.e = tile_expert(bk, p, t);
   const int off = tc::uniform(bk.off[ti.e]);
   const int size = tc::uniform(max(bk.off[ti.e + 1], off)) - off;
   const int local = t - tc::uniform(bk.cum[ti.e]);
-  const int tt = (size + BT - 1) / BT;
-  const int step = ((size + tt - 1) / tt + 63) & ~63;
-  ti.w_idx = local / tt;
-  ti.t0 = (local - ti.w_idx * tt) * step;
+  ti.w_idx = local;
+  ti.t0 = 0;
+  ti.tokens = size;
+  if (size > BT) {
+    const int tt = (size + BT - 1) / BT;
+    const int step = ((size + tt - 1) / tt + 63) & ~63;
+    ti.w_idx = local / tt;
+    ti.t0 = (local - ti.w_idx * tt) * step;
+    ti.tokens = min(size - ti.t0, step);
+  }
   ti.row0 = off + ti.t0;
-  ti.tokens = min(size - ti.t0, step);
   ti.n = (ti.tokens + 15) / 16 * 16;
   return ti;
 }
@@ -428,14 +439,8 @@ struct RowTile {
 constexpr int kGroupPairs = 16;  // raster group: token-tile pairs that share weight rows in L2
 
 MOE_DEVINL RowTile decode_row_tile(const Book &bk, const Fp4Params &p, int t, int crank) {
-  int lo = 0, hi = p.E - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (bk.cum[mid] <= t) lo = mid;
-    else hi = mid - 1;
-  }
   RowTile ti;
-  ti.e = tc::uniform(lo);
+  ti.e = tile_expert(bk, p, t);
   const int local = t - tc::uniform(bk.cum[ti.e]);
   ti.row0 = tc::uniform(bk.off[ti.e]);
   ti.row_end = max(tc::uniform(bk.off[ti.e + 1]), ti.row0);
@@ -582,6 +587,8 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
   // tile counts and the first weights' copies (each role then waits for itself).
   const bool early = EPI != kRows && p.early;
   if (!early) grid_dependency_begin();
+  for (int e = (int)threadIdx.x - 32; e < p.E; e += L::threads - 32)
+    if (e >= 0) bk.gb[e] = p.gb != nullptr ? ld_f32(p.gb + e) : 1.0f;
   if (warp == 0) {
     // per-expert tile counts and padded sizes, and their exclusive scans
     int carry = 0, pcarry = 0;
@@ -851,7 +858,7 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
       RowTile rt;
       if (EPI == kRows) rt = decode_row_tile(bk, p, t, crank);
       else ti = decode_tile(bk, p, t);
-      const float sc = p.gb != nullptr ? ga * ld_f32(p.gb + (EPI == kRows ? rt.e : ti.e)) : ga;
+      const float sc = ga * bk.gb[EPI == kRows ? rt.e : ti.e];
       const uint32_t a = acc_it & 1;
       const uint32_t aph = (acc_it >> 1) & 1;
       // the two warps of a pair give up together (one barrier between them below)
