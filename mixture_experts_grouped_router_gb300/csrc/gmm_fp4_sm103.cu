@@ -272,19 +272,20 @@ MOE_DEVINL bool pair_agree(bool ok, int pair) {
   return r != 0;
 }
 
-// A warp's chunks of 32 tokens, every other one, those of the columns that the two
+// A warp's chunks of 32 tokens, every other one from `first` on (the two warps of a
+// quarter change places from tile to tile, so that those of one chunk overlap), those of the columns that the two
 // accumulators share first: the last ones of the lower accumulator (a = 0), the first
 // ones of the upper.  Its first two are loaded together, after which the next tile's
 // products may take the shared columns; then one is always on its way.
 struct Chunks {
   uint32_t taddr;
-  int n, a;  // chunks of the tile, accumulator
+  int n, a, first;  // chunks of the tile, accumulator
   uint32_t cur[32], nxt[32];
 
   MOE_DEVINL int at(int i) const { return a ? i : n - 1 - i; }
-  MOE_DEVINL void begin(int sub, uint32_t shared_read, int lane) {
-    if (sub < n) tc::tmem_ld32_issue(taddr + at(sub) * 32, cur);
-    if (sub + 2 < n) tc::tmem_ld32_issue(taddr + at(sub + 2) * 32, nxt);
+  MOE_DEVINL void begin(uint32_t shared_read, int lane) {
+    if (first < n) tc::tmem_ld32_issue(taddr + at(first) * 32, cur);
+    if (first + 2 < n) tc::tmem_ld32_issue(taddr + at(first + 2) * 32, nxt);
     tc::tmem_wait_ld(cur);
     tc::reg_after(nxt);
     tc::tc_fence_before();
@@ -318,13 +319,13 @@ MOE_DEVINL void epilogue_swiglu(const Book &bk, const Fp4Params &p, const TileIn
   const int tok = (q & 1) * 16 + (lane >> 1), h = lane & 1;
   const int fh = f0 + 16 * h;  // this thread's features
 #pragma unroll 1
-  for (int i = sub; i < ch.n; i += 2) {
+  for (int i = ch.first; i < ch.n; i += 2) {
     const int c = ch.at(i);
     {
       float v[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(ch.cur[j]) * sc;
-      if (i > sub) pair_sync(pair);  // both warps are done with the last chunk
+      if (i > ch.first) pair_sync(pair);  // both warps are done with the last chunk
       stage_f32_t(stg_pair + (q & 1) * kStgBytes, lane, v);
     }
     ch.advance(i);
@@ -381,7 +382,7 @@ MOE_DEVINL void epilogue_plain(const Fp4Params &p, const TileInfo &ti, float sc,
   const int nc = ti.w_idx * BW + crank * (BW / 2) + q * 32;
   if (nc >= p.N) return;
 #pragma unroll 1
-  for (int i = sub; i < ch.n; i += 2) {
+  for (int i = ch.first; i < ch.n; i += 2) {
     const int c = ch.at(i);
     float v[32];
 #pragma unroll
@@ -393,7 +394,7 @@ MOE_DEVINL void epilogue_plain(const Fp4Params &p, const TileInfo &ti, float sc,
     // the last tile's stores have read them), fp32 ones all of it
     uint8_t *buf = p.c_f32 ? stg : stg + (i >> 1 & 1) * 2048;
     if (lane == 0) {
-      if (p.c_f32 || i == sub) tc::bulk_wait_read0();
+      if (p.c_f32 || i == ch.first) tc::bulk_wait_read0();
       else tc::bulk_wait_read<1>();
     }
     __syncwarp();
@@ -874,7 +875,8 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
         ch.taddr = taddr;
         ch.n = (ti.tokens + 31) / 32;
         ch.a = a;
-        ch.begin(sub, tc::mapa_shared(tc::smem_u32(&bk.shared_read), 0), lane);
+        ch.first = sub ^ (int)a;
+        ch.begin(tc::mapa_shared(tc::smem_u32(&bk.shared_read), 0), lane);
         if (EPI == MOE_EPI_SWIGLU_FWD)
           epilogue_swiglu<FMT>(bk, p, ti, sc, g2, inv6, ch, crank, q, sub, lane,
                                stg + (2 * sub + (q >> 1)) * 2 * kStgBytes);
