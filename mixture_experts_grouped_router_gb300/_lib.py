@@ -547,9 +547,8 @@ class Fp4BuffersArg(ctypes.Structure):
 
 def moe_fp4_experts(w, b, x, sorted_to_flat, k, group_offsets, stream=None):
     """w, b: Fp4WeightsArg, Fp4BuffersArg; x bf16 [T, d] -> y of b."""
-    _check(LIB.moe_fp4_experts(ctypes.byref(w), ctypes.byref(b), x.data_ptr(), _ld(x), x.shape[0],
-                               sorted_to_flat.data_ptr(), k, group_offsets.data_ptr(),
-                               _stream(stream)))
+    _check(_native.fp4_experts(ctypes.addressof(w), ctypes.addressof(b), x, sorted_to_flat, k,
+                               group_offsets, _stream(stream)))
 
 
 # -------------------------------------------------- activation checkpoints in 8 bits

@@ -262,6 +262,24 @@ PyObject *fp4_dequantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
   });
 }
 
+// addresses of moe_fp4_weights and moe_fp4_buffers, x, sorted_to_flat, k, group_offsets, stream
+PyObject *fp4_experts(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  return entry<7>(args, n, [](PyObject *const *a) {
+    const auto w = reinterpret_cast<const moe_fp4_weights *>(as_int(a[0]));
+    const auto b = reinterpret_cast<const moe_fp4_buffers *>(as_int(a[1]));
+    int64_t T;
+    int d;
+    sizes(a[2], T, d);
+    const int tokens = as_int32(T), k = int32_arg(a[4]);
+    const auto x = ptr<uint16_t>(a[2]);
+    const auto s2f = ptr<int32_t>(a[3]);
+    const auto off = ptr<int32_t>(a[5]);
+    const int64_t ldx = ld(a[2]);
+    const moe_stream_t st = stream(a[6]);
+    return unlocked([=] { return moe_fp4_experts(w, b, x, ldx, tokens, s2f, k, off, st); });
+  });
+}
+
 PyCFunction fast(PyObject *(*f)(PyObject *, PyObject *const *, Py_ssize_t)) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
 }
@@ -273,6 +291,7 @@ PyMethodDef methods[] = {
     {"act8_swiglu_bwd", fast(act8_swiglu_bwd), METH_FASTCALL, nullptr},
     {"fp4_quantize", fast(fp4_quantize), METH_FASTCALL, nullptr},
     {"fp4_dequantize", fast(fp4_dequantize), METH_FASTCALL, nullptr},
+    {"fp4_experts", fast(fp4_experts), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 
