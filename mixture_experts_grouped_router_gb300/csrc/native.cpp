@@ -1,6 +1,6 @@
 // Python calls of the short low-bit operators: the tensors' pointers, sizes and
 // leading dimensions are taken here and handed to the C ABI.  A call's kernels take a
-// few microseconds, so that the host's share counts: 3 us a call on an Arm core
+// few microseconds, so that the host's share counts: 3.2 us a call on an Arm core
 // with the launch (1.5), where ctypes takes 5.5.  `_lib.py` holds the functions
 // that a program calls, with their words, and raises what these return.
 //
