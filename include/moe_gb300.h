@@ -553,9 +553,10 @@ moe_status_t moe_tgmm_mx(const uint8_t *At, int64_t ldat, const uint8_t *sfa, in
  *   MOE_FP4_MX  32 elements, scale 2^s as the E8M0 code s + 127,
  *               s = floor(log2 max|x|) - 2 (OCP Microscaling (MX) v1.0);
  *               element value = code * 2^s
- *   MOE_FP4_NV  16 elements, scale E4M3(max|x| / (6 g)) with one fp32 scale
- *               g > 0 for the tensor (a weight: one an expert);
- *               element value = code * scale * g
+ *   MOE_FP4_NV  16 elements, scale E4M3(max|x| / (6 g)), at most 448, with one
+ *               fp32 scale g for the tensor (a weight: one an expert), 2^-126 <= g
+ *               <= 2^117; element value = code * scale * g; a block whose scale
+ *               times g is under 2^-126 takes zero codes
  * A block that holds a NaN or an infinity takes the NaN scale and zero codes
  * (it reads as NaN).  The `scale` arguments are g: fp32 on the device, one for
  * activations and one an expert for weights, NULL for 1; MXFP4 products take

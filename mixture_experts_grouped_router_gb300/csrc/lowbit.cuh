@@ -130,14 +130,15 @@ MOE_DEVINL float fp4_scale_value(uint32_t code, int fmt) {
 // scale (times g for NVFP4), or 0 where every code of the block is 0 (no magnitude,
 // or a NaN / infinity, which takes the NaN scale).
 //   MXFP4: t = 2^s, s = floor(log2 a) - 2 clamped to [-127, 127] (OCP MX v1.0)
-//   NVFP4: E4M3(a / (6 g)), g the tensor's fp32 scale; g6 = 6 g, inv6 = 1 / g6
+//   NVFP4: E4M3(a / (6 g)) saturated at 448, g the tensor's fp32 scale; g6 = 6 g, inv6 =
+//       1 / g6; a is cut to 448 g6 first, as a quotient past fp32's range has no residual
 template <int FMT>
 MOE_DEVINL uint32_t fp4_block_scale(float a, float g, float g6, float inv6, float &inv) {
   inv = 0.0f;
   const bool finite = a <= 3.402823466e38f;
   if (FMT == MOE_FP4_NV) {
     if (!finite) return 0x7Fu;
-    const uint32_t code = e4m3_code(div_exact(a, g6, inv6));
+    const uint32_t code = e4m3_code(div_exact(fminf(a, 448.0f * g6), g6, inv6));
     const float s = e4m3_value(code) * g;
     if (s >= 1.17549435e-38f) inv = rcp_approx(s);
     return code;
