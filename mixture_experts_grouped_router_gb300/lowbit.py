@@ -100,11 +100,12 @@ class Fp4Experts:
             E, N, kb = q.shape
             nb = L.moe_fp4_scale_bytes(E * N, 2 * kb, f, row_map, E)
             sf = torch.empty(nb, dtype=torch.uint8, device=q.device)
-            L.moe_fp4_arrange_scales(s, 2 * kb, f, row_map, E, sf, stream)
+            L.moe_fp4_arrange_scales(s, 2 * kb, f, row_map, E, sf)
             return sf
 
-        return cls(f, wi_q, atoms(wi_q, wi_s, L.FP4_ROWS_SWIGLU), wi_scale,
-                   wo_q, atoms(wo_q, wo_s, L.FP4_ROWS_EXPERTS), wo_scale, x_scale, act_scale)
+        with torch.cuda.stream(stream):  # (the allocations too)
+            wi_sf, wo_sf = atoms(wi_q, wi_s, L.FP4_ROWS_SWIGLU), atoms(wo_q, wo_s, L.FP4_ROWS_EXPERTS)
+        return cls(f, wi_q, wi_sf, wi_scale, wo_q, wo_sf, wo_scale, x_scale, act_scale)
 
     @classmethod
     def from_weights(cls, fmt, wi, wo, x_scale=None, act_scale=None, stream=None):
@@ -118,16 +119,17 @@ class Fp4Experts:
             scale = None
             if f == L.FP4_NV:
                 amax = torch.empty(E, dtype=torch.float32, device=w.device)
-                L.moe_fp8_amax(w.view(E * K, N), amax, groups=E, stream=stream)
+                L.moe_fp8_amax(w.view(E * K, N), amax, groups=E)
                 scale = (amax / (6.0 * 448.0)).bfloat16().float().clamp_(min=2.0 ** -64)
             nb = L.moe_fp4_scale_bytes(E * N, K, f, row_map, E)
             q = torch.empty(E, N, K // 2, dtype=torch.uint8, device=w.device)
             sf = torch.empty(nb, dtype=torch.uint8, device=w.device)
-            L.moe_fp4_quantize_weights(w, f, row_map, q, sf, scale, stream)
+            L.moe_fp4_quantize_weights(w, f, row_map, q, sf, scale)
             return q, sf, scale
 
-        return cls(f, *quantise(wi, L.FP4_ROWS_SWIGLU), *quantise(wo, L.FP4_ROWS_EXPERTS), x_scale,
-                   act_scale)
+        with torch.cuda.stream(stream):  # (torch's own steps and the allocations too)
+            parts = *quantise(wi, L.FP4_ROWS_SWIGLU), *quantise(wo, L.FP4_ROWS_EXPERTS)
+        return cls(f, *parts, x_scale, act_scale)
 
 
 class Fp4Buffers:
