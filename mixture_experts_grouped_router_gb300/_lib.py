@@ -510,7 +510,10 @@ def moe_fp4_quantize_weights(w, fmt, row_map, q, sf, scale=None, stream=None):
 def moe_fp4_arrange_scales(scales, cols, fmt, row_map, E, sf, stream=None):
     """scales uint8 [rows, cols / block] in row order -> sf uint8 scale atoms."""
     assert scales.is_contiguous(), "contiguous tensors only"
-    rows = scales.numel() // (cols // (16 if fmt == FP4_NV else 32))
+    blocks = cols // (16 if fmt == FP4_NV else 32)
+    rows = scales.numel() // max(blocks, 1)
+    if rows * blocks != scales.numel():
+        raise ValueError("%d scales are no rows of %d" % (scales.numel(), blocks))
     _check(LIB.moe_fp4_arrange_scales(_ptr(scales), rows, cols, fmt, row_map, E, _ptr(sf),
                                       sf.numel(), _stream(stream)))
 

@@ -36,6 +36,24 @@ def _fmt(fmt: str) -> int:
     return FORMATS[fmt]
 
 
+def _block(fmt: int) -> int:
+    """Columns of a scale."""
+    return 16 if fmt == L.FP4_NV else 32
+
+
+def _expect(name, t, shape, what, ok):
+    """t is a contiguous tensor of `shape` (None: any length) whose type passes `ok`."""
+    got = tuple(t.shape)
+    if len(got) != len(shape) or any(n is not None and n != m for n, m in zip(shape, got)) \
+            or not ok(t) or not t.is_contiguous():
+        raise ValueError("%s: %s %s, strides %s, for contiguous %s %s"
+                         % (name, t.dtype, got, t.stride(), what, tuple(shape)))
+
+
+def _bytes(t):  # codes and scales, whatever type of one byte they are called
+    return t.element_size() == 1
+
+
 # ------------------------------------------------------------------ 4-bit rows
 class Fp4Rows:
     """Codes and scale atoms of grouped activation rows [rows, cols] (E groups)."""
@@ -75,19 +93,24 @@ class Fp4Experts:
 
     def __init__(self, fmt, wi_q, wi_sf, wi_scale, wo_q, wo_sf, wo_scale, x_scale=None,
                  act_scale=None):
+        self.E, self.d, self.f = self._sizes(fmt, wi_q, wo_q)
         self.fmt = fmt
         self.wi_q, self.wi_sf, self.wi_scale = wi_q, wi_sf, wi_scale
         self.wo_q, self.wo_sf, self.wo_scale = wo_q, wo_sf, wo_scale
         self.x_scale, self.act_scale = x_scale, act_scale
-        self.E, self.d, self.f = wo_q.shape[0], wo_q.shape[1], 2 * wo_q.shape[2]
-        if wi_q.shape != (self.E, 2 * self.f, self.d // 2):
-            raise ValueError("wi codes of shape %s do not match wo's %s"
-                             % (tuple(wi_q.shape), tuple(wo_q.shape)))
-        if not (wi_q.is_contiguous() and wo_q.is_contiguous()):
-            raise ValueError("the weights' codes are contiguous")
         self.arg = L.Fp4WeightsArg(
             self.E, self.d, self.f, fmt, *(None if t is None else t.data_ptr() for t in (
                 wi_q, wi_sf, wi_scale, wo_q, wo_sf, wo_scale, x_scale, act_scale)))
+
+    @staticmethod
+    def _sizes(fmt, wi_q, wo_q):
+        """(E, d, f) of the weights' codes."""
+        if fmt not in FORMATS.values():
+            raise ValueError("fmt is FP4_MX or FP4_NV, not %r" % (fmt,))
+        _expect("wo_q", wo_q, (None, None, None), "one-byte codes", _bytes)
+        E, d, f = wo_q.shape[0], wo_q.shape[1], 2 * wo_q.shape[2]
+        _expect("wi_q", wi_q, (E, 2 * f, d // 2), "one-byte codes", _bytes)
+        return E, d, f
 
     @classmethod
     def from_codes(cls, fmt, wi_q, wi_s, wi_scale, wo_q, wo_s, wo_scale, x_scale=None,
@@ -95,6 +118,9 @@ class Fp4Experts:
         """From a 4-bit checkpoint: codes uint8 [E, 2f, d / 2] and [E, d, f / 2], scales in row
         order uint8 [E, 2f, d / block] and [E, d, f / block], fp32 [E] scales or None."""
         f = _fmt(fmt)
+        E, d, ff = cls._sizes(f, wi_q, wo_q)
+        _expect("wi_s", wi_s, (E, 2 * ff, d // _block(f)), "one-byte scales", _bytes)
+        _expect("wo_s", wo_s, (E, d, ff // _block(f)), "one-byte scales", _bytes)
 
         def atoms(q, s, row_map):
             E, N, kb = q.shape
