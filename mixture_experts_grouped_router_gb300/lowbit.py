@@ -54,6 +54,16 @@ def _bytes(t):  # codes and scales, whatever type of one byte they are called
     return t.element_size() == 1
 
 
+def _bf16(t):
+    return t.dtype == torch.bfloat16
+
+
+def _expect_scale(name, t, n):
+    """An fp32 scale of n elements, or None."""
+    if t is not None and (t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous()):
+        raise ValueError("%s: %s %s for %d contiguous fp32" % (name, t.dtype, tuple(t.shape), n))
+
+
 # ------------------------------------------------------------------ 4-bit rows
 class Fp4Rows:
     """Codes and scale atoms of grouped activation rows [rows, cols] (E groups)."""
@@ -94,13 +104,24 @@ class Fp4Experts:
     def __init__(self, fmt, wi_q, wi_sf, wi_scale, wo_q, wo_sf, wo_scale, x_scale=None,
                  act_scale=None):
         self.E, self.d, self.f = self._sizes(fmt, wi_q, wo_q)
+        for name, t, rows, cols, m in (("wi_sf", wi_sf, 2 * self.f, self.d, L.FP4_ROWS_SWIGLU),
+                                       ("wo_sf", wo_sf, self.d, self.f, L.FP4_ROWS_EXPERTS)):
+            _expect(name, t, (None,), "atoms of one-byte scales", _bytes)
+            nb = L.moe_fp4_scale_bytes(self.E * rows, cols, fmt, m, self.E)
+            if t.numel() < nb:
+                raise ValueError("%s: %d bytes of scale atoms, not %d" % (name, t.numel(), nb))
+        for name, t, n in (("wi_scale", wi_scale, self.E), ("wo_scale", wo_scale, self.E),
+                           ("x_scale", x_scale, 1), ("act_scale", act_scale, 1)):
+            _expect_scale(name, t, n)
+        tensors = (wi_q, wi_sf, wi_scale, wo_q, wo_sf, wo_scale, x_scale, act_scale)
+        if any(t is not None and t.device != wo_q.device for t in tensors):
+            raise ValueError("codes and scales on one device")
         self.fmt = fmt
         self.wi_q, self.wi_sf, self.wi_scale = wi_q, wi_sf, wi_scale
         self.wo_q, self.wo_sf, self.wo_scale = wo_q, wo_sf, wo_scale
         self.x_scale, self.act_scale = x_scale, act_scale
         self.arg = L.Fp4WeightsArg(
-            self.E, self.d, self.f, fmt, *(None if t is None else t.data_ptr() for t in (
-                wi_q, wi_sf, wi_scale, wo_q, wo_sf, wo_scale, x_scale, act_scale)))
+            self.E, self.d, self.f, fmt, *(None if t is None else t.data_ptr() for t in tensors))
 
     @staticmethod
     def _sizes(fmt, wi_q, wo_q):
@@ -139,6 +160,9 @@ class Fp4Experts:
         scale is its weight's max |w| / (6 * 448), kept in 8 significant bits, so that whether
         a ratio of two weights is a tie of the E4M3 or E2M1 grid does not hang on its last bit."""
         f = _fmt(fmt)
+        _expect("wo", wo, (None, None, None), "bf16", _bf16)
+        E, ff, d = wo.shape
+        _expect("wi", wi, (E, d, 2 * ff), "bf16", _bf16)
 
         def quantise(w, row_map):
             E, K, N = w.shape
