@@ -23,8 +23,8 @@ def test_from_codes_is_from_weights(fmt, E, d, f, typed):
 
     def checkpoint(w, g):  # codes and scales in row order, by the oracle
         parts = [R.fp4_quantize(w[e].T, fmt, 1.0 if g is None else float(g[e])) for e in range(E)]
-        q = np.stack([R.pack(p[0]) for p in parts])
-        s = torch.from_numpy(np.stack([p[1] for p in parts])).cuda()
+        q = np.ascontiguousarray([R.pack(p[0]) for p in parts])
+        s = torch.from_numpy(np.ascontiguousarray([p[1] for p in parts])).cuda()
         if typed and fmt == "nv":
             s = s.view(torch.float8_e4m3fn)
         return torch.from_numpy(q).cuda(), s
