@@ -474,6 +474,20 @@ FP4_ROWS_SWIGLU = 2
 FP4_ROWS_EXPERTS = 3
 
 
+def _need(name, t, n):
+    """t: None, or a contiguous tensor of n elements at least."""
+    if t is not None and (t.numel() < n or not t.is_contiguous()):
+        raise ValueError("%s: %s, strides %s, for %d contiguous elements"
+                         % (name, tuple(t.shape), t.stride(), n))
+
+
+def _need_matrix(name, t, rows, cols):
+    """t: None, or a matrix that holds [rows, cols] (a leading dimension under cols is left to
+    the library, which refuses it)."""
+    if t is not None and rows > 0 and (t.shape[-2] < rows or t.shape[-1] < cols <= t.stride(-2)):
+        raise ValueError("%s is %s for [%d, %d]" % (name, tuple(t.shape), rows, cols))
+
+
 def moe_fp4_scale_bytes(rows: int, cols: int, fmt: int, row_map: int, E: int = 1) -> int:
     return int(LIB.moe_fp4_scale_bytes(rows, cols, fmt, row_map, E))
 
@@ -503,6 +517,9 @@ def moe_fp4_quantize_weights(w, fmt, row_map, q, sf, scale=None, stream=None):
     """w bf16 [E, K, N] contiguous -> q uint8 [E, N, K / 2], sf uint8 scale atoms."""
     E, K, N = w.shape
     assert w.is_contiguous() and q.is_contiguous(), "contiguous tensors only"
+    _need("q", q, E * N * (K // 2))
+    if fmt == FP4_NV:
+        _need("scale", scale, E)
     _check(LIB.moe_fp4_quantize_weights(_ptr(w), E, K, N, fmt, row_map, _ptr(scale), _ptr(q),
                                         _ptr(sf), sf.numel(), _stream(stream)))
 
@@ -524,7 +541,19 @@ def moe_gmm_fp4(A, sfa, B, sfb, fmt, group_offsets, K=None, epilogue=EPI_NONE, C
     bf16 H with the SwiGLU epilogue), Q2 uint8 codes of Act [rows_cap, F / 2]."""
     E, N, kb = B.shape
     K = 2 * kb if K is None else K
+    rows, swiglu = A.shape[0], epilogue == EPI_SWIGLU_FWD
     c_dtype = DTYPE_F32 if C is not None and C.dtype == torch.float32 else DTYPE_BF16
+    _need_matrix("A", A, rows, K // 2)
+    _need_matrix("B", B, N, K // 2)
+    _need_matrix("C", C, rows, N)
+    if swiglu:
+        _need_matrix("Q2", Q2, rows, N // 4)
+        _need("sf2", sf2, 0)
+    _need("sfa", sfa, moe_fp4_scale_bytes(rows, K, fmt, FP4_ROWS_GROUPED, E))
+    _need("sfb", sfb, moe_fp4_scale_bytes(E * N, K, fmt,
+                                          FP4_ROWS_SWIGLU if swiglu else FP4_ROWS_EXPERTS, E))
+    _need("group_offsets", group_offsets, E + 1)
+    _need("b_scale", b_scale, E)
     _check(LIB.moe_gmm_fp4(_ptr(A), _ld(A), _ptr(sfa), _ptr(a_scale), _ptr(B), B.stride(1),
                            B.stride(0), _ptr(sfb), _ptr(b_scale), fmt, _ptr(group_offsets), E,
                            A.shape[0], K, N, epilogue, _ptr(C), c_dtype,

@@ -6,6 +6,8 @@
 //
 // Every function takes its arguments by position, tensors as such (None where the C
 // ABI takes a null pointer), the stream as an integer last, and returns the status.
+// The C ABI knows leading dimensions alone; that every operand has the rows, columns
+// and elements which the call's sizes name is checked here (ValueError).
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -13,7 +15,7 @@
 
 namespace {
 
-PyObject *s_data_ptr, *s_stride, *s_numel, *s_shape;
+PyObject *s_data_ptr, *s_stride, *s_numel, *s_shape, *s_is_contiguous;
 
 // An argument's value, or an error that ends the call.
 struct Failed {};
@@ -69,52 +71,93 @@ struct Tuple {
   Tuple(const Tuple &) = delete;
 };
 
-int64_t dim(PyObject *t, Py_ssize_t i) {
-  Tuple s(PyObject_GetAttr(t, s_shape));
-  return item(s.o, i);
-}
+// A row-major matrix (the last two dimensions of a tensor).
+struct Matrix {
+  void *p;
+  int64_t rows, cols, ld;
+  template <typename T>
+  T *as() const {
+    return static_cast<T *>(p);
+  }
+};
 
-// rows and columns of a matrix
-void sizes(PyObject *t, int64_t &rows, int &cols) {
-  Tuple s(PyObject_GetAttr(t, s_shape));
-  if (PyTuple_GET_SIZE(s.o) != 2) {
-    PyErr_SetString(PyExc_ValueError, "matrices only");
+Matrix matrix(PyObject *t, bool exact = false) {
+  Tuple shape(PyObject_GetAttr(t, s_shape));
+  const Py_ssize_t dims = PyTuple_GET_SIZE(shape.o);
+  if (dims < 2 || (exact && dims > 2)) {
+    PyErr_SetString(exact ? PyExc_ValueError : PyExc_AssertionError, "matrices only");
     throw Failed{};
   }
-  rows = item(s.o, 0);
-  cols = as_int32(item(s.o, 1));
+  Matrix m;
+  m.rows = item(shape.o, -2);
+  m.cols = m.ld = item(shape.o, -1);
+  bool empty = false;
+  for (Py_ssize_t i = 0; i < dims; ++i) empty |= item(shape.o, i) == 0;
+  if (!empty) {
+    Tuple stride(PyObject_CallMethodNoArgs(t, s_stride));
+    if (item(stride.o, -1) != 1) {
+      PyErr_SetString(PyExc_AssertionError, "row-major tensors only");
+      throw Failed{};
+    }
+    m.ld = item(stride.o, -2);
+  }
+  m.p = reinterpret_cast<void *>(call_int(t, s_data_ptr));
+  return m;
 }
 
-template <typename T>
-T *ptr(PyObject *t) {
-  return t == Py_None ? nullptr : reinterpret_cast<T *>(call_int(t, s_data_ptr));
+// m, `name` of the call, has to hold `rows` rows of `cols` columns.  A leading dimension
+// under that is left to the library, which refuses it.
+void need(const char *name, const Matrix &m, int64_t rows, int64_t cols) {
+  if (rows <= 0 || (m.rows >= rows && (m.cols >= cols || m.ld < cols))) return;
+  PyErr_Format(PyExc_ValueError, "%s is [%lld, %lld] for [%lld, %lld]", name, (long long)m.rows,
+               (long long)m.cols, (long long)rows, (long long)cols);
+  throw Failed{};
 }
 
-int64_t numel(PyObject *t) { return t == Py_None ? 0 : call_int(t, s_numel); }
+// The elements of a contiguous tensor; none of None (an empty tensor has no address either).
+struct Vector {
+  void *p = nullptr;
+  int64_t n = 0;
+  bool given = false;
+  template <typename T>
+  T *as() const {
+    return static_cast<T *>(p);
+  }
+};
 
-// The leading dimension of a row-major matrix.
-int64_t ld(PyObject *t) {
-  Tuple s(PyObject_CallMethodNoArgs(t, s_stride));
-  if (PyTuple_GET_SIZE(s.o) < 2) {
-    PyErr_SetString(PyExc_AssertionError, "matrices only");
+Vector vector(const char *name, PyObject *t) {
+  Vector v;
+  if (t == Py_None) return v;
+  v.given = true;
+  v.n = call_int(t, s_numel);
+  PyObject *r = PyObject_CallMethodNoArgs(t, s_is_contiguous);
+  if (r == nullptr) throw Failed{};
+  const bool whole = r == Py_True;
+  Py_DECREF(r);
+  if (!whole) {
+    PyErr_Format(PyExc_ValueError, "%s is not contiguous", name);
     throw Failed{};
   }
-  const bool empty = call_int(t, s_numel) == 0;
-  if (empty) return dim(t, -1);
-  if (item(s.o, -1) != 1) {
-    PyErr_SetString(PyExc_AssertionError, "row-major tensors only");
-    throw Failed{};
-  }
-  return item(s.o, -2);
+  v.p = reinterpret_cast<void *>(call_int(t, s_data_ptr));
+  return v;
+}
+
+void need(const char *name, const Vector &v, int64_t n) {
+  if (!v.given || v.n >= n) return;
+  PyErr_Format(PyExc_ValueError, "%s has %lld elements for %lld", name, (long long)v.n, (long long)n);
+  throw Failed{};
 }
 
 // group_offsets and the number of groups that it bounds
 const int32_t *offsets(PyObject *t, int &E, int without) {
   E = without;
   if (t == Py_None) return nullptr;
-  E = as_int32(dim(t, 0) - 1);
-  return ptr<int32_t>(t);
+  const Vector v = vector("group_offsets", t);
+  E = as_int32(v.n - 1);
+  return v.as<const int32_t>();
 }
+
+int64_t blocks32(int64_t cols) { return (cols + 31) / 32; }
 
 moe_stream_t stream(PyObject *o) { return reinterpret_cast<moe_stream_t>(as_int(o)); }
 
@@ -144,50 +187,52 @@ moe_status_t unlocked(F f) {
 // x, q, scales, group_offsets, stream
 PyObject *act8_quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return entry<5>(args, n, [](PyObject *const *a) {
-    int64_t rows;
-    int cols, E;
-    sizes(a[0], rows, cols);
+    const Matrix x = matrix(a[0], true), q = matrix(a[1]), s = matrix(a[2]);
+    const int cols = as_int32(x.cols);
+    need("q", q, x.rows, cols);
+    need("scales", s, x.rows, blocks32(cols));
+    int E;
     const int32_t *off = offsets(a[3], E, 0);
-    const auto x = ptr<uint16_t>(a[0]);
-    const auto q = ptr<int8_t>(a[1]);
-    const auto s = ptr<uint16_t>(a[2]);
-    const int64_t ldx = ld(a[0]), ldq = ld(a[1]), lds = ld(a[2]);
     const moe_stream_t st = stream(a[4]);
-    return unlocked([=] { return moe_act8_quantize(x, ldx, rows, cols, off, E, q, ldq, s, lds, st); });
+    return unlocked([=] {
+      return moe_act8_quantize(x.as<uint16_t>(), x.ld, x.rows, cols, off, E, q.as<int8_t>(), q.ld,
+                               s.as<uint16_t>(), s.ld, st);
+    });
   });
 }
 
 // q, scales, x, group_offsets, stream
 PyObject *act8_dequantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return entry<5>(args, n, [](PyObject *const *a) {
-    int64_t rows;
-    int cols, E;
-    sizes(a[2], rows, cols);
+    const Matrix q = matrix(a[0]), s = matrix(a[1]), x = matrix(a[2], true);
+    const int cols = as_int32(x.cols);
+    need("q", q, x.rows, cols);
+    need("scales", s, x.rows, blocks32(cols));
+    int E;
     const int32_t *off = offsets(a[3], E, 0);
-    const auto q = ptr<int8_t>(a[0]);
-    const auto s = ptr<uint16_t>(a[1]);
-    const auto x = ptr<uint16_t>(a[2]);
-    const int64_t ldq = ld(a[0]), lds = ld(a[1]), ldx = ld(a[2]);
     const moe_stream_t st = stream(a[4]);
-    return unlocked([=] { return moe_act8_dequantize(q, ldq, s, lds, rows, cols, off, E, x, ldx, st); });
+    return unlocked([=] {
+      return moe_act8_dequantize(q.as<int8_t>(), q.ld, s.as<uint16_t>(), s.ld, x.rows, cols, off, E,
+                                 x.as<uint16_t>(), x.ld, st);
+    });
   });
 }
 
 // h, act, q, scales, group_offsets, stream
 PyObject *act8_swiglu_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return entry<6>(args, n, [](PyObject *const *a) {
-    int64_t rows;
-    int F, E;
-    sizes(a[1], rows, F);
+    const Matrix h = matrix(a[0]), act = matrix(a[1], true), q = matrix(a[2]), s = matrix(a[3]);
+    const int64_t rows = act.rows;
+    const int F = as_int32(act.cols);
+    need("h", h, rows, 2 * act.cols);
+    need("q", q, rows, 2 * act.cols);
+    need("scales", s, rows, 2 * blocks32(F));
+    int E;
     const int32_t *off = offsets(a[4], E, 0);
-    const auto h = ptr<uint16_t>(a[0]);
-    const auto act = ptr<uint16_t>(a[1]);
-    const auto q = ptr<int8_t>(a[2]);
-    const auto s = ptr<uint16_t>(a[3]);
-    const int64_t ldh = ld(a[0]), lda = ld(a[1]), ldq = ld(a[2]), lds = ld(a[3]);
     const moe_stream_t st = stream(a[5]);
     return unlocked([=] {
-      return moe_act8_swiglu_fwd(h, ldh, rows, F, off, E, act, lda, q, ldq, s, lds, st);
+      return moe_act8_swiglu_fwd(h.as<uint16_t>(), h.ld, rows, F, off, E, act.as<uint16_t>(), act.ld,
+                                 q.as<int8_t>(), q.ld, s.as<uint16_t>(), s.ld, st);
     });
   });
 }
@@ -195,48 +240,57 @@ PyObject *act8_swiglu_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
 // q, scales, dact, dh, act, group_offsets, stream
 PyObject *act8_swiglu_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return entry<7>(args, n, [](PyObject *const *a) {
-    int64_t rows;
-    int F, E;
-    sizes(a[2], rows, F);
+    const Matrix q = matrix(a[0]), s = matrix(a[1]), dact = matrix(a[2], true), dh = matrix(a[3]);
+    const int64_t rows = dact.rows;
+    const int F = as_int32(dact.cols);
+    need("q", q, rows, 2 * dact.cols);
+    need("scales", s, rows, 2 * blocks32(F));
+    need("dh", dh, rows, 2 * dact.cols);
+    Matrix act = {nullptr, 0, 0, 0};
+    if (a[4] != Py_None) {
+      act = matrix(a[4]);
+      need("act", act, rows, F);
+    }
+    int E;
     const int32_t *off = offsets(a[5], E, 0);
-    const auto q = ptr<int8_t>(a[0]);
-    const auto s = ptr<uint16_t>(a[1]);
-    const auto dact = ptr<uint16_t>(a[2]);
-    const auto dh = ptr<uint16_t>(a[3]);
-    const auto act = ptr<uint16_t>(a[4]);
-    const int64_t ldq = ld(a[0]), lds = ld(a[1]), ldd = ld(a[2]), ldh = ld(a[3]);
-    const int64_t lda = a[4] == Py_None ? 0 : ld(a[4]);
     const moe_stream_t st = stream(a[6]);
     return unlocked([=] {
-      return moe_act8_swiglu_bwd(q, ldq, s, lds, dact, ldd, rows, F, off, E, dh, ldh, act, lda, st);
+      return moe_act8_swiglu_bwd(q.as<int8_t>(), q.ld, s.as<uint16_t>(), s.ld, dact.as<uint16_t>(),
+                                 dact.ld, rows, F, off, E, dh.as<uint16_t>(), dh.ld,
+                                 act.as<uint16_t>(), act.ld, st);
     });
   });
+}
+
+// An NVFP4 quantiser's fp32 scales: one, or one an expert of weights (MXFP4 reads none).
+Vector fp4_scale(PyObject *t, int fmt, int map, int E) {
+  const Vector v = vector("scale", t);
+  if (fmt == MOE_FP4_NV) need("scale", v, map == MOE_FP4_ROWS_GROUPED ? 1 : E);
+  return v;
 }
 
 // x, fmt, q, sf, row_map, group_offsets, groups, row_index, index_div, scale, workspace,
 // dev_status, stream
 PyObject *fp4_quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return entry<13>(args, n, [](PyObject *const *a) {
-    int64_t src_rows;
-    int cols, E;
-    sizes(a[0], src_rows, cols);
-    const int fmt = int32_arg(a[1]), map = int32_arg(a[4]);
+    const int fmt = int32_arg(a[1]), map = int32_arg(a[4]), div = int32_arg(a[8]);
+    const Matrix x = matrix(a[0], true), q = matrix(a[2]);
+    const int cols = as_int32(x.cols);
+    const int64_t rows = q.rows;
+    need("q", q, rows, cols / 2);
+    int E;
     const int32_t *off = offsets(a[5], E, int32_arg(a[6]));
-    const int64_t rows = dim(a[2], 0);
-    const auto x = ptr<uint16_t>(a[0]);
-    const auto q = ptr<uint8_t>(a[2]);
-    const auto sf = ptr<uint8_t>(a[3]);
-    const auto index = ptr<int32_t>(a[7]);
-    const int div = int32_arg(a[8]);
-    const auto scale = ptr<float>(a[9]);
-    void *const ws = ptr<void>(a[10]);
-    const auto status = ptr<int32_t>(a[11]);
-    const int64_t ldx = ld(a[0]), ldq = ld(a[2]);
-    const size_t sf_bytes = numel(a[3]), ws_bytes = numel(a[10]);
+    const Vector sf = vector("sf", a[3]), index = vector("row_index", a[7]),
+                 scale = fp4_scale(a[9], fmt, map, E), ws = vector("workspace", a[10]),
+                 status = vector("dev_status", a[11]);
+    need("row_index", index, rows);
+    need("dev_status", status, 1);
     const moe_stream_t st = stream(a[12]);
     return unlocked([=] {
-      return moe_fp4_quantize(x, ldx, src_rows, index, div, rows, cols, fmt, map, off, E, scale, q,
-                              ldq, sf, sf_bytes, ws, ws_bytes, status, st);
+      return moe_fp4_quantize(x.as<uint16_t>(), x.ld, x.rows, index.as<int32_t>(), div, rows, cols,
+                              fmt, map, off, E, scale.as<float>(), q.as<uint8_t>(), q.ld,
+                              sf.as<uint8_t>(), (size_t)sf.n, ws.p, (size_t)ws.n,
+                              status.as<int32_t>(), st);
     });
   });
 }
@@ -244,20 +298,17 @@ PyObject *fp4_quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
 // q, sf, fmt, x, row_map, group_offsets, groups, scale, stream
 PyObject *fp4_dequantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return entry<9>(args, n, [](PyObject *const *a) {
-    int64_t rows;
-    int cols, E;
-    sizes(a[3], rows, cols);
     const int fmt = int32_arg(a[2]), map = int32_arg(a[4]);
+    const Matrix q = matrix(a[0]), x = matrix(a[3], true);
+    const int cols = as_int32(x.cols);
+    need("q", q, x.rows, cols / 2);
+    int E;
     const int32_t *off = offsets(a[5], E, int32_arg(a[6]));
-    const auto q = ptr<uint8_t>(a[0]);
-    const auto sf = ptr<uint8_t>(a[1]);
-    const auto x = ptr<uint16_t>(a[3]);
-    const auto scale = ptr<float>(a[7]);
-    const int64_t ldq = ld(a[0]), ldx = ld(a[3]);
-    const size_t sf_bytes = numel(a[1]);
+    const Vector sf = vector("sf", a[1]), scale = fp4_scale(a[7], fmt, map, E);
     const moe_stream_t st = stream(a[8]);
     return unlocked([=] {
-      return moe_fp4_dequantize(q, ldq, sf, sf_bytes, rows, cols, fmt, map, off, E, scale, x, ldx, st);
+      return moe_fp4_dequantize(q.as<uint8_t>(), q.ld, sf.as<uint8_t>(), (size_t)sf.n, x.rows, cols,
+                                fmt, map, off, E, scale.as<float>(), x.as<uint16_t>(), x.ld, st);
     });
   });
 }
@@ -267,16 +318,19 @@ PyObject *fp4_experts(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return entry<7>(args, n, [](PyObject *const *a) {
     const auto w = reinterpret_cast<const moe_fp4_weights *>(as_int(a[0]));
     const auto b = reinterpret_cast<const moe_fp4_buffers *>(as_int(a[1]));
-    int64_t T;
-    int d;
-    sizes(a[2], T, d);
-    const int tokens = as_int32(T), k = int32_arg(a[4]);
-    const auto x = ptr<uint16_t>(a[2]);
-    const auto s2f = ptr<int32_t>(a[3]);
-    const auto off = ptr<int32_t>(a[5]);
-    const int64_t ldx = ld(a[2]);
+    const Matrix x = matrix(a[2], true);
+    const int tokens = as_int32(x.rows), k = int32_arg(a[4]);
+    const Vector s2f = vector("sorted_to_flat", a[3]), off = vector("group_offsets", a[5]);
+    if (w != nullptr && b != nullptr) {
+      need("x", x, tokens, w->d);
+      need("sorted_to_flat", s2f, b->rows_cap);
+      need("group_offsets", off, (int64_t)w->E + 1);
+    }
     const moe_stream_t st = stream(a[6]);
-    return unlocked([=] { return moe_fp4_experts(w, b, x, ldx, tokens, s2f, k, off, st); });
+    return unlocked([=] {
+      return moe_fp4_experts(w, b, x.as<uint16_t>(), x.ld, tokens, s2f.as<int32_t>(), k,
+                             off.as<int32_t>(), st);
+    });
   });
 }
 
@@ -304,7 +358,9 @@ PyMODINIT_FUNC PyInit__native(void) {
   s_stride = PyUnicode_InternFromString("stride");
   s_numel = PyUnicode_InternFromString("numel");
   s_shape = PyUnicode_InternFromString("shape");
-  if (s_data_ptr == nullptr || s_stride == nullptr || s_numel == nullptr || s_shape == nullptr)
+  s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
+  if (s_data_ptr == nullptr || s_stride == nullptr || s_numel == nullptr || s_shape == nullptr ||
+      s_is_contiguous == nullptr)
     return nullptr;
   return PyModule_Create(&module);
 }

@@ -95,3 +95,77 @@ def test_from_weights():
 def test_arranged_scales_are_whole_rows():
     with pytest.raises(ValueError, match="no rows of 4"):
         L.moe_fp4_arrange_scales(u8(67), 64, L.FP4_NV, L.FP4_ROWS_EXPERTS, 1, u8(4096))
+
+
+# ------------------------------------------------------- rows, columns and elements
+class NoStream:  # the null stream, without asking CUDA for the current one
+    cuda_stream = 0
+
+
+def i32(n):
+    return torch.zeros(n, dtype=torch.int32)
+
+
+def i8(*s):
+    return torch.zeros(*s, dtype=torch.int8)
+
+
+def refuses(f, good, **bad):
+    """f(**good, changed by one of bad) names the operand that is too small."""
+    for name, values in bad.items():
+        for v in values:
+            with pytest.raises(ValueError, match=name + "(:| is| has)"):
+                f(stream=NoStream, **dict(good, **{name: v}))
+
+
+def test_act8_rows():
+    x = bf(8, 72)
+    refuses(L.moe_act8_quantize, dict(x=x, q=i8(8, 72), scales=bf(8, 3)), q=[i8(7, 72), i8(8, 128)[:, :64]],
+            scales=[bf(7, 3), bf(1, 3), bf(8, 4)[:, :2]], group_offsets=[i32(6)[::2]])
+    refuses(L.moe_act8_dequantize, dict(x=x, q=i8(8, 72), scales=bf(8, 3)), q=[i8(7, 72)],
+            scales=[bf(7, 3)])
+    good = dict(h=bf(8, 144), act=bf(8, 72), q=i8(8, 144), scales=bf(8, 6))
+    refuses(L.moe_act8_swiglu_fwd, good, h=[bf(7, 144), bf(8, 200)[:, :72]], q=[i8(5, 144)],
+            scales=[bf(7, 6), bf(8, 6)[:, :5]])
+    good = dict(q=i8(8, 144), scales=bf(8, 6), dact=bf(8, 72), dh=bf(8, 144), act=bf(8, 72))
+    refuses(L.moe_act8_swiglu_bwd, good, q=[i8(5, 144)], scales=[bf(7, 6)], dh=[bf(7, 144)],
+            act=[bf(7, 72), bf(8, 144)[:, :64]])
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_fp4_rows(fmt):
+    nb = L.moe_fp4_scale_bytes(8, 64, fmt, L.FP4_ROWS_GROUPED, 2)
+    good = dict(x=bf(8, 64), fmt=fmt, q=u8(8, 32), sf=u8(nb), group_offsets=i32(3))
+    refuses(L.moe_fp4_quantize, good, row_index=[i32(0), i32(7), i32(16)[::2]], sf=[u8(2 * nb)[::2]],
+            workspace=[u8(8192)[::2]], dev_status=[i32(0)], q=[u8(8, 64)[:, :16]])
+    good = dict(q=u8(8, 32), sf=u8(nb), fmt=fmt, x=bf(8, 64), group_offsets=i32(3))
+    refuses(L.moe_fp4_dequantize, good, q=[u8(7, 32)], sf=[u8(2 * nb)[::2]])
+    nw = L.moe_fp4_scale_bytes(2 * 64, 64, fmt, L.FP4_ROWS_EXPERTS, 2)
+    w = dict(row_map=L.FP4_ROWS_EXPERTS, groups=2)
+    if fmt == L.FP4_NV:  # one scale an expert
+        refuses(L.moe_fp4_quantize, dict(w, x=bf(128, 64), fmt=fmt, q=u8(128, 32), sf=u8(nw)), scale=[f32(1)])
+        refuses(L.moe_fp4_dequantize, dict(w, x=bf(128, 64), fmt=fmt, q=u8(128, 32), sf=u8(nw)),
+                scale=[f32(1)])
+
+
+def test_weights_and_products():
+    w = dict(w=bf(2, 64, 128), fmt=1, row_map=L.FP4_ROWS_EXPERTS, q=u8(2, 128, 32), sf=u8(1 << 16))
+    refuses(L.moe_fp4_quantize_weights, w, q=[u8(1, 128, 32)], scale=[f32(1)])
+    nb = L.moe_fp4_scale_bytes
+    A = dict(A=u8(8, 32), sfa=u8(nb(8, 64, 1, L.FP4_ROWS_GROUPED, 2)), B=u8(2, 128, 32),
+             sfb=u8(nb(256, 64, 1, L.FP4_ROWS_EXPERTS, 2)), fmt=1, group_offsets=i32(3), C=bf(8, 128))
+    refuses(L.moe_gmm_fp4, A, sfa=[u8(512)], sfb=[u8(512)], group_offsets=[i32(2), i32(6)[::2]],
+                C=[bf(7, 128), bf(8, 256)[:, :120]], b_scale=[f32(1), f32(4)[::2]])
+    A.update(C=None, epilogue=L.EPI_SWIGLU_FWD, Q2=u8(8, 32), sf2=u8(1 << 16),
+             sfb=u8(nb(256, 64, 1, L.FP4_ROWS_SWIGLU, 2)))
+    refuses(L.moe_gmm_fp4, A, Q2=[u8(7, 32)], C=[bf(7, 128)], sf2=[u8(1 << 17)[::2]], sfb=[u8(512)])
+
+
+def test_experts_call():
+    w = experts()
+    arg = L.Fp4BuffersArg(12)  # of 12 rows
+    call = lambda x, s2f, off: L.moe_fp4_experts(w.arg, arg, x, s2f, 2, off, NoStream)  # noqa: E731
+    for x, s2f, off in ((bf(6, D)[:, :32], i32(12), i32(E + 1)), (bf(6, D), i32(11), i32(E + 1)),
+                        (bf(6, D), i32(12), i32(E)), (bf(6, D), i32(24)[::2], i32(E + 1))):
+        with pytest.raises(ValueError, match="x is|sorted_to_flat|group_offsets"):
+            call(x, s2f, off)
