@@ -474,16 +474,24 @@ FP4_ROWS_SWIGLU = 2
 FP4_ROWS_EXPERTS = 3
 
 
-def _need(name, t, n):
-    """t: None, or a contiguous tensor of n elements at least."""
+def _need_type(name, t, *types):
+    """t: None, or of one of `types`; torch.uint8 stands for any type of one byte."""
+    if t is not None and t.dtype not in types and not (torch.uint8 in types and t.element_size() == 1):
+        raise ValueError("%s is %s, not %s" % (name, t.dtype, " or ".join(map(str, types))))
+
+
+def _need(name, t, n, *types):
+    """t: None, or a contiguous tensor of n elements at least, of one of `types`."""
+    _need_type(name, t, *types)
     if t is not None and (t.numel() < n or not t.is_contiguous()):
         raise ValueError("%s: %s, strides %s, for %d contiguous elements"
                          % (name, tuple(t.shape), t.stride(), n))
 
 
-def _need_matrix(name, t, rows, cols):
-    """t: None, or a matrix that holds [rows, cols] (a leading dimension under cols is left to
-    the library, which refuses it)."""
+def _need_matrix(name, t, rows, cols, *types):
+    """t: None, or a matrix of one of `types` that holds [rows, cols] (a leading dimension under
+    cols is left to the library, which refuses it)."""
+    _need_type(name, t, *types)
     if t is not None and rows > 0 and (t.shape[-2] < rows or t.shape[-1] < cols <= t.stride(-2)):
         raise ValueError("%s is %s for [%d, %d]" % (name, tuple(t.shape), rows, cols))
 
@@ -517,9 +525,10 @@ def moe_fp4_quantize_weights(w, fmt, row_map, q, sf, scale=None, stream=None):
     """w bf16 [E, K, N] contiguous -> q uint8 [E, N, K / 2], sf uint8 scale atoms."""
     E, K, N = w.shape
     assert w.is_contiguous() and q.is_contiguous(), "contiguous tensors only"
-    _need("q", q, E * N * (K // 2))
-    if fmt == FP4_NV:
-        _need("scale", scale, E)
+    _need_type("w", w, torch.bfloat16)
+    _need("q", q, E * N * (K // 2), torch.uint8)
+    _need("sf", sf, 0, torch.uint8)
+    _need("scale", scale, E if fmt == FP4_NV else 0, torch.float32)
     _check(LIB.moe_fp4_quantize_weights(_ptr(w), E, K, N, fmt, row_map, _ptr(scale), _ptr(q),
                                         _ptr(sf), sf.numel(), _stream(stream)))
 
@@ -529,6 +538,8 @@ def moe_fp4_arrange_scales(scales, cols, fmt, row_map, E, sf, stream=None):
     assert scales.is_contiguous(), "contiguous tensors only"
     blocks = cols // (16 if fmt == FP4_NV else 32)
     rows = scales.numel() // max(blocks, 1)
+    _need("scales", scales, 0, torch.uint8)
+    _need("sf", sf, 0, torch.uint8)
     if rows * blocks != scales.numel():
         raise ValueError("%d scales are no rows of %d" % (scales.numel(), blocks))
     _check(LIB.moe_fp4_arrange_scales(_ptr(scales), rows, cols, fmt, row_map, E, _ptr(sf),
@@ -543,17 +554,21 @@ def moe_gmm_fp4(A, sfa, B, sfb, fmt, group_offsets, K=None, epilogue=EPI_NONE, C
     K = 2 * kb if K is None else K
     rows, swiglu = A.shape[0], epilogue == EPI_SWIGLU_FWD
     c_dtype = DTYPE_F32 if C is not None and C.dtype == torch.float32 else DTYPE_BF16
-    _need_matrix("A", A, rows, K // 2)
-    _need_matrix("B", B, N, K // 2)
-    _need_matrix("C", C, rows, N)
+    _need_matrix("A", A, rows, K // 2, torch.uint8)
+    _need_matrix("B", B, N, K // 2, torch.uint8)
+    _need_matrix("C", C, rows, N, torch.bfloat16, torch.float32)
     if swiglu:
-        _need_matrix("Q2", Q2, rows, N // 4)
-        _need("sf2", sf2, 0)
-    _need("sfa", sfa, moe_fp4_scale_bytes(rows, K, fmt, FP4_ROWS_GROUPED, E))
+        _need_matrix("Q2", Q2, rows, N // 4, torch.uint8)
+        _need("sf2", sf2, 0, torch.uint8)
+    _need("sfa", sfa, moe_fp4_scale_bytes(rows, K, fmt, FP4_ROWS_GROUPED, E), torch.uint8)
     _need("sfb", sfb, moe_fp4_scale_bytes(E * N, K, fmt,
-                                          FP4_ROWS_SWIGLU if swiglu else FP4_ROWS_EXPERTS, E))
-    _need("group_offsets", group_offsets, E + 1)
-    _need("b_scale", b_scale, E)
+                                          FP4_ROWS_SWIGLU if swiglu else FP4_ROWS_EXPERTS, E),
+          torch.uint8)
+    _need("group_offsets", group_offsets, E + 1, torch.int32)
+    _need("a_scale", a_scale, 1, torch.float32)
+    _need("b_scale", b_scale, E, torch.float32)
+    _need("q2_scale", q2_scale, 1, torch.float32)
+    _need("dev_status", dev_status, 1, torch.int32)
     _check(LIB.moe_gmm_fp4(_ptr(A), _ld(A), _ptr(sfa), _ptr(a_scale), _ptr(B), B.stride(1),
                            B.stride(0), _ptr(sfb), _ptr(b_scale), fmt, _ptr(group_offsets), E,
                            A.shape[0], K, N, epilogue, _ptr(C), c_dtype,

@@ -6,8 +6,9 @@
 //
 // Every function takes its arguments by position, tensors as such (None where the C
 // ABI takes a null pointer), the stream as an integer last, and returns the status.
-// The C ABI knows leading dimensions alone; that every operand has the rows, columns
-// and elements which the call's sizes name is checked here (ValueError).
+// The C ABI knows addresses and leading dimensions alone; that every operand has the
+// rows, columns and elements which the call's sizes name, and their type, is checked here
+// (ValueError).
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -15,7 +16,9 @@
 
 namespace {
 
-PyObject *s_data_ptr, *s_stride, *s_numel, *s_shape, *s_is_contiguous;
+PyObject *s_data_ptr, *s_stride, *s_numel, *s_shape, *s_is_contiguous, *s_dtype,
+    *s_itemsize;
+PyObject *t_bf16, *t_u8, *t_i32, *t_f32;  // torch's types
 
 // An argument's value, or an error that ends the call.
 struct Failed {};
@@ -71,6 +74,23 @@ struct Tuple {
   Tuple(const Tuple &) = delete;
 };
 
+// `name` of the call holds elements of `type`; any type of one byte where that is uint8
+// (codes and scales, as which of them they are called).
+void check_type(const char *name, PyObject *t, PyObject *type) {
+  PyObject *d = PyObject_GetAttr(t, s_dtype);
+  if (d == nullptr) throw Failed{};
+  bool ok = d == type;
+  if (!ok && type == t_u8) {
+    PyObject *size = PyObject_GetAttr(d, s_itemsize);
+    ok = size != nullptr && PyLong_AsLong(size) == 1;
+    Py_XDECREF(size);
+    PyErr_Clear();
+  }
+  if (!ok) PyErr_Format(PyExc_ValueError, "%s is %S, not %S", name, d, type);
+  Py_DECREF(d);
+  if (!ok) throw Failed{};
+}
+
 // A row-major matrix (the last two dimensions of a tensor).
 struct Matrix {
   void *p;
@@ -81,7 +101,7 @@ struct Matrix {
   }
 };
 
-Matrix matrix(PyObject *t, bool exact = false) {
+Matrix matrix(const char *name, PyObject *t, PyObject *type, bool exact = false) {
   Tuple shape(PyObject_GetAttr(t, s_shape));
   const Py_ssize_t dims = PyTuple_GET_SIZE(shape.o);
   if (dims < 2 || (exact && dims > 2)) {
@@ -101,6 +121,7 @@ Matrix matrix(PyObject *t, bool exact = false) {
     }
     m.ld = item(stride.o, -2);
   }
+  check_type(name, t, type);
   m.p = reinterpret_cast<void *>(call_int(t, s_data_ptr));
   return m;
 }
@@ -125,7 +146,7 @@ struct Vector {
   }
 };
 
-Vector vector(const char *name, PyObject *t) {
+Vector vector(const char *name, PyObject *t, PyObject *type) {
   Vector v;
   if (t == Py_None) return v;
   v.given = true;
@@ -138,6 +159,7 @@ Vector vector(const char *name, PyObject *t) {
     PyErr_Format(PyExc_ValueError, "%s is not contiguous", name);
     throw Failed{};
   }
+  check_type(name, t, type);
   v.p = reinterpret_cast<void *>(call_int(t, s_data_ptr));
   return v;
 }
@@ -152,7 +174,7 @@ void need(const char *name, const Vector &v, int64_t n) {
 const int32_t *offsets(PyObject *t, int &E, int without) {
   E = without;
   if (t == Py_None) return nullptr;
-  const Vector v = vector("group_offsets", t);
+  const Vector v = vector("group_offsets", t, t_i32);
   E = as_int32(v.n - 1);
   return v.as<const int32_t>();
 }
@@ -187,7 +209,8 @@ moe_status_t unlocked(F f) {
 // x, q, scales, group_offsets, stream
 PyObject *act8_quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return entry<5>(args, n, [](PyObject *const *a) {
-    const Matrix x = matrix(a[0], true), q = matrix(a[1]), s = matrix(a[2]);
+    const Matrix x = matrix("x", a[0], t_bf16, true), q = matrix("q", a[1], t_u8),
+                 s = matrix("scales", a[2], t_bf16);
     const int cols = as_int32(x.cols);
     need("q", q, x.rows, cols);
     need("scales", s, x.rows, blocks32(cols));
@@ -204,7 +227,8 @@ PyObject *act8_quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
 // q, scales, x, group_offsets, stream
 PyObject *act8_dequantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return entry<5>(args, n, [](PyObject *const *a) {
-    const Matrix q = matrix(a[0]), s = matrix(a[1]), x = matrix(a[2], true);
+    const Matrix q = matrix("q", a[0], t_u8), s = matrix("scales", a[1], t_bf16),
+                 x = matrix("x", a[2], t_bf16, true);
     const int cols = as_int32(x.cols);
     need("q", q, x.rows, cols);
     need("scales", s, x.rows, blocks32(cols));
@@ -221,7 +245,8 @@ PyObject *act8_dequantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
 // h, act, q, scales, group_offsets, stream
 PyObject *act8_swiglu_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return entry<6>(args, n, [](PyObject *const *a) {
-    const Matrix h = matrix(a[0]), act = matrix(a[1], true), q = matrix(a[2]), s = matrix(a[3]);
+    const Matrix h = matrix("h", a[0], t_bf16), act = matrix("act", a[1], t_bf16, true),
+                 q = matrix("q", a[2], t_u8), s = matrix("scales", a[3], t_bf16);
     const int64_t rows = act.rows;
     const int F = as_int32(act.cols);
     need("h", h, rows, 2 * act.cols);
@@ -240,7 +265,8 @@ PyObject *act8_swiglu_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
 // q, scales, dact, dh, act, group_offsets, stream
 PyObject *act8_swiglu_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return entry<7>(args, n, [](PyObject *const *a) {
-    const Matrix q = matrix(a[0]), s = matrix(a[1]), dact = matrix(a[2], true), dh = matrix(a[3]);
+    const Matrix q = matrix("q", a[0], t_u8), s = matrix("scales", a[1], t_bf16),
+                 dact = matrix("dact", a[2], t_bf16, true), dh = matrix("dh", a[3], t_bf16);
     const int64_t rows = dact.rows;
     const int F = as_int32(dact.cols);
     need("q", q, rows, 2 * dact.cols);
@@ -248,7 +274,7 @@ PyObject *act8_swiglu_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
     need("dh", dh, rows, 2 * dact.cols);
     Matrix act = {nullptr, 0, 0, 0};
     if (a[4] != Py_None) {
-      act = matrix(a[4]);
+      act = matrix("act", a[4], t_bf16);
       need("act", act, rows, F);
     }
     int E;
@@ -264,7 +290,7 @@ PyObject *act8_swiglu_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 // An NVFP4 quantiser's fp32 scales: one, or one an expert of weights (MXFP4 reads none).
 Vector fp4_scale(PyObject *t, int fmt, int map, int E) {
-  const Vector v = vector("scale", t);
+  const Vector v = vector("scale", t, t_f32);
   if (fmt == MOE_FP4_NV) need("scale", v, map == MOE_FP4_ROWS_GROUPED ? 1 : E);
   return v;
 }
@@ -274,15 +300,15 @@ Vector fp4_scale(PyObject *t, int fmt, int map, int E) {
 PyObject *fp4_quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return entry<13>(args, n, [](PyObject *const *a) {
     const int fmt = int32_arg(a[1]), map = int32_arg(a[4]), div = int32_arg(a[8]);
-    const Matrix x = matrix(a[0], true), q = matrix(a[2]);
+    const Matrix x = matrix("x", a[0], t_bf16, true), q = matrix("q", a[2], t_u8);
     const int cols = as_int32(x.cols);
     const int64_t rows = q.rows;
     need("q", q, rows, cols / 2);
     int E;
     const int32_t *off = offsets(a[5], E, int32_arg(a[6]));
-    const Vector sf = vector("sf", a[3]), index = vector("row_index", a[7]),
-                 scale = fp4_scale(a[9], fmt, map, E), ws = vector("workspace", a[10]),
-                 status = vector("dev_status", a[11]);
+    const Vector sf = vector("sf", a[3], t_u8), index = vector("row_index", a[7], t_i32),
+                 scale = fp4_scale(a[9], fmt, map, E), ws = vector("workspace", a[10], t_u8),
+                 status = vector("dev_status", a[11], t_i32);
     need("row_index", index, rows);
     need("dev_status", status, 1);
     const moe_stream_t st = stream(a[12]);
@@ -299,12 +325,12 @@ PyObject *fp4_quantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
 PyObject *fp4_dequantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return entry<9>(args, n, [](PyObject *const *a) {
     const int fmt = int32_arg(a[2]), map = int32_arg(a[4]);
-    const Matrix q = matrix(a[0]), x = matrix(a[3], true);
+    const Matrix q = matrix("q", a[0], t_u8), x = matrix("x", a[3], t_bf16, true);
     const int cols = as_int32(x.cols);
     need("q", q, x.rows, cols / 2);
     int E;
     const int32_t *off = offsets(a[5], E, int32_arg(a[6]));
-    const Vector sf = vector("sf", a[1]), scale = fp4_scale(a[7], fmt, map, E);
+    const Vector sf = vector("sf", a[1], t_u8), scale = fp4_scale(a[7], fmt, map, E);
     const moe_stream_t st = stream(a[8]);
     return unlocked([=] {
       return moe_fp4_dequantize(q.as<uint8_t>(), q.ld, sf.as<uint8_t>(), (size_t)sf.n, x.rows, cols,
@@ -318,9 +344,10 @@ PyObject *fp4_experts(PyObject *, PyObject *const *args, Py_ssize_t n) {
   return entry<7>(args, n, [](PyObject *const *a) {
     const auto w = reinterpret_cast<const moe_fp4_weights *>(as_int(a[0]));
     const auto b = reinterpret_cast<const moe_fp4_buffers *>(as_int(a[1]));
-    const Matrix x = matrix(a[2], true);
+    const Matrix x = matrix("x", a[2], t_bf16, true);
     const int tokens = as_int32(x.rows), k = int32_arg(a[4]);
-    const Vector s2f = vector("sorted_to_flat", a[3]), off = vector("group_offsets", a[5]);
+    const Vector s2f = vector("sorted_to_flat", a[3], t_i32),
+                 off = vector("group_offsets", a[5], t_i32);
     if (w != nullptr && b != nullptr) {
       need("x", x, tokens, w->d);
       need("sorted_to_flat", s2f, b->rows_cap);
@@ -354,13 +381,20 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods};
 }  // namespace
 
 PyMODINIT_FUNC PyInit__native(void) {
-  s_data_ptr = PyUnicode_InternFromString("data_ptr");
-  s_stride = PyUnicode_InternFromString("stride");
-  s_numel = PyUnicode_InternFromString("numel");
-  s_shape = PyUnicode_InternFromString("shape");
-  s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
-  if (s_data_ptr == nullptr || s_stride == nullptr || s_numel == nullptr || s_shape == nullptr ||
-      s_is_contiguous == nullptr)
-    return nullptr;
+  struct {
+    PyObject **o;
+    const char *name;
+  } const names[] = {{&s_data_ptr, "data_ptr"}, {&s_stride, "stride"}, {&s_numel, "numel"},
+                     {&s_shape, "shape"}, {&s_is_contiguous, "is_contiguous"}, {&s_dtype, "dtype"},
+                     {&s_itemsize, "itemsize"}},
+      types[] = {{&t_bf16, "bfloat16"}, {&t_u8, "uint8"}, {&t_i32, "int32"}, {&t_f32, "float32"}};
+  for (const auto &n : names)
+    if ((*n.o = PyUnicode_InternFromString(n.name)) == nullptr) return nullptr;
+  PyObject *torch = PyImport_ImportModule("torch");
+  if (torch == nullptr) return nullptr;
+  for (const auto &n : types) *n.o = PyObject_GetAttrString(torch, n.name);
+  Py_DECREF(torch);
+  for (const auto &n : types)
+    if (*n.o == nullptr) return nullptr;
   return PyModule_Create(&module);
 }

@@ -258,6 +258,9 @@ class Fp4Layer:
         if T > s.T or logits.shape != (T, s.E):
             raise ValueError("x of %d tokens (at most %d), logits of shape %s"
                              % (T, s.T, tuple(logits.shape)))
+        L._need_matrix("x", x, T, s.d, torch.bfloat16)
+        L._need_type("logits", logits, torch.float32)
+        L._need("expert_bias", expert_bias, s.E, torch.float32)
         idx, w, f2s, out = self.topk_idx[:T], self.topk_w[:T], self.f2s[:T * s.k], self.out[:T]
         if T == 0:
             return out

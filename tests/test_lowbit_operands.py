@@ -169,3 +169,59 @@ def test_experts_call():
                         (bf(6, D), i32(12), i32(E)), (bf(6, D), i32(24)[::2], i32(E + 1))):
         with pytest.raises(ValueError, match="x is|sorted_to_flat|group_offsets"):
             call(x, s2f, off)
+
+
+# ------------------------------------------------------------------------- types
+def test_types_of_the_native_calls():
+    """Elements of another type would be read as bf16, int32 or fp32."""
+    i64 = lambda n: i32(n).long()  # noqa: E731
+    a = dict(x=bf(8, 64), q=i8(8, 64), scales=bf(8, 2), group_offsets=i32(3))
+    refuses(L.moe_act8_quantize, a, x=[f32(8, 64), bf(8, 64).half()], q=[f32(8, 64)],
+            scales=[f32(8, 2)], group_offsets=[i64(3)])
+    refuses(L.moe_act8_dequantize, a, x=[f32(8, 64)], q=[bf(8, 64)], scales=[f32(8, 2)])
+    a = dict(h=bf(8, 128), act=bf(8, 64), q=i8(8, 128), scales=bf(8, 4))
+    refuses(L.moe_act8_swiglu_fwd, a, h=[f32(8, 128)], act=[f32(8, 64)], q=[i32(1024).view(8, 128)],
+            scales=[bf(8, 4).half()])
+    a = dict(q=i8(8, 128), scales=bf(8, 4), dact=bf(8, 64), dh=bf(8, 128), act=bf(8, 64))
+    refuses(L.moe_act8_swiglu_bwd, a, q=[f32(8, 128)], scales=[f32(8, 4)], dact=[f32(8, 64)],
+            dh=[f32(8, 128)], act=[f32(8, 64)])
+    sf = u8(L.moe_fp4_scale_bytes(8, 64, 1, 1, 2))
+    a = dict(x=bf(8, 64), fmt=1, q=u8(8, 32), sf=sf, group_offsets=i32(3))
+    refuses(L.moe_fp4_quantize, a, x=[f32(8, 64)], q=[bf(8, 32)], sf=[sf.float()],
+            group_offsets=[i64(3)], row_index=[i64(8)], scale=[f32(1).double(), bf(1)],
+            dev_status=[i64(1)])
+    refuses(L.moe_fp4_dequantize, a, x=[f32(8, 64)], q=[f32(8, 32)], sf=[sf.float()], scale=[bf(1)])
+    w, arg = experts(), L.Fp4BuffersArg(12)
+    for x, s2f, off in ((f32(6, D), i32(12), i32(E + 1)), (bf(6, D), i64(12), i32(E + 1)),
+                        (bf(6, D), i32(12), i64(E + 1))):
+        with pytest.raises(ValueError, match="is torch"):
+            L.moe_fp4_experts(w.arg, arg, x, s2f, 2, off, NoStream)
+
+
+def test_codes_are_any_bytes():
+    """What checkpoints call them does not matter: no work here, and no refusal either."""
+    L.moe_act8_quantize(bf(0, 64), u8(0, 64), bf(0, 2), stream=NoStream)
+    L.moe_fp4_dequantize(i8(0, 32), torch.zeros(0, dtype=torch.float8_e4m3fn), 1, bf(0, 64),
+                         group_offsets=i32(3), stream=NoStream)
+
+
+def test_types_of_weights_and_products():
+    w = dict(w=bf(2, 64, 128), fmt=1, row_map=L.FP4_ROWS_EXPERTS, q=u8(2, 128, 32), sf=u8(1 << 16))
+    refuses(L.moe_fp4_quantize_weights, w, w=[f32(2, 64, 128)], q=[f32(2, 128, 32)], scale=[bf(2)])
+    refuses(L.moe_fp4_arrange_scales, dict(scales=u8(128, 4), cols=64, fmt=1, row_map=3, E=1, sf=u8(4096)),
+            scales=[f32(128, 4)], sf=[f32(4096)])
+    nb = L.moe_fp4_scale_bytes
+    a = dict(A=u8(8, 32), sfa=u8(nb(8, 64, 1, L.FP4_ROWS_GROUPED, 2)), B=u8(2, 128, 32),
+             sfb=u8(nb(256, 64, 1, L.FP4_ROWS_EXPERTS, 2)), fmt=1, group_offsets=i32(3), C=bf(8, 128))
+    refuses(L.moe_gmm_fp4, a, A=[bf(8, 32)], B=[bf(2, 128, 32)], C=[bf(8, 128).half()],
+            group_offsets=[i32(3).long()], a_scale=[bf(1)], b_scale=[bf(2)], dev_status=[i32(1).long()])
+
+
+def test_types_of_the_serving_layer():
+    from mixture_experts_grouped_router_gb300 import layer
+    m = lowbit.Fp4Layer(experts(), layer.LayerShape(8, D, F, E, 2))
+    for x, logits, bias in ((f32(4, D), f32(4, E), None), (bf(4, D), bf(4, E), None),
+                            (bf(4, D), f32(4, E), bf(E)), (bf(4, D), f32(4, E), f32(1)),
+                            (bf(4, D + 32)[:, :32], f32(4, E), None)):
+        with pytest.raises(ValueError, match="is torch|x is|expert_bias"):
+            m.forward(x, logits, expert_bias=bias, stream=NoStream)
