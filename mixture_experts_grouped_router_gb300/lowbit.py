@@ -227,8 +227,9 @@ def fp4_experts(w: Fp4Experts, b: Fp4Buffers, x, sorted_to_flat, k, group_offset
 
 
 class Fp4Layer:
-    """The serving layer for up to T tokens: routing (a LayerShape's router options), the 4-bit
-    experts and the combine.  ``forward(x, logits)`` -> out bf16 [T', d] for x bf16 [T', d],
+    """The serving layer for up to T tokens: routing (a LayerShape's router, alignment and
+    capacity options; biases, other precisions, K-chunks and the auxiliary loss are refused),
+    the 4-bit experts and the combine.  ``forward(x, logits)`` -> out bf16 [T', d] for x bf16 [T', d],
     logits fp32 [T', E], T' <= T (a view of the layer's buffer)."""
 
     def __init__(self, w: Fp4Experts, s):
@@ -237,6 +238,9 @@ class Fp4Layer:
                              % (s.E, s.d, s.f, w.E, w.d, w.f))
         if s.bias:
             raise ValueError("the 4-bit experts take no biases")
+        # the products' precision and schedule and the training loss are not the serving layer's
+        if s.fp8 or s.mxfp8 or s.num_chunks > 1 or s.aux_coeff:
+            raise ValueError("the 4-bit serving layer takes no fp8, mxfp8, num_chunks or aux_coeff")
         dev = w.wo_q.device
         i32 = dict(dtype=torch.int32, device=dev)
         self.w, self.s = w, s

@@ -225,3 +225,11 @@ def test_types_of_the_serving_layer():
                             (bf(4, D + 32)[:, :32], f32(4, E), None)):
         with pytest.raises(ValueError, match="is torch|x is|expert_bias"):
             m.forward(x, logits, expert_bias=bias, stream=NoStream)
+
+
+@pytest.mark.parametrize("option", [dict(fp8=True), dict(mxfp8=True), dict(num_chunks=2),
+                                    dict(aux_coeff=1e-3), dict(bias=True)])
+def test_the_serving_layer_refuses_what_it_does_not_serve(option):
+    from mixture_experts_grouped_router_gb300 import layer
+    with pytest.raises(ValueError, match=list(option)[0]):
+        lowbit.Fp4Layer(experts(), layer.LayerShape(8, D, F, E, 2, **option))
