@@ -96,7 +96,18 @@ def fp4_dequantize(rows: Fp4Rows, group_offsets, out, scale=None, stream=None):
 
 
 # --------------------------------------------------------------- 4-bit experts
-class Fp4Experts:
+class _Fixed:
+    """Attributes are set once: the calls' arguments hold the tensors' addresses, and another
+    tensor in their place would not be read."""
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError("%s is fixed; write into the tensor, or make another %s"
+                                 % (name, type(self).__name__))
+        super().__setattr__(name, value)
+
+
+class Fp4Experts(_Fixed):
     """The weights of E experts in 4 bits: wi [E, 2f, d] ([gate | up]) and wo [E, d, f], both
     K-major codes with scale atoms and (nv) one fp32 scale an expert; x_scale and act_scale
     (fp32 [1], nv) are the calibrated scales of the experts' input and of Act."""
@@ -182,7 +193,7 @@ class Fp4Experts:
         return cls(f, *parts, x_scale, act_scale)
 
 
-class Fp4Buffers:
+class Fp4Buffers(_Fixed):
     """Device buffers of the 4-bit experts for up to rows_cap permuted rows."""
 
     def __init__(self, w: Fp4Experts, rows_cap: int, save_h=False):

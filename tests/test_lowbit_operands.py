@@ -233,3 +233,15 @@ def test_the_serving_layer_refuses_what_it_does_not_serve(option):
     from mixture_experts_grouped_router_gb300 import layer
     with pytest.raises(ValueError, match=list(option)[0]):
         lowbit.Fp4Layer(experts(), layer.LayerShape(8, D, F, E, 2, **option))
+
+
+def test_tensors_are_not_exchanged_behind_the_calls_arguments():
+    """A scale calibrated anew goes into the tensor: the calls hold its address."""
+    w = experts()
+    b = lowbit.Fp4Buffers(w, 12, save_h=True)
+    for o, names in ((w, ("x_scale", "act_scale", "wi_q", "wo_sf", "fmt")), (b, ("h", "y", "x", "rows_cap"))):
+        for n in names:
+            with pytest.raises(AttributeError, match=n):
+                setattr(o, n, getattr(o, n))
+    w.x_scale.fill_(2.0)
+    assert w.arg.x_scale == w.x_scale.data_ptr() and b.arg.y == b.y.data_ptr()
