@@ -157,7 +157,7 @@ struct Maps {
   CUtensorMap t[4];  // token codes, boxes of 32, 64, 96 and 128 rows
   CUtensorMap sw;    // weight scale atoms
   CUtensorMap st[2]; // token scale atoms, boxes of one and two atom rows
-  CUtensorMap c;     // plain output
+  CUtensorMap c;     // plain output (no other form reads it)
 };
 
 struct TileInfo {
@@ -577,11 +577,12 @@ gmm_fp4_kernel(const __grid_constant__ Maps m, const Fp4Params p) {
     tc::fence_mbar_init();
   }
   if (warp == 2 && lane == 0) {
+    // (those that the launch has encoded: kRows loads its tokens by the last box alone)
     tc::tma_prefetch(&m.w);
-    tc::tma_prefetch(&m.t[0]);
+    tc::tma_prefetch(&m.t[EPI == kRows ? 3 : 0]);
     tc::tma_prefetch(&m.sw);
     tc::tma_prefetch(&m.st[0]);
-    tc::tma_prefetch(&m.c);
+    if (EPI == MOE_EPI_NONE) tc::tma_prefetch(&m.c);
   }
   if (warp == 1) {
     tc::tmem_alloc_2sm(&bk.tmem_base, kTmemCols);
@@ -1047,7 +1048,7 @@ moe_status_t launch_gmm_fp4(const GmmFp4Args &a, cudaStream_t s) {
   p.wait_limit_ns = wait_limit_ns();
   p.stall_loads = test_stall_loads();
   p.early = a.early;
-  Maps m;
+  Maps m{};
   const int64_t ac = (a.K + acols - 1) / acols;
   const int64_t stride_b = a.E > 1 ? a.stride_b : (int64_t)a.N * a.ldb;
   bool ok = make_scale_map(&m.sw, a.sfb, ac, (int64_t)a.E * p.w_atoms, atoms, 1) &&
@@ -1070,7 +1071,6 @@ moe_status_t launch_gmm_fp4(const GmmFp4Args &a, cudaStream_t s) {
     const uint32_t box[5] = {kRowBytes, 32, nb, nb, 1};
     ok = ok && make_map(&m.w, a.B, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, dims, st, box,
                         CU_TENSOR_MAP_SWIZZLE_128B);
-    m.c = m.w;
   } else {
     ok = ok && make_code_map(&m.w, a.B, 3, a.K / 2, a.N, a.ldb, a.E, stride_b, BW / 2) &&
          make_out_map(&m.c, a.C, p.c_f32, a.N, a.rows_cap, a.ldc);
