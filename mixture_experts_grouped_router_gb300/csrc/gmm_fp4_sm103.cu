@@ -972,30 +972,34 @@ moe_status_t launch(const Maps &m, const Fp4Params &p, int64_t tiles_upper,
                     cudaStream_t s) {
   constexpr int kSmem = smem_bytes<FMT, EPI>();
   constexpr int kThreads = Lay<FMT, EPI>::threads;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  static int max_clusters = 0;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(gmm_fp4_kernel<FMT, EPI>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (attr_err != cudaSuccess) return;
+  struct Setup {
+    cudaError_t err;
+    int max_clusters;  // clusters of two CTAs that the device holds at a time
+  };
+  static PerDevice<Setup> known;
+  const Setup setup = known.get(current_device(), [] {
+    Setup u{cudaFuncSetAttribute(gmm_fp4_kernel<FMT, EPI>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem),
+            0};
+    if (u.err != cudaSuccess) return u;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (unsigned)num_sms());
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
-    if (cudaOccupancyMaxActiveClusters(&max_clusters, gmm_fp4_kernel<FMT, EPI>, &cfg) !=
+    if (cudaOccupancyMaxActiveClusters(&u.max_clusters, gmm_fp4_kernel<FMT, EPI>, &cfg) !=
             cudaSuccess ||
-        max_clusters <= 0) {
+        u.max_clusters <= 0) {
       cudaGetLastError();
-      max_clusters = num_sms() / 2;
+      u.max_clusters = num_sms() / 2;
     }
+    return u;
   });
-  if (attr_err != cudaSuccess) {
+  if (setup.err != cudaSuccess) {
     set_error("moe_gmm_fp4: cannot reserve %d bytes of shared memory: %s", kSmem,
-              cudaGetErrorString(attr_err));
+              cudaGetErrorString(setup.err));
     return MOE_ERR_CUDA;
   }
-  const int grid = 2 * (int)std::max<int64_t>(1, std::min<int64_t>(max_clusters, tiles_upper));
+  const int grid = 2 * (int)std::max<int64_t>(1, std::min<int64_t>(setup.max_clusters, tiles_upper));
   const cudaError_t e = launch_dependent(gmm_fp4_kernel<FMT, EPI>, grid, kThreads, kSmem, s, m, p);
   if (e != cudaSuccess) {
     set_error("moe_gmm_fp4 launch: %s", cudaGetErrorString(e));

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "moe_gb300.h"
+#include "per_device.h"
 
 namespace moe {
 
@@ -184,19 +185,24 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, s
   return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
 }
 
+// The calling thread's device (-1: there is none; the launch will say so).
+inline int current_device() {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+
 // Blocks of `threads` threads of a kernel that one SM holds at a time.
 template <auto Kernel>
 int blocks_per_sm(int threads) {
-  static int n = 0;  // same answer whichever thread asks first
-  if (n == 0) {
+  static PerDevice<int> known;
+  return known.get(current_device(), [threads] {
     int v = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v, Kernel, threads, 0) != cudaSuccess) {
       cudaGetLastError();
       v = 1;
     }
-    n = v > 0 ? v : 1;
-  }
-  return n;
+    return v > 0 ? v : 1;
+  });
 }
 
 // fp4.cu (4-bit block-scaled formats: quantisers, scale layout)
