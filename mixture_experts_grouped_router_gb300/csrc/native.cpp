@@ -12,13 +12,31 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <initializer_list>
+
 #include "moe_gb300.h"
 
 namespace {
 
-PyObject *s_data_ptr, *s_stride, *s_numel, *s_shape, *s_is_contiguous, *s_dtype,
-    *s_itemsize;
-PyObject *t_bf16, *t_u8, *t_i32, *t_f32;  // torch's types
+PyObject *t_bf16, *t_u8, *t_i8, *t_i32, *t_f32;  // torch's types
+
+// A method or an attribute of a tensor, by its descriptor in torch's tensor type (which
+// saves the look-up); of what is no tensor by its name, which fails as in Python.
+PyTypeObject *tensor_type;
+struct Member {
+  const char *text;
+  PyObject *name, *descr;
+  PyObject *call(PyObject *t) const {
+    if (!PyObject_TypeCheck(t, tensor_type)) return PyObject_CallMethodNoArgs(t, name);
+    return PyObject_Vectorcall(descr, &t, 1, nullptr);
+  }
+  PyObject *get(PyObject *t) const {
+    if (!PyObject_TypeCheck(t, tensor_type)) return PyObject_GetAttr(t, name);
+    return Py_TYPE(descr)->tp_descr_get(descr, t, (PyObject *)Py_TYPE(t));
+  }
+};
+Member m_data_ptr = {"data_ptr"}, m_stride = {"stride"}, m_numel = {"numel"}, m_shape = {"shape"},
+       m_is_contiguous = {"is_contiguous"}, m_dtype = {"dtype"};
 
 // An argument's value, or an error that ends the call.
 struct Failed {};
@@ -39,8 +57,8 @@ int as_int32(int64_t v) {
 
 int int32_arg(PyObject *o) { return as_int32(as_int(o)); }
 
-int64_t call_int(PyObject *t, PyObject *name) {
-  PyObject *r = PyObject_CallMethodNoArgs(t, name);
+int64_t call_int(PyObject *t, const Member &m) {
+  PyObject *r = m.call(t);
   if (r == nullptr) throw Failed{};
   const unsigned long long v = PyLong_AsUnsignedLongLong(r);
   Py_DECREF(r);
@@ -74,14 +92,21 @@ struct Tuple {
   Tuple(const Tuple &) = delete;
 };
 
+bool is_contiguous(PyObject *t) {
+  PyObject *r = m_is_contiguous.call(t);
+  if (r == nullptr) throw Failed{};
+  Py_DECREF(r);
+  return r == Py_True;
+}
+
 // `name` of the call holds elements of `type`; any type of one byte where that is uint8
 // (codes and scales, as which of them they are called).
 void check_type(const char *name, PyObject *t, PyObject *type) {
-  PyObject *d = PyObject_GetAttr(t, s_dtype);
+  PyObject *d = m_dtype.get(t);
   if (d == nullptr) throw Failed{};
-  bool ok = d == type;
+  bool ok = d == type || (d == t_i8 && type == t_u8);
   if (!ok && type == t_u8) {
-    PyObject *size = PyObject_GetAttr(d, s_itemsize);
+    PyObject *size = PyObject_GetAttrString(d, "itemsize");
     ok = size != nullptr && PyLong_AsLong(size) == 1;
     Py_XDECREF(size);
     PyErr_Clear();
@@ -102,7 +127,7 @@ struct Matrix {
 };
 
 Matrix matrix(const char *name, PyObject *t, PyObject *type, bool exact = false) {
-  Tuple shape(PyObject_GetAttr(t, s_shape));
+  Tuple shape(m_shape.get(t));
   const Py_ssize_t dims = PyTuple_GET_SIZE(shape.o);
   if (dims < 2 || (exact && dims > 2)) {
     PyErr_SetString(exact ? PyExc_ValueError : PyExc_AssertionError, "matrices only");
@@ -111,10 +136,8 @@ Matrix matrix(const char *name, PyObject *t, PyObject *type, bool exact = false)
   Matrix m;
   m.rows = item(shape.o, -2);
   m.cols = m.ld = item(shape.o, -1);
-  bool empty = false;
-  for (Py_ssize_t i = 0; i < dims; ++i) empty |= item(shape.o, i) == 0;
-  if (!empty) {
-    Tuple stride(PyObject_CallMethodNoArgs(t, s_stride));
+  if (!is_contiguous(t)) {  // (neither an empty one nor a single row is)
+    Tuple stride(m_stride.call(t));
     if (item(stride.o, -1) != 1) {
       PyErr_SetString(PyExc_AssertionError, "row-major tensors only");
       throw Failed{};
@@ -122,7 +145,7 @@ Matrix matrix(const char *name, PyObject *t, PyObject *type, bool exact = false)
     m.ld = item(stride.o, -2);
   }
   check_type(name, t, type);
-  m.p = reinterpret_cast<void *>(call_int(t, s_data_ptr));
+  m.p = reinterpret_cast<void *>(call_int(t, m_data_ptr));
   return m;
 }
 
@@ -150,17 +173,13 @@ Vector vector(const char *name, PyObject *t, PyObject *type) {
   Vector v;
   if (t == Py_None) return v;
   v.given = true;
-  v.n = call_int(t, s_numel);
-  PyObject *r = PyObject_CallMethodNoArgs(t, s_is_contiguous);
-  if (r == nullptr) throw Failed{};
-  const bool whole = r == Py_True;
-  Py_DECREF(r);
-  if (!whole) {
+  v.n = call_int(t, m_numel);
+  if (!is_contiguous(t)) {
     PyErr_Format(PyExc_ValueError, "%s is not contiguous", name);
     throw Failed{};
   }
   check_type(name, t, type);
-  v.p = reinterpret_cast<void *>(call_int(t, s_data_ptr));
+  v.p = reinterpret_cast<void *>(call_int(t, m_data_ptr));
   return v;
 }
 
@@ -381,20 +400,23 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods};
 }  // namespace
 
 PyMODINIT_FUNC PyInit__native(void) {
+  PyObject *torch = PyImport_ImportModule("torch");
+  if (torch == nullptr) return nullptr;
+  PyObject *tensor = PyObject_GetAttrString(torch, "Tensor");
   struct {
     PyObject **o;
     const char *name;
-  } const names[] = {{&s_data_ptr, "data_ptr"}, {&s_stride, "stride"}, {&s_numel, "numel"},
-                     {&s_shape, "shape"}, {&s_is_contiguous, "is_contiguous"}, {&s_dtype, "dtype"},
-                     {&s_itemsize, "itemsize"}},
-      types[] = {{&t_bf16, "bfloat16"}, {&t_u8, "uint8"}, {&t_i32, "int32"}, {&t_f32, "float32"}};
-  for (const auto &n : names)
-    if ((*n.o = PyUnicode_InternFromString(n.name)) == nullptr) return nullptr;
-  PyObject *torch = PyImport_ImportModule("torch");
-  if (torch == nullptr) return nullptr;
-  for (const auto &n : types) *n.o = PyObject_GetAttrString(torch, n.name);
+  } const types[] = {{&t_bf16, "bfloat16"}, {&t_u8, "uint8"}, {&t_i8, "int8"}, {&t_i32, "int32"},
+                     {&t_f32, "float32"}};
+  bool ok = tensor != nullptr && PyType_Check(tensor);
+  for (const auto &n : types) ok = ok && (*n.o = PyObject_GetAttrString(torch, n.name)) != nullptr;
   Py_DECREF(torch);
-  for (const auto &n : types)
-    if (*n.o == nullptr) return nullptr;
+  if (!ok) return nullptr;
+  tensor_type = (PyTypeObject *)tensor;
+  for (Member *m : {&m_data_ptr, &m_stride, &m_numel, &m_shape, &m_is_contiguous, &m_dtype}) {
+    m->name = PyUnicode_InternFromString(m->text);
+    m->descr = PyObject_GetAttrString(tensor, m->text);
+    if (m->name == nullptr || m->descr == nullptr) return nullptr;
+  }
   return PyModule_Create(&module);
 }
