@@ -153,7 +153,7 @@ MOE_DEVINL void quantize_piece(const uint4 *w, int c0, int cols, int lane, float
     const uint32_t code =
         fp4_block_scale<FMT>(__uint_as_float(a << 16), g, 6.0f * g, inv6, inv);
     bf16x8_to_f32(w[i], v);
-    codes[i] = fp4_codes8<FMT>(v, inv);
+    codes[i] = fp4_codes8<FMT>(v, inv, code, g);
     words[i] = scale_word<FMT>(c < cols ? code : 0u, lane);
   }
 }
@@ -412,7 +412,7 @@ fp4_quantize_weights_kernel(const uint16_t *__restrict__ w, int K, int N, int ro
       v[j] = __uint_as_float((uint32_t)tile[kb + b * kB + j][nn] << 16);
 #pragma unroll
     for (int j = 0; j < kB / 8; ++j)
-      codes[b * (kB / 8) + j] = fp4_codes8<FMT>(v + 8 * j, inv);
+      codes[b * (kB / 8) + j] = fp4_codes8<FMT>(v + 8 * j, inv, code, g);
     const int blk = k / kB + b;
     if (blk < 4 * ac) sf[fp4_scale_byte(pr, blk, ac)] = k < K ? (uint8_t)code : (uint8_t)0;
   }

@@ -129,3 +129,87 @@ def test_act_saturates_in_the_epilogue(L, sizes, K):
     sure = (np.abs(gate) > err[:, :F]) & (np.abs(up) > err[:, F:])  # both signs are certain
     assert sure.mean() > 0.9
     assert (got[sure] == np.where((gate < 0) != (up < 0), 15, 7)[sure]).all()
+
+
+TIES = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+
+
+def beside_ties(n, seed):
+    """n blocks [n, 16] and their fp32 scales g [n] of 24 bits: in each block some values whose
+    quotient by the block's scale S g lies 2^-22 to 2^-18 (relative) beside a tie.  S g and the
+    quotient are rounded to 2^-24 each on the way: the side is certain."""
+    rng = np.random.default_rng(seed)
+    S = 1.0 + rng.integers(0, 8, n) / 8
+    tie = rng.choice(TIES, n)
+    x = f64(bf16((1.0 + rng.random(n)) * np.exp2(rng.integers(-6, 7, n))))
+    g = (x / (tie * S)).astype(np.float32)
+    g = (g.view(np.int32) + (rng.choice([-1, 1], n) * rng.integers(8, 17, n)).astype(np.int32)).view(np.float32)
+    d = np.abs(x / (tie * S * g.astype(np.float64)) - 1)
+    assert (d >= 2.0 ** -22).all() and (d <= 2.0 ** -18).all()
+    b = np.zeros((n, 16))
+    b[:, 0] = f64(bf16(6.0 * S * g))  # the block's largest: its scale is S
+    b[:, 3], b[:, 4], b[:, 15] = x, -x, x
+    el, code, _ = R.fp4_quantize(b[:1], "nv", float(g[0]))
+    assert R.e4m3_value(code[0, 0]) == S[0]
+    return b, g
+
+
+def test_quotients_beside_a_tie(L):
+    """A scale of 24 bits (one an expert): the side that the quotient is on decides."""
+    n = 4096
+    b, g = beside_ties(2 * n, 21)
+    x, gg = b.reshape(n, 32), g.reshape(n, 2)
+    x = np.stack([x, x[:, np.r_[16:32, 0:16]]], 1)  # two rows an expert: each scale's blocks
+    for half in (0, 1):
+        gt = torch.from_numpy(np.ascontiguousarray(gg[:, half])).cuda()
+        q = torch.empty(2 * n, 16, dtype=torch.uint8, device="cuda")
+        sf = torch.empty(L.moe_fp4_scale_bytes(2 * n, 32, 1, 3, n), dtype=torch.uint8, device="cuda")
+        L.moe_fp4_quantize(bf16(x.reshape(2 * n, 32)), 1, q, sf, row_map=3, groups=n, scale=gt)
+        got = R.unpack(q.cpu().numpy()).reshape(n, 2, 2, 16)
+        want = np.stack([R.fp4_quantize(b.reshape(n, 2, 16)[i, half][None], "nv", float(gg[i, half]))[0][0]
+                         for i in range(n)])
+        assert (got[:, 0, half] == want).all() and (got[:, 1, 1 - half] == want).all()
+        # the same as weights that are laid out
+        q2, sf2 = torch.empty(n, 2, 16, dtype=torch.uint8, device="cuda"), torch.empty_like(sf)
+        L.moe_fp4_quantize_weights(bf16(x.transpose(0, 2, 1)), 1, 3, q2, sf2, gt)
+        assert (q2.view(2 * n, 16) == q).all()
+
+
+@pytest.mark.parametrize("i", range(12))
+def test_quotients_beside_a_tie_of_the_tensors_scale(L, i):
+    """As activations, one scale for all rows, directly and gathered."""
+    b, g = beside_ties(12, 22)
+    g = float(g[i])
+    x = np.repeat(b[i][None], 8, 0).reshape(4, 32)
+    el, code, _ = R.fp4_quantize(x, "nv", g)
+    gt = torch.tensor([g], device="cuda")
+    for idx in (None, i32([3, 1, 0, 2])):
+        q = torch.empty(4, 16, dtype=torch.uint8, device="cuda")
+        sf = torch.empty(L.moe_fp4_scale_bytes(4, 32, 1, 1, 1), dtype=torch.uint8, device="cuda")
+        L.moe_fp4_quantize(bf16(x), 1, q, sf, group_offsets=i32([0, 4]), row_index=idx, scale=gt)
+        assert (R.unpack(q.cpu().numpy()) == el).all()
+
+
+@pytest.mark.parametrize("g", [0.0137, 6.0 / 2688, 1.1e-30, 3.3e20])
+def test_scales_of_24_bits_over_the_whole_range(L, g):
+    """Bit for bit but for ratios 2^-22 beside a tie, of which there are next to none."""
+    g = float(np.float32(g))
+    rng = np.random.default_rng(23)
+    n, cols = 261, 96
+    x = whole_range(rng, n, cols)
+    q = torch.empty(n, cols // 2, dtype=torch.uint8, device="cuda")
+    sf = torch.empty(L.moe_fp4_scale_bytes(n, cols, 1, 1, 1), dtype=torch.uint8, device="cuda")
+    L.moe_fp4_quantize(bf16(x), 1, q, sf, group_offsets=i32([0, n]), scale=torch.tensor([g], device="cuda"))
+    el, code, _ = R.fp4_quantize(x, "nv", g)
+    s = grouped_scales(sf.cpu().numpy(), list(range(n)), cols // 16, -(-cols // 64))
+    a = np.abs(x).reshape(n, -1, 16).max(-1) / (6.0 * g)
+    step = np.exp2(np.floor(np.log2(np.maximum(a, 2.0 ** -6))) - 3)
+    sure = np.abs(np.mod(a / step, 1.0) - 0.5) > 2.0 ** -19  # 16 steps to a binade at most
+    sure |= a > 448
+    assert sure.mean() > 0.99 and (s == code)[sure].all()
+    t = np.repeat(R.e4m3_value(code) * g, 16, 1)
+    r = np.abs(x) / np.where(t > 0, t, 1.0)
+    near = (np.abs(r[..., None] / TIES - 1) < 2.0 ** -22).any(-1)
+    ok = np.repeat(sure, 16, 1) & ~near
+    got = R.unpack(q.cpu().numpy())
+    assert ok.mean() > 0.98 and ((got == el) | ((el & 7 == 0) & (got & 7 == 0)))[ok].all()
