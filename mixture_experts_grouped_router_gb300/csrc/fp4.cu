@@ -138,9 +138,9 @@ MOE_DEVINL uint32_t scale_word(uint32_t c, int lane) {
 // A warp's 4 chunks of 256 columns of a row (a lane 8 values of each, 16 bytes in,
 // 4 bytes of codes out): the codes, and the words of the scale atoms (4 blocks
 // each; the lanes that share a word all hold it).
-template <int FMT>
-MOE_DEVINL void quantize_piece(const uint4 *w, int c0, int cols, int lane, float g, float inv6,
-                               uint32_t *codes, uint32_t *words) {
+template <int FMT, bool FEW>
+MOE_DEVINL void quantize_chunks(const uint4 *w, int c0, int cols, int lane, float g, float inv6,
+                                uint32_t *codes, uint32_t *words) {
 #pragma unroll
   for (int i = 0; i < kUnroll; ++i) {
     const int c = c0 + 256 * i;
@@ -153,9 +153,18 @@ MOE_DEVINL void quantize_piece(const uint4 *w, int c0, int cols, int lane, float
     const uint32_t code =
         fp4_block_scale<FMT>(__uint_as_float(a << 16), g, 6.0f * g, inv6, inv);
     bf16x8_to_f32(w[i], v);
-    codes[i] = fp4_codes8<FMT>(v, inv, code, g);
+    codes[i] = fp4_codes8<FMT, FEW>(v, inv, code, g);
     words[i] = scale_word<FMT>(c < cols ? code : 0u, lane);
   }
+}
+
+template <int FMT>
+MOE_DEVINL void quantize_piece(const uint4 *w, int c0, int cols, int lane, float g, float inv6,
+                               uint32_t *codes, uint32_t *words) {
+  if (FMT == MOE_FP4_MX || fp4_few_bits(g))
+    quantize_chunks<FMT, true>(w, c0, cols, lane, g, inv6, codes, words);
+  else
+    quantize_chunks<FMT, false>(w, c0, cols, lane, g, inv6, codes, words);
 }
 
 // Stores a piece as row r, padded row pr.
@@ -412,7 +421,8 @@ fp4_quantize_weights_kernel(const uint16_t *__restrict__ w, int K, int N, int ro
       v[j] = __uint_as_float((uint32_t)tile[kb + b * kB + j][nn] << 16);
 #pragma unroll
     for (int j = 0; j < kB / 8; ++j)
-      codes[b * (kB / 8) + j] = fp4_codes8<FMT>(v + 8 * j, inv, code, g);
+      codes[b * (kB / 8) + j] = fp4_few_bits(g) ? fp4_codes8<FMT, true>(v + 8 * j, inv, code, g)
+                                                : fp4_codes8<FMT, false>(v + 8 * j, inv, code, g);
     const int blk = k / kB + b;
     if (blk < 4 * ac) sf[fp4_scale_byte(pr, blk, ac)] = k < K ? (uint8_t)code : (uint8_t)0;
   }
