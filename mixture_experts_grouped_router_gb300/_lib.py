@@ -550,32 +550,8 @@ def moe_gmm_fp4(A, sfa, B, sfb, fmt, group_offsets, K=None, epilogue=EPI_NONE, C
                 sf2=None, a_scale=None, b_scale=None, q2_scale=None, dev_status=None, stream=None):
     """A uint8 codes [rows_cap, K / 2], B uint8 codes [E, N, K / 2]; C bf16 or fp32 (optional
     bf16 H with the SwiGLU epilogue), Q2 uint8 codes of Act [rows_cap, F / 2]."""
-    E, N, kb = B.shape
-    K = 2 * kb if K is None else K
-    rows, swiglu = A.shape[0], epilogue == EPI_SWIGLU_FWD
-    c_dtype = DTYPE_F32 if C is not None and C.dtype == torch.float32 else DTYPE_BF16
-    _need_matrix("A", A, rows, K // 2, torch.uint8)
-    _need_matrix("B", B, N, K // 2, torch.uint8)
-    _need_matrix("C", C, rows, N, torch.bfloat16, torch.float32)
-    if swiglu:
-        _need_matrix("Q2", Q2, rows, N // 4, torch.uint8)
-        _need("sf2", sf2, 0, torch.uint8)
-    _need("sfa", sfa, moe_fp4_scale_bytes(rows, K, fmt, FP4_ROWS_GROUPED, E), torch.uint8)
-    _need("sfb", sfb, moe_fp4_scale_bytes(E * N, K, fmt,
-                                          FP4_ROWS_SWIGLU if swiglu else FP4_ROWS_EXPERTS, E),
-          torch.uint8)
-    _need("group_offsets", group_offsets, E + 1, torch.int32)
-    _need("a_scale", a_scale, 1, torch.float32)
-    _need("b_scale", b_scale, E, torch.float32)
-    _need("q2_scale", q2_scale, 1, torch.float32)
-    _need("dev_status", dev_status, 1, torch.int32)
-    _check(LIB.moe_gmm_fp4(_ptr(A), _ld(A), _ptr(sfa), _ptr(a_scale), _ptr(B), B.stride(1),
-                           B.stride(0), _ptr(sfb), _ptr(b_scale), fmt, _ptr(group_offsets), E,
-                           A.shape[0], K, N, epilogue, _ptr(C), c_dtype,
-                           _ld(C) if C is not None else 0, _ptr(Q2),
-                           _ld(Q2) if Q2 is not None else 0, _ptr(sf2),
-                           sf2.numel() if sf2 is not None else 0, _ptr(q2_scale),
-                           _ptr(dev_status), _stream(stream)))
+    _check(_native.gmm_fp4(A, sfa, B, sfb, fmt, group_offsets, -1 if K is None else K, epilogue, C, Q2,
+                           sf2, a_scale, b_scale, q2_scale, dev_status, _stream(stream)))
 
 
 class Fp4WeightsArg(ctypes.Structure):

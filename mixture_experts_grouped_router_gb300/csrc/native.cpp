@@ -380,6 +380,66 @@ PyObject *fp4_experts(PyObject *, PyObject *const *args, Py_ssize_t n) {
   });
 }
 
+// A, sfa, B, sfb, fmt, group_offsets, K (under 0: of B), epilogue, C, Q2, sf2, a_scale, b_scale,
+// q2_scale, dev_status, stream
+PyObject *gmm_fp4(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  return entry<16>(args, n, [](PyObject *const *a) {
+    const int fmt = int32_arg(a[4]), epilogue = int32_arg(a[7]);
+    const bool swiglu = epilogue == MOE_EPI_SWIGLU_FWD;
+    const Matrix A = matrix("A", a[0], t_u8), B = matrix("B", a[2], t_u8);
+    int E;
+    int64_t stride_b;
+    {
+      Tuple shape(m_shape.get(a[2])), stride(m_stride.call(a[2]));
+      if (PyTuple_GET_SIZE(shape.o) != 3) {
+        PyErr_SetString(PyExc_ValueError, "B is [E, N, K / 2]");
+        throw Failed{};
+      }
+      E = as_int32(item(shape.o, 0));
+      stride_b = item(stride.o, 0);
+    }
+    int K = int32_arg(a[6]);
+    if (K < 0) K = as_int32(2 * B.cols);
+    const int N = as_int32(B.rows);
+    const int64_t rows = A.rows;
+    need("A", A, rows, K / 2);
+    need("B", B, N, K / 2);
+    Matrix C = {nullptr, 0, 0, 0}, Q2 = C;
+    int c_dtype = MOE_DTYPE_BF16;
+    if (a[8] != Py_None) {
+      PyObject *d = m_dtype.get(a[8]);
+      if (d == nullptr) throw Failed{};
+      Py_DECREF(d);  // (the type lives on)
+      if (d == t_f32) c_dtype = MOE_DTYPE_F32;
+      C = matrix("C", a[8], d == t_f32 ? t_f32 : t_bf16);
+      need("C", C, rows, N);
+    }
+    if (a[9] != Py_None) {
+      Q2 = matrix("Q2", a[9], t_u8);
+      if (swiglu) need("Q2", Q2, rows, N / 4);
+    }
+    const Vector sfa = vector("sfa", a[1], t_u8), sfb = vector("sfb", a[3], t_u8),
+                 off = vector("group_offsets", a[5], t_i32), sf2 = vector("sf2", a[10], t_u8),
+                 ga = vector("a_scale", a[11], t_f32), gb = vector("b_scale", a[12], t_f32),
+                 g2 = vector("q2_scale", a[13], t_f32), status = vector("dev_status", a[14], t_i32);
+    need("sfa", sfa, moe_fp4_scale_bytes(rows, K, fmt, MOE_FP4_ROWS_GROUPED, E));
+    need("sfb", sfb, moe_fp4_scale_bytes((int64_t)E * N, K, fmt,
+                                         swiglu ? MOE_FP4_ROWS_SWIGLU : MOE_FP4_ROWS_EXPERTS, E));
+    need("group_offsets", off, (int64_t)E + 1);
+    need("a_scale", ga, 1);
+    need("b_scale", gb, E);
+    need("q2_scale", g2, 1);
+    need("dev_status", status, 1);
+    const moe_stream_t st = stream(a[15]);
+    return unlocked([=] {
+      return moe_gmm_fp4(A.as<uint8_t>(), A.ld, sfa.as<uint8_t>(), ga.as<float>(), B.as<uint8_t>(),
+                         B.ld, stride_b, sfb.as<uint8_t>(), gb.as<float>(), fmt, off.as<int32_t>(), E,
+                         rows, K, N, epilogue, C.p, c_dtype, C.ld, Q2.as<uint8_t>(), Q2.ld,
+                         sf2.as<uint8_t>(), (size_t)sf2.n, g2.as<float>(), status.as<int32_t>(), st);
+    });
+  });
+}
+
 PyCFunction fast(PyObject *(*f)(PyObject *, PyObject *const *, Py_ssize_t)) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
 }
@@ -391,6 +451,7 @@ PyMethodDef methods[] = {
     {"act8_swiglu_bwd", fast(act8_swiglu_bwd), METH_FASTCALL, nullptr},
     {"fp4_quantize", fast(fp4_quantize), METH_FASTCALL, nullptr},
     {"fp4_dequantize", fast(fp4_dequantize), METH_FASTCALL, nullptr},
+    {"gmm_fp4", fast(gmm_fp4), METH_FASTCALL, nullptr},
     {"fp4_experts", fast(fp4_experts), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
