@@ -216,24 +216,24 @@ class Fp4Buffers(_Fixed):
 def fp4_experts(w: Fp4Experts, b: Fp4Buffers, x, sorted_to_flat, k, group_offsets, stream=None,
                 rows=None):
     """Expert outputs y bf16 [rows_cap, d] of the permuted rows of x bf16 [T, d]
-    (sorted_to_flat int32 [rows_cap], group_offsets int32 [E + 1] as moe_permute leaves them;
+    (sorted_to_flat int32 [rows], group_offsets int32 [E + 1] as moe_permute leaves them;
     rows past group_offsets[E] are not written).  With b.h also H = [gate | up] in bf16.
-    rows: the first so many rows hold every group (fewer than rows_cap where x is short of what
+    rows: the first so many rows hold every group (rows_cap, or fewer where x is short of what
     the buffers are for); group_offsets past them are clamped."""
-    if sorted_to_flat.shape[0] < b.rows_cap or group_offsets.shape[0] != w.E + 1:
-        raise ValueError("sorted_to_flat of %d rows (rows_cap %d), group_offsets of %d (E %d)"
-                         % (sorted_to_flat.shape[0], b.rows_cap, group_offsets.shape[0], w.E))
+    cap = b.rows_cap if rows is None else rows
+    if not 0 <= cap <= b.rows_cap:
+        raise ValueError("rows = %d of %d" % (cap, b.rows_cap))
+    if sorted_to_flat.shape[0] < cap or group_offsets.shape[0] != w.E + 1:
+        raise ValueError("sorted_to_flat of %d rows (%d), group_offsets of %d (E %d)"
+                         % (sorted_to_flat.shape[0], cap, group_offsets.shape[0], w.E))
     if x.shape[1] != w.d or b.y.shape[1] != w.d or b.act.cols != w.f:
         raise ValueError("x of %d columns, buffers for (%d, %d), experts (%d, %d)"
                          % (x.shape[1], b.y.shape[1], b.act.cols, w.d, w.f))
-    if rows is not None and rows != b.rows_cap:
-        if not 0 <= rows <= b.rows_cap:
-            raise ValueError("rows = %d of %d" % (rows, b.rows_cap))
+    arg = b.arg
+    if cap != b.rows_cap:
         arg = L.Fp4BuffersArg.from_buffer_copy(b.arg)
-        arg.rows_cap = rows
-        L.moe_fp4_experts(w.arg, arg, x, sorted_to_flat, k, group_offsets, stream)
-    else:
-        L.moe_fp4_experts(w.arg, b.arg, x, sorted_to_flat, k, group_offsets, stream)
+        arg.rows_cap = cap
+    L.moe_fp4_experts(w.arg, arg, x, sorted_to_flat, k, group_offsets, stream)
     return b.y
 
 

@@ -49,3 +49,25 @@ def test_from_codes_is_from_weights(fmt, E, d, f, typed):
         at = [R.scale_byte(R.padded_row(r, N, m), b, ac) for r in range(E * N) for b in range(4 * ac)]
         at = torch.tensor(at, device="cuda")
         assert torch.equal(sf[at], sw[at])
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_a_short_permutation_in_larger_buffers(fmt):
+    """rows below the buffers' rows_cap, with a sorted_to_flat of just as many: the same outputs
+    as buffers of that size give, the rest of y untouched."""
+    from mixture_experts_grouped_router_gb300 import lowbit
+    rng = np.random.default_rng(5)
+    E, d, f, T = 4, 96, 64, 21
+    w = lowbit.Fp4Experts.from_weights(fmt, bf16(rng.standard_normal((E, d, 2 * f))),
+                                       bf16(rng.standard_normal((E, f, d))))
+    x = bf16(rng.standard_normal((T, d)))
+    order, off = i32(rng.permutation(T)), i32([0, 3, 3, 15, T])
+    want = lowbit.fp4_experts(w, lowbit.Fp4Buffers(w, T), x, order, 1, off)
+    b = lowbit.Fp4Buffers(w, 300)
+    b.y.fill_(9.0)
+    got = lowbit.fp4_experts(w, b, x, order, 1, off, rows=T)
+    assert torch.equal(got[:T], want) and (got[T:] == 9.0).all()
+    assert int(b.dev_status.item()) == 0
+    for rows, s2f in ((T, order[:-1]), (301, order), (-1, order), (None, order)):
+        with pytest.raises(ValueError, match="rows"):
+            lowbit.fp4_experts(w, b, x, s2f, 1, off, rows=rows)
