@@ -310,6 +310,7 @@ class Checkpoint8:
             raise ValueError("8-bit checkpoints are of the bf16 layer without column-wise copies")
         if s.d % 8 or s.f % 8:
             raise ValueError("d=%d and f=%d must be multiples of 8" % (s.d, s.f))
+        self.s = s
         dev = b.workspace.device
         R, nf = b.rows_cap, -(-s.f // 32)
 
@@ -331,8 +332,13 @@ class Checkpoint8:
         ts = [*self.xs, *self.h, *self.y, *self.routing.values()]
         return sum(t.numel() * t.element_size() for t in ts)
 
+    def _same_shape(self, b):
+        if b.s != self.s:
+            raise ValueError("a checkpoint of %r for buffers of %r" % (self.s, b.s))
+
     def save(self, b, stream=None):
         """After layer.forward(b, ...): afterwards b is free for another layer's forward."""
+        self._same_shape(b)
         if b.logits is None:
             raise ValueError("Checkpoint8.save before a forward")
         f, nf = b.s.f, self.nf
@@ -354,6 +360,7 @@ class Checkpoint8:
     def backward(self, b, dout, wi, wo, stream=None):
         """layer.backward of the saved forward: (dx, dwi, dwo, d_topk_w) in b's buffers, the
         router-logit gradient in b.d_logits, bias gradients in b.dbi and b.dbo."""
+        self._same_shape(b)
         if not self.saved:
             raise ValueError("Checkpoint8.backward before save")
         s, r = b.s, self.routing
