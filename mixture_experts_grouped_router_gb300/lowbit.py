@@ -359,10 +359,12 @@ class Checkpoint8:
 
     def backward(self, b, dout, wi, wo, stream=None):
         """layer.backward of the saved forward: (dx, dwi, dwo, d_topk_w) in b's buffers, the
-        router-logit gradient in b.d_logits, bias gradients in b.dbi and b.dbo."""
+        router-logit gradient in b.d_logits, bias gradients in b.dbi and b.dbo.  A forward that
+        b still holds is lost (save it first): its state gives way."""
         self._same_shape(b)
         if not self.saved:
             raise ValueError("Checkpoint8.backward before save")
+        b.logits = None  # layer.backward and save of that forward are refused
         s, r = b.s, self.routing
         off, f2s, st = r["group_offsets"], r["f2s"], b.dev_status
         act8_dequantize(*self.y, b.y, off, stream)

@@ -1,4 +1,5 @@
-"""What 8-bit checkpoints refuse: buffers of another layer."""
+"""What 8-bit checkpoints refuse: buffers of another layer, and a forward that their backward
+has overwritten."""
 import dataclasses
 
 import pytest
@@ -17,6 +18,25 @@ def one():
     b = layer.MoEBuffers(layer_shape(cfg, False))
     x, wi, wo, dout = (dev_bf16(inp[n]) for n in ("x", "wi", "wo", "dout"))
     return layer, lowbit, b, x, torch.from_numpy(inp["logits"]).cuda(), wi, wo, dout
+
+
+def test_a_forward_that_the_backward_has_overwritten():
+    layer, lowbit, b, x, logits, wi, wo, dout = one()
+    from mixture_experts_grouped_router_gb300 import _lib as L
+    ck = lowbit.Checkpoint8(b)
+    layer.forward(b, x, logits, wi, wo)
+    want = layer.backward(b, dout, wi, wo)[0].clone()
+    ck.save(b)
+    layer.forward(b, -x, -logits, wi, wo)
+    ck.backward(b, dout, wi, wo)
+    with pytest.raises(L.MoEError, match="null"):
+        layer.backward(b, dout, wi, wo)
+    with pytest.raises(ValueError, match="before a forward"):
+        ck.save(b)
+    layer.forward(b, x, logits, wi, wo)  # and the buffers go on
+    assert torch.equal(layer.backward(b, dout, wi, wo)[0], want)
+    torch.cuda.synchronize()
+    assert int(b.dev_status.item()) == 0
 
 
 def test_buffers_of_another_layer():
