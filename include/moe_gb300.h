@@ -697,7 +697,8 @@ moe_status_t moe_fp4_experts(const moe_fp4_weights *w, const moe_fp4_buffers *b,
  * moe_act8_quantize    x bf16 [rows, ldx] -> q int8 [rows, ldq >= cols], scales
  *                      bf16 [rows, lds >= ceil(cols / 32)]
  * moe_act8_dequantize  the values, rounded once to bf16
- * moe_act8_swiglu_fwd  h bf16 [rows, ldh >= 2F] = [gate | up] -> act bf16 =
+ * moe_act8_swiglu_fwd  for programs that have h from a product of their own:
+ *                      h bf16 [rows, ldh >= 2F] = [gate | up] -> act bf16 =
  *                      silu(gate) * up (from the bf16 values) and the codes of h:
  *                      q int8 [rows, ldq >= 2F], scales [rows, lds >= 2 ceil(F /
  *                      32)] (the up half's blocks start at ceil(F / 32))

@@ -22,10 +22,10 @@
 // The kernels stream: a warp takes four chunks of 256 columns of a row (a lane 16
 // bytes of each) and loads the next row's before it works on them.  What bounds
 // them, 32768 rows of 4096 gathered from 16384 tokens, NVFP4, measured copy 6676 GB/s:
-//   quantise    41 us, of it linking 5: 208 MB would take 31; the issue of some 15
-//       instructions a value (two chunks a warp, or five or more resident blocks,
-//       which leaves fewer registers: 54 to 72 us)
-//   dequantise  57 us, 6030 GB/s: HBM, mostly its writes
+//   quantise    43 us with the linking (single launches 42 and 6): 208 MB would take 31;
+//       the issue of some 16 instructions a value (two chunks a warp, or five or more
+//       resident blocks, which leaves fewer registers: 54 to 72 us)
+//   dequantise  58 us in a single launch, 6000 GB/s: HBM, mostly its writes
 #include <algorithm>
 
 #include "internal.h"
@@ -478,9 +478,10 @@ int64_t fp4_atom_rows(int64_t rows, int row_map, int E) {
 }
 
 // Linked quantisation pays from so many gathered values on, for its two more
-// launches (about 5 us): NVFP4, 32768 rows of 4096 from 16384 tokens 69 us directly, 41
-// linked; MXFP4, 6216 rows of 7168 from 777 tokens 25 and 13 us; at 2^24 values, 4096
-// rows of 4096 from 2048 tokens, 11.4 and 10.6 us.
+// launches (about 5 us): NVFP4, 32768 rows of 4096 from 16384 tokens 69 us directly, 43
+// linked; MXFP4, 6216 rows of 7168 from 777 tokens 25 and 14 us; at 2^25 values, 8192
+// rows of 4096 from 4096 tokens, 19.8 and 18.5 (MXFP4 19.5 and 17.4); at 2^24 the two are
+// even, 4096 rows of 4096 from 2048 tokens 12.0 and 12.5, from 1024 11.8 and 11.6.
 constexpr int64_t kLinkFrom = 1 << 24;
 
 size_t fp4_quantize_workspace_bytes(int64_t src_rows, int64_t rows) {

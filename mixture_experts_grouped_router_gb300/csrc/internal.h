@@ -167,8 +167,11 @@ struct TgmmMxArgs {
 moe_status_t launch_tgmm_mx(const TgmmMxArgs &a, cudaStream_t s);
 
 // Launch as a programmatic dependent: the kernel's blocks may be placed while the
-// one before it in the stream drains; it calls grid_dependency_wait() before it
-// touches global memory.  Hides most of a launch's latency where kernels are short.
+// one before it in the stream drains; it waits for that one (grid_dependency_wait() or
+// _begin()) before it touches global memory that the one before may write or read.  What
+// earlier kernels wrote is complete by then, as every kernel launched so waits before it
+// lets the next one start: the 4-bit products read offsets and weights before their own
+// wait (GmmFp4Args::early).  Hides most of a launch's latency where kernels are short.
 template <typename... Params, typename... Args>
 cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
                              cudaStream_t s, Args... args) {

@@ -154,7 +154,7 @@ MOE_DEVINL uint32_t fp4_block_scale(float a, float g, float g6, float inv6, floa
 
 // Whether the tensor's scale has 8 significant bits at most, which decides how quotients
 // are taken below: 32768 rows of 4096 gathered from 16384 tokens (NVFP4) 43 us linked and
-// 70 direct if so, 47 and 77 if not.
+// 69 direct if so, 47 and 77 if not.
 MOE_DEVINL bool fp4_few_bits(float g) { return (__float_as_uint(g) & 0xFFFFu) == 0; }
 
 // 8 values -> 8 codes, by the block's scale code and inv.  MXFP4: products with a power
