@@ -59,6 +59,8 @@ enum { MOE_FP8_E4M3 = 0, MOE_FP8_E5M2 = 1 };
 enum { MOE_FP4_MX = 0, MOE_FP4_NV = 1 };
 /* row orders of their scale atoms */
 enum { MOE_FP4_ROWS_GROUPED = 1, MOE_FP4_ROWS_SWIGLU = 2, MOE_FP4_ROWS_EXPERTS = 3 };
+/* 8-bit outputs of moe_rms_norm */
+enum { MOE_CODES_NONE = 0, MOE_CODES_MX = 1, MOE_CODES_ACT8 = 2 };
 /* row orders of block-scale atoms (moe_mx_quantize) */
 enum { MOE_MX_ROWS_PLAIN = 0, MOE_MX_ROWS_GROUPED = 1, MOE_MX_ROWS_SWIGLU = 2,
        MOE_MX_ROWS_TILES = 3 };
@@ -765,6 +767,148 @@ moe_status_t moe_unpermute_bwd(const uint16_t *d_out, int64_t ld_dout, const uin
                                const float *topk_w, int T, int k, int d, int E,
                                int64_t rows_cap, uint16_t *dY, int64_t ld_dy, float *d_topk_w,
                                moe_stream_t stream);
+
+/* ------------------------------------- what a step has around the expert layer --
+ * moe_rms_norm -- the RMS norm before the experts, with the residual's addition and
+ * an output in bf16, in 8 bits with scales, or both:
+ *     h = round(x + residual),  r = (mean_j h_j^2 + eps)^(-1/2),  y_j = bf16(h_j r w_j)
+ * (h rounded to the type of the residual stream, and the norm that of the rounded h).
+ *   x          bf16 [rows, ldx >= cols] (the output of the layer before, e.g. of
+ *              moe_combine) or NULL;  residual  stream_dtype [rows, ld_res >= cols] or
+ *              NULL (one of them at least; what is NULL counts as zeros)
+ *   stream_dtype, w_dtype  MOE_DTYPE_*;  w [cols];  0 < eps <= 1
+ *   h          stream_dtype [rows, ldh >= cols] or NULL (not kept); may be residual
+ *   y          bf16 [rows, ldy >= cols] or NULL (codes alone); may be x
+ *   codes      MOE_CODES_NONE
+ *              MOE_CODES_MX    E4M3 codes q [rows, ldq >= cols] and scale atoms in
+ *                 MOE_MX_ROWS_PLAIN order (scales_bytes >= moe_mx_scale_bytes): A
+ *                 operand of moe_gmm_mx with one group; cols % 128 == 0, rows of q on
+ *                 16 bytes
+ *              MOE_CODES_ACT8  int8 codes and bf16 scales [rows, lds >= ceil(cols /
+ *                 32)], what moe_act8_dequantize reads; rows of q on 8 bytes
+ *              the codes are those that moe_mx_quantize and moe_act8_quantize make of y
+ * cols % 8 == 0, cols <= 16384; rows of the matrices start on 16 bytes.  fp32 sums; a
+ * row whose squares pass fp32's range reads as zeros in y, one with a NaN as NaN.
+ */
+moe_status_t moe_rms_norm(const uint16_t *x, int64_t ldx, const void *residual, int64_t ld_res,
+                          int stream_dtype, int64_t rows, int cols, const void *w, int w_dtype,
+                          float eps, void *h, int64_t ldh, uint16_t *y, int64_t ldy, int codes,
+                          uint8_t *q, int64_t ldq, void *scales, int64_t lds, size_t scales_bytes,
+                          moe_stream_t stream);
+
+/*
+ * moe_rms_norm_bwd -- from dy, the h that the forward kept and the gradient that
+ * reaches h past the block:
+ *     g_j = dy_j w_j,  dh_j = r g_j - r^3 mean(g h) h_j + d_residual_j
+ *     dw_j = (dw_j +) sum over rows of dy_j h_j r
+ *   dy          bf16 [rows, ld_dy];  h stream_dtype [rows, ldh]
+ *   d_residual  stream_dtype [rows, ld_dres] or NULL
+ *   dh          stream_dtype [rows, ld_dh] out: the gradient of x and of residual; may be
+ *               d_residual
+ *   dx          bf16 [rows, ld_dx] out or NULL: dh rounded to bf16 as well (an fp32
+ *               stream's gradient for the layer that wrote x); may be dy
+ *   dw          fp32 [cols] out or NULL (no gradient of w); added to if accumulate != 0
+ *   workspace   moe_rms_norm_bwd_workspace_bytes(rows, cols) bytes, 16-byte aligned (where
+ *               dw is given); contents on entry are ignored
+ * Sums in a fixed order: the result does not vary between runs.  No rows: dw = 0 (kept
+ * when accumulating).
+ */
+size_t moe_rms_norm_bwd_workspace_bytes(int64_t rows, int cols);
+moe_status_t moe_rms_norm_bwd(const uint16_t *dy, int64_t ld_dy, const void *h, int64_t ldh,
+                              int stream_dtype, int64_t rows, int cols, const void *w, int w_dtype,
+                              float eps, const void *d_residual, int64_t ld_dres, void *dh,
+                              int64_t ld_dh, uint16_t *dx, int64_t ld_dx, float *dw, int accumulate,
+                              void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * moe_mx_dequantize -- the values of block-scaled codes q uint8 [rows, ldq >= cols]
+ * with scale atoms in MOE_MX_ROWS_PLAIN order, rounded once to bf16 (exact but for
+ * values under bf16's normal range): x bf16 [rows, ldx >= cols].  cols % 128 == 0.
+ */
+moe_status_t moe_mx_dequantize(const uint8_t *q, int64_t ldq, const uint8_t *sf, size_t sf_bytes,
+                               int64_t rows, int cols, int fmt, uint16_t *x, int64_t ldx,
+                               moe_stream_t stream);
+
+/*
+ * moe_seq_aux_loss -- the load-balancing loss of every sequence of a ragged batch
+ * and the router's z loss.  Sequence b is tokens [seq_offsets[b], seq_offsets[b + 1]);
+ * a token is live if it lies in a sequence and its mask is not 0.  With n_b live tokens
+ * of sequence b, counts c_be of their choices (a choice out of [0, E) counts for nothing)
+ * and p as in moe_aux_loss (softmax, or sigmoid scores over their sum):
+ *     f_be = E c_be / (k n_b),  P_be = mean over the live tokens of p_te
+ *     loss[0] = coeff / S sum over b, e of f_be P_be   (S sequences that have live tokens)
+ *     loss[1] = z_coeff / N sum over live t of lse_t^2 (N live tokens, lse_t =
+ *               log(sum_e exp(logit_te)))
+ * One sequence of all tokens and no mask: loss[0] is moe_aux_loss's.
+ *   logits       fp32 [T, ld_logits >= E];  topk_idx int32 [T, k]
+ *   seq_offsets  int32 [B + 1] device, ascending; tokens before the first and from the
+ *                last on belong to no sequence (values outside [0, T] are clamped)
+ *   token_mask   uint8 [T] or NULL (all live)
+ *   counts       int32 [B, E] out; tokens int32 [B] out: n_b; probs_mean fp32 [B, E]
+ *                out: P (zeros for a sequence without live tokens)
+ *   loss         fp32 [2] out
+ *   d_logits     fp32 [T, ld_dlogits >= E] or NULL: the gradient (below) from the same
+ *                pass over the logits; not logits themselves
+ *   workspace    moe_seq_aux_loss_workspace_bytes(T, E, B) bytes, 4-byte aligned;
+ *                contents on entry are ignored
+ * A token whose logits are all -inf (or NaN) has p = 0 and no z.  fp32 sums in a fixed
+ * order.  E <= 256, k <= 16, T <= 2^30, 1 <= B <= 65536.
+ *
+ * moe_seq_aux_loss_bwd -- the gradient by itself, from counts and tokens as
+ * moe_seq_aux_loss wrote them (held fixed), times d_loss:
+ *     d_l = d_loss [coeff / (S n_b) J_te (f_be - sum_j f_bj p_tj) +
+ *                   2 z_coeff / N lse_t softmax_te],   J = p, or s (1 - s) / sum s
+ * written, or added to d_logits where accumulate != 0 (on top of moe_route_topk_bwd's);
+ * tokens that are not live get zeros, or keep theirs.
+ */
+size_t moe_seq_aux_loss_workspace_bytes(int T, int E, int B);
+moe_status_t moe_seq_aux_loss(const float *logits, int64_t ld_logits, int T, int E, int k,
+                              int score_fn, const int32_t *topk_idx, const int32_t *seq_offsets, int B,
+                              const uint8_t *token_mask, float coeff, float z_coeff, int32_t *counts,
+                              int32_t *tokens, float *probs_mean, float *loss, float d_loss,
+                              float *d_logits, int64_t ld_dlogits, int accumulate, void *workspace,
+                              size_t workspace_bytes, moe_stream_t stream);
+moe_status_t moe_seq_aux_loss_bwd(const float *logits, int64_t ld_logits, int T, int E, int k,
+                                  int score_fn, const int32_t *seq_offsets, int B,
+                                  const uint8_t *token_mask, float coeff, float z_coeff,
+                                  const int32_t *counts, const int32_t *tokens, float d_loss,
+                                  float *d_logits, int64_t ld_dlogits, int accumulate,
+                                  moe_stream_t stream);
+
+/*
+ * moe_clip_grads -- the norm of all gradients together, and their clipping:
+ *     norm = scale sqrt(sum over tensors and elements of g^2)
+ *     out  = g scale min(1, max_norm / (norm + 1e-6)), rounded to out's type
+ * (scale: 1 / loss scale).  A norm that is infinite or no number clips nothing: out = g
+ * scale, and the caller, who reads the norm, leaves the step out.  Tensors lie anywhere:
+ * contiguous, any number of elements, aligned to their elements, bf16 or fp32; out may be g
+ * itself (of the same type) or memory that no g lies in.
+ *   moe_grad  one tensor: g [n] of g_dtype, out [n] of out_dtype (MOE_DTYPE_*)
+ *   moe_clip_plan_chunks  pieces that the tensors are taken in (-1 and the reason in
+ *             moe_last_error() for bad arguments); moe_clip_plan writes 32 bytes for each
+ *             to HOST memory, which the caller copies to the device (16-byte aligned)
+ *             once.  Both are host computations.  The plan holds the tensors' addresses.
+ *   norm      fp32 [1] out (device);  max_norm >= 0 (infinity: only scale);  scale > 0
+ *   workspace moe_clip_workspace_bytes() bytes of device memory, 8-byte aligned, contents
+ *             on entry are ignored; calls that share it do not overlap
+ * moe_grad_norm -- the norm alone; nothing else is written.
+ * Squares are summed in a fixed order, in fp32 over 8 values at a time and then in 64
+ * bits, so that no finite gradient is too large or too small for its square.
+ */
+typedef struct moe_grad {
+  const void *g;
+  void *out;
+  int64_t n;
+  int32_t g_dtype, out_dtype;
+} moe_grad;
+
+int64_t moe_clip_plan_chunks(const moe_grad *grads, int n);
+moe_status_t moe_clip_plan(const moe_grad *grads, int n, void *plan, size_t plan_bytes);
+size_t moe_clip_workspace_bytes(void);
+moe_status_t moe_grad_norm(const void *plan, int64_t chunks, float scale, float *norm, void *workspace,
+                           size_t workspace_bytes, moe_stream_t stream);
+moe_status_t moe_clip_grads(const void *plan, int64_t chunks, float max_norm, float scale, float *norm,
+                            void *workspace, size_t workspace_bytes, moe_stream_t stream);
 
 /* ---------------------------------------------------- expert parallelism --
  * Dispatch of the permuted rows to the shards that own their experts with a

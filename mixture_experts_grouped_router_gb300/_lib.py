@@ -1,4 +1,4 @@
-"""Binding of libmoe_gb300.so by ctypes (the short low-bit operators by _native.so):
+"""Binding of libmoe_gb300.so by ctypes (the short operators by _native.so):
 one Python function per C entry point, same names, argument marshalling only
 (tensor -> pointer, shape -> sizes, current torch stream -> cudaStream_t).  Every step of the layer runs in the
 library's CUDA kernels; there is no fallback: if the library is missing the
@@ -118,6 +118,22 @@ _SIGS = {
     "moe_act8_swiglu_fwd": (_I, [_P, _I64, _I64, _I, _P, _I, _P, _I64, _P, _I64, _P, _I64, _P]),
     "moe_act8_swiglu_bwd": (_I, [_P, _I64, _P, _I64, _P, _I64, _I64, _I, _P, _I, _P, _I64, _P,
                                  _I64, _P]),
+    "moe_rms_norm": (_I, [_P, _I64, _P, _I64, _I, _I64, _I, _P, _I, ctypes.c_float, _P, _I64, _P, _I64,
+                          _I, _P, _I64, _P, _I64, _SZ, _P]),
+    "moe_rms_norm_bwd_workspace_bytes": (_SZ, [_I64, _I]),
+    "moe_rms_norm_bwd": (_I, [_P, _I64, _P, _I64, _I, _I64, _I, _P, _I, ctypes.c_float, _P, _I64, _P,
+                              _I64, _P, _I64, _P, _I, _P, _SZ, _P]),
+    "moe_mx_dequantize": (_I, [_P, _I64, _P, _SZ, _I64, _I, _I, _P, _I64, _P]),
+    "moe_seq_aux_loss_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "moe_seq_aux_loss": (_I, [_P, _I64, _I, _I, _I, _I, _P, _P, _I, _P, ctypes.c_float, ctypes.c_float,
+                              _P, _P, _P, _P, ctypes.c_float, _P, _I64, _I, _P, _SZ, _P]),
+    "moe_seq_aux_loss_bwd": (_I, [_P, _I64, _I, _I, _I, _I, _P, _I, _P, ctypes.c_float, ctypes.c_float,
+                                  _P, _P, ctypes.c_float, _P, _I64, _I, _P]),
+    "moe_clip_plan_chunks": (_I64, [_P, _I]),
+    "moe_clip_plan": (_I, [_P, _I, _P, _SZ]),
+    "moe_clip_workspace_bytes": (_SZ, []),
+    "moe_grad_norm": (_I, [_P, _I64, ctypes.c_float, _P, _P, _SZ, _P]),
+    "moe_clip_grads": (_I, [_P, _I64, ctypes.c_float, ctypes.c_float, _P, _P, _SZ, _P]),
     "moe_ep_recv_rows_cap": (_I64, [_I, _I, _I, _I, _I]),
     "moe_ep_a2a_params": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P]),
     "moe_ep_local_layout": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P]),
@@ -172,6 +188,13 @@ def _stream(stream):
     if _raw_stream is not None:
         return _raw_stream(_raw_device())
     return torch.cuda.current_stream().cuda_stream
+
+
+def _device(stream):
+    """The GPU that a call on `stream` (None: the current one) runs on."""
+    if stream is not None:
+        return stream.device_index
+    return _raw_device() if _raw_device is not None else torch.cuda.current_device()
 
 
 def _ld(t):
@@ -496,6 +519,12 @@ def _need_matrix(name, t, rows, cols, *types):
         raise ValueError("%s is %s for [%d, %d]" % (name, tuple(t.shape), rows, cols))
 
 
+def _need_device(name, t, stream):
+    """t lies on the GPU that a call on `stream` runs on."""
+    if t.get_device() != _device(stream) or not t.is_cuda:
+        raise ValueError("%s is on %s, the call on GPU %d" % (name, t.device, _device(stream)))
+
+
 def moe_fp4_scale_bytes(rows: int, cols: int, fmt: int, row_map: int, E: int = 1) -> int:
     return int(LIB.moe_fp4_scale_bytes(rows, cols, fmt, row_map, E))
 
@@ -594,6 +623,94 @@ def moe_act8_swiglu_fwd(h, act, q, scales, group_offsets=None, stream=None):
 def moe_act8_swiglu_bwd(q, scales, dact, dh, act=None, group_offsets=None, stream=None):
     """Codes of h and dact bf16 [rows, F] -> dh bf16 [rows, 2F], act bf16 [rows, F]."""
     _check(_native.act8_swiglu_bwd(q, scales, dact, dh, act, group_offsets, _stream(stream)))
+
+
+# ------------------------------------------------- around the expert layer
+CODES_NONE = 0
+CODES_MX = 1
+CODES_ACT8 = 2
+
+
+def moe_rms_norm(x, residual, w, eps, h=None, y=None, codes=CODES_NONE, q=None, scales=None,
+                 stream=None):
+    """x bf16, residual and h bf16 or fp32, y bf16, q one-byte codes: [rows, cols]; scales: uint8
+    atoms (CODES_MX) or bf16 [rows, ceil(cols / 32)] (CODES_ACT8)."""
+    _check(_native.rms_norm(x, residual, w, eps, h, y, codes, q, scales, _device(stream),
+                            _stream(stream)))
+
+
+def moe_rms_norm_bwd_workspace_bytes(rows: int, cols: int) -> int:
+    return int(LIB.moe_rms_norm_bwd_workspace_bytes(rows, cols))
+
+
+def moe_rms_norm_bwd(dy, h, w, eps, dh, dw=None, workspace=None, d_residual=None, dx=None,
+                     accumulate=False, stream=None):
+    """dy and dx bf16, h, d_residual and dh bf16 or fp32: [rows, cols]; dw fp32 [cols]."""
+    _check(_native.rms_norm_bwd(dy, h, w, eps, d_residual, dh, dx, dw, int(accumulate), workspace,
+                                _device(stream), _stream(stream)))
+
+
+def moe_mx_dequantize(q, sf, fmt, x, stream=None):
+    """Codes q uint8 [rows, cols] with scale atoms sf (MX_ROWS_PLAIN) -> x bf16 [rows, cols]."""
+    _check(_native.mx_dequantize(q, sf, fmt, x, _device(stream), _stream(stream)))
+
+
+def moe_seq_aux_loss_workspace_bytes(T: int, E: int, B: int) -> int:
+    return int(LIB.moe_seq_aux_loss_workspace_bytes(T, E, B))
+
+
+def moe_seq_aux_loss(logits, topk_idx, seq_offsets, score_fn, coeff, z_coeff, counts, tokens,
+                     probs_mean, loss, workspace, token_mask=None, d_logits=None, d_loss=1.0,
+                     accumulate=False, stream=None):
+    """logits fp32 [T, E], topk_idx int32 [T, k], seq_offsets int32 [B + 1] -> counts int32 [B, E],
+    tokens int32 [B], probs_mean fp32 [B, E], loss fp32 [2] and (given) d_logits fp32 [T, E]."""
+    _check(_native.seq_aux_loss(logits, topk_idx, seq_offsets, token_mask, score_fn, coeff, z_coeff,
+                                counts, tokens, probs_mean, loss, d_loss, d_logits, int(accumulate),
+                                workspace, _device(stream), _stream(stream)))
+
+
+def moe_seq_aux_loss_bwd(logits, k, seq_offsets, score_fn, coeff, z_coeff, counts, tokens, d_logits,
+                         token_mask=None, d_loss=1.0, accumulate=True, stream=None):
+    """counts and tokens as moe_seq_aux_loss wrote them -> d_logits fp32 [T, E]."""
+    _check(_native.seq_aux_loss_bwd(logits, k, seq_offsets, token_mask, score_fn, coeff, z_coeff,
+                                    counts, tokens, d_loss, d_logits, int(accumulate),
+                                    _device(stream), _stream(stream)))
+
+
+class GradArg(ctypes.Structure):
+    """moe_grad."""
+    _fields_ = [("g", _P), ("out", _P), ("n", _I64), ("g_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
+
+
+def moe_clip_plan(grads, outs):
+    """The chunks of tensors bf16 / fp32 (contiguous): (uint8 [32 chunks] host tensor, chunks)."""
+    code = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+    arr = (GradArg * max(1, len(grads)))(*(
+        GradArg(g.data_ptr(), o.data_ptr(), g.numel(), code[g.dtype], code[o.dtype])
+        for g, o in zip(grads, outs)))
+    chunks = int(LIB.moe_clip_plan_chunks(arr, len(grads)))
+    if chunks < 0:
+        raise MoEError(MOE_ERR_INVALID_ARG, last_error())
+    plan = torch.empty(32 * max(1, chunks), dtype=torch.uint8)
+    _check(LIB.moe_clip_plan(arr, len(grads), plan.data_ptr(), plan.numel()))
+    return plan, chunks
+
+
+def moe_clip_workspace_bytes() -> int:
+    return int(LIB.moe_clip_workspace_bytes())
+
+
+def moe_grad_norm(plan, chunks, scale, norm, workspace, stream=None):
+    """plan: moe_clip_plan's on the device; norm fp32 [1]."""
+    _check(_native.clip_grads(plan, chunks, None, scale, norm, workspace, _device(stream),
+                              _stream(stream)))
+
+
+def moe_clip_grads(plan, chunks, max_norm, scale, norm, workspace, stream=None):
+    """The norm, and the tensors of the plan scaled and clipped."""
+    _check(_native.clip_grads(plan, chunks, float(max_norm), scale, norm, workspace, _device(stream),
+                              _stream(stream)))
 
 
 # ------------------------------------------------------------ expert parallelism

@@ -257,4 +257,56 @@ cudaError_t launch_act8_swiglu_bwd(const int8_t *q, int64_t ldq, const uint16_t 
                                    const int32_t *offsets, int E, uint16_t *dh, int64_t lddh,
                                    uint16_t *act, int64_t lda, cudaStream_t st);
 
+// norm.cu (RMS norm with the residual's addition)
+struct RmsNormArgs {
+  const uint16_t *x; int64_t ldx;                  // or null
+  const void *residual; int64_t ld_res;            // of stream_dtype, or null
+  int stream_dtype; int64_t rows; int cols;
+  const void *w; int w_dtype; float eps;
+  void *h; int64_t ldh;                            // of stream_dtype, or null
+  uint16_t *y; int64_t ldy;                        // or null
+  int codes; uint8_t *q; int64_t ldq; void *scales; int64_t lds;
+};
+cudaError_t launch_rms_norm(const RmsNormArgs &a, cudaStream_t s);
+
+struct RmsNormBwdArgs {
+  const uint16_t *dy; int64_t ld_dy;
+  const void *h; int64_t ldh;                      // of stream_dtype, as dh and d_residual
+  int stream_dtype; int64_t rows; int cols;
+  const void *w; int w_dtype; float eps;
+  const void *d_residual; int64_t ld_dres;         // or null
+  void *dh; int64_t ld_dh;
+  uint16_t *dx; int64_t ld_dx;                     // or null
+  float *dw; int accumulate;                       // dw or null
+};
+size_t rms_norm_bwd_workspace_bytes(int64_t rows, int cols);
+cudaError_t launch_rms_norm_bwd(const RmsNormBwdArgs &a, float *part, cudaStream_t s);
+cudaError_t launch_mx_dequantize(const uint8_t *q, int64_t ldq, const uint8_t *sf, int64_t rows,
+                                 int cols, int fmt, uint16_t *x, int64_t ldx, cudaStream_t s);
+
+// seqaux.cu (balance loss of sequences, router z loss)
+struct SeqAuxArgs {
+  const float *logits; int64_t ld; int T, E, k; int score_fn;
+  const int32_t *idx;                              // null: counts and tokens are given
+  const int32_t *offsets; int B;
+  const uint8_t *mask;                             // or null
+  float coeff, z_coeff;
+  int32_t *counts, *tokens;
+  float *probs, *loss;                             // null: the gradient alone
+  float d_loss; float *d_logits; int64_t ld_d; int accumulate;  // or null
+};
+size_t seq_aux_workspace_bytes(int T, int E, int B);
+cudaError_t launch_seq_aux(const SeqAuxArgs &a, void *ws, cudaStream_t s);
+
+// clip.cu (global gradient norm and clipping)
+struct alignas(32) ClipChunk {  // a piece of a tensor, by the plan's own order
+  const void *g;
+  void *out;
+  int32_t n;
+  int32_t kind;  // bit 0: g is fp32; 1: out is fp32; 2: no 16-byte accesses
+};
+constexpr int kClipMaxBlocks = 2048;
+cudaError_t launch_clip(const ClipChunk *plan, int64_t chunks, float scale, float max_norm, bool write,
+                        float *norm, double *part, cudaStream_t s);
+
 }  // namespace moe

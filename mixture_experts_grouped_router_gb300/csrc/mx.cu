@@ -30,8 +30,8 @@
 //            [F + 96 t, F + 96 t + 96), at padded rows 256 t ...
 #include <algorithm>
 
-#include "common.cuh"
 #include "internal.h"
+#include "lowbit.cuh"
 
 namespace moe {
 namespace {
@@ -344,7 +344,40 @@ mx_quantize_2x_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t rows,
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// Values of block-scaled codes (PLAIN scales), rounded once to bf16: a warp takes 256 columns
+// of a row, 8 a lane.
+__global__ void __launch_bounds__(kMxThreads)
+mx_dequantize_kernel(const uint8_t *__restrict__ q, int64_t ldq, const uint8_t *__restrict__ sf,
+                     int64_t rows, int cols, int fmt, uint16_t *__restrict__ x, int64_t ldx) {
+  const int chunks = (cols + 255) / 256, lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * (kMxThreads / 32);
+  grid_dependency_begin();
+  for (int64_t at = (int64_t)blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5); at < rows * chunks;
+       at += warps) {
+    const int64_t r = at / chunks;
+    const int c = (int)(at - r * chunks) * 256 + lane * 8;
+    if (c >= cols) continue;
+    const uint2 w = ld_stream_v2(q + r * ldq + c);
+    const uint32_t code = ld_u8(sf + scale_byte(r, c >> 5, cols));
+    const float s = e8m0_value(code);
+    float v[8];
+    f8x8_to_f32(w, fmt, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= s;
+    st_v4(x + r * ldx + c, f32_to_bf16x8(v));
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_mx_dequantize(const uint8_t *q, int64_t ldq, const uint8_t *sf, int64_t rows,
+                                 int cols, int fmt, uint16_t *x, int64_t ldx, cudaStream_t s) {
+  const int64_t warps = rows * ((cols + 255) / 256);
+  const int64_t blocks = (warps + kMxThreads / 32 - 1) / (kMxThreads / 32);
+  const int64_t most = (int64_t)num_sms() * blocks_per_sm<mx_dequantize_kernel>(kMxThreads);
+  return launch_dependent(mx_dequantize_kernel, (unsigned)std::min(blocks, most), kMxThreads, 0, s, q,
+                          ldq, sf, rows, cols, fmt, x, ldx);
+}
 
 int64_t mx_atom_rows(int64_t rows, int row_map, int E) {
   if (row_map == MOE_MX_ROWS_GROUPED) return f8_padded_rows(rows, E) / 128;

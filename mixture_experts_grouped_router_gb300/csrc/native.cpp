@@ -1,4 +1,5 @@
-// Python calls of the short low-bit operators: the tensors' pointers, sizes and
+// Python calls of the short operators (low-bit formats, and what a step has around the
+// expert layer): the tensors' pointers, sizes and
 // leading dimensions are taken here and handed to the C ABI.  A call's kernels take a
 // few microseconds, so that the host's share counts: 3.2 us a call on an Arm core
 // with the launch (1.5), where ctypes takes 5.5.  `_lib.py` holds the functions
@@ -36,7 +37,7 @@ struct Member {
   }
 };
 Member m_data_ptr = {"data_ptr"}, m_stride = {"stride"}, m_numel = {"numel"}, m_shape = {"shape"},
-       m_is_contiguous = {"is_contiguous"}, m_dtype = {"dtype"};
+       m_is_contiguous = {"is_contiguous"}, m_dtype = {"dtype"}, m_get_device = {"get_device"};
 
 // An argument's value, or an error that ends the call.
 struct Failed {};
@@ -440,6 +441,259 @@ PyObject *gmm_fp4(PyObject *, PyObject *const *args, Py_ssize_t n) {
   });
 }
 
+// ------------------------------------------------ around the expert layer
+float float_arg(PyObject *o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Failed{};
+  return (float)v;
+}
+
+// `name` of the call, if given, lies on GPU `dev`.
+void on_device(const char *name, PyObject *t, int64_t dev) {
+  if (t == Py_None) return;
+  PyObject *r = m_get_device.call(t);
+  if (r == nullptr) throw Failed{};
+  const long long at = PyLong_AsLongLong(r);
+  Py_DECREF(r);
+  if (at == dev && at >= 0) return;
+  if (!PyErr_Occurred())
+    PyErr_Format(PyExc_ValueError, at < 0 ? "%s is not on a GPU" : "%s is on GPU %lld, the call on %lld",
+                 name, at, (long long)dev);
+  throw Failed{};
+}
+
+// MOE_DTYPE_* of a tensor that may be bf16 or fp32.
+int real_type(const char *name, PyObject *t) {
+  PyObject *d = m_dtype.get(t);
+  if (d == nullptr) throw Failed{};
+  const bool f32 = d == t_f32, ok = f32 || d == t_bf16;
+  if (!ok) PyErr_Format(PyExc_ValueError, "%s is %S, not %S or %S", name, d, t_bf16, t_f32);
+  Py_DECREF(d);
+  if (!ok) throw Failed{};
+  return f32 ? MOE_DTYPE_F32 : MOE_DTYPE_BF16;
+}
+
+PyObject *type_object(int dtype) { return dtype == MOE_DTYPE_F32 ? t_f32 : t_bf16; }
+
+// A matrix that may be None; given, of [rows, cols] (rows < 0: any, which it then sets).
+Matrix optional(const char *name, PyObject *t, PyObject *type, int64_t &rows, int64_t &cols) {
+  if (t == Py_None) return {nullptr, 0, 0, 0};
+  const Matrix m = matrix(name, t, type, true);
+  if (rows < 0) {
+    rows = m.rows;
+    cols = m.cols;
+  } else if (m.rows != rows || m.cols != cols) {
+    PyErr_Format(PyExc_ValueError, "%s is [%lld, %lld], not [%lld, %lld]", name, (long long)m.rows,
+                 (long long)m.cols, (long long)rows, (long long)cols);
+    throw Failed{};
+  }
+  return m;
+}
+
+// x, residual, w, eps, h, y, codes, q, scales, device, stream
+PyObject *rms_norm(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  return entry<11>(args, n, [](PyObject *const *a) {
+    int64_t rows = -1, cols = 0;
+    const Matrix x = optional("x", a[0], t_bf16, rows, cols);
+    const int dtype = a[1] != Py_None   ? real_type("residual", a[1])
+                      : a[4] != Py_None ? real_type("h", a[4])
+                                        : MOE_DTYPE_BF16;
+    const Matrix res = optional("residual", a[1], type_object(dtype), rows, cols),
+                 h = optional("h", a[4], type_object(dtype), rows, cols),
+                 y = optional("y", a[5], t_bf16, rows, cols);
+    if (a[0] == Py_None && a[1] == Py_None) {
+      PyErr_SetString(PyExc_ValueError, "neither x nor residual");
+      throw Failed{};
+    }
+    const int wt = real_type("w", a[2]);
+    const Vector w = vector("w", a[2], type_object(wt));
+    need("w", w, cols);
+    const float eps = float_arg(a[3]);
+    const int codes = int32_arg(a[6]), c = as_int32(cols);
+    Matrix q = {nullptr, 0, 0, 0}, s = q;
+    size_t bytes = 0;
+    if (codes != MOE_CODES_NONE) {
+      q = optional("q", a[7], t_u8, rows, cols);
+      if (a[8] != Py_None && codes == MOE_CODES_ACT8) {
+        s = matrix("scales", a[8], t_bf16, true);
+        need("scales", s, rows, blocks32(cols));
+        bytes = s.rows > 0 ? 2 * (size_t)((s.rows - 1) * s.ld + s.cols) : 0;
+      } else {
+        const Vector v = vector("scales", a[8], t_u8);
+        s.p = v.p;
+        bytes = (size_t)v.n;
+      }
+    }
+    const int64_t dev = as_int(a[9]);
+    const char *names[] = {"x", "residual", "w", nullptr, "h", "y", nullptr, "q", "scales"};
+    for (int i = 0; i < 9; ++i)
+      if (names[i] != nullptr && (i < 7 || codes != MOE_CODES_NONE)) on_device(names[i], a[i], dev);
+    const moe_stream_t st = stream(a[10]);
+    return unlocked([=] {
+      return moe_rms_norm(x.as<uint16_t>(), x.ld, res.p, res.ld, dtype, rows, c, w.p, wt, eps, h.p,
+                          h.ld, y.as<uint16_t>(), y.ld, codes, q.as<uint8_t>(), q.ld, s.p, s.ld, bytes,
+                          st);
+    });
+  });
+}
+
+// dy, h, w, eps, d_residual, dh, dx, dw, accumulate, workspace, device, stream
+PyObject *rms_norm_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  return entry<12>(args, n, [](PyObject *const *a) {
+    int64_t rows = -1, cols = 0;
+    const Matrix dy = optional("dy", a[0], t_bf16, rows, cols);
+    if (a[0] == Py_None || a[5] == Py_None) {
+      PyErr_SetString(PyExc_ValueError, "dy and dh are needed");
+      throw Failed{};
+    }
+    const int dtype = real_type("h", a[1]);
+    const Matrix h = optional("h", a[1], type_object(dtype), rows, cols),
+                 res = optional("d_residual", a[4], type_object(dtype), rows, cols),
+                 dh = optional("dh", a[5], type_object(dtype), rows, cols),
+                 dx = optional("dx", a[6], t_bf16, rows, cols);
+    const int wt = real_type("w", a[2]);
+    const Vector w = vector("w", a[2], type_object(wt)), dw = vector("dw", a[7], t_f32),
+                 ws = vector("workspace", a[9], t_u8);
+    need("w", w, cols);
+    need("dw", dw, cols);
+    const float eps = float_arg(a[3]);
+    const int c = as_int32(cols), accumulate = int32_arg(a[8]);
+    const int64_t dev = as_int(a[10]);
+    const char *names[] = {"dy", "h", "w", nullptr, "d_residual", "dh", "dx", "dw", nullptr, "workspace"};
+    for (int i = 0; i < 10; ++i)
+      if (names[i] != nullptr) on_device(names[i], a[i], dev);
+    const moe_stream_t st = stream(a[11]);
+    return unlocked([=] {
+      return moe_rms_norm_bwd(dy.as<uint16_t>(), dy.ld, h.p, h.ld, dtype, rows, c, w.p, wt, eps, res.p,
+                              res.ld, dh.p, dh.ld, dx.as<uint16_t>(), dx.ld, dw.as<float>(), accumulate,
+                              ws.p, (size_t)ws.n, st);
+    });
+  });
+}
+
+// q, sf, fmt, x, device, stream
+PyObject *mx_dequantize(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  return entry<6>(args, n, [](PyObject *const *a) {
+    const Matrix q = matrix("q", a[0], t_u8, true), x = matrix("x", a[3], t_bf16, true);
+    need("q", q, x.rows, x.cols);
+    const Vector sf = vector("sf", a[1], t_u8);
+    const int fmt = int32_arg(a[2]), cols = as_int32(x.cols);
+    const int64_t dev = as_int(a[4]);
+    on_device("q", a[0], dev);
+    on_device("sf", a[1], dev);
+    on_device("x", a[3], dev);
+    const moe_stream_t st = stream(a[5]);
+    return unlocked([=] {
+      return moe_mx_dequantize(q.as<uint8_t>(), q.ld, sf.as<uint8_t>(), (size_t)sf.n, x.rows, cols, fmt,
+                               x.as<uint16_t>(), x.ld, st);
+    });
+  });
+}
+
+// What the two calls of the sequences' loss have in common.
+struct SeqAux {
+  Matrix logits, d_logits = {nullptr, 0, 0, 0};
+  Vector offsets, mask, counts, tokens;
+  int T, E, B, score_fn, accumulate;
+  float coeff, z_coeff, d_loss;
+  SeqAux(PyObject *l, PyObject *off, PyObject *m, PyObject *fn, PyObject *c, PyObject *z, PyObject *cnt,
+         PyObject *tok, PyObject *dl, PyObject *d, PyObject *acc)
+      : logits(matrix("logits", l, t_f32, true)), offsets(vector("seq_offsets", off, t_i32)),
+        mask(vector("token_mask", m, t_u8)), counts(vector("counts", cnt, t_i32)),
+        tokens(vector("tokens", tok, t_i32)), T(as_int32(logits.rows)), E(as_int32(logits.cols)),
+        B(as_int32(offsets.n - 1)), score_fn(int32_arg(fn)), accumulate(int32_arg(acc)),
+        coeff(float_arg(c)), z_coeff(float_arg(z)), d_loss(float_arg(dl)) {
+    int64_t rows = T, cols = E;
+    d_logits = optional("d_logits", d, t_f32, rows, cols);
+    need("token_mask", mask, T);
+    need("counts", counts, (int64_t)B * E);
+    need("tokens", tokens, B);
+  }
+  static void on(int64_t dev, PyObject *l, PyObject *off, PyObject *m, PyObject *cnt, PyObject *tok,
+                 PyObject *d) {
+    on_device("logits", l, dev);
+    on_device("seq_offsets", off, dev);
+    on_device("token_mask", m, dev);
+    on_device("counts", cnt, dev);
+    on_device("tokens", tok, dev);
+    on_device("d_logits", d, dev);
+  }
+};
+
+// logits, topk_idx, seq_offsets, token_mask, score_fn, coeff, z_coeff, counts, tokens, probs_mean,
+// loss, d_loss, d_logits, accumulate, workspace, device, stream
+PyObject *seq_aux_loss(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  return entry<17>(args, n, [](PyObject *const *a) {
+    const int64_t dev = as_int(a[15]);
+    const Matrix idx = matrix("topk_idx", a[1], t_i32, true);
+    const Vector flat = vector("topk_idx", a[1], t_i32), probs = vector("probs_mean", a[9], t_f32),
+                 loss = vector("loss", a[10], t_f32), ws = vector("workspace", a[14], t_u8);
+    const SeqAux s(a[0], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[11], a[12], a[13]);
+    const int k = as_int32(idx.cols);
+    if (idx.rows != s.T) {
+      PyErr_Format(PyExc_ValueError, "topk_idx of %lld tokens, logits of %d", (long long)idx.rows, s.T);
+      throw Failed{};
+    }
+    need("probs_mean", probs, (int64_t)s.B * s.E);
+    need("loss", loss, 2);
+    SeqAux::on(dev, a[0], a[2], a[3], a[7], a[8], a[12]);
+    on_device("topk_idx", a[1], dev);
+    on_device("probs_mean", a[9], dev);
+    on_device("loss", a[10], dev);
+    on_device("workspace", a[14], dev);
+    const moe_stream_t st = stream(a[16]);
+    return unlocked([&] {
+      return moe_seq_aux_loss(s.logits.as<float>(), s.logits.ld, s.T, s.E, k, s.score_fn,
+                              flat.as<int32_t>(), s.offsets.as<int32_t>(), s.B, s.mask.as<uint8_t>(),
+                              s.coeff, s.z_coeff, s.counts.as<int32_t>(), s.tokens.as<int32_t>(),
+                              probs.as<float>(), loss.as<float>(), s.d_loss, s.d_logits.as<float>(),
+                              s.d_logits.ld, s.accumulate, ws.p, (size_t)ws.n, st);
+    });
+  });
+}
+
+// logits, k, seq_offsets, token_mask, score_fn, coeff, z_coeff, counts, tokens, d_loss, d_logits,
+// accumulate, device, stream
+PyObject *seq_aux_loss_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  return entry<14>(args, n, [](PyObject *const *a) {
+    const SeqAux s(a[0], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9], a[10], a[11]);
+    const int k = int32_arg(a[1]);
+    SeqAux::on(as_int(a[12]), a[0], a[2], a[3], a[7], a[8], a[10]);
+    const moe_stream_t st = stream(a[13]);
+    return unlocked([&] {
+      return moe_seq_aux_loss_bwd(s.logits.as<float>(), s.logits.ld, s.T, s.E, k, s.score_fn,
+                                  s.offsets.as<int32_t>(), s.B, s.mask.as<uint8_t>(), s.coeff,
+                                  s.z_coeff, s.counts.as<int32_t>(), s.tokens.as<int32_t>(), s.d_loss,
+                                  s.d_logits.as<float>(), s.d_logits.ld, s.accumulate, st);
+    });
+  });
+}
+
+// plan, chunks, max_norm (None: the norm alone), scale, norm, workspace, device, stream
+PyObject *clip_grads(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  return entry<8>(args, n, [](PyObject *const *a) {
+    const Vector plan = vector("plan", a[0], t_u8), norm = vector("norm", a[4], t_f32),
+                 ws = vector("workspace", a[5], t_u8);
+    const int64_t chunks = as_int(a[1]), dev = as_int(a[6]);
+    if (chunks < 0 || plan.n / 32 < chunks) {
+      PyErr_Format(PyExc_ValueError, "a plan of %lld bytes for %lld chunks", (long long)plan.n,
+                   (long long)chunks);
+      throw Failed{};
+    }
+    need("norm", norm, 1);
+    const float scale = float_arg(a[3]), most = a[2] == Py_None ? 0.0f : float_arg(a[2]);
+    const bool clip = a[2] != Py_None;
+    on_device("plan", a[0], dev);
+    on_device("norm", a[4], dev);
+    on_device("workspace", a[5], dev);
+    const moe_stream_t st = stream(a[7]);
+    return unlocked([=] {
+      return clip ? moe_clip_grads(plan.p, chunks, most, scale, norm.as<float>(), ws.p, (size_t)ws.n, st)
+                  : moe_grad_norm(plan.p, chunks, scale, norm.as<float>(), ws.p, (size_t)ws.n, st);
+    });
+  });
+}
+
 PyCFunction fast(PyObject *(*f)(PyObject *, PyObject *const *, Py_ssize_t)) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
 }
@@ -453,6 +707,12 @@ PyMethodDef methods[] = {
     {"fp4_dequantize", fast(fp4_dequantize), METH_FASTCALL, nullptr},
     {"gmm_fp4", fast(gmm_fp4), METH_FASTCALL, nullptr},
     {"fp4_experts", fast(fp4_experts), METH_FASTCALL, nullptr},
+    {"rms_norm", fast(rms_norm), METH_FASTCALL, nullptr},
+    {"rms_norm_bwd", fast(rms_norm_bwd), METH_FASTCALL, nullptr},
+    {"mx_dequantize", fast(mx_dequantize), METH_FASTCALL, nullptr},
+    {"seq_aux_loss", fast(seq_aux_loss), METH_FASTCALL, nullptr},
+    {"seq_aux_loss_bwd", fast(seq_aux_loss_bwd), METH_FASTCALL, nullptr},
+    {"clip_grads", fast(clip_grads), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 
@@ -474,7 +734,7 @@ PyMODINIT_FUNC PyInit__native(void) {
   Py_DECREF(torch);
   if (!ok) return nullptr;
   tensor_type = (PyTypeObject *)tensor;
-  for (Member *m : {&m_data_ptr, &m_stride, &m_numel, &m_shape, &m_is_contiguous, &m_dtype}) {
+  for (Member *m : {&m_data_ptr, &m_stride, &m_numel, &m_shape, &m_is_contiguous, &m_dtype, &m_get_device}) {
     m->name = PyUnicode_InternFromString(m->text);
     m->descr = PyObject_GetAttrString(tensor, m->text);
     if (m->name == nullptr || m->descr == nullptr) return nullptr;

@@ -1,0 +1,154 @@
+"""The global gradient norm and clipping against the fp64 oracle.  Tolerances: squares are summed
+in fp32 8 at a time (4 additions and a product: 5 half-ulps of a sum of positive terms), then in
+64 bits; the root halves that, one rounding to fp32 at the end: 2^-21.  A clipped value is off by the
+norm's error, the products' and the rounding to its type."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import block_ref as R
+from oracle.lowbit_ref import bf16_half_step
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def block():
+    from mixture_experts_grouped_router_gb300 import block
+    return block
+
+
+def f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64).ravel()
+
+
+def check_outs(grads, outs, factor, slack=2.0 ** -20):
+    for g, o in zip(grads, outs):
+        want = g * factor
+        half = bf16_half_step(want) if o.dtype == BF else np.abs(want) * 2.0 ** -24 + 2.0 ** -149
+        assert (np.abs(f64(o) - want) <= half + slack * np.abs(want)).all()
+
+
+SETS = [[1], [8], [0, 3], [4096, 1, 1023, 1024, 1025, 7, 0, 33], [100000], [1 << 21, 12345],
+        [(1 << 24) + 1000, 17]]
+
+
+@pytest.mark.parametrize("sizes", SETS, ids=str)
+@pytest.mark.parametrize("types", ["bf16", "fp32", "mixed"])
+@pytest.mark.parametrize("into", ["place", "same", "fp32", "bf16"])
+def test_norm_and_clip(block, sizes, types, into):
+    gen = torch.Generator(device="cuda").manual_seed(len(sizes))
+    t = {"bf16": [BF], "fp32": [F32], "mixed": [BF, F32]}[types]
+    grads = [torch.randn(n, generator=gen, device="cuda").to(t[i % len(t)]) for i, n in enumerate(sizes)]
+    values = [f64(g) for g in grads]
+    outs = None
+    if into != "place":
+        want_t = {"same": None, "fp32": F32, "bf16": BF}[into]
+        outs = [torch.full_like(g, 9.0, dtype=want_t or g.dtype) for g in grads]
+    c = block.GradClip(grads, outs)
+    norm, _ = R.clip(values, 1.0, 0.25)
+    assert abs(float(c.norm(0.25)) - norm) <= 2.0 ** -21 * norm
+    assert all((f64(g) == v).all() for g, v in zip(grads, values))
+    most = 0.3 * norm
+    want_norm, factor = R.clip(values, most, 0.25)
+    assert abs(float(c.clip(most, 0.25)) - want_norm) <= 2.0 ** -21 * want_norm
+    check_outs(values, grads if outs is None else outs, factor)
+
+
+@pytest.mark.parametrize("shift", [1, 2, 3, 5, 7])
+@pytest.mark.parametrize("out_shift", [None, 0, 1, 4])
+@pytest.mark.parametrize("g_type,o_type", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
+def test_views_at_odd_offsets(block, shift, out_shift, g_type, o_type):
+    n = 5000
+    gen = torch.Generator(device="cuda").manual_seed(shift)
+    whole = torch.randn(n + 16, generator=gen, device="cuda").to(g_type)
+    g = whole[shift:shift + n]
+    v, before = f64(g), whole.clone()
+    outs, ow = None, None
+    if out_shift is not None:
+        ow = torch.full((n + 16,), 9.0, dtype=o_type, device="cuda")
+        outs = [ow[out_shift:out_shift + n]]
+    elif g_type != o_type:
+        pytest.skip("in place with one type")
+    c = block.GradClip([g], outs)
+    norm, factor = R.clip([v], 2.0, 1.0)
+    assert abs(float(c.clip(2.0)) - norm) <= 2.0 ** -21 * norm
+    check_outs([v], [g if outs is None else outs[0]], factor)
+    if outs is None:  # what lies around the view stays
+        assert torch.equal(whole[:shift], before[:shift]) and torch.equal(whole[shift + n:], before[shift + n:])
+    else:
+        assert torch.equal(whole, before)
+        assert (ow[:out_shift] == 9.0).all() and (ow[out_shift + n:] == 9.0).all()
+
+
+def test_small_norms_are_not_clipped(block):
+    g = torch.tensor([3.0, 4.0], device="cuda")
+    out = torch.empty_like(g)
+    assert float(block.GradClip([g], [out]).clip(5.1)) == 5.0 and torch.equal(out, g)
+    assert float(block.GradClip([g]).clip(float("inf"))) == 5.0 and g.tolist() == [3.0, 4.0]
+    assert float(block.GradClip([g], [out]).clip(float("inf"), 0.5)) == 2.5 and out.tolist() == [1.5, 2.0]
+    assert float(block.GradClip([g], [out]).clip(0.0)) == 5.0 and out.tolist() == [0.0, 0.0]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("size", [1e-38, 1e-30, 1e-22, 1e-12, 1e18, 1e25, 1e35])
+def test_squares_past_fp32(block, dtype, size):
+    """Values whose squares are over or under fp32's range, alone and beside ordinary ones."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    base = torch.randn(3001, generator=gen, device="cuda").double().clamp(-2.5, 2.5)
+    g = (base * size).to(dtype)
+    v = f64(g)
+    norm = float(np.sqrt((v * v).sum()))
+    got = float(block.GradClip([g]).norm())
+    # (a subnormal norm's own spacing)
+    assert abs(got - norm) <= 2.0 ** -21 * norm + 2.0 ** -149
+    mixed = block.GradClip([g, torch.zeros(5000, dtype=BF, device="cuda"), torch.ones(100, device="cuda")])
+    both = float(np.sqrt((v * v).sum() + 100.0))
+    assert abs(float(mixed.norm()) - both) <= 2.0 ** -21 * both
+    out = torch.empty_like(g)
+    float(block.GradClip([g], [out]).clip(0.5 * norm if norm > 1e-4 else 1.0))
+    if norm > 1e-4:
+        check_outs([v], [out], 0.5 / (1 + 1e-6 / norm))
+    else:
+        assert torch.equal(out, g)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_a_norm_that_is_no_number_clips_nothing(block, bad):
+    g = torch.ones(3000, device="cuda").to(BF)
+    g[1234] = bad
+    before = g.clone()
+    c = block.GradClip([g])
+    n = float(c.clip(1.0))
+    assert (np.isnan(n) if np.isnan(bad) else n == np.inf)
+    torch.testing.assert_close(g, before, rtol=0, atol=0, equal_nan=True)
+
+
+def test_same_numbers_each_time_and_zeros(block):
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    g = [torch.randn(n, generator=gen, device="cuda").to(BF) for n in (70001, 300000, 5)]
+    c = block.GradClip(g)
+    assert len({float(c.norm()) for _ in range(5)}) == 1
+    z = torch.zeros(9999, device="cuda")
+    assert float(block.GradClip([z]).clip(1.0)) == 0.0 and (z == 0).all()
+
+
+def test_many_tensors(block):
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    g = [torch.randn(1 + (i * 37) % 500, generator=gen, device="cuda").to(BF if i % 3 else F32) for i in range(1500)]
+    v = [f64(t) for t in g]
+    norm, factor = R.clip(v, 1.0, 1.0)
+    assert abs(float(block.GradClip(g).clip(1.0)) - norm) <= 2.0 ** -21 * norm
+    check_outs(v, g, factor)
+
+
+def test_a_tensor_past_32_bits(block):
+    n = (1 << 32) + 4099
+    g = torch.zeros(n, dtype=BF, device="cuda")
+    at = torch.tensor([0, (1 << 31) + 1, (1 << 32) + 4098], device="cuda")
+    g[at] = torch.tensor([3.0, 4.0, 12.0], device="cuda").to(BF)
+    c = block.GradClip([g])
+    assert float(c.clip(6.5)) == 13.0
+    assert g[at].tolist() == [1.5, 2.0, 6.0] and int(torch.count_nonzero(g)) == 3

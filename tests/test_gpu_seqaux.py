@@ -1,0 +1,209 @@
+"""The balance loss of sequences with the z loss against the fp64 oracle.  Tolerances: the
+exponentials, logarithms and divisions are within 2 ulp of fp32, a token's sums over at most 8
+values a lane and 5 lanes' additions: 2^-19 of a probability, twice that of the gradient's terms
+(2^-18 of their size); lse also half an ulp of its own size and 2^-22 of the largest logit.  Means
+over tokens take at most `adds` additions: adds 2^-24."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import block_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def block():
+    from mixture_experts_grouped_router_gb300 import block
+    return block
+
+
+@pytest.fixture(scope="module")
+def L():
+    from mixture_experts_grouped_router_gb300 import _lib
+    return _lib
+
+
+def f64(t):
+    return t.detach().cpu().numpy().astype(np.float64)
+
+
+def i32(a):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
+
+
+def case(T, E, k, seed=0):
+    rng = np.random.default_rng(seed + 7 * T + E)
+    x = (rng.standard_normal((T, E)) + 0.7 * rng.standard_normal(E)).astype(np.float32)
+    return rng, x, np.argsort(-x, 1, kind="stable")[:, :k].astype(np.int32)
+
+
+def check(got, want, E, T, factor=1.0):
+    loss, counts, tokens, probs, d = got
+    assert (counts.cpu().numpy() == want["counts"]).all()
+    assert (tokens.cpu().numpy() == want["tokens"]).all()
+    mean = 2.0 ** -19 + (T / 152.0 + 64) * 2.0 ** -24
+    assert (np.abs(f64(probs) - want["probs"]) <= mean * want["probs"] + 1e-37).all()
+    assert (np.abs(f64(loss) - want["loss"]) <= 2 * mean * np.abs(want["loss"]) + 1e-37).all()
+    if d is not None:
+        assert (np.abs(f64(d) - factor * want["d_logits"])
+                <= 2.0 ** -18 * abs(factor) * want["size"] + 1e-37).all()
+
+
+SHAPES = [(1, 2, 1), (5, 7, 3), (256, 8, 2), (1000, 16, 4), (257, 32, 8), (300, 60, 6), (2000, 64, 1),
+          (777, 100, 2), (130, 160, 8), (500, 255, 5), (1111, 256, 16)]
+
+
+@pytest.mark.parametrize("T,E,k", SHAPES)
+@pytest.mark.parametrize("sigmoid", [0, 1])
+@pytest.mark.parametrize("B,masked", [(1, False), (4, True), (40, False)])
+def test_loss_and_gradient(block, T, E, k, sigmoid, B, masked):
+    rng, x, idx = case(T, E, k, B)
+    cut = np.sort(rng.integers(0, T + 1, B + 1))
+    if B == 1:
+        cut = np.array([0, T])
+    if B == 4:
+        cut[2] = cut[1]                # an empty sequence
+    mask = rng.random(T) > 0.3 if masked else None
+    if masked:
+        mask[cut[0]:cut[1]] = False    # and one without live tokens
+    m = None if mask is None else torch.tensor(mask, device="cuda")
+    want = R.seq_aux(x, idx, cut, mask, bool(sigmoid), 0.3, 0.05)
+    lx, li, off = torch.tensor(x, device="cuda"), i32(idx), i32(cut)
+    s = block.SeqAuxLoss(T + 3, E, k, B, sigmoid, 0.3, 0.05)
+    s.workspace.fill_(0xFF)
+    d = torch.full((T, E), 9.0, device="cuda")
+    assert s.forward(lx, li, off, m, d_logits=d) is s.loss
+    check((s.loss, s.counts, s.tokens, s.probs, d), want, E, T)
+    # the gradient by itself is the same one
+    d2 = torch.full_like(d, 9.0)
+    s.backward(lx, off, d2, m, accumulate=False)
+    assert torch.equal(d, d2)
+    # scaled, and added: tokens that are not live keep theirs
+    base = torch.randn(T, E, device="cuda")
+    d3 = base.clone()
+    s.backward(lx, off, d3, m, d_loss=-2.0)
+    sum_ = f64(base) - 2.0 * want["d_logits"]
+    assert (np.abs(f64(d3) - sum_) <= 2.0 ** -17 * want["size"] + 2.0 ** -23 * np.abs(sum_) + 1e-37).all()
+    dead = np.ones(T, bool)
+    dead[np.concatenate(R.live_tokens(T, cut, mask))] = False
+    dead = torch.tensor(dead, device="cuda")
+    assert torch.equal(d3[dead], base[dead]) and (d[dead] == 0).all()
+    # the loss alone; the same numbers each time
+    first = [t.clone() for t in (s.loss, s.counts, s.tokens, s.probs)]
+    s.forward(lx, li, off, m)
+    assert all(torch.equal(a, b) for a, b in zip(first, (s.loss, s.counts, s.tokens, s.probs)))
+    d4 = base.clone()
+    s.forward(lx, li, off, m, d_logits=d4, d_loss=-2.0, accumulate=True)
+    assert torch.equal(d3, d4)
+
+
+@pytest.mark.parametrize("sigmoid", [0, 1])
+def test_one_sequence_is_moe_aux_loss(L, block, sigmoid):
+    T, E, k = 500, 32, 4
+    _, x, idx = case(T, E, k)
+    lx, li = torch.tensor(x, device="cuda"), i32(idx)
+    s = block.SeqAuxLoss(T, E, k, 1, sigmoid, 0.1)
+    d, d_old = torch.empty_like(lx), torch.empty_like(lx)
+    s.forward(lx, li, i32([0, T]), d_logits=d)
+    counts, probs, loss = torch.empty(E, dtype=torch.int32, device="cuda"), torch.empty(E, device="cuda"), torch.empty(1, device="cuda")
+    ws = torch.empty(L.moe_aux_loss_workspace_bytes(T, E), dtype=torch.uint8, device="cuda")
+    L.moe_aux_loss(lx, li, sigmoid, 0.1, counts, probs, loss, ws)
+    L.moe_aux_loss_bwd(lx, counts, k, sigmoid, 0.1, d_old, accumulate=False)
+    assert torch.equal(s.counts[0], counts) and s.loss[1] == 0
+    torch.testing.assert_close(s.loss[:1], loss, rtol=1e-5, atol=0)
+    torch.testing.assert_close(s.probs[0], probs, rtol=1e-5, atol=0)
+    torch.testing.assert_close(d, d_old, rtol=1e-4, atol=float(d_old.abs().max()) * 1e-5)
+
+
+@pytest.mark.parametrize("E,pad", [(8, 4), (60, 4), (64, 3), (33, 2), (256, 8)])
+def test_strided_rows(block, E, pad):
+    """Leading dimensions that keep rows on 16 bytes and that do not; spare columns stay."""
+    T, k = 300, 2
+    _, x, idx = case(T, E, k)
+    want = R.seq_aux(x, idx, [10, 200, 290], None, False, 0.3, 0.05)
+    whole = torch.full((T, E + pad), 1e30, device="cuda")
+    whole[:, :E] = torch.tensor(x)
+    dw = torch.full((T, E + pad), 9.0, device="cuda")
+    s = block.SeqAuxLoss(T, E, k, 2, 0, 0.3, 0.05)
+    s.forward(whole[:, :E], i32(idx), i32([10, 200, 290]), d_logits=dw[:, :E])
+    check((s.loss, s.counts, s.tokens, s.probs, dw[:, :E]), want, E, T)
+    assert (dw[:, E:] == 9.0).all()
+    # a base address off 16 bytes
+    flat = torch.empty(T * E + 1, device="cuda")
+    odd = flat[1:].view(T, E)
+    odd.copy_(torch.tensor(x))
+    s.forward(odd, i32(idx), i32([10, 200, 290]), d_logits=dw[:, :E])
+    check((s.loss, s.counts, s.tokens, s.probs, dw[:, :E]), want, E, T)
+
+
+@pytest.mark.parametrize("sigmoid", [0, 1])
+def test_odd_logits_and_choices(block, sigmoid):
+    """-inf for closed experts, rows of -inf alone, NaN, huge logits; choices out of range."""
+    T, E, k = 64, 12, 2
+    _, x, idx = case(T, E, k)
+    x[:, 5] = -np.inf
+    x[3] = -np.inf
+    x[4] = np.nan
+    x[5, 2] = np.nan
+    x[6] = np.where(np.arange(E) == 1, 1e4, -1e4)
+    x[7] = np.finfo(np.float32).min
+    idx[8, 0], idx[9, 1], idx[10, 0] = -1, E, 2 ** 31 - 1
+    off = [0, 30, T]
+    want = R.seq_aux(x, idx, off, None, bool(sigmoid), 0.3, 0.0)
+    s = block.SeqAuxLoss(T, E, k, 2, sigmoid, 0.3)
+    d = torch.empty(T, E, device="cuda")
+    s.forward(torch.tensor(x, device="cuda"), i32(idx), i32(off), d_logits=d)
+    check((s.loss, s.counts, s.tokens, s.probs, d), want, E, T)
+    assert torch.isfinite(d).all()
+
+
+def test_offsets_out_of_range_stay_in_bounds(block):
+    """Offsets past T or below 0 are clamped."""
+    T, E, k = 100, 8, 2
+    _, x, idx = case(T, E, k)
+    s = block.SeqAuxLoss(T, E, k, 3, 0, 0.3, 0.05)
+    d = torch.empty(T, E, device="cuda")
+    off = [-5, 20, 90, 5000]
+    s.forward(torch.tensor(x, device="cuda"), i32(idx), i32(off), d_logits=d)
+    check((s.loss, s.counts, s.tokens, s.probs, d), R.seq_aux(x, idx, off, None, False, 0.3, 0.05), E, T)
+
+
+@pytest.mark.parametrize("T", [0, 40])
+def test_nothing_live(block, T):
+    E, k, B = 8, 2, 3
+    s = block.SeqAuxLoss(T, E, k, B, 0, 0.3, 0.05)
+    x = torch.randn(T, E, device="cuda")
+    d = torch.full((T, E), 9.0, device="cuda")
+    for mask, off in ((torch.zeros(T, dtype=torch.bool, device="cuda"), [0, 10, 20, T]), (None, [T] * 4)):
+        s.loss.fill_(5.0), s.counts.fill_(5), s.tokens.fill_(5), s.probs.fill_(5.0)
+        s.forward(x, torch.zeros(T, k, dtype=torch.int32, device="cuda"), i32(off), mask, d_logits=d)
+        assert all((t == 0).all() for t in (s.loss, s.counts, s.tokens, s.probs, d))
+        s.backward(x, i32(off), d, mask, accumulate=False)
+        assert (d == 0).all()
+
+
+@pytest.mark.parametrize("T,E,k,B", [(40000, 8, 2, 1), (9000, 256, 8, 1), (5000, 16, 2, 3000)])
+def test_long_and_many_sequences(block, T, E, k, B):
+    """One sequence over every block (its choices counted by a cluster), and more sequences than
+    blocks, most of a token or none."""
+    rng, x, idx = case(T, E, k)
+    cut = np.array([0, T]) if B == 1 else np.sort(rng.integers(0, T + 1, B + 1))
+    want = R.seq_aux(x, idx, cut, None, True, 0.3, 0.05)
+    s = block.SeqAuxLoss(T, E, k, B, 1, 0.3, 0.05)
+    d = torch.empty(T, E, device="cuda")
+    s.forward(torch.tensor(x, device="cuda"), i32(idx), i32(cut), d_logits=d)
+    check((s.loss, s.counts, s.tokens, s.probs, d), want, E, T)
+
+
+def test_gradient_by_differences(block):
+    T, E, k = 6, 5, 2
+    rng, x, idx = case(T, E, k)
+    s = block.SeqAuxLoss(T, E, k, 2, 0, 0.9, 0.4)
+    d = torch.empty(T, E, device="cuda")
+    s.forward(torch.tensor(x, device="cuda"), i32(idx), i32([0, 2, 6]), d_logits=d)
+    f = lambda v: R.seq_aux(v, idx, [0, 2, 6], None, False, 0.9, 0.4)["loss"].sum()  # noqa: E731
+    for i in np.ndindex(T, E):
+        e = np.zeros((T, E))
+        e[i] = 1e-5
+        assert abs((f(x + e) - f(x - e)) / 2e-5 - f64(d)[i]) <= 1e-5
