@@ -63,20 +63,20 @@ static moe_status_t check_rows(const char *who, const char *name, const void *p,
 // ---------------------------------------------------------------- gradient clipping
 static int64_t elem_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
 
-// Elements of a chunk: 1024 where there are few in all, so that every warp gets some
+// Elements of a chunk (a warp's piece): 1024 where there are few in all, so that every warp gets some
 static int64_t chunk_elems(const moe_grad *grads, int n) {
   int64_t all = 0;
   for (int i = 0; i < n; ++i) all += std::max<int64_t>(0, grads[i].n);
-  return all < (1ll << 24) ? 1024 : 4096;
+  return all < (1ll << 24) ? 1024 : 8192;
 }
 
-// Elements before the first that starts on 16 bytes in g and, of the type of out, in out; -1:
-// there is none.
+// Elements before the first where 8 of them start on their own size (16 or 32 bytes) in g and in
+// out; -1: there is none.
 static int64_t peel(const moe_grad &t) {
   const int64_t gb = elem_bytes(t.g_dtype), ob = elem_bytes(t.out_dtype);
   for (int64_t p = 0; p < 8; ++p)
-    if ((reinterpret_cast<uintptr_t>(t.g) + p * gb) % 16 == 0 &&
-        (reinterpret_cast<uintptr_t>(t.out) + p * ob) % 16 == 0)
+    if ((reinterpret_cast<uintptr_t>(t.g) + p * gb) % (8 * gb) == 0 &&
+        (reinterpret_cast<uintptr_t>(t.out) + p * ob) % (8 * ob) == 0)
       return std::min(p, t.n);
   return -1;
 }
@@ -204,7 +204,7 @@ moe_status_t moe_mx_dequantize(const uint8_t *q, int64_t ldq, const uint8_t *sf,
   REQUIRE(rows >= 0 && cols > 0, MOE_ERR_INVALID_ARG, "%s: rows=%lld cols=%d", who, (long long)rows,
           cols);
   REQUIRE(fmt == MOE_FP8_E4M3 || fmt == MOE_FP8_E5M2, MOE_ERR_INVALID_ARG, "%s: bad fmt %d", who, fmt);
-  REQUIRE(cols % 128 == 0 && rows < (1ll << 31), MOE_ERR_UNSUPPORTED,
+  REQUIRE(cols % 128 == 0 && rows < (1ll << 31) - (1 << 20), MOE_ERR_UNSUPPORTED,
           "%s: cols=%d is no multiple of 128, or rows of 2^31 and more", who, cols);
   if (rows == 0) return MOE_OK;
   REQUIRE(q && sf && x, MOE_ERR_INVALID_ARG, "%s: null pointer", who);

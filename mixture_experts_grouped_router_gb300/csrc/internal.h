@@ -287,12 +287,12 @@ cudaError_t launch_mx_dequantize(const uint8_t *q, int64_t ldq, const uint8_t *s
 // seqaux.cu (balance loss of sequences, router z loss)
 struct SeqAuxArgs {
   const float *logits; int64_t ld; int T, E, k; int score_fn;
-  const int32_t *idx;                              // null: counts and tokens are given
+  const int32_t *idx;                              // with loss
   const int32_t *offsets; int B;
   const uint8_t *mask;                             // or null
   float coeff, z_coeff;
   int32_t *counts, *tokens;
-  float *probs, *loss;                             // null: the gradient alone
+  float *probs, *loss;                             // null: the gradient alone, counts and tokens given
   float d_loss; float *d_logits; int64_t ld_d; int accumulate;  // or null
 };
 size_t seq_aux_workspace_bytes(int T, int E, int B);
@@ -303,7 +303,7 @@ struct alignas(32) ClipChunk {  // a piece of a tensor, by the plan's own order
   const void *g;
   void *out;
   int32_t n;
-  int32_t kind;  // bit 0: g is fp32; 1: out is fp32; 2: no 16-byte accesses
+  int32_t kind;  // bit 0: g is fp32; 1: out is fp32; 2: element by element
 };
 constexpr int kClipMaxBlocks = 2048;
 cudaError_t launch_clip(const ClipChunk *plan, int64_t chunks, float scale, float max_norm, bool write,

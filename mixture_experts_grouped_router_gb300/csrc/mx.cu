@@ -345,26 +345,46 @@ mx_quantize_2x_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t rows,
 }
 
 // Values of block-scaled codes (PLAIN scales), rounded once to bf16: a warp takes 256 columns
-// of a row, 8 a lane.
+// of a row at a time, 8 a lane, four such pieces in flight.
 __global__ void __launch_bounds__(kMxThreads)
 mx_dequantize_kernel(const uint8_t *__restrict__ q, int64_t ldq, const uint8_t *__restrict__ sf,
-                     int64_t rows, int cols, int fmt, uint16_t *__restrict__ x, int64_t ldx) {
+                     int rows, int cols, int fmt, uint16_t *__restrict__ x, int64_t ldx) {
+  constexpr int kU = 4;
   const int chunks = (cols + 255) / 256, lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (kMxThreads / 32);
+  const int warp = (int)(blockIdx.x * kMxThreads + threadIdx.x) >> 5;
+  const int warps = (int)gridDim.x * (kMxThreads / 32);
+  int row = warp / chunks, ch = warp - row * chunks;
+  const int d_row = warps / chunks, d_ch = warps - d_row * chunks;
   grid_dependency_begin();
-  for (int64_t at = (int64_t)blockIdx.x * (kMxThreads / 32) + (threadIdx.x >> 5); at < rows * chunks;
-       at += warps) {
-    const int64_t r = at / chunks;
-    const int c = (int)(at - r * chunks) * 256 + lane * 8;
-    if (c >= cols) continue;
-    const uint2 w = ld_stream_v2(q + r * ldq + c);
-    const uint32_t code = ld_u8(sf + scale_byte(r, c >> 5, cols));
-    const float s = e8m0_value(code);
-    float v[8];
-    f8x8_to_f32(w, fmt, v);
+  while (row < rows) {
+    uint2 w[kU];
+    uint32_t code[kU];
+    int at[kU], col[kU];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= s;
-    st_v4(x + r * ldx + c, f32_to_bf16x8(v));
+    for (int i = 0; i < kU; ++i) {
+      at[i] = row;
+      col[i] = ch * 256 + lane * 8;
+      if (row < rows && col[i] < cols) {
+        w[i] = ld_stream_v2(q + row * ldq + col[i]);
+        code[i] = ld_u8(sf + scale_byte(row, col[i] >> 5, cols));
+      }
+      row += d_row;
+      ch += d_ch;
+      if (ch >= chunks) {
+        ch -= chunks;
+        ++row;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      if (at[i] >= rows || col[i] >= cols) continue;
+      const float s = e8m0_value(code[i]);
+      float v[8];
+      f8x8_to_f32(w[i], fmt, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= s;
+      st_v4(x + at[i] * ldx + col[i], f32_to_bf16x8(v));
+    }
   }
 }
 
@@ -376,7 +396,7 @@ cudaError_t launch_mx_dequantize(const uint8_t *q, int64_t ldq, const uint8_t *s
   const int64_t blocks = (warps + kMxThreads / 32 - 1) / (kMxThreads / 32);
   const int64_t most = (int64_t)num_sms() * blocks_per_sm<mx_dequantize_kernel>(kMxThreads);
   return launch_dependent(mx_dequantize_kernel, (unsigned)std::min(blocks, most), kMxThreads, 0, s, q,
-                          ldq, sf, rows, cols, fmt, x, ldx);
+                          ldq, sf, (int)rows, cols, fmt, x, ldx);
 }
 
 int64_t mx_atom_rows(int64_t rows, int row_map, int E) {

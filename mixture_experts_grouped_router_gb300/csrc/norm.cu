@@ -27,6 +27,8 @@ struct Vec8<uint16_t> {
   uint4 a;
   MOE_DEVINL void zero() { a = make_uint4(0, 0, 0, 0); }
   MOE_DEVINL void load(const uint16_t *p) { a = ld_stream_v4(p); }
+  template <typename F>
+  MOE_DEVINL void take(F piece) { a = piece(0); }  // from its pieces of 16 bytes
   MOE_DEVINL void get(float *v) const { bf16x8_to_f32(a, v); }
   MOE_DEVINL void set(const float *v) { a = f32_to_bf16x8(v); }
   MOE_DEVINL void store(uint16_t *p) const { st_v4(p, a); }
@@ -39,6 +41,11 @@ struct Vec8<float> {
   MOE_DEVINL void load(const float *p) {
     a = ld_stream_v4(p);
     b = ld_stream_v4(p + 4);
+  }
+  template <typename F>
+  MOE_DEVINL void take(F piece) {
+    a = piece(0);
+    b = piece(1);
   }
   MOE_DEVINL void get(float *v) const {
     const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -122,6 +129,10 @@ rms_norm_kernel(const RmsNormArgs a, int W, int teams) {
       if (res != nullptr) hv[v].load(res + row * a.ld_res + c);
     }
   }
+  // one vector a lane (few rows): the weights come along, not a latency later
+  constexpr bool kEarly = VPL == 1;
+  float we[8];
+  if (kEarly && t.col(0) < a.cols) load_w(a.w, a.w_dtype, t.col(0), we);
   float ss = 0.0f;
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
@@ -144,9 +155,9 @@ rms_norm_kernel(const RmsNormArgs a, int W, int teams) {
     const bool in = c < a.cols;
     float f[8], w[8];
     hv[v].get(f);
-    if (in) load_w(a.w, a.w_dtype, c, w);
+    if (!kEarly && in) load_w(a.w, a.w_dtype, c, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = in ? f[i] * r * w[i] : 0.0f;
+    for (int i = 0; i < 8; ++i) f[i] = in ? f[i] * r * (kEarly ? we[i] : w[i]) : 0.0f;
     const uint4 y = f32_to_bf16x8(f);
     if (a.y != nullptr && in) st_v4(a.y + row * a.ldy + c, y);
     if (CODES == MOE_CODES_MX) {
@@ -184,43 +195,87 @@ MOE_DEVINL void weights(const RmsNormBwdArgs &a, int col, float *w) {
   if (col < a.cols) load_w(a.w, a.w_dtype, col, w);
 }
 
+// 16 bytes from global to shared memory, asynchronously.
+MOE_DEVINL void copy_async(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
+}
+
 // Backward: a block's teams walk over rows and keep their columns' sums of dy h r in
 // registers; at the end the block's teams are added up in order and the block's row of
 // `part` is written.  part == NULL: no gradient of w is wanted.
+//
+// Rows come in by asynchronous copies, `stages` rows ahead of the arithmetic: every thread
+// copies what it will read itself (h, dy, d_residual: kChunks pieces of 16 bytes), so that
+// no barrier is needed and loads stay under way while a row's sums are taken.
 // kThreads: the most that a block has; w stays in registers where that is 512.
 template <int VPL, typename S, int kThreads>
 __global__ void __launch_bounds__(kThreads)
-rms_norm_bwd_kernel(const RmsNormBwdArgs a, int W, int teams, float *__restrict__ part) {
+rms_norm_bwd_kernel(const RmsNormBwdArgs a, int W, int teams, int stages, float *__restrict__ part) {
+  constexpr int kWide = sizeof(S) / 2;             // pieces of 8 elements of the stream
+  constexpr int kPieces = VPL * (2 * kWide + 1);   // of a thread and row
   __shared__ float red[2][2][32];
-  extern __shared__ float s_dw[];  // [teams - 1][cols]
+  extern __shared__ __align__(16) uint8_t smem[];  // [stages][kPieces][threads][16]
   const Team t(W);
   constexpr bool kKeepW = kThreads <= 512;
   float dw[VPL][8], kept[kKeepW ? VPL : 1][8];
+  const S *h = static_cast<const S *>(a.h);
+  const S *res = static_cast<const S *>(a.d_residual);
+  S *dh = static_cast<S *>(a.dh);
+  const int64_t step = (int64_t)gridDim.x * teams;
+  int64_t row = (int64_t)blockIdx.x * teams + t.id, ahead = row;
+  const int piece = blockDim.x * 16, stage = kPieces * piece;
+  uint8_t *mine = smem + threadIdx.x * 16;
+  auto fetch = [&](int s) {
+    if (ahead < a.rows) {
+      uint8_t *to = mine + s * stage;
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) {
+        const int c = t.col(v);
+        if (c < a.cols) {
+#pragma unroll
+          for (int k = 0; k < kWide; ++k) {
+            copy_async(to + (v * kWide + k) * piece, h + ahead * a.ldh + c + 4 * k);
+            if (res != nullptr)
+              copy_async(to + ((VPL + v) * kWide + k) * piece, res + ahead * a.ld_dres + c + 4 * k);
+          }
+          copy_async(to + (2 * VPL * kWide + v) * piece, a.dy + ahead * a.ld_dy + c);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ahead += step;
+  };
+  auto piece_at = [&](int s, int k) {
+    return *reinterpret_cast<const uint4 *>(mine + s * stage + k * piece);
+  };
   grid_dependency_begin();
+  for (int s = 0; s < stages; ++s) fetch(s);
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[v][i] = 0.0f;
     if (kKeepW) weights(a, t.col(v), kept[v]);
   }
-  const S *h = static_cast<const S *>(a.h);
-  const S *res = static_cast<const S *>(a.d_residual);
-  S *dh = static_cast<S *>(a.dh);
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * teams + t.id; row < a.rows;
-       row += (int64_t)gridDim.x * teams, turn ^= 1) {
+  int turn = 0, s = 0;
+  for (; row < a.rows; row += step, turn ^= 1) {
+    // all but the rows ahead have landed
+    if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (stages == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
     uint4 dy[VPL];
     Vec8<S> hv[VPL], rv[VPL];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-      const int c = t.col(v);
       dy[v] = make_uint4(0, 0, 0, 0);
       hv[v].zero();
       rv[v].zero();
-      if (c < a.cols) {
-        hv[v].load(h + row * a.ldh + c);
-        dy[v] = ld_stream_v4(a.dy + row * a.ld_dy + c);
-        if (res != nullptr) rv[v].load(res + row * a.ld_dres + c);
+      if (t.col(v) < a.cols) {
+        hv[v].take([&](int k) { return piece_at(s, v * kWide + k); });
+        if (res != nullptr) rv[v].take([&](int k) { return piece_at(s, (VPL + v) * kWide + k); });
+        dy[v] = piece_at(s, 2 * VPL * kWide + v);
       }
     }
     float ss = 0.0f, gh = 0.0f;
@@ -236,6 +291,8 @@ rms_norm_bwd_kernel(const RmsNormBwdArgs a, int W, int teams, float *__restrict_
         gh = fmaf(g[i] * (kKeepW ? kept[v][i] : w[i]), f[i], gh);
       }
     }
+    fetch(s);  // (what was there is in registers)
+    if (++s == stages) s = 0;
     ss = warp_sum(ss);
     gh = warp_sum(gh);
     if (W > 1) {  // (two buffers in turn: the next row's sums need no second barrier)
@@ -248,7 +305,7 @@ rms_norm_bwd_kernel(const RmsNormBwdArgs a, int W, int teams, float *__restrict_
       gh = warp_sum(t.lane < W ? red[turn][1][t.id * W + t.lane] : 0.0f);
     }
     const float r = rsqrtf(ss / (float)a.cols + a.eps);
-    const float s = r * r * r * (gh / (float)a.cols);
+    const float s3 = r * r * r * (gh / (float)a.cols);
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       const int c = t.col(v);
@@ -260,7 +317,7 @@ rms_norm_bwd_kernel(const RmsNormBwdArgs a, int W, int teams, float *__restrict_
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         dw[v][i] = fmaf(g[i], f[i] * r, dw[v][i]);
-        d[i] += fmaf(-s, f[i], r * (g[i] * (kKeepW ? kept[v][i] : w[i])));
+        d[i] += fmaf(-s3, f[i], r * (g[i] * (kKeepW ? kept[v][i] : w[i])));
       }
       if (c < a.cols) {
         Vec8<S> o;
@@ -271,6 +328,9 @@ rms_norm_bwd_kernel(const RmsNormBwdArgs a, int W, int teams, float *__restrict_
     }
   }
   if (part == nullptr) return;
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  float *s_dw = reinterpret_cast<float *>(smem);  // [teams - 1][cols]
   if (t.id > 0) {
 #pragma unroll
     for (int v = 0; v < VPL; ++v)
@@ -342,23 +402,54 @@ cudaError_t norm_by_size(const RmsNormArgs &a, cudaStream_t st) {
 
 constexpr int kBwdVpl = 2;  // 16384 columns in 32 warps
 
-// Blocks that the backward is launched with at most: two a SM of 512 threads or less.
+// How the backward is laid out over a SM: blocks, rows ahead, bytes of a block.
+struct BwdShape {
+  int W, teams, threads, per_sm, stages;
+  size_t smem;
+  BwdShape(int cols, int elem) {
+    W = team_warps(cols, kBwdVpl);
+    teams = std::max(1, 8 / W);
+    threads = 32 * W * teams;
+    per_sm = std::max(1, kBwdResident / threads);
+    const size_t stage = (size_t)threads * 16 * kBwdVpl * (elem + 1);
+    const size_t each = kBwdSmem / per_sm;
+    stages = (int)std::min<size_t>(3, each / stage);
+    smem = std::max(stage * stages, (size_t)(teams - 1) * cols * sizeof(float));
+  }
+  static constexpr int kBwdResident = 512;   // threads of a SM (128 registers)
+  static constexpr size_t kBwdSmem = 216 << 10;
+};
+
+// Blocks that the backward is launched with at most (its rows of `part`).
 int64_t bwd_parts(int64_t rows, int cols) {
-  const int W = team_warps(cols, kBwdVpl), teams = std::max(1, 8 / W);
-  const int64_t most = 160 * std::max(1, 1024 / (32 * W * teams));
-  return std::min<int64_t>((rows + teams - 1) / teams, most);
+  const BwdShape b(cols, 2);
+  return std::min<int64_t>((rows + b.teams - 1) / b.teams, 160 * b.per_sm);
+}
+
+template <auto Kernel>
+cudaError_t allow_smem() {
+  static PerDevice<cudaError_t> done;
+  return done.get(current_device(), [] {
+    return cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)BwdShape::kBwdSmem);
+  });
+}
+
+template <typename S, int kThreads>
+cudaError_t bwd_kernel(const RmsNormBwdArgs &a, const BwdShape &b, unsigned grid, float *part, cudaStream_t st) {
+  const cudaError_t e = allow_smem<rms_norm_bwd_kernel<kBwdVpl, S, kThreads>>();
+  if (e != cudaSuccess) return e;
+  return launch_dependent(rms_norm_bwd_kernel<kBwdVpl, S, kThreads>, grid, b.threads, b.smem, st, a, b.W,
+                          b.teams, b.stages, part);
 }
 
 template <typename S>
 cudaError_t bwd_launch(const RmsNormBwdArgs &a, float *part, cudaStream_t st) {
-  const int W = team_warps(a.cols, kBwdVpl), teams = std::max(1, 8 / W);
-  const int threads = 32 * W * teams;
-  const int64_t resident = (int64_t)num_sms() * std::max(1, 1024 / threads);
-  const unsigned grid = (unsigned)std::min(bwd_parts(a.rows, a.cols), resident);
-  const size_t smem = part == nullptr ? 0 : (size_t)(teams - 1) * a.cols * sizeof(float);
-  cudaError_t e = threads <= 512
-      ? launch_dependent(rms_norm_bwd_kernel<kBwdVpl, S, 512>, grid, threads, smem, st, a, W, teams, part)
-      : launch_dependent(rms_norm_bwd_kernel<kBwdVpl, S, 1024>, grid, threads, smem, st, a, W, teams, part);
+  const BwdShape b(a.cols, (int)sizeof(S));
+  const unsigned grid =
+      (unsigned)std::min<int64_t>(bwd_parts(a.rows, a.cols), (int64_t)num_sms() * b.per_sm);
+  const cudaError_t e = b.threads <= 512 ? bwd_kernel<S, 512>(a, b, grid, part, st)
+                                         : bwd_kernel<S, 1024>(a, b, grid, part, st);
   if (e != cudaSuccess || part == nullptr) return e;
   return launch_dependent(dw_sum_kernel, (unsigned)((a.cols + 31) / 32), dim3(32, kSumRows), 0, st,
                           part, (int)grid, a.cols, a.dw, a.accumulate);

@@ -154,8 +154,8 @@ def test_clip(L):
 
 
 def test_a_plan_covers_every_element_once(L):
-    """Chunks of tensors of any size, type and alignment: in order, whole, 16-byte accesses only
-    where both sides of a chunk start on 16 bytes."""
+    """Chunks of tensors of any size, type and alignment: in order, whole, accesses of 8 elements
+    only where both sides of a chunk start on the size of 8 (16 or 32 bytes)."""
     import struct
     for g_at, o_at, gt, ot, n in [(4096, 8192, 0, 0, 5000), (4098, 8194, 0, 0, 5000), (4098, 8192, 0, 1, 3000),
                                   (4100, 8200, 1, 1, 4097), (4104, 8208, 0, 1, 9000), (4110, 8196, 0, 1, 7),
@@ -170,7 +170,7 @@ def test_a_plan_covers_every_element_once(L):
             assert p == g_at + at * gs and o == o_at + at * os and m > 0
             assert (kind & 1) == gt and (kind >> 1 & 1) == ot
             if not kind & 4:
-                assert p % 16 == 0 and o % 16 == 0
+                assert p % (8 * gs) == 0 and o % (8 * os) == 0
             at += m
         assert at == n
 
