@@ -28,9 +28,7 @@ MOE_DEVINL ClipChunk load_chunk(const ClipChunk *p) {
 // A type's 8 consecutive elements, in one access (32 bytes of fp32).
 struct Bf16x8 {
   using Elem = uint16_t;
-  static constexpr int kU = 8;  // vectors in flight: 128 bytes a lane
   uint4 a;
-  MOE_DEVINL void zero() { a = make_uint4(0, 0, 0, 0); }
   MOE_DEVINL void load(const uint16_t *p) { a = ld_stream_v4(p); }
   MOE_DEVINL void get(float *v) const { bf16x8_to_f32(a, v); }
   MOE_DEVINL static float one(const uint16_t *p) { return __uint_as_float(ld_u16(p) << 16); }
@@ -42,12 +40,7 @@ struct Bf16x8 {
 
 struct F32x8 {
   using Elem = float;
-  static constexpr int kU = 4;
   float f[8];
-  MOE_DEVINL void zero() {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 0.0f;
-  }
   MOE_DEVINL void load(const float *p) { ld_stream_f32x8(p, f); }
   MOE_DEVINL void get(float *v) const {
 #pragma unroll
@@ -58,66 +51,87 @@ struct F32x8 {
   MOE_DEVINL static void store_one(float *p, float v) { *p = v; }
 };
 
-// Values whose squares leave fp32's range are squared in 64 bits.  That is looked at for
-// 32 or 64 values at a time, by their fp32 sum: one that is neither 0 nor in the range's
+// Squares are summed from pieces of 16 bytes, kPieces a lane at a time, copied to shared
+// memory kAhead times ahead (each lane reads what it copied: no barrier).
+constexpr int kPieces = 8;
+constexpr int kAhead = 3;
+constexpr int kSquareSmem = kAhead * kPieces * 16 * kThreads;
+
+// Values whose squares leave fp32's range are squared in 64 bits.  That is looked at for 32
+// or 64 values at a time, by their fp32 sum: one that is neither 0 nor in the range's
 // middle, where squares that vanish are nothing beside it.  (64-bit additions are slow on
-// GB300: one for every 8 values took 0.3 ms of 1.4 G values.)
+// GB300: one for every 8 values took 0.1 ms of 1.4 G values.)
 MOE_DEVINL bool in_range(float s) { return s >= 1e-28f && s <= 1e37f; }
 
-template <typename V>
-MOE_DEVINL double square_sum_64(const V *raw) {
-  double s = 0.0;
-  for (int u = 0; u < V::kU; ++u) {
-    float v[8];
-    raw[u].get(v);
-    for (int i = 0; i < 8; ++i) s += (double)v[i] * (double)v[i];
+MOE_DEVINL int values(const uint4 &w, bool f32, float *v) {
+  if (!f32) {
+    bf16x8_to_f32(w, v);
+    return 8;
   }
-  return s;
+  v[0] = __uint_as_float(w.x);
+  v[1] = __uint_as_float(w.y);
+  v[2] = __uint_as_float(w.z);
+  v[3] = __uint_as_float(w.w);
+  return 4;
 }
 
-// The warp's lanes' sums of squares of a chunk, added to acc.
-template <typename V>
-MOE_DEVINL void chunk_squares(const ClipChunk &c, int lane, double &acc) {
-  const typename V::Elem *g = static_cast<const typename V::Elem *>(c.g);
-  int i = 0;
-  if (!(c.kind & 4)) {
-    for (; i + 8 <= c.n; i += 256 * V::kU) {
-      V raw[V::kU];
+template <bool F32>
+MOE_DEVINL void add_squares(const uint8_t *mine, double &acc) {
+  constexpr int kN = F32 ? 4 : 8;
+  float s[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int u = 0; u < V::kU; ++u) {
-        const int j = i + 256 * u + 8 * lane;
-        raw[u].zero();
-        if (j + 8 <= c.n) raw[u].load(g + j);
-      }
-      float s[2] = {0.0f, 0.0f}, any = 0.0f;
+  for (int u = 0; u < kPieces; ++u) {
+    float v[8];
+    values(*reinterpret_cast<const uint4 *>(mine + u * (16 * kThreads)), F32, v);
 #pragma unroll
-      for (int u = 0; u < V::kU; ++u) {
-        float v[8];
-        raw[u].get(v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[e & 1] = fmaf(v[e], v[e], s[e & 1]);
-      }
-      const float sum = s[0] + s[1];
-      if (in_range(sum)) {
-        acc += (double)sum;
-      } else {
-#pragma unroll
-        for (int u = 0; u < V::kU; ++u) {
-          float v[8];
-          raw[u].get(v);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) any = v[e] != 0.0f ? 1.0f : any;
-        }
-        if (any != 0.0f) acc += square_sum_64(raw);
-      }
-    }
-    i = c.n & ~7;
+    for (int e = 0; e < kN; ++e) s[e & 1] = fmaf(v[e], v[e], s[e & 1]);
   }
-  for (i += lane; i < c.n; i += 32) {
-    const double v = (double)V::one(g + i);
-    acc += v * v;
+  const float sum = s[0] + s[1];
+  if (in_range(sum)) {
+    acc += (double)sum;
+    return;
+  }
+  for (int u = 0; u < kPieces; ++u) {
+    float v[8];
+    values(*reinterpret_cast<const uint4 *>(mine + u * (16 * kThreads)), F32, v);
+#pragma unroll
+    for (int e = 0; e < kN; ++e)
+      if (v[e] != 0.0f) acc += (double)v[e] * (double)v[e];
   }
 }
+
+// A warp's walk over its chunks, a step of kPieces * 32 pieces at a time.
+struct Steps {
+  const ClipChunk *plan;
+  int64_t at, chunks, stride;
+  ClipChunk c, next;
+  int i, n;  // the chunk's first piece that is not taken, its pieces
+  MOE_DEVINL void start() {
+    i = 0;
+    n = at < chunks && !(c.kind & 4) ? (c.kind & 1 ? c.n >> 2 : c.n >> 3) : 0;
+  }
+  MOE_DEVINL void fetch_next() {
+    if (at + stride < chunks) next = load_chunk(plan + at + stride);
+  }
+  MOE_DEVINL Steps(const ClipChunk *p, int64_t first, int64_t count, int64_t by)
+      : plan(p), at(first), chunks(count), stride(by), c{}, next{} {
+    if (at < chunks) c = load_chunk(plan + at);
+    fetch_next();
+    start();
+  }
+  MOE_DEVINL bool done() const { return at >= chunks; }
+  // whether the step that was taken was the chunk's last one
+  MOE_DEVINL bool step() {
+    i += 32 * kPieces;
+    return i >= n;
+  }
+  MOE_DEVINL void advance() {
+    at += stride;
+    c = next;
+    fetch_next();
+    start();
+  }
+};
 
 // Sum over the block's threads, in thread 0's warp (64-bit additions being slow, by few).
 MOE_DEVINL double block_sum(double v, double *s) {
@@ -132,24 +146,55 @@ MOE_DEVINL double block_sum(double v, double *s) {
   return v;
 }
 
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 2)
 grad_square_kernel(const ClipChunk *__restrict__ plan, int64_t chunks, double *__restrict__ part) {
+  extern __shared__ __align__(16) uint8_t ring[];  // [kAhead][kPieces][threads][16]
   __shared__ double s[kThreads];
+  constexpr int kStage = kPieces * 16 * kThreads;
   const int lane = threadIdx.x & 31;
-  const int64_t step = (int64_t)gridDim.x * kWarps;
-  int64_t at = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  uint8_t *mine = ring + threadIdx.x * 16;
   double acc = 0.0;
   grid_dependency_begin();
-  ClipChunk c = {};
-  if (at < chunks) c = load_chunk(plan + at);
-  while (at < chunks) {
-    at += step;
-    ClipChunk next = {};
-    if (at < chunks) next = load_chunk(plan + at);  // on its way while this one is summed
-    if (c.kind & 1) chunk_squares<F32x8>(c, lane, acc);
-    else chunk_squares<Bf16x8>(c, lane, acc);
-    c = next;
+  const int64_t first = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  Steps in(plan, first, chunks, (int64_t)gridDim.x * kWarps);  // what is copied
+  Steps out = in;                                              // what is summed
+  auto copy = [&](int stage) {
+    if (!in.done()) {
+      const uint8_t *g = static_cast<const uint8_t *>(in.c.g);
+      uint8_t *to = mine + stage * kStage;
+#pragma unroll
+      for (int u = 0; u < kPieces; ++u) {
+        const int j = in.i + 32 * u + lane;
+        // (a copy of no bytes fills its 16 with zeros)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(to + u * (16 * kThreads))),
+                     "l"(j < in.n ? g + 16ll * j : (const uint8_t *)plan), "r"(j < in.n ? 16 : 0)
+                     : "memory");
+      }
+      if (in.step()) in.advance();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) copy(k);
+  int stage = 0;
+  while (!out.done()) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    if (out.c.kind & 1) add_squares<true>(mine + stage * kStage, acc);
+    else add_squares<false>(mine + stage * kStage, acc);
+    if (out.step()) {  // the elements that fill no piece
+      const bool f32 = out.c.kind & 1;
+      for (int i = out.c.kind & 4 ? lane : (out.n << (f32 ? 2 : 3)) + lane; i < out.c.n; i += 32) {
+        const double v = f32 ? F32x8::one(static_cast<const float *>(out.c.g) + i)
+                             : Bf16x8::one(static_cast<const uint16_t *>(out.c.g) + i);
+        acc += v * v;
+      }
+      out.advance();
+    }
+    copy(stage);
+    if (++stage == kAhead) stage = 0;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   acc = block_sum(acc, s);
   if (threadIdx.x == 0) part[blockIdx.x] = acc;
 }
@@ -163,6 +208,19 @@ MOE_DEVINL double total_of(const double *part, int parts, double *s) {
     v += p;
   }
   return block_sum(v, s);
+}
+
+// The norm, and the factor that clips (a norm that is infinite or no number: none).  In fp32
+// where everything is well inside its range: a 64-bit root and quotient take 2 us.
+MOE_DEVINL float norm_of(double sum, float scale, float &factor, float max_norm) {
+  if (sum >= 1e-30 && sum <= 1e30 && scale >= 1e-15f && scale <= 1e15f) {
+    const float total = scale * sqrtf((float)sum), q = max_norm / (total + 1e-6f);
+    factor = q < 1.0f ? scale * q : scale;
+    return total;
+  }
+  const double total = (double)scale * sqrt(sum), q = (double)max_norm / (total + 1e-6);
+  factor = total <= 1.7e308 && q < 1.0 ? (float)((double)scale * q) : scale;
+  return (float)total;
 }
 
 template <typename V, typename O>
@@ -195,7 +253,7 @@ MOE_DEVINL void chunk_scale(const ClipChunk &c, int lane, float f) {
   for (i += lane; i < c.n; i += 32) O::store_one(out + i, V::one(g + i) * f);
 }
 
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 3)
 grad_scale_kernel(const ClipChunk *__restrict__ plan, int64_t chunks, const double *__restrict__ part,
                   int parts, float scale, float max_norm, float *__restrict__ norm) {
   __shared__ double s[kThreads];
@@ -209,11 +267,8 @@ grad_scale_kernel(const ClipChunk *__restrict__ plan, int64_t chunks, const doub
   grid_dependency_begin();
   const double sum = total_of(part, parts, s);
   if (threadIdx.x == 0) {
-    const double total = (double)scale * sqrt(sum);
-    if (blockIdx.x == 0) *norm = (float)total;
-    // a norm that is no number, or infinite, clips nothing
-    const double q = (double)max_norm / (total + 1e-6);
-    s_f = total <= 1.7e308 && q < 1.0 ? (float)((double)scale * q) : scale;
+    const float total = norm_of(sum, scale, s_f, max_norm);
+    if (blockIdx.x == 0) *norm = total;
   }
   __syncthreads();
   const float f = s_f;
@@ -238,7 +293,8 @@ grad_norm_kernel(const double *__restrict__ part, int parts, float scale, float 
   __shared__ double s[kThreads];
   grid_dependency_begin();
   const double sum = total_of(part, parts, s);
-  if (threadIdx.x == 0) *norm = (float)((double)scale * sqrt(sum));
+  float factor;
+  if (threadIdx.x == 0) *norm = norm_of(sum, scale, factor, 0.0f);
 }
 
 }  // namespace
@@ -249,8 +305,13 @@ cudaError_t launch_clip(const ClipChunk *plan, int64_t chunks, float scale, floa
     const int64_t want = std::max<int64_t>(1, (chunks + kWarps - 1) / kWarps);
     return (int)std::min<int64_t>({want, (int64_t)num_sms() * per_sm, (int64_t)kClipMaxBlocks});
   };
-  const int parts = grid(blocks_per_sm<grad_square_kernel>(kThreads));
-  cudaError_t e = launch_dependent(grad_square_kernel, parts, kThreads, 0, st, plan, chunks, part);
+  static PerDevice<cudaError_t> allowed;
+  cudaError_t e = allowed.get(current_device(), [] {
+    return cudaFuncSetAttribute(grad_square_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSquareSmem);
+  });
+  if (e != cudaSuccess) return e;
+  const int parts = grid(2);
+  e = launch_dependent(grad_square_kernel, parts, kThreads, kSquareSmem, st, plan, chunks, part);
   if (e != cudaSuccess) return e;
   if (!write) return launch_dependent(grad_norm_kernel, 1, kThreads, 0, st, part, parts, scale, norm);
   return launch_dependent(grad_scale_kernel, grid(blocks_per_sm<grad_scale_kernel>(kThreads)), kThreads,

@@ -264,20 +264,20 @@ MOE_DEVINL uint2 mx_quantize8(const uint4 &w, uint32_t &code) {
   uint32_t a = amax_bits8(w);
   a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
   a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-  // floor(log2) from the bf16 bits: the exponent field, or the leading bit of a subnormal
-  const int e = a >= 0x80u ? (int)(a >> 7) - 127 : a > 0u ? (31 - __clz(a)) - 133 : -127;
-  const int s = max(-127, e - 8);
-  const float inv = __uint_as_float((uint32_t)(127 - s) << 23);  // x * 2^-s is exact
-  float v[8];
-  bf16x8_to_f32(w, v);
+  // the exponent less 8, at least 2^-127 (where subnormals and zeros end up too)
+  code = max(a >> 7, 8u) - 8u;
+  const float inv = __uint_as_float((254u - code) << 23);  // x * 2^-s is exact
+  const uint64_t inv2 = pack2(inv, inv);
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   uint16_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-        : "=h"(c[i])
-        : "f"(v[2 * i + 1] * inv), "f"(v[2 * i] * inv));
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    unpack2(mul2(pack2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u)), inv2), lo, hi);
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c[i]) : "f"(hi), "f"(lo));
+  }
   const bool finite = a < 0x7F80u;
-  code = finite ? (uint32_t)(s + 127) : 0xFFu;
+  if (!finite) code = 0xFFu;
   return finite ? make_uint2(c[0] | ((uint32_t)c[1] << 16), c[2] | ((uint32_t)c[3] << 16))
                 : make_uint2(0u, 0u);
 }

@@ -42,31 +42,51 @@ MOE_DEVINL int warp_sum_i(int v) {
   return v;
 }
 
-// Counts by sequence.  A histogram has a column a lane, so that a warp's choices of one expert
-// do not meet in a bank.
+// Counts by sequence.  A histogram has 8 columns, by lane, so that a warp's choices of one
+// expert seldom meet.
+constexpr int kCols = 8;
+constexpr int kCountThreads = 1024;  // at most
+
 struct Histogram {
-  int (*h)[32];
-  int E, lane;
+  int *h;  // [E][kCols]
+  int E;
+  MOE_DEVINL void clear() {
+    for (int i = threadIdx.x; i < E * kCols; i += blockDim.x) h[i] = 0;
+  }
   MOE_DEVINL void add(int e) {
-    if ((uint32_t)e < (uint32_t)E) atomicAdd(&h[e][lane], 1);
+    if ((uint32_t)e < (uint32_t)E) atomicAdd(&h[e * kCols + (threadIdx.x & (kCols - 1))], 1);
+  }
+  // Expert e's count (the columns in an order that keeps a warp's reads apart).
+  MOE_DEVINL int total(int e) const {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) n += h[e * kCols + ((i + (e >> 2)) & (kCols - 1))];
+    return n;
   }
   // Choices of the live tokens of [lo, hi) by the block's threads; returns the thread's live tokens.
   MOE_DEVINL int count(const SeqAuxArgs &a, int lo, int hi) {
+    const int step = blockDim.x;
     if (a.mask == nullptr) {
       const int64_t end = (int64_t)hi * a.k;
       int64_t i = (int64_t)lo * a.k + threadIdx.x;
-      for (; i + 7 * kThreads < end; i += 8 * kThreads) {
+      for (; i + 7 * step < end; i += 8 * step) {
         int e[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) e[u] = ld_i32(a.idx + i + u * kThreads);
+        for (int u = 0; u < 8; ++u) e[u] = ld_i32(a.idx + i + u * step);
 #pragma unroll
         for (int u = 0; u < 8; ++u) add(e[u]);
       }
-      for (; i < end; i += kThreads) add(ld_i32(a.idx + i));
+      for (; i < end; i += 4 * step) {
+        int e[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) e[u] = i + u * step < end ? ld_i32(a.idx + i + u * step) : -1;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) add(e[u]);
+      }
       return threadIdx.x == 0 ? hi - lo : 0;
     }
     int n = 0;
-    for (int t = lo + threadIdx.x; t < hi; t += kThreads) {
+    for (int t = lo + threadIdx.x; t < hi; t += step) {
       const bool live = ld_u8(a.mask + t) != 0;
       n += live;
       const int32_t *row = a.idx + (int64_t)t * a.k;
@@ -82,29 +102,24 @@ struct Histogram {
   }
 };
 
-// A block a sequence, where sequences are short.
-__global__ void __launch_bounds__(kThreads)
+// A block a sequence.
+__global__ void __launch_bounds__(kCountThreads)
 seq_count_kernel(const SeqAuxArgs a) {
-  __shared__ int hist[kMaxE][32];
-  __shared__ int s_n[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.x;
-  for (int i = threadIdx.x; i < a.E * 32; i += kThreads) hist[0][i] = 0;
+  __shared__ int hist[kMaxE * kCols];
+  __shared__ int s_n;
+  const int lane = threadIdx.x & 31, b = blockIdx.x;
+  Histogram h = {hist, a.E};
+  h.clear();
+  if (threadIdx.x == 0) s_n = 0;
   __syncthreads();
   grid_dependency_begin();
   const int lo = clampi(ld_i32(a.offsets + b), 0, a.T);
   const int hi = clampi(ld_i32(a.offsets + b + 1), lo, a.T);
-  Histogram h = {hist, a.E, lane};
-  int n = warp_sum_i(h.count(a, lo, hi));
-  if (lane == 0) s_n[warp] = n;
+  const int n = warp_sum_i(h.count(a, lo, hi));
+  if (lane == 0 && n > 0) atomicAdd(&s_n, n);
   __syncthreads();
-  for (int e = warp; e < a.E; e += kWarps) {
-    n = warp_sum_i(hist[e][lane]);
-    if (lane == 0) a.counts[(int64_t)b * a.E + e] = n;
-  }
-  if (warp == 0) {
-    n = warp_sum_i(lane < kWarps ? s_n[lane] : 0);
-    if (lane == 0) a.tokens[b] = n;
-  }
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) a.counts[(int64_t)b * a.E + e] = h.total(e);
+  if (threadIdx.x == 0) a.tokens[b] = s_n;
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -130,38 +145,41 @@ MOE_DEVINL int last_at_most(const int32_t *v, int n, int t, int lane) {
   return lo;
 }
 
-// A block a chunk of tokens, where a sequence is counted by many.
+// A block a chunk of tokens, where a sequence may be counted by many.
 __global__ void __launch_bounds__(kThreads)
 seq_count_chunks_kernel(const SeqAuxArgs a, int chunk) {
-  __shared__ int hist[kMaxE][32];
-  __shared__ int s_n[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = threadIdx.x; i < a.E * 32; i += kThreads) hist[0][i] = 0;
+  __shared__ int hist[kMaxE * kCols];
+  const int lane = threadIdx.x & 31;
+  const int t0 = blockIdx.x * chunk, t1 = min(a.T, t0 + chunk);
+  Histogram h = {hist, a.E};
+  h.clear();
+  // (offsets, choices and mask are older than the kernel before this one, which clears counts)
+  int b = last_at_most(a.offsets, a.B + 1, t0, lane);
   __syncthreads();
-  grid_dependency_begin();
-  const int t1 = min(a.T, (int)(blockIdx.x + 1) * chunk);
-  Histogram h = {hist, a.E, lane};
-  for (int t = blockIdx.x * chunk; t < t1;) {
-    const int b = last_at_most(a.offsets, a.B + 1, t, lane);
+  bool waited = false;
+  for (int t = t0; t < t1;) {
     const int next = b < a.B ? ld_i32(a.offsets + b + 1) : a.T;
     const int end = min(t1, max(next, t + 1));
     if (b >= 0 && b < a.B) {
-      int n = warp_sum_i(h.count(a, t, end));
-      if (lane == 0) s_n[warp] = n;
+      const int n = warp_sum_i(h.count(a, t, end));
       __syncthreads();
-      for (int e = warp; e < a.E; e += kWarps) {
-        n = warp_sum_i(hist[e][lane]);
-        hist[e][lane] = 0;
-        if (lane == 0 && n > 0) atomicAdd(a.counts + (int64_t)b * a.E + e, n);
+      if (!waited) grid_dependency_wait();
+      waited = true;
+      for (int e = threadIdx.x; e < a.E; e += kThreads) {
+        const int c = h.total(e);
+        if (c > 0) atomicAdd(a.counts + (int64_t)b * a.E + e, c);
       }
-      if (warp == 0) {
-        n = warp_sum_i(lane < kWarps ? s_n[lane] : 0);
-        if (lane == 0 && n > 0) atomicAdd(a.tokens + b, n);
+      if (lane == 0 && n > 0) atomicAdd(a.tokens + b, n);
+      if (end < t1) {
+        __syncthreads();
+        h.clear();
+        __syncthreads();
       }
-      __syncthreads();
     }
     t = end;
+    if (t < t1) b = last_at_most(a.offsets, a.B + 1, t, lane);
   }
+  grid_dependency_begin();
 }
 
 // (sequences with live tokens, live tokens) of the batch, in every thread.
@@ -574,9 +592,11 @@ cudaError_t launch_pass(const SeqAuxArgs &a, const Workspace &w, int *blocks, in
 
 cudaError_t launch_count(const SeqAuxArgs &a, cudaStream_t s) {
   const int64_t choices = (int64_t)a.T * a.k;
-  // A block a sequence where they are short on average and none can be long
-  if (choices <= 4096 || (choices / a.B <= 4096 && choices <= (1 << 17)))
-    return launch_dependent(seq_count_kernel, (unsigned)a.B, kThreads, 0, s, a);
+  // A block a sequence (of more threads where there are few) where none can have many choices
+  // (2^16: 6 us); else chunks, whose counts meet in atomics
+  if (choices <= (1 << 16) || (choices <= (1 << 18) && choices / a.B <= 2048))
+    return launch_dependent(seq_count_kernel, (unsigned)a.B, choices / a.B <= 2048 ? 256 : kCountThreads, 0,
+                            s, a);
   const int64_t cells = (int64_t)a.B * (a.E + 1);
   const unsigned zero = (unsigned)std::min<int64_t>((cells + kThreads - 1) / kThreads, num_sms());
   const cudaError_t e = launch_dependent(seq_zero_kernel, zero, kThreads, 0, s, a);
