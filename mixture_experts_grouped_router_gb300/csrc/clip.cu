@@ -25,37 +25,17 @@ MOE_DEVINL ClipChunk load_chunk(const ClipChunk *p) {
   return c;
 }
 
-// A type's 8 consecutive elements, in one access (32 bytes of fp32).
-struct Bf16x8 {
-  using Elem = uint16_t;
-  uint4 a;
-  MOE_DEVINL void load(const uint16_t *p) { a = ld_stream_v4(p); }
-  MOE_DEVINL void get(float *v) const { bf16x8_to_f32(a, v); }
-  MOE_DEVINL static float one(const uint16_t *p) { return __uint_as_float(ld_u16(p) << 16); }
-  MOE_DEVINL static void store(uint16_t *p, const float *v) { st_v4(p, f32_to_bf16x8(v)); }
-  MOE_DEVINL static void store_one(uint16_t *p, float v) {
-    *reinterpret_cast<bf16_t *>(p) = __float2bfloat16_rn(v);
-  }
-};
+MOE_DEVINL float load_one(const ClipChunk &c, int i) {
+  return c.kind & 1 ? ld_f32(static_cast<const float *>(c.g) + i)
+                    : __uint_as_float(ld_u16(static_cast<const uint16_t *>(c.g) + i) << 16);
+}
 
-struct F32x8 {
-  using Elem = float;
-  float f[8];
-  MOE_DEVINL void load(const float *p) { ld_stream_f32x8(p, f); }
-  MOE_DEVINL void get(float *v) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = f[i];
-  }
-  MOE_DEVINL static float one(const float *p) { return ld_f32(p); }
-  MOE_DEVINL static void store(float *p, const float *v) { st_f32x8(p, v); }
-  MOE_DEVINL static void store_one(float *p, float v) { *p = v; }
-};
-
-// Squares are summed from pieces of 16 bytes, kPieces a lane at a time, copied to shared
-// memory kAhead times ahead (each lane reads what it copied: no barrier).
+// Gradients come in pieces of 16 bytes, kPieces a lane at a time, copied to shared memory
+// kAhead times ahead (each lane reads what it copied: no barrier).
 constexpr int kPieces = 8;
 constexpr int kAhead = 3;
-constexpr int kSquareSmem = kAhead * kPieces * 16 * kThreads;
+constexpr int kStage = kPieces * 16 * kThreads;
+constexpr int kRing = kAhead * kStage;
 
 // Values whose squares leave fp32's range are squared in 64 bits.  That is looked at for 32
 // or 64 values at a time, by their fp32 sum: one that is neither 0 nor in the range's
@@ -100,22 +80,27 @@ MOE_DEVINL void add_squares(const uint8_t *mine, double &acc) {
   }
 }
 
-// A warp's walk over its chunks, a step of kPieces * 32 pieces at a time.
+// A warp's walk over its chunks (from the plan's end back where REVERSE), a step of kPieces *
+// 32 pieces at a time.
+template <bool REVERSE>
 struct Steps {
   const ClipChunk *plan;
   int64_t at, chunks, stride;
   ClipChunk c, next;
   int i, n;  // the chunk's first piece that is not taken, its pieces
+  bool skip; // chunks in place are left as they are
+  MOE_DEVINL ClipChunk chunk(int64_t k) const { return load_chunk(plan + (REVERSE ? chunks - 1 - k : k)); }
   MOE_DEVINL void start() {
     i = 0;
     n = at < chunks && !(c.kind & 4) ? (c.kind & 1 ? c.n >> 2 : c.n >> 3) : 0;
+    if (skip && c.g == c.out) n = c.n = 0;
   }
   MOE_DEVINL void fetch_next() {
-    if (at + stride < chunks) next = load_chunk(plan + at + stride);
+    if (at + stride < chunks) next = chunk(at + stride);  // on its way while this one is worked on
   }
-  MOE_DEVINL Steps(const ClipChunk *p, int64_t first, int64_t count, int64_t by)
-      : plan(p), at(first), chunks(count), stride(by), c{}, next{} {
-    if (at < chunks) c = load_chunk(plan + at);
+  MOE_DEVINL Steps(const ClipChunk *p, int64_t first, int64_t count, int64_t by, bool skip_in_place = false)
+      : plan(p), at(first), chunks(count), stride(by), c{}, next{}, skip(skip_in_place) {
+    if (at < chunks) c = chunk(at);
     fetch_next();
     start();
   }
@@ -131,6 +116,25 @@ struct Steps {
     fetch_next();
     start();
   }
+  // the step's pieces into `to`
+  MOE_DEVINL void copy(uint8_t *to, int lane) {
+    if (!done()) {
+      const uint8_t *g = static_cast<const uint8_t *>(c.g);
+#pragma unroll
+      for (int u = 0; u < kPieces; ++u) {
+        const int j = i + 32 * u + lane;
+        // (a copy of no bytes fills its 16 with zeros)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(to + u * (16 * kThreads))),
+                     "l"(j < n ? g + 16ll * j : (const uint8_t *)plan), "r"(j < n ? 16 : 0)
+                     : "memory");
+      }
+      if (step()) advance();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // the first of the elements that fill no piece
+  MOE_DEVINL int rest() const { return c.kind & 4 ? 0 : n << (c.kind & 1 ? 2 : 3); }
 };
 
 // Sum over the block's threads, in thread 0's warp (64-bit additions being slow, by few).
@@ -150,48 +154,28 @@ __global__ void __launch_bounds__(kThreads, 2)
 grad_square_kernel(const ClipChunk *__restrict__ plan, int64_t chunks, double *__restrict__ part) {
   extern __shared__ __align__(16) uint8_t ring[];  // [kAhead][kPieces][threads][16]
   __shared__ double s[kThreads];
-  constexpr int kStage = kPieces * 16 * kThreads;
   const int lane = threadIdx.x & 31;
   uint8_t *mine = ring + threadIdx.x * 16;
   double acc = 0.0;
   grid_dependency_begin();
-  const int64_t first = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  Steps in(plan, first, chunks, (int64_t)gridDim.x * kWarps);  // what is copied
-  Steps out = in;                                              // what is summed
-  auto copy = [&](int stage) {
-    if (!in.done()) {
-      const uint8_t *g = static_cast<const uint8_t *>(in.c.g);
-      uint8_t *to = mine + stage * kStage;
+  Steps<false> in(plan, (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), chunks,
+                  (int64_t)gridDim.x * kWarps);  // what is copied
+  Steps<false> out = in;                         // what is summed
 #pragma unroll
-      for (int u = 0; u < kPieces; ++u) {
-        const int j = in.i + 32 * u + lane;
-        // (a copy of no bytes fills its 16 with zeros)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                         (uint32_t)__cvta_generic_to_shared(to + u * (16 * kThreads))),
-                     "l"(j < in.n ? g + 16ll * j : (const uint8_t *)plan), "r"(j < in.n ? 16 : 0)
-                     : "memory");
-      }
-      if (in.step()) in.advance();
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-#pragma unroll
-  for (int k = 0; k < kAhead; ++k) copy(k);
+  for (int k = 0; k < kAhead; ++k) in.copy(mine + k * kStage, lane);
   int stage = 0;
   while (!out.done()) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
     if (out.c.kind & 1) add_squares<true>(mine + stage * kStage, acc);
     else add_squares<false>(mine + stage * kStage, acc);
-    if (out.step()) {  // the elements that fill no piece
-      const bool f32 = out.c.kind & 1;
-      for (int i = out.c.kind & 4 ? lane : (out.n << (f32 ? 2 : 3)) + lane; i < out.c.n; i += 32) {
-        const double v = f32 ? F32x8::one(static_cast<const float *>(out.c.g) + i)
-                             : Bf16x8::one(static_cast<const uint16_t *>(out.c.g) + i);
+    if (out.step()) {
+      for (int i = out.rest() + lane; i < out.c.n; i += 32) {
+        const double v = load_one(out.c, i);
         acc += v * v;
       }
       out.advance();
     }
-    copy(stage);
+    in.copy(mine + stage * kStage, lane);
     if (++stage == kAhead) stage = 0;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -223,47 +207,41 @@ MOE_DEVINL float norm_of(double sum, float scale, float &factor, float max_norm)
   return (float)total;
 }
 
-template <typename V, typename O>
-MOE_DEVINL void chunk_scale(const ClipChunk &c, int lane, float f) {
-  constexpr int kU = 4;
-  const typename V::Elem *g = static_cast<const typename V::Elem *>(c.g);
-  typename O::Elem *out = static_cast<typename O::Elem *>(c.out);
-  int i = 0;
-  if (!(c.kind & 4)) {
-    for (; i + 8 <= c.n; i += 256 * kU) {
-      V raw[kU];
+// Piece j of a chunk, scaled, to its place.
+MOE_DEVINL void scale_piece(const ClipChunk &c, int j, const uint4 &w, float f) {
+  float v[8];
+  values(w, c.kind & 1, v);
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int j = i + 256 * u + 8 * lane;
-        if (j + 8 <= c.n) raw[u].load(g + j);
-      }
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int j = i + 256 * u + 8 * lane;
-        if (j + 8 > c.n) continue;
-        float v[8];
-        raw[u].get(v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= f;
-        O::store(out + j, v);
-      }
+  for (int e = 0; e < 8; ++e) v[e] *= f;  // (fp32: the last four are no values)
+  if (c.kind & 1) {
+    if (c.kind & 2) {
+      st_v4(static_cast<float *>(c.out) + 4 * j,
+            make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                       __float_as_uint(v[3])));
+    } else {
+      const uint4 q = f32_to_bf16x8(v);
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(c.out) + 4 * j) = make_uint2(q.x, q.y);
     }
-    i = c.n & ~7;
+  } else if (c.kind & 2) {
+    st_f32x8(static_cast<float *>(c.out) + 8 * j, v);
+  } else {
+    st_v4(static_cast<uint16_t *>(c.out) + 8 * j, f32_to_bf16x8(v));
   }
-  for (i += lane; i < c.n; i += 32) O::store_one(out + i, V::one(g + i) * f);
 }
 
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 2)
 grad_scale_kernel(const ClipChunk *__restrict__ plan, int64_t chunks, const double *__restrict__ part,
                   int parts, float scale, float max_norm, float *__restrict__ norm) {
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ double s[kThreads];
   __shared__ float s_f;
   const int lane = threadIdx.x & 31;
-  const int64_t step = (int64_t)gridDim.x * kWarps;
-  int64_t k = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  // the plan is older than the kernel before this one
-  ClipChunk c = {};
-  if (k < chunks) c = load_chunk(plan + (chunks - 1 - k));
+  uint8_t *mine = ring + threadIdx.x * 16;
+  const int64_t first = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), stride = (int64_t)gridDim.x * kWarps;
+  // the plan and the gradients are older than the kernel before this one
+  Steps<true> in(plan, first, chunks, stride), out = in;
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) in.copy(mine + k * kStage, lane);
   grid_dependency_begin();
   const double sum = total_of(part, parts, s);
   if (threadIdx.x == 0) {
@@ -272,20 +250,33 @@ grad_scale_kernel(const ClipChunk *__restrict__ plan, int64_t chunks, const doub
   }
   __syncthreads();
   const float f = s_f;
-  while (k < chunks) {
-    k += step;
-    ClipChunk next = {};
-    if (k < chunks) next = load_chunk(plan + (chunks - 1 - k));
-    if (f != 1.0f || c.g != c.out) {
-      switch (c.kind & 3) {
-        case 0: chunk_scale<Bf16x8, Bf16x8>(c, lane, f); break;
-        case 1: chunk_scale<F32x8, Bf16x8>(c, lane, f); break;
-        case 2: chunk_scale<Bf16x8, F32x8>(c, lane, f); break;
-        default: chunk_scale<F32x8, F32x8>(c, lane, f); break;
-      }
-    }
-    c = next;
+  if (f == 1.0f) {  // only what is not in place
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    in = out = Steps<true>(plan, first, chunks, stride, true);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) in.copy(mine + k * kStage, lane);
   }
+  int stage = 0;
+  while (!out.done()) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int j = out.i + 32 * u + lane;
+      if (j < out.n)
+        scale_piece(out.c, j, *reinterpret_cast<const uint4 *>(mine + stage * kStage + u * (16 * kThreads)), f);
+    }
+    if (out.step()) {
+      for (int i = out.rest() + lane; i < out.c.n; i += 32) {
+        const float v = load_one(out.c, i) * f;
+        if (out.c.kind & 2) static_cast<float *>(out.c.out)[i] = v;
+        else static_cast<bf16_t *>(out.c.out)[i] = __float2bfloat16_rn(v);
+      }
+      out.advance();
+    }
+    in.copy(mine + stage * kStage, lane);
+    if (++stage == kAhead) stage = 0;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -301,21 +292,21 @@ grad_norm_kernel(const double *__restrict__ part, int parts, float scale, float 
 
 cudaError_t launch_clip(const ClipChunk *plan, int64_t chunks, float scale, float max_norm, bool write,
                         float *norm, double *part, cudaStream_t st) {
-  auto grid = [&](int per_sm) {
-    const int64_t want = std::max<int64_t>(1, (chunks + kWarps - 1) / kWarps);
-    return (int)std::min<int64_t>({want, (int64_t)num_sms() * per_sm, (int64_t)kClipMaxBlocks});
-  };
   static PerDevice<cudaError_t> allowed;
   cudaError_t e = allowed.get(current_device(), [] {
-    return cudaFuncSetAttribute(grad_square_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSquareSmem);
+    const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    const cudaError_t a = cudaFuncSetAttribute(grad_square_kernel, at, kRing);
+    return a != cudaSuccess ? a : cudaFuncSetAttribute(grad_scale_kernel, at, kRing);
   });
   if (e != cudaSuccess) return e;
-  const int parts = grid(2);
-  e = launch_dependent(grad_square_kernel, parts, kThreads, kSquareSmem, st, plan, chunks, part);
+  // two blocks a SM, as their rings go
+  const int blocks = (int)std::min<int64_t>({std::max<int64_t>(1, (chunks + kWarps - 1) / kWarps),
+                                             2ll * num_sms(), (int64_t)kClipMaxBlocks});
+  e = launch_dependent(grad_square_kernel, blocks, kThreads, kRing, st, plan, chunks, part);
   if (e != cudaSuccess) return e;
-  if (!write) return launch_dependent(grad_norm_kernel, 1, kThreads, 0, st, part, parts, scale, norm);
-  return launch_dependent(grad_scale_kernel, grid(blocks_per_sm<grad_scale_kernel>(kThreads)), kThreads,
-                          0, st, plan, chunks, part, parts, scale, max_norm, norm);
+  if (!write) return launch_dependent(grad_norm_kernel, 1, kThreads, 0, st, part, blocks, scale, norm);
+  return launch_dependent(grad_scale_kernel, blocks, kThreads, kRing, st, plan, chunks, part, blocks, scale,
+                          max_norm, norm);
 }
 
 }  // namespace moe

@@ -420,8 +420,18 @@ dw_sum_kernel(const float *__restrict__ part, int parts, int cols, float *__rest
   grid_dependency_begin();
   const int c = blockIdx.x * 32 + threadIdx.x, k = threadIdx.y;
   float v = 0.0f;
-  if (c < cols)
-    for (int p = k; p < parts; p += kSumRows) v += ld_f32(part + (int64_t)p * cols + c);
+  if (c < cols) {
+    for (int p = k; p < parts; p += 8 * kSumRows) {
+      float x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int q = p + u * kSumRows;
+        x[u] = q < parts ? ld_f32(part + (int64_t)q * cols + c) : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v += x[u];
+    }
+  }
   s[k][threadIdx.x] = v;
   __syncthreads();
   // row k of the transposed sums: one warp a column

@@ -23,8 +23,8 @@
 
 #include <algorithm>
 
-#include "common.cuh"
 #include "internal.h"
+#include "lowbit.cuh"
 
 namespace moe {
 namespace {
@@ -85,18 +85,30 @@ struct Histogram {
       }
       return threadIdx.x == 0 ? hi - lo : 0;
     }
-    int n = 0;
-    for (int t = lo + threadIdx.x; t < hi; t += step) {
-      const bool live = ld_u8(a.mask + t) != 0;
-      n += live;
-      const int32_t *row = a.idx + (int64_t)t * a.k;
-      for (int j = 0; j < a.k; j += 8) {  // (on their way beside the mask)
-        int e[8];
+    // choice i is slot r of token t; both move on by additions
+    const int dt = step / a.k, dr = step - dt * a.k;
+    int t = lo + threadIdx.x / a.k, r = threadIdx.x % a.k, n = 0;
+    while (t < hi) {
+      int e[8];
+      bool live[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) e[u] = j + u < a.k ? ld_i32(row + j + u) : -1;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) add(live ? e[u] : -1);
+      for (int u = 0; u < 8; ++u) {
+        e[u] = -1;
+        live[u] = false;
+        if (t < hi) {
+          live[u] = ld_u8(a.mask + t) != 0;
+          e[u] = ld_i32(a.idx + (int64_t)t * a.k + r);
+          if (r == 0) n += live[u];
+        }
+        t += dt;
+        r += dr;
+        if (r >= a.k) {
+          r -= a.k;
+          ++t;
+        }
       }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) add(live[u] ? e[u] : -1);
     }
     return n;
   }
@@ -225,89 +237,108 @@ MOE_DEVINL float token_max(float v) {
   return v;
 }
 
-// A token's probabilities p, the factor J of its gradient, the softmax and lse, from its
-// logits x (8 a lane, -inf past the last expert).  Where no logit of the warp is over 30, or
-// under -30 but for -inf, e^x needs no shift and the sigmoid is e^x / (1 + e^x): one
-// exponential for both, no maximum over the experts.
+// e^x of pairs (x >= -200; under -87 it is 0): 2^t with t = x log2(e) rounded, times e^d for
+// what the rounding and log2(e)'s own left (d = ln2 (x log2(e) - t), |d| < 2^-16, 1 + d).
+MOE_DEVINL uint64_t exp2x(uint64_t x) {
+  const float kL = 1.44269502f, kRest = 1.92596303e-8f, kLn2 = 0.693147181f;
+  const uint64_t minus_t = mul2(x, pack2(-kL, -kL));
+  uint64_t d = fma2(x, pack2(kL, kL), minus_t);
+  d = mul2(fma2(x, pack2(kRest, kRest), d), pack2(kLn2, kLn2));
+  float t0, t1, e0, e1;
+  unpack2(minus_t, t0, t1);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(-t0));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(-t1));
+  const uint64_t e = pack2(e0, e1);
+  return fma2(e, d, e);
+}
+
+MOE_DEVINL float both(uint64_t v) {
+  float lo, hi;
+  unpack2(v, lo, hi);
+  return lo + hi;
+}
+
+// A token's numbers, 8 experts a lane: u = e^(x - shift), s the score before it is normalised
+// and j its derivative (softmax: u itself); their sums over the token's experts, and that of
+// f s.
+struct Token {
+  uint64_t u[4], s[4], j[4];
+  float sum, size, fs, shift;
+};
+
+// Of logits x (-inf: no expert, or a token that is not live).  No shift where the sum of e^x
+// stays well inside fp32's range: no maximum over the experts, and one exponential for the
+// softmax and the sigmoid e^x / (1 + e^x).
 template <int LPT, bool SIGMOID>
-MOE_DEVINL void token_probs(float *x, bool with_soft, float *p, float *jac, float *soft, float &lse) {
-  bool tame = true;
+MOE_DEVINL void token_scores(const float *x, const uint64_t *f, Token &k) {
+  uint64_t sum = 0, size = 0, fs = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) tame &= fabsf(x[i]) <= 30.0f || x[i] == -INFINITY;
-  lse = 0.0f;
-  if (__all_sync(0xffffffffu, tame)) {
-    float sum = 0.0f, size = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      soft[i] = expf(x[i]);
-      sum += soft[i];
-    }
+  for (int i = 0; i < 4; ++i) {
+    // (a NaN ranks below every number)
+    k.u[i] = exp2x(pack2(fmaxf(x[2 * i], -200.0f), fmaxf(x[2 * i + 1], -200.0f)));
+    sum = add2(sum, k.u[i]);
     if (SIGMOID) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float r = rcp_f(1.0f + soft[i]);
-        p[i] = soft[i] * r;
-        jac[i] = p[i] * r;
-        size += p[i];
-      }
+      float a, b;
+      unpack2(add2(k.u[i], pack2(1.0f, 1.0f)), a, b);
+      const uint64_t r = pack2(rcp_f(a), rcp_f(b));
+      k.s[i] = mul2(k.u[i], r);
+      k.j[i] = mul2(k.s[i], r);
+      size = add2(size, k.s[i]);
+    } else {
+      k.s[i] = k.j[i] = k.u[i];
     }
-    if (with_soft) {
-      sum = token_sum<LPT>(sum);
-      // (a token without a logit above -inf, or not live, has p = 0 and no z)
-      const float inv = sum > 0.0f ? rcp_f(sum) : 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) soft[i] *= inv;
-      if (sum > 0.0f) lse = logf(sum);
-    }
-    if (SIGMOID) {
-      size = token_sum<LPT>(size);
-      const float inv = size > 0.0f ? rcp_f(size) : 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        p[i] *= inv;
-        jac[i] *= inv;
-      }
-    }
-  } else {
-    float m = -INFINITY, sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (x[i] != x[i]) x[i] = -INFINITY;  // NaN ranks below every number
-      m = fmaxf(m, x[i]);
-    }
-    m = token_max<LPT>(m);
-    const bool some = m > -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      soft[i] = some ? expf(x[i] - m) : 0.0f;
-      sum += soft[i];
-    }
-    sum = token_sum<LPT>(sum);
-    const float inv = some ? rcp_f(sum) : 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) soft[i] *= inv;
-    if (some && with_soft) lse = m + logf(sum);
-    if (SIGMOID) {
-      float size = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        p[i] = 1.0f / (1.0f + expf(-x[i]));
-        jac[i] = p[i] * (1.0f - p[i]);
-        size += p[i];
-      }
-      size = token_sum<LPT>(size);
-      const float by = size > 0.0f ? 1.0f / size : 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        p[i] *= by;
-        jac[i] *= by;
-      }
-    }
+    fs = fma2(f[i], k.s[i], fs);
   }
-  if (!SIGMOID) {
+  k.sum = token_sum<LPT>(both(sum));
+  k.size = SIGMOID ? token_sum<LPT>(both(size)) : k.sum;
+  k.fs = token_sum<LPT>(both(fs));
+  k.shift = 0.0f;
+}
+
+// The same with the largest logit as the shift, for any logits.
+struct Any {
+  float x[8];
+  uint64_t f[4];
+  Token k;
+};
+
+template <int LPT, bool SIGMOID>
+__device__ __noinline__ void token_scores_any(Any &a) {
+  const float *x = a.x;
+  const uint64_t *f = a.f;
+  Token &k = a.k;
+  float v[8], s[8], j[8], m = -INFINITY, sum = 0.0f, size = 0.0f, fs = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = jac[i] = soft[i];
+  for (int i = 0; i < 8; ++i) {
+    v[i] = x[i] != x[i] ? -INFINITY : x[i];
+    m = fmaxf(m, v[i]);
   }
+  m = token_max<LPT>(m);
+  k.shift = m > -INFINITY ? m : 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float u = expf(v[i] - k.shift);
+    sum += u;
+    s[i] = j[i] = u;
+    if (SIGMOID) {
+      s[i] = 1.0f / (1.0f + expf(-v[i]));
+      j[i] = s[i] * (1.0f - s[i]);
+      size += s[i];
+    }
+    float f0, f1;
+    unpack2(f[i >> 1], f0, f1);
+    fs = fmaf(i & 1 ? f1 : f0, s[i], fs);
+    v[i] = u;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    k.u[i] = pack2(v[2 * i], v[2 * i + 1]);
+    k.s[i] = pack2(s[2 * i], s[2 * i + 1]);
+    k.j[i] = pack2(j[2 * i], j[2 * i + 1]);
+  }
+  k.sum = token_sum<LPT>(sum);
+  k.size = SIGMOID ? token_sum<LPT>(size) : k.sum;
+  k.fs = token_sum<LPT>(fs);
 }
 
 // A row's experts of a lane: columns 4 and 4 consecutive (VEC) or LPT apart.
@@ -361,7 +392,7 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, float *__restrict__ part, float2 *
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane / LPT;
   const Columns<LPT, VEC> col = {lane % LPT, a.E};
   const bool sums = a.probs != nullptr, grad = a.d_logits != nullptr;
-  const bool with_soft = !SIGMOID || a.z_coeff != 0.0f;
+  const bool with_z = a.z_coeff != 0.0f;
   // Logits, offsets and mask are older than the kernel before this one where that is one of
   // this call (it waited for them); the counts are not.
   if (!sums) grid_dependency_begin();
@@ -389,11 +420,17 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, float *__restrict__ part, float2 *
     const int n = b >= 0 && b < a.B ? ld_i32(a.tokens + b) : 0;
     const float by_n = n > 0 ? 1.0f / (float)n : 0.0f;
     const float g0 = per_seq * by_n, fs = (float)a.E / (float)a.k * by_n;
-    float f[8], acc[8];
+    uint64_t f[4], acc2[4];
+    {
+      float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      f[i] = n > 0 && col.at(i) < a.E ? fs * (float)ld_i32(a.counts + (int64_t)b * a.E + col.at(i)) : 0.0f;
-      acc[i] = 0.0f;
+      for (int i = 0; i < 8; ++i)
+        v[i] = n > 0 && col.at(i) < a.E ? fs * (float)ld_i32(a.counts + (int64_t)b * a.E + col.at(i)) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[i] = pack2(v[2 * i], v[2 * i + 1]);
+        acc2[i] = 0;
+      }
     }
     for (int u0 = t + warp * kTok; u0 < end; u0 += kWarps * kTok) {
       const int u = u0 + grp;
@@ -403,34 +440,54 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, float *__restrict__ part, float2 *
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = on ? x[i] : -INFINITY;
       if (u0 + kWarps * kTok < end) live = fetch(u + kWarps * kTok, end, x);
-      float p[8], soft[8], jac[8], lse;
-      token_probs<LPT, SIGMOID>(y, with_soft, p, jac, soft, lse);
-      float c = 0.0f;
+      Token k;
+      token_scores<LPT, SIGMOID>(y, f, k);
+      if (__any_sync(0xffffffffu, on && !(k.sum >= 1e-13f && k.sum <= 1e34f))) {
+        Any any;  // (a copy: what the call is given lies in memory)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) c = fmaf(f[i], p[i], c);
-      c = token_sum<LPT>(c);
+        for (int i = 0; i < 8; ++i) any.x[i] = y[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) any.f[i] = f[i];
+        token_scores_any<LPT, SIGMOID>(any);
+        k = any.k;
+      }
+      // (a token that is not live, or has no logit above -inf: p = 0 and no z)
+      const bool some = k.sum > 0.0f;
+      const float inv = k.size > 0.0f ? rcp_f(k.size) : 0.0f, c = k.fs * inv;
+      const float lse = with_z && some ? k.shift + logf(k.sum) : 0.0f;
       if (sums) {
+        const uint64_t inv2 = pack2(inv, inv);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += p[i];
+        for (int i = 0; i < 4; ++i) acc2[i] = fma2(k.s[i], inv2, acc2[i]);
         if (col.l == 0) {
           z = fmaf(lse, lse, z);
           bal = fmaf(c, by_n, bal);
         }
       }
       if (grad && valid && (on || !a.accumulate)) {
+        // d = k1 j (f - c) + k2 u
+        const float k1 = g0 * inv, k2 = some ? gz * lse * rcp_f(k.sum) : 0.0f;
+        const float k0 = SIGMOID ? -c * k1 : fmaf(-c, k1, k2);
+        const uint64_t k12 = pack2(k1, k1), k22 = pack2(k2, k2), k02 = pack2(k0, k0);
         float *out = a.d_logits + (int64_t)u * a.ld_d;
-        const float zl = gz * lse;
-        float g[8];
-        if (a.accumulate) col.load(out, g, 0.0f);
+        float g[8], old[8];
+        if (a.accumulate) col.load(out, old, 0.0f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float d = g0 * jac[i] * (f[i] - c);
-          if (with_soft) d = fmaf(zl, soft[i], d);
-          g[i] = a.accumulate ? g[i] + d : on ? d : 0.0f;
+        for (int i = 0; i < 4; ++i) {
+          uint64_t d = mul2(fma2(f[i], k12, k02), k.j[i]);
+          if (SIGMOID) d = fma2(k.u[i], k22, d);
+          unpack2(d, g[2 * i], g[2 * i + 1]);
+        }
+        if (a.accumulate) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) g[i] += old[i];
         }
         col.store(out, g);
       }
     }
+    float acc[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack2(acc2[i], acc[2 * i], acc[2 * i + 1]);
     if (sums && n > 0) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -592,10 +649,10 @@ cudaError_t launch_pass(const SeqAuxArgs &a, const Workspace &w, int *blocks, in
 
 cudaError_t launch_count(const SeqAuxArgs &a, cudaStream_t s) {
   const int64_t choices = (int64_t)a.T * a.k;
-  // A block a sequence (of more threads where there are few) where none can have many choices
-  // (2^16: 6 us); else chunks, whose counts meet in atomics
-  if (choices <= (1 << 16) || (choices <= (1 << 18) && choices / a.B <= 2048))
-    return launch_dependent(seq_count_kernel, (unsigned)a.B, choices / a.B <= 2048 ? 256 : kCountThreads, 0,
+  // A block a sequence (of more threads where they are long) where there are few choices, or not
+  // many and sequences are short; else chunks, whose counts meet in atomics
+  if (choices <= (1 << 13) || (choices <= (1 << 17) && choices / a.B <= 2048))
+    return launch_dependent(seq_count_kernel, (unsigned)a.B, choices / a.B <= 1024 ? 256 : kCountThreads, 0,
                             s, a);
   const int64_t cells = (int64_t)a.B * (a.E + 1);
   const unsigned zero = (unsigned)std::min<int64_t>((cells + kThreads - 1) / kThreads, num_sms());
