@@ -296,17 +296,8 @@ MOE_DEVINL void token_scores(const float *x, const uint64_t *f, Token &k) {
 }
 
 // The same with the largest logit as the shift, for any logits.
-struct Any {
-  float x[8];
-  uint64_t f[4];
-  Token k;
-};
-
 template <int LPT, bool SIGMOID>
-__device__ __noinline__ void token_scores_any(Any &a) {
-  const float *x = a.x;
-  const uint64_t *f = a.f;
-  Token &k = a.k;
+MOE_DEVINL void token_scores_any(const float *x, const uint64_t *f, Token &k) {
   float v[8], s[8], j[8], m = -INFINITY, sum = 0.0f, size = 0.0f, fs = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -380,11 +371,52 @@ struct Columns {
   }
 };
 
+// The loss of S sequences and N tokens.
+MOE_DEVINL void write_loss(const SeqAuxArgs &a, float bal, float z, int S, int N) {
+  a.loss[0] = a.coeff * bal / (float)max(S, 1);
+  // (without a z loss the squares may have passed fp32's range)
+  a.loss[1] = a.z_coeff != 0.0f ? a.z_coeff * z / (float)max(N, 1) : 0.0f;
+}
+
+// A small batch's counts and tokens, and zeros for P of sequences without live tokens, by one
+// block; cell: kSmallCells words of its shared memory.
+constexpr int kSmallCells = kWarps * kMaxE;
+MOE_DEVINL void count_small(const SeqAuxArgs &a, int *cell) {
+  const int cells = a.B * (a.E + 1);  // counts, then tokens
+  int *tokens = cell + a.B * a.E;
+  for (int i = threadIdx.x; i < cells; i += kThreads) cell[i] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.T * a.k; i += kThreads) {
+    const int t = i / a.k, e = ld_i32(a.idx + i);
+    if (a.mask != nullptr && ld_u8(a.mask + t) == 0) continue;
+    int b = -1, hi = a.B + 1;  // the last offset at or before t
+    while (hi - b > 1) {
+      const int mid = (b + hi) >> 1;
+      if (ld_i32(a.offsets + mid) <= t) b = mid;
+      else hi = mid;
+    }
+    if (b < 0 || b >= a.B) continue;
+    if ((uint32_t)e < (uint32_t)a.E) atomicAdd(&cell[b * a.E + e], 1);
+    if (i == t * a.k) atomicAdd(&tokens[b], 1);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < cells; i += kThreads) {
+    if (i >= a.B * a.E) {
+      a.tokens[i - a.B * a.E] = cell[i];
+    } else {
+      a.counts[i] = cell[i];
+      if (tokens[i / a.E] == 0) a.probs[i] = 0.0f;
+    }
+  }
+  __syncthreads();
+}
+
 // One pass over the logits: a token is LPT lanes of 8 experts each, a block takes `chunk`
 // consecutive tokens, the next token's logits on their way while one is computed.
 template <int LPT, bool VEC, bool SIGMOID>
 __global__ void __launch_bounds__(kThreads, 3)
-seq_aux_kernel(const SeqAuxArgs a, int chunk, float *__restrict__ part, float2 *__restrict__ terms) {
+seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ part,
+               float2 *__restrict__ terms) {
   constexpr int kTok = 32 / LPT;  // tokens of a warp at a time
   __shared__ float s_p[kWarps][kMaxE];
   __shared__ float s_t[2][kWarps];
@@ -395,7 +427,8 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, float *__restrict__ part, float2 *
   const bool with_z = a.z_coeff != 0.0f;
   // Logits, offsets and mask are older than the kernel before this one where that is one of
   // this call (it waited for them); the counts are not.
-  if (!sums) grid_dependency_begin();
+  if (!sums || single) grid_dependency_begin();
+  if (single) count_small(a, reinterpret_cast<int *>(s_p));
   const int t0 = blockIdx.x * chunk, t1 = min(a.T, t0 + chunk);
   // token u of the walk below, or one that is not live
   auto fetch = [&](int u, int end, float *x) -> bool {
@@ -406,51 +439,34 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, float *__restrict__ part, float2 *
   float x[8];
   bool live = fetch(t0 + warp * kTok + grp, t1, x);
   int b = last_at_most(a.offsets, a.B + 1, t0, lane);
-  if (sums) grid_dependency_begin();
+  if (sums && !single) grid_dependency_begin();
   float per_seq = 0.0f, gz = 0.0f;
-  if (grad) {
-    const int2 sn = batch_size(a.tokens, a.B, s_n);
+  int2 sn = make_int2(0, 0);
+  if (grad || single) {
+    sn = batch_size(a.tokens, a.B, s_n);
     per_seq = a.d_loss * a.coeff / (float)max(sn.x, 1);
     gz = a.d_loss * 2.0f * a.z_coeff / (float)max(sn.y, 1);
   }
   float z = 0.0f, bal = 0.0f;
   for (int t = t0; t < t1;) {
+    const bool of_one = b >= 0 && b < a.B;
     const int next = b < a.B ? ld_i32(a.offsets + b + 1) : a.T;
+    const int n = of_one ? ld_i32(a.tokens + b) : 0;
+    uint64_t f[4], acc2[4];
+    int count[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      count[i] = of_one && col.at(i) < a.E ? ld_i32(a.counts + (int64_t)b * a.E + col.at(i)) : 0;
     const int end = min(t1, max(next, t + 1));
-    const int n = b >= 0 && b < a.B ? ld_i32(a.tokens + b) : 0;
     const float by_n = n > 0 ? 1.0f / (float)n : 0.0f;
     const float g0 = per_seq * by_n, fs = (float)a.E / (float)a.k * by_n;
-    uint64_t f[4], acc2[4];
-    {
-      float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] = n > 0 && col.at(i) < a.E ? fs * (float)ld_i32(a.counts + (int64_t)b * a.E + col.at(i)) : 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[i] = pack2(v[2 * i], v[2 * i + 1]);
-        acc2[i] = 0;
-      }
+    for (int i = 0; i < 4; ++i) {
+      f[i] = pack2(fs * (float)count[2 * i], fs * (float)count[2 * i + 1]);
+      acc2[i] = 0;
     }
-    for (int u0 = t + warp * kTok; u0 < end; u0 += kWarps * kTok) {
-      const int u = u0 + grp;
-      if (t != t0 && u0 == t + warp * kTok) live = fetch(u, end, x);  // a sequence's first
-      float y[8];
-      const bool valid = u < end, on = live && valid && n > 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = on ? x[i] : -INFINITY;
-      if (u0 + kWarps * kTok < end) live = fetch(u + kWarps * kTok, end, x);
-      Token k;
-      token_scores<LPT, SIGMOID>(y, f, k);
-      if (__any_sync(0xffffffffu, on && !(k.sum >= 1e-13f && k.sum <= 1e34f))) {
-        Any any;  // (a copy: what the call is given lies in memory)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) any.x[i] = y[i];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) any.f[i] = f[i];
-        token_scores_any<LPT, SIGMOID>(any);
-        k = any.k;
-      }
+    // what a token adds to the sums, and its gradient
+    auto finish = [&](const Token &k, int u, bool valid, bool on) {
       // (a token that is not live, or has no logit above -inf: p = 0 and no z)
       const bool some = k.sum > 0.0f;
       const float inv = k.size > 0.0f ? rcp_f(k.size) : 0.0f, c = k.fs * inv;
@@ -470,8 +486,7 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, float *__restrict__ part, float2 *
         const float k0 = SIGMOID ? -c * k1 : fmaf(-c, k1, k2);
         const uint64_t k12 = pack2(k1, k1), k22 = pack2(k2, k2), k02 = pack2(k0, k0);
         float *out = a.d_logits + (int64_t)u * a.ld_d;
-        float g[8], old[8];
-        if (a.accumulate) col.load(out, old, 0.0f);
+        float g[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint64_t d = mul2(fma2(f[i], k12, k02), k.j[i]);
@@ -479,11 +494,36 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, float *__restrict__ part, float2 *
           unpack2(d, g[2 * i], g[2 * i + 1]);
         }
         if (a.accumulate) {
+          float old[8];
+          col.load(out, old, 0.0f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) g[i] += old[i];
         }
         col.store(out, g);
       }
+    };
+    int u0 = t + warp * kTok;
+    if (t != t0) live = fetch(u0 + grp, end, x);
+    for (; u0 < end; u0 += kWarps * kTok) {
+      const int u = u0 + grp;
+      const bool valid = u < end, on = live && valid && n > 0;
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = on ? x[i] : -INFINITY;
+      Token k;
+      token_scores<LPT, SIGMOID>(y, f, k);
+      if (__any_sync(0xffffffffu, on && !(k.sum >= 1e-13f && k.sum <= 1e34f))) break;
+      if (u0 + kWarps * kTok < end) live = fetch(u + kWarps * kTok, end, x);
+      finish(k, u, valid, on);
+    }
+    for (; u0 < end; u0 += kWarps * kTok) {  // from a token with such logits on
+      const int u = u0 + grp;
+      const bool valid = u < end, on = fetch(u, end, x) && valid && n > 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = on ? x[i] : -INFINITY;
+      Token k;
+      token_scores_any<LPT, SIGMOID>(x, f, k);
+      finish(k, u, valid, on);
     }
     float acc[8];
 #pragma unroll
@@ -500,12 +540,17 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, float *__restrict__ part, float2 *
         float v = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) v += s_p[w][e];
-        part[((int64_t)blockIdx.x + b) * a.E + e] = v;
+        if (single) a.probs[(int64_t)b * a.E + e] = v * by_n;
+        else part[((int64_t)blockIdx.x + b) * a.E + e] = v;
       }
       __syncthreads();
     }
     t = end;
-    if (t < t1) b = last_at_most(a.offsets, a.B + 1, t, lane);
+    if (t < t1) {  // most often the next sequence
+      ++b;
+      if (b >= a.B || ld_i32(a.offsets + b) > t || ld_i32(a.offsets + b + 1) <= t)
+        b = last_at_most(a.offsets, a.B + 1, t, lane);
+    }
   }
   if (!sums) return;
   z = warp_sum(z);
@@ -521,7 +566,8 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, float *__restrict__ part, float2 *
       bal += s_t[0][w];
       z += s_t[1][w];
     }
-    terms[blockIdx.x] = make_float2(bal, z);
+    if (single) write_loss(a, bal, z, sn.x, sn.y);
+    else terms[blockIdx.x] = make_float2(bal, z);
   }
 }
 
@@ -570,9 +616,7 @@ seq_aux_finish_kernel(const SeqAuxArgs a, int chunk, int blocks, const float *__
         S += s_n[0][w];
         N += s_n[1][w];
       }
-      a.loss[0] = a.coeff * bal / (float)max(S, 1);
-      // (without a z loss the squares may have passed fp32's range)
-      a.loss[1] = a.z_coeff != 0.0f ? a.z_coeff * z / (float)max(N, 1) : 0.0f;
+      write_loss(a, bal, z, S, N);
     }
     return;
   }
@@ -625,13 +669,25 @@ struct Workspace {
   }
 };
 
+// Whether one block takes the whole call (one launch and not three or four: a batch of 256 tokens
+// and 8 experts 3.5 us, was 6.8): few logits, whose counts fit its shared memory.
+bool small(const SeqAuxArgs &a) {
+  return a.loss != nullptr && a.T > 0 && (int64_t)a.T * a.E <= 8192 && a.T * a.k <= 4096 &&
+         (int64_t)a.B * (a.E + 1) <= kSmallCells;
+}
+
 // The pass over the logits; its blocks and their tokens are left for the finish.
 template <int LPT, bool VEC, bool SIGMOID>
 cudaError_t launch_pass(const SeqAuxArgs &a, const Workspace &w, int *blocks, int *chunk, cudaStream_t s) {
+  const bool single = small(a);
   split(a.T, a.E, [] { return blocks_per_sm<seq_aux_kernel<LPT, VEC, SIGMOID>>(kThreads); }, blocks, chunk);
+  if (single) {
+    *blocks = 1;
+    *chunk = a.T;
+  }
   if (*blocks == 0) return cudaSuccess;
-  return launch_dependent(seq_aux_kernel<LPT, VEC, SIGMOID>, *blocks, kThreads, 0, s, a, *chunk, w.part,
-                          w.terms);
+  return launch_dependent(seq_aux_kernel<LPT, VEC, SIGMOID>, *blocks, kThreads, 0, s, a, *chunk, single,
+                          w.part, w.terms);
 }
 
 template <int LPT>
@@ -672,7 +728,7 @@ size_t seq_aux_workspace_bytes(int T, int E, int B) { return Workspace(nullptr, 
 cudaError_t launch_seq_aux(const SeqAuxArgs &a, void *ws, cudaStream_t s) {
   const Workspace w(ws, a.T, a.E, a.B);
   cudaError_t e = cudaSuccess;
-  if (a.loss != nullptr) e = launch_count(a, s);
+  if (a.loss != nullptr && !small(a)) e = launch_count(a, s);
   if (e != cudaSuccess) return e;
   int blocks = 0, chunk = 1;
   switch (lanes_per_token(a.E)) {
@@ -683,7 +739,7 @@ cudaError_t launch_seq_aux(const SeqAuxArgs &a, void *ws, cudaStream_t s) {
     case 16: e = launch_pass<16>(a, w, &blocks, &chunk, s); break;
     default: e = launch_pass<32>(a, w, &blocks, &chunk, s); break;
   }
-  if (e != cudaSuccess || a.loss == nullptr) return e;
+  if (e != cudaSuccess || a.loss == nullptr || small(a)) return e;
   return launch_dependent(seq_aux_finish_kernel, dim3((unsigned)a.B + 1, (unsigned)((a.E + 31) / 32)),
                           kFinishThreads, 0, s, a, chunk, blocks, w.part, w.terms);
 }
