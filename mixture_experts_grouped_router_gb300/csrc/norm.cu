@@ -47,6 +47,9 @@ MOE_DEVINL uint4 to_bf16(const Pairs &v) {
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
+// Makes w a new value to the compiler, so that what it was unpacked to before is not kept.
+MOE_DEVINL void afresh(uint4 &w) { asm volatile("" : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w)); }
+
 MOE_DEVINL Pairs from_f32(const uint4 &a, const uint4 &b) {
   const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   Pairs r;
@@ -64,15 +67,18 @@ MOE_DEVINL float both(uint64_t v) {
 }
 
 // Streamed loads and stores of 8 elements of the residual stream.  fp32: one access of 32 bytes
-// where rows are aligned to that (FULL).
-template <typename S, bool FULL>
+// where rows are aligned to that (WIDE; halves of 16 bytes cost up to a quarter of the
+// bandwidth: 2712 columns 5.7 and 6.4 TB/s).
+template <typename S, bool WIDE>
 struct Vec8;
 
-template <bool FULL>
-struct Vec8<uint16_t, FULL> {
+template <bool WIDE>
+struct Vec8<uint16_t, WIDE> {
   uint4 a;
   MOE_DEVINL void zero() { a = make_uint4(0, 0, 0, 0); }
   MOE_DEVINL void load(const uint16_t *p) { a = ld_stream_v4(p); }
+  MOE_DEVINL void take(const uint4 *p) { a = p[0]; }
+  MOE_DEVINL void again() { afresh(a); }
   // + x, rounded once
   MOE_DEVINL void add(const uint4 &x) {
     __nv_bfloat162 *v = reinterpret_cast<__nv_bfloat162 *>(&a);
@@ -85,12 +91,12 @@ struct Vec8<uint16_t, FULL> {
   MOE_DEVINL void store(uint16_t *p) const { st_v4(p, a); }
 };
 
-template <bool FULL>
-struct Vec8<float, FULL> {
+template <bool WIDE>
+struct Vec8<float, WIDE> {
   Pairs v;
   MOE_DEVINL void zero() { v.zero(); }
   MOE_DEVINL void load(const float *p) {
-    if (FULL) {
+    if (WIDE) {
       float f[8];
       ld_stream_f32x8(p, f);
 #pragma unroll
@@ -99,6 +105,8 @@ struct Vec8<float, FULL> {
       v = from_f32(ld_stream_v4(p), ld_stream_v4(p + 4));
     }
   }
+  MOE_DEVINL void take(const uint4 *p) { v = from_f32(p[0], p[1]); }
+  MOE_DEVINL void again() {}
   MOE_DEVINL void add(const uint4 &x) {
     const Pairs u = from_bf16(x);
 #pragma unroll
@@ -110,7 +118,7 @@ struct Vec8<float, FULL> {
     float f[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) unpack2(v.p[i], f[2 * i], f[2 * i + 1]);
-    if (FULL) {
+    if (WIDE) {
       st_f32x8(p, f);
     } else {
       st_v4(p, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
@@ -161,12 +169,16 @@ struct Team {
   }
 };
 
-// FULL: the team's lanes have cols columns exactly, and fp32 rows start on 32 bytes.  What
-// bounds it: HBM for bf16 output (16384 x 4096: 79 us, 6800 GB/s); with codes the issue of
+// How the operands fit a kernel: fp32 rows start on 32 bytes, and the team's lanes have the
+// columns exactly.
+enum { kAny = 0, kWide = 1, kFull = 2 };
+
+// What bounds it: HBM for bf16 output (16384 x 4096: 79 us, 6800 GB/s); with codes the issue of
 // instructions came first (290 for 8 values a lane before the arithmetic in pairs, 80 us).
-template <int VPL, typename S, int CODES, bool FULL>
+template <int VPL, typename S, int CODES, int FIT>
 __global__ void __launch_bounds__(VPL > 2 ? 512 : 1024)
 rms_norm_kernel(const RmsNormArgs a, int W, int teams) {
+  constexpr bool FULL = FIT == kFull;
   __shared__ float red[32];
   const Team t(W);
   grid_dependency_begin();
@@ -177,7 +189,7 @@ rms_norm_kernel(const RmsNormArgs a, int W, int teams) {
   const S *res = static_cast<const S *>(a.residual) + row * a.ld_res + c0;
   const uint16_t *x = a.x + row * a.ldx + c0;
   uint4 xv[VPL];
-  Vec8<S, FULL> hv[VPL];
+  Vec8<S, FIT != kAny> hv[VPL];
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
     xv[v] = make_uint4(0, 0, 0, 0);
@@ -253,20 +265,28 @@ MOE_DEVINL void copy_async(void *dst, const void *src) {
 // registers; at the end the block's teams are added up in order and the block's row of
 // `part` is written.  part == NULL: no gradient of w is wanted.
 //
-// Rows come in by asynchronous copies, `stages` rows ahead of the arithmetic: a warp copies
-// what its own lanes will read (h, dy, d_residual), so that a warp's barrier is enough and
-// loads stay under way while a row's sums are taken (16384 x 4096 bf16: 82 us, 6550 GB/s;
-// without: 106 us).  kThreads: the most that a block has; w stays in registers where that is
-// 512.
-template <int VPL, typename S, int kThreads>
-__global__ void __launch_bounds__(kThreads)
+// Rows come in by asynchronous copies, `stages` of them a team: a warp copies what its own
+// lanes will read (h, dy, d_residual), so that a warp's barrier is enough and loads stay
+// under way while a row's sums are taken (16384 x 4096 bf16: 79 us, 6800 GB/s; without: 106
+// us).  The row at hand is held in registers, as it came, so that its place is free for the
+// next one before the sums (read twice from shared memory: 99 us).  DIRECT (wide fp32 rows,
+// of which two would not fit): d_residual is loaded past shared memory.
+// Threads of a SM, as their registers go: 128 a thread, fewer where the row at hand is unpacked
+// a second time (TIGHT) instead of kept in fp32.
+constexpr int bwd_threads(int vpl, int elem, bool tight) {
+  return !tight || vpl == 4 ? 512 : elem == 4 || vpl == 2 ? 768 : 1024;
+}
+
+template <int VPL, typename S, bool DIRECT, bool TIGHT>
+__global__ void __launch_bounds__(bwd_threads(VPL, sizeof(S), TIGHT))
 rms_norm_bwd_kernel(const RmsNormBwdArgs a, int W, int teams, int stages, float *__restrict__ part) {
   constexpr int kWide = sizeof(S) / 2;             // copies of a warp for 8 elements a lane
-  constexpr int kCopies = VPL * (2 * kWide + 1);   // of a warp and row, 512 bytes each
+  constexpr int kDy = (DIRECT ? 1 : 2) * VPL * kWide;
+  constexpr int kCopies = kDy + VPL;               // of a warp and row, 512 bytes each
   __shared__ float red[2][2][32];
   extern __shared__ __align__(16) uint8_t smem[];  // [stages][warps][kCopies][512]
   const Team t(W);
-  constexpr bool kKeepW = kThreads <= 512;
+  constexpr bool kKeepW = VPL <= 2;
   const int c0 = t.warp * (256 * VPL) + t.lane * 8;
   auto in = [&](int v) { return c0 + 256 * v < a.cols; };
   Pairs dw[VPL], kept[kKeepW ? VPL : 1];
@@ -289,20 +309,15 @@ rms_norm_bwd_kernel(const RmsNormBwdArgs a, int W, int teams, int stages, float 
           const int c = w0 + 256 * v + (256 / kWide) * k + t.lane * (8 / kWide);
           if (c < a.cols) {
             copy_async(to + (v * kWide + k) * 512, h + ahead * a.ldh + c);
-            if (res != nullptr)
+            if (!DIRECT && res != nullptr)
               copy_async(to + ((VPL + v) * kWide + k) * 512, res + ahead * a.ld_dres + c);
           }
         }
-        if (in(v)) copy_async(to + (2 * VPL * kWide + v) * 512, a.dy + ahead * a.ld_dy + c0 + 256 * v);
+        if (in(v)) copy_async(to + (kDy + v) * 512, a.dy + ahead * a.ld_dy + c0 + 256 * v);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     ahead += step;
-  };
-  // the lane's 8 elements of the stream's operand number n
-  auto take = [&](int s, int n) {
-    const uint4 *p = reinterpret_cast<const uint4 *>(mine + s * stage + n * (kWide * 512)) + t.lane * kWide;
-    return kWide == 1 ? from_bf16(p[0]) : from_f32(p[0], p[kWide - 1]);
   };
   grid_dependency_begin();
   for (int s = 0; s < stages; ++s) fetch(s);
@@ -314,38 +329,47 @@ rms_norm_bwd_kernel(const RmsNormBwdArgs a, int W, int teams, int stages, float 
       if (in(v)) kept[v] = load_w(a.w, a.w_dtype, c0 + 256 * v);
     }
   }
+  // (past the last column h and dy are 0, and any weight will do)
+  auto weight = [&](int v) { return kKeepW ? kept[v] : load_w(a.w, a.w_dtype, min(c0 + 256 * v, a.cols - 8)); };
   int turn = 0, s = 0;
   for (; row < a.rows; row += step, turn ^= 1) {
+    Vec8<S, false> hv[VPL], rv[VPL];
+    uint4 dy[VPL];
+    if (DIRECT) {
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) {
+        rv[v].zero();
+        if (res != nullptr && in(v)) rv[v].load(res + row * a.ld_dres + c0 + 256 * v);
+      }
+    }
     // all but the rows ahead have landed
     if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
     else if (stages == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
     else asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncwarp();
-    Pairs hv[VPL], gv[VPL], rv[VPL];
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       hv[v].zero();
-      gv[v].zero();
-      rv[v].zero();
+      if (!DIRECT) rv[v].zero();
+      dy[v] = make_uint4(0, 0, 0, 0);
       if (in(v)) {
-        hv[v] = take(s, v);
-        if (res != nullptr) rv[v] = take(s, VPL + v);
-        gv[v] = from_bf16(reinterpret_cast<const uint4 *>(mine + s * stage + (2 * VPL * kWide + v) * 512)[t.lane]);
+        const uint4 *at = reinterpret_cast<const uint4 *>(mine + s * stage);
+        hv[v].take(at + v * (kWide * 32) + t.lane * kWide);
+        if (!DIRECT && res != nullptr) rv[v].take(at + (VPL + v) * (kWide * 32) + t.lane * kWide);
+        dy[v] = at[(kDy + v) * 32 + t.lane];
       }
     }
     __syncwarp();
-    fetch(s);  // (what was there is in registers)
+    fetch(s);  // (every lane has what was there)
     if (++s == stages) s = 0;
     uint64_t ss2 = 0, gh2 = 0;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-      Pairs w;
-      if (!kKeepW && in(v)) w = load_w(a.w, a.w_dtype, c0 + 256 * v);
-      else if (!kKeepW) w.zero();
+      const Pairs f = hv[v].get(), g = from_bf16(dy[v]), w = weight(v);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        ss2 = fma2(hv[v].p[i], hv[v].p[i], ss2);
-        gh2 = fma2(mul2(gv[v].p[i], kKeepW ? kept[v].p[i] : w.p[i]), hv[v].p[i], gh2);
+        ss2 = fma2(f.p[i], f.p[i], ss2);
+        gh2 = fma2(mul2(g.p[i], w.p[i]), f.p[i], gh2);
       }
     }
     float ss = warp_sum(both(ss2)), gh = warp_sum(both(gh2));
@@ -364,20 +388,22 @@ rms_norm_bwd_kernel(const RmsNormBwdArgs a, int W, int teams, int stages, float 
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       const int c = c0 + 256 * v;
-      Pairs w;
-      if (!kKeepW && in(v)) w = load_w(a.w, a.w_dtype, c);
-      else if (!kKeepW) w.zero();
+      if (TIGHT) {
+        hv[v].again();
+        afresh(dy[v]);
+      }
+      const Pairs f = hv[v].get(), g = from_bf16(dy[v]), w = weight(v);
+      Pairs d = rv[v].get();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        dw[v].p[i] = fma2(gv[v].p[i], mul2(hv[v].p[i], r2), dw[v].p[i]);
-        const uint64_t g = mul2(mul2(gv[v].p[i], kKeepW ? kept[v].p[i] : w.p[i]), r2);
-        rv[v].p[i] = add2(fma2(s2, hv[v].p[i], g), rv[v].p[i]);
+        dw[v].p[i] = fma2(g.p[i], mul2(f.p[i], r2), dw[v].p[i]);
+        d.p[i] = add2(fma2(s2, f.p[i], mul2(mul2(g.p[i], w.p[i]), r2)), d.p[i]);
       }
       if (in(v)) {
         Vec8<S, false> o;
-        o.set(rv[v]);
+        o.set(d);
         o.store(dh + row * a.ld_dh + c);
-        if (a.dx != nullptr) st_v4(a.dx + row * a.ld_dx + c, to_bf16(rv[v]));
+        if (a.dx != nullptr) st_v4(a.dx + row * a.ld_dx + c, to_bf16(d));
       }
     }
   }
@@ -443,66 +469,77 @@ dw_sum_kernel(const float *__restrict__ part, int parts, int cols, float *__rest
 // Warps of a row's team with `vpl` vectors of 8 a lane.
 int team_warps(int cols, int vpl) { return (cols + 256 * vpl - 1) / (256 * vpl); }
 
-template <int VPL, typename S, bool FULL>
+template <int VPL, typename S, int FIT>
 cudaError_t norm_launch(const RmsNormArgs &a, int W, cudaStream_t st) {
   const int teams = std::max(1, 8 / W);
   const unsigned grid = (unsigned)((a.rows + teams - 1) / teams);
   const dim3 block(32 * W * teams);
   switch (a.codes) {
     case MOE_CODES_MX:
-      return launch_dependent(rms_norm_kernel<VPL, S, MOE_CODES_MX, FULL>, grid, block, 0, st, a, W, teams);
+      return launch_dependent(rms_norm_kernel<VPL, S, MOE_CODES_MX, FIT>, grid, block, 0, st, a, W, teams);
     case MOE_CODES_ACT8:
-      return launch_dependent(rms_norm_kernel<VPL, S, MOE_CODES_ACT8, FULL>, grid, block, 0, st, a, W, teams);
+      return launch_dependent(rms_norm_kernel<VPL, S, MOE_CODES_ACT8, FIT>, grid, block, 0, st, a, W, teams);
     default:
-      return launch_dependent(rms_norm_kernel<VPL, S, MOE_CODES_NONE, FULL>, grid, block, 0, st, a, W, teams);
+      return launch_dependent(rms_norm_kernel<VPL, S, MOE_CODES_NONE, FIT>, grid, block, 0, st, a, W, teams);
   }
 }
 
-// Rows of the stream that 8 elements at a time start on their own size.
-bool whole8(const void *p, int64_t ld, int elem) {
-  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % (8 * elem) == 0 && ld % 8 == 0);
+// Rows of which 8 elements at a time start on their own size.
+template <typename S>
+bool whole8(const void *p, int64_t ld) {
+  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % (8 * sizeof(S)) == 0 && ld % 8 == 0);
 }
 
 template <int VPL, typename S>
 cudaError_t norm_launch(const RmsNormArgs &a, cudaStream_t st) {
-  const int W = team_warps(a.cols, VPL), elem = (int)sizeof(S);
-  const bool full = W * VPL * 256 == a.cols && whole8(a.residual, a.ld_res, elem) && whole8(a.h, a.ldh, elem);
-  return full ? norm_launch<VPL, S, true>(a, W, st) : norm_launch<VPL, S, false>(a, W, st);
+  const int W = team_warps(a.cols, VPL);
+  const bool wide = whole8<S>(a.residual, a.ld_res) && whole8<S>(a.h, a.ldh);
+  if (wide && W * VPL * 256 == a.cols) return norm_launch<VPL, S, kFull>(a, W, st);
+  if (wide && sizeof(S) == 4) return norm_launch<VPL, S, kWide>(a, W, st);
+  return norm_launch<VPL, S, kAny>(a, W, st);
 }
 
+// Vectors a lane.  Few rows: one, for the latency.  Else four (4096 columns: 79 us, one or two 82)
+// but where a row has not so many (256: one 73 us, four 96; 512: two 80, four 83).
 template <typename S>
 cudaError_t norm_by_size(const RmsNormArgs &a, cudaStream_t st) {
-  // few rows: more warps a row, for the latency
   const bool few = a.rows < 2 * num_sms();
-  if (few && a.cols <= 8192) return norm_launch<1, S>(a, st);
-  if (few) return norm_launch<2, S>(a, st);
+  if (few ? a.cols <= 8192 : a.cols <= 256) return norm_launch<1, S>(a, st);
+  if (few || a.cols <= 512) return norm_launch<2, S>(a, st);
   return norm_launch<4, S>(a, st);
 }
 
-constexpr int kBwdVpl = 2;  // 16384 columns in 32 warps
-
-// How the backward is laid out over a SM: blocks, rows ahead, bytes of a block.
+// How the backward is laid out: a lane's vectors, a block's teams, blocks of a SM, rows ahead.
+// One vector where a row has no more (bf16 256 columns: 69 us, with two 83; fp32 128: 61 and 89,
+// but 256: 119 and 109), four past 8192 columns.  TIGHT with two vectors: blocks of which one
+// leaves a good part of the SM without threads and two fit so (5000 columns: 96 us, else 116;
+// 4096: 91 and 85).
 struct BwdShape {
-  int W, teams, threads, per_sm, stages;
+  int vpl, W, teams, threads, per_sm, stages;
+  bool direct, tight;
   size_t smem;
   BwdShape(int cols, int elem) {
-    W = team_warps(cols, kBwdVpl);
+    vpl = cols <= 512 / elem ? 1 : cols <= 8192 ? 2 : 4;
+    W = team_warps(cols, vpl);
     teams = std::max(1, 8 / W);
     threads = 32 * W * teams;
-    per_sm = std::max(1, kBwdResident / threads);
-    const size_t stage = (size_t)threads * 16 * kBwdVpl * (elem + 1);
-    const size_t each = kBwdSmem / per_sm;
-    stages = (int)std::min<size_t>(3, each / stage);
+    direct = vpl == 4 && elem == 4;
+    tight = vpl != 2 || (elem == 2 && threads > 256 && threads <= 384);
+    const size_t stage = (size_t)threads * 8 * vpl * (2 + elem * (direct ? 1 : 2));
+    // as many blocks as leave each two rows
+    per_sm = std::max(1, bwd_threads(vpl, elem, tight) / threads);
+    while (per_sm > 1 && kBwdSmem / per_sm < 2 * stage) --per_sm;
+    stages = (int)std::min<size_t>(3, kBwdSmem / per_sm / stage);
     smem = std::max(stage * stages, (size_t)(teams - 1) * cols * sizeof(float));
   }
-  static constexpr int kBwdResident = 512;   // threads of a SM (128 registers)
   static constexpr size_t kBwdSmem = 216 << 10;
 };
 
-// Blocks that the backward is launched with at most (its rows of `part`).
+// Blocks that the backward is launched with at most, of either type (its rows of `part`).
 int64_t bwd_parts(int64_t rows, int cols) {
-  const BwdShape b(cols, 2);
-  return std::min<int64_t>((rows + b.teams - 1) / b.teams, 160 * b.per_sm);
+  const BwdShape b(cols, 2), f(cols, 4);
+  const int64_t teams = std::min(b.teams, f.teams);
+  return std::min<int64_t>((rows + teams - 1) / teams, 160 * std::max(b.per_sm, f.per_sm));
 }
 
 template <auto Kernel>
@@ -514,21 +551,23 @@ cudaError_t allow_smem() {
   });
 }
 
-template <typename S, int kThreads>
+template <int VPL, typename S, bool DIRECT, bool TIGHT>
 cudaError_t bwd_kernel(const RmsNormBwdArgs &a, const BwdShape &b, unsigned grid, float *part, cudaStream_t st) {
-  const cudaError_t e = allow_smem<rms_norm_bwd_kernel<kBwdVpl, S, kThreads>>();
+  const cudaError_t e = allow_smem<rms_norm_bwd_kernel<VPL, S, DIRECT, TIGHT>>();
   if (e != cudaSuccess) return e;
-  return launch_dependent(rms_norm_bwd_kernel<kBwdVpl, S, kThreads>, grid, b.threads, b.smem, st, a, b.W,
+  return launch_dependent(rms_norm_bwd_kernel<VPL, S, DIRECT, TIGHT>, grid, b.threads, b.smem, st, a, b.W,
                           b.teams, b.stages, part);
 }
 
 template <typename S>
 cudaError_t bwd_launch(const RmsNormBwdArgs &a, float *part, cudaStream_t st) {
   const BwdShape b(a.cols, (int)sizeof(S));
-  const unsigned grid =
-      (unsigned)std::min<int64_t>(bwd_parts(a.rows, a.cols), (int64_t)num_sms() * b.per_sm);
-  const cudaError_t e = b.threads <= 512 ? bwd_kernel<S, 512>(a, b, grid, part, st)
-                                         : bwd_kernel<S, 1024>(a, b, grid, part, st);
+  const unsigned grid = (unsigned)std::min<int64_t>((a.rows + b.teams - 1) / b.teams, (int64_t)std::min(num_sms(), 160) * b.per_sm);
+  cudaError_t e;
+  if (b.vpl == 1) e = bwd_kernel<1, S, false, true>(a, b, grid, part, st);
+  else if (b.vpl == 4) e = bwd_kernel<4, S, sizeof(S) == 4, true>(a, b, grid, part, st);
+  else if (sizeof(S) == 2 && b.tight) e = bwd_kernel<2, uint16_t, false, true>(a, b, grid, part, st);
+  else e = bwd_kernel<2, S, false, false>(a, b, grid, part, st);
   if (e != cudaSuccess || part == nullptr) return e;
   return launch_dependent(dw_sum_kernel, (unsigned)((a.cols + 31) / 32), dim3(32, kSumRows), 0, st,
                           part, (int)grid, a.cols, a.dw, a.accumulate);
