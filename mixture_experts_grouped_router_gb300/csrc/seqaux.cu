@@ -197,10 +197,15 @@ seq_count_chunks_kernel(const SeqAuxArgs a, int chunk) {
 // (sequences with live tokens, live tokens) of the batch, in every thread.
 MOE_DEVINL int2 batch_size(const int32_t *tokens, int B, int (*s)[kWarps]) {
   int S = 0, N = 0;
-  for (int b = threadIdx.x; b < B; b += kThreads) {
-    const int n = ld_i32(tokens + b);
-    S += n > 0;
-    N += n;
+  for (int b = threadIdx.x; b < B; b += 4 * kThreads) {
+    int n[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) n[u] = b + u * kThreads < B ? ld_i32(tokens + b + u * kThreads) : 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      S += n[u] > 0;
+      N += n[u];
+    }
   }
   S = warp_sum_i(S);
   N = warp_sum_i(N);
@@ -448,15 +453,17 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
     gz = a.d_loss * 2.0f * a.z_coeff / (float)max(sn.y, 1);
   }
   float z = 0.0f, bal = 0.0f;
+  int next = b < a.B ? ld_i32(a.offsets + b + 1) : a.T;
   for (int t = t0; t < t1;) {
     const bool of_one = b >= 0 && b < a.B;
-    const int next = b < a.B ? ld_i32(a.offsets + b + 1) : a.T;
     const int n = of_one ? ld_i32(a.tokens + b) : 0;
     uint64_t f[4], acc2[4];
     int count[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       count[i] = of_one && col.at(i) < a.E ? ld_i32(a.counts + (int64_t)b * a.E + col.at(i)) : 0;
+    // where the next sequence ends, wanted after this one
+    const int after = b + 1 < a.B ? ld_i32(a.offsets + b + 2) : a.T;
     const int end = min(t1, max(next, t + 1));
     const float by_n = n > 0 ? 1.0f / (float)n : 0.0f;
     const float g0 = per_seq * by_n, fs = (float)a.E / (float)a.k * by_n;
@@ -502,8 +509,10 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
         col.store(out, g);
       }
     };
+    // x holds the warp's first token; past its last one the first of the next sequence is fetched
+    const int first = end + warp * kTok + grp;
     int u0 = t + warp * kTok;
-    if (t != t0) live = fetch(u0 + grp, end, x);
+    if (u0 >= end) live = fetch(first, t1, x);
     for (; u0 < end; u0 += kWarps * kTok) {
       const int u = u0 + grp;
       const bool valid = u < end, on = live && valid && n > 0;
@@ -513,17 +522,21 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
       Token k;
       token_scores<LPT, SIGMOID>(y, f, k);
       if (__any_sync(0xffffffffu, on && !(k.sum >= 1e-13f && k.sum <= 1e34f))) break;
-      if (u0 + kWarps * kTok < end) live = fetch(u + kWarps * kTok, end, x);
+      const bool more = u0 + kWarps * kTok < end;
+      live = fetch(more ? u + kWarps * kTok : first, more ? end : t1, x);
       finish(k, u, valid, on);
     }
-    for (; u0 < end; u0 += kWarps * kTok) {  // from a token with such logits on
-      const int u = u0 + grp;
-      const bool valid = u < end, on = fetch(u, end, x) && valid && n > 0;
+    if (u0 < end) {  // from a token with such logits on
+      for (; u0 < end; u0 += kWarps * kTok) {
+        const int u = u0 + grp;
+        const bool valid = u < end, on = fetch(u, end, x) && valid && n > 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = on ? x[i] : -INFINITY;
-      Token k;
-      token_scores_any<LPT, SIGMOID>(x, f, k);
-      finish(k, u, valid, on);
+        for (int i = 0; i < 8; ++i) x[i] = on ? x[i] : -INFINITY;
+        Token k;
+        token_scores_any<LPT, SIGMOID>(x, f, k);
+        finish(k, u, valid, on);
+      }
+      live = fetch(first, t1, x);
     }
     float acc[8];
 #pragma unroll
@@ -547,9 +560,13 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
     }
     t = end;
     if (t < t1) {  // most often the next sequence
-      ++b;
-      if (b >= a.B || ld_i32(a.offsets + b) > t || ld_i32(a.offsets + b + 1) <= t)
+      if (t == next && after > t && b + 1 < a.B) {
+        ++b;
+        next = after;
+      } else {
         b = last_at_most(a.offsets, a.B + 1, t, lane);
+        next = b < a.B ? ld_i32(a.offsets + b + 1) : a.T;
+      }
     }
   }
   if (!sums) return;
@@ -573,25 +590,24 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
 
 // P of 32 experts of a sequence from its slots (block (b, group of 32)); the first block past
 // the sequences adds up the loss.
-constexpr int kFinishThreads = 512;
+constexpr int kFinishThreads = 512;  // at most
 __global__ void __launch_bounds__(kFinishThreads)
 seq_aux_finish_kernel(const SeqAuxArgs a, int chunk, int blocks, const float *__restrict__ part,
                       const float2 *__restrict__ terms) {
-  constexpr int kW = kFinishThreads / 32;
-  __shared__ float s[kW][33];
-  __shared__ int s_n[2][kW];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ float s[kFinishThreads / 32][33];
+  __shared__ int s_n[2][kFinishThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kW = blockDim.x >> 5;
   const int b = blockIdx.x, e = blockIdx.y * 32 + lane;
   grid_dependency_begin();
   if (b == a.B) {
     if (blockIdx.y > 0) return;
     float bal = 0.0f, z = 0.0f;
     int S = 0, N = 0;
-    for (int i = threadIdx.x; i < blocks; i += kFinishThreads) {
+    for (int i = threadIdx.x; i < blocks; i += blockDim.x) {
       bal += ld_f32(&terms[i].x);
       z += ld_f32(&terms[i].y);
     }
-    for (int i = threadIdx.x; i < a.B; i += kFinishThreads) {
+    for (int i = threadIdx.x; i < a.B; i += blockDim.x) {
       const int n = ld_i32(a.tokens + i);
       S += n > 0;
       N += n;
@@ -633,7 +649,6 @@ seq_aux_finish_kernel(const SeqAuxArgs a, int chunk, int blocks, const float *__
   __syncthreads();
   if (warp == 0 && e < a.E) {
     v = 0.0f;
-#pragma unroll
     for (int w = 0; w < kW; ++w) v += s[w][lane];
     a.probs[(int64_t)b * a.E + e] = n > 0 ? v / (float)n : 0.0f;
   }
@@ -740,8 +755,10 @@ cudaError_t launch_seq_aux(const SeqAuxArgs &a, void *ws, cudaStream_t s) {
     default: e = launch_pass<32>(a, w, &blocks, &chunk, s); break;
   }
   if (e != cudaSuccess || a.loss == nullptr || small(a)) return e;
+  // a sequence has blocks / B + 1 slots on average
+  const int threads = blocks / a.B < 8 ? 128 : kFinishThreads;
   return launch_dependent(seq_aux_finish_kernel, dim3((unsigned)a.B + 1, (unsigned)((a.E + 31) / 32)),
-                          kFinishThreads, 0, s, a, chunk, blocks, w.part, w.terms);
+                          threads, 0, s, a, chunk, blocks, w.part, w.terms);
 }
 
 }  // namespace moe
