@@ -242,19 +242,14 @@ MOE_DEVINL float token_max(float v) {
   return v;
 }
 
-// e^x of pairs (x >= -200; under -87 it is 0): 2^t with t = x log2(e) rounded, times e^d for
-// what the rounding and log2(e)'s own left (d = ln2 (x log2(e) - t), |d| < 2^-16, 1 + d).
-MOE_DEVINL uint64_t exp2x(uint64_t x) {
-  const float kL = 1.44269502f, kRest = 1.92596303e-8f, kLn2 = 0.693147181f;
-  const uint64_t minus_t = mul2(x, pack2(-kL, -kL));
-  uint64_t d = fma2(x, pack2(kL, kL), minus_t);
-  d = mul2(fma2(x, pack2(kRest, kRest), d), pack2(kLn2, kLn2));
+// e^x of pairs, within |x| 2^-24 + 2^-22 of it (the product's rounding, and the power's); 0 from
+// -88 on, no number for an infinity or none.
+MOE_DEVINL uint64_t exp_near(uint64_t x) {
   float t0, t1, e0, e1;
-  unpack2(minus_t, t0, t1);
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(-t0));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(-t1));
-  const uint64_t e = pack2(e0, e1);
-  return fma2(e, d, e);
+  unpack2(mul2(x, pack2(1.44269502f, 1.44269502f)), t0, t1);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(t0));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(t1));
+  return pack2(e0, e1);
 }
 
 MOE_DEVINL float both(uint64_t v) {
@@ -271,16 +266,18 @@ struct Token {
   float sum, size, fs, shift;
 };
 
-// Of logits x (-inf: no expert, or a token that is not live).  No shift where the sum of e^x
-// stays well inside fp32's range: no maximum over the experts, and one exponential for the
-// softmax and the sigmoid e^x / (1 + e^x).
+// Of logits x (-200: no expert, or a token that is not live).  No shift where the sum of e^x
+// says that the largest logit is no further than 17 from 0 (tame_sum; a logit that is
+// infinite or no number makes the sum one too): no maximum over the experts, and one
+// exponential for the softmax and the sigmoid e^x / (1 + e^x).
+MOE_DEVINL bool tame_sum(float sum) { return sum >= 1e-5f && sum <= 1e7f; }
+
 template <int LPT, bool SIGMOID>
 MOE_DEVINL void token_scores(const float *x, const uint64_t *f, Token &k) {
   uint64_t sum = 0, size = 0, fs = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    // (a NaN ranks below every number)
-    k.u[i] = exp2x(pack2(fmaxf(x[2 * i], -200.0f), fmaxf(x[2 * i + 1], -200.0f)));
+    k.u[i] = exp_near(pack2(x[2 * i], x[2 * i + 1]));
     sum = add2(sum, k.u[i]);
     if (SIGMOID) {
       float a, b;
@@ -342,23 +339,40 @@ template <int LPT, bool VEC>
 struct Columns {
   int l, E;
   MOE_DEVINL int at(int i) const { return VEC ? ((i >> 2) * LPT + l) * 4 + (i & 3) : i * LPT + l; }
-  MOE_DEVINL void load(const float *row, float *x, float fill) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = fill;
+  // the row into the thread's place of a stage, and back from there
+  MOE_DEVINL void copy(float *place, const float *row) const {
     if (VEC) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        if (at(4 * h) < E) {
-          const uint4 w = ld_stream_v4(row + at(4 * h));
-          x[4 * h] = __uint_as_float(w.x);
-          x[4 * h + 1] = __uint_as_float(w.y);
-          x[4 * h + 2] = __uint_as_float(w.z);
-          x[4 * h + 3] = __uint_as_float(w.w);
-        }
+        if (at(4 * h) < E)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                           (uint32_t)__cvta_generic_to_shared(place + h * (4 * kThreads) + 4 * threadIdx.x)),
+                       "l"(row + at(4 * h))
+                       : "memory");
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (at(i) < E) x[i] = ld_f32(row + at(i));
+        if (at(i) < E)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                           (uint32_t)__cvta_generic_to_shared(place + i * kThreads + threadIdx.x)),
+                       "l"(row + at(i))
+                       : "memory");
+    }
+  }
+  MOE_DEVINL void take(const float *place, float *x, bool on, float fill) const {
+    if (VEC) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 w = *reinterpret_cast<const float4 *>(place + h * (4 * kThreads) + 4 * threadIdx.x);
+        const bool in = on && at(4 * h) < E;
+        x[4 * h] = in ? w.x : fill;
+        x[4 * h + 1] = in ? w.y : fill;
+        x[4 * h + 2] = in ? w.z : fill;
+        x[4 * h + 3] = in ? w.w : fill;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = on && at(i) < E ? place[i * kThreads + threadIdx.x] : fill;
     }
   }
   MOE_DEVINL void store(float *row, const float *x) const {
@@ -417,43 +431,62 @@ MOE_DEVINL void count_small(const SeqAuxArgs &a, int *cell) {
 }
 
 // One pass over the logits: a token is LPT lanes of 8 experts each, a block takes `chunk`
-// consecutive tokens, the next token's logits on their way while one is computed.
+// consecutive tokens in steps of kWarps * 32 / LPT.  A step's logits (and the gradients that
+// are added to) come by asynchronous copies kAhead steps ahead, each lane's to a place of its
+// own: a step's chain of sums and exponentials is 0.5 us long, a load's way as long again.
+// A step that holds the end of a sequence is taken by both.
+constexpr int kAhead = 4;
+constexpr int kMaskTokens = 2048;  // of a block, kept in shared memory
+constexpr int kStage = 8 * kThreads;
 template <int LPT, bool VEC, bool SIGMOID>
 __global__ void __launch_bounds__(kThreads, 3)
 seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ part,
                float2 *__restrict__ terms) {
   constexpr int kTok = 32 / LPT;  // tokens of a warp at a time
+  constexpr int kStep = kWarps * kTok;
+  extern __shared__ __align__(16) float ring[];  // logits [kAhead][kStage], then gradients
   __shared__ float s_p[kWarps][kMaxE];
   __shared__ float s_t[2][kWarps];
   __shared__ int s_n[2][kWarps];
+  __shared__ uint8_t s_mask[kMaskTokens];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane / LPT;
   const Columns<LPT, VEC> col = {lane % LPT, a.E};
   const bool sums = a.probs != nullptr, grad = a.d_logits != nullptr;
-  const bool with_z = a.z_coeff != 0.0f;
-  // Logits, offsets and mask are older than the kernel before this one where that is one of
-  // this call (it waited for them); the counts are not.
+  const bool with_z = a.z_coeff != 0.0f, add = grad && a.accumulate;
+  // Logits, offsets, mask and what is added to are older than the kernel before this one
+  // where that is one of this call (it waited for them); the counts are not.
   if (!sums || single) grid_dependency_begin();
-  if (single) count_small(a, reinterpret_cast<int *>(s_p));
   const int t0 = blockIdx.x * chunk, t1 = min(a.T, t0 + chunk);
-  // token u of the walk below, or one that is not live
-  auto fetch = [&](int u, int end, float *x) -> bool {
-    const bool live = u < end && (a.mask == nullptr || ld_u8(a.mask + u) != 0);
-    if (u < end) col.load(a.logits + (int64_t)u * a.ld, x, -INFINITY);
-    return live;
+  const int mine = warp * kTok + grp;  // the lane's token of a step
+  int ahead = 0;                       // the step that is copied next
+  auto fetch = [&]() {
+    const int u = t0 + ahead * kStep + mine;
+    if (u < t1) {
+      float *place = ring + (ahead % kAhead) * kStage;
+      col.copy(place, a.logits + (int64_t)u * a.ld);
+      if (add) col.copy(place + kAhead * kStage, a.d_logits + (int64_t)u * a.ld_d);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ++ahead;
   };
-  float x[8];
-  bool live = fetch(t0 + warp * kTok + grp, t1, x);
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) fetch();
+  const bool masked = a.mask != nullptr, near_mask = chunk <= kMaskTokens;
+  if (masked && near_mask)
+    for (int i = threadIdx.x; i < t1 - t0; i += kThreads) s_mask[i] = (uint8_t)ld_u8(a.mask + t0 + i);
+  if (single) count_small(a, reinterpret_cast<int *>(s_p));
   int b = last_at_most(a.offsets, a.B + 1, t0, lane);
   if (sums && !single) grid_dependency_begin();
-  float per_seq = 0.0f, gz = 0.0f;
   int2 sn = make_int2(0, 0);
+  float per_seq = 0.0f, gz = 0.0f;
   if (grad || single) {
     sn = batch_size(a.tokens, a.B, s_n);
     per_seq = a.d_loss * a.coeff / (float)max(sn.x, 1);
     gz = a.d_loss * 2.0f * a.z_coeff / (float)max(sn.y, 1);
   }
+  __syncthreads();
   float z = 0.0f, bal = 0.0f;
-  int next = b < a.B ? ld_i32(a.offsets + b + 1) : a.T;
+  int next = b < a.B ? ld_i32(a.offsets + b + 1) : a.T, step = 0;
   for (int t = t0; t < t1;) {
     const bool of_one = b >= 0 && b < a.B;
     const int n = of_one ? ld_i32(a.tokens + b) : 0;
@@ -473,7 +506,7 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
       acc2[i] = 0;
     }
     // what a token adds to the sums, and its gradient
-    auto finish = [&](const Token &k, int u, bool valid, bool on) {
+    auto finish = [&](const Token &k, int u, bool valid, bool on, const float *place) {
       // (a token that is not live, or has no logit above -inf: p = 0 and no z)
       const bool some = k.sum > 0.0f;
       const float inv = k.size > 0.0f ? rcp_f(k.size) : 0.0f, c = k.fs * inv;
@@ -487,12 +520,11 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
           bal = fmaf(c, by_n, bal);
         }
       }
-      if (grad && valid && (on || !a.accumulate)) {
+      if (grad && valid && (on || !add)) {
         // d = k1 j (f - c) + k2 u
         const float k1 = g0 * inv, k2 = some ? gz * lse * rcp_f(k.sum) : 0.0f;
         const float k0 = SIGMOID ? -c * k1 : fmaf(-c, k1, k2);
         const uint64_t k12 = pack2(k1, k1), k22 = pack2(k2, k2), k02 = pack2(k0, k0);
-        float *out = a.d_logits + (int64_t)u * a.ld_d;
         float g[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -500,43 +532,55 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
           if (SIGMOID) d = fma2(k.u[i], k22, d);
           unpack2(d, g[2 * i], g[2 * i + 1]);
         }
-        if (a.accumulate) {
+        if (add) {
           float old[8];
-          col.load(out, old, 0.0f);
+          col.take(place + kAhead * kStage, old, true, 0.0f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) g[i] += old[i];
         }
-        col.store(out, g);
+        col.store(a.d_logits + (int64_t)u * a.ld_d, g);
       }
     };
-    // x holds the warp's first token; past its last one the first of the next sequence is fetched
-    const int first = end + warp * kTok + grp;
-    int u0 = t + warp * kTok;
-    if (u0 >= end) live = fetch(first, t1, x);
-    for (; u0 < end; u0 += kWarps * kTok) {
-      const int u = u0 + grp;
-      const bool valid = u < end, on = live && valid && n > 0;
-      float y[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = on ? x[i] : -INFINITY;
-      Token k;
-      token_scores<LPT, SIGMOID>(y, f, k);
-      if (__any_sync(0xffffffffu, on && !(k.sum >= 1e-13f && k.sum <= 1e34f))) break;
-      const bool more = u0 + kWarps * kTok < end;
-      live = fetch(more ? u + kWarps * kTok : first, more ? end : t1, x);
-      finish(k, u, valid, on);
-    }
-    if (u0 < end) {  // from a token with such logits on
-      for (; u0 < end; u0 += kWarps * kTok) {
-        const int u = u0 + grp;
-        const bool valid = u < end, on = fetch(u, end, x) && valid && n > 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = on ? x[i] : -INFINITY;
+    // the logits of the lane's token of this step, `fill` where it is not live or not of this sequence
+    auto take = [&](float *x, float fill, int &u, bool &valid, const float *&place) -> bool {
+      u = t0 + step * kStep + mine;
+      valid = u >= t && u < end;
+      bool on = valid && n > 0;
+      if (masked && on) on = (near_mask ? s_mask[u - t0] : ld_u8(a.mask + u)) != 0;
+      place = ring + (step % kAhead) * kStage;
+      col.take(place, x, on, fill);
+      return on;
+    };
+    // on to the next step, if this one ends before the sequence does
+    auto onward = [&]() -> bool {
+      if (t0 + (step + 1) * kStep > end && end < t1) return false;
+      fetch();
+      ++step;
+      return t0 + step * kStep < end;
+    };
+    for (bool more = true; more;) {
+      float x[8];
+      int u;
+      bool valid;
+      const float *place;
+      bool odd = false;
+      while (more) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        const bool on = take(x, -200.0f, u, valid, place);
+        Token k;
+        token_scores<LPT, SIGMOID>(x, f, k);
+        odd = __any_sync(0xffffffffu, on && !tame_sum(k.sum));
+        if (odd) break;
+        finish(k, u, valid, on, place);
+        more = onward();
+      }
+      if (odd) {  // a step with such logits
+        const bool on = take(x, -INFINITY, u, valid, place);
         Token k;
         token_scores_any<LPT, SIGMOID>(x, f, k);
-        finish(k, u, valid, on);
+        finish(k, u, valid, on, place);
+        more = onward();
       }
-      live = fetch(first, t1, x);
     }
     float acc[8];
 #pragma unroll
@@ -569,6 +613,7 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
       }
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (!sums) return;
   z = warp_sum(z);
   bal = warp_sum(bal);
@@ -661,10 +706,9 @@ int lanes_per_token(int E) {
 }
 
 // Blocks of the pass over the logits (one wave), and the tokens of each.
-template <typename F>
-void split(int T, int E, F resident, int *blocks, int *chunk) {
+void split(int T, int E, int per_sm, int *blocks, int *chunk) {
   const int step = kWarps * (32 / lanes_per_token(E));
-  const int most = std::min(kMaxBlocks, resident() * num_sms());
+  const int most = std::min(kMaxBlocks, per_sm * num_sms());
   const int64_t steps = ((int64_t)T + step - 1) / step;
   const int64_t each = std::max<int64_t>(1, (steps + most - 1) / most);
   *chunk = (int)(each * step);
@@ -694,15 +738,29 @@ bool small(const SeqAuxArgs &a) {
 // The pass over the logits; its blocks and their tokens are left for the finish.
 template <int LPT, bool VEC, bool SIGMOID>
 cudaError_t launch_pass(const SeqAuxArgs &a, const Workspace &w, int *blocks, int *chunk, cudaStream_t s) {
+  constexpr auto kernel = seq_aux_kernel<LPT, VEC, SIGMOID>;
+  constexpr size_t ring = sizeof(float) * kAhead * kStage;
+  struct Set {
+    cudaError_t status;
+    int per_sm[2];  // resident blocks, without and with gradients to add to
+  };
+  static PerDevice<Set> known;
+  const Set set = known.get(current_device(), [] {
+    Set v = {cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(2 * ring)), {1, 1}};
+    for (int k = 0; k < 2 && v.status == cudaSuccess; ++k)
+      v.status = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&v.per_sm[k], kernel, kThreads, (k + 1) * ring);
+    return v;
+  });
+  if (set.status != cudaSuccess) return set.status;
+  const int add = a.d_logits != nullptr && a.accumulate ? 1 : 0;
   const bool single = small(a);
-  split(a.T, a.E, [] { return blocks_per_sm<seq_aux_kernel<LPT, VEC, SIGMOID>>(kThreads); }, blocks, chunk);
+  split(a.T, a.E, std::max(1, set.per_sm[add]), blocks, chunk);
   if (single) {
     *blocks = 1;
     *chunk = a.T;
   }
   if (*blocks == 0) return cudaSuccess;
-  return launch_dependent(seq_aux_kernel<LPT, VEC, SIGMOID>, *blocks, kThreads, 0, s, a, *chunk, single,
-                          w.part, w.terms);
+  return launch_dependent(kernel, *blocks, kThreads, (1 + add) * ring, s, a, *chunk, single, w.part, w.terms);
 }
 
 template <int LPT>

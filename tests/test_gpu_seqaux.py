@@ -1,8 +1,9 @@
-"""The balance loss of sequences with the z loss against the fp64 oracle.  Tolerances: the
-exponentials, logarithms and divisions are within 2 ulp of fp32, a token's sums over at most 8
-values a lane and 5 lanes' additions: 2^-19 of a probability, twice that of the gradient's terms
-(2^-18 of their size); lse also half an ulp of its own size and 2^-22 of the largest logit.  Means
-over tokens take at most `adds` additions: adds 2^-24."""
+"""The balance loss of sequences with the z loss against the fp64 oracle.  Tolerances: e^x of a
+logit is within |x| 2^-24 + 2^-22 of itself (logits here are within 6 of 0: 2^-20.6), reciprocals
+within 2^-23, a token's sums take at most 8 values a lane and 5 lanes' additions, each half an ulp:
+2^-19 of a probability, twice that of the gradient's terms (2^-18 of their size); lse also half an
+ulp of its own size and 2^-22 of the largest logit.  Means over tokens take at most `adds`
+additions: adds 2^-24."""
 import numpy as np
 import pytest
 import torch
