@@ -787,8 +787,8 @@ moe_status_t moe_unpermute_bwd(const uint16_t *d_out, int64_t ld_dout, const uin
  *              MOE_CODES_ACT8  int8 codes and bf16 scales [rows, lds >= ceil(cols /
  *                 32)], what moe_act8_dequantize reads; rows of q on 8 bytes
  *              the codes are those that moe_mx_quantize and moe_act8_quantize make of y
- * cols % 8 == 0, cols <= 16384; rows of the matrices start on 16 bytes.  fp32 sums; a
- * row whose squares pass fp32's range reads as zeros in y, one with a NaN as NaN.
+ * cols % 8 == 0, cols <= 16384; w and the rows of the matrices start on 16 bytes.  fp32
+ * sums; a row whose squares pass fp32's range reads as zeros in y, one with a NaN as NaN.
  */
 moe_status_t moe_rms_norm(const uint16_t *x, int64_t ldx, const void *residual, int64_t ld_res,
                           int stream_dtype, int64_t rows, int cols, const void *w, int w_dtype,
@@ -852,7 +852,9 @@ moe_status_t moe_mx_dequantize(const uint8_t *q, int64_t ldq, const uint8_t *sf,
  *   workspace    moe_seq_aux_loss_workspace_bytes(T, E, B) bytes, 4-byte aligned;
  *                contents on entry are ignored
  * A token whose logits are all -inf (or NaN) has p = 0 and no z.  fp32 sums in a fixed
- * order.  E <= 256, k <= 16, T <= 2^30, 1 <= B <= 65536.
+ * order; rows of logits and gradients on 16 bytes with E % 4 == 0 are read 16 bytes at a
+ * time; logits of -inf, NaN or no nearer to 0 than 17 take a slower way.  E <= 256, k <=
+ * 16, T <= 2^30, 1 <= B <= 65536.
  *
  * moe_seq_aux_loss_bwd -- the gradient by itself, from counts and tokens as
  * moe_seq_aux_loss wrote them (held fixed), times d_loss:

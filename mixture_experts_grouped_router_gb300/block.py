@@ -101,6 +101,7 @@ class SeqAuxLoss:
         self.counts, self.tokens = torch.empty(B, E, **i32), torch.empty(B, **i32)
         self.probs, self.loss = torch.empty(B, E, **f32), torch.empty(2, **f32)
         self.workspace = torch.empty(nb, dtype=torch.uint8, device=device)
+        self.seen = None  # tokens of the last forward
 
     def _shape(self, logits, seq_offsets):
         if logits.dim() != 2 or logits.shape[0] > self.T or logits.shape[1] != self.E \
@@ -119,12 +120,16 @@ class SeqAuxLoss:
         L.moe_seq_aux_loss(logits, topk_idx, seq_offsets, self.score_fn, self.coeff, self.z_coeff,
                            self.counts, self.tokens, self.probs, self.loss, self.workspace,
                            token_mask, d_logits, d_loss, accumulate, stream)
+        self.seen = logits.shape[0]
         return self.loss
 
     def backward(self, logits, seq_offsets, d_logits, token_mask=None, d_loss=1.0, accumulate=True,
                  stream=None):
         """The gradient of the last forward (the same logits, offsets and mask) into d_logits."""
         self._shape(logits, seq_offsets)
+        if logits.shape[0] != self.seen:
+            raise ValueError("SeqAuxLoss.backward of %d tokens, the last forward was of %s"
+                             % (logits.shape[0], self.seen))
         L.moe_seq_aux_loss_bwd(logits, self.k, seq_offsets, self.score_fn, self.coeff, self.z_coeff,
                                self.counts, self.tokens, d_logits, token_mask, d_loss, accumulate, stream)
         return d_logits
@@ -186,6 +191,6 @@ class GradClip:
 
     def clip(self, max_norm, scale=1.0, stream=None):
         """outs = grads * scale * min(1, max_norm / (norm + 1e-6)); returns the norm (of the scaled
-        gradients).  A norm that is not finite clips nothing: leave the step out."""
+        gradients; the same tensor each time).  A norm that is not finite clips nothing: leave the step out."""
         L.moe_clip_grads(self.plan, self.chunks, max_norm, scale, self.total, self.workspace, stream)
         return self.total

@@ -251,6 +251,7 @@ moe_status_t moe_seq_aux_loss(const float *logits, int64_t ld_logits, int T, int
   REQUIRE((T == 0 || topk_idx) && counts && tokens && probs_mean && loss, MOE_ERR_INVALID_ARG,
           "%s: null pointer", who);
   REQUIRE(d_logits == nullptr || ld_dlogits >= E, MOE_ERR_INVALID_ARG, "%s: ld_dlogits < E", who);
+  REQUIRE(d_logits == nullptr || d_logits != logits, MOE_ERR_INVALID_ARG, "%s: d_logits are logits", who);
   REQUIRE(workspace && workspace_bytes >= moe::seq_aux_workspace_bytes(T, E, B), MOE_ERR_INVALID_ARG,
           "%s: workspace of %zu bytes < %zu", who, workspace_bytes,
           moe::seq_aux_workspace_bytes(T, E, B));
@@ -272,6 +273,7 @@ moe_status_t moe_seq_aux_loss_bwd(const float *logits, int64_t ld_logits, int T,
   CHECK(check_seq(who, T, E, k, B, score_fn, logits, ld_logits, seq_offsets, coeff, z_coeff));
   REQUIRE(counts && tokens && (T == 0 || d_logits), MOE_ERR_INVALID_ARG, "%s: null pointer", who);
   REQUIRE(ld_dlogits >= E, MOE_ERR_INVALID_ARG, "%s: ld_dlogits < E", who);
+  REQUIRE(d_logits == nullptr || d_logits != logits, MOE_ERR_INVALID_ARG, "%s: d_logits are logits", who);
   const moe::SeqAuxArgs a = {logits, ld_logits, T, E, k, score_fn, nullptr, seq_offsets, B, token_mask,
                              coeff, z_coeff, const_cast<int32_t *>(counts), const_cast<int32_t *>(tokens),
                              nullptr, nullptr, d_loss, d_logits, ld_dlogits, accumulate};

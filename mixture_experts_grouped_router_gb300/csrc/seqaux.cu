@@ -314,8 +314,11 @@ MOE_DEVINL void token_scores_any(const float *x, const uint64_t *f, Token &k) {
     sum += u;
     s[i] = j[i] = u;
     if (SIGMOID) {
-      s[i] = 1.0f / (1.0f + expf(-v[i]));
-      j[i] = s[i] * (1.0f - s[i]);
+      // s and 1 - s; where every logit is under 0, s times e^-shift, which their quotients lose again
+      // (so that logits whose sigmoids all vanish in fp32 keep their proportions)
+      const float r = 1.0f / (1.0f + expf(v[i]));
+      s[i] = k.shift < 0.0f ? u * r : 1.0f / (1.0f + expf(-v[i]));
+      j[i] = s[i] * r;
       size += s[i];
     }
     float f0, f1;
@@ -759,7 +762,6 @@ cudaError_t launch_pass(const SeqAuxArgs &a, const Workspace &w, int *blocks, in
     *blocks = 1;
     *chunk = a.T;
   }
-  if (*blocks == 0) return cudaSuccess;
   return launch_dependent(kernel, *blocks, kThreads, (1 + add) * ring, s, a, *chunk, single, w.part, w.terms);
 }
 
@@ -805,7 +807,8 @@ cudaError_t launch_seq_aux(const SeqAuxArgs &a, void *ws, cudaStream_t s) {
   if (a.loss != nullptr && !small(a)) e = launch_count(a, s);
   if (e != cudaSuccess) return e;
   int blocks = 0, chunk = 1;
-  switch (lanes_per_token(a.E)) {
+  switch (a.T > 0 ? lanes_per_token(a.E) : 0) {
+    case 0: break;  // no tokens
     case 1: e = launch_pass<1>(a, w, &blocks, &chunk, s); break;
     case 2: e = launch_pass<2>(a, w, &blocks, &chunk, s); break;
     case 4: e = launch_pass<4>(a, w, &blocks, &chunk, s); break;

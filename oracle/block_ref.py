@@ -41,10 +41,12 @@ def probabilities(x, sigmoid):
     lse = np.where(some, m + np.log(total), 0.0)
     if not sigmoid:
         return soft, soft, soft, lse
-    s = np.where(x > -np.inf, 1.0 / (1.0 + np.exp(-np.where(x > -np.inf, x, 0.0))), 0.0)
-    size = s.sum(1, keepdims=True)
-    size = np.where(size > 0, size, 1.0)
-    return s / size, s * (1.0 - s) / size, soft, lse
+    # by logarithms, so that scores that vanish keep their proportions
+    log_s = -np.logaddexp(0.0, -x)
+    top = np.where(some, np.max(log_s, 1, keepdims=True, initial=-np.inf), 0.0)
+    p = np.exp(log_s - top)
+    p = p / np.where(some, p.sum(1, keepdims=True), 1.0)
+    return p, p * np.exp(-np.logaddexp(0.0, x)), soft, lse
 
 
 def seq_aux(logits, idx, offsets, mask, sigmoid, coeff, z_coeff):

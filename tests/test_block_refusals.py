@@ -96,7 +96,7 @@ def test_mx_dequantize(L):
     assert d(q=P(4100)) == uns and d(rows=0, q=None) == L.MOE_OK
 
 
-def seq(L, lg=P(), ld=8, T=10, E=8, k=2, fn=0, idx=P(), off=P(), B=3, c=0.1, z=0.1, cnt=P(), tok=P(),
+def seq(L, lg=P(1 << 16), ld=8, T=10, E=8, k=2, fn=0, idx=P(), off=P(), B=3, c=0.1, z=0.1, cnt=P(), tok=P(),
         pr=P(), loss=P(), d=P(), ldd=8, ws=P(), nb=BIG):
     return L.LIB.moe_seq_aux_loss(lg, ld, T, E, k, fn, idx, off, B, None, c, z, cnt, tok, pr, loss, 1.0,
                                   d, ldd, 0, ws, nb, None)
@@ -108,6 +108,7 @@ def test_seq_aux_loss(L):
     assert seq(L, E=257, ld=257, ldd=257) == uns and seq(L, E=20, ld=20, ldd=20, k=17) == uns
     assert seq(L, T=(1 << 30) + 1) == uns and seq(L, B=65537) == uns
     assert seq(L, fn=2) == bad and seq(L, ld=7) == bad and seq(L, ldd=7) == bad
+    assert seq(L, d=P(1 << 16)) == bad and "d_logits are logits" in L.last_error()
     for p in ("lg", "idx", "off", "cnt", "tok", "pr", "loss", "ws"):
         assert seq(L, **{p: None}) == bad
     for v in (float("nan"), float("inf")):
@@ -117,12 +118,12 @@ def test_seq_aux_loss(L):
     f = L.moe_seq_aux_loss_workspace_bytes
     assert f(-1, 8, 1) == 0 and f(8, 0, 1) == 0 and f(8, 257, 1) == 0 and f(8, 8, 0) == 0
 
-    def bwd(lg=P(), ld=8, T=10, E=8, k=2, fn=0, off=P(), B=3, cnt=P(), tok=P(), d=P(), ldd=8):
+    def bwd(lg=P(1 << 16), ld=8, T=10, E=8, k=2, fn=0, off=P(), B=3, cnt=P(), tok=P(), d=P(), ldd=8):
         return L.LIB.moe_seq_aux_loss_bwd(lg, ld, T, E, k, fn, off, B, None, 0.1, 0.1, cnt, tok, 1.0, d,
                                           ldd, 0, None)
     for p in ("lg", "off", "cnt", "tok", "d"):
         assert bwd(**{p: None}) == bad
-    assert bwd(ldd=7) == bad and bwd(E=300, ld=300, ldd=300) == uns and bwd(fn=-1) == bad
+    assert bwd(d=P(1 << 16)) == bad and bwd(ldd=7) == bad and bwd(E=300, ld=300, ldd=300) == uns and bwd(fn=-1) == bad
     assert bwd(T=0, lg=None, d=None) == L.MOE_OK
 
 
@@ -283,6 +284,11 @@ def test_tensors_of_the_loss(block):
         s.forward(f32(16, 8), idx, off, torch.ones(16), stream=S)
     with pytest.raises(ValueError, match="d_logits"):
         s.forward(f32(16, 8), idx, off, d_logits=f32(15, 8), stream=S)
+    with pytest.raises(ValueError, match="last forward was of None"):
+        s.backward(f32(16, 8), off, f32(16, 8), stream=S)
+    s.seen = 16  # as after a forward
+    with pytest.raises(ValueError, match="of 15 tokens, the last forward was of 16"):
+        s.backward(f32(15, 8), off, f32(15, 8), stream=S)
     with pytest.raises(ValueError, match="d_logits"):
         s.backward(f32(16, 8), off, f32(16, 9), stream=S)
     with pytest.raises(ValueError, match="GPU"):

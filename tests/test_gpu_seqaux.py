@@ -208,3 +208,57 @@ def test_gradient_by_differences(block):
         e = np.zeros((T, E))
         e[i] = 1e-5
         assert abs((f(x + e) - f(x - e)) / 2e-5 - f64(d)[i]) <= 1e-5
+
+
+@pytest.mark.parametrize("E,sigmoid", [(64, 0), (256, 1), (30, 1), (8, 0)])
+def test_odd_logits_among_others(block, E, sigmoid):
+    """Steps that hold closed experts, far logits and rows without any, in ragged masked sequences;
+    written and added to."""
+    T, k = 3001, 2
+    rng, x, idx = case(T, E, k, 5)
+    x[rng.random(T) < 0.05] += 40.0
+    x[rng.random(T) < 0.05] -= 300.0
+    closed = rng.random((T, E)) < 0.3
+    x = np.where((rng.random(T) < 0.1)[:, None] & closed, -np.inf, x).astype(np.float32)
+    x[rng.integers(0, T, 5)] = -np.inf
+    cut = np.sort(rng.integers(0, T + 1, 18))
+    mask = rng.random(T) > 0.2
+    want = R.seq_aux(x, idx, cut, mask, bool(sigmoid), 0.3, 0.0)
+    lx, li, off, m = torch.tensor(x, device="cuda"), i32(idx), i32(cut), torch.tensor(mask, device="cuda")
+    s = block.SeqAuxLoss(T, E, k, 17, sigmoid, 0.3)
+    d = torch.full((T, E), 9.0, device="cuda")
+    s.forward(lx, li, off, m, d_logits=d)
+    check((s.loss, s.counts, s.tokens, s.probs, d), want, E, T)
+    base = torch.randn(T, E, device="cuda") * 1e-3
+    added = base.clone()
+    s.backward(lx, off, added, m)
+    sum_ = f64(base) + want["d_logits"]
+    assert (np.abs(f64(added) - sum_) <= 2.0 ** -18 * want["size"] + 2.0 ** -23 * np.abs(sum_) + 1e-37).all()
+
+
+@pytest.mark.parametrize("masked", [False, True])
+def test_a_million_tokens(block, masked):
+    """More tokens a block than it keeps the mask of."""
+    T, E, k, B = 1_100_003, 2, 1, 3
+    rng, x, idx = case(T, E, k)
+    cut = np.array([7, 300_000, 300_000, T - 5])
+    mask = rng.random(T) > 0.5 if masked else None
+    want = R.seq_aux(x, idx, cut, mask, False, 0.3, 0.05)
+    s = block.SeqAuxLoss(T, E, k, B, 0, 0.3, 0.05)
+    d = torch.full((T, E), 9.0, device="cuda")
+    s.forward(torch.tensor(x, device="cuda"), i32(idx), i32(cut),
+              None if mask is None else torch.tensor(mask, device="cuda"), d_logits=d)
+    # (two experts: lse may lie near 0, where it is off by half an ulp of the logits' size)
+    want["size"] += 2.0 * 0.05 / want["tokens"].sum() * 2.0 ** -4
+    check((s.loss, s.counts, s.tokens, s.probs, d), want, E, T)
+
+
+def test_the_gradient_is_that_of_the_last_forward(block):
+    s = block.SeqAuxLoss(10, 8, 2, 1, 0, 0.3)
+    x, off = torch.randn(6, 8, device="cuda"), i32([0, 6])
+    with pytest.raises(ValueError, match="last forward"):
+        s.backward(x, off, torch.empty_like(x))
+    s.forward(x, x.topk(2, 1).indices.to(torch.int32), off)
+    s.backward(x, off, torch.empty_like(x))
+    with pytest.raises(ValueError, match="last forward"):
+        s.backward(x[:5], off, torch.empty(5, 8, device="cuda"))

@@ -67,6 +67,20 @@ def test_rows_without_a_logit_add_nothing():
     assert got["loss"][1] == pytest.approx(np.log(2.0) ** 2 / 2) and (got["d_logits"][1] == 0).all()
 
 
+def test_vanishing_scores_keep_their_proportions():
+    """Sigmoids of far negative logits are e^x: their quotients are the softmax; of equal ones 1 / E."""
+    x = np.array([[-900.0, -901.0, -np.inf], [-1e30, -1e30, -1e30]])
+    p, jac, soft, _ = R.probabilities(x, True)
+    np.testing.assert_allclose(p, soft, rtol=1e-12)
+    np.testing.assert_allclose(jac, p, rtol=1e-12)
+    np.testing.assert_allclose(p[1], 1 / 3)
+    x = np.array([[800.0, -2.0]])
+    p, jac, _, _ = R.probabilities(x, True)
+    s = 1 / (1 + np.exp(2.0))
+    np.testing.assert_allclose(p, [[1 / (1 + s), s / (1 + s)]], rtol=1e-12)
+    np.testing.assert_allclose(jac, [[0.0, s * (1 - s) / (1 + s)]], rtol=1e-12, atol=1e-300)
+
+
 def test_clip_closed_forms():
     g = [np.array([3.0]), np.array([0.0, 4.0])]
     norm, c = R.clip(g, 1.0, 0.5)
