@@ -7,6 +7,10 @@
 // launch.  The first kernel writes a sum a block, the second adds these up again in every
 // block (the same order, so the same number) and scales.  It walks the chunks from the last
 // one back: what the first one read last is still in L2.
+//
+// HBM bounds both: 1.41 G bf16 gradients take 405 us (7.0 TB/s) to square and 885 us (6.4 TB/s of
+// reads and writes) to scale, 1244 us at the measured copy's rate; loads that wait for the
+// arithmetic of the ones before them took 668 and 887.
 #include <algorithm>
 
 #include "common.cuh"

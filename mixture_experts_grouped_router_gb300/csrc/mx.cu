@@ -345,7 +345,8 @@ mx_quantize_2x_kernel(const uint16_t *__restrict__ x, int64_t ldx, int64_t rows,
 }
 
 // Values of block-scaled codes (PLAIN scales), rounded once to bf16: a warp takes 256 columns
-// of a row at a time, 8 a lane, four such pieces in flight.
+// of a row at a time, 8 a lane, four such pieces in flight (16384 x 4096: 32 us, 6.3 TB/s;
+// one piece: 39).
 __global__ void __launch_bounds__(kMxThreads)
 mx_dequantize_kernel(const uint8_t *__restrict__ q, int64_t ldq, const uint8_t *__restrict__ sf,
                      int rows, int cols, int fmt, uint16_t *__restrict__ x, int64_t ldx) {

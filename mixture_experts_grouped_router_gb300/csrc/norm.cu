@@ -9,7 +9,8 @@
 // The norm is of the h that is stored, so that the backward, which reads it back, is the
 // derivative of what the forward computed.  The 8-bit codes are those of the bf16 y (what
 // the block-scaled and the checkpoint quantisers make of it, bit for bit): a program that
-// keeps both has codes of the tensor it computed with.  All sums and products are fp32.
+// keeps both has codes of the tensor it computed with.  All sums and products are fp32; h is
+// rounded to the stream's type, as the residual stream goes on with it, y to bf16.
 #include <algorithm>
 
 #include "internal.h"
