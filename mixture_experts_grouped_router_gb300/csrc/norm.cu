@@ -271,7 +271,7 @@ MOE_DEVINL void copy_async(void *dst, const void *src) {
 // under way while a row's sums are taken (16384 x 4096 bf16: 79 us, 6800 GB/s; without: 106
 // us).  The row at hand is held in registers, as it came, so that its place is free for the
 // next one before the sums (read twice from shared memory: 99 us).  DIRECT (wide fp32 rows,
-// of which two would not fit): d_residual is loaded past shared memory.
+// which would not fit beside the weights): d_residual is loaded past shared memory.
 // Threads of a SM, as their registers go: 128 a thread, fewer where the row at hand is unpacked
 // a second time (TIGHT) instead of kept in fp32.
 constexpr int bwd_threads(int vpl, int elem, bool tight) {
@@ -285,12 +285,13 @@ rms_norm_bwd_kernel(const RmsNormBwdArgs a, int W, int teams, int stages, float 
   constexpr int kDy = (DIRECT ? 1 : 2) * VPL * kWide;
   constexpr int kCopies = kDy + VPL;               // of a warp and row, 512 bytes each
   __shared__ float red[2][2][32];
-  extern __shared__ __align__(16) uint8_t smem[];  // [stages][warps][kCopies][512]
+  // [stages][warps][kCopies][512], then (four vectors a lane) the lanes' weights, each its own
+  extern __shared__ __align__(16) uint8_t smem[];
   const Team t(W);
   constexpr bool kKeepW = VPL <= 2;
   const int c0 = t.warp * (256 * VPL) + t.lane * 8;
   auto in = [&](int v) { return c0 + 256 * v < a.cols; };
-  Pairs dw[VPL], kept[kKeepW ? VPL : 1];
+  Pairs dw[VPL], kept[kKeepW ? VPL : 1];  // kept: the weights
   const S *h = static_cast<const S *>(a.h);
   const S *res = static_cast<const S *>(a.d_residual);
   S *dh = static_cast<S *>(a.dh);
@@ -330,8 +331,21 @@ rms_norm_bwd_kernel(const RmsNormBwdArgs a, int W, int teams, int stages, float 
       if (in(v)) kept[v] = load_w(a.w, a.w_dtype, c0 + 256 * v);
     }
   }
-  // (past the last column h and dy are 0, and any weight will do)
-  auto weight = [&](int v) { return kKeepW ? kept[v] : load_w(a.w, a.w_dtype, min(c0 + 256 * v, a.cols - 8)); };
+  uint4 *own_w = reinterpret_cast<uint4 *>(smem + stages * stage) + threadIdx.x;
+  if (!kKeepW) {
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      Pairs w;
+      w.zero();
+      if (in(v)) w = load_w(a.w, a.w_dtype, c0 + 256 * v);
+      own_w[2 * v * blockDim.x] = *reinterpret_cast<const uint4 *>(&w.p[0]);
+      own_w[(2 * v + 1) * blockDim.x] = *reinterpret_cast<const uint4 *>(&w.p[2]);
+    }
+  }
+  auto weight = [&](int v) {
+    if (kKeepW) return kept[v];
+    return from_f32(own_w[2 * v * blockDim.x], own_w[(2 * v + 1) * blockDim.x]);
+  };
   int turn = 0, s = 0;
   for (; row < a.rows; row += step, turn ^= 1) {
     Vec8<S, false> hv[VPL], rv[VPL];
@@ -514,7 +528,8 @@ cudaError_t norm_by_size(const RmsNormArgs &a, cudaStream_t st) {
 // One vector where a row has no more (bf16 256 columns: 69 us, with two 83; fp32 128: 61 and 89,
 // but 256: 119 and 109), four past 8192 columns.  TIGHT with two vectors: blocks of which one
 // leaves a good part of the SM without threads and two fit so (5000 columns: 96 us, else 116;
-// 4096: 91 and 85).
+// 4096: 91 and 85).  With four vectors the weights are kept in shared memory (read twice a row
+// from L2 16384 columns took 129 us).
 struct BwdShape {
   int vpl, W, teams, threads, per_sm, stages;
   bool direct, tight;
@@ -524,14 +539,15 @@ struct BwdShape {
     W = team_warps(cols, vpl);
     teams = std::max(1, 8 / W);
     threads = 32 * W * teams;
-    direct = vpl == 4 && elem == 4;
+    const size_t weights = vpl == 4 ? (size_t)threads * vpl * 32 : 0;
+    direct = (size_t)threads * 8 * vpl * (2 + elem * 2) + weights > kBwdSmem;
     tight = vpl != 2 || (elem == 2 && threads > 256 && threads <= 384);
     const size_t stage = (size_t)threads * 8 * vpl * (2 + elem * (direct ? 1 : 2));
     // as many blocks as leave each two rows
     per_sm = std::max(1, bwd_threads(vpl, elem, tight) / threads);
     while (per_sm > 1 && kBwdSmem / per_sm < 2 * stage) --per_sm;
-    stages = (int)std::min<size_t>(3, kBwdSmem / per_sm / stage);
-    smem = std::max(stage * stages, (size_t)(teams - 1) * cols * sizeof(float));
+    stages = (int)std::min<size_t>(3, (kBwdSmem / per_sm - weights) / stage);
+    smem = std::max(stage * stages + weights, (size_t)(teams - 1) * cols * sizeof(float));
   }
   static constexpr size_t kBwdSmem = 216 << 10;
 };
@@ -566,7 +582,8 @@ cudaError_t bwd_launch(const RmsNormBwdArgs &a, float *part, cudaStream_t st) {
   const unsigned grid = (unsigned)std::min<int64_t>((a.rows + b.teams - 1) / b.teams, (int64_t)std::min(num_sms(), 160) * b.per_sm);
   cudaError_t e;
   if (b.vpl == 1) e = bwd_kernel<1, S, false, true>(a, b, grid, part, st);
-  else if (b.vpl == 4) e = bwd_kernel<4, S, sizeof(S) == 4, true>(a, b, grid, part, st);
+  else if (b.vpl == 4 && b.direct) e = bwd_kernel<4, float, true, true>(a, b, grid, part, st);
+  else if (b.vpl == 4) e = bwd_kernel<4, S, false, true>(a, b, grid, part, st);
   else if (sizeof(S) == 2 && b.tight) e = bwd_kernel<2, uint16_t, false, true>(a, b, grid, part, st);
   else e = bwd_kernel<2, S, false, false>(a, b, grid, part, st);
   if (e != cudaSuccess || part == nullptr) return e;
