@@ -21,8 +21,8 @@
 // no two parts share a slot.
 //
 // What bounds it: the issue of instructions.  65521 tokens of 256 experts, sigmoid: 23 us for
-// the loss, 25 us for the gradient (2.9 and 5.4 TB/s), some 240 instructions a token and warp,
-// 68% of the issue slots taken; small batches the latency of the launches (count, logits,
+// the loss, 24 us for the gradient (3.0 and 5.6 TB/s), some 200 instructions a token and warp,
+// two thirds of the issue slots taken; small batches the latency of the launches (count, logits,
 // finish; 7 to 10 us in a graph).
 #include <math.h>
 
@@ -263,11 +263,12 @@ MOE_DEVINL float both(uint64_t v) {
   return lo + hi;
 }
 
-// A token's numbers, 8 experts a lane: u = e^(x - shift), s the score before it is normalised
+// A token's numbers, V experts a lane: u = e^(x - shift), s the score before it is normalised
 // and j its derivative (softmax: u itself); their sums over the token's experts, and that of
 // f s.
+template <int V>
 struct Token {
-  uint64_t u[4], s[4], j[4];
+  uint64_t u[V / 2], s[V / 2], j[V / 2];
   float sum, size, fs, shift;
 };
 
@@ -277,11 +278,11 @@ struct Token {
 // exponential for the softmax and the sigmoid e^x / (1 + e^x).
 MOE_DEVINL bool tame_sum(float sum) { return sum >= 1e-5f && sum <= 1e7f; }
 
-template <int LPT, bool SIGMOID>
-MOE_DEVINL void token_scores(const float *x, const uint64_t *f, Token &k) {
+template <int LPT, int V, bool SIGMOID>
+MOE_DEVINL void token_scores(const float *x, const uint64_t *f, Token<V> &k) {
   uint64_t sum = 0, size = 0, fs = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < V / 2; ++i) {
     k.u[i] = exp_near(pack2(x[2 * i], x[2 * i + 1]));
     sum = add2(sum, k.u[i]);
     if (SIGMOID) {
@@ -303,18 +304,18 @@ MOE_DEVINL void token_scores(const float *x, const uint64_t *f, Token &k) {
 }
 
 // The same with the largest logit as the shift, for any logits.
-template <int LPT, bool SIGMOID>
-MOE_DEVINL void token_scores_any(const float *x, const uint64_t *f, Token &k) {
-  float v[8], s[8], j[8], m = -INFINITY, sum = 0.0f, size = 0.0f, fs = 0.0f;
+template <int LPT, int V, bool SIGMOID>
+MOE_DEVINL void token_scores_any(const float *x, const uint64_t *f, Token<V> &k) {
+  float v[V], s[V], j[V], m = -INFINITY, sum = 0.0f, size = 0.0f, fs = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < V; ++i) {
     v[i] = x[i] != x[i] ? -INFINITY : x[i];
     m = fmaxf(m, v[i]);
   }
   m = token_max<LPT>(m);
   k.shift = m > -INFINITY ? m : 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < V; ++i) {
     const float u = expf(v[i] - k.shift);
     sum += u;
     s[i] = j[i] = u;
@@ -332,7 +333,7 @@ MOE_DEVINL void token_scores_any(const float *x, const uint64_t *f, Token &k) {
     v[i] = u;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < V / 2; ++i) {
     k.u[i] = pack2(v[2 * i], v[2 * i + 1]);
     k.s[i] = pack2(s[2 * i], s[2 * i + 1]);
     k.j[i] = pack2(j[2 * i], j[2 * i + 1]);
@@ -343,7 +344,7 @@ MOE_DEVINL void token_scores_any(const float *x, const uint64_t *f, Token &k) {
 }
 
 // A row's experts of a lane: columns 4 and 4 consecutive (VEC) or LPT apart.
-template <int LPT, bool VEC>
+template <int LPT, int V, bool VEC>
 struct Columns {
   int l, E;
   MOE_DEVINL int at(int i) const { return VEC ? ((i >> 2) * LPT + l) * 4 + (i & 3) : i * LPT + l; }
@@ -351,7 +352,7 @@ struct Columns {
   MOE_DEVINL void copy(float *place, const float *row) const {
     if (VEC) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < V / 4; ++h)
         if (at(4 * h) < E)
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                            (uint32_t)__cvta_generic_to_shared(place + h * (4 * kThreads) + 4 * threadIdx.x)),
@@ -359,7 +360,7 @@ struct Columns {
                        : "memory");
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < V; ++i)
         if (at(i) < E)
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
                            (uint32_t)__cvta_generic_to_shared(place + i * kThreads + threadIdx.x)),
@@ -370,7 +371,7 @@ struct Columns {
   MOE_DEVINL void take(const float *place, float *x, bool on, float fill) const {
     if (VEC) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < V / 4; ++h) {
         const float4 w = *reinterpret_cast<const float4 *>(place + h * (4 * kThreads) + 4 * threadIdx.x);
         const bool in = on && at(4 * h) < E;
         x[4 * h] = in ? w.x : fill;
@@ -380,19 +381,19 @@ struct Columns {
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = on && at(i) < E ? place[i * kThreads + threadIdx.x] : fill;
+      for (int i = 0; i < V; ++i) x[i] = on && at(i) < E ? place[i * kThreads + threadIdx.x] : fill;
     }
   }
   MOE_DEVINL void store(float *row, const float *x) const {
     if (VEC) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < V / 4; ++h)
         if (at(4 * h) < E)
           st_v4(row + at(4 * h), make_uint4(__float_as_uint(x[4 * h]), __float_as_uint(x[4 * h + 1]),
                                             __float_as_uint(x[4 * h + 2]), __float_as_uint(x[4 * h + 3])));
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < V; ++i)
         if (at(i) < E) row[at(i)] = x[i];
     }
   }
@@ -438,27 +439,26 @@ MOE_DEVINL void count_small(const SeqAuxArgs &a, int *cell) {
   __syncthreads();
 }
 
-// One pass over the logits: a token is LPT lanes of 8 experts each, a block takes `chunk`
+// One pass over the logits: a token is LPT lanes of V experts each, a block takes `chunk`
 // consecutive tokens in steps of kWarps * 32 / LPT.  A step's logits (and the gradients that
 // are added to) come by asynchronous copies kAhead steps ahead, each lane's to a place of its
 // own: a step's chain of sums and exponentials is 0.5 us long, a load's way as long again.
 // A step that holds the end of a sequence is taken by both.
-constexpr int kAhead = 4;
 constexpr int kMaskTokens = 2048;  // of a block, kept in shared memory
-constexpr int kStage = 8 * kThreads;
-template <int LPT, bool VEC, bool SIGMOID>
-__global__ void __launch_bounds__(kThreads, 3)
+constexpr int ahead_of(int v) { return v > 8 ? 2 : 4; }
+template <int LPT, int V, bool VEC, bool SIGMOID>
+__global__ void __launch_bounds__(kThreads, V > 8 ? 2 : 3)
 seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ part,
                float2 *__restrict__ terms) {
   constexpr int kTok = 32 / LPT;  // tokens of a warp at a time
-  constexpr int kStep = kWarps * kTok;
+  constexpr int kStep = kWarps * kTok, kStage = V * kThreads, kAhead = ahead_of(V);
   extern __shared__ __align__(16) float ring[];  // logits [kAhead][kStage], then gradients
   __shared__ float s_p[kWarps][kMaxE];
   __shared__ float s_t[2][kWarps];
   __shared__ int s_n[2][kWarps];
   __shared__ uint8_t s_mask[kMaskTokens];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane / LPT;
-  const Columns<LPT, VEC> col = {lane % LPT, a.E};
+  const Columns<LPT, V, VEC> col = {lane % LPT, a.E};
   const bool sums = a.probs != nullptr, grad = a.d_logits != nullptr;
   const bool with_z = a.z_coeff != 0.0f, add = grad && a.accumulate;
   // Logits, offsets, mask and what is added to are older than the kernel before this one
@@ -498,10 +498,10 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
   for (int t = t0; t < t1;) {
     const bool of_one = b >= 0 && b < a.B;
     const int n = of_one ? ld_i32(a.tokens + b) : 0;
-    uint64_t f[4], acc2[4];
-    int count[8];
+    uint64_t f[V / 2], acc2[V / 2];
+    int count[V];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < V; ++i)
       count[i] = of_one && col.at(i) < a.E ? ld_i32(a.counts + (int64_t)b * a.E + col.at(i)) : 0;
     // where the next sequence ends, wanted after this one
     const int after = b + 1 < a.B ? ld_i32(a.offsets + b + 2) : a.T;
@@ -509,12 +509,12 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
     const float by_n = n > 0 ? 1.0f / (float)n : 0.0f;
     const float g0 = per_seq * by_n, fs = (float)a.E / (float)a.k * by_n;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < V / 2; ++i) {
       f[i] = pack2(fs * (float)count[2 * i], fs * (float)count[2 * i + 1]);
       acc2[i] = 0;
     }
     // what a token adds to the sums, and its gradient
-    auto finish = [&](const Token &k, int u, bool valid, bool on, const float *place) {
+    auto finish = [&](const Token<V> &k, int u, bool valid, bool on, const float *place) {
       // (a token that is not live, or has no logit above -inf: p = 0 and no z)
       const bool some = k.sum > 0.0f;
       const float inv = k.size > 0.0f ? rcp_f(k.size) : 0.0f, c = k.fs * inv;
@@ -522,7 +522,7 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
       if (sums) {
         const uint64_t inv2 = pack2(inv, inv);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc2[i] = fma2(k.s[i], inv2, acc2[i]);
+        for (int i = 0; i < V / 2; ++i) acc2[i] = fma2(k.s[i], inv2, acc2[i]);
         if (col.l == 0) {
           z = fmaf(lse, lse, z);
           bal = fmaf(c, by_n, bal);
@@ -533,18 +533,18 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
         const float k1 = g0 * inv, k2 = some ? gz * lse * rcp_f(k.sum) : 0.0f;
         const float k0 = SIGMOID ? -c * k1 : fmaf(-c, k1, k2);
         const uint64_t k12 = pack2(k1, k1), k22 = pack2(k2, k2), k02 = pack2(k0, k0);
-        float g[8];
+        float g[V];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < V / 2; ++i) {
           uint64_t d = mul2(fma2(f[i], k12, k02), k.j[i]);
           if (SIGMOID) d = fma2(k.u[i], k22, d);
           unpack2(d, g[2 * i], g[2 * i + 1]);
         }
         if (add) {
-          float old[8];
+          float old[V];
           col.take(place + kAhead * kStage, old, true, 0.0f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) g[i] += old[i];
+          for (int i = 0; i < V; ++i) g[i] += old[i];
         }
         col.store(a.d_logits + (int64_t)u * a.ld_d, g);
       }
@@ -567,7 +567,7 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
       return t0 + step * kStep < end;
     };
     for (bool more = true; more;) {
-      float x[8];
+      float x[V];
       int u;
       bool valid;
       const float *place;
@@ -575,8 +575,8 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
       while (more) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
         const bool on = take(x, -200.0f, u, valid, place);
-        Token k;
-        token_scores<LPT, SIGMOID>(x, f, k);
+        Token<V> k;
+        token_scores<LPT, V, SIGMOID>(x, f, k);
         odd = __any_sync(0xffffffffu, on && !tame_sum(k.sum));
         if (odd) break;
         finish(k, u, valid, on, place);
@@ -584,18 +584,18 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
       }
       if (odd) {  // a step with such logits
         const bool on = take(x, -INFINITY, u, valid, place);
-        Token k;
-        token_scores_any<LPT, SIGMOID>(x, f, k);
+        Token<V> k;
+        token_scores_any<LPT, V, SIGMOID>(x, f, k);
         finish(k, u, valid, on, place);
         more = onward();
       }
     }
-    float acc[8];
+    float acc[V];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) unpack2(acc2[i], acc[2 * i], acc[2 * i + 1]);
+    for (int i = 0; i < V / 2; ++i) unpack2(acc2[i], acc[2 * i], acc[2 * i + 1]);
     if (sums && n > 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < V; ++i) {
 #pragma unroll
         for (int o = LPT; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
         if (grp == 0 && col.at(i) < a.E) s_p[warp][col.at(i)] = acc[i];
@@ -707,9 +707,14 @@ seq_aux_finish_kernel(const SeqAuxArgs a, int chunk, int blocks, const float *__
   }
 }
 
+// Experts a lane, and lanes a token.  16 past 128 experts (half of a token's sums across lanes and
+// of its scalars: 60000 tokens of 160 28.3 us in all, with eight 30.9); fewer experts gain nothing
+// (64: 9.3 and 9.5) or lose (500 sequences of 262 tokens 27.9 and 25.5: longer steps, more of them cut).
+int experts_per_lane(int E) { return E > 128 ? 16 : 8; }
+
 int lanes_per_token(int E) {
   int l = 1;
-  while (8 * l < E) l *= 2;
+  while (experts_per_lane(E) * l < E) l *= 2;
   return l;
 }
 
@@ -744,10 +749,10 @@ bool small(const SeqAuxArgs &a) {
 }
 
 // The pass over the logits; its blocks and their tokens are left for the finish.
-template <int LPT, bool VEC, bool SIGMOID>
+template <int LPT, int V, bool VEC, bool SIGMOID>
 cudaError_t launch_pass(const SeqAuxArgs &a, const Workspace &w, int *blocks, int *chunk, cudaStream_t s) {
-  constexpr auto kernel = seq_aux_kernel<LPT, VEC, SIGMOID>;
-  constexpr size_t ring = sizeof(float) * kAhead * kStage;
+  constexpr auto kernel = seq_aux_kernel<LPT, V, VEC, SIGMOID>;
+  constexpr size_t ring = sizeof(float) * ahead_of(V) * V * kThreads;
   struct Set {
     cudaError_t status;
     int per_sm[2];  // resident blocks, without and with gradients to add to
@@ -770,17 +775,17 @@ cudaError_t launch_pass(const SeqAuxArgs &a, const Workspace &w, int *blocks, in
   return launch_dependent(kernel, *blocks, kThreads, (1 + add) * ring, s, a, *chunk, single, w.part, w.terms);
 }
 
-template <int LPT>
+template <int LPT, int V>
 cudaError_t launch_pass(const SeqAuxArgs &a, const Workspace &w, int *blocks, int *chunk, cudaStream_t s) {
   auto whole = [](const float *p, int64_t ld) {
     return p == nullptr || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 4 == 0);
   };
   const bool sigmoid = a.score_fn == MOE_SCORE_SIGMOID;
   if (a.E % 4 == 0 && whole(a.logits, a.ld) && whole(a.d_logits, a.ld_d))
-    return sigmoid ? launch_pass<LPT, true, true>(a, w, blocks, chunk, s)
-                   : launch_pass<LPT, true, false>(a, w, blocks, chunk, s);
-  return sigmoid ? launch_pass<LPT, false, true>(a, w, blocks, chunk, s)
-                 : launch_pass<LPT, false, false>(a, w, blocks, chunk, s);
+    return sigmoid ? launch_pass<LPT, V, true, true>(a, w, blocks, chunk, s)
+                   : launch_pass<LPT, V, true, false>(a, w, blocks, chunk, s);
+  return sigmoid ? launch_pass<LPT, V, false, true>(a, w, blocks, chunk, s)
+                 : launch_pass<LPT, V, false, false>(a, w, blocks, chunk, s);
 }
 
 cudaError_t launch_count(const SeqAuxArgs &a, cudaStream_t s) {
@@ -812,18 +817,20 @@ cudaError_t launch_seq_aux(const SeqAuxArgs &a, void *ws, cudaStream_t s) {
   if (a.loss != nullptr && !small(a)) e = launch_count(a, s);
   if (e != cudaSuccess) return e;
   int blocks = 0, chunk = 1;
-  switch (a.T > 0 ? lanes_per_token(a.E) : 0) {
-    case 0: break;  // no tokens
-    case 1: e = launch_pass<1>(a, w, &blocks, &chunk, s); break;
-    case 2: e = launch_pass<2>(a, w, &blocks, &chunk, s); break;
-    case 4: e = launch_pass<4>(a, w, &blocks, &chunk, s); break;
-    case 8: e = launch_pass<8>(a, w, &blocks, &chunk, s); break;
-    case 16: e = launch_pass<16>(a, w, &blocks, &chunk, s); break;
-    default: e = launch_pass<32>(a, w, &blocks, &chunk, s); break;
+  if (a.T > 0 && experts_per_lane(a.E) == 16) {
+    e = launch_pass<16, 16>(a, w, &blocks, &chunk, s);
+  } else if (a.T > 0) {
+    switch (lanes_per_token(a.E)) {
+      case 1: e = launch_pass<1, 8>(a, w, &blocks, &chunk, s); break;
+      case 2: e = launch_pass<2, 8>(a, w, &blocks, &chunk, s); break;
+      case 4: e = launch_pass<4, 8>(a, w, &blocks, &chunk, s); break;
+      case 8: e = launch_pass<8, 8>(a, w, &blocks, &chunk, s); break;
+      default: e = launch_pass<16, 8>(a, w, &blocks, &chunk, s); break;
+    }
   }
   if (e != cudaSuccess || a.loss == nullptr || small(a)) return e;
   // a sequence has blocks / B + 1 slots on average
-  const int threads = blocks / a.B < 8 ? 128 : kFinishThreads;
+  const int threads = blocks / a.B < 4 ? 128 : kFinishThreads;
   return launch_dependent(seq_aux_finish_kernel, dim3((unsigned)a.B + 1, (unsigned)((a.E + 31) / 32)),
                           threads, 0, s, a, chunk, blocks, w.part, w.terms);
 }
