@@ -197,6 +197,14 @@ def _device(stream):
     return _raw_device() if _raw_device is not None else torch.cuda.current_device()
 
 
+def _where(stream):
+    """(GPU, stream handle) that a call on `stream` (None: the current one) runs on."""
+    if stream is not None:
+        return stream.device_index, stream.cuda_stream
+    dev = _device(None)
+    return dev, _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
 def _ld(t):
     st = t.stride()
     assert len(st) >= 2, "matrices only"
@@ -635,8 +643,7 @@ def moe_rms_norm(x, residual, w, eps, h=None, y=None, codes=CODES_NONE, q=None, 
                  stream=None):
     """x bf16, residual and h bf16 or fp32, y bf16, q one-byte codes: [rows, cols]; scales: uint8
     atoms (CODES_MX) or bf16 [rows, ceil(cols / 32)] (CODES_ACT8)."""
-    _check(_native.rms_norm(x, residual, w, eps, h, y, codes, q, scales, _device(stream),
-                            _stream(stream)))
+    _check(_native.rms_norm(x, residual, w, eps, h, y, codes, q, scales, *_where(stream)))
 
 
 def moe_rms_norm_bwd_workspace_bytes(rows: int, cols: int) -> int:
@@ -647,12 +654,12 @@ def moe_rms_norm_bwd(dy, h, w, eps, dh, dw=None, workspace=None, d_residual=None
                      accumulate=False, stream=None):
     """dy and dx bf16, h, d_residual and dh bf16 or fp32: [rows, cols]; dw fp32 [cols]."""
     _check(_native.rms_norm_bwd(dy, h, w, eps, d_residual, dh, dx, dw, int(accumulate), workspace,
-                                _device(stream), _stream(stream)))
+                                *_where(stream)))
 
 
 def moe_mx_dequantize(q, sf, fmt, x, stream=None):
     """Codes q uint8 [rows, cols] with scale atoms sf (MX_ROWS_PLAIN) -> x bf16 [rows, cols]."""
-    _check(_native.mx_dequantize(q, sf, fmt, x, _device(stream), _stream(stream)))
+    _check(_native.mx_dequantize(q, sf, fmt, x, *_where(stream)))
 
 
 def moe_seq_aux_loss_workspace_bytes(T: int, E: int, B: int) -> int:
@@ -666,7 +673,7 @@ def moe_seq_aux_loss(logits, topk_idx, seq_offsets, score_fn, coeff, z_coeff, co
     tokens int32 [B], probs_mean fp32 [B, E], loss fp32 [2] and (given) d_logits fp32 [T, E]."""
     _check(_native.seq_aux_loss(logits, topk_idx, seq_offsets, token_mask, score_fn, coeff, z_coeff,
                                 counts, tokens, probs_mean, loss, d_loss, d_logits, int(accumulate),
-                                workspace, _device(stream), _stream(stream)))
+                                workspace, *_where(stream)))
 
 
 def moe_seq_aux_loss_bwd(logits, k, seq_offsets, score_fn, coeff, z_coeff, counts, tokens, d_logits,
@@ -674,7 +681,7 @@ def moe_seq_aux_loss_bwd(logits, k, seq_offsets, score_fn, coeff, z_coeff, count
     """counts and tokens as moe_seq_aux_loss wrote them -> d_logits fp32 [T, E]."""
     _check(_native.seq_aux_loss_bwd(logits, k, seq_offsets, token_mask, score_fn, coeff, z_coeff,
                                     counts, tokens, d_loss, d_logits, int(accumulate),
-                                    _device(stream), _stream(stream)))
+                                    *_where(stream)))
 
 
 class GradArg(ctypes.Structure):
@@ -703,14 +710,12 @@ def moe_clip_workspace_bytes() -> int:
 
 def moe_grad_norm(plan, chunks, scale, norm, workspace, stream=None):
     """plan: moe_clip_plan's on the device; norm fp32 [1]."""
-    _check(_native.clip_grads(plan, chunks, None, scale, norm, workspace, _device(stream),
-                              _stream(stream)))
+    _check(_native.clip_grads(plan, chunks, None, scale, norm, workspace, *_where(stream)))
 
 
 def moe_clip_grads(plan, chunks, max_norm, scale, norm, workspace, stream=None):
     """The norm, and the tensors of the plan scaled and clipped."""
-    _check(_native.clip_grads(plan, chunks, float(max_norm), scale, norm, workspace, _device(stream),
-                              _stream(stream)))
+    _check(_native.clip_grads(plan, chunks, float(max_norm), scale, norm, workspace, *_where(stream)))
 
 
 # ------------------------------------------------------------ expert parallelism

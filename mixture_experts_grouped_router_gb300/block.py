@@ -64,7 +64,7 @@ def rms_norm(x, w, eps, y=None, residual=None, h=None, codes=None, stream=None):
     one type (the residual stream's; h may be residual); w bf16 or fp32 [cols]; y bf16 or None;
     codes: a Codes8 of [rows, cols] that takes y in 8 bits, or None.  Returns y."""
     if codes is None:
-        L.moe_rms_norm(x, residual, w, eps, h, y, stream=stream)
+        L.moe_rms_norm(x, residual, w, eps, h, y, 0, None, None, stream)
     else:
         L.moe_rms_norm(x, residual, w, eps, h, y, CODES[codes.fmt], codes.q, codes.scales, stream)
     return y

@@ -1,5 +1,7 @@
 // C ABI of what a step has around the expert layer (RMS norm, balance loss of
 // sequences, gradient norm): argument validation and the launches.
+#include <string.h>
+
 #include <algorithm>
 
 #include "internal.h"
@@ -292,12 +294,14 @@ moe_status_t moe_clip_plan(const moe_grad *grads, int n, void *plan, size_t plan
   const int64_t chunks = moe_clip_plan_chunks(grads, n);
   REQUIRE(plan_bytes >= (size_t)chunks * sizeof(moe::ClipChunk) && (plan || chunks == 0),
           MOE_ERR_INVALID_ARG, "moe_clip_plan: %zu bytes for %lld chunks", plan_bytes, (long long)chunks);
-  moe::ClipChunk *c = static_cast<moe::ClipChunk *>(plan);
-  each_chunk(grads, n, [c](int64_t k, const moe_grad &t, int64_t lo, int64_t hi, int kind) {
-    c[k].g = static_cast<const char *>(t.g) + lo * elem_bytes(t.g_dtype);
-    c[k].out = static_cast<char *>(t.out) + lo * elem_bytes(t.out_dtype);
-    c[k].n = (int32_t)(hi - lo);
-    c[k].kind = kind;
+  char *to = static_cast<char *>(plan);  // (of any alignment here)
+  each_chunk(grads, n, [to](int64_t k, const moe_grad &t, int64_t lo, int64_t hi, int kind) {
+    moe::ClipChunk c = {};
+    c.g = static_cast<const char *>(t.g) + lo * elem_bytes(t.g_dtype);
+    c.out = static_cast<char *>(t.out) + lo * elem_bytes(t.out_dtype);
+    c.n = (int32_t)(hi - lo);
+    c.kind = kind;
+    memcpy(to + k * sizeof c, &c, sizeof c);
   });
   return MOE_OK;
 }
