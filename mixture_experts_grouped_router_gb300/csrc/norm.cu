@@ -514,20 +514,15 @@ cudaError_t norm_launch(const RmsNormArgs &a, cudaStream_t st) {
   return norm_launch<VPL, S, kAny>(a, W, st);
 }
 
-// Vectors a lane.  One while its warps are no more than the GPU holds, for the latency (600 x 4096:
-// 4.7 us, four vectors 5.4; of longer rows a block is most of a SM: 320 x 7168 6.0 and 5.5), and
-// for fp32 rows that it fits (2047 x 7168: 28.0 and 29.4; 8000 x 4096: 57.9 and 59.5; with 8-bit
-// codes 40 and 31).  Else four
-// (16384 x 4096: 79 us, one or two 82) but where a row has not so many (256 columns: one 73 us, four
-// 96; 512: two 80, four 83).
+// Vectors a lane, by the matrix alone, so that y is the same number with codes and without.  One
+// while its warps are some half of what the GPU holds, for the latency (1000 x 1024: 3.1 us and with
+// codes 3.4, four vectors 3.9 and 4.3; 100 x 7168 3.0 and 4.2; but 600 x 4096 with codes 6.1 and
+// 5.9).  Else four (16384 x 4096: 79 us, one or two 82) but where a row has not so many (256
+// columns: one 73 us, four 96; 512: two 80, four 83).
 template <typename S>
 cudaError_t norm_by_size(const RmsNormArgs &a, cudaStream_t st) {
-  const int64_t warps = a.rows * team_warps(a.cols, 1), sms = num_sms();
-  const bool few = a.codes != MOE_CODES_NONE ? a.rows < 2 * sms
-                   : a.cols <= 4096         ? warps <= 64 * sms
-                                            : a.rows <= sms;
-  const bool fits = sizeof(S) == 4 && a.codes == MOE_CODES_NONE && a.cols >= 4096 && a.cols % 256 == 0;
-  if (a.cols <= 8192 && (few || fits || a.cols <= 256)) return norm_launch<1, S>(a, st);
+  const bool few = a.rows * team_warps(a.cols, 1) <= 36ll * num_sms();
+  if (few ? a.cols <= 8192 : a.cols <= 256) return norm_launch<1, S>(a, st);
   if (few || a.cols <= 512) return norm_launch<2, S>(a, st);
   return norm_launch<4, S>(a, st);
 }
