@@ -443,12 +443,15 @@ MOE_DEVINL void count_small(const SeqAuxArgs &a, int *cell) {
 // consecutive tokens in steps of kWarps * 32 / LPT.  A step's logits (and the gradients that
 // are added to) come by asynchronous copies kAhead steps ahead, each lane's to a place of its
 // own: a step's chain of sums and exponentials is 0.5 us long, a load's way as long again.
-// A step that holds the end of a sequence is taken by both.
+// A step that holds the end of a sequence is taken by both.  How the tokens are dealt out: a chunk
+// a block, all to one block, or a sequence a block (and what lies before the first and behind
+// the last sequence to two more).
+enum { kChunks = 0, kOneBlock = 1, kSequences = 2 };
 constexpr int kMaskTokens = 2048;  // of a block, kept in shared memory
 constexpr int ahead_of(int v) { return v > 8 ? 2 : 4; }
 template <int LPT, int V, bool VEC, bool SIGMOID>
 __global__ void __launch_bounds__(kThreads, V > 8 ? 2 : 3)
-seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ part,
+seq_aux_kernel(const SeqAuxArgs a, int chunk, int mode, float *__restrict__ part,
                float2 *__restrict__ terms) {
   constexpr int kTok = 32 / LPT;  // tokens of a warp at a time
   constexpr int kStep = kWarps * kTok, kStage = V * kThreads, kAhead = ahead_of(V);
@@ -463,8 +466,13 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
   const bool with_z = a.z_coeff != 0.0f, add = grad && a.accumulate;
   // Logits, offsets, mask and what is added to are older than the kernel before this one
   // where that is one of this call (it waited for them); the counts are not.
-  if (!sums || single) grid_dependency_begin();
-  const int t0 = blockIdx.x * chunk, t1 = min(a.T, t0 + chunk);
+  if (!sums || mode == kOneBlock) grid_dependency_begin();
+  int t0 = blockIdx.x * chunk, t1 = min(a.T, t0 + chunk);
+  if (mode == kSequences) {
+    const int q = blockIdx.x;
+    t0 = q == a.B ? 0 : clampi(ld_i32(a.offsets + min(q, a.B)), 0, a.T);
+    t1 = q > a.B ? a.T : clampi(ld_i32(a.offsets + (q == a.B ? 0 : q + 1)), t0, a.T);
+  }
   const int mine = warp * kTok + grp;  // the lane's token of a step
   int ahead = 0;                       // the step that is copied next
   auto fetch = [&]() {
@@ -479,22 +487,31 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
   };
 #pragma unroll
   for (int k = 0; k < kAhead; ++k) fetch();
-  const bool masked = a.mask != nullptr, near_mask = chunk <= kMaskTokens;
+  const bool masked = a.mask != nullptr, near_mask = t1 - t0 <= kMaskTokens;
   if (masked && near_mask)
     for (int i = threadIdx.x; i < t1 - t0; i += kThreads) s_mask[i] = (uint8_t)ld_u8(a.mask + t0 + i);
-  if (single) count_small(a, reinterpret_cast<int *>(s_p));
-  int b = last_at_most(a.offsets, a.B + 1, t0, lane);
-  if (sums && !single) grid_dependency_begin();
+  if (mode == kOneBlock) count_small(a, reinterpret_cast<int *>(s_p));
+  int b, next;
+  if (mode == kSequences) {
+    b = (int)blockIdx.x == a.B ? -1 : min((int)blockIdx.x, a.B);
+    next = t1;
+  } else {
+    b = last_at_most(a.offsets, a.B + 1, t0, lane);
+    next = b < a.B ? ld_i32(a.offsets + b + 1) : a.T;
+  }
+  if (sums && mode != kOneBlock) grid_dependency_begin();
   int2 sn = make_int2(0, 0);
   float per_seq = 0.0f, gz = 0.0f;
-  if (grad || single) {
+  if (grad || mode == kOneBlock) {
     sn = batch_size(a.tokens, a.B, s_n);
     per_seq = a.d_loss * a.coeff / (float)max(sn.x, 1);
     gz = a.d_loss * 2.0f * a.z_coeff / (float)max(sn.y, 1);
   }
   __syncthreads();
+  if (mode == kSequences && sums && b >= 0 && b < a.B && ld_i32(a.tokens + b) <= 0)
+    for (int e = threadIdx.x; e < a.E; e += kThreads) a.probs[(int64_t)b * a.E + e] = 0.0f;
   float z = 0.0f, bal = 0.0f;
-  int next = b < a.B ? ld_i32(a.offsets + b + 1) : a.T, step = 0;
+  int step = 0;
   for (int t = t0; t < t1;) {
     const bool of_one = b >= 0 && b < a.B;
     const int n = of_one ? ld_i32(a.tokens + b) : 0;
@@ -605,7 +622,7 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
         float v = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) v += s_p[w][e];
-        if (single) a.probs[(int64_t)b * a.E + e] = v * by_n;
+        if (mode != kChunks) a.probs[(int64_t)b * a.E + e] = v * by_n;
         else part[((int64_t)blockIdx.x + b) * a.E + e] = v;
       }
       __syncthreads();
@@ -636,21 +653,21 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, bool single, float *__restrict__ p
       bal += s_t[0][w];
       z += s_t[1][w];
     }
-    if (single) write_loss(a, bal, z, sn.x, sn.y);
+    if (mode == kOneBlock) write_loss(a, bal, z, sn.x, sn.y);
     else terms[blockIdx.x] = make_float2(bal, z);
   }
 }
 
-// P of 32 experts of a sequence from its slots (block (b, group of 32)); the first block past
-// the sequences adds up the loss.
+// P of 32 experts of a sequence from its slots (block (b - first, group of 32)); the first block
+// past the sequences adds up the loss.
 constexpr int kFinishThreads = 512;  // at most
 __global__ void __launch_bounds__(kFinishThreads)
-seq_aux_finish_kernel(const SeqAuxArgs a, int chunk, int blocks, const float *__restrict__ part,
+seq_aux_finish_kernel(const SeqAuxArgs a, int first, int chunk, int blocks, const float *__restrict__ part,
                       const float2 *__restrict__ terms) {
   __shared__ float s[kFinishThreads / 32][33];
   __shared__ int s_n[2][kFinishThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kW = blockDim.x >> 5;
-  const int b = blockIdx.x, e = blockIdx.y * 32 + lane;
+  const int b = first + blockIdx.x, e = blockIdx.y * 32 + lane;
   grid_dependency_begin();
   if (b == a.B) {
     if (blockIdx.y > 0) return;
@@ -736,16 +753,22 @@ struct Workspace {
     const int step = kWarps * (32 / lanes_per_token(E));
     const size_t blocks = (size_t)std::min<int64_t>(kMaxBlocks, ((int64_t)T + step - 1) / step);
     terms = static_cast<float2 *>(p);
-    part = reinterpret_cast<float *>(terms + blocks);
-    bytes = 16 + 8 * blocks + 4 * (blocks + (size_t)B) * (size_t)E;
+    part = reinterpret_cast<float *>(terms + blocks + (size_t)B + 2);
+    bytes = 16 + 8 * (blocks + (size_t)B + 2) + 4 * (blocks + (size_t)B) * (size_t)E;
   }
 };
 
-// Whether one block takes the whole call: few logits, whose counts fit its shared memory (256
-// tokens of 8 experts 4.1 us in a graph, in three kernels 6.6; but 1000 of 16 11.4 and 7.7).
-bool small(const SeqAuxArgs &a) {
-  return a.loss != nullptr && a.T > 0 && (int64_t)a.T * a.E <= 8192 && a.T * a.k <= 4096 &&
-         (int64_t)a.B * (a.E + 1) <= kSmallCells;
+// How the tokens are dealt out.  One block takes the whole call where there are few logits, whose
+// counts fit its shared memory (256 tokens of 8 experts 4.1 us in a graph, in three kernels 6.6;
+// but 1000 of 16 11.4 and 7.7).  A block a sequence where these are shorter than half a step, as
+// each end costs a block 0.6 us (145 tokens of 16 experts in 273 sequences 161 us by chunks of 128
+// tokens), and none can be longer than 64 steps.
+int mode_of(const SeqAuxArgs &a) {
+  const int step = kWarps * (32 / lanes_per_token(a.E));
+  if (a.loss != nullptr && a.T > 0 && (int64_t)a.T * a.E <= 8192 && a.T * a.k <= 4096 && a.B <= 8 &&
+      a.B * (a.E + 1) <= kSmallCells)
+    return kOneBlock;
+  return 2ll * a.T < (int64_t)a.B * step && a.T <= 64 * step ? kSequences : kChunks;
 }
 
 // The pass over the logits; its blocks and their tokens are left for the finish.
@@ -766,13 +789,15 @@ cudaError_t launch_pass(const SeqAuxArgs &a, const Workspace &w, int *blocks, in
   });
   if (set.status != cudaSuccess) return set.status;
   const int add = a.d_logits != nullptr && a.accumulate ? 1 : 0;
-  const bool single = small(a);
+  const int mode = mode_of(a);
   split(a.T, a.E, std::max(1, set.per_sm[add]), blocks, chunk);
-  if (single) {
+  if (mode == kOneBlock) {
     *blocks = 1;
     *chunk = a.T;
+  } else if (mode == kSequences) {
+    *blocks = a.B + 2;
   }
-  return launch_dependent(kernel, *blocks, kThreads, (1 + add) * ring, s, a, *chunk, single, w.part, w.terms);
+  return launch_dependent(kernel, *blocks, kThreads, (1 + add) * ring, s, a, *chunk, mode, w.part, w.terms);
 }
 
 template <int LPT, int V>
@@ -814,7 +839,8 @@ size_t seq_aux_workspace_bytes(int T, int E, int B) { return Workspace(nullptr, 
 cudaError_t launch_seq_aux(const SeqAuxArgs &a, void *ws, cudaStream_t s) {
   const Workspace w(ws, a.T, a.E, a.B);
   cudaError_t e = cudaSuccess;
-  if (a.loss != nullptr && !small(a)) e = launch_count(a, s);
+  const int mode = mode_of(a);
+  if (a.loss != nullptr && mode != kOneBlock) e = launch_count(a, s);
   if (e != cudaSuccess) return e;
   int blocks = 0, chunk = 1;
   if (a.T > 0 && experts_per_lane(a.E) == 16) {
@@ -828,11 +854,13 @@ cudaError_t launch_seq_aux(const SeqAuxArgs &a, void *ws, cudaStream_t s) {
       default: e = launch_pass<16, 8>(a, w, &blocks, &chunk, s); break;
     }
   }
-  if (e != cudaSuccess || a.loss == nullptr || small(a)) return e;
+  if (e != cudaSuccess || a.loss == nullptr || mode == kOneBlock) return e;
+  if (mode == kSequences && a.T > 0)  // P is there
+    return launch_dependent(seq_aux_finish_kernel, 1, kFinishThreads, 0, s, a, a.B, chunk, blocks, w.part, w.terms);
   // a sequence has blocks / B + 1 slots on average
   const int threads = blocks / a.B < 4 ? 128 : kFinishThreads;
   return launch_dependent(seq_aux_finish_kernel, dim3((unsigned)a.B + 1, (unsigned)((a.E + 31) / 32)),
-                          threads, 0, s, a, chunk, blocks, w.part, w.terms);
+                          threads, 0, s, a, 0, chunk, blocks, w.part, w.terms);
 }
 
 }  // namespace moe

@@ -262,3 +262,37 @@ def test_the_gradient_is_that_of_the_last_forward(block):
     s.backward(x, off, torch.empty_like(x))
     with pytest.raises(ValueError, match="last forward"):
         s.backward(x[:5], off, torch.empty(5, 8, device="cuda"))
+
+
+@pytest.mark.parametrize("T,E,k,B", [(145, 16, 4, 273), (394, 32, 2, 180), (17, 128, 2, 166), (1, 8, 2, 40),
+                                     (60, 256, 8, 60), (2000, 8, 2, 900), (300, 33, 3, 100), (100, 8, 2, 100)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_sequences_of_few_tokens(block, T, E, k, B, masked):
+    """Sequences shorter than a step, many of them empty, and tokens on both sides of all; one that
+    holds nearly every token."""
+    for long in (False, True):
+        rng, x, idx = case(T, E, k, B + long)
+        cut = np.sort(rng.integers(0, T + 1, B + 1))
+        if long:
+            cut = np.sort(np.where(rng.random(B + 1) < 0.5, cut.min(), T - T // 8))
+        mask = rng.random(T) > 0.4 if masked else None
+        want = R.seq_aux(x, idx, cut, mask, True, 0.3, 0.05)
+        lx, off = torch.tensor(x, device="cuda"), i32(cut)
+        m = None if mask is None else torch.tensor(mask, device="cuda")
+        s = block.SeqAuxLoss(T, E, k, B, 1, 0.3, 0.05)
+        s.workspace.fill_(0xFF)
+        for t in (s.probs, s.loss):
+            t.fill_(9.0)
+        d = torch.full((T, E), 9.0, device="cuda")
+        s.forward(lx, i32(idx), off, m, d_logits=d)
+        check((s.loss, s.counts, s.tokens, s.probs, d), want, E, T)
+        d2 = torch.full((T, E), 9.0, device="cuda")
+        s.backward(lx, off, d2, m, accumulate=False)
+        assert torch.equal(d, d2)
+        base = torch.randn(T, E, device="cuda")
+        added = base.clone()
+        s.backward(lx, off, added, m, d_loss=2.0)
+        sum_ = f64(base) + 2.0 * want["d_logits"]
+        assert (np.abs(f64(added) - sum_) <= 2.0 ** -17 * want["size"] + 2.0 ** -23 * np.abs(sum_) + 1e-37).all()
+        dead = (want["d_logits"] == 0).all(1)
+        assert torch.equal(added[torch.tensor(dead, device="cuda")], base[torch.tensor(dead, device="cuda")])
