@@ -152,3 +152,22 @@ def test_a_tensor_past_32_bits(block):
     c = block.GradClip([g])
     assert float(c.clip(6.5)) == 13.0
     assert g[at].tolist() == [1.5, 2.0, 6.0] and int(torch.count_nonzero(g)) == 3
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("low,high", [(-38, 38), (-38, -10), (-20, -8), (8, 38), (-15, -13), (17, 20)])
+def test_neighbours_of_any_size(block, dtype, low, high):
+    """Values of up to 76 powers of ten side by side, some of them 0.  At most 32 squares are added
+    one after the other in fp32, which the root halves; its own and two more roundings."""
+    gen = torch.Generator(device="cuda").manual_seed(high - low)
+    e = torch.rand(20003, generator=gen, device="cuda", dtype=torch.float64) * (high - low) + low
+    sign = torch.randint(-1, 2, (20003,), generator=gen, device="cuda")
+    for n in (20003, 4099, 31, 1):
+        g = (10.0 ** e * sign)[:n].to(dtype)
+        v = f64(g)
+        norm = float(np.sqrt((v * v).sum()))
+        got = float(block.GradClip([g]).norm())
+        if norm > 3.4e38:
+            assert got == float("inf") or got >= 3.4e38 * (1 - 2.0 ** -20)
+        else:
+            assert abs(got - norm) <= 20 * 2.0 ** -24 * norm + 2.0 ** -149
