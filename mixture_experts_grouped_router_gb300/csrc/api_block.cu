@@ -81,14 +81,15 @@ static int64_t chunk_elems(const moe_grad *grads, int n) {
 }
 
 // Elements before the first where 8 of them start on their own size (16 or 32 bytes) in g and in
-// out; -1: there is none.
-static int64_t peel(const moe_grad &t) {
+// out, or, if there is none (`apart`), where g starts on 16 bytes.
+static int64_t peel(const moe_grad &t, bool *apart) {
   const int64_t gb = elem_bytes(t.g_dtype), ob = elem_bytes(t.out_dtype);
+  const uintptr_t g = reinterpret_cast<uintptr_t>(t.g), out = reinterpret_cast<uintptr_t>(t.out);
+  *apart = false;
   for (int64_t p = 0; p < 8; ++p)
-    if ((reinterpret_cast<uintptr_t>(t.g) + p * gb) % (8 * gb) == 0 &&
-        (reinterpret_cast<uintptr_t>(t.out) + p * ob) % (8 * ob) == 0)
-      return std::min(p, t.n);
-  return -1;
+    if ((g + p * gb) % (8 * gb) == 0 && (out + p * ob) % (8 * ob) == 0) return std::min(p, t.n);
+  *apart = true;
+  return std::min<int64_t>((16 - g % 16) % 16 / gb, t.n);
 }
 
 static moe_status_t check_grads(const char *who, const moe_grad *grads, int n) {
@@ -114,12 +115,12 @@ static int64_t each_chunk(const moe_grad *grads, int n, F f) {
   int64_t chunks = 0;
   for (int i = 0; i < n; ++i) {
     const moe_grad &t = grads[i];
-    const int64_t p = peel(t);
+    bool apart;
+    const int64_t p = peel(t, &apart);
     const int kind = (t.g_dtype == MOE_DTYPE_F32 ? 1 : 0) | (t.out_dtype == MOE_DTYPE_F32 ? 2 : 0);
     for (int64_t lo = 0; lo < t.n;) {
-      const bool odd = p < 0 || lo < p;
-      const int64_t hi = std::min(t.n, p > 0 && lo < p ? p : lo + size);
-      f(chunks++, t, lo, hi, kind | (odd ? 4 : 0));
+      const int64_t hi = std::min(t.n, lo < p ? p : lo + size);
+      f(chunks++, t, lo, hi, kind | (lo < p ? 4 : apart ? 4 | 8 : 0));
       lo = hi;
     }
   }

@@ -303,7 +303,7 @@ struct alignas(32) ClipChunk {  // a piece of a tensor, by the plan's own order
   const void *g;
   void *out;
   int32_t n;
-  int32_t kind;  // bit 0: g is fp32; 1: out is fp32; 2: element by element
+  int32_t kind;  // bit 0: g is fp32; 1: out is fp32; 2: out starts on no piece; 3 with 2: but g does
 };
 constexpr int kClipMaxBlocks = 2048;
 cudaError_t launch_clip(const ClipChunk *plan, int64_t chunks, float scale, float max_norm, bool write,

@@ -171,3 +171,23 @@ def test_neighbours_of_any_size(block, dtype, low, high):
             assert got == float("inf") or got >= 3.4e38 * (1 - 2.0 ** -20)
         else:
             assert abs(got - norm) <= 20 * 2.0 ** -24 * norm + 2.0 ** -149
+
+
+@pytest.mark.parametrize("n", [1, 6, 9, 255, 2047, 2049, 70001])
+@pytest.mark.parametrize("shifts", [(1, 0), (0, 1), (4, 0), (3, 5), (8, 1)], ids=str)
+@pytest.mark.parametrize("g_type,o_type", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
+def test_views_that_start_apart(block, n, shifts, g_type, o_type):
+    """Slices of a flat buffer of gradients written to tensors of their own, and the other way."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    whole = torch.randn(n + 24, generator=gen, device="cuda").to(g_type)
+    ow = torch.full((n + 24,), 9.0, dtype=o_type, device="cuda")
+    g, o = whole[shifts[0]:][:n], ow[shifts[1]:][:n]
+    v = f64(g)
+    small = torch.ones(3, device="cuda")
+    c = block.GradClip([g, small], [o, torch.empty(3, device="cuda")])
+    want, factor = R.clip([v, np.ones(3)], 0.5, 1.0)
+    assert abs(float(c.clip(0.5)) - want) <= 20 * 2.0 ** -24 * want
+    check_outs([v], [o], factor)
+    assert (ow[:shifts[1]] == 9).all() and (ow[shifts[1] + n:] == 9).all()
+    c.clip(1e9)
+    assert torch.equal(o, g.to(o_type))
