@@ -74,12 +74,12 @@ struct Histogram {
     if (a.mask == nullptr) {
       const int64_t end = (int64_t)hi * a.k;
       int64_t i = (int64_t)lo * a.k + threadIdx.x;
-      for (; i + 7 * step < end; i += 8 * step) {
-        int e[8];
+      for (; i + 15 * step < end; i += 16 * step) {
+        int e[16];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) e[u] = ld_i32(a.idx + i + u * step);
+        for (int u = 0; u < 16; ++u) e[u] = ld_i32(a.idx + i + u * step);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) add(e[u]);
+        for (int u = 0; u < 16; ++u) add(e[u]);
       }
       for (; i < end; i += 4 * step) {
         int e[4];
@@ -162,39 +162,103 @@ MOE_DEVINL int last_at_most(const int32_t *v, int n, int t, int lane) {
   return lo;
 }
 
-// A block a chunk of tokens, where a sequence may be counted by many.
+// The last j in [lo, hi) with v[j] <= t, by each lane for itself (v[lo] <= t, or lo is -1).
+MOE_DEVINL int last_between(const int32_t *v, int lo, int hi, int t) {
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (ld_i32(v + mid) <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// A block a chunk of tokens, where a sequence may be counted by many.  A chunk of one sequence is a
+// histogram; those of several look for each choice's sequence, and count in shared memory as long as
+// that has a cell for each sequence and expert.
+constexpr int kCells = kMaxE * kCols;
+constexpr int kDeep = 4;  // choices of a thread at a time
 __global__ void __launch_bounds__(kThreads)
 seq_count_chunks_kernel(const SeqAuxArgs a, int chunk) {
-  __shared__ int hist[kMaxE * kCols];
-  const int lane = threadIdx.x & 31;
+  __shared__ int hist[kCells];
+  __shared__ int s_n, s_b[2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t0 = blockIdx.x * chunk, t1 = min(a.T, t0 + chunk);
-  Histogram h = {hist, a.E};
-  h.clear();
+  for (int i = threadIdx.x; i < kCells; i += kThreads) hist[i] = 0;
+  if (threadIdx.x == 0) s_n = 0;
   // (offsets, choices and mask are older than the kernel before this one, which clears counts)
-  int b = last_at_most(a.offsets, a.B + 1, t0, lane);
+  const int choices = (t1 - t0) * a.k;
+  int e[kDeep], t[kDeep];
+  bool live[kDeep];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const int i = i0 + u * kThreads;
+      t[u] = t0 + i / a.k;
+      live[u] = i < choices && (a.mask == nullptr || ld_u8(a.mask + t[u]) != 0);
+      e[u] = i < choices ? ld_i32(a.idx + (int64_t)t0 * a.k + i) : -1;
+    }
+  };
+  load(threadIdx.x);
+  if (warp < 2) {
+    const int at = last_at_most(a.offsets, a.B + 1, warp == 0 ? t0 : t1 - 1, lane);
+    if (lane == 0) s_b[warp] = at;
+  }
   __syncthreads();
-  bool waited = false;
-  for (int t = t0; t < t1;) {
-    const int next = b < a.B ? ld_i32(a.offsets + b + 1) : a.T;
-    const int end = min(t1, max(next, t + 1));
+  const int b = s_b[0], last = s_b[1];
+  if (last <= b) {
     if (b >= 0 && b < a.B) {
-      const int n = warp_sum_i(h.count(a, t, end));
+      Histogram h = {hist, a.E};
+      int n = 0;
+      for (int i0 = threadIdx.x; i0 < choices; i0 += kDeep * kThreads) {
+        if (i0 >= kDeep * kThreads) load(i0);
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) {
+          if (!live[u]) continue;
+          h.add(e[u]);
+          n += i0 + u * kThreads == (t[u] - t0) * a.k;
+        }
+      }
+      n = warp_sum_i(n);
+      if (lane == 0 && n > 0) atomicAdd(&s_n, n);
       __syncthreads();
-      if (!waited) grid_dependency_wait();
-      waited = true;
+      grid_dependency_wait();
       for (int e = threadIdx.x; e < a.E; e += kThreads) {
         const int c = h.total(e);
         if (c > 0) atomicAdd(a.counts + (int64_t)b * a.E + e, c);
       }
-      if (lane == 0 && n > 0) atomicAdd(a.tokens + b, n);
-      if (end < t1) {
-        __syncthreads();
-        h.clear();
-        __syncthreads();
+      if (threadIdx.x == 0 && s_n > 0) atomicAdd(a.tokens + b, s_n);
+    }
+    grid_dependency_begin();
+    return;
+  }
+  const int cell_of = a.E + 1;  // a sequence's counts, and its tokens
+  const bool shared = (int64_t)(last - b + 1) * cell_of <= kCells;
+  if (!shared) grid_dependency_wait();
+  for (int i0 = threadIdx.x; i0 < choices; i0 += kDeep * kThreads) {
+    if (i0 >= kDeep * kThreads) load(i0);
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      if (!live[u]) continue;
+      const int c = last_between(a.offsets, b, last + 1, t[u]);
+      if (c < 0 || c >= a.B) continue;
+      const bool counts = (uint32_t)e[u] < (uint32_t)a.E, first = i0 + u * kThreads == (t[u] - t0) * a.k;
+      if (shared) {
+        int *cell = hist + (c - b) * cell_of;
+        if (counts) atomicAdd(cell + e[u], 1);
+        if (first) atomicAdd(cell + a.E, 1);
+      } else {
+        if (counts) atomicAdd(a.counts + (int64_t)c * a.E + e[u], 1);
+        if (first) atomicAdd(a.tokens + c, 1);
       }
     }
-    t = end;
-    if (t < t1) b = last_at_most(a.offsets, a.B + 1, t, lane);
+  }
+  if (shared) {
+    __syncthreads();
+    grid_dependency_wait();
+    for (int i = threadIdx.x; i < (last - b + 1) * cell_of; i += kThreads) {
+      const int c = i / cell_of, e = i - c * cell_of, n = hist[i];
+      if (n > 0) atomicAdd(e < a.E ? a.counts + (int64_t)(b + c) * a.E + e : a.tokens + b + c, n);
+    }
   }
   grid_dependency_begin();
 }
@@ -417,12 +481,7 @@ MOE_DEVINL void count_small(const SeqAuxArgs &a, int *cell) {
   for (int i = threadIdx.x; i < a.T * a.k; i += kThreads) {
     const int t = i / a.k, e = ld_i32(a.idx + i);
     if (a.mask != nullptr && ld_u8(a.mask + t) == 0) continue;
-    int b = -1, hi = a.B + 1;  // the last offset at or before t
-    while (hi - b > 1) {
-      const int mid = (b + hi) >> 1;
-      if (ld_i32(a.offsets + mid) <= t) b = mid;
-      else hi = mid;
-    }
+    const int b = last_between(a.offsets, -1, a.B + 1, t);
     if (b < 0 || b >= a.B) continue;
     if ((uint32_t)e < (uint32_t)a.E) atomicAdd(&cell[b * a.E + e], 1);
     if (i == t * a.k) atomicAdd(&tokens[b], 1);
@@ -448,6 +507,7 @@ MOE_DEVINL void count_small(const SeqAuxArgs &a, int *cell) {
 // the last sequence to two more).
 enum { kChunks = 0, kOneBlock = 1, kSequences = 2 };
 constexpr int kMaskTokens = 2048;  // of a block, kept in shared memory
+constexpr int kManyEnds = 3;
 constexpr int ahead_of(int v) { return v > 8 ? 2 : 4; }
 template <int LPT, int V, bool VEC, bool SIGMOID>
 __global__ void __launch_bounds__(kThreads, V > 8 ? 2 : 3)
@@ -456,7 +516,8 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, int mode, float *__restrict__ part
   constexpr int kTok = 32 / LPT;  // tokens of a warp at a time
   constexpr int kStep = kWarps * kTok, kStage = V * kThreads, kAhead = ahead_of(V);
   extern __shared__ __align__(16) float ring[];  // logits [kAhead][kStage], then gradients
-  __shared__ float s_p[kWarps][kMaxE];
+  __shared__ float s_p[V * kThreads];  // [kWarps][kMaxE] of sums, or [kStep][V * LPT] of probabilities
+  __shared__ int s_seq[kStep];
   __shared__ float s_t[2][kWarps];
   __shared__ int s_n[2][kWarps];
   __shared__ uint8_t s_mask[kMaskTokens];
@@ -512,7 +573,113 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, int mode, float *__restrict__ part
     for (int e = threadIdx.x; e < a.E; e += kThreads) a.probs[(int64_t)b * a.E + e] = 0.0f;
   float z = 0.0f, bal = 0.0f;
   int step = 0;
+  // what a token adds to the sums, and its gradient
+  auto finish_token = [&](const uint64_t *f, uint64_t *acc2, float by_n, float g0, const Token<V> &k, int u,
+                          bool valid, bool on, const float *place) {
+    // (a token that is not live, or has no logit above -inf: p = 0 and no z)
+    const bool some = k.sum > 0.0f;
+    const float inv = k.size > 0.0f ? rcp_f(k.size) : 0.0f, c = k.fs * inv;
+    const float lse = with_z && some ? k.shift + logf(k.sum) : 0.0f;
+    if (sums) {
+      const uint64_t inv2 = pack2(inv, inv);
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) acc2[i] = fma2(k.s[i], inv2, acc2[i]);
+      if (col.l == 0) {
+        z = fmaf(lse, lse, z);
+        bal = fmaf(c, by_n, bal);
+      }
+    }
+    if (grad && valid && (on || !add)) {
+      // d = k1 j (f - c) + k2 u
+      const float k1 = g0 * inv, k2 = some ? gz * lse * rcp_f(k.sum) : 0.0f;
+      const float k0 = SIGMOID ? -c * k1 : fmaf(-c, k1, k2);
+      const uint64_t k12 = pack2(k1, k1), k22 = pack2(k2, k2), k02 = pack2(k0, k0);
+      float g[V];
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        uint64_t d = mul2(fma2(f[i], k12, k02), k.j[i]);
+        if (SIGMOID) d = fma2(k.u[i], k22, d);
+        unpack2(d, g[2 * i], g[2 * i + 1]);
+      }
+      if (add) {
+        float old[V];
+        col.take(place + kAhead * kStage, old, true, 0.0f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] += old[i];
+      }
+      col.store(a.d_logits + (int64_t)u * a.ld_d, g);
+    }
+  };
   for (int t = t0; t < t1;) {
+    // Where a step holds the ends of several sequences they are taken at once, each token with the
+    // numbers of its own: an end by itself costs a block 0.6 us (65521 tokens of 256 experts, 36
+    // sequences of one token and a long one: 226 us, now 71)
+    if (mode != kSequences && next <= t0 + (step + 1) * kStep && b + 1 < a.B &&
+        ld_i32(a.offsets + b + 2) <= t0 + (step + 1) * kStep) {
+      const int step_end = min(t1, t0 + (step + 1) * kStep), u = t0 + step * kStep + mine;
+      const int last = last_at_most(a.offsets, a.B + 1, step_end, lane);
+      const int end = last >= 0 ? min(ld_i32(a.offsets + last), step_end) : 0;
+      if (last - b >= kManyEnds && end > t) {
+        const int c = last_between(a.offsets, b, last + 1, u);
+        const bool valid = u >= t && u < end;
+        const int n = c >= 0 && c < a.B ? ld_i32(a.tokens + c) : 0;
+        const float by_n = n > 0 ? 1.0f / (float)n : 0.0f;
+        const float fs = (float)a.E / (float)a.k * by_n;
+        if (col.l == 0) s_seq[mine] = valid && n > 0 ? c : -1;
+        uint64_t f[V / 2], p2[V / 2];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+          float v[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int e = col.at(2 * i + h);
+            v[h] = n > 0 && e < a.E ? fs * (float)ld_i32(a.counts + (int64_t)c * a.E + e) : 0.0f;
+          }
+          f[i] = pack2(v[0], v[1]);
+          p2[i] = 0;
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        const bool on = valid && n > 0 && (!masked || (near_mask ? s_mask[u - t0] : ld_u8(a.mask + u)) != 0);
+        const float *place = ring + (step % kAhead) * kStage;
+        float x[V];
+        col.take(place, x, on, -200.0f);
+        Token<V> k;
+        token_scores<LPT, V, SIGMOID>(x, f, k);
+        if (__any_sync(0xffffffffu, on && !tame_sum(k.sum))) {
+          col.take(place, x, on, -INFINITY);
+          token_scores_any<LPT, V, SIGMOID>(x, f, k);
+        }
+        finish_token(f, p2, by_n, per_seq * by_n, k, u, valid, on, place);
+        if (sums) {
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) {
+            float p0, p1;
+            unpack2(p2[i], p0, p1);
+            s_p[mine * (V * LPT) + col.at(2 * i)] = p0;
+            s_p[mine * (V * LPT) + col.at(2 * i + 1)] = p1;
+          }
+          __syncthreads();
+          // a sequence's sum by the thread that finds its first token
+          for (int i = threadIdx.x; i < kStep * a.E; i += kThreads) {
+            const int v = i / a.E, e = i - v * a.E, q = s_seq[v];
+            if (q < 0 || (v > 0 && s_seq[v - 1] == q)) continue;
+            float p = 0.0f;
+            for (int w = v; w < kStep && s_seq[w] == q; ++w) p += s_p[w * (V * LPT) + e];
+            if (mode != kChunks) a.probs[(int64_t)q * a.E + e] = p / (float)ld_i32(a.tokens + q);
+            else part[((int64_t)blockIdx.x + q) * a.E + e] = p;
+          }
+          __syncthreads();
+        }
+        if (end == t0 + (step + 1) * kStep) {
+          fetch();
+          ++step;
+        }
+        t = end;
+        b = last;
+        next = b < a.B ? ld_i32(a.offsets + b + 1) : a.T;
+        continue;
+      }
+    }
     const bool of_one = b >= 0 && b < a.B;
     const int n = of_one ? ld_i32(a.tokens + b) : 0;
     uint64_t f[V / 2], acc2[V / 2];
@@ -530,41 +697,8 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, int mode, float *__restrict__ part
       f[i] = pack2(fs * (float)count[2 * i], fs * (float)count[2 * i + 1]);
       acc2[i] = 0;
     }
-    // what a token adds to the sums, and its gradient
     auto finish = [&](const Token<V> &k, int u, bool valid, bool on, const float *place) {
-      // (a token that is not live, or has no logit above -inf: p = 0 and no z)
-      const bool some = k.sum > 0.0f;
-      const float inv = k.size > 0.0f ? rcp_f(k.size) : 0.0f, c = k.fs * inv;
-      const float lse = with_z && some ? k.shift + logf(k.sum) : 0.0f;
-      if (sums) {
-        const uint64_t inv2 = pack2(inv, inv);
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) acc2[i] = fma2(k.s[i], inv2, acc2[i]);
-        if (col.l == 0) {
-          z = fmaf(lse, lse, z);
-          bal = fmaf(c, by_n, bal);
-        }
-      }
-      if (grad && valid && (on || !add)) {
-        // d = k1 j (f - c) + k2 u
-        const float k1 = g0 * inv, k2 = some ? gz * lse * rcp_f(k.sum) : 0.0f;
-        const float k0 = SIGMOID ? -c * k1 : fmaf(-c, k1, k2);
-        const uint64_t k12 = pack2(k1, k1), k22 = pack2(k2, k2), k02 = pack2(k0, k0);
-        float g[V];
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-          uint64_t d = mul2(fma2(f[i], k12, k02), k.j[i]);
-          if (SIGMOID) d = fma2(k.u[i], k22, d);
-          unpack2(d, g[2 * i], g[2 * i + 1]);
-        }
-        if (add) {
-          float old[V];
-          col.take(place + kAhead * kStage, old, true, 0.0f);
-#pragma unroll
-          for (int i = 0; i < V; ++i) g[i] += old[i];
-        }
-        col.store(a.d_logits + (int64_t)u * a.ld_d, g);
-      }
+      finish_token(f, acc2, by_n, g0, k, u, valid, on, place);
     };
     // the logits of the lane's token of this step, `fill` where it is not live or not of this sequence
     auto take = [&](float *x, float fill, int &u, bool &valid, const float *&place) -> bool {
@@ -615,13 +749,13 @@ seq_aux_kernel(const SeqAuxArgs a, int chunk, int mode, float *__restrict__ part
       for (int i = 0; i < V; ++i) {
 #pragma unroll
         for (int o = LPT; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-        if (grp == 0 && col.at(i) < a.E) s_p[warp][col.at(i)] = acc[i];
+        if (grp == 0 && col.at(i) < a.E) s_p[warp * kMaxE + col.at(i)] = acc[i];
       }
       __syncthreads();
       for (int e = threadIdx.x; e < a.E; e += kThreads) {
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += s_p[w][e];
+        for (int w = 0; w < kWarps; ++w) v += s_p[w * kMaxE + e];
         if (mode != kChunks) a.probs[(int64_t)b * a.E + e] = v * by_n;
         else part[((int64_t)blockIdx.x + b) * a.E + e] = v;
       }
@@ -815,18 +949,20 @@ cudaError_t launch_pass(const SeqAuxArgs &a, const Workspace &w, int *blocks, in
 
 cudaError_t launch_count(const SeqAuxArgs &a, cudaStream_t s) {
   const int64_t choices = (int64_t)a.T * a.k;
-  // A block a sequence where none can have many choices, or few have (one launch less: 4096 tokens
-  // of 8 choices in 4 sequences 9.0 us in all and not 9.8; but 8192 in 2, of 32768 each, 15.4 and
-  // 10.1); else chunks, whose counts meet in atomics
+  // A block a sequence where none can have many choices, or few have: one launch less, 2 us, which
+  // a sequence of most of 2^17 choices pays back (131072 tokens of 500 sequences 24.6 us in all by
+  // sequences and 27.4 by chunks, 69 and 36 if all but a few lie in one; 100000 of 20000 138 and 104;
+  // 8192 of 8 choices in 2 15.4 and 10.1).  Else chunks, whose counts meet in atomics.
   const int64_t each = choices / a.B;
-  if (choices <= (1 << 13) || (choices <= (1 << 15) && each <= (1 << 13)) || (choices <= (1 << 17) && each <= (1 << 11)))
+  if (choices <= (1 << 13) || (choices <= (1 << 15) && each <= (1 << 13)) ||
+      (choices <= (1 << 17) && each >= 128 && each <= (1 << 11)))
     return launch_dependent(seq_count_kernel, (unsigned)a.B, each <= 1024 ? 256 : kCountThreads, 0, s, a);
   const int64_t cells = (int64_t)a.B * (a.E + 1);
   const unsigned zero = (unsigned)std::min<int64_t>((cells + kThreads - 1) / kThreads, num_sms());
   const cudaError_t e = launch_dependent(seq_zero_kernel, zero, kThreads, 0, s, a);
   if (e != cudaSuccess) return e;
-  // tokens of a block: 2048 choices, more where that is over four blocks a SM
-  const int64_t most = 4ll * num_sms(), least = (2048 + a.k - 1) / a.k;
+  // tokens of a block: 512 choices (2048: 55.5 us of 65521 tokens of 8, not 52.6), more where that is over four blocks a SM
+  const int64_t most = 4ll * num_sms(), least = (512 + a.k - 1) / a.k;
   const int64_t chunk = std::max(least, (a.T + most - 1) / most);
   return launch_dependent(seq_count_chunks_kernel, (unsigned)((a.T + chunk - 1) / chunk), kThreads, 0, s,
                           a, (int)chunk);
@@ -857,8 +993,9 @@ cudaError_t launch_seq_aux(const SeqAuxArgs &a, void *ws, cudaStream_t s) {
   if (e != cudaSuccess || a.loss == nullptr || mode == kOneBlock) return e;
   if (mode == kSequences && a.T > 0)  // P is there
     return launch_dependent(seq_aux_finish_kernel, 1, kFinishThreads, 0, s, a, a.B, chunk, blocks, w.part, w.terms);
-  // a sequence has blocks / B + 1 slots on average
-  const int threads = blocks / a.B < 4 ? 128 : kFinishThreads;
+  // a sequence has blocks / B + 1 slots on average (but one may have nearly all: with 128 threads
+  // 131072 tokens of which one of 500 sequences has most took 50 us, 36 with 256)
+  const int threads = blocks / a.B < 4 ? 256 : kFinishThreads;
   return launch_dependent(seq_aux_finish_kernel, dim3((unsigned)a.B + 1, (unsigned)((a.E + 31) / 32)),
                           threads, 0, s, a, 0, chunk, blocks, w.part, w.terms);
 }

@@ -296,3 +296,48 @@ def test_sequences_of_few_tokens(block, T, E, k, B, masked):
         assert (np.abs(f64(added) - sum_) <= 2.0 ** -17 * want["size"] + 2.0 ** -23 * np.abs(sum_) + 1e-37).all()
         dead = (want["d_logits"] == 0).all(1)
         assert torch.equal(added[torch.tensor(dead, device="cuda")], base[torch.tensor(dead, device="cuda")])
+
+
+def ragged(rng, T, kind):
+    """Offsets of a batch with runs of sequences of no, one or a few tokens among long ones."""
+    lens = {"few": lambda: int(rng.integers(0, 4)), "mixed": lambda: int(rng.choice([0, 0, 1, 1, 2, 5, 17, 300])),
+            "ones": lambda: 1}[kind]
+    cut = [int(rng.integers(0, 3))]
+    if kind == "ones":
+        cut += [cut[0] + T // 3]
+    while cut[-1] < T - 2 and len(cut) < 3000:
+        cut.append(min(T, cut[-1] + lens()))
+    if kind == "ones" and T > 1000:  # and a long one behind them
+        cut = [c for c in cut if c < T // 3 + 400] + [T]
+    return np.array(cut)
+
+
+@pytest.mark.parametrize("T,E,k", [(700, 8, 2), (3001, 16, 1), (2500, 30, 4), (1500, 64, 6), (900, 100, 2),
+                                   (800, 160, 8), (1203, 256, 8), (40000, 8, 4)])
+@pytest.mark.parametrize("kind", ["few", "mixed", "ones"])
+@pytest.mark.parametrize("sigmoid,masked,odd", [(0, True, False), (1, False, True), (1, True, False)])
+def test_short_sequences_among_long_ones(block, T, E, k, kind, sigmoid, masked, odd):
+    rng, x, idx = case(T, E, k, len(kind))
+    cut = ragged(rng, T, kind)
+    B = len(cut) - 1
+    mask = rng.random(T) > 0.4 if masked else None
+    if odd:  # logits far from 0, which a step takes in another way
+        x[::97] += 30.0
+    m = None if mask is None else torch.tensor(mask, device="cuda")
+    want = R.seq_aux(x, idx, cut, mask, bool(sigmoid), 0.3, 0.0 if odd else 0.05)
+    lx, li, off = torch.tensor(x, device="cuda"), i32(idx), i32(cut)
+    s = block.SeqAuxLoss(T, E, k, B, sigmoid, 0.3, 0.0 if odd else 0.05)
+    s.workspace.fill_(0xFF)
+    d = torch.full((T, E), 9.0, device="cuda")
+    s.forward(lx, li, off, m, d_logits=d)
+    check((s.loss, s.counts, s.tokens, s.probs, d), want, E, T)
+    first = [t.clone() for t in (s.loss, s.counts, s.tokens, s.probs)]
+    d2 = torch.full_like(d, 9.0)
+    s.backward(lx, off, d2, m, accumulate=False)
+    assert torch.equal(d, d2)
+    base = torch.randn(T, E, device="cuda")
+    d3 = base.clone()
+    s.forward(lx, li, off, m, d_logits=d3, d_loss=-2.0, accumulate=True)
+    assert all(torch.equal(a, b) for a, b in zip(first, (s.loss, s.counts, s.tokens, s.probs)))
+    sum_ = f64(base) - 2.0 * want["d_logits"]
+    assert (np.abs(f64(d3) - sum_) <= 2.0 ** -17 * want["size"] + 2.0 ** -23 * np.abs(sum_) + 1e-37).all()
