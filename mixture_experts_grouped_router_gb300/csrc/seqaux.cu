@@ -20,10 +20,9 @@
 // b) of the workspace: both grow along the tokens, one at least from part to part, so that
 // no two parts share a slot.
 //
-// What bounds it: the issue of instructions.  65521 tokens of 256 experts, sigmoid: 23 us for
-// the loss, 24 us for the gradient (3.0 and 5.6 TB/s), some 200 instructions a token and warp,
-// two thirds of the issue slots taken; small batches the latency of the launches (count, logits,
-// finish; 7 to 10 us in a graph).
+// What bounds it: a step's instructions and their chain.  65521 tokens of 256 experts, sigmoid: 23 us
+// for the loss, 25 us for the gradient (3.0 and 5.3 TB/s), some 175 warp instructions a token at 16
+// warps a SM; small batches the latency of the launches (count, logits, finish; 7 to 10 us in a graph).
 #include <math.h>
 
 #include <algorithm>
