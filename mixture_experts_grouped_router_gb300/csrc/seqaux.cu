@@ -29,6 +29,7 @@
 
 #include "internal.h"
 #include "lowbit.cuh"
+#include "seqaux_layout.h"
 
 namespace moe {
 namespace {
@@ -871,9 +872,11 @@ int lanes_per_token(int E) {
   return l;
 }
 
+int tokens_per_step(int E) { return kWarps * (32 / lanes_per_token(E)); }
+
 // Blocks of the pass over the logits (one wave), and the tokens of each.
 void split(int T, int E, int per_sm, int *blocks, int *chunk) {
-  const int step = kWarps * (32 / lanes_per_token(E));
+  const int step = tokens_per_step(E);
   const int most = std::min(kMaxBlocks, per_sm * num_sms());
   const int64_t steps = ((int64_t)T + step - 1) / step;
   const int64_t each = std::max<int64_t>(1, (steps + most - 1) / most);
@@ -881,17 +884,15 @@ void split(int T, int E, int per_sm, int *blocks, int *chunk) {
   *blocks = (int)((steps + each - 1) / each);
 }
 
-struct Workspace {
+// The workspace of a call (of the bytes that it is asked for, whatever its address).
+struct Workspace : SeqAuxLayout {
   float *part;
   float2 *terms;
-  size_t bytes;
-  Workspace(void *p, int T, int E, int B) {
-    const int step = kWarps * (32 / lanes_per_token(E));
-    const size_t blocks = (size_t)std::min<int64_t>(kMaxBlocks, ((int64_t)T + step - 1) / step);
-    terms = static_cast<float2 *>(p);
-    part = reinterpret_cast<float *>(terms + blocks + (size_t)B + 2);
-    bytes = 16 + 8 * (blocks + (size_t)B + 2) + 4 * (blocks + (size_t)B) * (size_t)E;
-  }
+  Workspace(void *p, int T, int E, int B)
+      : SeqAuxLayout(p, std::min<int64_t>(kMaxBlocks, ((int64_t)T + tokens_per_step(E) - 1) / tokens_per_step(E)),
+                     E, B),
+        part(static_cast<float *>(part_at)),
+        terms(static_cast<float2 *>(terms_at)) {}
 };
 
 // How the tokens are dealt out.  One block takes the whole call where there are few logits, whose
@@ -900,7 +901,7 @@ struct Workspace {
 // each end costs a block 0.6 us (145 tokens of 16 experts in 273 sequences 161 us by chunks of 128
 // tokens), and none can be longer than 64 steps.
 int mode_of(const SeqAuxArgs &a) {
-  const int step = kWarps * (32 / lanes_per_token(a.E));
+  const int step = tokens_per_step(a.E);
   if (a.loss != nullptr && a.T > 0 && (int64_t)a.T * a.E <= 8192 && a.T * a.k <= 4096 && a.B <= 8 &&
       a.B * (a.E + 1) <= kSmallCells)
     return kOneBlock;
