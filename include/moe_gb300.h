@@ -811,7 +811,8 @@ moe_status_t moe_rms_norm(const uint16_t *x, int64_t ldx, const void *residual, 
  *   workspace   moe_rms_norm_bwd_workspace_bytes(rows, cols) bytes, 16-byte aligned (where
  *               dw is given); contents on entry are ignored
  * Sums in a fixed order: the result does not vary between runs.  No rows: dw = 0 (kept
- * when accumulating).
+ * when accumulating).  A row whose squares pass fp32's range (zeros in y): dh = d_residual,
+ * and nothing for dw.
  */
 size_t moe_rms_norm_bwd_workspace_bytes(int64_t rows, int cols);
 moe_status_t moe_rms_norm_bwd(const uint16_t *dy, int64_t ld_dy, const void *h, int64_t ldh,

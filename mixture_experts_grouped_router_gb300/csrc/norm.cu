@@ -398,8 +398,11 @@ rms_norm_bwd_kernel(const RmsNormBwdArgs a, int W, int teams, int stages, float 
       gh = warp_sum(t.lane < W ? red[turn][1][t.id * W + t.lane] : 0.0f);
     }
     const float r = rsqrtf(ss / (float)a.cols + a.eps);
-    const float s3 = -(r * r * r * (gh / (float)a.cols));
-    const uint64_t r2 = pack2(r, r), s2 = pack2(s3, s3);
+    // dh = r g + m (h r) + d_residual: h r and r mean(g h) are of ordinary size for any eps, r^3 is
+    // not (a row of zeros, eps under 2e-26: infinity times 0).  r = 0: the squares pass fp32's range,
+    // the forward's y is constant there, and the mean, which may be no number, is left out.
+    const float m = r == 0.0f ? 0.0f : -(r * (r * (gh / (float)a.cols)));
+    const uint64_t r2 = pack2(r, r), m2 = pack2(m, m);
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       const int c = c0 + 256 * v;
@@ -411,8 +414,9 @@ rms_norm_bwd_kernel(const RmsNormBwdArgs a, int W, int teams, int stages, float 
       Pairs d = rv[v].get();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        dw[v].p[i] = fma2(g.p[i], mul2(f.p[i], r2), dw[v].p[i]);
-        d.p[i] = add2(fma2(s2, f.p[i], mul2(mul2(g.p[i], w.p[i]), r2)), d.p[i]);
+        const uint64_t n = mul2(f.p[i], r2);
+        dw[v].p[i] = fma2(g.p[i], n, dw[v].p[i]);
+        d.p[i] = add2(fma2(m2, n, mul2(mul2(g.p[i], w.p[i]), r2)), d.p[i]);
       }
       if (in(v)) {
         Vec8<S, false> o;

@@ -285,3 +285,58 @@ def test_rows_past_32_bit_offsets(block):
     assert torch.equal(y, want)
     block.rms_norm(x, w, EPS, x)
     assert torch.equal(x, want)
+
+
+@pytest.mark.parametrize("cols", [256, 1000, 4096, 5000, 16384])
+@pytest.mark.parametrize("stream", ["bf16", "fp32"])
+@pytest.mark.parametrize("eps", [1e-20, 1e-30, 1e-37])
+def test_small_eps(block, cols, stream, eps):
+    """Rows of zeros and of values about the root of eps, where the reciprocal root's third power
+    passes fp32's range.  Tolerances as above."""
+    rows = 9
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    st, eps = TYPES[stream], float(np.float32(eps))
+    h = torch.randn(rows, cols, generator=g, device="cuda", dtype=torch.float64)
+    h *= torch.tensor([1, 0, eps ** 0.5, 0.1 * eps ** 0.5, 30 * eps ** 0.5, 0, 1e-3, 0, 1], device="cuda",
+                      dtype=torch.float64)[:, None]
+    h[7, 3] = eps ** 0.5
+    h = h.to(st)
+    w = 1.0 + 0.1 * torch.randn(cols, generator=g, device="cuda")
+    dy = (0.1 * torch.randn(rows, cols, generator=g, device="cuda")).bfloat16()
+    res = torch.randn(rows, cols, generator=g, device="cuda").to(st)
+    y, dh, dw = torch.empty_like(dy), torch.empty_like(h), torch.empty(cols, device="cuda")
+    block.rms_norm(None, w, eps, y, residual=h)
+    block.rms_norm_bwd(dy, h, w, eps, dh, dw, block.rms_norm_bwd_workspace(rows, cols), d_residual=res)
+    hv, wv, dv, rv = f64(h), f64(w), f64(dy), f64(res)
+    want, r = R.rms_norm(hv, wv, eps)
+    assert (np.abs(f64(y) - want) <= half_step(want, torch.bfloat16) + 2.0 ** -18 * np.abs(want)).all()
+    want, want_dw = R.rms_norm_bwd(dv, hv, wv, eps, rv)
+    gr = np.abs(dv * wv) * r
+    terms = gr + r * np.abs(hv) * r * r * np.abs(dv * wv * hv).mean(1, keepdims=True) + np.abs(rv)
+    assert (np.abs(f64(dh) - want) <= half_step(want, st) + 2.0 ** -18 * terms).all()
+    assert (np.abs(f64(dw) - want_dw) <= 2.0 ** -16 * np.abs(dv * hv * r).sum(0)).all()
+
+
+@pytest.mark.parametrize("cols", [256, 4096, 16384])
+@pytest.mark.parametrize("stream", ["bf16", "fp32"])
+def test_backward_of_rows_past_fp32(block, cols, stream):
+    """Rows whose squares pass fp32's range read as zeros in y: nothing but d_residual reaches them,
+    and they add nothing to dw."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    st = TYPES[stream]
+    h = torch.randn(4, cols, generator=g, device="cuda")
+    h[1] = 3e38 * torch.sign(h[1])
+    h[2, 7] = 2e19
+    h = h.to(st)
+    w = torch.ones(cols, device="cuda")
+    dy = (10.0 * torch.randn(4, cols, generator=g, device="cuda")).bfloat16()
+    res = torch.randn(4, cols, generator=g, device="cuda").to(st)
+    y, dh, dw = torch.empty_like(dy), torch.empty_like(h), torch.empty(cols, device="cuda")
+    ws = block.rms_norm_bwd_workspace(4, cols)
+    block.rms_norm(None, w, EPS, y, residual=h)
+    block.rms_norm_bwd(dy, h, w, EPS, dh, dw, ws, d_residual=res)
+    assert (y[1:3] == 0).all() and torch.equal(dh[1:3], res[1:3])
+    hv, dv = f64(h)[::3], f64(dy)[::3]
+    _, want_dw = R.rms_norm_bwd(dv, hv, f64(w), EPS)
+    size = np.abs(dv * hv / np.sqrt((hv * hv).mean(1, keepdims=True) + EPS)).sum(0)
+    assert (np.abs(f64(dw) - want_dw) <= 2.0 ** -16 * size).all()
