@@ -11,6 +11,8 @@
 // HBM bounds both: 1.41 G bf16 gradients take 405 us (7.0 TB/s) to square and 885 us (6.4 TB/s of
 // reads and writes) to scale, 1244 us at the measured copy's rate; loads that wait for the
 // arithmetic of the ones before them took 668 and 887.
+#include <float.h>
+
 #include <algorithm>
 
 #include "common.cuh"
@@ -219,8 +221,9 @@ MOE_DEVINL double total_of(const double *part, int parts, double *s) {
   return block_sum(v, s);
 }
 
-// The norm, and the factor that clips (a norm that is infinite or no number: none).  In fp32
-// where everything is well inside its range: a 64-bit root and quotient take 2 us.
+// The norm, and the factor that clips (a norm that is infinite in fp32, as the caller reads it, or no
+// number: none).  In fp32 where everything is well inside its range: a 64-bit root and quotient
+// take 2 us.
 MOE_DEVINL float norm_of(double sum, float scale, float &factor, float max_norm) {
   if (sum >= 1e-30 && sum <= 1e30 && scale >= 1e-15f && scale <= 1e15f) {
     const float total = scale * sqrtf((float)sum), q = max_norm / (total + 1e-6f);
@@ -228,8 +231,9 @@ MOE_DEVINL float norm_of(double sum, float scale, float &factor, float max_norm)
     return total;
   }
   const double total = (double)scale * sqrt(sum), q = (double)max_norm / (total + 1e-6);
-  factor = total <= 1.7e308 && q < 1.0 ? (float)((double)scale * q) : scale;
-  return (float)total;
+  const float norm = (float)total;
+  factor = norm <= FLT_MAX && q < 1.0 ? (float)((double)scale * q) : scale;
+  return norm;
 }
 
 // Piece j of a chunk, scaled, to its place.

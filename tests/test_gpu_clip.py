@@ -191,3 +191,14 @@ def test_views_that_start_apart(block, n, shifts, g_type, o_type):
     assert (ow[:shifts[1]] == 9).all() and (ow[shifts[1] + n:] == 9).all()
     c.clip(1e9)
     assert torch.equal(o, g.to(o_type))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_norm_past_fp32_clips_nothing(block, dtype):
+    """The norm that is returned is infinite: nothing is clipped, as where a gradient is."""
+    g = torch.full((3000,), 3e38, device="cuda").to(dtype)
+    g[::7] = 1.0
+    before = g.clone()
+    assert float(block.GradClip([g]).clip(1.0)) == float("inf") and torch.equal(g, before)
+    out = torch.empty_like(g)
+    assert float(block.GradClip([g], [out]).clip(1.0, 0.5)) == float("inf") and torch.equal(out, 0.5 * g)
