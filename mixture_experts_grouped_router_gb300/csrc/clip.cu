@@ -12,6 +12,7 @@
 // reads and writes) to scale, 1244 us at the measured copy's rate; loads that wait for the
 // arithmetic of the ones before them took 668 and 887.
 #include <float.h>
+#include <math.h>
 
 #include <algorithm>
 
@@ -221,27 +222,37 @@ MOE_DEVINL double total_of(const double *part, int parts, double *s) {
   return block_sum(v, s);
 }
 
+// out = (g before) by.  A factor that fp32 holds with few bits or not at all (the norm of large
+// gradients, a small max_norm) has a power of two taken out, which g is multiplied with first: that is
+// exact but for elements whose output vanishes.
+struct Factor {
+  float by, before;
+};
+
 // The norm, and the factor that clips (a norm that is infinite in fp32, as the caller reads it, or no
 // number: none).  In fp32 where everything is well inside its range: a 64-bit root and quotient
 // take 2 us.
-MOE_DEVINL float norm_of(double sum, float scale, float &factor, float max_norm) {
+MOE_DEVINL float norm_of(double sum, float scale, float max_norm, Factor &f) {
   if (sum >= 1e-30 && sum <= 1e30 && scale >= 1e-15f && scale <= 1e15f) {
     const float total = scale * sqrtf((float)sum), q = max_norm / (total + 1e-6f);
-    factor = q < 1.0f ? scale * q : scale;
-    return total;
+    f = {q < 1.0f ? scale * q : scale, 1.0f};
+    if (f.by >= 0x1p-64f) return total;
   }
   const double total = (double)scale * sqrt(sum), q = (double)max_norm / (total + 1e-6);
   const float norm = (float)total;
-  factor = norm <= FLT_MAX && q < 1.0 ? (float)((double)scale * q) : scale;
+  const double by = norm <= FLT_MAX && q < 1.0 ? (double)scale * q : (double)scale;
+  if (by >= 0x1p-100) f = {(float)by, 1.0f};
+  else if (by >= 0x1p-160) f = {(float)(by * 0x1p64), 0x1p-64f};
+  else f = {(float)(by * 0x1p126), 0x1p-126f};
   return norm;
 }
 
 // Piece j of a chunk, scaled, to its place.
-MOE_DEVINL void scale_piece(const ClipChunk &c, int j, const uint4 &w, float f) {
+MOE_DEVINL void scale_piece(const ClipChunk &c, int j, const uint4 &w, const Factor &f) {
   float v[8];
   values(w, c.kind & 1, v);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] *= f;  // (fp32: the last four are no values)
+  for (int e = 0; e < 8; ++e) v[e] = v[e] * f.before * f.by;  // (fp32: the last four are no values)
   if (c.kind & 1) {
     if (c.kind & 2) {
       st_v4(static_cast<float *>(c.out) + 4 * j,
@@ -262,7 +273,7 @@ MOE_DEVINL void scale_piece(const ClipChunk &c, int j, const uint4 &w, float f) 
 // lanes copied them, element by element in order.  100 M bf16 clipped to bf16: 118 us, 99 where both
 // start alike, 913 with elements that are read one by one.
 template <typename G, typename O>
-MOE_DEVINL void scale_in_order(const Steps<true> &at, const uint8_t *row, float f, int lane) {
+MOE_DEVINL void scale_in_order(const Steps<true> &at, const uint8_t *row, const Factor &f, int lane) {
   constexpr int kN = 16 / (int)sizeof(G);
 #pragma unroll
   for (int u = 0; u < kPieces; ++u) {
@@ -273,8 +284,8 @@ MOE_DEVINL void scale_in_order(const Steps<true> &at, const uint8_t *row, float 
     for (int e = 0; e < kN; ++e) {
       const int j = 32 * e + lane;
       if (j < left) {
-        if constexpr (sizeof(O) == 4) to[j] = (float)from[j] * f;
-        else to[j] = __float2bfloat16_rn((float)from[j] * f);
+        if constexpr (sizeof(O) == 4) to[j] = (float)from[j] * f.before * f.by;
+        else to[j] = __float2bfloat16_rn((float)from[j] * f.before * f.by);
       }
     }
   }
@@ -285,7 +296,7 @@ grad_scale_kernel(const ClipChunk *__restrict__ plan, int64_t chunks, const doub
                   int parts, float scale, float max_norm, float *__restrict__ norm) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ double s[kThreads];
-  __shared__ float s_f;
+  __shared__ Factor s_f;
   const int lane = threadIdx.x & 31;
   uint8_t *mine = ring + threadIdx.x * 16;
   const int64_t first = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), stride = (int64_t)gridDim.x * kWarps;
@@ -296,12 +307,12 @@ grad_scale_kernel(const ClipChunk *__restrict__ plan, int64_t chunks, const doub
   grid_dependency_begin();
   const double sum = total_of(part, parts, s);
   if (threadIdx.x == 0) {
-    const float total = norm_of(sum, scale, s_f, max_norm);
+    const float total = norm_of(sum, scale, max_norm, s_f);
     if (blockIdx.x == 0) *norm = total;
   }
   __syncthreads();
-  const float f = s_f;
-  if (f == 1.0f) {  // only what is not in place
+  const Factor f = s_f;
+  if (f.by == 1.0f) {  // only what is not in place
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     in = out = Steps<true>(plan, first, chunks, stride, true);
 #pragma unroll
@@ -331,7 +342,7 @@ grad_scale_kernel(const ClipChunk *__restrict__ plan, int64_t chunks, const doub
     }
     if (out.step()) {
       for (int i = out.rest() + lane; i < out.c.n; i += 32) {
-        const float v = load_one(out.c, i) * f;
+        const float v = load_one(out.c, i) * f.before * f.by;
         if (out.c.kind & 2) static_cast<float *>(out.c.out)[i] = v;
         else static_cast<bf16_t *>(out.c.out)[i] = __float2bfloat16_rn(v);
       }
@@ -348,8 +359,8 @@ grad_norm_kernel(const double *__restrict__ part, int parts, float scale, float 
   __shared__ double s[kThreads];
   grid_dependency_begin();
   const double sum = total_of(part, parts, s);
-  float factor;
-  if (threadIdx.x == 0) *norm = norm_of(sum, scale, factor, 0.0f);
+  Factor none;
+  if (threadIdx.x == 0) *norm = norm_of(sum, scale, INFINITY, none);
 }
 
 }  // namespace

@@ -202,3 +202,39 @@ def test_a_norm_past_fp32_clips_nothing(block, dtype):
     assert float(block.GradClip([g]).clip(1.0)) == float("inf") and torch.equal(g, before)
     out = torch.empty_like(g)
     assert float(block.GradClip([g], [out]).clip(1.0, 0.5)) == float("inf") and torch.equal(out, 0.5 * g)
+
+
+@pytest.mark.parametrize("g_type,o_type", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
+@pytest.mark.parametrize("size,scale,most", [(1e36, 1.0, 1e-3), (1e38, 2.0 ** -3, 1e-2), (1e14, 1.0, 1e-30),
+                                             (1e30, 1e-30, 1e-15), (3e37, 1e-8, 1e-12), (1e20, 1.0, 1e-19)])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_factors_under_fp32(block, g_type, o_type, size, scale, most, shift):
+    """Factors that fp32 holds with few bits or not at all, of gradients large enough that the
+    clipped ones are ordinary numbers; also into a tensor that starts apart.  The norm's error and one
+    half-ulp more, as elsewhere: 2^-20."""
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    n = 5003
+    g = (size * torch.randn(n, generator=gen, device="cuda").clamp(-2, 2)).to(g_type)
+    g[5], g[6] = 0.0, 1e-30
+    whole = torch.empty(n + 8, dtype=o_type, device="cuda")
+    v, s = f64(g), float(np.float32(scale))
+    c = block.GradClip([g], [whole[shift:shift + n]])
+    norm, factor = R.clip([v], float(np.float32(most)), s)
+    got = float(c.clip(most, scale))
+    if norm > 3.402823466e38:  # as documented: infinite, and not clipped
+        assert got == float("inf")
+        factor = s
+    else:
+        assert abs(got - norm) <= 20 * 2.0 ** -24 * norm
+    check_outs([v], [whole[shift:shift + n]], factor)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_scale_that_brings_the_norm_back(block, dtype):
+    """The norm of these values is past fp32, the scaled one is not: clipped, by a factor under fp32."""
+    g = torch.full((3000,), 3e38, device="cuda").to(dtype)
+    g[::7] = 1.0
+    out = torch.empty_like(g)
+    want, factor = R.clip([f64(g)], 1.0, 2.0 ** -20)  # a scale that brings it back
+    assert abs(float(block.GradClip([g], [out]).clip(1.0, 2.0 ** -20)) - want) <= 20 * 2.0 ** -24 * want
+    check_outs([f64(g)], [out], factor)
