@@ -52,7 +52,8 @@ class Codes8:
         if self.fmt == "mx":
             L.moe_mx_dequantize(self.q, self.scales, L.FP8_E4M3, out, stream)
         else:
-            L._need_device("out", out, stream)
+            for name, t in (("q", self.q), ("scales", self.scales), ("out", out)):
+                L._need_device(name, t, stream)
             L.moe_act8_dequantize(self.q, self.scales, out, None, stream)
         return out
 

@@ -340,3 +340,16 @@ def test_tensors_that_share_memory(block):
                         ([Gpu0(4096, 1000), b], [Gpu0(9000, 1000), Gpu0(4700, 100)])):
         with pytest.raises(ValueError, match="shares memory"):
             apart(grads, outs)
+
+
+def test_codes_on_another_device(block):
+    """Codes that were made on the host are not read by a call on GPU 0."""
+    class Out:  # stands for a bf16 tensor [3, 128] on GPU 0, up to the call itself
+        shape, dtype, device, is_cuda = (3, 128), torch.bfloat16, "cuda:0", True
+        get_device = staticmethod(lambda: 0)
+        stride = staticmethod(lambda: (128, 1))
+        is_contiguous = staticmethod(lambda: True)
+        data_ptr = staticmethod(lambda: 4096)
+    for fmt in ("act8", "mx"):
+        with pytest.raises(ValueError, match="q is (on cpu|not on a GPU)"):
+            block.Codes8(3, 128, fmt, device="cpu").dequantize(Out(), stream=S)
