@@ -895,17 +895,31 @@ struct Workspace : SeqAuxLayout {
         terms(static_cast<float2 *>(terms_at)) {}
 };
 
+// Sequences of which a block each is worth its reading of every sequence's tokens; a shorter finish
+// pays it back where there are many experts.  us in a graph, by sequences / by chunks, 145 tokens:
+//   sequences              1024           4096          65536
+//   8 experts, loss     11.2 / 12.4    25.5 / 21.6
+//     gradient           7.1 / 5.9     21.1 / 6.6     1329 / 13
+//     both at once      12.4 / 13.2    30.5 / 22.2    1236 / 199
+//   256 experts, loss   13.3 / 21.9    32.5 / 51.9
+//     gradient           7.6 / 5.6     21.0 / 6.7     1348 / 13
+//     both at once      14.6 / 22.6    38.6 / 52.9    1598 / 645
+// One limit for all three calls, so that the gradient by itself takes the loss's steps: a step with far
+// logits is taken another way, which differs in the last bits.
+int most_by_sequence(int E) { return std::max(1024, 16 * E); }
+
 // How the tokens are dealt out.  One block takes the whole call where there are few logits, whose
 // counts fit its shared memory (256 tokens of 8 experts 4.1 us in a graph, in three kernels 6.6;
-// but 1000 of 16 11.4 and 7.7).  A block a sequence where these are shorter than half a step, as
-// each end costs a block 0.6 us (145 tokens of 16 experts in 273 sequences 161 us by chunks of 128
-// tokens), and none can be longer than 64 steps.
+// but 1000 of 16 11.4 and 7.7).  A block a sequence where these are shorter than half a step, none
+// can be longer than 64 steps, and they are not too many (145 tokens of 16 experts in 273 sequences
+// 8.2 us, by chunks 11.2).
 int mode_of(const SeqAuxArgs &a) {
   const int step = tokens_per_step(a.E);
   if (a.loss != nullptr && a.T > 0 && (int64_t)a.T * a.E <= 8192 && a.T * a.k <= 4096 && a.B <= 8 &&
       a.B * (a.E + 1) <= kSmallCells)
     return kOneBlock;
-  return 2ll * a.T < (int64_t)a.B * step && a.T <= 64 * step ? kSequences : kChunks;
+  const bool short_ones = 2ll * a.T < (int64_t)a.B * step && a.T <= 64 * step;
+  return short_ones && a.B <= most_by_sequence(a.E) ? kSequences : kChunks;
 }
 
 // The pass over the logits; its blocks and their tokens are left for the finish.

@@ -341,3 +341,24 @@ def test_short_sequences_among_long_ones(block, T, E, k, kind, sigmoid, masked, 
     assert all(torch.equal(a, b) for a, b in zip(first, (s.loss, s.counts, s.tokens, s.probs)))
     sum_ = f64(base) - 2.0 * want["d_logits"]
     assert (np.abs(f64(d3) - sum_) <= 2.0 ** -17 * want["size"] + 2.0 ** -23 * np.abs(sum_) + 1e-37).all()
+
+
+@pytest.mark.parametrize("T,E,k,B", [(3000, 8, 2, 65536), (200, 64, 4, 1500), (64, 256, 2, 9000), (300, 16, 2, 700)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_more_sequences_than_a_block_each_pays_for(block, T, E, k, B, masked):
+    """Thousands of sequences of few tokens or none, the loss with its gradient and the gradient alone."""
+    rng, x, idx = case(T, E, k, B)
+    cut = np.sort(rng.integers(0, T + 1, B + 1))
+    mask = rng.random(T) > 0.4 if masked else None
+    want = R.seq_aux(x, idx, cut, mask, True, 0.3, 0.05)
+    lx, off = torch.tensor(x, device="cuda"), i32(cut)
+    m = None if mask is None else torch.tensor(mask, device="cuda")
+    s = block.SeqAuxLoss(T, E, k, B, 1, 0.3, 0.05)
+    s.workspace.fill_(0xFF)
+    for t in (s.probs, s.loss):
+        t.fill_(9.0)
+    d, d2 = (torch.full((T, E), 9.0, device="cuda") for _ in range(2))
+    s.forward(lx, i32(idx), off, m, d_logits=d)
+    check((s.loss, s.counts, s.tokens, s.probs, d), want, E, T)
+    s.backward(lx, off, d2, m, accumulate=False)
+    assert torch.equal(d, d2)
