@@ -362,3 +362,43 @@ def test_more_sequences_than_a_block_each_pays_for(block, T, E, k, B, masked):
     check((s.loss, s.counts, s.tokens, s.probs, d), want, E, T)
     s.backward(lx, off, d2, m, accumulate=False)
     assert torch.equal(d, d2)
+
+
+def cut_of(kind, T, B, rng):
+    """Offsets of B sequences: of equal lengths; one that holds all but a few tokens of the others; or
+    runs of one token and of none among long ones, with tokens before the first and behind the last."""
+    if kind == "even":
+        return np.arange(B + 1) * T // B
+    if kind == "one":
+        lens = np.where(np.arange(B) < B // 2, 1, 0)
+        lens[B // 3] = T - lens.sum()
+        return np.concatenate(([0], np.cumsum(lens)))
+    lens = rng.integers(0, 2, B)
+    lens[:: max(1, B // 5)] = (T - 40 - B) // 6
+    return 17 + np.concatenate(([0], np.cumsum(lens)))
+
+
+@pytest.mark.parametrize("T,E,k,B", [(9000, 256, 8, 60), (9000, 256, 8, 200), (20000, 64, 8, 300), (70000, 8, 1, 900),
+                                     (40000, 33, 1, 100), (16384, 64, 4, 500), (2048, 128, 16, 64), (8000, 16, 4, 250)])
+@pytest.mark.parametrize("kind", ["even", "one", "runs"])
+@pytest.mark.parametrize("masked", [False, True])
+def test_counts_by_lengths(block, T, E, k, B, kind, masked):
+    """Around 2^15 and 2^17 choices: sequences counted by a block each, by several blocks, and several
+    in a block, with and without a cell of its shared memory for each sequence and expert."""
+    rng, x, idx = case(T, E, k, B)
+    cut = cut_of(kind, T, B, rng)
+    assert cut[0] >= 0 and cut[-1] <= T and (np.diff(cut) >= 0).all()
+    idx[rng.integers(0, T, 20), 0] = -1
+    mask = rng.random(T) > 0.3 if masked else None
+    want = R.seq_aux(x, idx, cut, mask, False, 0.3, 0.05)
+    s = block.SeqAuxLoss(T, E, k, B, 0, 0.3, 0.05)
+    for t in (s.counts, s.tokens):
+        t.fill_(77)
+    s.workspace.fill_(0xFF)
+    d = torch.full((T, E), 9.0, device="cuda")
+    args = (torch.tensor(x, device="cuda"), i32(idx), i32(cut), None if mask is None else torch.tensor(mask, device="cuda"))
+    s.forward(*args, d_logits=d)
+    check((s.loss, s.counts, s.tokens, s.probs, d), want, E, T)
+    first = [t.clone() for t in (s.loss, s.counts, s.tokens, s.probs, d)]
+    s.forward(*args, d_logits=d)
+    assert all(torch.equal(a, b) for a, b in zip(first, (s.loss, s.counts, s.tokens, s.probs, d)))
