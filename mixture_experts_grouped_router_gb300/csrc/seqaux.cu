@@ -966,13 +966,14 @@ cudaError_t launch_pass(const SeqAuxArgs &a, const Workspace &w, int *blocks, in
 
 cudaError_t launch_count(const SeqAuxArgs &a, cudaStream_t s) {
   const int64_t choices = (int64_t)a.T * a.k;
-  // A block a sequence where none can have many choices, or few have: one launch less, 2 us, which
-  // a sequence of most of 2^17 choices pays back (131072 tokens of 500 sequences 24.6 us in all by
-  // sequences and 27.4 by chunks, 69 and 36 if all but a few lie in one; 100000 of 20000 138 and 104;
-  // 8192 of 8 choices in 2 15.4 and 10.1).  Else chunks, whose counts meet in atomics.
+  // A block a sequence up to 2^15 choices: a launch and the atomics less, 1.3 to 2.4 us (8192 tokens of 4
+  // choices, 64 even sequences 7.3 us in all, by chunks 9.0; all but a token each in one of them 21.4 and
+  // 17.2).  The host does not see lengths, and what one long sequence of many choices would cost the
+  // block that counts it grows with them (131072 tokens, 500 even sequences 18.6 and 21.3, one with most
+  // of them 85 and 63; 128 sequences 16.2 and 18.1, 60 and 37): past that chunks, whose counts meet in
+  // atomics, and for two or three sequences of some thousand tokens (8192 of 8 choices in 2 11.7 by chunks).
   const int64_t each = choices / a.B;
-  if (choices <= (1 << 13) || (choices <= (1 << 15) && each <= (1 << 13)) ||
-      (choices <= (1 << 17) && each >= 128 && each <= (1 << 11)))
+  if (choices <= (1 << 13) || (choices <= (1 << 15) && each <= (1 << 13)))
     return launch_dependent(seq_count_kernel, (unsigned)a.B, each <= 1024 ? 256 : kCountThreads, 0, s, a);
   const int64_t cells = (int64_t)a.B * (a.E + 1);
   const unsigned zero = (unsigned)std::min<int64_t>((cells + kThreads - 1) / kThreads, num_sms());
