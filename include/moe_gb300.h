@@ -854,8 +854,8 @@ moe_status_t moe_mx_dequantize(const uint8_t *q, int64_t ldq, const uint8_t *sf,
  *                contents on entry are ignored
  * A token whose logits are all -inf (or NaN) has p = 0 and no z.  fp32 sums in a fixed
  * order; rows of logits and gradients on 16 bytes with E % 4 == 0 are read 16 bytes at a
- * time; logits of -inf, NaN or no nearer to 0 than 17 take a slower way.  E <= 256, k <=
- * 16, T <= 2^30, 1 <= B <= 65536.
+ * time; tokens whose sum of e^logit is not within 1e-5 to 1e7 (logits over 16, all of them
+ * far under 0, NaN) take a slower way.  E <= 256, k <= 16, T <= 2^30, 1 <= B <= 65536.
  *
  * moe_seq_aux_loss_bwd -- the gradient by itself, from counts and tokens as
  * moe_seq_aux_loss wrote them (held fixed), times d_loss:
@@ -895,8 +895,9 @@ moe_status_t moe_seq_aux_loss_bwd(const float *logits, int64_t ld_logits, int T,
  *   workspace moe_clip_workspace_bytes() bytes of device memory, 8-byte aligned, contents
  *             on entry are ignored; calls that share it do not overlap
  * moe_grad_norm -- the norm alone; nothing else is written.
- * Squares are summed in a fixed order, in fp32 over 8 values at a time and then in 64
- * bits, so that no finite gradient is too large or too small for its square.
+ * Squares are summed in a fixed order, in fp32 over 64 bf16 or 32 fp32 values at a time (two
+ * chains) and then in 64 bits; those that fp32 cannot hold are summed of the values times a
+ * power of two, so that no finite gradient is too large or too small for its square.
  */
 typedef struct moe_grad {
   const void *g;

@@ -126,7 +126,8 @@ class SeqAuxLoss:
 
     def backward(self, logits, seq_offsets, d_logits, token_mask=None, d_loss=1.0, accumulate=True,
                  stream=None):
-        """The gradient of the last forward (the same logits, offsets and mask) into d_logits."""
+        """The gradient of the last forward into d_logits: of the same logits, offsets and mask, as
+        the counts are those of that forward (no other batch in between, of the same size either)."""
         self._shape(logits, seq_offsets)
         if logits.shape[0] != self.seen:
             raise ValueError("SeqAuxLoss.backward of %d tokens, the last forward was of %s"
